@@ -32,7 +32,10 @@ EXPORTS = ("dlrm_version", "dlrm_status_string", "dlrm_create", "dlrm_forward",
            "pairwise_dot_lower_tri",
            "pairwise_pair_map", "linear_bias_act", "dlrm_test_stall",
            "dlrm_set_cluster_batch_limit", "dlrm_get_cluster_batch_limit",
-           "dlrm_forward_kernels")
+           "dlrm_forward_kernels",
+           "history_work_bytes", "history_reset", "history_append", "history_fork",
+           "history_copy", "history_free", "history_trim", "history_compact",
+           "history_attention", "window_attention")
 NOALLOC_SCRATCH_BYTES = 16 << 20
 TRACE_SLOTS = 40
 
@@ -663,3 +666,8 @@ class DlrmModel:
             self.close()
         except Exception:
             pass
+
+
+from .history import (HistoryCache, history_append, history_attention,  # noqa: E402
+                      history_compact, history_copy, history_fork, history_free, history_trim,
+                      window_attention)

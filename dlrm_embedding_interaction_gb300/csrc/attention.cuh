@@ -1,0 +1,114 @@
+// What the attention kernels share: which events a row sees, where a CTA's
+// work lies in a ragged batch, and the fragments of the warp-level MMA.
+#pragma once
+
+#include "history.cuh"
+
+namespace dlrm {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// m16n8k16, f16 operands, fp32 sums.
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// m16n8k8, tf32 operands, fp32 sums.
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float quad_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+__device__ __forceinline__ float quad_sum(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 1);
+  return x + __shfl_xor_sync(0xffffffffu, x, 2);
+}
+
+// The events that the row at position pos sees: [0, end) less the gap
+// [gap0, gap1) between the sinks and the window.
+struct Visible {
+  int end, gap0, gap1;
+};
+__device__ __forceinline__ Visible visible(int pos, int len, int window, int sinks) {
+  Visible v;
+  v.end = max(min(len, pos + 1), 0);
+  v.gap0 = v.gap1 = 0;
+  if (window > 0) {
+    v.gap1 = max(pos - window + 1, 0);
+    v.gap0 = min(sinks, v.gap1);
+  }
+  return v;
+}
+__device__ __forceinline__ bool sees(const Visible& v, int t) {
+  return t < v.end && (t < v.gap0 || t >= v.gap1);
+}
+
+// Finds where a CTA's work lies: request b has units(b) >= 0 units, and the
+// CTA wants the request that holds unit `target` of all of them, or wants the
+// total (target < 0). Block-wide; every thread gets the answer. `shared` has
+// 40 int64.
+template <int THREADS, class F>
+__device__ __forceinline__ void locate(int batch, const F& units, int64_t target, int64_t* shared,
+                                       int& request, int64_t& first, int64_t& total) {
+  const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
+  constexpr int kWarps = THREADS / kWarp;
+  const int per = (batch + THREADS - 1) / THREADS;
+  const int b0 = min(batch, static_cast<int>(threadIdx.x) * per), b1 = min(batch, b0 + per);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) mine += units(b);
+  int64_t inc = mine;
+#pragma unroll
+  for (int d = 1; d < kWarp; d *= 2) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += y;
+  }
+  __syncthreads();
+  if (lane == kWarp - 1) shared[warp] = inc;
+  if (threadIdx.x == 0) {
+    shared[36] = batch;
+    shared[37] = 0;
+  }
+  __syncthreads();
+  int64_t at = inc - mine;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const int64_t s = shared[w];
+    at += w < warp ? s : 0;
+    total += s;
+  }
+  if (target >= 0 && target >= at && target < at + mine) {
+    for (int b = b0; b < b1; ++b) {
+      const int64_t n = units(b);
+      if (target < at + n) {
+        shared[36] = b;
+        shared[37] = at;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  request = static_cast<int>(shared[36]);
+  first = shared[37];
+}
+
+}  // namespace dlrm

@@ -1,0 +1,618 @@
+// Attention of queries over event histories kept in 8 bits (include/dlrm.h,
+// history_attention).
+//
+// One launch. The unit of work is a chunk of events (kWarps blocks of 32
+// events) of one row tile: one kv head of one request and up to kRows of its
+// query rows (rows are (query, head of the group) pairs, so heads that share
+// a kv head share its bytes). All chunks of the batch form one sequence,
+// request by request; every CTA takes an equal, contiguous part of it,
+// whatever the histories' lengths, so a long history is split over many CTAs
+// and a short one costs one chunk. A tile that lies in one CTA is finished
+// there; one that is split leaves partial results (maximum, sum, weighted
+// values per row) in scratch, and the CTA that arrives last joins them, in the
+// order of the events: results do not depend on timing.
+//
+// In a CTA, warp w takes block w of each chunk and keeps its own running
+// maximum, sum and output in registers; the warps are joined once per tile.
+// Per block, S = Q K^T and O += P V are m16n8k16 MMAs whose fragments come
+// straight from global memory, without shared memory: the MMA does not care
+// which element of the head (for S) or which event (for P V) an index of its
+// inner dimension stands for, as long as both operands agree, so a thread
+// takes 16 contiguous bytes of an event's key, and 4 to 16 of a value, and
+// converts them (e4m3 to f16 is exact) in place.
+//   keys: thread (g, c) = (lane / 4, lane % 4) holds event g of an 8-event
+//     tile, elements 64 j + 16 c + 4 ks + e (j: 64-byte part, ks: k step);
+//   values: thread (g, c) holds events 2c, 2c+1, 2c+8, 2c+9 of a 16-event
+//     step, elements g D/8 .. (g+1) D/8 - 1; the bytes of a pair of events
+//     are interleaved, then converted. Output column 2c + i of n tile nt is
+//     element (2c + i) D/8 + nt.
+// Scales: a block lies in one page, so the page's key scale multiplies S and
+// its value scale the block's P V, both in fp32 (one FMA per output, which
+// also applies the running maximum's correction).
+//
+// Queries become f16 after a division by a power of two for each row. A bf16
+// or fp16 query and P (11 bits) take one MMA row: 16 rows a tile. An fp32
+// query is split into an f16 head and a rest of 11 more bits, which take two
+// MMA rows, and so is P: 8 rows a tile, errors as of fp32.
+//
+// What bounds it: reading the codes (2 D bytes an event and kv head).
+#include <atomic>
+
+#include "attention.cuh"
+
+namespace dlrm {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * kWarp;
+constexpr int kBlock = 32;                       // events of a warp's step
+
+struct Params {
+  dlrm_history_t h;
+  dlrm_attention_t a;
+  int group;                                     // query heads of a kv head
+  int32_t* counters;
+  float* partials;
+};
+
+// What a CTA needs to know of a request.
+struct Span {
+  int slot, rows, len, q0, tiles;                // rows: queries * group
+  int sink_blocks, block0, blocks, chunks;       // blocks of events: the sinks', then from block0 on
+};
+
+template <int ROWS>
+__device__ __forceinline__ Span span_of(const Params& p, int b, bool report) {
+  Span s;
+  const int q0 = p.a.q_starts[b], q1 = p.a.q_starts[b + 1];
+  s.slot = p.a.slots[b];
+  s.q0 = q0;
+  s.rows = 0;
+  s.len = 0;
+  const bool bad = q0 < 0 || q1 < q0 || q1 > p.a.q_rows;
+  if (!bad) s.rows = (q1 - q0) * p.group;
+  if (s.slot >= 0 && s.slot < p.h.n_slots) {
+    const int64_t cap = static_cast<int64_t>(p.h.max_pages) * p.h.page_tokens;
+    s.len = static_cast<int>(min(static_cast<int64_t>(max(p.h.lengths[s.slot], 0)), cap));
+  } else if (report) {
+    flag(p.h.err, DLRM_ERRBIT_INDEX_OOB);
+  }
+  if (bad && report) flag(p.h.err, DLRM_ERRBIT_OFFSETS);
+  s.tiles = (s.rows + ROWS - 1) / ROWS;
+  // the events that any row of the request sees
+  const Visible first =
+      visible(p.a.causal ? s.len - (q1 - q0) : s.len - 1, s.len, p.a.window, p.a.sinks);
+  const int end = (s.len + kBlock - 1) / kBlock;
+  const int sink = min(p.a.sinks, s.len);
+  s.block0 = first.gap1 / kBlock;
+  s.sink_blocks = first.gap1 > 0 ? (sink + kBlock - 1) / kBlock : 0;
+  if (s.sink_blocks >= s.block0) s.sink_blocks = s.block0;   // no gap: blocks from 0 on
+  s.blocks = s.sink_blocks + max(end - s.block0, 0);
+  s.chunks = max((s.blocks + kWarps - 1) / kWarps, 1);        // an empty one writes zeros
+  return s;
+}
+
+template <int N>
+struct Words {
+  uint32_t w[N];
+};
+
+// Loads N consecutive words.
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t* w, const uint8_t* p) {
+  if (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(p) + i);
+      w[4 * i] = x.x;
+      w[4 * i + 1] = x.y;
+      w[4 * i + 2] = x.z;
+      w[4 * i + 3] = x.w;
+    }
+  } else if (N == 2) {
+    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+    w[0] = x.x;
+    w[1] = x.y;
+  } else {
+    w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+  }
+}
+
+// Element of a thread's key or query word: part j, step ks, pair element e.
+template <int D>
+__device__ __forceinline__ int key_element(int c, int word) {
+  if (D == 32) return 8 * c + 4 * word;
+  return 64 * (word / 4) + 16 * c + 4 * (word % 4);
+}
+
+// One row of the tile from the definition, event by event, for a row whose
+// output is not finite: 0 * NaN of a masked event's value must not reach it.
+// One CTA, every thread.
+template <int DT>
+__device__ __noinline__ void careful_row(const Params& p, const Span& s, int head, int row,
+                                         float* sm) {
+  const int G = p.h.page_tokens, D = p.h.head_dim, M = p.h.max_pages, H = p.h.n_heads;
+  const int i = row / p.group, hq = head * p.group + row % p.group;
+  const Visible v = visible(p.a.causal ? s.len - s.rows / p.group + i : s.len - 1, s.len,
+                            p.a.window, p.a.sinks);
+  const int64_t q_at = (s.q0 + static_cast<int64_t>(i)) * p.a.ld_q + hq * p.a.ld_q_head;
+  const int32_t* row_pages = p.h.table + static_cast<int64_t>(s.slot) * M;
+  float* prob = sm;                               // one per thread
+  float* red = sm + kThreads;
+  auto code = [](uint8_t c) { return f16x2_to_float2(e4m3x2_to_f16x2(c)).x; };
+  float top = -INFINITY, sum = 0.f, acc = 0.f;
+  const int d = threadIdx.x;
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int t0 = 0; t0 < v.end; t0 += kThreads) {
+      const int t = t0 + static_cast<int>(threadIdx.x);
+      float x = -INFINITY;
+      if (t < v.end && sees(v, t)) {
+        const int page = row_pages[t / G];
+        if (page >= 0 && page < p.h.n_pages) {
+          const int64_t place = static_cast<int64_t>(page) * H + head;
+          const uint8_t* k = p.h.k_codes + (place * G + t % G) * D;
+          float dot = 0.f;
+          for (int e = 0; e < D; ++e) dot = fmaf(load_element<DT>(p.a.q, q_at + e), code(k[e]), dot);
+          x = dot * (p.h.k_scales[place] * p.a.scale * kLog2e);
+        }
+      }
+      if (pass == 0) {
+        top = (x > top || x != x) ? x : top;      // a NaN stays
+      } else {
+        __syncthreads();
+        prob[threadIdx.x] = x == -INFINITY ? -1.f : exp2f(x - top);
+        __syncthreads();
+        const int n = min(kThreads, v.end - t0);
+        for (int u = 0; u < n; ++u) {
+          const float pr = prob[u];
+          if (pr == -1.f) continue;
+          sum += pr;
+          if (d < D) {
+            const int page = row_pages[(t0 + u) / G];
+            const int64_t place = static_cast<int64_t>(page) * H + head;
+            acc = fmaf(pr * p.h.v_scales[place], code(p.h.v_codes[(place * G + (t0 + u) % G) * D + d]),
+                       acc);
+          }
+        }
+      }
+    }
+    if (pass == 0) {
+      __syncthreads();
+      red[threadIdx.x] = top;
+      __syncthreads();
+      for (int u = 0; u < kThreads; ++u) {
+        const float y = red[u];
+        top = (y > top || y != y) ? y : top;
+      }
+      if (top == -INFINITY) top = 0.f;
+    }
+  }
+  const int64_t o_at = (s.q0 + static_cast<int64_t>(i)) * p.a.ld_out + hq * p.a.ld_out_head;
+  if (d < D) store_element<DT>(p.a.out, o_at + d, sum == 0.f ? 0.f : acc / sum);
+  if (d == 0 && p.a.lse)
+    p.a.lse[(s.q0 + static_cast<int64_t>(i)) * p.a.n_heads + hq] =
+        sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
+  __syncthreads();
+}
+
+template <int D, int DT>
+__global__ void __launch_bounds__(kThreads) history_attention_kernel(const Params p) {
+  constexpr bool kSplit = DT == DLRM_DTYPE_FP32;
+  constexpr int kRows = kSplit ? 8 : 16;
+  constexpr int KW = D / 16;                      // key words of a thread and event tile
+  constexpr int VW = D / 32;                      // value words of a thread and event
+  constexpr int NT = D / 8;                       // n tiles of the output
+  constexpr int kStride = D + 2;                  // a row's sums, maximum, sum of weights
+  constexpr int kAcc = kSplit ? 2 : 4;            // output values of a thread and n tile
+  __shared__ int64_t scan[40];
+  __shared__ float joined[kWarps][kRows][kStride];
+  __shared__ float row_factor[kRows];
+  __shared__ int odd[kRows + 1];
+
+  const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
+  const int g = lane / 4, c = lane % 4;
+  const int G = p.h.page_tokens, H = p.h.n_heads;
+  pdl_wait();
+  pdl_trigger();
+
+  auto units = [&](int b) {
+    const Span s = span_of<kRows>(p, b, false);
+    return static_cast<int64_t>(s.tiles) * s.chunks * H;
+  };
+  int b;
+  int64_t at, total;
+  locate<kThreads>(p.a.batch, units, -1, scan, b, at, total);
+  const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < p.a.batch; i += kThreads) span_of<kRows>(p, i, true);
+  if (blockIdx.x >= ctas) return;
+  const int64_t begin = blockIdx.x * total / ctas, end = (blockIdx.x + 1) * total / ctas;
+  locate<kThreads>(p.a.batch, units, begin, scan, b, at, total);
+
+  for (int64_t u = begin; u < end;) {
+    Span s = span_of<kRows>(p, b, false);
+    const int64_t units_b = static_cast<int64_t>(s.tiles) * s.chunks * H;
+    if (u >= at + units_b) {
+      at += units_b;
+      ++b;
+      continue;
+    }
+    const int64_t seg = (u - at) / s.chunks;      // (head, tile) of the request
+    const int head = static_cast<int>(seg / s.tiles), tile = static_cast<int>(seg % s.tiles);
+    const int64_t seg0 = at + seg * s.chunks, seg1 = seg0 + s.chunks;
+    const int chunk0 = static_cast<int>(u - seg0);
+    const int chunk1 = static_cast<int>(min(end, seg1) - seg0);
+    const int rows = min(kRows, s.rows - tile * kRows);
+    u = seg0 + chunk1;
+
+    // ---- queries: fragments of the tile, scaled to f16
+    uint32_t qa[KW][4];
+    float qf[2];
+    Visible vis[2];
+    {
+      float x[2][KW][4];
+#pragma unroll
+      for (int r2 = 0; r2 < 2; ++r2) {
+        // rows past the last stand for it (their queries are zero), so that
+        // they do not make blocks of events partly visible
+        const int r = min(kSplit ? g : g + 8 * r2, rows - 1);
+        const int row = tile * kRows + r;
+        const int i = row / p.group;
+        const bool in = r == g + 8 * r2;
+        const int64_t q_at = (s.q0 + static_cast<int64_t>(i)) * p.a.ld_q +
+                             (head * p.group + row % p.group) * p.a.ld_q_head;
+        float big = 0.f;
+#pragma unroll
+        for (int w = 0; w < KW; ++w)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[r2][w][e] = in ? load_element<DT>(p.a.q, q_at + key_element<D>(c, w) + e) : 0.f;
+            big = fmaxf(big, fabsf(x[r2][w][e]));
+          }
+        big = quad_max(big);
+        const int ex = max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -100);
+        const float f = pow2f(min(8 - ex, 127));
+        qf[r2] = pow2f(max(ex - 8, -126)) * p.a.scale * kLog2e;
+#pragma unroll
+        for (int w = 0; w < KW; ++w)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[r2][w][e] *= f;
+        vis[r2] = visible(p.a.causal ? s.len - s.rows / p.group + i : s.len - 1, s.len, p.a.window,
+                          p.a.sinks);
+      }
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        qa[w][0] = pack_f16x2(x[0][w][0], x[0][w][1]);
+        qa[w][2] = pack_f16x2(x[0][w][2], x[0][w][3]);
+        if (kSplit) {
+          const float2 h0 = f16x2_to_float2(qa[w][0]), h1 = f16x2_to_float2(qa[w][2]);
+          qa[w][1] = pack_f16x2((x[0][w][0] - h0.x) * 2048.f, (x[0][w][1] - h0.y) * 2048.f);
+          qa[w][3] = pack_f16x2((x[0][w][2] - h1.x) * 2048.f, (x[0][w][3] - h1.y) * 2048.f);
+        } else {
+          qa[w][1] = pack_f16x2(x[1][w][0], x[1][w][1]);
+          qa[w][3] = pack_f16x2(x[1][w][2], x[1][w][3]);
+        }
+      }
+      if (kSplit) {
+        qf[1] = qf[0];
+        vis[1] = vis[0];
+      }
+    }
+
+    // ---- events
+    float o[NT][kAcc];
+    float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < kAcc; ++i) o[nt][i] = 0.f;
+    const int32_t* pages = p.h.table + static_cast<int64_t>(s.slot) * p.h.max_pages;
+    const int n0 = chunk0 * kWarps + warp, n1 = min(chunk1 * kWarps, s.blocks);
+    for (int n = n0; n < n1; n += kWarps) {
+      const int t0 = (n < s.sink_blocks ? n : n - s.sink_blocks + s.block0) * kBlock;
+      const int page = pages[t0 / G];
+      if (page < 0 || page >= p.h.n_pages) {
+        // trimmed, or a broken table: no row may need these events
+        bool need = false;
+        for (int t = t0; t < min(t0 + kBlock, s.len); ++t) need |= sees(vis[0], t) | sees(vis[1], t);
+        if (need) flag(p.h.err, DLRM_ERRBIT_INDEX_OOB);
+        continue;
+      }
+      const int64_t place = static_cast<int64_t>(page) * H + head;
+      const int64_t codes = (place * G + t0 % G) * D;
+      uint32_t kw[kBlock / 8][KW], vw[kBlock / 16][4][VW];
+#pragma unroll
+      for (int j = 0; j < kBlock / 8; ++j) {
+        const uint8_t* kp = p.h.k_codes + codes + (8 * j + g) * D;
+        if (D == 32) {
+          load_words<2>(kw[j], kp + 8 * c);
+        } else {
+#pragma unroll
+          for (int i = 0; i < KW / 4; ++i) load_words<4>(&kw[j][4 * i], kp + 64 * i + 16 * c);
+        }
+      }
+#pragma unroll
+      for (int kt = 0; kt < kBlock / 16; ++kt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = 16 * kt + 2 * c + (i & 1) + 8 * (i >> 1);
+          load_words<VW>(vw[kt][i], p.h.v_codes + codes + t * D + g * (D / 8));
+        }
+      const float ks = p.h.k_scales[place], vs = p.h.v_scales[place];
+
+      // S = Q K^T
+      float sc[kBlock / 8][4];
+#pragma unroll
+      for (int j = 0; j < kBlock / 8; ++j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[j][i] = 0.f;
+#pragma unroll
+        for (int w = 0; w < KW; ++w)
+          mma_f16(sc[j], qa[w], e4m3x2_lo_to_f16x2(kw[j][w]), e4m3x2_hi_to_f16x2(kw[j][w]));
+      }
+      // masked log2 weights; values of events past the end are cleared, as
+      // their codes are whatever an earlier history left there
+      const float f0 = qf[0] * ks, f1 = qf[1] * ks;
+      const bool whole = t0 + kBlock <= min(vis[0].end, vis[1].end) &&
+                         (t0 >= vis[0].gap1 || t0 + kBlock <= vis[0].gap0) &&
+                         (t0 >= vis[1].gap1 || t0 + kBlock <= vis[1].gap0);
+      float big[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int j = 0; j < kBlock / 8; ++j) {
+        if (kSplit) {
+          sc[j][0] = fmaf(sc[j][2], 1.f / 2048.f, sc[j][0]) * f0;
+          sc[j][1] = fmaf(sc[j][3], 1.f / 2048.f, sc[j][1]) * f0;
+        } else {
+          sc[j][0] *= f0;
+          sc[j][1] *= f0;
+          sc[j][2] *= f1;
+          sc[j][3] *= f1;
+        }
+        if (!whole) {
+          const int t = t0 + 8 * j + 2 * c;
+          if (!sees(vis[0], t)) sc[j][0] = -INFINITY;
+          if (!sees(vis[0], t + 1)) sc[j][1] = -INFINITY;
+          if (!kSplit) {
+            if (!sees(vis[1], t)) sc[j][2] = -INFINITY;
+            if (!sees(vis[1], t + 1)) sc[j][3] = -INFINITY;
+          }
+        }
+        big[0] = fmaxf(big[0], fmaxf(sc[j][0], sc[j][1]));
+        if (!kSplit) big[1] = fmaxf(big[1], fmaxf(sc[j][2], sc[j][3]));
+      }
+      if (t0 + kBlock > s.len) {
+#pragma unroll
+        for (int kt = 0; kt < kBlock / 16; ++kt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (t0 + 16 * kt + 2 * c + (i & 1) + 8 * (i >> 1) >= s.len)
+#pragma unroll
+              for (int w = 0; w < VW; ++w) vw[kt][i][w] = 0;
+      }
+      // running maximum and sum
+      float alpha[2] = {1.f, 1.f};
+#pragma unroll
+      for (int r = 0; r < (kSplit ? 1 : 2); ++r) {
+        const float m = fmaxf(top[r], quad_max(big[r]));
+        const float base = m == -INFINITY ? 0.f : m;
+        alpha[r] = exp2_approx(top[r] - base);
+        top[r] = m;
+        float add = 0.f;
+#pragma unroll
+        for (int j = 0; j < kBlock / 8; ++j) {
+          sc[j][2 * r] = exp2_approx(sc[j][2 * r] - base);
+          sc[j][2 * r + 1] = exp2_approx(sc[j][2 * r + 1] - base);
+          add += sc[j][2 * r] + sc[j][2 * r + 1];
+        }
+        sum[r] = fmaf(sum[r], alpha[r], add);
+      }
+      // O = alpha O + vs P V
+      uint32_t pa[kBlock / 16][4];
+#pragma unroll
+      for (int kt = 0; kt < kBlock / 16; ++kt) {
+        pa[kt][0] = pack_f16x2(sc[2 * kt][0], sc[2 * kt][1]);
+        pa[kt][2] = pack_f16x2(sc[2 * kt + 1][0], sc[2 * kt + 1][1]);
+        if (kSplit) {
+          const float2 h0 = f16x2_to_float2(pa[kt][0]), h1 = f16x2_to_float2(pa[kt][2]);
+          pa[kt][1] = pack_f16x2((sc[2 * kt][0] - h0.x) * 2048.f, (sc[2 * kt][1] - h0.y) * 2048.f);
+          pa[kt][3] =
+              pack_f16x2((sc[2 * kt + 1][0] - h1.x) * 2048.f, (sc[2 * kt + 1][1] - h1.y) * 2048.f);
+        } else {
+          pa[kt][1] = pack_f16x2(sc[2 * kt][2], sc[2 * kt][3]);
+          pa[kt][3] = pack_f16x2(sc[2 * kt + 1][2], sc[2 * kt + 1][3]);
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < VW; ++w) {
+        float acc[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll
+        for (int kt = 0; kt < kBlock / 16; ++kt) {
+          // bytes of a pair of events side by side: n tiles 4w, 4w+1 and 4w+2, 4w+3
+          const uint32_t l0 = __byte_perm(vw[kt][0][w], vw[kt][1][w], 0x5140);
+          const uint32_t l1 = __byte_perm(vw[kt][0][w], vw[kt][1][w], 0x7362);
+          const uint32_t h0 = __byte_perm(vw[kt][2][w], vw[kt][3][w], 0x5140);
+          const uint32_t h1 = __byte_perm(vw[kt][2][w], vw[kt][3][w], 0x7362);
+          mma_f16(acc[0], pa[kt], e4m3x2_lo_to_f16x2(l0), e4m3x2_lo_to_f16x2(h0));
+          mma_f16(acc[1], pa[kt], e4m3x2_hi_to_f16x2(l0), e4m3x2_hi_to_f16x2(h0));
+          mma_f16(acc[2], pa[kt], e4m3x2_lo_to_f16x2(l1), e4m3x2_lo_to_f16x2(h1));
+          mma_f16(acc[3], pa[kt], e4m3x2_hi_to_f16x2(l1), e4m3x2_hi_to_f16x2(h1));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float* out = o[4 * w + i];
+          if (kSplit) {
+            out[0] = fmaf(out[0], alpha[0], vs * fmaf(acc[i][2], 1.f / 2048.f, acc[i][0]));
+            out[1] = fmaf(out[1], alpha[0], vs * fmaf(acc[i][3], 1.f / 2048.f, acc[i][1]));
+          } else {
+            out[0] = fmaf(out[0], alpha[0], vs * acc[i][0]);
+            out[1] = fmaf(out[1], alpha[0], vs * acc[i][1]);
+            out[2] = fmaf(out[2], alpha[1], vs * acc[i][2]);
+            out[3] = fmaf(out[3], alpha[1], vs * acc[i][3]);
+          }
+        }
+      }
+    }
+
+    // ---- join the warps
+    __syncthreads();                              // `joined` of the tile before is read
+#pragma unroll
+    for (int r = 0; r < (kSplit ? 1 : 2); ++r) {
+      const float l = quad_sum(sum[r]);
+      float* out = joined[warp][g + 8 * r];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        out[2 * c * (D / 8) + nt] = o[nt][2 * r];
+        out[(2 * c + 1) * (D / 8) + nt] = o[nt][2 * r + 1];
+      }
+      if (c == 0) {
+        out[D] = top[r];
+        out[D + 1] = l;
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x < kRows) {
+      float m = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, joined[w][threadIdx.x][D]);
+      const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = exp2_approx(joined[w][threadIdx.x][D] - base);
+        l = fmaf(f, joined[w][threadIdx.x][D + 1], l);
+        joined[w][threadIdx.x][D] = f;
+      }
+      joined[0][threadIdx.x][D + 1] = l;
+      row_factor[threadIdx.x] = m;
+    }
+    __syncthreads();
+    const bool split = chunk0 > 0 || chunk1 < s.chunks;
+    float* mine = p.partials + (static_cast<int64_t>(blockIdx.x) * 2 + (chunk0 > 0 ? 0 : 1)) * kAttnPartial;
+    for (int e = threadIdx.x; e < rows * D; e += kThreads) {
+      const int r = e / D, d = e % D;
+      float x = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) x = fmaf(joined[w][r][D], joined[w][r][d], x);
+      if (split)
+        mine[r * kStride + d] = x;
+      else
+        joined[0][r][d] = x;
+    }
+    if (split) {
+      if (threadIdx.x < rows) {
+        mine[threadIdx.x * kStride + D] = row_factor[threadIdx.x];
+        mine[threadIdx.x * kStride + D + 1] = joined[0][threadIdx.x][D + 1];
+      }
+      // the CTAs that share this tile: first .. last, one part each
+      const int64_t first = ((seg0 + 1) * ctas - 1) / total, last = (seg1 * ctas - 1) / total;
+      const int parts = static_cast<int>(last - first) + 1;
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        const int before = atomicAdd(&p.counters[first], 1);
+        odd[kRows] = before == parts - 1;
+        if (before == parts - 1) p.counters[first] = 0;
+      }
+      __syncthreads();
+      if (!odd[kRows]) continue;
+      __threadfence();
+      auto part = [&](int i) {
+        return p.partials + ((first + i) * 2 + (i > 0 ? 0 : 1)) * kAttnPartial;
+      };
+      // maximum of each row over the parts, then the weighted sums
+      for (int r = warp; r < rows; r += kWarps) {
+        float m = -INFINITY;
+        for (int i = lane; i < parts; i += kWarp) m = fmaxf(m, __ldcg(part(i) + r * kStride + D));
+#pragma unroll
+        for (int x = 16; x > 0; x /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+        if (lane == 0) row_factor[r] = m;
+      }
+      __syncthreads();
+      for (int e = threadIdx.x; e < rows * (D + 1); e += kThreads) {
+        const int r = e / (D + 1);
+        const int d = e % (D + 1) == D ? D + 1 : e % (D + 1);
+        const float base = row_factor[r] == -INFINITY ? 0.f : row_factor[r];
+        float x = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < parts; ++i) {
+          const float* q = part(i) + r * kStride;
+          x = fmaf(exp2_approx(__ldcg(q + D) - base), __ldcg(q + d), x);
+        }
+        joined[0][r][d] = x;
+      }
+    }
+    if (threadIdx.x <= kRows) odd[threadIdx.x] = 0;
+    __syncthreads();
+
+    // ---- outputs
+    for (int e = threadIdx.x; e < rows * D; e += kThreads) {
+      const int r = e / D, d = e % D;
+      const int row = tile * kRows + r;
+      const float l = joined[0][r][D + 1];
+      const float x = l == 0.f ? 0.f : joined[0][r][d] / l;
+      const int64_t i = s.q0 + static_cast<int64_t>(row / p.group);
+      const int hq = head * p.group + row % p.group;
+      store_element<DT>(p.a.out, i * p.a.ld_out + hq * p.a.ld_out_head + d, x);
+      if (d == 0 && p.a.lse)
+        p.a.lse[i * p.a.n_heads + hq] = l == 0.f ? -INFINITY : row_factor[r] * kLn2 + logf(l);
+      if (!finite(x)) odd[r] = odd[kRows] = 1;
+    }
+    __syncthreads();
+    if (odd[kRows]) {
+      for (int r = 0; r < rows; ++r)
+        if (odd[r]) careful_row<DT>(p, s, head, tile * kRows + r, &joined[0][0][0]);
+    }
+  }
+}
+
+template <int D, int DT>
+cudaError_t launch(const Params& p, cudaStream_t stream) {
+  constexpr int kRows = DT == DLRM_DTYPE_FP32 ? 8 : 16;
+  static std::atomic<int> resident{0};            // CTAs of an SM: the same for every GB300
+  int per_sm = resident.load(std::memory_order_relaxed);
+  if (per_sm == 0) {
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+        &per_sm, history_attention_kernel<D, DT>, kThreads, 0);
+    if (e != cudaSuccess) return e;
+    per_sm = std::max(1, std::min(per_sm, kAttnMaxCtas / 152));
+    resident.store(per_sm, std::memory_order_relaxed);
+  }
+  // no more CTAs than chunks there can be
+  const int64_t chunk = kWarps * kBlock;
+  const int64_t events = static_cast<int64_t>(p.h.max_pages) * p.h.page_tokens;
+  const int64_t tiles = p.a.q_rows * p.group / kRows + p.a.batch;
+  const int64_t chunks = tiles * p.h.n_heads * ((events + chunk - 1) / chunk + 1);
+  const int64_t grid = std::min<int64_t>(
+      {chunks, static_cast<int64_t>(device_sm_count()) * per_sm, int64_t(kAttnMaxCtas)});
+  return launch_pdl(history_attention_kernel<D, DT>, dim3(static_cast<unsigned>(grid)),
+                    dim3(kThreads), 0, stream, p);
+}
+
+template <int D>
+cudaError_t launch_d(const Params& p, cudaStream_t stream) {
+  if (p.a.dtype == DLRM_DTYPE_FP32) return launch<D, DLRM_DTYPE_FP32>(p, stream);
+  if (p.a.dtype == DLRM_DTYPE_BF16) return launch<D, DLRM_DTYPE_BF16>(p, stream);
+  return launch<D, DLRM_DTYPE_FP16>(p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_history_attention(const dlrm_history_t& h, const dlrm_attention_t& a,
+                                     cudaStream_t stream) {
+  const HistoryWork w = history_work(h);
+  Params p;
+  p.h = h;
+  p.a = a;
+  p.group = a.n_heads / h.n_heads;
+  p.counters = work_part<int32_t>(h, w.counters);
+  p.partials = work_part<float>(h, w.partials);
+  if (h.head_dim == 32) return launch_d<32>(p, stream);
+  if (h.head_dim == 64) return launch_d<64>(p, stream);
+  return launch_d<128>(p, stream);
+}
+
+}  // namespace dlrm

@@ -1,0 +1,682 @@
+// Pages of event histories: append (quantise), fork, copy, free, trim and
+// compact. include/dlrm.h defines the pool and what each call does.
+//
+// Tables, reference counts and the free stack are read and changed on the
+// device, so no call waits for the GPU and all can be captured in a graph.
+// A call is a chain of small launches (programmatic dependent launches: each
+// starts its set-up while the one before it ends):
+//   append     plan (one CTA), write
+//   fork/copy  plan (one CTA), copy
+//   free/trim  release, count, push (one CTA a request)
+//   compact    count, match, move, rename
+// The plan gives every request its place in the free stack by a prefix sum
+// over the requests, so page numbers do not depend on timing; freed pages are
+// pushed in an order that is likewise a prefix sum over (request, page).
+#include "history.cuh"
+
+namespace dlrm {
+
+namespace {
+
+constexpr int kPlanThreads = 1024;
+
+// Words of the scratch's head.
+enum { kHeadItems = 0, kHeadTop = 1, kHeadLive = 2, kHeadMoves = 3 };
+
+// What the plan knows of one request. item0: its first work item.
+struct Request {
+  int32_t slot;      // destination, or -1: no effect
+  int32_t source;
+  int32_t length;    // events before the call (append), or of the source
+  int32_t count;     // events to append
+  int32_t base;      // pages taken from the stack by earlier requests
+  int32_t need;      // pages this one takes
+  int32_t item0;
+  int32_t items;
+};
+static_assert(sizeof(Request) == 32, "scratch size of a request");
+
+struct Pool {
+  dlrm_history_t h;
+  int32_t* head;
+  int32_t* mark_slot;
+  int32_t* mark_page;
+  Request* request;
+  int2* items;
+  int32_t* stash;
+  int32_t* remap;
+  int32_t* holes;
+  int32_t* movers;
+  int32_t* tiles;
+};
+
+Pool make_pool(const dlrm_history_t& h) {
+  const HistoryWork w = history_work(h);
+  Pool p;
+  p.h = h;
+  p.head = work_part<int32_t>(h, w.head);
+  p.mark_slot = work_part<int32_t>(h, w.mark_slot);
+  p.mark_page = work_part<int32_t>(h, w.mark_page);
+  p.request = work_part<Request>(h, w.request);
+  p.items = work_part<int2>(h, w.items);
+  p.stash = work_part<int32_t>(h, w.stash);
+  p.remap = work_part<int32_t>(h, w.remap);
+  p.holes = work_part<int32_t>(h, w.holes);
+  p.movers = work_part<int32_t>(h, w.movers);
+  p.tiles = work_part<int32_t>(h, w.tiles);
+  return p;
+}
+
+__device__ __forceinline__ int warp_inclusive(int x) {
+  const int lane = threadIdx.x % kWarp;
+#pragma unroll
+  for (int d = 1; d < kWarp; d *= 2) {
+    const int y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  return x;
+}
+
+// Exclusive prefix sum over the block; total in every thread. sums: one int
+// per warp and one more.
+__device__ __forceinline__ int block_exclusive(int x, int* sums, int& total) {
+  const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
+  const int warps = blockDim.x / kWarp;
+  const int inc = warp_inclusive(x);
+  __syncthreads();
+  if (lane == kWarp - 1) sums[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    const int s = lane < warps ? sums[lane] : 0;
+    const int si = warp_inclusive(s);
+    if (lane < warps) sums[lane] = si - s;
+    if (lane == kWarp - 1) sums[kWarp] = si;
+  }
+  __syncthreads();
+  total = sums[kWarp];
+  return sums[warp] + inc - x;
+}
+
+enum PlanOp { kAppend, kFork, kCopy };
+
+// One CTA: gives every request its pages. Phases over all requests, with a
+// barrier between them, so that a request sees the pool as it was before the
+// call: (1) mark the slots written, the first request of a slot winning;
+// (2) check each request and count the pages it needs; (3) prefix sums give
+// stack places and work items; (4) write tables and reference counts.
+template <int OP>
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(Pool p, const int32_t* src,
+                                                            const int32_t* dst,
+                                                            const int32_t* starts, int batch,
+                                                            int64_t rows) {
+  __shared__ int sums[kWarp + 1];
+  __shared__ int done;
+  const dlrm_history_t& h = p.h;
+  const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp, warps = kPlanThreads / kWarp;
+  const int G = h.page_tokens, M = h.max_pages;
+  pdl_wait();
+  pdl_trigger();
+  const int nfree = min(max(*h.n_free, 0), h.n_pages);
+  if (threadIdx.x == 0) done = 0;
+
+  for (int b = threadIdx.x; b < batch; b += kPlanThreads) {
+    const int d = dst[b];
+    if (d >= 0 && d < h.n_slots) atomicMin(&p.mark_slot[d], b);
+  }
+  __syncthreads();
+
+  for (int b = warp; b < batch; b += warps) {
+    Request r{-1, -1, 0, 0, 0, 0, 0, 0};
+    const int d = dst[b], s = OP == kAppend ? d : src[b];
+    uint32_t bad = 0;
+    if (d < 0 || d >= h.n_slots || s < 0 || s >= h.n_slots) {
+      bad = DLRM_ERRBIT_INDEX_OOB;
+    } else if (p.mark_slot[d] != b) {
+      bad = DLRM_ERRBIT_INVALID_ARG;
+    } else {
+      r.slot = d;
+      r.source = s;
+      const int64_t cap = static_cast<int64_t>(M) * G;
+      r.length = static_cast<int>(min(static_cast<int64_t>(max(h.lengths[s], 0)), cap));
+      if (OP == kAppend) {
+        const int t0 = starts[b], t1 = starts[b + 1];
+        if (t0 < 0 || t1 < t0 || t1 > rows) {
+          bad = DLRM_ERRBIT_OFFSETS;
+        } else if (r.length + static_cast<int64_t>(t1 - t0) > cap) {
+          bad = DLRM_ERRBIT_INVALID_ARG;
+        } else {
+          r.count = t1 - t0;
+          const int old = (r.length + G - 1) / G;
+          r.need = static_cast<int>((r.length + static_cast<int64_t>(r.count) + G - 1) / G) - old;
+          r.items = r.need + (r.count > 0 && r.length % G != 0 ? 1 : 0);
+        }
+      } else if (h.lengths[d] != 0) {
+        bad = DLRM_ERRBIT_INVALID_ARG;
+      } else if (OP == kFork) {
+        r.need = r.length % G != 0 ? 1 : 0;
+        r.items = r.need;
+      } else {
+        const int n = (r.length + G - 1) / G;
+        int c = 0;
+        for (int j = lane; j < n; j += kWarp)
+          c += h.table[static_cast<int64_t>(s) * M + j] >= 0 ? 1 : 0;
+        r.need = __reduce_add_sync(0xffffffffu, c);
+        r.items = r.need;
+      }
+    }
+    if (bad) {
+      r.slot = -1;
+      r.need = r.items = 0;
+    }
+    if (lane == 0) {
+      if (bad) flag(h.err, bad);
+      p.request[b] = r;
+    }
+  }
+  __syncthreads();
+
+  int base = 0, items = 0;
+  for (int b0 = 0; b0 < batch; b0 += kPlanThreads) {
+    const int b = b0 + static_cast<int>(threadIdx.x);
+    Request r{-1, -1, 0, 0, 0, 0, 0, 0};
+    if (b < batch) r = p.request[b];
+    int total;
+    r.base = base + block_exclusive(r.need, sums, total);
+    // saturates: past nfree every later request that needs a page fails
+    base = min(base + total, h.n_pages + 1);
+    const bool short_of = r.need > 0 && r.base + static_cast<int64_t>(r.need) > nfree;
+    if (short_of) {
+      flag(h.err, DLRM_ERRBIT_OOM);
+      r.slot = -1;
+      r.items = 0;
+    } else if (r.need > 0) {
+      atomicMax(&done, r.base + r.need);
+    }
+    r.item0 = items + block_exclusive(r.items, sums, total);
+    items += total;
+    if (b < batch) p.request[b] = r;
+  }
+  __syncthreads();
+
+  for (int b = warp; b < batch; b += warps) {
+    const Request r = p.request[b];
+    if (lane == 0) {
+      const int d = dst[b];
+      if (d >= 0 && d < h.n_slots && p.mark_slot[d] == b) p.mark_slot[d] = INT32_MAX;
+    }
+    if (r.slot < 0) continue;
+    int32_t* row = h.table + static_cast<int64_t>(r.slot) * M;
+    if (OP == kAppend) {
+      const int first = (r.length + G - 1) / G;
+      for (int i = lane; i < r.need; i += kWarp) {
+        const int page = h.free_pages[nfree - 1 - (r.base + i)];
+        row[first + i] = page;
+        h.refs[page] = 1;
+      }
+      for (int i = lane; i < r.items; i += kWarp)
+        p.items[r.item0 + i] = make_int2(b, r.length / G + i);
+      if (lane == 0) h.lengths[r.slot] = r.length + r.count;
+    } else {
+      const int32_t* from = h.table + static_cast<int64_t>(r.source) * M;
+      const int n = (r.length + G - 1) / G;
+      const int full = OP == kFork ? r.length / G : 0;
+      int taken = 0;
+      for (int j0 = 0; j0 < n; j0 += kWarp) {
+        const int j = j0 + lane;
+        const int old = j < n ? from[j] : -1;
+        const bool fresh = old >= 0 && j >= full;
+        const unsigned mask = __ballot_sync(0xffffffffu, fresh);
+        if (fresh) {
+          const int rank = taken + __popc(mask & ((1u << lane) - 1));
+          // a page missing from a fork's last entry leaves its stack place
+          // unused only if the table broke its own rules; never read past it
+          const int page = h.free_pages[nfree - 1 - (r.base + rank)];
+          row[j] = page;
+          h.refs[page] = 1;
+          p.items[r.item0 + rank] = make_int2(old, page);
+        } else if (j < n) {
+          row[j] = old;
+          if (old >= 0) atomicAdd(&h.refs[old], 1);
+        }
+        taken += __popc(mask);
+      }
+      if (lane == 0) h.lengths[r.slot] = r.length;
+    }
+  }
+  if (threadIdx.x == 0) {
+    p.head[kHeadItems] = items;
+    *h.n_free = nfree - done;
+  }
+}
+
+// ------------------------------------------------------------------ copy
+
+constexpr int kCopyThreads = 256;
+constexpr int kCopyVec = 4;                                    // 16-byte loads in flight a thread
+constexpr int kCopyPiece = kCopyThreads * kCopyVec * 16;       // bytes
+
+// Copies piece `piece` of the codes of one side of a page, and the scales with
+// the first. Pages of H * G * D bytes, a multiple of 1 KB.
+__device__ __forceinline__ void copy_piece(const dlrm_history_t& h, int side, int piece, int from,
+                                           int to) {
+  uint8_t* codes = side ? h.v_codes : h.k_codes;
+  const int64_t bytes = static_cast<int64_t>(h.n_heads) * h.page_tokens * h.head_dim;
+  const uint4* s = reinterpret_cast<const uint4*>(codes + from * bytes);
+  uint4* d = reinterpret_cast<uint4*>(codes + to * bytes);
+  const int n = static_cast<int>(bytes / 16);
+  const int i0 = piece * (kCopyPiece / 16) + threadIdx.x;
+  uint4 x[kCopyVec];
+#pragma unroll
+  for (int i = 0; i < kCopyVec; ++i)
+    if (i0 + i * kCopyThreads < n) x[i] = s[i0 + i * kCopyThreads];
+#pragma unroll
+  for (int i = 0; i < kCopyVec; ++i)
+    if (i0 + i * kCopyThreads < n) d[i0 + i * kCopyThreads] = x[i];
+  if (piece == 0) {
+    float* scales = side ? h.v_scales : h.k_scales;
+    for (int i = threadIdx.x; i < h.n_heads; i += kCopyThreads)
+      scales[static_cast<int64_t>(to) * h.n_heads + i] =
+          scales[static_cast<int64_t>(from) * h.n_heads + i];
+  }
+}
+
+__host__ __device__ __forceinline__ int pieces_of(const dlrm_history_t& h) {
+  const int64_t bytes = static_cast<int64_t>(h.n_heads) * h.page_tokens * h.head_dim;
+  return static_cast<int>((bytes + kCopyPiece - 1) / kCopyPiece);
+}
+
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(Pool p, int pieces) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t n = static_cast<int64_t>(p.head[kHeadItems]) * 2 * pieces;
+  for (int64_t w = blockIdx.x; w < n; w += gridDim.x) {
+    const int2 item = p.items[w / (2 * pieces)];
+    const int rest = static_cast<int>(w % (2 * pieces));
+    copy_piece(p.h, rest / pieces, rest % pieces, item.x, item.y);
+  }
+}
+
+// ------------------------------------------------------------------ append
+
+constexpr int kWriteThreads = 128;
+
+// Quantises the new events of one page, head and side per iteration. The
+// scale needs the largest magnitude first, so the new rows are read twice,
+// the second time from L1 or L2. Where the page already holds events and its
+// scale grows, their codes are re-rounded: exact but for codes that become
+// subnormal, as scales are powers of two.
+template <int DT>
+__global__ void __launch_bounds__(kWriteThreads)
+append_kernel(Pool p, const int32_t* starts, const void* k, int64_t ld_k, int64_t ld_k_head,
+              const void* v, int64_t ld_v, int64_t ld_v_head) {
+  __shared__ uint32_t top[kWriteThreads / kWarp];
+  const dlrm_history_t& h = p.h;
+  const int G = h.page_tokens, D = h.head_dim, H = h.n_heads;
+  pdl_wait();
+  pdl_trigger();
+  const int64_t n = static_cast<int64_t>(p.head[kHeadItems]) * H * 2;
+  for (int64_t w = blockIdx.x; w < n; w += gridDim.x) {
+    const int side = static_cast<int>(w & 1);
+    const int head = static_cast<int>((w >> 1) % H);
+    const int2 item = p.items[(w >> 1) / H];
+    const Request r = p.request[item.x];
+    const int page = h.table[static_cast<int64_t>(r.slot) * h.max_pages + item.y];
+    if (page < 0 || page >= h.n_pages) {   // a trimmed last page: cannot be, never written
+      flag(h.err, DLRM_ERRBIT_INDEX_OOB);
+      continue;
+    }
+    const int kept = max(r.length - item.y * G, 0);             // events there already
+    const int end = min(static_cast<int>(min(static_cast<int64_t>(r.length) + r.count -
+                                                 static_cast<int64_t>(item.y) * G,
+                                             static_cast<int64_t>(G))), G);
+    const int64_t row0 = starts[item.x] + static_cast<int64_t>(item.y) * G - r.length;
+    const void* x = side ? v : k;
+    const int64_t ld = side ? ld_v : ld_k;
+    const int64_t off = head * (side ? ld_v_head : ld_k_head);
+    const int64_t place = static_cast<int64_t>(page) * H + head;
+    uint8_t* codes = (side ? h.v_codes : h.k_codes) + place * G * D;
+    float* scale = (side ? h.v_scales : h.k_scales) + place;
+
+    uint32_t big = 0;
+    for (int e = kept * D + threadIdx.x; e < end * D; e += kWriteThreads) {
+      const float f = load_element<DT>(x, (row0 + e / D) * ld + off + e % D);
+      const uint32_t u = __float_as_uint(f) & 0x7fffffffu;
+      if (u < 0x7f800000u) big = max(big, u);
+    }
+    big = __reduce_max_sync(0xffffffffu, big);
+    __syncthreads();
+    if (threadIdx.x % kWarp == 0) top[threadIdx.x / kWarp] = big;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kWriteThreads / kWarp; ++i) big = max(big, top[i]);
+    int e_new = scale_exponent(big);
+    if (kept > 0) {
+      const float was = *scale;
+      const int e_old = static_cast<int>(__float_as_uint(was) >> 23) - 127;
+      e_new = max(e_new, min(max(e_old, -kScaleExpMax), kScaleExpMax));
+      if (e_new > e_old) {
+        const float f = pow2f(max(e_old - e_new, -126));
+        uint32_t* c4 = reinterpret_cast<uint32_t*>(codes);
+        for (int i = threadIdx.x; i < kept * D / 4; i += kWriteThreads) {
+          const uint32_t c = c4[i];
+          const float2 a = f16x2_to_float2(e4m3x2_lo_to_f16x2(c));
+          const float2 b = f16x2_to_float2(e4m3x2_hi_to_f16x2(c));
+          c4[i] = floats_to_e4m3x2(a.x * f, a.y * f) | (floats_to_e4m3x2(b.x * f, b.y * f) << 16);
+        }
+      }
+    }
+    __syncthreads();                                            // every thread has read *scale
+    if (threadIdx.x == 0) *scale = pow2f(e_new);
+    const float inv = pow2f(-e_new);
+    uint16_t* c2 = reinterpret_cast<uint16_t*>(codes);
+    for (int e = kept * D / 2 + threadIdx.x; e < end * D / 2; e += kWriteThreads) {
+      const int64_t at = (row0 + 2 * e / D) * ld + off + 2 * e % D;
+      c2[e] = static_cast<uint16_t>(
+          floats_to_e4m3x2(load_element<DT>(x, at) * inv, load_element<DT>(x, at + 1) * inv));
+    }
+  }
+}
+
+// ------------------------------------------------------------------ free, trim
+
+constexpr int kFreeThreads = 256;
+
+// Takes the pages [first, last) of request b's slot out of its table; every
+// page loses a reference and remembers the last (request, page) position that
+// released it, which is the one that will push it.
+__global__ void __launch_bounds__(kFreeThreads) release_kernel(Pool p, const int32_t* slots,
+                                                               int window, int sinks) {
+  const dlrm_history_t& h = p.h;
+  const int G = h.page_tokens, M = h.max_pages, b = blockIdx.x;
+  pdl_wait();
+  pdl_trigger();
+  const int slot = slots[b];
+  Request r{-1, -1, 0, 0, 0, 0, 0, 0};
+  if (b == 0 && threadIdx.x == 0) p.head[kHeadTop] = min(max(*h.n_free, 0), h.n_pages);
+  if (slot < 0 || slot >= h.n_slots) {
+    if (threadIdx.x == 0) flag(h.err, DLRM_ERRBIT_INDEX_OOB);
+  } else {
+    bool again = false;                                         // listed before: nothing left
+    for (int i = threadIdx.x; i < b; i += kFreeThreads) again |= slots[i] == slot;
+    if (!__syncthreads_or(again)) {
+      const int64_t len = max(h.lengths[slot], 0);
+      r.slot = slot;
+      r.count = static_cast<int>(min((len + G - 1) / G, static_cast<int64_t>(M)));
+      if (window > 0) {
+        r.base = static_cast<int>(min((static_cast<int64_t>(sinks) + G - 1) / G,
+                                      static_cast<int64_t>(r.count)));
+        r.count = static_cast<int>(max((len - window) / G, static_cast<int64_t>(r.base)));
+        if (len < window) r.count = r.base;
+      }
+    }
+  }
+  if (threadIdx.x == 0) p.request[b] = r;
+  if (r.slot < 0) return;
+  int32_t* row = h.table + static_cast<int64_t>(slot) * M;
+  for (int j = r.base + threadIdx.x; j < r.count; j += kFreeThreads) {
+    int page = row[j];
+    if (page < 0 || page >= h.n_pages) {
+      page = -1;
+    } else {
+      atomicSub(&h.refs[page], 1);
+      atomicMax(&p.mark_page[page], b * M + j);
+    }
+    row[j] = -1;
+    p.stash[b * M + j] = page;
+  }
+}
+
+__device__ __forceinline__ bool pushes(const Pool& p, const Request& r, int b, int j, int& page) {
+  page = -1;
+  if (r.slot < 0 || j >= r.count) return false;
+  page = p.stash[b * p.h.max_pages + j];
+  if (page < 0) return false;
+  if (p.mark_page[page] != b * p.h.max_pages + j) {
+    page = -1;
+    return false;
+  }
+  return p.h.refs[page] <= 0;
+}
+
+__global__ void __launch_bounds__(kFreeThreads) count_freed_kernel(Pool p) {
+  pdl_wait();
+  pdl_trigger();
+  const int b = blockIdx.x;
+  const Request r = p.request[b];
+  int n = 0;
+  for (int j0 = r.base; j0 < r.count; j0 += kFreeThreads) {
+    int page;
+    n += __syncthreads_count(pushes(p, r, b, j0 + static_cast<int>(threadIdx.x), page));
+  }
+  if (threadIdx.x == 0) p.request[b].items = n;
+}
+
+// Position q of the freed pages, counted from the last one down, goes to place
+// top + q of the stack.
+__global__ void __launch_bounds__(kFreeThreads) push_kernel(Pool p, int batch, int whole) {
+  __shared__ int sums[kWarp + 1];
+  pdl_wait();
+  pdl_trigger();
+  const dlrm_history_t& h = p.h;
+  const int b = blockIdx.x;
+  int before = 0, after = 0;
+  for (int i = threadIdx.x; i < batch; i += kFreeThreads) {
+    const int n = p.request[i].items;
+    before += i <= b ? n : 0;
+    after += i > b ? n : 0;
+  }
+  int upto, later;
+  block_exclusive(before, sums, upto);
+  block_exclusive(after, sums, later);
+  const Request r = p.request[b];
+  const int top = p.head[kHeadTop];
+  int left = r.items;                                            // of this request, not pushed yet
+  for (int j0 = r.base; j0 < r.count; j0 += kFreeThreads) {
+    int page, n;
+    const bool push = pushes(p, r, b, j0 + static_cast<int>(threadIdx.x), page);
+    const int rank = block_exclusive(push ? 1 : 0, sums, n);
+    if (push) {
+      const int q = later + left - 1 - rank;
+      if (top + q < h.n_pages) h.free_pages[top + q] = page;
+      h.refs[page] = 0;
+    }
+    if (page >= 0) p.mark_page[page] = -1;
+    left -= n;
+  }
+  if (threadIdx.x == 0) {
+    if (whole && r.slot >= 0) h.lengths[r.slot] = 0;
+    if (b == batch - 1) *h.n_free = min(top + upto, h.n_pages);
+  }
+}
+
+// ------------------------------------------------------------------ compact
+
+constexpr int kTile = 1024;   // pages a CTA looks at
+
+__global__ void __launch_bounds__(kTile) count_live_kernel(Pool p) {
+  pdl_wait();
+  pdl_trigger();
+  const int i = blockIdx.x * kTile + threadIdx.x;
+  const int n = __syncthreads_count(i < p.h.n_pages && p.h.refs[i] > 0);
+  if (threadIdx.x == 0) p.tiles[blockIdx.x] = n;
+}
+
+// Lists the free pages below n (n pages are live) and the live ones from n on,
+// both in ascending order: equally many.
+__global__ void __launch_bounds__(kTile) match_kernel(Pool p, int tiles) {
+  __shared__ int sums[kWarp + 1];
+  pdl_wait();
+  pdl_trigger();
+  const int P = p.h.n_pages;
+  int mine = 0, all = 0;
+  for (int t = threadIdx.x; t < tiles; t += kTile) {
+    const int n = p.tiles[t];
+    all += n;
+    mine += t < static_cast<int>(blockIdx.x) ? n : 0;
+  }
+  int live, before;
+  block_exclusive(all, sums, live);
+  block_exclusive(mine, sums, before);
+  // live pages below n: whole tiles, then the part of n's own tile
+  int low = 0;
+  for (int t = threadIdx.x; t < live / kTile; t += kTile) low += p.tiles[t];
+  const int at = live / kTile * kTile + static_cast<int>(threadIdx.x);
+  low += at < live && p.h.refs[at] > 0 ? 1 : 0;
+  int kept;
+  block_exclusive(low, sums, kept);
+  const int i = blockIdx.x * kTile + threadIdx.x;
+  const bool is_live = i < P && p.h.refs[i] > 0;
+  int total;
+  const int rank = before + block_exclusive(is_live ? 1 : 0, sums, total);
+  if (i < live && !is_live) p.holes[i - rank] = i;
+  if (i >= live && is_live) p.movers[rank - kept] = i;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    p.head[kHeadLive] = live;
+    p.head[kHeadMoves] = live - kept;
+  }
+}
+
+__global__ void __launch_bounds__(kCopyThreads) move_kernel(Pool p, int pieces) {
+  pdl_wait();
+  pdl_trigger();
+  const dlrm_history_t& h = p.h;
+  const int64_t n = static_cast<int64_t>(p.head[kHeadMoves]) * 2 * pieces;
+  for (int64_t w = blockIdx.x; w < n; w += gridDim.x) {
+    const int m = static_cast<int>(w / (2 * pieces));
+    const int rest = static_cast<int>(w % (2 * pieces));
+    const int from = p.movers[m], to = p.holes[m];
+    copy_piece(h, rest / pieces, rest % pieces, from, to);
+    if (rest == 0 && threadIdx.x == 0) {
+      h.refs[to] = h.refs[from];
+      h.refs[from] = 0;
+      p.remap[from] = to;
+    }
+  }
+}
+
+__global__ void __launch_bounds__(256) rename_kernel(Pool p) {
+  pdl_wait();
+  pdl_trigger();
+  const dlrm_history_t& h = p.h;
+  const int live = p.head[kHeadLive];
+  const int64_t entries = static_cast<int64_t>(h.n_slots) * h.max_pages;
+  const int64_t first = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t i = first; i < entries; i += step) {
+    const int page = h.table[i];
+    if (page >= live && page < h.n_pages) h.table[i] = p.remap[page];
+  }
+  for (int64_t i = first; i < h.n_pages - live; i += step)
+    h.free_pages[i] = h.n_pages - 1 - static_cast<int>(i);
+  if (first == 0) *h.n_free = h.n_pages - live;
+}
+
+__global__ void __launch_bounds__(256) reset_kernel(Pool p, int32_t* counters, int n_counters) {
+  const dlrm_history_t& h = p.h;
+  const int64_t first = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  const int64_t entries = static_cast<int64_t>(h.n_slots) * h.max_pages;
+  for (int64_t i = first; i < entries; i += step) h.table[i] = -1;
+  for (int64_t i = first; i < h.n_pages; i += step) {
+    h.refs[i] = 0;
+    h.free_pages[i] = h.n_pages - 1 - static_cast<int>(i);
+    p.mark_page[i] = -1;
+  }
+  for (int64_t i = first; i < h.n_slots; i += step) {
+    h.lengths[i] = 0;
+    p.mark_slot[i] = INT32_MAX;
+  }
+  for (int64_t i = first; i < n_counters; i += step) counters[i] = 0;
+  if (first == 0) {
+    *h.n_free = h.n_pages;
+    *h.err = 0;
+  }
+}
+
+unsigned grid_for(int64_t units, int per_sm) {
+  return static_cast<unsigned>(std::max<int64_t>(
+      1, std::min<int64_t>(units, static_cast<int64_t>(device_sm_count()) * per_sm)));
+}
+
+template <int DT>
+cudaError_t launch_write(const Pool& p, const int32_t* starts, const void* k, int64_t ld_k,
+                         int64_t ld_k_head, const void* v, int64_t ld_v, int64_t ld_v_head,
+                         unsigned grid, cudaStream_t stream) {
+  return launch_pdl(append_kernel<DT>, dim3(grid), dim3(kWriteThreads), 0, stream, p, starts, k,
+                    ld_k, ld_k_head, v, ld_v, ld_v_head);
+}
+
+}  // namespace
+
+cudaError_t launch_history_reset(const dlrm_history_t& h, cudaStream_t stream) {
+  const int64_t most = std::max<int64_t>(static_cast<int64_t>(h.n_slots) * h.max_pages, h.n_pages);
+  const HistoryWork w = history_work(h);
+  reset_kernel<<<grid_for((most + 255) / 256, 8), 256, 0, stream>>>(
+      make_pool(h), work_part<int32_t>(h, w.counters), kAttnMaxCtas);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_history_append(const dlrm_history_t& h, const int32_t* slots,
+                                  const int32_t* starts, int batch, const void* k, int64_t ld_k,
+                                  int64_t ld_k_head, const void* v, int64_t ld_v,
+                                  int64_t ld_v_head, int64_t rows, int dtype,
+                                  cudaStream_t stream) {
+  const Pool p = make_pool(h);
+  cudaError_t e = launch_pdl(plan_kernel<kAppend>, dim3(1), dim3(kPlanThreads), 0, stream, p,
+                             static_cast<const int32_t*>(nullptr), slots, starts, batch, rows);
+  if (e != cudaSuccess) return e;
+  // n new events touch at most n / G + 2 pages of a history
+  const int64_t pages = std::min<int64_t>(rows, rows / h.page_tokens + 2 * int64_t(batch));
+  const unsigned grid = grid_for(pages * h.n_heads * 2, 16);
+  if (dtype == DLRM_DTYPE_FP32)
+    return launch_write<DLRM_DTYPE_FP32>(p, starts, k, ld_k, ld_k_head, v, ld_v, ld_v_head, grid, stream);
+  if (dtype == DLRM_DTYPE_BF16)
+    return launch_write<DLRM_DTYPE_BF16>(p, starts, k, ld_k, ld_k_head, v, ld_v, ld_v_head, grid, stream);
+  return launch_write<DLRM_DTYPE_FP16>(p, starts, k, ld_k, ld_k_head, v, ld_v, ld_v_head, grid, stream);
+}
+
+cudaError_t launch_history_fork(const dlrm_history_t& h, const int32_t* src, const int32_t* dst,
+                                int batch, bool share, cudaStream_t stream) {
+  const Pool p = make_pool(h);
+  cudaError_t e = share ? launch_pdl(plan_kernel<kFork>, dim3(1), dim3(kPlanThreads), 0, stream, p,
+                                     src, dst, static_cast<const int32_t*>(nullptr), batch,
+                                     int64_t(0))
+                        : launch_pdl(plan_kernel<kCopy>, dim3(1), dim3(kPlanThreads), 0, stream, p,
+                                     src, dst, static_cast<const int32_t*>(nullptr), batch,
+                                     int64_t(0));
+  if (e != cudaSuccess) return e;
+  const int pieces = pieces_of(h);
+  const int64_t pages = std::min<int64_t>(h.n_pages, int64_t(batch) * (share ? 1 : h.max_pages));
+  return launch_pdl(copy_kernel, dim3(grid_for(pages * 2 * pieces, 8)), dim3(kCopyThreads), 0,
+                    stream, p, pieces);
+}
+
+cudaError_t launch_history_free(const dlrm_history_t& h, const int32_t* slots, int batch,
+                                int window, int sinks, cudaStream_t stream) {
+  const Pool p = make_pool(h);
+  cudaError_t e = launch_pdl(release_kernel, dim3(batch), dim3(kFreeThreads), 0, stream, p, slots,
+                             window, sinks);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(count_freed_kernel, dim3(batch), dim3(kFreeThreads), 0, stream, p);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(push_kernel, dim3(batch), dim3(kFreeThreads), 0, stream, p, batch,
+                    window > 0 ? 0 : 1);
+}
+
+cudaError_t launch_history_compact(const dlrm_history_t& h, cudaStream_t stream) {
+  const Pool p = make_pool(h);
+  const int tiles = (h.n_pages + kTile - 1) / kTile;
+  cudaError_t e = launch_pdl(count_live_kernel, dim3(tiles), dim3(kTile), 0, stream, p);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(match_kernel, dim3(tiles), dim3(kTile), 0, stream, p, tiles);
+  if (e != cudaSuccess) return e;
+  const int pieces = pieces_of(h);
+  e = launch_pdl(move_kernel, dim3(grid_for(int64_t(h.n_pages) * pieces, 8)), dim3(kCopyThreads),
+                 0, stream, p, pieces);
+  if (e != cudaSuccess) return e;
+  const int64_t entries = std::max<int64_t>(int64_t(h.n_slots) * h.max_pages, h.n_pages);
+  return launch_pdl(rename_kernel, dim3(grid_for((entries + 255) / 256, 8)), dim3(256), 0, stream,
+                    p);
+}
+
+}  // namespace dlrm

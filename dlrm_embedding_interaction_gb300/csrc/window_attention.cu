@@ -1,0 +1,382 @@
+// Causal attention of ragged rows with a sliding window and sinks over plain
+// keys and values (include/dlrm.h, window_attention).
+//
+// A CTA takes a tile of kWarps * 16 rows of one kv head of a request (rows
+// are (query, head of the group) pairs), a warp 16 of them; every warp walks
+// the blocks of 32 events that its own rows see, with a running maximum and
+// sum, and keeps its output in registers. Fragments come straight from global
+// memory (the four warps of a CTA read nearly the same events: L1 serves
+// them), with the inner dimensions of the MMAs permuted so that a thread's
+// loads are contiguous, as in history_attention.cu.
+//   bf16, fp16: m16n8k16 in the input's own type; P is rounded to that type.
+//   fp32: m16n8k8 in tf32, three products per product (head * head,
+//     head * rest, rest * head), errors as of fp32.
+#include "attention.cuh"
+
+namespace dlrm {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * kWarp;
+constexpr int kBlock = 32;
+constexpr int kTileRows = kWarps * 16;
+
+struct Params {
+  dlrm_attention_t a;
+  int group;
+  int vec;                                       // rows can be loaded 16 bytes at a time
+};
+
+struct Span {
+  int q0, k0, rows, len, tiles;
+};
+
+__device__ __forceinline__ Span span_of(const Params& p, int b, bool report) {
+  Span s;
+  const int q0 = p.a.q_starts[b], q1 = p.a.q_starts[b + 1];
+  const int k0 = p.a.k_starts[b], k1 = p.a.k_starts[b + 1];
+  const bool bad = q0 < 0 || q1 < q0 || q1 > p.a.q_rows || k0 < 0 || k1 < k0 || k1 > p.a.k_rows;
+  if (bad && report) flag(p.a.err, DLRM_ERRBIT_OFFSETS);
+  s.q0 = q0;
+  s.k0 = k0;
+  s.rows = bad ? 0 : (q1 - q0) * p.group;
+  s.len = bad ? 0 : k1 - k0;
+  s.tiles = (s.rows + kTileRows - 1) / kTileRows;
+  return s;
+}
+
+// N consecutive 32-bit words at a byte address, 16 bytes at a time if aligned.
+template <int N, bool HALF>
+__device__ __forceinline__ void load_row_words(uint32_t* w, const uint8_t* p, bool vec) {
+  if (vec && N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(p) + i);
+      w[4 * i] = x.x;
+      w[4 * i + 1] = x.y;
+      w[4 * i + 2] = x.z;
+      w[4 * i + 3] = x.w;
+    }
+  } else if (vec && N == 2) {
+    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+    w[0] = x.x;
+    w[1] = x.y;
+  } else if (!HALF) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint16_t lo = __ldg(reinterpret_cast<const uint16_t*>(p) + 2 * i);
+      const uint16_t hi = __ldg(reinterpret_cast<const uint16_t*>(p) + 2 * i + 1);
+      w[i] = lo | (static_cast<uint32_t>(hi) << 16);
+    }
+  }
+}
+
+// One row from the definition, event by event, by one warp: for a row whose
+// output is not finite (0 * a masked event's infinity or NaN).
+template <int D, int DT>
+__device__ __noinline__ void careful_row(const Params& p, const Span& s, int head, int row) {
+  const int lane = threadIdx.x % kWarp;
+  const int i = row / p.group, hq = head * p.group + row % p.group;
+  const Visible v = visible(s.len - s.rows / p.group + i, s.len, p.a.window, p.a.sinks);
+  const int64_t q_at = (s.q0 + static_cast<int64_t>(i)) * p.a.ld_q + hq * p.a.ld_q_head;
+  constexpr int N = D / kWarp;
+  float q[N], acc[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    q[e] = load_element<DT>(p.a.q, q_at + lane + 32 * e) * (p.a.scale * kLog2e);
+    acc[e] = 0.f;
+  }
+  float top = -INFINITY, sum = 0.f;
+  for (int t = 0; t < v.end; ++t) {
+    if (!sees(v, t)) {
+      t = v.gap1 - 1;
+      continue;
+    }
+    const int64_t kt = s.k0 + static_cast<int64_t>(t);
+    float x = 0.f;
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      x = fmaf(q[e], load_element<DT>(p.a.k, kt * p.a.ld_k + head * p.a.ld_k_head + lane + 32 * e), x);
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) x += __shfl_xor_sync(0xffffffffu, x, d);
+    const float m = (x > top || x != x) ? x : top;              // a NaN stays
+    const float base = m == -INFINITY ? 0.f : m;
+    const float f = exp2f(top - base), w = exp2f(x - base);
+    top = m;
+    sum = fmaf(sum, f, w);
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      acc[e] = fmaf(acc[e], f, w * load_element<DT>(p.a.v, kt * p.a.ld_v + head * p.a.ld_v_head + lane + 32 * e));
+  }
+  const int64_t o = (s.q0 + static_cast<int64_t>(i)) * p.a.ld_out + hq * p.a.ld_out_head;
+#pragma unroll
+  for (int e = 0; e < N; ++e) store_element<DT>(p.a.out, o + lane + 32 * e, sum == 0.f ? 0.f : acc[e] / sum);
+  if (lane == 0 && p.a.lse)
+    p.a.lse[(s.q0 + static_cast<int64_t>(i)) * p.a.n_heads + hq] =
+        sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
+}
+
+template <int D, int DT>
+__global__ void __launch_bounds__(kThreads) window_attention_kernel(const Params p) {
+  constexpr bool kF32 = DT == DLRM_DTYPE_FP32;
+  constexpr int EB = kF32 ? 4 : 2;
+  constexpr int EW = 4 / EB;                      // elements of a word
+  constexpr int KW = D / 4 / EW;                  // words of a thread and row: D/4 elements
+  constexpr int VW = D / 8 / EW;
+  constexpr int NT = D / 8;
+  constexpr int kQ = kF32 ? 2 * KW : KW;          // query words of a thread, both rows
+  __shared__ int64_t scan[40];
+  const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
+  const int g = lane / 4, c = lane % 4;
+  const int heads = p.a.n_kv_heads;
+  pdl_wait();
+  pdl_trigger();
+  int b;
+  int64_t at, total;
+  // CTA (tile, head) with the head fastest
+  const int64_t unit = blockIdx.x / heads;
+  const int head = blockIdx.x % heads;
+  locate<kThreads>(p.a.batch, [&](int i) { return static_cast<int64_t>(span_of(p, i, false).tiles); },
+                   unit, scan, b, at, total);
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < p.a.batch; i += kThreads) span_of(p, i, true);
+  if (unit >= total) return;
+  const Span s = span_of(p, b, false);
+  const int row0 = static_cast<int>(unit - at) * kTileRows + warp * 16;
+  if (row0 >= s.rows) return;                     // no barrier follows
+  const int last_row = min(row0 + 15, s.rows - 1);
+
+  // queries: fragments of the 16 rows
+  uint32_t qw[2][KW];
+  Visible vis[2];
+  float qf = p.a.scale * kLog2e;
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int row = min(row0 + g + 8 * r, last_row);
+    const int i = row / p.group;
+    const uint8_t* q = static_cast<const uint8_t*>(p.a.q) +
+                       ((s.q0 + static_cast<int64_t>(i)) * p.a.ld_q +
+                        (head * p.group + row % p.group) * p.a.ld_q_head + c * (D / 4)) * EB;
+    load_row_words<KW, !kF32>(qw[r], q, p.vec);
+    vis[r] = visible(s.len - s.rows / p.group + i, s.len, p.a.window, p.a.sinks);
+  }
+  // the events that any of the warp's rows sees
+  const int i0 = row0 / p.group, i1 = last_row / p.group;
+  const Visible v0 = visible(s.len - s.rows / p.group + i0, s.len, p.a.window, p.a.sinks);
+  const Visible v1 = visible(s.len - s.rows / p.group + i1, s.len, p.a.window, p.a.sinks);
+
+  float o[NT][4];
+  float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[nt][i] = 0.f;
+
+  const uint8_t* kp = static_cast<const uint8_t*>(p.a.k) +
+                      (s.k0 * p.a.ld_k + head * p.a.ld_k_head + c * (D / 4)) * EB;
+  const uint8_t* vp = static_cast<const uint8_t*>(p.a.v) +
+                      (s.k0 * p.a.ld_v + head * p.a.ld_v_head + g * (D / 8)) * EB;
+  const int64_t k_step = p.a.ld_k * EB, v_step = p.a.ld_v * EB;
+
+  for (int t0 = 0; t0 < v1.end; t0 += kBlock) {
+    // past the sinks of every row and before the window of the first: skip to it
+    if (t0 >= v1.gap0 && t0 + kBlock <= v0.gap1) {
+      t0 = v0.gap1 / kBlock * kBlock - kBlock;
+      continue;
+    }
+    float sc[kBlock / 8][4];
+#pragma unroll
+    for (int j = 0; j < kBlock / 8; ++j) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sc[j][i] = 0.f;
+      uint32_t kw[KW];
+      // an event past the end stands for the last one; its weight is zero
+      load_row_words<KW, !kF32>(kw, kp + min(t0 + 8 * j + g, s.len - 1) * k_step, p.vec);
+      if (!kF32) {
+#pragma unroll
+        for (int w = 0; w < KW; w += 2) {
+          const uint32_t a[4] = {qw[0][w], qw[1][w], qw[0][w + 1], qw[1][w + 1]};
+          if (DT == DLRM_DTYPE_BF16)
+            mma_bf16(sc[j], a, kw[w], kw[w + 1]);
+          else
+            mma_f16(sc[j], a, kw[w], kw[w + 1]);
+        }
+      } else {
+#pragma unroll
+        for (int w = 0; w < KW; w += 2) {
+          uint32_t a[4] = {qw[0][w], qw[1][w], qw[0][w + 1], qw[1][w + 1]}, hi[4], lo[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            hi[i] = a[i] & 0xffffe000u;
+            lo[i] = __float_as_uint(__uint_as_float(a[i]) - __uint_as_float(hi[i]));
+          }
+          const uint32_t h0 = kw[w] & 0xffffe000u, h1 = kw[w + 1] & 0xffffe000u;
+          const uint32_t l0 = __float_as_uint(__uint_as_float(kw[w]) - __uint_as_float(h0));
+          const uint32_t l1 = __float_as_uint(__uint_as_float(kw[w + 1]) - __uint_as_float(h1));
+          mma_tf32(sc[j], lo, h0, h1);
+          mma_tf32(sc[j], hi, l0, l1);
+          mma_tf32(sc[j], hi, h0, h1);
+        }
+      }
+    }
+    const bool whole = t0 + kBlock <= min(vis[0].end, vis[1].end) &&
+                       (t0 >= vis[0].gap1 || t0 + kBlock <= vis[0].gap0) &&
+                       (t0 >= vis[1].gap1 || t0 + kBlock <= vis[1].gap0);
+    float big[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int j = 0; j < kBlock / 8; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sc[j][i] *= qf;
+        if (!whole && !sees(vis[i >> 1], t0 + 8 * j + 2 * c + (i & 1))) sc[j][i] = -INFINITY;
+        big[i >> 1] = fmaxf(big[i >> 1], sc[j][i]);
+      }
+    float alpha[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const float m = fmaxf(top[r], quad_max(big[r]));
+      const float base = m == -INFINITY ? 0.f : m;
+      alpha[r] = exp2_approx(top[r] - base);
+      top[r] = m;
+      float add = 0.f;
+#pragma unroll
+      for (int j = 0; j < kBlock / 8; ++j) {
+        sc[j][2 * r] = exp2_approx(sc[j][2 * r] - base);
+        sc[j][2 * r + 1] = exp2_approx(sc[j][2 * r + 1] - base);
+        add += sc[j][2 * r] + sc[j][2 * r + 1];
+      }
+      sum[r] = fmaf(sum[r], alpha[r], add);
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[nt][i] *= alpha[i >> 1];
+    if (!kF32) {
+#pragma unroll
+      for (int kt = 0; kt < kBlock / 16; ++kt) {
+        uint32_t vw[4][VW];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          load_row_words<VW, true>(vw[i], vp + min(t0 + 16 * kt + 2 * c + (i & 1) + 8 * (i >> 1), s.len - 1) * v_step, p.vec);
+        uint32_t pa[4];
+        if (DT == DLRM_DTYPE_BF16) {
+          pa[0] = pack_bf16(sc[2 * kt][0], sc[2 * kt][1]);
+          pa[1] = pack_bf16(sc[2 * kt][2], sc[2 * kt][3]);
+          pa[2] = pack_bf16(sc[2 * kt + 1][0], sc[2 * kt + 1][1]);
+          pa[3] = pack_bf16(sc[2 * kt + 1][2], sc[2 * kt + 1][3]);
+        } else {
+          pa[0] = pack_f16x2(sc[2 * kt][0], sc[2 * kt][1]);
+          pa[1] = pack_f16x2(sc[2 * kt][2], sc[2 * kt][3]);
+          pa[2] = pack_f16x2(sc[2 * kt + 1][0], sc[2 * kt + 1][1]);
+          pa[3] = pack_f16x2(sc[2 * kt + 1][2], sc[2 * kt + 1][3]);
+        }
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+          // a pair of events side by side: n tiles 2w and 2w + 1
+          const uint32_t l0 = __byte_perm(vw[0][w], vw[1][w], 0x5410);
+          const uint32_t l1 = __byte_perm(vw[0][w], vw[1][w], 0x7632);
+          const uint32_t h0 = __byte_perm(vw[2][w], vw[3][w], 0x5410);
+          const uint32_t h1 = __byte_perm(vw[2][w], vw[3][w], 0x7632);
+          if (DT == DLRM_DTYPE_BF16) {
+            mma_bf16(o[2 * w], pa, l0, h0);
+            mma_bf16(o[2 * w + 1], pa, l1, h1);
+          } else {
+            mma_f16(o[2 * w], pa, l0, h0);
+            mma_f16(o[2 * w + 1], pa, l1, h1);
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kBlock / 8; ++j) {
+        uint32_t vw[2][VW], hi[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          load_row_words<VW, false>(vw[i], vp + min(t0 + 8 * j + 2 * c + i, s.len - 1) * v_step, p.vec);
+        const float pr[4] = {sc[j][0], sc[j][2], sc[j][1], sc[j][3]};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          hi[i] = __float_as_uint(pr[i]) & 0xffffe000u;
+          lo[i] = __float_as_uint(pr[i] - __uint_as_float(hi[i]));
+        }
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+          const uint32_t h0 = vw[0][w] & 0xffffe000u, h1 = vw[1][w] & 0xffffe000u;
+          const uint32_t l0 = __float_as_uint(__uint_as_float(vw[0][w]) - __uint_as_float(h0));
+          const uint32_t l1 = __float_as_uint(__uint_as_float(vw[1][w]) - __uint_as_float(h1));
+          mma_tf32(o[w], lo, h0, h1);
+          mma_tf32(o[w], hi, l0, l1);
+          mma_tf32(o[w], hi, h0, h1);
+        }
+      }
+    }
+  }
+
+  uint32_t odd = 0;                               // rows to be done again, by bit
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const float l = quad_sum(sum[r]);
+    const int row = row0 + g + 8 * r;
+    const bool in = row <= last_row;
+    const int i = row / p.group, hq = head * p.group + row % p.group;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t at_o = (s.q0 + static_cast<int64_t>(i)) * p.a.ld_out + hq * p.a.ld_out_head;
+    bool bad = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float x = l == 0.f ? 0.f : o[nt][2 * r + e] * inv;
+        bad |= !finite(x);
+        if (in) store_element<DT>(p.a.out, at_o + (2 * c + e) * (D / 8) + nt, x);
+      }
+    }
+    if (in && c == 0 && p.a.lse)
+      p.a.lse[(s.q0 + static_cast<int64_t>(i)) * p.a.n_heads + hq] =
+          l == 0.f ? -INFINITY : top[r] * kLn2 + logf(l);
+    const unsigned who = __ballot_sync(0xffffffffu, bad && in);
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      if ((who >> (4 * x)) & 0xfu) odd |= 1u << (x + 8 * r);
+  }
+  __syncwarp();
+  for (; odd; odd &= odd - 1) careful_row<D, DT>(p, s, head, row0 + __ffs(odd) - 1);
+}
+
+template <int D, int DT>
+cudaError_t launch(const Params& p, cudaStream_t stream) {
+  const int64_t tiles = p.a.q_rows * p.group / kTileRows + p.a.batch;
+  const int64_t grid = tiles * p.a.n_kv_heads;
+  return launch_pdl(window_attention_kernel<D, DT>, dim3(static_cast<unsigned>(grid)),
+                    dim3(kThreads), 0, stream, p);
+}
+
+template <int D>
+cudaError_t launch_d(const Params& p, cudaStream_t stream) {
+  if (p.a.dtype == DLRM_DTYPE_FP32) return launch<D, DLRM_DTYPE_FP32>(p, stream);
+  if (p.a.dtype == DLRM_DTYPE_BF16) return launch<D, DLRM_DTYPE_BF16>(p, stream);
+  return launch<D, DLRM_DTYPE_FP16>(p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_window_attention(const dlrm_attention_t& a, cudaStream_t stream) {
+  Params p;
+  p.a = a;
+  p.group = a.n_heads / a.n_kv_heads;
+  const int64_t eb = dtype_bytes(a.dtype);
+  auto vec = [&](const void* x, int64_t ld, int64_t ld_head) {
+    return reinterpret_cast<uintptr_t>(x) % 16 == 0 && ld * eb % 16 == 0 && ld_head * eb % 16 == 0;
+  };
+  p.vec = vec(a.q, a.ld_q, a.ld_q_head) && vec(a.k, a.ld_k, a.ld_k_head) &&
+          vec(a.v, a.ld_v, a.ld_v_head);
+  if (a.head_dim == 32) return launch_d<32>(p, stream);
+  if (a.head_dim == 64) return launch_d<64>(p, stream);
+  return launch_d<128>(p, stream);
+}
+
+}  // namespace dlrm

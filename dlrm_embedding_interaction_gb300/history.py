@@ -1,0 +1,347 @@
+"""Event histories: an 8-bit paged cache of keys and values, attention over
+it, and windowed attention over plain rows.
+
+Argument checks and marshalling only, like the rest of the binding:
+include/dlrm.h defines the pool, the codes and every operator, and says which
+faults only the device sees (they set bits in the cache's error word, read by
+``HistoryCache.error()``). Nothing here waits for the GPU but ``error()``.
+
+    cache = HistoryCache(n_pages, n_slots, max_pages, n_heads, head_dim)
+    history_append(cache, slots, starts, k, v)            # (rows, n_heads, head_dim)
+    out = history_attention(cache, slots, starts, q)      # (rows, query heads, head_dim)
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+from . import (DlrmError, ERR_INDEX_OOB, ERR_INVALID_ARG, ERR_OOM, ERR_TIMEOUT, ERR_UNSUPPORTED,
+               OK, _check, _stream, lib)
+
+DTYPE_FP32, DTYPE_BF16, DTYPE_FP16 = 0, 1, 2
+PAGE_TOKENS = (32, 64, 128)
+HEAD_DIMS = (32, 64, 128)
+
+_VP, _I32, _I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+
+
+class _History(ctypes.Structure):
+    _fields_ = ([(n, _I32) for n in ("n_pages", "page_tokens", "n_heads", "head_dim", "n_slots",
+                                     "max_pages")]
+                + [(n, _VP) for n in ("k_codes", "v_codes", "k_scales", "v_scales", "table",
+                                      "lengths", "refs", "free_pages", "n_free", "err", "work")]
+                + [("work_bytes", _I64)])
+
+
+class _Attention(ctypes.Structure):
+    _fields_ = ([(n, _VP) for n in ("q", "k", "v", "out", "lse", "slots", "q_starts", "k_starts")]
+                + [(n, _I64) for n in ("q_rows", "k_rows", "ld_q", "ld_q_head", "ld_k", "ld_k_head",
+                                       "ld_v", "ld_v_head", "ld_out", "ld_out_head")]
+                + [(n, _I32) for n in ("batch", "n_heads", "n_kv_heads", "head_dim", "dtype",
+                                       "causal", "window", "sinks")]
+                + [("scale", ctypes.c_float), ("err", _VP)])
+
+
+def _bind(lib_):
+    st, h, a = ctypes.c_int, ctypes.POINTER(_History), ctypes.POINTER(_Attention)
+    sig = {
+        "history_work_bytes": ([h], _I64),
+        "history_reset": ([h, _VP], st),
+        "history_append": ([h, _VP, _VP, _I32, _VP, _I64, _I64, _VP, _I64, _I64, _I64, _I32, _VP],
+                           st),
+        "history_fork": ([h, _VP, _VP, _I32, _VP], st),
+        "history_copy": ([h, _VP, _VP, _I32, _VP], st),
+        "history_free": ([h, _VP, _I32, _VP], st),
+        "history_trim": ([h, _VP, _I32, _I32, _I32, _VP], st),
+        "history_compact": ([h, _VP], st),
+        "history_attention": ([h, a, _VP], st),
+        "window_attention": ([a, _VP], st),
+    }
+    for name, (args, res) in sig.items():
+        fn = getattr(lib_, name)
+        fn.argtypes, fn.restype = args, res
+
+
+def _dtype_code(t, name: str) -> int:
+    import torch
+    codes = {torch.float32: DTYPE_FP32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16}
+    if t.dtype not in codes:
+        raise TypeError(f"{name}: expected float32, bfloat16 or float16, got {t.dtype}")
+    return codes[t.dtype]
+
+
+def _int32_vector(t, name: str, n: Optional[int], device) -> int:
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
+        raise TypeError(f"{name}: expected an int32 tensor")
+    if t.dim() != 1 or (n is not None and t.shape[0] != n):
+        raise ValueError(f"{name}: expected ({'n' if n is None else n},), got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name}: must be on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.shape[0]
+
+
+def _rows(t, name: str, heads: Optional[int], dim: Optional[int], device):
+    """A (rows, heads, dim) tensor with unit stride along dim."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (
+            dim is not None and t.shape[2] != dim):
+        raise ValueError(f"{name}: expected (rows, {heads or 'heads'}, {dim or 'dim'}), "
+                         f"got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name}: must be on {device}")
+    if t.numel() and t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: its last dimension must be contiguous")
+
+
+class HistoryCache:
+    """A pool of pages for event histories and the tables of its slots.
+
+    ``n_pages`` pages of ``page_tokens`` events of ``n_heads`` heads; ``n_slots``
+    histories of at most ``max_pages`` pages each. The tensors (``k_codes``,
+    ``v_codes``, ``k_scales``, ``v_scales``, ``table``, ``lengths``, ``refs``,
+    ``free_pages``, ``n_free``, ``err``) are the caller's to read, e.g. to save
+    a pool; calls on one cache go to one stream.
+    """
+
+    def __init__(self, n_pages: int, n_slots: int, max_pages: int, n_heads: int, head_dim: int,
+                 page_tokens: int = 64, device="cuda", stream=None):
+        import torch
+        device = torch.device(device)
+        if device.type != "cuda":
+            raise ValueError("HistoryCache: device must be a CUDA device")
+        c = _History(int(n_pages), int(page_tokens), int(n_heads), int(head_dim), int(n_slots),
+                     int(max_pages))
+        bound = _bound()
+        work = int(bound.history_work_bytes(ctypes.byref(c)))
+        if work < 0:
+            bad = min(n_pages, n_slots, max_pages, n_heads) < 1
+            raise DlrmError(ERR_INVALID_ARG if bad else ERR_UNSUPPORTED, "HistoryCache")
+        if device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        shape = (n_pages, n_heads, page_tokens, head_dim)
+        new = dict(device=device)
+        i32 = dict(dtype=torch.int32, device=device)
+        self.k_codes = torch.zeros(shape, dtype=torch.uint8, **new).view(torch.float8_e4m3fn)
+        self.v_codes = torch.zeros(shape, dtype=torch.uint8, **new).view(torch.float8_e4m3fn)
+        self.k_scales = torch.zeros(shape[:2], **new)
+        self.v_scales = torch.zeros(shape[:2], **new)
+        self.table = torch.empty((n_slots, max_pages), **i32)
+        self.lengths = torch.empty(n_slots, **i32)
+        self.refs = torch.empty(n_pages, **i32)
+        self.free_pages = torch.empty(n_pages, **i32)
+        self.n_free = torch.empty(1, **i32)
+        self.err = torch.empty(1, **i32)
+        self._work = torch.empty(work, dtype=torch.uint8, **new)
+        for name in ("k_codes", "v_codes", "k_scales", "v_scales", "table", "lengths", "refs",
+                     "free_pages", "n_free", "err"):
+            setattr(c, name, getattr(self, name).data_ptr())
+        c.work, c.work_bytes = self._work.data_ptr(), work
+        self.device, self.n_slots, self.max_pages = device, int(n_slots), int(max_pages)
+        self.n_heads, self.head_dim, self.page_tokens = int(n_heads), int(head_dim), int(page_tokens)
+        self._c, self._ref = c, ctypes.byref(c)
+        self.reset(stream)
+
+    def reset(self, stream=None) -> None:
+        """Every page free, every slot empty, the error word cleared."""
+        _check(_bound().history_reset(self._ref, _stream(stream)), "history_reset")
+
+    def error(self, stream=None) -> int:
+        """Waits for ``stream``, returns the first error that the device recorded
+        since the last call (INDEX_OOB before UNSUPPORTED, OOM, INVALID_ARG and
+        TIMEOUT; OK if none) and clears it."""
+        import torch
+        s = torch.cuda.current_stream(self.device) if stream is None else stream
+        if not isinstance(s, torch.cuda.Stream):
+            s = torch.cuda.ExternalStream(int(s), device=self.device)
+        with torch.cuda.stream(s):
+            bits = int(self.err.item())
+            if bits:
+                self.err.zero_()
+        for code in (ERR_INDEX_OOB, ERR_UNSUPPORTED, ERR_OOM, ERR_INVALID_ARG, ERR_TIMEOUT):
+            if bits & (1 << code):
+                return code
+        return OK
+
+
+_bound_lib = None
+
+
+def _bound():
+    global _bound_lib
+    if _bound_lib is None:
+        loaded = lib()
+        _bind(loaded)
+        _bound_lib = loaded
+    return _bound_lib
+
+
+def _cache_of(cache, where: str):
+    if not isinstance(cache, HistoryCache):
+        raise TypeError(f"{where}: cache must be a HistoryCache")
+    return cache
+
+
+def history_append(cache: HistoryCache, slots, starts, k, v, stream=None) -> None:
+    """Appends rows [starts[b], starts[b+1]) of ``k`` and ``v``, (rows, n_heads,
+    head_dim) in float32, bfloat16 or float16, to history ``slots[b]``. ``slots``
+    (B,) and ``starts`` (B+1,) are int32; a slot occurs once."""
+    where = "history_append"
+    c = _cache_of(cache, where)
+    b = _int32_vector(slots, f"{where}: slots", None, c.device)
+    _int32_vector(starts, f"{where}: starts", b + 1, c.device)
+    dt = _dtype_code(k, f"{where}: k")
+    if v.dtype != k.dtype:
+        raise TypeError(f"{where}: v: expected {k.dtype}, got {v.dtype}")
+    _rows(k, f"{where}: k", c.n_heads, c.head_dim, c.device)
+    _rows(v, f"{where}: v", c.n_heads, c.head_dim, c.device)
+    if k.shape[0] != v.shape[0]:
+        raise ValueError(f"{where}: k and v must have as many rows")
+    if b > c.n_slots:
+        raise ValueError(f"{where}: {b} requests for {c.n_slots} slots")
+    _check(_bound().history_append(c._ref, slots.data_ptr(), starts.data_ptr(), b, k.data_ptr(),
+                                   k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
+                                   v.stride(1), k.shape[0], dt, _stream(stream)), where)
+
+
+def _slots_call(name: str, cache, vectors, stream, *more) -> None:
+    c = _cache_of(cache, name)
+    b = None
+    for label, t in vectors:
+        b = _int32_vector(t, f"{name}: {label}", b, c.device)
+    if b > c.n_slots:
+        raise ValueError(f"{name}: {b} requests for {c.n_slots} slots")
+    _check(getattr(_bound(), name)(c._ref, *[t.data_ptr() for _, t in vectors], b, *more,
+                                   _stream(stream)), name)
+
+
+def history_fork(cache: HistoryCache, src, dst, stream=None) -> None:
+    """The empty slot ``dst[b]`` becomes a history like ``src[b]``'s: full pages are
+    shared, a last page that is not full is copied."""
+    _slots_call("history_fork", cache, (("src", src), ("dst", dst)), stream)
+
+
+def history_copy(cache: HistoryCache, src, dst, stream=None) -> None:
+    """As history_fork, with every page copied."""
+    _slots_call("history_copy", cache, (("src", src), ("dst", dst)), stream)
+
+
+def history_free(cache: HistoryCache, slots, stream=None) -> None:
+    """Empties slots; pages that no slot holds any more become free."""
+    _slots_call("history_free", cache, (("slots", slots),), stream)
+
+
+def history_trim(cache: HistoryCache, slots, window: int, sinks: int = 0, stream=None) -> None:
+    """Gives up the pages that attention with this window and these sinks no
+    longer reads, in queries at the histories' ends or later."""
+    if window < 1 or sinks < 0:
+        raise ValueError("history_trim: window must be at least 1, sinks at least 0")
+    _slots_call("history_trim", cache, (("slots", slots),), stream, int(window), int(sinks))
+
+
+def history_compact(cache: HistoryCache, stream=None) -> None:
+    """Moves pages in use to the front of the pool and rebuilds the free stack."""
+    _check(_bound().history_compact(_cache_of(cache, "history_compact")._ref, _stream(stream)),
+           "history_compact")
+
+
+def _attention(where, a, q, out, lse, scale, window, sinks, device):
+    import torch
+    a.dtype = _dtype_code(q, f"{where}: q")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=device)
+    elif out.dtype != q.dtype:
+        raise TypeError(f"{where}: out: expected {q.dtype}, got {out.dtype}")
+    _rows(out, f"{where}: out", q.shape[1], q.shape[2], device)
+    if out.shape[0] != q.shape[0]:
+        raise ValueError(f"{where}: out: expected {q.shape[0]} rows, got {out.shape[0]}")
+    if lse is not None:
+        if not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32:
+            raise TypeError(f"{where}: lse: expected a float32 tensor")
+        if tuple(lse.shape) != tuple(q.shape[:2]) or lse.device != device or not lse.is_contiguous():
+            raise ValueError(f"{where}: lse: expected contiguous {tuple(q.shape[:2])} on {device}")
+        a.lse = lse.data_ptr()
+    if window < 0 or sinks < 0:
+        raise ValueError(f"{where}: window and sinks must not be negative")
+    a.q, a.out = q.data_ptr(), out.data_ptr()
+    a.q_rows, a.n_heads, a.head_dim = q.shape
+    a.ld_q, a.ld_q_head = q.stride(0), q.stride(1)
+    a.ld_out, a.ld_out_head = out.stride(0), out.stride(1)
+    a.window, a.sinks = int(window), int(sinks)
+    a.scale = q.shape[2] ** -0.5 if scale is None else float(scale)
+    return out
+
+
+def history_attention(cache: HistoryCache, slots, starts, q, out=None, *, scale=None,
+                      causal: bool = False, window: int = 0, sinks: int = 0, lse=None,
+                      stream=None):
+    """Attention of the query rows [starts[b], starts[b+1]) of ``q``, (rows, query
+    heads, head_dim), over history ``slots[b]``; returns ``out``.
+
+    Query heads are a multiple of the cache's heads; consecutive ones share a
+    head. With ``causal`` the rows are the history's last events; otherwise each
+    sees all of it (candidates to rank). ``window`` > 0 leaves a row the last
+    ``window`` events and the first ``sinks``. ``scale`` defaults to head_dim
+    ** -0.5. ``lse``, (rows, query heads) float32, receives the log of the sum of
+    exponentials."""
+    where = "history_attention"
+    c = _cache_of(cache, where)
+    b = _int32_vector(slots, f"{where}: slots", None, c.device)
+    _int32_vector(starts, f"{where}: starts", b + 1, c.device)
+    _rows(q, f"{where}: q", None, c.head_dim, c.device)
+    if q.shape[1] < 1 or q.shape[1] % c.n_heads:
+        raise ValueError(f"{where}: q: {q.shape[1]} heads are no multiple of the cache's {c.n_heads}")
+    a = _Attention()
+    out = _attention(where, a, q, out, lse, scale, window, sinks, c.device)
+    a.slots, a.q_starts, a.batch, a.causal = slots.data_ptr(), starts.data_ptr(), b, int(causal)
+    _check(_bound().history_attention(c._ref, ctypes.byref(a), _stream(stream)), where)
+    return out
+
+
+def window_attention(q, k, v, starts, out=None, *, k_starts=None, scale=None, window: int = 0,
+                     sinks: int = 0, lse=None, err_flag=None, stream=None):
+    """Causal attention of ragged rows over plain keys and values; returns ``out``.
+
+    Sequence b has the query rows [starts[b], starts[b+1]) of ``q`` (rows, heads,
+    head_dim) and the rows [k_starts[b], k_starts[b+1]) of ``k`` and ``v`` (rows,
+    kv heads, head_dim); ``k_starts`` defaults to ``starts``. Its queries stand at
+    the last positions of its keys. ``window``, ``sinks``, ``scale`` and ``lse`` as in
+    history_attention. ``err_flag``: (1,) int32, receives the error bit of bad starts."""
+    import torch
+    where = "window_attention"
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{where}: {name} must be a torch.Tensor")
+        if t.dtype != q.dtype:
+            raise TypeError(f"{where}: {name}: expected {q.dtype}, got {t.dtype}")
+    if not q.is_cuda:
+        raise ValueError(f"{where}: q must be a CUDA tensor")
+    dev = q.device
+    _rows(q, f"{where}: q", None, None, dev)
+    _rows(k, f"{where}: k", None, q.shape[2], dev)
+    _rows(v, f"{where}: v", k.shape[1], q.shape[2], dev)
+    if k.shape[0] != v.shape[0]:
+        raise ValueError(f"{where}: k and v must have as many rows")
+    if k.shape[1] < 1 or q.shape[1] < 1 or q.shape[1] % k.shape[1]:
+        raise ValueError(f"{where}: {q.shape[1]} query heads are no multiple of {k.shape[1]} kv heads")
+    if k_starts is None:
+        k_starts = starts
+    b = _int32_vector(starts, f"{where}: starts", None, dev) - 1
+    if b < 0:
+        raise ValueError(f"{where}: starts: expected at least one entry")
+    _int32_vector(k_starts, f"{where}: k_starts", b + 1, dev)
+    a = _Attention()
+    out = _attention(where, a, q, out, lse, scale, window, sinks, dev)
+    if err_flag is not None:
+        _int32_vector(err_flag, f"{where}: err_flag", 1, dev)
+        a.err = err_flag.data_ptr()
+    a.k, a.v = k.data_ptr(), v.data_ptr()
+    a.k_rows, a.n_kv_heads = k.shape[0], k.shape[1]
+    a.ld_k, a.ld_k_head, a.ld_v, a.ld_v_head = k.stride(0), k.stride(1), v.stride(0), v.stride(1)
+    a.q_starts, a.k_starts, a.batch, a.causal = starts.data_ptr(), k_starts.data_ptr(), b, 1
+    _check(_bound().window_attention(ctypes.byref(a), _stream(stream)), where)
+    return out

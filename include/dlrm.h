@@ -468,6 +468,156 @@ dlrm_status_t linear_bias_act(const float* x, int32_t ld_x, const float* W, cons
                               float* y, int32_t ld_y, int32_t M, int32_t N, int32_t K,
                               dlrm_act_t act, dlrm_math_t math, void* stream);
 
+/* ------------------------------------------------------------ event histories
+ *
+ * A user's event history as keys and values of H heads of D elements, kept
+ * between requests in a pool of pages and read by attention: the sequence
+ * counterpart of the bag sums above (a bag weighs its rows alike; attention
+ * weighs a history's events by the query, e.g. a candidate to rank). No
+ * counterpart exists on the pages.
+ *
+ * A page holds page_tokens events of every head. Keys and values are 8-bit
+ * e4m3 codes with one scale for each page, head and side, a power of two:
+ *   value = code * scale,  scale = 2^e,  e the least integer in [-60, 60] with
+ *   |x| <= 448 * 2^e for every finite x that the page holds.
+ * Codes are rounded to nearest even; an infinity (and a finite value past
+ * 448 * 2^60) becomes the largest code of its sign, a NaN stays NaN.
+ *
+ * Everything below lives in caller-owned DEVICE memory; nothing allocates.
+ *   k_codes, v_codes   (n_pages, n_heads, page_tokens, head_dim) e4m3, 16-byte
+ *                      aligned
+ *   k_scales, v_scales (n_pages, n_heads) fp32
+ *   table              (n_slots, max_pages) int32: entry j of a slot is the
+ *                      page of its events [j * page_tokens, (j+1) * page_tokens),
+ *                      -1 for none
+ *   lengths            (n_slots) int32 events per slot
+ *   refs               (n_pages) int32: slots that hold the page (0: free)
+ *   free_pages, n_free stack of the free pages: the next page taken is
+ *                      free_pages[n_free - 1]
+ *   err                (1) int32 error word: DLRM_ERRBIT_* bits are OR-ed in,
+ *                      never cleared here
+ *   work               scratch of history_work_bytes() bytes, 16-byte aligned
+ * history_reset makes the pool empty and must run once before the others.
+ * page_tokens is 32, 64 or 128, head_dim 32, 64 or 128 (else UNSUPPORTED).
+ * Calls on one pool are serialised on one stream (shared work and state).
+ *
+ * Page tables are read and changed on the device only, so no call waits for
+ * the GPU, and every result, the page numbers included, is the same in each
+ * run. What only the device can see sets a bit in err and leaves that request
+ * (not the others) without effect:
+ *   DLRM_ERRBIT_INDEX_OOB    a slot outside [0, n_slots), or a page that a
+ *                            query needs and the table does not hold
+ *   DLRM_ERRBIT_OFFSETS      starts that decrease or pass the row count
+ *   DLRM_ERRBIT_OOM          too few free pages: this request and every later
+ *                            one of the call that needs a page
+ *   DLRM_ERRBIT_INVALID_ARG  a slot written twice in one call (the first
+ *                            counts), a fork or copy into a slot that is not
+ *                            empty, a history past max_pages */
+#define DLRM_ERRBIT_INVALID_ARG (1u << DLRM_ERR_INVALID_ARG)
+#define DLRM_ERRBIT_OOM         (1u << DLRM_ERR_OOM)
+
+/* Element types of the attention calls' rows. */
+typedef enum { DLRM_DTYPE_FP32 = 0, DLRM_DTYPE_BF16 = 1, DLRM_DTYPE_FP16 = 2 } dlrm_dtype_t;
+
+typedef struct {
+  int32_t n_pages, page_tokens, n_heads, head_dim, n_slots, max_pages;
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  float* k_scales;
+  float* v_scales;
+  int32_t* table;
+  int32_t* lengths;
+  int32_t* refs;
+  int32_t* free_pages;
+  int32_t* n_free;
+  int32_t* err;
+  void* work;
+  int64_t work_bytes;
+} dlrm_history_t;
+
+/* Bytes of scratch for a pool of this shape (the pointers are not read), or
+ * -1 for a shape that history_reset refuses. */
+int64_t history_work_bytes(const dlrm_history_t* h);
+
+/* Empties the pool: every page free (page 0 the first to be taken), every slot
+ * empty, err cleared, scratch initialised. Codes and scales stay as they are. */
+dlrm_status_t history_reset(const dlrm_history_t* h, void* stream);
+
+/* Appends events: request b adds rows [starts[b], starts[b+1]) of k and v, in
+ * order, to slots[b].
+ *   slots (batch) int32, starts (batch + 1) int32, batch <= n_slots
+ *   k, v  (rows, n_heads, head_dim) of `dtype`, element (t, h, d) at
+ *         t * ld + h * ld_head + d (strides in elements) */
+dlrm_status_t history_append(const dlrm_history_t* h, const int32_t* slots, const int32_t* starts,
+                             int32_t batch, const void* k, int64_t ld_k, int64_t ld_k_head,
+                             const void* v, int64_t ld_v, int64_t ld_v_head, int64_t rows,
+                             int32_t dtype, void* stream);
+
+/* dst[b], an empty slot, becomes a history like src[b]'s: history_fork shares
+ * every full page (refs) and copies a last page that is not full, so that each
+ * side can append on its own; history_copy copies every page. A source may
+ * occur many times. Both read the slots as they were before the call. */
+dlrm_status_t history_fork(const dlrm_history_t* h, const int32_t* src, const int32_t* dst,
+                           int32_t batch, void* stream);
+dlrm_status_t history_copy(const dlrm_history_t* h, const int32_t* src, const int32_t* dst,
+                           int32_t batch, void* stream);
+
+/* Empties slots: their pages lose a reference, and pages without one return
+ * to the free stack (the last page of the last slot first, so that what was
+ * taken last is the first to be taken again). */
+dlrm_status_t history_free(const dlrm_history_t* h, const int32_t* slots, int32_t batch,
+                           void* stream);
+
+/* history_free of the pages that attention with this window and these sinks
+ * no longer reads in queries at the history's end or later: all their events
+ * lie at or after `sinks` and before length - window. Lengths stay. window >= 1. */
+dlrm_status_t history_trim(const dlrm_history_t* h, const int32_t* slots, int32_t batch,
+                           int32_t window, int32_t sinks, void* stream);
+
+/* Packs the pool: with n pages in use, those numbered n and above move (in
+ * ascending order) into the free ones below n, tables follow, and the free
+ * stack is rebuilt with page n on top. */
+dlrm_status_t history_compact(const dlrm_history_t* h, void* stream);
+
+/* Attention of ragged queries; request b has the query rows
+ * [q_starts[b], q_starts[b+1]):
+ *   out[i][hq] = sum_t p[t] v[t][hk],  p = softmax over the visible events t of
+ *                scale * <q[i][hq], k[t][hk]>,  hk = hq / (n_heads / n_kv_heads)
+ * Row i of a request's n rows over `len` events stands at position
+ * len - n + i with causal != 0, else at len - 1. Event t is visible when
+ * t < len, t <= position, and, with window > 0, t > position - window or
+ * t < sinks. A row that sees nothing gets zeros and lse -infinity. Scores,
+ * softmax statistics and sums are fp32; masked events have no influence,
+ * whatever they hold.
+ *   q, out  (q_rows, n_heads, head_dim) of dtype; (t, h, d) at
+ *           t * ld + h * ld_head + d; out must not overlap an input
+ *   lse     (q_rows, n_heads) fp32 or NULL: log of the sum of exponentials
+ * history_attention reads the events of slots[b] from a pool (k, v, k_starts,
+ * k_rows and their strides are not read; n_kv_heads and head_dim are the
+ * pool's); window_attention reads rows [k_starts[b], k_starts[b+1]) of k and v,
+ * (k_rows, n_kv_heads, head_dim) of dtype, is always causal, and flags bad
+ * starts in err (NULL allowed): such a request has no rows.
+ * head_dim is 32, 64 or 128 (else UNSUPPORTED). */
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* out;
+  float* lse;
+  const int32_t* slots;
+  const int32_t* q_starts;
+  const int32_t* k_starts;
+  int64_t q_rows, k_rows;
+  int64_t ld_q, ld_q_head, ld_k, ld_k_head, ld_v, ld_v_head, ld_out, ld_out_head;
+  int32_t batch, n_heads, n_kv_heads, head_dim;
+  int32_t dtype, causal, window, sinks;
+  float scale;
+  int32_t* err;
+} dlrm_attention_t;
+
+dlrm_status_t history_attention(const dlrm_history_t* h, const dlrm_attention_t* a, void* stream);
+dlrm_status_t window_attention(const dlrm_attention_t* a, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
