@@ -11,7 +11,7 @@
 //   bf16, fp16: m16n8k16 in the input's own type; P is rounded to that type.
 //   fp32: m16n8k8 in tf32, three products per product (head * head,
 //     head * rest, rest * head), errors as of fp32.
-#include "attention.cuh"
+#include "window_attention.cuh"
 
 namespace dlrm {
 
@@ -21,30 +21,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * kWarp;
 constexpr int kBlock = 32;
 constexpr int kTileRows = kWarps * 16;
-
-struct Params {
-  dlrm_attention_t a;
-  int group;
-  int vec;                                       // rows can be loaded 16 bytes at a time
-};
-
-struct Span {
-  int q0, k0, rows, len, tiles;
-};
-
-__device__ __forceinline__ Span span_of(const Params& p, int b, bool report) {
-  Span s;
-  const int q0 = p.a.q_starts[b], q1 = p.a.q_starts[b + 1];
-  const int k0 = p.a.k_starts[b], k1 = p.a.k_starts[b + 1];
-  const bool bad = q0 < 0 || q1 < q0 || q1 > p.a.q_rows || k0 < 0 || k1 < k0 || k1 > p.a.k_rows;
-  if (bad && report) flag(p.a.err, DLRM_ERRBIT_OFFSETS);
-  s.q0 = q0;
-  s.k0 = k0;
-  s.rows = bad ? 0 : (q1 - q0) * p.group;
-  s.len = bad ? 0 : k1 - k0;
-  s.tiles = (s.rows + kTileRows - 1) / kTileRows;
-  return s;
-}
+using Params = WindowParams;
 
 // N consecutive 32-bit words at a byte address, 16 bytes at a time if aligned.
 template <int N, bool HALF>
@@ -75,51 +52,6 @@ __device__ __forceinline__ void load_row_words(uint32_t* w, const uint8_t* p, bo
   }
 }
 
-// One row from the definition, event by event, by one warp: for a row whose
-// output is not finite (0 * a masked event's infinity or NaN).
-template <int D, int DT>
-__device__ __noinline__ void careful_row(const Params& p, const Span& s, int head, int row) {
-  const int lane = threadIdx.x % kWarp;
-  const int i = row / p.group, hq = head * p.group + row % p.group;
-  const Visible v = visible(s.len - s.rows / p.group + i, s.len, p.a.window, p.a.sinks);
-  const int64_t q_at = (s.q0 + static_cast<int64_t>(i)) * p.a.ld_q + hq * p.a.ld_q_head;
-  constexpr int N = D / kWarp;
-  float q[N], acc[N];
-#pragma unroll
-  for (int e = 0; e < N; ++e) {
-    q[e] = load_element<DT>(p.a.q, q_at + lane + 32 * e) * (p.a.scale * kLog2e);
-    acc[e] = 0.f;
-  }
-  float top = -INFINITY, sum = 0.f;
-  for (int t = 0; t < v.end; ++t) {
-    if (!sees(v, t)) {
-      t = v.gap1 - 1;
-      continue;
-    }
-    const int64_t kt = s.k0 + static_cast<int64_t>(t);
-    float x = 0.f;
-#pragma unroll
-    for (int e = 0; e < N; ++e)
-      x = fmaf(q[e], load_element<DT>(p.a.k, kt * p.a.ld_k + head * p.a.ld_k_head + lane + 32 * e), x);
-#pragma unroll
-    for (int d = 16; d > 0; d /= 2) x += __shfl_xor_sync(0xffffffffu, x, d);
-    const float m = (x > top || x != x) ? x : top;              // a NaN stays
-    const float base = m == -INFINITY ? 0.f : m;
-    const float f = exp2f(top - base), w = exp2f(x - base);
-    top = m;
-    sum = fmaf(sum, f, w);
-#pragma unroll
-    for (int e = 0; e < N; ++e)
-      acc[e] = fmaf(acc[e], f, w * load_element<DT>(p.a.v, kt * p.a.ld_v + head * p.a.ld_v_head + lane + 32 * e));
-  }
-  const int64_t o = (s.q0 + static_cast<int64_t>(i)) * p.a.ld_out + hq * p.a.ld_out_head;
-#pragma unroll
-  for (int e = 0; e < N; ++e) store_element<DT>(p.a.out, o + lane + 32 * e, sum == 0.f ? 0.f : acc[e] / sum);
-  if (lane == 0 && p.a.lse)
-    p.a.lse[(s.q0 + static_cast<int64_t>(i)) * p.a.n_heads + hq] =
-        sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
-}
-
 template <int D, int DT>
 __global__ void __launch_bounds__(kThreads) window_attention_kernel(const Params p) {
   constexpr bool kF32 = DT == DLRM_DTYPE_FP32;
@@ -128,7 +60,6 @@ __global__ void __launch_bounds__(kThreads) window_attention_kernel(const Params
   constexpr int KW = D / 4 / EW;                  // words of a thread and row: D/4 elements
   constexpr int VW = D / 8 / EW;
   constexpr int NT = D / 8;
-  constexpr int kQ = kF32 ? 2 * KW : KW;          // query words of a thread, both rows
   __shared__ int64_t scan[40];
   const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
   const int g = lane / 4, c = lane % 4;
@@ -140,12 +71,12 @@ __global__ void __launch_bounds__(kThreads) window_attention_kernel(const Params
   // CTA (tile, head) with the head fastest
   const int64_t unit = blockIdx.x / heads;
   const int head = blockIdx.x % heads;
-  locate<kThreads>(p.a.batch, [&](int i) { return static_cast<int64_t>(span_of(p, i, false).tiles); },
+  locate<kThreads>(p.a.batch, [&](int i) { return static_cast<int64_t>(window_span(p, i, kTileRows, false).tiles); },
                    unit, scan, b, at, total);
   if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < p.a.batch; i += kThreads) span_of(p, i, true);
+    for (int i = threadIdx.x; i < p.a.batch; i += kThreads) window_span(p, i, kTileRows, true);
   if (unit >= total) return;
-  const Span s = span_of(p, b, false);
+  const WindowSpan s = window_span(p, b, kTileRows, false);
   const int row0 = static_cast<int>(unit - at) * kTileRows + warp * 16;
   if (row0 >= s.rows) return;                     // no barrier follows
   const int last_row = min(row0 + 15, s.rows - 1);
@@ -344,7 +275,7 @@ __global__ void __launch_bounds__(kThreads) window_attention_kernel(const Params
       if ((who >> (4 * x)) & 0xfu) odd |= 1u << (x + 8 * r);
   }
   __syncwarp();
-  for (; odd; odd &= odd - 1) careful_row<D, DT>(p, s, head, row0 + __ffs(odd) - 1);
+  for (; odd; odd &= odd - 1) window_careful_row<D, DT>(p, s, head, row0 + __ffs(odd) - 1);
 }
 
 template <int D, int DT>
@@ -365,6 +296,7 @@ cudaError_t launch_d(const Params& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_window_attention(const dlrm_attention_t& a, cudaStream_t stream) {
+  if (window_tc_takes(a)) return launch_window_attention_tc(a, stream);
   Params p;
   p.a = a;
   p.group = a.n_heads / a.n_kv_heads;

@@ -1,0 +1,760 @@
+// window_attention on the 5th-generation tensor cores: bf16 and fp16 rows that
+// TMA can read (window_attention.cu takes every other call).
+//
+// A work unit is 256 rows, as two tiles of 128 (the MMA's M), of one kv head of
+// a request; rows are (query, head of the group) pairs. Persistent CTAs, one
+// per SM, take units round-robin. Per unit the keys that any of its rows sees
+// flow by in key tiles of at most 128 events: the sinks that lie apart from the
+// window first (a narrow tile), then the window from its first event on.
+//   warp 9, one lane: TMA of key and value tiles (boxes of 32 events x 64
+//     elements, 128-byte swizzle) through rings of two stages each;
+//   warps 10, 11: the queries of tile 0 and 1, loaded a unit ahead;
+//   warp 8, one lane: S_t = Q_t K^T (operands from shared memory), then, when
+//     the weights are there, O_t += P_t V (P from tensor memory, V as stored:
+//     the MN-major operand form);
+//   warps 0-3 and 4-7: softmax of tile 0 and 1. A thread owns a row: it reads
+//     its 128 scores from tensor memory, masks, takes the maximum, writes the
+//     weights in the input's type over the scores, and keeps its sum. The
+//     output is only corrected when a row's maximum has grown by more than 2^8
+//     over the reference in use (weights up to 2^8 are as exact, and the sum is
+//     fp32), which real scores do in the first tiles only.
+// While one tile's softmax runs, the tensor core works on the other's products.
+// Tensor memory: S_t (128 columns, P_t over them) and O_t (up to 128 columns).
+//
+// What bounds it: the exponentials (16 a cycle and SM: 1024 cycles a tile of
+// 128 x 128) for head_dim 32 and 64, and as much the tensor core (1024 cycles)
+// for 128.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <atomic>
+
+#include "tc.cuh"
+#include "window_attention.cuh"
+
+namespace dlrm {
+
+using namespace tc;
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kUnit = 256;                       // rows of a work unit
+constexpr int kKeys = 128;                       // events of a key tile
+constexpr int kBox = 32;                         // events of one TMA box
+constexpr int kBlockBytes = 128 * 128;           // 128 rows of 128 bytes (64 elements)
+constexpr int kStages = 2;                       // of keys, and of values
+constexpr float kSlack = 8.f;                    // log2 of the largest weight
+
+template <int D>
+struct Layout {
+  static constexpr int kBlocks = (D + 63) / 64;  // 64-element column blocks
+  static constexpr int kTile = kBlocks * kBlockBytes;
+  static constexpr int kQ = 0;                   // two query tiles
+  static constexpr int kK = 2 * kTile;
+  static constexpr int kV = kK + kStages * kTile;
+  static constexpr int kBars = kV + kStages * kTile;
+  // more than half an SM's shared memory, so that one CTA is resident: it
+  // takes all of the tensor memory
+  static constexpr int kSmem = kBars + 1024 + 256 > 120 * 1024 ? kBars + 1024 + 256 : 120 * 1024;
+  static_assert(kSmem <= 232448, "shared memory of one CTA");
+};
+
+struct Bars {
+  uint64_t q_full[2], q_empty[2], k_full[kStages], k_empty[kStages], v_full[kStages],
+      v_empty[kStages], s_full[2], p_full[2], o_full[2], o_empty[2], drain;
+  uint32_t tmem;
+  int abort;
+};
+
+struct TcParams {
+  WindowParams w;
+  int vec_out;
+  WaitCfg wait;
+};
+
+__device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count)
+               : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(
+                   smem_addr(bar)),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                            int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// Bounded wait for a phase; false once this or another thread gave up.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                       int32_t* err, uint64_t limit) {
+  const uint32_t a = smem_addr(bar);
+  const uint64_t t0 = now_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (try_wait(a, parity)) return true;
+    if ((i & 15) == 0) {
+      if (*abort_flag) return false;
+      if (now_ns() - t0 > limit) {
+        *abort_flag = 1;
+        flag(err, DLRM_ERRBIT_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+struct Waiter {
+  volatile int* abort_flag;
+  int32_t* err;
+  uint64_t limit;
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
+    if (try_wait(smem_addr(bar), parity)) return true;
+    return wait_slow(bar, parity, abort_flag, err, limit);
+  }
+  // regardless of the abort flag: work in flight
+  __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) const {
+    const uint64_t t0 = now_ns();
+    while (!try_wait(smem_addr(bar), parity)) {
+      if (now_ns() - t0 > limit) {
+        flag(err, DLRM_ERRBIT_TIMEOUT);
+        return;
+      }
+    }
+  }
+};
+
+// D (+)= A B with A in tensor memory (the weights).
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t at) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, "
+      "%27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, "
+      "%27, %28, %29, %30, %31, %32};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+// Shared-memory descriptor of a value tile as the B operand of P V: MN-major,
+// 128-byte swizzle (an event's 64 elements are a row of 128 bytes), 8-event
+// groups 1024 bytes apart, 64-element column blocks kBlockBytes apart.
+__device__ __forceinline__ uint64_t value_desc(uint32_t addr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((addr >> 4) & 0x3FFF);
+  d |= static_cast<uint64_t>(kBlockBytes >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+// One work unit: what every role derives for itself, by whole warps.
+struct Unit {
+  WindowSpan s;
+  int head, row0;                                // first row of tile 0
+  Visible first[2], last[2];                     // of each tile's first and last row
+  int rows[2];                                   // rows of each tile
+  int sink, lo, end, sink_tiles, tiles;          // keys [0, sink) and [lo, end)
+
+  // Key tile k: events [key0, key0 + n), computed `width` wide.
+  __device__ __forceinline__ void tile(int k, int& key0, int& n, int& width) const {
+    if (k < sink_tiles) {
+      key0 = k * kKeys;
+      n = min(kKeys, sink - key0);
+    } else {
+      key0 = lo + (k - sink_tiles) * kKeys;
+      n = min(kKeys, end - key0);
+    }
+    width = (n + kBox - 1) / kBox * kBox;
+  }
+  // (selects, not indexing, so that a unit stays in registers)
+  __device__ __forceinline__ int rows_of(int t) const { return t ? rows[1] : rows[0]; }
+  __device__ __forceinline__ bool needs(int t, int key0, int n) const {
+    const int end1 = t ? last[1].end : last[0].end, gap0 = t ? last[1].gap0 : last[0].gap0;
+    const int gap1 = t ? first[1].gap1 : first[0].gap1;
+    return rows_of(t) > 0 && key0 < end1 && !(key0 >= gap0 && key0 + n <= gap1);
+  }
+};
+
+// Walks the units of a CTA in order; every warp keeps one of its own.
+struct Walk {
+  int b = 0;
+  int before = 0;                                // units of the requests before b
+
+  // Warp-wide. False past the last unit.
+  __device__ __forceinline__ bool find(const WindowParams& p, int u, Unit& x) {
+    const int lane = threadIdx.x % kWarp;
+    const int heads = p.a.n_kv_heads;
+    for (;;) {
+      if (b >= p.a.batch) return false;
+      int n = 0;
+      if (b + lane < p.a.batch) n = window_span(p, b + lane, kUnit, false).tiles * heads;
+      int inc = n;
+#pragma unroll
+      for (int d = 1; d < kWarp; d *= 2) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += y;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, before + inc > u);
+      if (past) {
+        const int at = __ffs(past) - 1;
+        before += __shfl_sync(0xffffffffu, inc - n, at);
+        b += at;
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, inc, kWarp - 1);
+      b += kWarp;
+    }
+    x.s = window_span(p, b, kUnit, false);
+    const int i = u - before;
+    // the last rows of a request first: without a window they see the most
+    x.head = i % heads;
+    const int tile = x.s.tiles - 1 - i / heads;
+    x.row0 = tile * kUnit;
+    const int pos0 = x.s.len - x.s.rows / p.group;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      x.rows[t] = max(0, min(128, x.s.rows - x.row0 - 128 * t));
+      const int r0 = min(x.row0 + 128 * t, x.s.rows - 1), r1 = max(r0, r0 + x.rows[t] - 1);
+      x.first[t] = visible(pos0 + r0 / p.group, x.s.len, p.a.window, p.a.sinks);
+      x.last[t] = visible(pos0 + r1 / p.group, x.s.len, p.a.window, p.a.sinks);
+    }
+    x.end = x.rows[1] > 0 ? x.last[1].end : x.last[0].end;
+    const int gap0 = x.rows[1] > 0 ? x.last[1].gap0 : x.last[0].gap0;
+    const bool apart = x.first[0].gap1 > gap0;
+    x.lo = apart ? min(x.first[0].gap1, x.end) : 0;
+    x.sink = apart ? min(gap0, x.end) : 0;
+    x.sink_tiles = (x.sink + kKeys - 1) / kKeys;
+    x.tiles = x.sink_tiles + (x.end - x.lo + kKeys - 1) / kKeys;
+    return true;
+  }
+};
+
+template <int D, int DT>
+__global__ void __launch_bounds__(kThreads, 1)
+window_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                 const TcParams p) {
+  using L = Layout<D>;
+  constexpr int kFormat = DT == DLRM_DTYPE_BF16 ? 1 : 0;
+  // D fp32; A, B formats; M = 128; B of the second product is MN-major
+  constexpr uint32_t kIdescS = (1u << 4) | (kFormat << 7) | (kFormat << 10) | (8u << 24);
+  constexpr uint32_t kIdescO = kIdescS | (1u << 16) | (static_cast<uint32_t>(D / 8) << 17);
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* base = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  Bars& bars = *reinterpret_cast<Bars*>(base + L::kBars);
+  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+  const WindowParams& w = p.w;
+  const Waiter wait{&bars.abort, w.a.err, wait_limit_ns(p.wait)};
+
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(&bars.tmem)),
+                 "n"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      bar_init(&bars.q_full[t], 1);
+      bar_init(&bars.q_empty[t], 1);
+      bar_init(&bars.s_full[t], 1);
+      bar_init(&bars.p_full[t], 4);
+      bar_init(&bars.o_full[t], 1);
+      bar_init(&bars.o_empty[t], 4);
+    }
+    for (int i = 0; i < kStages; ++i) {
+      bar_init(&bars.k_full[i], 1);
+      bar_init(&bars.k_empty[i], 1);
+      bar_init(&bars.v_full[i], 1);
+      bar_init(&bars.v_empty[i], 1);
+    }
+    bar_init(&bars.drain, 1);
+    bars.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = bars.tmem;
+  pdl_wait();
+  pdl_trigger();
+
+  Walk walk;
+  Unit x;
+  if (warp < 8) {
+    // ------------------------------------------------------------ softmax
+    const int t = warp / 4;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + lanes + t * kKeys, o_at = tmem + lanes + 256 + t * 128;
+    const float f = w.a.scale * kLog2e;
+    uint32_t s_phase = 0, o_phase = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && walk.find(w, u, x); u += gridDim.x) {
+      if (x.rows_of(t) == 0) continue;
+      const int r = (warp & 3) * 32 + lane;
+      const int row = min(x.row0 + 128 * t + r, x.s.rows - 1);
+      const bool in = r < x.rows_of(t);
+      const Visible v =
+          visible(x.s.len - x.s.rows / w.group + row / w.group, x.s.len, w.a.window, w.a.sinks);
+      float top = -INFINITY, sum = 0.f;
+      bool any = false;
+      for (int k = 0; k < x.tiles; ++k) {
+        int key0, n, width;
+        x.tile(k, key0, n, width);
+        if (!x.needs(t, key0, n)) continue;
+        ok = __all_sync(0xffffffffu, wait(&bars.s_full[t], s_phase));
+        if (!ok) break;
+        s_phase ^= 1;
+        fence_after();
+        const int chunks = width / 32;
+        const bool whole = __all_sync(0xffffffffu, n == width && key0 + n <= v.end &&
+                                                       (key0 >= v.gap1 || key0 + n <= v.gap0));
+        // what the row sees of the tile: columns [0, a) and [b, e)
+        const int e = min(n, v.end - key0);
+        const int b = v.gap1 - key0, a = min(v.gap0 - key0, e);
+        // the scores are read twice, for the maximum and for the weights, 32 at
+        // a time with the next 32 under way: tensor memory is read much faster
+        // than the exponentials are made, and no thread needs 128 registers
+        uint32_t s[2][32];
+        auto next = [&](int c) {
+          tmem_wait_ld();
+          if (c + 1 < chunks) tmem_ld32(s[(c + 1) & 1], s_at + 32 * (c + 1));
+          if (!whole) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int col = 32 * c + i;
+              if (!(col < a || (col >= b && col < e))) s[c & 1][i] = 0xff800000u;
+            }
+          }
+        };
+        float big[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        tmem_ld32(s[0], s_at);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (c < chunks) {
+            next(c);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) big[i & 3] = fmaxf(big[i & 3], __uint_as_float(s[c & 1][i]));
+          }
+        const float m = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * f;
+        // keep the reference unless the maximum passed it by more than the slack
+        const bool grow = m > top + kSlack || (top == -INFINITY && m > -INFINITY);
+        if (__any_sync(0xffffffffu, grow)) {
+          const float alpha = grow ? exp2_approx(top - m) : 1.f;
+          if (grow) top = m;
+          sum *= alpha;
+          if (any) {                              // the products so far are complete (s_full)
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(o, o_at + c);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(o_at + c, o);
+            }
+          }
+        }
+        any = true;
+        const float off = top == -INFINITY ? 0.f : top;
+        float add[4] = {0.f, 0.f, 0.f, 0.f};
+        tmem_ld32(s[0], s_at);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (c < chunks) {
+            next(c);
+            uint32_t pw[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float p0 = exp2_approx(fmaf(__uint_as_float(s[c & 1][2 * i]), f, -off));
+              const float p1 = exp2_approx(fmaf(__uint_as_float(s[c & 1][2 * i + 1]), f, -off));
+              add[(2 * i) & 3] += p0;
+              add[(2 * i + 1) & 3] += p1;
+              pw[i] = DT == DLRM_DTYPE_BF16 ? pack_bf16(p0, p1) : pack_f16x2(p0, p1);
+            }
+            // over the scores of columns already read: 16 c + 15 < 32 (c + 1)
+            tmem_st16(s_at + 16 * c, pw);
+          }
+        sum += (add[0] + add[1]) + (add[2] + add[3]);
+        tmem_wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bars.p_full[t]);
+      }
+      if (!ok) break;
+      // ---- output
+      float inv = 0.f;
+      if (any) {
+        if (!__all_sync(0xffffffffu, wait(&bars.o_full[t], o_phase))) break;
+        o_phase ^= 1;
+        fence_after();
+        inv = sum == 0.f ? 0.f : 1.f / sum;
+      }
+      const int i = row / w.group, hq = x.head * w.group + row % w.group;
+      const int64_t q = x.s.q0 + static_cast<int64_t>(i);
+      const int64_t o_row = q * w.a.ld_out + hq * w.a.ld_out_head;
+      bool odd = false;
+#pragma unroll
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32], h[16];
+        if (any) {
+          tmem_ld32(o, o_at + c);
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          float a = 0.f, b = 0.f;
+          if (sum != 0.f) {
+            a = __uint_as_float(o[2 * j]) * inv;
+            b = __uint_as_float(o[2 * j + 1]) * inv;
+          }
+          odd |= !finite(a) || !finite(b);
+          h[j] = DT == DLRM_DTYPE_BF16 ? pack_bf16(a, b) : pack_f16x2(a, b);
+        }
+        if (in) {
+          uint16_t* out = static_cast<uint16_t*>(w.a.out) + o_row + c;
+          if (p.vec_out) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              reinterpret_cast<uint4*>(out)[j] =
+                  make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              out[2 * j] = static_cast<uint16_t>(h[j]);
+              out[2 * j + 1] = static_cast<uint16_t>(h[j] >> 16);
+            }
+          }
+        }
+      }
+      if (any) {
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bars.o_empty[t]);
+      }
+      if (in && w.a.lse)
+        w.a.lse[q * w.a.n_heads + hq] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
+      for (unsigned who = __ballot_sync(0xffffffffu, odd && in); who; who &= who - 1) {
+        __syncwarp();
+        window_careful_row<D, DT>(w, x.s, x.head, x.row0 + 128 * t + (warp & 3) * 32 + __ffs(who) - 1);
+      }
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ products
+    uint32_t k_it = 0, v_it = 0, p_phase[2] = {0, 0}, q_phase[2] = {0, 0}, o_uses[2] = {0, 0};
+    bool ok = true;
+    for (int u = blockIdx.x; ok && walk.find(w, u, x); u += gridDim.x) {
+      // tile t's product with the values of the key tile before is still due
+      bool due[2] = {false, false}, begun[2] = {false, false}, loaded[2] = {false, false};
+      int due_width = 0;
+      bool v_used = false;
+      for (int k = 0; k <= x.tiles && ok; ++k) {
+        int key0 = 0, n = 0, width = 0;
+        bool need[2] = {false, false};
+        if (k < x.tiles) {
+          x.tile(k, key0, n, width);
+          need[0] = x.needs(0, key0, n);
+          need[1] = x.needs(1, key0, n);
+        }
+        const bool k_used = need[0] || need[1];
+        if (lane == 0) {
+          const uint32_t ks = k_it % kStages, vs = v_it % kStages;
+          for (int t = 0; t < 2 && ok; ++t) {
+            if (due[t]) {
+              ok = wait(&bars.v_full[vs], (v_it / kStages) & 1) && wait(&bars.p_full[t], p_phase[t]);
+              if (ok && !begun[t] && o_uses[t] > 0) ok = wait(&bars.o_empty[t], (o_uses[t] - 1) & 1);
+              if (!ok) break;
+              p_phase[t] ^= 1;
+              fence_after();
+              const uint64_t dv = value_desc(smem_addr(base + L::kV + vs * L::kTile));
+              const uint32_t o = tmem + 256 + t * 128, pa = tmem + t * kKeys;
+              for (int j = 0; j < due_width / 16; ++j)
+                mma_ts(o, pa + 8 * j, dv + static_cast<uint64_t>(j * (2048 >> 4)), kIdescO,
+                       begun[t] || j > 0);
+              begun[t] = true;
+            }
+            if (need[t]) {
+              if (!loaded[t]) {
+                if (!(ok = wait(&bars.q_full[t], q_phase[t]))) break;
+                q_phase[t] ^= 1;
+                loaded[t] = true;
+              }
+              if (!(ok = wait(&bars.k_full[ks], (k_it / kStages) & 1))) break;
+              fence_after();
+              const uint32_t idesc = kIdescS | (static_cast<uint32_t>(width / 8) << 17);
+              const uint32_t sa = tmem + t * kKeys;
+#pragma unroll
+              for (int j = 0; j < D / 16; ++j) {
+                const uint32_t off = (j / 4) * kBlockBytes + (j % 4) * 32;
+                mma<true>(sa, smem_desc(smem_addr(base + L::kQ + t * L::kTile) + off),
+                          smem_desc(smem_addr(base + L::kK + ks * L::kTile) + off), idesc, j > 0);
+              }
+              mma_commit(smem_addr(&bars.s_full[t]));
+            }
+          }
+          if (ok && v_used) mma_commit(smem_addr(&bars.v_empty[vs]));
+          if (ok && k_used) mma_commit(smem_addr(&bars.k_empty[ks]));
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (v_used) ++v_it;
+        if (k_used) ++k_it;
+        v_used = k_used;                          // the same events' values come next
+        due[0] = need[0];
+        due[1] = need[1];
+        due_width = width;
+      }
+      if (lane == 0 && ok) {
+        for (int t = 0; t < 2; ++t)
+          if (begun[t]) {
+            // every score of the tile is made: its queries may be replaced
+            mma_commit(smem_addr(&bars.q_empty[t]));
+            mma_commit(smem_addr(&bars.o_full[t]));
+            ++o_uses[t];
+          }
+      }
+    }
+    if (lane == 0) {
+      // nothing of the tensor core's may be in flight when its memory is freed
+      mma_commit(smem_addr(&bars.drain));
+      wait.drain(&bars.drain, 0);
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ keys and values
+    uint32_t it = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && walk.find(w, u, x); u += gridDim.x) {
+      for (int k = 0; k < x.tiles && ok; ++k) {
+        int key0, n, width;
+        x.tile(k, key0, n, width);
+        if (!x.needs(0, key0, n) && !x.needs(1, key0, n)) continue;
+        if (lane == 0) {
+          const uint32_t st = it % kStages, ph = ((it / kStages) & 1) ^ 1;
+          for (int side = 0; side < 2 && ok; ++side) {
+            uint64_t* full = side ? &bars.v_full[st] : &bars.k_full[st];
+            if (it >= kStages && !(ok = wait(side ? &bars.v_empty[st] : &bars.k_empty[st], ph))) break;
+            bar_expect(full, static_cast<uint32_t>(width) * 128 * L::kBlocks);
+            const uint32_t dst = smem_addr(base + (side ? L::kV : L::kK) + st * L::kTile);
+            for (int r = 0; r < width; r += kBox)
+#pragma unroll
+              for (int c = 0; c < L::kBlocks; ++c)
+                tma_load_3d(dst + c * kBlockBytes + r * 128, side ? &map_v : &map_k, c * 64, x.head,
+                            x.s.k0 + key0 + r, full);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        ++it;
+      }
+    }
+    if (lane == 0) {
+      // loads in flight must land before the shared memory is released; after
+      // a wait that gave up, the keys of a stage may be loaded and its values not
+      const uint32_t from = it > kStages ? it - kStages : 0;
+      for (uint32_t q = from; ok && q < it; ++q) {
+        wait.drain(&bars.k_full[q % kStages], (q / kStages) & 1);
+        wait.drain(&bars.v_full[q % kStages], (q / kStages) & 1);
+      }
+      if (!ok) {
+        const uint64_t t0 = now_ns();
+        while (now_ns() - t0 < 1000000) {}        // landed long before
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ queries
+    const int t = warp - 10;
+    uint32_t it = 0;
+    for (int u = blockIdx.x; walk.find(w, u, x); u += gridDim.x) {
+      bool used = false;
+      for (int k = 0; k < x.tiles && !used; ++k) {
+        int key0, n, width;
+        x.tile(k, key0, n, width);
+        used = x.needs(t, key0, n);
+      }
+      if (!used) continue;
+      if (it > 0 && !__all_sync(0xffffffffu, wait(&bars.q_empty[t], (it - 1) & 1))) break;
+      ++it;
+      constexpr int kChunks = D / 8;              // 16-byte chunks of a row
+      constexpr int kStep = kWarp / kChunks;      // rows of one warp-wide load
+      const int ch = lane % kChunks;
+      unsigned char* dst = base + L::kQ + t * L::kTile + (ch / 8) * kBlockBytes;
+      for (int r0 = 0; r0 < 128; r0 += 8 * kStep) {
+        uint4 q[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int r = r0 + j * kStep + lane / kChunks;
+          const int row = x.row0 + 128 * t + r;
+          q[j] = make_uint4(0, 0, 0, 0);
+          if (r < x.rows_of(t))
+            q[j] = __ldg(reinterpret_cast<const uint4*>(
+                             static_cast<const uint16_t*>(w.a.q) +
+                             (x.s.q0 + static_cast<int64_t>(row / w.group)) * w.a.ld_q +
+                             (x.head * w.group + row % w.group) * w.a.ld_q_head) +
+                         ch);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<uint4*>(dst + swz_offset(r0 + j * kStep + lane / kChunks, ch % 8)) = q[j];
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) bar_arrive(&bars.q_full[t]);
+    }
+    if (blockIdx.x == 0 && t == 0)
+      for (int i = lane; i < w.a.batch; i += kWarp) window_span(w, i, kUnit, true);
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512)
+                 : "memory");
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static std::atomic<void*> fn{nullptr};
+  void* f = fn.load(std::memory_order_acquire);
+  if (!f) {
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    fn.store(f, std::memory_order_release);
+  }
+  return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+}
+
+// (rows, heads, D) with strides ld, ld_head: boxes of kBox rows x 64 elements
+// of one head; zeros past D and past the last row.
+bool encode_rows(CUtensorMap* map, const void* x, int64_t rows, int heads, int dim, int64_t ld,
+                 int64_t ld_head, int dtype) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+  if (!enc) return false;
+  if (heads == 1) ld_head = dim;                  // not used
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld_head) * 2, static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[3] = {64, 1, kBox};
+  const cuuint32_t steps[3] = {1, 1, 1};
+  return enc(map,
+             dtype == DLRM_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+             3, const_cast<void*>(x), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int DT>
+cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const TcParams& p, unsigned grid,
+                   cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
+  if (!bit || !(done.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(window_tc_kernel<D, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Layout<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  return launch_pdl(window_tc_kernel<D, DT>, dim3(grid), dim3(kThreads), Layout<D>::kSmem, stream,
+                    mk, mv, p);
+}
+
+}  // namespace
+
+bool window_tc_takes(const dlrm_attention_t& a) {
+  if (a.dtype == DLRM_DTYPE_FP32 || !(a.scale > 0.f) || a.k_rows < 1) return false;
+  auto rows_ok = [&](const void* x, int64_t ld, int64_t ld_head, int heads) {
+    return reinterpret_cast<uintptr_t>(x) % 16 == 0 && ld % 8 == 0 && (heads == 1 || ld_head % 8 == 0);
+  };
+  // TMA: strides of 16-byte multiples, below 2^40, that grow by whole multiples
+  auto tma_ok = [&](int64_t ld, int64_t ld_head) {
+    if (a.n_kv_heads == 1) return ld >= a.head_dim && ld % a.head_dim == 0 && ld < (int64_t(1) << 38);
+    return ld_head >= a.head_dim && ld > 0 && ld % ld_head == 0 && ld < (int64_t(1) << 38);
+  };
+  return rows_ok(a.q, a.ld_q, a.ld_q_head, a.n_heads) &&
+         rows_ok(a.k, a.ld_k, a.ld_k_head, a.n_kv_heads) &&
+         rows_ok(a.v, a.ld_v, a.ld_v_head, a.n_kv_heads) && tma_ok(a.ld_k, a.ld_k_head) &&
+         tma_ok(a.ld_v, a.ld_v_head);
+}
+
+cudaError_t launch_window_attention_tc(const dlrm_attention_t& a, cudaStream_t stream) {
+  TcParams p{};
+  p.w.a = a;
+  p.w.group = a.n_heads / a.n_kv_heads;
+  p.w.vec = 1;
+  p.vec_out = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.ld_out % 8 == 0 &&
+              (a.n_heads == 1 || a.ld_out_head % 8 == 0);
+  alignas(64) CUtensorMap mk, mv;
+  if (!encode_rows(&mk, a.k, a.k_rows, a.n_kv_heads, a.head_dim, a.ld_k, a.ld_k_head, a.dtype) ||
+      !encode_rows(&mv, a.v, a.k_rows, a.n_kv_heads, a.head_dim, a.ld_v, a.ld_v_head, a.dtype))
+    return cudaErrorInvalidValue;
+  const int64_t units = (a.q_rows * p.w.group / kUnit + a.batch) * a.n_kv_heads;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(units, device_sm_count()));
+  const bool bf16 = a.dtype == DLRM_DTYPE_BF16;
+  if (a.head_dim == 32)
+    return bf16 ? launch<32, DLRM_DTYPE_BF16>(mk, mv, p, grid, stream)
+                : launch<32, DLRM_DTYPE_FP16>(mk, mv, p, grid, stream);
+  if (a.head_dim == 64)
+    return bf16 ? launch<64, DLRM_DTYPE_BF16>(mk, mv, p, grid, stream)
+                : launch<64, DLRM_DTYPE_FP16>(mk, mv, p, grid, stream);
+  return bf16 ? launch<128, DLRM_DTYPE_BF16>(mk, mv, p, grid, stream)
+              : launch<128, DLRM_DTYPE_FP16>(mk, mv, p, grid, stream);
+}
+
+}  // namespace dlrm
