@@ -6,18 +6,21 @@
 // per SM, take units round-robin. Per unit the keys that any of its rows sees
 // flow by in key tiles of at most 128 events: the sinks that lie apart from the
 // window first (a narrow tile), then the window from its first event on.
+//   warp 11: finds the units and writes what the others need of them into a
+//     ring in shared memory;
+//   warp 10: the queries of both tiles, by TMA where the group divides 128;
 //   warp 9, one lane: TMA of key and value tiles (boxes of 32 events x 64
 //     elements, 128-byte swizzle) through rings of two stages each;
-//   warps 10, 11: the queries of tile 0 and 1, loaded a unit ahead;
-//   warp 8, one lane: S_t = Q_t K^T (operands from shared memory), then, when
-//     the weights are there, O_t += P_t V (P from tensor memory, V as stored:
-//     the MN-major operand form);
+//   warp 8: S_t = Q_t K^T (operands from shared memory), then, when the weights
+//     are there, O_t += P_t V (P from tensor memory, V as stored: the MN-major
+//     operand form);
 //   warps 0-3 and 4-7: softmax of tile 0 and 1. A thread owns a row: it reads
 //     its 128 scores from tensor memory, masks, takes the maximum, writes the
 //     weights in the input's type over the scores, and keeps its sum. The
 //     output is only corrected when a row's maximum has grown by more than 2^8
 //     over the reference in use (weights up to 2^8 are as exact, and the sum is
-//     fp32), which real scores do in the first tiles only.
+//     fp32), which real scores do in the first tiles only. 32 columns that none
+//     of a warp's rows sees are neither read nor exponentiated.
 // While one tile's softmax runs, the tensor core works on the other's products.
 // Tensor memory: S_t (128 columns, P_t over them) and O_t (up to 128 columns).
 //
@@ -56,20 +59,32 @@ struct Layout {
   static constexpr int kBars = kV + kStages * kTile;
   // more than half an SM's shared memory, so that one CTA is resident: it
   // takes all of the tensor memory
-  static constexpr int kSmem = kBars + 1024 + 256 > 120 * 1024 ? kBars + 1024 + 256 : 120 * 1024;
+  static constexpr int kSmem = kBars + 1024 + 1024 > 120 * 1024 ? kBars + 1024 + 1024 : 120 * 1024;
   static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
 
-struct Bars {
-  uint64_t q_full[2], q_empty[2], k_full[kStages], k_empty[kStages], v_full[kStages],
-      v_empty[kStages], s_full[2], p_full[2], o_full[2], o_empty[2], drain;
-  uint32_t tmem;
-  int abort;
+// n / d for 0 <= n < 2^31 by a multiplication: with s = ceil(log2 d) and
+// mul = floor(2^32 (2^s - d) / d) + 1, n / d = (hi32(n mul) + n) >> s (the
+// method of Granlund and Montgomery for invariant divisors).
+struct FastDiv {
+  uint32_t mul, shift, d;
+  __device__ __forceinline__ int operator()(int n) const {
+    return static_cast<int>((__umulhi(static_cast<uint32_t>(n), mul) + static_cast<uint32_t>(n)) >> shift);
+  }
 };
+FastDiv fast_div(int d) {
+  FastDiv f{};
+  f.d = static_cast<uint32_t>(d);
+  while ((uint64_t(1) << f.shift) < f.d) ++f.shift;
+  f.mul = static_cast<uint32_t>(((uint64_t(1) << 32) * ((uint64_t(1) << f.shift) - f.d)) / f.d + 1);
+  return f;
+}
 
 struct TcParams {
   WindowParams w;
+  FastDiv group, heads;
   int vec_out;
+  int q_tma;                                     // queries by TMA: boxes of group x 128 / group
   WaitCfg wait;
 };
 
@@ -133,13 +148,34 @@ struct Waiter {
   }
 };
 
-// D (+)= A B with A in tensor memory (the weights).
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+// Shared-memory descriptors: the low word holds the start address (and the
+// leading byte offset), the high word is the same for all operands here:
+// 8-row groups 1024 bytes apart, version 1, 128-byte swizzle.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+// rows of the inner dimension (queries, keys): K-major
+__device__ __forceinline__ uint32_t rows_desc(uint32_t addr) { return (addr >> 4) | (1u << 16); }
+// values, as the B operand of P V: MN-major, an event's 64 elements are a row
+// of 128 bytes, 64-element column blocks kBlockBytes apart
+__device__ __forceinline__ uint32_t values_desc(uint32_t addr) {
+  return (addr >> 4) | (static_cast<uint32_t>(kBlockBytes >> 4) << 16);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
                                        uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
+      : "memory");
+}
+// A in tensor memory: the weights.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
       : "memory");
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t at) {
@@ -154,17 +190,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t at) {
         "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(at));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t at) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, "
-      "%27, %28, %29, %30, %31, %32};" ::"r"(at),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-      "r"(r[30]), "r"(r[31])
-      : "memory");
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(at));
 }
 __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
   asm volatile(
@@ -187,25 +220,14 @@ __device__ __forceinline__ void fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
-// Shared-memory descriptor of a value tile as the B operand of P V: MN-major,
-// 128-byte swizzle (an event's 64 elements are a row of 128 bytes), 8-event
-// groups 1024 bytes apart, 64-element column blocks kBlockBytes apart.
-__device__ __forceinline__ uint64_t value_desc(uint32_t addr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((addr >> 4) & 0x3FFF);
-  d |= static_cast<uint64_t>(kBlockBytes >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
-}
-
-// One work unit: what every role derives for itself, by whole warps.
+// One work unit, in shared memory.
 struct Unit {
+  int valid, head, row0;                         // row0: first row of tile 0
   WindowSpan s;
-  int head, row0;                                // first row of tile 0
-  Visible first[2], last[2];                     // of each tile's first and last row
+  int pos0;                                      // position of the request's first query
   int rows[2];                                   // rows of each tile
+  int end1[2], gap0[2], gap1[2];                 // of a tile's last row: end, gap0; of its first: gap1
+  int last[2];                                   // last key tile that a tile needs, -1: none
   int sink, lo, end, sink_tiles, tiles;          // keys [0, sink) and [lo, end)
 
   // Key tile k: events [key0, key0 + n), computed `width` wide.
@@ -219,28 +241,43 @@ struct Unit {
     }
     width = (n + kBox - 1) / kBox * kBox;
   }
-  // (selects, not indexing, so that a unit stays in registers)
-  __device__ __forceinline__ int rows_of(int t) const { return t ? rows[1] : rows[0]; }
   __device__ __forceinline__ bool needs(int t, int key0, int n) const {
-    const int end1 = t ? last[1].end : last[0].end, gap0 = t ? last[1].gap0 : last[0].gap0;
-    const int gap1 = t ? first[1].gap1 : first[0].gap1;
-    return rows_of(t) > 0 && key0 < end1 && !(key0 >= gap0 && key0 + n <= gap1);
+    return rows[t] > 0 && key0 < end1[t] && !(key0 >= gap0[t] && key0 + n <= gap1[t]);
   }
 };
+constexpr int kUnits = 3;                        // units known ahead
+constexpr int kReaders = 11;                     // warps that read a unit
 
-// Walks the units of a CTA in order; every warp keeps one of its own.
+struct Bars {
+  uint64_t q_full[2], q_empty[2], k_full[kStages], k_empty[kStages], v_full[kStages],
+      v_empty[kStages], s_full[2], p_full[2], o_full[2], o_empty[2], u_full[kUnits],
+      u_empty[kUnits], drain;
+  uint32_t tmem;
+  int abort;
+  Unit units[kUnits];
+};
+static_assert(sizeof(Bars) <= 1024, "space behind the tiles");
+
+// Finds a CTA's units in order, by one warp.
 struct Walk {
   int b = 0;
   int before = 0;                                // units of the requests before b
 
-  // Warp-wide. False past the last unit.
-  __device__ __forceinline__ bool find(const WindowParams& p, int u, Unit& x) {
+  __device__ __forceinline__ void find(const TcParams& tp, int u, Unit& x) {
+    const WindowParams& p = tp.w;
     const int lane = threadIdx.x % kWarp;
     const int heads = p.a.n_kv_heads;
+    WindowSpan s{};
     for (;;) {
-      if (b >= p.a.batch) return false;
+      if (b >= p.a.batch) {
+        if (lane == 0) x.valid = 0;
+        return;
+      }
       int n = 0;
-      if (b + lane < p.a.batch) n = window_span(p, b + lane, kUnit, false).tiles * heads;
+      if (b + lane < p.a.batch) {
+        s = window_span(p, b + lane, kUnit, false);
+        n = s.tiles * heads;
+      }
       int inc = n;
 #pragma unroll
       for (int d = 1; d < kWarp; d *= 2) {
@@ -251,41 +288,108 @@ struct Walk {
       if (past) {
         const int at = __ffs(past) - 1;
         before += __shfl_sync(0xffffffffu, inc - n, at);
+        if (lane == at) {
+          fill(tp, u - before, s, x);
+        }
         b += at;
-        break;
+        return;
       }
       before += __shfl_sync(0xffffffffu, inc, kWarp - 1);
       b += kWarp;
     }
-    x.s = window_span(p, b, kUnit, false);
-    const int i = u - before;
+  }
+
+  // Unit i of the request with rows s, by one thread.
+  __device__ __forceinline__ void fill(const TcParams& tp, int i, const WindowSpan& s, Unit& out) {
+    const WindowParams& p = tp.w;
+    Unit x;
+    x.valid = 1;
+    x.s = s;
     // the last rows of a request first: without a window they see the most
-    x.head = i % heads;
-    const int tile = x.s.tiles - 1 - i / heads;
-    x.row0 = tile * kUnit;
-    const int pos0 = x.s.len - x.s.rows / p.group;
+    const int tile = tp.heads(i);
+    x.head = i - tile * p.a.n_kv_heads;
+    x.row0 = (s.tiles - 1 - tile) * kUnit;
+    x.pos0 = s.len - tp.group(s.rows);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      x.rows[t] = max(0, min(128, x.s.rows - x.row0 - 128 * t));
-      const int r0 = min(x.row0 + 128 * t, x.s.rows - 1), r1 = max(r0, r0 + x.rows[t] - 1);
-      x.first[t] = visible(pos0 + r0 / p.group, x.s.len, p.a.window, p.a.sinks);
-      x.last[t] = visible(pos0 + r1 / p.group, x.s.len, p.a.window, p.a.sinks);
+      x.rows[t] = max(0, min(128, s.rows - x.row0 - 128 * t));
+      const int r0 = min(x.row0 + 128 * t, s.rows - 1), r1 = max(r0, r0 + x.rows[t] - 1);
+      const Visible first = visible(x.pos0 + tp.group(r0), s.len, p.a.window, p.a.sinks);
+      const Visible last = visible(x.pos0 + tp.group(r1), s.len, p.a.window, p.a.sinks);
+      x.end1[t] = last.end;
+      x.gap0[t] = last.gap0;
+      x.gap1[t] = first.gap1;
     }
-    x.end = x.rows[1] > 0 ? x.last[1].end : x.last[0].end;
-    const int gap0 = x.rows[1] > 0 ? x.last[1].gap0 : x.last[0].gap0;
-    const bool apart = x.first[0].gap1 > gap0;
-    x.lo = apart ? min(x.first[0].gap1, x.end) : 0;
-    x.sink = apart ? min(gap0, x.end) : 0;
+    const int u = x.rows[1] > 0 ? 1 : 0;
+    x.end = x.end1[u];
+    const bool apart = x.gap1[0] > x.gap0[u];
+    x.lo = apart ? min(x.gap1[0], x.end) : 0;
+    x.sink = apart ? min(x.gap0[u], x.end) : 0;
     x.sink_tiles = (x.sink + kKeys - 1) / kKeys;
     x.tiles = x.sink_tiles + (x.end - x.lo + kKeys - 1) / kKeys;
-    return true;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      x.last[t] = -1;
+      for (int k = x.tiles - 1; k >= 0; --k) {
+        int key0, n, width;
+        x.tile(k, key0, n, width);
+        if (x.needs(t, key0, n)) {
+          x.last[t] = k;
+          break;
+        }
+      }
+    }
+    out = x;
   }
 };
 
+// A warp's place in the ring of units.
+struct Units {
+  Bars& bars;
+  const Waiter& wait;
+  int it = 0;
+  __device__ __forceinline__ const Unit* next() {
+    const int slot = it % kUnits;
+    if (!__all_sync(0xffffffffu, wait(&bars.u_full[slot], (it / kUnits) & 1))) return nullptr;
+    const Unit* x = &bars.units[slot];
+    return x->valid ? x : nullptr;
+  }
+  __device__ __forceinline__ void done() {
+    __syncwarp();
+    if (threadIdx.x % kWarp == 0) bar_arrive(&bars.u_empty[it % kUnits]);
+    ++it;
+  }
+};
+
+// 32 values as pairs, for the packed fp32 instructions.
+__device__ __forceinline__ void fma2(float& x, float& y, float f, float c) {
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\t"
+      "mov.b64 c, {%3, %3};\n\tfma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(f), "f"(c));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+// Bits [0, n) of a word, n any integer.
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1;
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+
 template <int D, int DT>
 __global__ void __launch_bounds__(kThreads, 1)
-window_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                 const TcParams p) {
+window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                 const __grid_constant__ CUtensorMap map_v, const __grid_constant__ TcParams p) {
   using L = Layout<D>;
   constexpr int kFormat = DT == DLRM_DTYPE_BF16 ? 1 : 0;
   // D fp32; A, B formats; M = 128; B of the second product is MN-major
@@ -321,6 +425,10 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
       bar_init(&bars.v_full[i], 1);
       bar_init(&bars.v_empty[i], 1);
     }
+    for (int i = 0; i < kUnits; ++i) {
+      bar_init(&bars.u_full[i], 1);
+      bar_init(&bars.u_empty[i], kReaders);
+    }
     bar_init(&bars.drain, 1);
     bars.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -332,8 +440,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
   pdl_wait();
   pdl_trigger();
 
-  Walk walk;
-  Unit x;
+  Units units{bars, wait};
   if (warp < 8) {
     // ------------------------------------------------------------ softmax
     const int t = warp / 4;
@@ -342,93 +449,128 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     const float f = w.a.scale * kLog2e;
     uint32_t s_phase = 0, o_phase = 0;
     bool ok = true;
-    for (int u = blockIdx.x; ok && walk.find(w, u, x); u += gridDim.x) {
-      if (x.rows_of(t) == 0) continue;
+    for (const Unit* x; ok && (x = units.next()); units.done()) {
+      const int rows = x->rows[t];
+      if (rows == 0) continue;
       const int r = (warp & 3) * 32 + lane;
-      const int row = min(x.row0 + 128 * t + r, x.s.rows - 1);
-      const bool in = r < x.rows_of(t);
-      const Visible v =
-          visible(x.s.len - x.s.rows / w.group + row / w.group, x.s.len, w.a.window, w.a.sinks);
+      const int row = min(x->row0 + 128 * t + r, x->s.rows - 1);
+      const bool in = r < rows;
+      const int i = p.group(row);
+      const Visible v = visible(x->pos0 + i, x->s.len, w.a.window, w.a.sinks);
       float top = -INFINITY, sum = 0.f;
       bool any = false;
-      for (int k = 0; k < x.tiles; ++k) {
+      const int tiles = x->last[t] + 1;
+      for (int k = 0; k < tiles; ++k) {
         int key0, n, width;
-        x.tile(k, key0, n, width);
-        if (!x.needs(t, key0, n)) continue;
+        x->tile(k, key0, n, width);
+        if (!x->needs(t, key0, n)) continue;
         ok = __all_sync(0xffffffffu, wait(&bars.s_full[t], s_phase));
         if (!ok) break;
         s_phase ^= 1;
         fence_after();
-        const int chunks = width / 32;
-        const bool whole = __all_sync(0xffffffffu, n == width && key0 + n <= v.end &&
-                                                       (key0 >= v.gap1 || key0 + n <= v.gap0));
-        // what the row sees of the tile: columns [0, a) and [b, e)
-        const int e = min(n, v.end - key0);
-        const int b = v.gap1 - key0, a = min(v.gap0 - key0, e);
-        // the scores are read twice, for the maximum and for the weights, 32 at
-        // a time with the next 32 under way: tensor memory is read much faster
-        // than the exponentials are made, and no thread needs 128 registers
-        uint32_t s[2][32];
-        auto next = [&](int c) {
-          tmem_wait_ld();
-          if (c + 1 < chunks) tmem_ld32(s[(c + 1) & 1], s_at + 32 * (c + 1));
-          if (!whole) {
+        // a running maximum m (times f) of scores not seen before: keeps the
+        // reference unless m passed it by more than the slack
+        auto raise = [&](float m) {
+          const bool grow = m > top + kSlack || (top == -INFINITY && m > -INFINITY);
+          if (__any_sync(0xffffffffu, grow)) {
+            const float alpha = grow ? exp2_approx(top - m) : 1.f;
+            if (grow) top = m;
+            sum *= alpha;
+            if (any) {                            // the products so far are complete (s_full)
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
+                uint32_t o[16];
+                tmem_ld16(o, o_at + c);
+                tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int col = 32 * c + i;
-              if (!(col < a || (col >= b && col < e))) s[c & 1][i] = 0xff800000u;
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                tmem_st16(o_at + c, o);
+              }
             }
           }
+          return top == -INFINITY ? 0.f : -top;
         };
-        float big[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        tmem_ld32(s[0], s_at);
+        // 32 scores to 16 words of weights
+        auto weigh = [&](uint32_t (&pw)[16], const uint32_t* s, float off) {
+          float add[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (c < chunks) {
-            next(c);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) big[i & 3] = fmaxf(big[i & 3], __uint_as_float(s[c & 1][i]));
+          for (int j = 0; j < 16; ++j) {
+            float a = __uint_as_float(s[2 * j]), b = __uint_as_float(s[2 * j + 1]);
+            fma2(a, b, f, off);
+            a = exp2_approx(a);
+            b = exp2_approx(b);
+            add2(add[2 * (j & 1)], add[2 * (j & 1) + 1], a, b);
+            pw[j] = DT == DLRM_DTYPE_BF16 ? pack_bf16(a, b) : pack_f16x2(a, b);
           }
-        const float m = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * f;
-        // keep the reference unless the maximum passed it by more than the slack
-        const bool grow = m > top + kSlack || (top == -INFINITY && m > -INFINITY);
-        if (__any_sync(0xffffffffu, grow)) {
-          const float alpha = grow ? exp2_approx(top - m) : 1.f;
-          if (grow) top = m;
-          sum *= alpha;
-          if (any) {                              // the products so far are complete (s_full)
+          sum += (add[0] + add[1]) + (add[2] + add[3]);
+        };
+        if (__all_sync(0xffffffffu, n == kKeys && key0 + n <= v.end &&
+                                        (key0 >= v.gap1 || key0 + n <= v.gap0))) {
+          // every row sees the whole tile: all scores in registers at once
+          uint32_t s[128];
 #pragma unroll
-            for (int c = 0; c < D; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(o, o_at + c);
-              tmem_wait_ld();
+          for (int c = 0; c < 4; ++c)
+            tmem_ld32(*reinterpret_cast<uint32_t(*)[32]>(&s[32 * c]), s_at + 32 * c);
+          tmem_wait_ld();
+          float big[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tmem_st32(o_at + c, o);
+          for (int j = 0; j < 128; ++j) big[j & 3] = fmaxf(big[j & 3], __uint_as_float(s[j]));
+          const float off = raise(fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * f);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pw[16];
+            weigh(pw, &s[32 * c], off);
+            tmem_st16(s_at + 16 * c, pw);
+          }
+        } else {
+          // 32 columns at a time, twice: what none of the warp's rows sees is
+          // skipped, what only some see is masked
+          const int chunks = width / 32;
+          uint32_t some = 0, part = 0;            // chunks that any row sees; that some row sees in part
+          for (int c = 0; c < chunks; ++c) {
+            const int c0 = key0 + 32 * c, c1 = c0 + 32;
+            const bool all = 32 * c + 32 <= n && c1 <= v.end && (c0 >= v.gap1 || c1 <= v.gap0);
+            const bool none = 32 * c >= n || c0 >= v.end || (c0 >= v.gap0 && c1 <= v.gap1);
+            some |= __any_sync(0xffffffffu, !none) ? 1u << c : 0u;
+            part |= __any_sync(0xffffffffu, !all) ? 1u << c : 0u;
+          }
+          auto load = [&](uint32_t (&s)[32], int c) {
+            tmem_ld32(s, s_at + 32 * c);
+            tmem_wait_ld();
+            if (part & (1u << c)) {
+              const int e = min(n, v.end - key0) - 32 * c;
+              const uint32_t bits = low_bits(min(v.gap0 - key0 - 32 * c, e)) |
+                                    (low_bits(e) & ~low_bits(v.gap1 - key0 - 32 * c));
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!(bits & (1u << j))) s[j] = 0xff800000u;
             }
+          };
+          float big[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int c = 0; c < chunks; ++c)
+            if (some & (1u << c)) {
+              uint32_t s[32];
+              load(s, c);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) big[j & 3] = fmaxf(big[j & 3], __uint_as_float(s[j]));
+            }
+          const float off = raise(fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * f);
+#pragma unroll 1
+          for (int c = 0; c < chunks; ++c) {
+            uint32_t pw[16];
+            if (some & (1u << c)) {
+              uint32_t s[32];
+              load(s, c);
+              weigh(pw, s, off);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) pw[j] = 0;
+            }
+            tmem_st16(s_at + 16 * c, pw);         // over scores that are read: 16 c + 15 < 32 (c + 1)
           }
         }
         any = true;
-        const float off = top == -INFINITY ? 0.f : top;
-        float add[4] = {0.f, 0.f, 0.f, 0.f};
-        tmem_ld32(s[0], s_at);
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (c < chunks) {
-            next(c);
-            uint32_t pw[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float p0 = exp2_approx(fmaf(__uint_as_float(s[c & 1][2 * i]), f, -off));
-              const float p1 = exp2_approx(fmaf(__uint_as_float(s[c & 1][2 * i + 1]), f, -off));
-              add[(2 * i) & 3] += p0;
-              add[(2 * i + 1) & 3] += p1;
-              pw[i] = DT == DLRM_DTYPE_BF16 ? pack_bf16(p0, p1) : pack_f16x2(p0, p1);
-            }
-            // over the scores of columns already read: 16 c + 15 < 32 (c + 1)
-            tmem_st16(s_at + 16 * c, pw);
-          }
-        sum += (add[0] + add[1]) + (add[2] + add[3]);
         tmem_wait_st();
         fence_before();
         __syncwarp();
@@ -438,13 +580,14 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
       // ---- output
       float inv = 0.f;
       if (any) {
-        if (!__all_sync(0xffffffffu, wait(&bars.o_full[t], o_phase))) break;
+        ok = __all_sync(0xffffffffu, wait(&bars.o_full[t], o_phase));
+        if (!ok) break;
         o_phase ^= 1;
         fence_after();
         inv = sum == 0.f ? 0.f : 1.f / sum;
       }
-      const int i = row / w.group, hq = x.head * w.group + row % w.group;
-      const int64_t q = x.s.q0 + static_cast<int64_t>(i);
+      const int hq = x->head * w.group + row - i * w.group;
+      const int64_t q = x->s.q0 + static_cast<int64_t>(i);
       const int64_t o_row = q * w.a.ld_out + hq * w.a.ld_out_head;
       bool odd = false;
 #pragma unroll
@@ -489,66 +632,88 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         w.a.lse[q * w.a.n_heads + hq] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
       for (unsigned who = __ballot_sync(0xffffffffu, odd && in); who; who &= who - 1) {
         __syncwarp();
-        window_careful_row<D, DT>(w, x.s, x.head, x.row0 + 128 * t + (warp & 3) * 32 + __ffs(who) - 1);
+        window_careful_row<D, DT>(w, x->s, x->head, x->row0 + 128 * t + (warp & 3) * 32 + __ffs(who) - 1);
       }
     }
   } else if (warp == 8) {
     // ------------------------------------------------------------ products
+    // the whole warp walks and waits, so that operands stay uniform; one lane issues
+    const bool leader = elect_one();
     uint32_t k_it = 0, v_it = 0, p_phase[2] = {0, 0}, q_phase[2] = {0, 0}, o_uses[2] = {0, 0};
     bool ok = true;
-    for (int u = blockIdx.x; ok && walk.find(w, u, x); u += gridDim.x) {
-      // tile t's product with the values of the key tile before is still due
-      bool due[2] = {false, false}, begun[2] = {false, false}, loaded[2] = {false, false};
+    const uint32_t q_desc = rows_desc(smem_addr(base + L::kQ));
+    const uint32_t k_desc = rows_desc(smem_addr(base + L::kK));
+    const uint32_t v_desc = values_desc(smem_addr(base + L::kV));
+    auto until = [&](uint64_t* bar, uint32_t parity) {
+      ok = ok && __all_sync(0xffffffffu, wait(bar, parity));
+    };
+    for (const Unit* x; ok && (x = units.next()); units.done()) {
+      // a tile's product with the values of the key tile before is still due
+      bool due[2] = {false, false}, begun[2] = {false, false};
       int due_width = 0;
       bool v_used = false;
-      for (int k = 0; k <= x.tiles && ok; ++k) {
+      const int tiles = x->tiles;
+      for (int k = 0; k <= tiles && ok; ++k) {
         int key0 = 0, n = 0, width = 0;
         bool need[2] = {false, false};
-        if (k < x.tiles) {
-          x.tile(k, key0, n, width);
-          need[0] = x.needs(0, key0, n);
-          need[1] = x.needs(1, key0, n);
+        if (k < tiles) {
+          x->tile(k, key0, n, width);
+          need[0] = x->needs(0, key0, n);
+          need[1] = x->needs(1, key0, n);
         }
         const bool k_used = need[0] || need[1];
-        if (lane == 0) {
-          const uint32_t ks = k_it % kStages, vs = v_it % kStages;
-          for (int t = 0; t < 2 && ok; ++t) {
-            if (due[t]) {
-              ok = wait(&bars.v_full[vs], (v_it / kStages) & 1) && wait(&bars.p_full[t], p_phase[t]);
-              if (ok && !begun[t] && o_uses[t] > 0) ok = wait(&bars.o_empty[t], (o_uses[t] - 1) & 1);
-              if (!ok) break;
-              p_phase[t] ^= 1;
-              fence_after();
-              const uint64_t dv = value_desc(smem_addr(base + L::kV + vs * L::kTile));
-              const uint32_t o = tmem + 256 + t * 128, pa = tmem + t * kKeys;
-              for (int j = 0; j < due_width / 16; ++j)
-                mma_ts(o, pa + 8 * j, dv + static_cast<uint64_t>(j * (2048 >> 4)), kIdescO,
-                       begun[t] || j > 0);
-              begun[t] = true;
+        const uint32_t ks = k_it % kStages, vs = v_it % kStages;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (due[t]) {
+            until(&bars.v_full[vs], (v_it / kStages) & 1);
+            if (!begun[t] && o_uses[t] > 0) until(&bars.o_empty[t], (o_uses[t] - 1) & 1);
+            until(&bars.p_full[t], p_phase[t]);
+            if (!ok) break;
+            p_phase[t] ^= 1;
+            fence_after();
+            const uint32_t vd = v_desc + vs * (L::kTile >> 4);
+            const uint32_t o = tmem + 256 + t * 128, pa = tmem + t * kKeys;
+            if (leader) {
+              mma_ts(o, pa, vd, kIdescO, begun[t] ? 1u : 0u);
+              mma_ts(o, pa + 8, vd + (2048 >> 4), kIdescO, 1u);
+#pragma unroll
+              for (int j = 2; j < 8; j += 2)
+                if (j * 16 < due_width) {
+                  mma_ts(o, pa + 8 * j, vd + j * (2048 >> 4), kIdescO, 1u);
+                  mma_ts(o, pa + 8 * j + 8, vd + (j + 1) * (2048 >> 4), kIdescO, 1u);
+                }
             }
-            if (need[t]) {
-              if (!loaded[t]) {
-                if (!(ok = wait(&bars.q_full[t], q_phase[t]))) break;
-                q_phase[t] ^= 1;
-                loaded[t] = true;
-              }
-              if (!(ok = wait(&bars.k_full[ks], (k_it / kStages) & 1))) break;
-              fence_after();
-              const uint32_t idesc = kIdescS | (static_cast<uint32_t>(width / 8) << 17);
-              const uint32_t sa = tmem + t * kKeys;
+            begun[t] = true;
+          }
+          if (need[t]) {
+            if (!begun[t] && !due[t]) {           // the tile's first scores of the unit
+              until(&bars.q_full[t], q_phase[t]);
+              q_phase[t] ^= 1;
+            }
+            until(&bars.k_full[ks], (k_it / kStages) & 1);
+            if (!ok) break;
+            fence_after();
+            const uint32_t idesc = kIdescS | (static_cast<uint32_t>(width / 8) << 17);
+            const uint32_t sa = tmem + t * kKeys;
+            const uint32_t qd = q_desc + t * (L::kTile >> 4), kd = k_desc + ks * (L::kTile >> 4);
+            if (leader) {
 #pragma unroll
               for (int j = 0; j < D / 16; ++j) {
-                const uint32_t off = (j / 4) * kBlockBytes + (j % 4) * 32;
-                mma<true>(sa, smem_desc(smem_addr(base + L::kQ + t * L::kTile) + off),
-                          smem_desc(smem_addr(base + L::kK + ks * L::kTile) + off), idesc, j > 0);
+                const uint32_t off = ((j / 4) * kBlockBytes + (j % 4) * 32) >> 4;
+                mma_ss(sa, qd + off, kd + off, idesc, j > 0 ? 1u : 0u);
               }
               mma_commit(smem_addr(&bars.s_full[t]));
+              // every score of the tile is made: its queries may be replaced
+              if (k == x->last[t]) mma_commit(smem_addr(&bars.q_empty[t]));
             }
           }
-          if (ok && v_used) mma_commit(smem_addr(&bars.v_empty[vs]));
-          if (ok && k_used) mma_commit(smem_addr(&bars.k_empty[ks]));
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        if (leader) {
+          if (v_used) mma_commit(smem_addr(&bars.v_empty[vs]));
+          if (k_used) mma_commit(smem_addr(&bars.k_empty[ks]));
+        }
         if (v_used) ++v_it;
         if (k_used) ++k_it;
         v_used = k_used;                          // the same events' values come next
@@ -556,30 +721,30 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         due[1] = need[1];
         due_width = width;
       }
-      if (lane == 0 && ok) {
-        for (int t = 0; t < 2; ++t)
-          if (begun[t]) {
-            // every score of the tile is made: its queries may be replaced
-            mma_commit(smem_addr(&bars.q_empty[t]));
-            mma_commit(smem_addr(&bars.o_full[t]));
-            ++o_uses[t];
-          }
-      }
+      if (!ok) break;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (begun[t]) {
+          if (leader) mma_commit(smem_addr(&bars.o_full[t]));
+          ++o_uses[t];
+        }
     }
-    if (lane == 0) {
+    if (leader) {
       // nothing of the tensor core's may be in flight when its memory is freed
       mma_commit(smem_addr(&bars.drain));
       wait.drain(&bars.drain, 0);
     }
+    __syncwarp();
   } else if (warp == 9) {
     // ------------------------------------------------------------ keys and values
     uint32_t it = 0;
     bool ok = true;
-    for (int u = blockIdx.x; ok && walk.find(w, u, x); u += gridDim.x) {
-      for (int k = 0; k < x.tiles && ok; ++k) {
+    for (const Unit* x; ok && (x = units.next()); units.done()) {
+      const int tiles = x->tiles, head = x->head, k0 = x->s.k0;
+      for (int k = 0; k < tiles && ok; ++k) {
         int key0, n, width;
-        x.tile(k, key0, n, width);
-        if (!x.needs(0, key0, n) && !x.needs(1, key0, n)) continue;
+        x->tile(k, key0, n, width);
+        if (!x->needs(0, key0, n) && !x->needs(1, key0, n)) continue;
         if (lane == 0) {
           const uint32_t st = it % kStages, ph = ((it / kStages) & 1) ^ 1;
           for (int side = 0; side < 2 && ok; ++side) {
@@ -590,8 +755,8 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             for (int r = 0; r < width; r += kBox)
 #pragma unroll
               for (int c = 0; c < L::kBlocks; ++c)
-                tma_load_3d(dst + c * kBlockBytes + r * 128, side ? &map_v : &map_k, c * 64, x.head,
-                            x.s.k0 + key0 + r, full);
+                tma_load_3d(dst + c * kBlockBytes + r * 128, side ? &map_v : &map_k, c * 64, head,
+                            k0 + key0 + r, full);
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -611,47 +776,78 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         while (now_ns() - t0 < 1000000) {}        // landed long before
       }
     }
-  } else {
+    __syncwarp();
+  } else if (warp == 10) {
     // ------------------------------------------------------------ queries
-    const int t = warp - 10;
-    uint32_t it = 0;
-    for (int u = blockIdx.x; walk.find(w, u, x); u += gridDim.x) {
-      bool used = false;
-      for (int k = 0; k < x.tiles && !used; ++k) {
-        int key0, n, width;
-        x.tile(k, key0, n, width);
-        used = x.needs(t, key0, n);
-      }
-      if (!used) continue;
-      if (it > 0 && !__all_sync(0xffffffffu, wait(&bars.q_empty[t], (it - 1) & 1))) break;
-      ++it;
-      constexpr int kChunks = D / 8;              // 16-byte chunks of a row
-      constexpr int kStep = kWarp / kChunks;      // rows of one warp-wide load
-      const int ch = lane % kChunks;
-      unsigned char* dst = base + L::kQ + t * L::kTile + (ch / 8) * kBlockBytes;
-      for (int r0 = 0; r0 < 128; r0 += 8 * kStep) {
-        uint4 q[8];
+    uint32_t uses[2] = {0, 0};
+    bool ok = true;
+    for (const Unit* x; ok && (x = units.next()); units.done()) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int r = r0 + j * kStep + lane / kChunks;
-          const int row = x.row0 + 128 * t + r;
-          q[j] = make_uint4(0, 0, 0, 0);
-          if (r < x.rows_of(t))
-            q[j] = __ldg(reinterpret_cast<const uint4*>(
-                             static_cast<const uint16_t*>(w.a.q) +
-                             (x.s.q0 + static_cast<int64_t>(row / w.group)) * w.a.ld_q +
-                             (x.head * w.group + row % w.group) * w.a.ld_q_head) +
-                         ch);
+      for (int t = 0; t < 2; ++t) {
+        if (x->last[t] < 0) continue;
+        if (uses[t] > 0) ok = ok && __all_sync(0xffffffffu, wait(&bars.q_empty[t], (uses[t] - 1) & 1));
+        if (!ok) break;
+        ++uses[t];
+        const int row0 = x->row0 + 128 * t;
+        if (p.q_tma) {
+          if (lane == 0) {
+            bar_expect(&bars.q_full[t], L::kTile);
+#pragma unroll
+            for (int c = 0; c < L::kBlocks; ++c)
+              tma_load_3d(smem_addr(base + L::kQ + t * L::kTile + c * kBlockBytes), &map_q, c * 64,
+                          x->head * w.group, x->s.q0 + p.group(row0), &bars.q_full[t]);
+          }
+          __syncwarp();
+          continue;
         }
+        constexpr int kChunks = D / 8;            // 16-byte chunks of a row
+        constexpr int kStep = kWarp / kChunks;    // rows of one warp-wide load
+        const int ch = lane % kChunks;
+        unsigned char* dst = base + L::kQ + t * L::kTile + (ch / 8) * kBlockBytes;
+        for (int r0 = 0; r0 < 128; r0 += 8 * kStep) {
+          uint4 q[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          *reinterpret_cast<uint4*>(dst + swz_offset(r0 + j * kStep + lane / kChunks, ch % 8)) = q[j];
+          for (int j = 0; j < 8; ++j) {
+            const int r = r0 + j * kStep + lane / kChunks;
+            const int i = p.group(row0 + r);
+            q[j] = make_uint4(0, 0, 0, 0);
+            if (r < x->rows[t])
+              q[j] = __ldg(reinterpret_cast<const uint4*>(
+                               static_cast<const uint16_t*>(w.a.q) +
+                               (x->s.q0 + static_cast<int64_t>(i)) * w.a.ld_q +
+                               (x->head * w.group + row0 + r - i * w.group) * w.a.ld_q_head) +
+                           ch);
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(dst + swz_offset(r0 + j * kStep + lane / kChunks, ch % 8)) = q[j];
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bars.q_full[t]);
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) bar_arrive(&bars.q_full[t]);
     }
-    if (blockIdx.x == 0 && t == 0)
+    // queries in flight must land before the shared memory is released
+    if (p.q_tma && lane == 0)
+      for (int t = 0; t < 2; ++t)
+        if (uses[t] > 0) wait.drain(&bars.q_full[t], (uses[t] - 1) & 1);
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ units
+    Walk walk;
+    for (int it = 0, u = blockIdx.x;; ++it, u += gridDim.x) {
+      const int slot = it % kUnits;
+      if (it >= kUnits &&
+          !__all_sync(0xffffffffu, wait(&bars.u_empty[slot], ((it / kUnits) & 1) ^ 1)))
+        break;
+      walk.find(p, u, bars.units[slot]);
+      __syncwarp();
+      const bool valid = bars.units[slot].valid != 0;
+      __syncwarp();
+      if (lane == 0) bar_arrive(&bars.u_full[slot]);
+      if (!valid) break;
+    }
+    if (blockIdx.x == 0)
       for (int i = lane; i < w.a.batch; i += kWarp) window_span(w, i, kUnit, true);
   }
   fence_before();
@@ -677,17 +873,17 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
 }
 
-// (rows, heads, D) with strides ld, ld_head: boxes of kBox rows x 64 elements
-// of one head; zeros past D and past the last row.
+// (rows, heads, D) with strides ld, ld_head: boxes of box_rows rows x box_heads
+// heads x 64 elements; zeros past D and past the last row.
 bool encode_rows(CUtensorMap* map, const void* x, int64_t rows, int heads, int dim, int64_t ld,
-                 int64_t ld_head, int dtype) {
+                 int64_t ld_head, int dtype, int box_rows, int box_heads) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
   if (!enc) return false;
   if (heads == 1) ld_head = dim;                  // not used
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads),
                               static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld_head) * 2, static_cast<cuuint64_t>(ld) * 2};
-  const cuuint32_t box[3] = {64, 1, kBox};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t steps[3] = {1, 1, 1};
   return enc(map,
              dtype == DLRM_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
@@ -698,7 +894,7 @@ bool encode_rows(CUtensorMap* map, const void* x, int64_t rows, int heads, int d
 }
 
 template <int D, int DT>
-cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const TcParams& p, unsigned grid,
+cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const TcParams& p, unsigned grid,
                    cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   int dev = 0;
@@ -712,25 +908,30 @@ cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const TcParams&
     done.fetch_or(bit, std::memory_order_acq_rel);
   }
   return launch_pdl(window_tc_kernel<D, DT>, dim3(grid), dim3(kThreads), Layout<D>::kSmem, stream,
-                    mk, mv, p);
+                    mq, mk, mv, p);
+}
+
+}  // namespace
+
+namespace {
+
+// What TMA asks of (rows, heads, dim) in 16 bits: a 16-byte aligned base,
+// strides that are multiples of 16 bytes, below 2^40, each a whole multiple of
+// the one before.
+bool tma_rows(const void* x, int64_t ld, int64_t ld_head, int heads, int dim) {
+  if (reinterpret_cast<uintptr_t>(x) % 16 != 0 || ld % 8 != 0 || ld >= (int64_t(1) << 38)) return false;
+  if (heads == 1) return ld >= dim && ld % dim == 0;
+  return ld_head % 8 == 0 && ld_head >= dim && ld > 0 && ld % ld_head == 0;
 }
 
 }  // namespace
 
 bool window_tc_takes(const dlrm_attention_t& a) {
   if (a.dtype == DLRM_DTYPE_FP32 || !(a.scale > 0.f) || a.k_rows < 1) return false;
-  auto rows_ok = [&](const void* x, int64_t ld, int64_t ld_head, int heads) {
-    return reinterpret_cast<uintptr_t>(x) % 16 == 0 && ld % 8 == 0 && (heads == 1 || ld_head % 8 == 0);
-  };
-  // TMA: strides of 16-byte multiples, below 2^40, that grow by whole multiples
-  auto tma_ok = [&](int64_t ld, int64_t ld_head) {
-    if (a.n_kv_heads == 1) return ld >= a.head_dim && ld % a.head_dim == 0 && ld < (int64_t(1) << 38);
-    return ld_head >= a.head_dim && ld > 0 && ld % ld_head == 0 && ld < (int64_t(1) << 38);
-  };
-  return rows_ok(a.q, a.ld_q, a.ld_q_head, a.n_heads) &&
-         rows_ok(a.k, a.ld_k, a.ld_k_head, a.n_kv_heads) &&
-         rows_ok(a.v, a.ld_v, a.ld_v_head, a.n_kv_heads) && tma_ok(a.ld_k, a.ld_k_head) &&
-         tma_ok(a.ld_v, a.ld_v_head);
+  return reinterpret_cast<uintptr_t>(a.q) % 16 == 0 && a.ld_q % 8 == 0 &&
+         (a.n_heads == 1 || a.ld_q_head % 8 == 0) &&
+         tma_rows(a.k, a.ld_k, a.ld_k_head, a.n_kv_heads, a.head_dim) &&
+         tma_rows(a.v, a.ld_v, a.ld_v_head, a.n_kv_heads, a.head_dim);
 }
 
 cudaError_t launch_window_attention_tc(const dlrm_attention_t& a, cudaStream_t stream) {
@@ -738,23 +939,32 @@ cudaError_t launch_window_attention_tc(const dlrm_attention_t& a, cudaStream_t s
   p.w.a = a;
   p.w.group = a.n_heads / a.n_kv_heads;
   p.w.vec = 1;
+  p.group = fast_div(p.w.group);
+  p.heads = fast_div(a.n_kv_heads);
   p.vec_out = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.ld_out % 8 == 0 &&
               (a.n_heads == 1 || a.ld_out_head % 8 == 0);
-  alignas(64) CUtensorMap mk, mv;
-  if (!encode_rows(&mk, a.k, a.k_rows, a.n_kv_heads, a.head_dim, a.ld_k, a.ld_k_head, a.dtype) ||
-      !encode_rows(&mv, a.v, a.k_rows, a.n_kv_heads, a.head_dim, a.ld_v, a.ld_v_head, a.dtype))
+  p.q_tma = 128 % p.w.group == 0 && tma_rows(a.q, a.ld_q, a.ld_q_head, a.n_heads, a.head_dim);
+  alignas(64) CUtensorMap mq, mk, mv;
+  const int box_q = p.q_tma ? 128 / p.w.group : 1;
+  if (!encode_rows(&mk, a.k, a.k_rows, a.n_kv_heads, a.head_dim, a.ld_k, a.ld_k_head, a.dtype, kBox, 1) ||
+      !encode_rows(&mv, a.v, a.k_rows, a.n_kv_heads, a.head_dim, a.ld_v, a.ld_v_head, a.dtype, kBox, 1))
+    return cudaErrorInvalidValue;
+  if (!p.q_tma)
+    mq = mk;                                      // not read
+  else if (!encode_rows(&mq, a.q, a.q_rows, a.n_heads, a.head_dim, a.ld_q, a.ld_q_head, a.dtype,
+                        box_q, p.w.group))
     return cudaErrorInvalidValue;
   const int64_t units = (a.q_rows * p.w.group / kUnit + a.batch) * a.n_kv_heads;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(units, device_sm_count()));
   const bool bf16 = a.dtype == DLRM_DTYPE_BF16;
   if (a.head_dim == 32)
-    return bf16 ? launch<32, DLRM_DTYPE_BF16>(mk, mv, p, grid, stream)
-                : launch<32, DLRM_DTYPE_FP16>(mk, mv, p, grid, stream);
+    return bf16 ? launch<32, DLRM_DTYPE_BF16>(mq, mk, mv, p, grid, stream)
+                : launch<32, DLRM_DTYPE_FP16>(mq, mk, mv, p, grid, stream);
   if (a.head_dim == 64)
-    return bf16 ? launch<64, DLRM_DTYPE_BF16>(mk, mv, p, grid, stream)
-                : launch<64, DLRM_DTYPE_FP16>(mk, mv, p, grid, stream);
-  return bf16 ? launch<128, DLRM_DTYPE_BF16>(mk, mv, p, grid, stream)
-              : launch<128, DLRM_DTYPE_FP16>(mk, mv, p, grid, stream);
+    return bf16 ? launch<64, DLRM_DTYPE_BF16>(mq, mk, mv, p, grid, stream)
+                : launch<64, DLRM_DTYPE_FP16>(mq, mk, mv, p, grid, stream);
+  return bf16 ? launch<128, DLRM_DTYPE_BF16>(mq, mk, mv, p, grid, stream)
+              : launch<128, DLRM_DTYPE_FP16>(mq, mk, mv, p, grid, stream);
 }
 
 }  // namespace dlrm
