@@ -4,28 +4,31 @@
 // A work unit is 256 rows, as two tiles of 128 (the MMA's M), of one kv head of
 // a request; rows are (query, head of the group) pairs. Persistent CTAs, one
 // per SM, take units round-robin. Per unit the keys that any of its rows sees
-// flow by in key tiles of at most 128 events: the sinks that lie apart from the
+// flow by in key tiles of at most 64 events: the sinks that lie apart from the
 // window first (a narrow tile), then the window from its first event on.
 //   warp 11: finds the units and writes what the others need of them into a
 //     ring in shared memory;
-//   warp 10: the queries of both tiles, by TMA where the group divides 128;
-//   warp 9, one lane: TMA of key and value tiles (boxes of 32 events x 64
-//     elements, 128-byte swizzle) through rings of two stages each;
-//   warp 8: S_t = Q_t K^T (operands from shared memory), then, when the weights
-//     are there, O_t += P_t V (P from tensor memory, V as stored: the MN-major
-//     operand form);
+//   warp 10, one lane: TMA of key and value tiles (boxes of 32 events x 64
+//     elements, 128-byte swizzle) through rings of four stages each;
+//   warps 8 and 9, one lane each: the products of tile 0 and 1: S_t = Q_t K^T
+//     (operands from shared memory), then, when the weights are there, O_t += P_t V
+//     (P from tensor memory, V as stored: the MN-major operand form). One lane's
+//     waits and issues take about as long as a tile's softmax, hence two warps.
+//     They also load their tile's queries, by TMA where the group divides 128
+//     (else the softmax warps do);
 //   warps 0-3 and 4-7: softmax of tile 0 and 1. A thread owns a row: it reads
-//     its 128 scores from tensor memory, masks, takes the maximum, writes the
+//     its 64 scores from tensor memory, masks, takes the maximum, writes the
 //     weights in the input's type over the scores, and keeps its sum. The
 //     output is only corrected when a row's maximum has grown by more than 2^8
 //     over the reference in use (weights up to 2^8 are as exact, and the sum is
 //     fp32), which real scores do in the first tiles only. 32 columns that none
 //     of a warp's rows sees are neither read nor exponentiated.
-// While one tile's softmax runs, the tensor core works on the other's products.
-// Tensor memory: S_t (128 columns, P_t over them) and O_t (up to 128 columns).
+// Tensor memory: two score buffers of 64 columns a tile (weights over the
+// scores) and the output, up to 128 columns a tile. With two buffers the scores
+// of the next key tile are made while the softmax works on this one's.
 //
-// What bounds it: the exponentials (16 a cycle and SM: 1024 cycles a tile of
-// 128 x 128) for head_dim 32 and 64, and as much the tensor core (1024 cycles)
+// What bounds it: the exponentials (16 a cycle and SM: 512 cycles a tile of
+// 128 x 64) for head_dim 32 and 64, and as much the tensor core (320 + 256 cycles)
 // for 128.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -43,18 +46,20 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kUnit = 256;                       // rows of a work unit
-constexpr int kKeys = 128;                       // events of a key tile
+constexpr int kKeys = 64;                        // events of a key tile
 constexpr int kBox = 32;                         // events of one TMA box
-constexpr int kBlockBytes = 128 * 128;           // 128 rows of 128 bytes (64 elements)
-constexpr int kStages = 2;                       // of keys, and of values
+constexpr int kQBlock = 128 * 128;               // 128 rows of 128 bytes (64 elements)
+constexpr int kBlockBytes = kKeys * 128;         // the same of a key tile
+constexpr int kStages = 4;                       // of keys, and of values
 constexpr float kSlack = 8.f;                    // log2 of the largest weight
 
 template <int D>
 struct Layout {
   static constexpr int kBlocks = (D + 63) / 64;  // 64-element column blocks
   static constexpr int kTile = kBlocks * kBlockBytes;
+  static constexpr int kQTile = kBlocks * kQBlock;
   static constexpr int kQ = 0;                   // two query tiles
-  static constexpr int kK = 2 * kTile;
+  static constexpr int kK = 2 * kQTile;
   static constexpr int kV = kK + kStages * kTile;
   static constexpr int kBars = kV + kStages * kTile;
   // more than half an SM's shared memory, so that one CTA is resident: it
@@ -248,10 +253,36 @@ struct Unit {
 constexpr int kUnits = 3;                        // units known ahead
 constexpr int kReaders = 11;                     // warps that read a unit
 
+// What a loop over key tiles needs of a unit, in registers.
+struct Keys {
+  int lo, end, sink, sink_tiles, tiles;
+  bool have[2];
+  int end1[2], gap0[2], gap1[2];
+  __device__ __forceinline__ explicit Keys(const Unit& x)
+      : lo(x.lo), end(x.end), sink(x.sink), sink_tiles(x.sink_tiles), tiles(x.tiles) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      have[t] = x.rows[t] > 0;
+      end1[t] = x.end1[t];
+      gap0[t] = x.gap0[t];
+      gap1[t] = x.gap1[t];
+    }
+  }
+  __device__ __forceinline__ void tile(int k, int& key0, int& n) const {
+    const bool s = k < sink_tiles;
+    key0 = s ? k * kKeys : lo + (k - sink_tiles) * kKeys;
+    n = min(kKeys, (s ? sink : end) - key0);
+  }
+  template <int T>
+  __device__ __forceinline__ bool needs(int key0, int n) const {
+    return have[T] && key0 < end1[T] && !(key0 >= gap0[T] && key0 + n <= gap1[T]);
+  }
+};
+
 struct Bars {
-  uint64_t q_full[2], q_empty[2], k_full[kStages], k_empty[kStages], v_full[kStages],
-      v_empty[kStages], s_full[2], p_full[2], o_full[2], o_empty[2], u_full[kUnits],
-      u_empty[kUnits], drain;
+  uint64_t q_full[2], k_full[kStages], k_empty[kStages], v_full[kStages],
+      v_empty[kStages], s_full[2][2], p_full[2][2], pv_done[2][2], o_empty[2], u_full[kUnits],
+      u_empty[kUnits], drain[2];
   uint32_t tmem;
   int abort;
   Unit units[kUnits];
@@ -343,18 +374,24 @@ struct Walk {
   }
 };
 
-// A warp's place in the ring of units.
+// A warp's place in the ring of units; one lane of it may walk alone.
 struct Units {
   Bars& bars;
   const Waiter& wait;
   int it = 0;
   __device__ __forceinline__ const Unit* next() {
     const int slot = it % kUnits;
-    if (!__all_sync(0xffffffffu, wait(&bars.u_full[slot], (it / kUnits) & 1))) return nullptr;
+    const bool ok = wait(&bars.u_full[slot], (it / kUnits) & 1);
     const Unit* x = &bars.units[slot];
-    return x->valid ? x : nullptr;
+    return ok && x->valid ? x : nullptr;
   }
-  __device__ __forceinline__ void done() {
+  __device__ __forceinline__ void done() { bar_arrive(&bars.u_empty[it++ % kUnits]); }
+  // by all lanes
+  __device__ __forceinline__ const Unit* next_warp() {
+    const Unit* x = next();
+    return __all_sync(0xffffffffu, x != nullptr) ? x : nullptr;
+  }
+  __device__ __forceinline__ void done_warp() {
     __syncwarp();
     if (threadIdx.x % kWarp == 0) bar_arrive(&bars.u_empty[it % kUnits]);
     ++it;
@@ -386,15 +423,109 @@ __device__ __forceinline__ bool elect_one() {
   return ok != 0;
 }
 
-template <int D, int DT>
-__global__ void __launch_bounds__(kThreads, 1)
-window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                 const __grid_constant__ CUtensorMap map_v, const __grid_constant__ TcParams p) {
+// The products of tile T of every unit, by one lane.
+template <int D, int DT, int T>
+__device__ __forceinline__ void products(const TcParams& p, const CUtensorMap* map_q, Bars& bars,
+                                         const Waiter& wait, unsigned char* base, uint32_t tmem) {
   using L = Layout<D>;
   constexpr int kFormat = DT == DLRM_DTYPE_BF16 ? 1 : 0;
   // D fp32; A, B formats; M = 128; B of the second product is MN-major
   constexpr uint32_t kIdescS = (1u << 4) | (kFormat << 7) | (kFormat << 10) | (8u << 24);
   constexpr uint32_t kIdescO = kIdescS | (1u << 16) | (static_cast<uint32_t>(D / 8) << 17);
+  const uint32_t q_desc = rows_desc(smem_addr(base + L::kQ + T * L::kQTile));
+  const uint32_t k_desc = rows_desc(smem_addr(base + L::kK));
+  const uint32_t v_desc = values_desc(smem_addr(base + L::kV));
+  const uint32_t s_base = tmem + T * 128, o = tmem + 256 + T * 128;
+  uint32_t kv = 0, it = 0, units_done = 0;       // key tiles of the CTA, of this tile; its units
+  Units units{bars, wait};
+  for (const Unit* x; (x = units.next()); units.done()) {
+    const Keys keys(*x);
+    // the queries: every score of the unit before has been read, so the tile
+    // may be replaced
+    if (p.q_tma && x->last[T] >= 0) {
+      bar_expect(&bars.q_full[T], L::kQTile);
+#pragma unroll
+      for (int c = 0; c < L::kBlocks; ++c)
+        tma_load_3d(smem_addr(base + L::kQ + T * L::kQTile + c * kQBlock), map_q, c * 64,
+                    x->head * p.w.group, x->s.q0 + p.group(x->row0 + 128 * T), &bars.q_full[T]);
+    }
+    bool due = false, begun = false, used_before = false;
+    int due_width = 0;
+    for (int k = 0; k <= keys.tiles; ++k) {
+      int key0 = 0, n = 0;
+      bool need = false, used = false;
+      if (k < keys.tiles) {
+        keys.tile(k, key0, n);
+        need = keys.needs<T>(key0, n);
+        used = need || keys.needs<1 - T>(key0, n);
+      }
+      if (used) {
+        // scores of this tile, into the buffer that the weights before last lay in
+        const uint32_t st = kv % kStages;
+        bool ok = wait(&bars.k_full[st], (kv / kStages) & 1);
+        // (queries in flight land before anything gives up)
+        if (need && !begun && !due) {
+          if (ok) ok = wait(&bars.q_full[T], units_done & 1);
+          if (!ok && p.q_tma) wait.drain(&bars.q_full[T], units_done & 1);
+        }
+        if (!ok) return;
+        if (need) {
+          // products of different shapes are not ordered among themselves: those
+          // weights must have been used. (Product i completes phase i / 2 of
+          // barrier i % 2. Whoever waits for it knows that i - 2 is complete and
+          // that i + 2 is not issued, so the phase's parity says enough.)
+          if (it >= 2 && !wait(&bars.pv_done[T][it & 1], ((it - 2) >> 1) & 1)) return;
+          fence_after();
+          const uint32_t idesc = kIdescS | (n > 32 ? 8u << 17 : 4u << 17);
+          const uint32_t sa = s_base + (it & 1) * kKeys, kd = k_desc + st * (L::kTile >> 4);
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j)
+            mma_ss(sa, q_desc + (((j / 4) * kQBlock + (j % 4) * 32) >> 4),
+                   kd + (((j / 4) * kBlockBytes + (j % 4) * 32) >> 4), idesc, j > 0 ? 1u : 0u);
+          mma_commit(smem_addr(&bars.s_full[T][it & 1]));
+          mma_commit(smem_addr(&bars.k_empty[st]));
+          ++it;
+        } else {
+          bar_arrive(&bars.k_empty[st]);
+        }
+        ++kv;
+      }
+      if (used_before) {
+        // products with the values of the tile before
+        const uint32_t vi = kv - 1 - (used ? 1 : 0), st = vi % kStages;
+        if (!wait(&bars.v_full[st], (vi / kStages) & 1)) return;
+        if (due) {
+          const uint32_t of = it - 1 - (need ? 1 : 0);
+          if (!begun && units_done > 0 && !wait(&bars.o_empty[T], (units_done - 1) & 1)) return;
+          if (!wait(&bars.p_full[T][of & 1], (of >> 1) & 1)) return;
+          fence_after();
+          const uint32_t vd = v_desc + st * (L::kTile >> 4), pa = s_base + (of & 1) * kKeys;
+          mma_ts(o, pa, vd, kIdescO, begun ? 1u : 0u);
+          mma_ts(o, pa + 8, vd + (2048 >> 4), kIdescO, 1u);
+          if (due_width > 32) {
+            mma_ts(o, pa + 16, vd + 2 * (2048 >> 4), kIdescO, 1u);
+            mma_ts(o, pa + 24, vd + 3 * (2048 >> 4), kIdescO, 1u);
+          }
+          mma_commit(smem_addr(&bars.pv_done[T][of & 1]));
+          mma_commit(smem_addr(&bars.v_empty[st]));
+          begun = true;
+        } else {
+          bar_arrive(&bars.v_empty[st]);
+        }
+      }
+      used_before = used;
+      due = need;
+      due_width = n;
+    }
+    units_done += begun ? 1 : 0;
+  }
+}
+
+template <int D, int DT>
+__global__ void __launch_bounds__(kThreads, 1)
+window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                 const __grid_constant__ CUtensorMap map_v, const __grid_constant__ TcParams p) {
+  using L = Layout<D>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -412,24 +543,25 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
   }
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
-      bar_init(&bars.q_full[t], 1);
-      bar_init(&bars.q_empty[t], 1);
-      bar_init(&bars.s_full[t], 1);
-      bar_init(&bars.p_full[t], 4);
-      bar_init(&bars.o_full[t], 1);
+      bar_init(&bars.q_full[t], p.q_tma ? 1 : 4);
+      for (int i = 0; i < 2; ++i) {
+        bar_init(&bars.s_full[t][i], 1);
+        bar_init(&bars.p_full[t][i], 4);
+        bar_init(&bars.pv_done[t][i], 1);
+      }
       bar_init(&bars.o_empty[t], 4);
     }
     for (int i = 0; i < kStages; ++i) {
       bar_init(&bars.k_full[i], 1);
-      bar_init(&bars.k_empty[i], 1);
+      bar_init(&bars.k_empty[i], 2);
       bar_init(&bars.v_full[i], 1);
-      bar_init(&bars.v_empty[i], 1);
+      bar_init(&bars.v_empty[i], 2);
     }
     for (int i = 0; i < kUnits; ++i) {
       bar_init(&bars.u_full[i], 1);
       bar_init(&bars.u_empty[i], kReaders);
     }
-    bar_init(&bars.drain, 1);
+    for (int t = 0; t < 2; ++t) bar_init(&bars.drain[t], 1);
     bars.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -445,28 +577,43 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     // ------------------------------------------------------------ softmax
     const int t = warp / 4;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t s_at = tmem + lanes + t * kKeys, o_at = tmem + lanes + 256 + t * 128;
+    const uint32_t o_at = tmem + lanes + 256 + t * 128;
     const float f = w.a.scale * kLog2e;
-    uint32_t s_phase = 0, o_phase = 0;
+    uint32_t it = 0;                              // key tiles so far
     bool ok = true;
-    for (const Unit* x; ok && (x = units.next()); units.done()) {
+    for (const Unit* x; ok && (x = units.next_warp()); units.done_warp()) {
       const int rows = x->rows[t];
       if (rows == 0) continue;
+      const Keys keys(*x);
       const int r = (warp & 3) * 32 + lane;
       const int row = min(x->row0 + 128 * t + r, x->s.rows - 1);
       const bool in = r < rows;
       const int i = p.group(row);
       const Visible v = visible(x->pos0 + i, x->s.len, w.a.window, w.a.sinks);
+      if (!p.q_tma && x->last[t] >= 0) {
+        // this row's queries; zeros past the last row
+        unsigned char* dst = base + L::kQ + t * L::kQTile;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const uint16_t*>(w.a.q) + (x->s.q0 + static_cast<int64_t>(i)) * w.a.ld_q +
+            (x->head * w.group + row - i * w.group) * w.a.ld_q_head);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+          *reinterpret_cast<uint4*>(dst + (c / 8) * kQBlock + swz_offset(r, c % 8)) =
+              in ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bars.q_full[t]);
+      }
       float top = -INFINITY, sum = 0.f;
       bool any = false;
       const int tiles = x->last[t] + 1;
       for (int k = 0; k < tiles; ++k) {
-        int key0, n, width;
-        x->tile(k, key0, n, width);
-        if (!x->needs(t, key0, n)) continue;
-        ok = __all_sync(0xffffffffu, wait(&bars.s_full[t], s_phase));
+        int key0, n;
+        keys.tile(k, key0, n);
+        if (!(t ? keys.needs<1>(key0, n) : keys.needs<0>(key0, n))) continue;
+        const uint32_t s_at = tmem + lanes + t * 128 + (it & 1) * kKeys;
+        ok = __all_sync(0xffffffffu, wait(&bars.s_full[t][it & 1], (it >> 1) & 1));
         if (!ok) break;
-        s_phase ^= 1;
         fence_after();
         // a running maximum m (times f) of scores not seen before: keeps the
         // reference unless m passed it by more than the slack
@@ -476,7 +623,12 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             const float alpha = grow ? exp2_approx(top - m) : 1.f;
             if (grow) top = m;
             sum *= alpha;
-            if (any) {                            // the products so far are complete (s_full)
+            if (any) {
+              // the product before this tile's must be complete; the one before
+              // that is (its weights lay where these scores are)
+              ok = __all_sync(0xffffffffu,
+                              wait(&bars.pv_done[t][(it - 1) & 1], ((it - 1) >> 1) & 1));
+              fence_after();
 #pragma unroll 1
               for (int c = 0; c < D; c += 16) {
                 uint32_t o[16];
@@ -504,85 +656,68 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
           }
           sum += (add[0] + add[1]) + (add[2] + add[3]);
         };
-        if (__all_sync(0xffffffffu, n == kKeys && key0 + n <= v.end &&
-                                        (key0 >= v.gap1 || key0 + n <= v.gap0))) {
-          // every row sees the whole tile: all scores in registers at once
-          uint32_t s[128];
+        // columns [0, 32) and [32, 64): skipped where none of the warp's rows
+        // sees any, masked where some do not see all
+        uint32_t s[2][32];
+        bool some[2] = {true, true}, part[2] = {false, false};
+        if (!__all_sync(0xffffffffu, n == kKeys && key0 + kKeys <= v.end &&
+                                         (key0 >= v.gap1 || key0 + kKeys <= v.gap0))) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            tmem_ld32(*reinterpret_cast<uint32_t(*)[32]>(&s[32 * c]), s_at + 32 * c);
-          tmem_wait_ld();
-          float big[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int j = 0; j < 128; ++j) big[j & 3] = fmaxf(big[j & 3], __uint_as_float(s[j]));
-          const float off = raise(fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * f);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t pw[16];
-            weigh(pw, &s[32 * c], off);
-            tmem_st16(s_at + 16 * c, pw);
-          }
-        } else {
-          // 32 columns at a time, twice: what none of the warp's rows sees is
-          // skipped, what only some see is masked
-          const int chunks = width / 32;
-          uint32_t some = 0, part = 0;            // chunks that any row sees; that some row sees in part
-          for (int c = 0; c < chunks; ++c) {
+          for (int c = 0; c < 2; ++c) {
             const int c0 = key0 + 32 * c, c1 = c0 + 32;
             const bool all = 32 * c + 32 <= n && c1 <= v.end && (c0 >= v.gap1 || c1 <= v.gap0);
             const bool none = 32 * c >= n || c0 >= v.end || (c0 >= v.gap0 && c1 <= v.gap1);
-            some |= __any_sync(0xffffffffu, !none) ? 1u << c : 0u;
-            part |= __any_sync(0xffffffffu, !all) ? 1u << c : 0u;
+            some[c] = __any_sync(0xffffffffu, !none);
+            part[c] = __any_sync(0xffffffffu, !all);
           }
-          auto load = [&](uint32_t (&s)[32], int c) {
-            tmem_ld32(s, s_at + 32 * c);
-            tmem_wait_ld();
-            if (part & (1u << c)) {
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          if (some[c]) tmem_ld32(s[c], s_at + 32 * c);
+        tmem_wait_ld();
+        float big[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          if (some[c]) {
+            if (part[c]) {
               const int e = min(n, v.end - key0) - 32 * c;
               const uint32_t bits = low_bits(min(v.gap0 - key0 - 32 * c, e)) |
                                     (low_bits(e) & ~low_bits(v.gap1 - key0 - 32 * c));
 #pragma unroll
               for (int j = 0; j < 32; ++j)
-                if (!(bits & (1u << j))) s[j] = 0xff800000u;
+                if (!(bits & (1u << j))) s[c][j] = 0xff800000u;
             }
-          };
-          float big[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-          for (int c = 0; c < chunks; ++c)
-            if (some & (1u << c)) {
-              uint32_t s[32];
-              load(s, c);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) big[j & 3] = fmaxf(big[j & 3], __uint_as_float(s[j]));
-            }
-          const float off = raise(fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * f);
-#pragma unroll 1
-          for (int c = 0; c < chunks; ++c) {
+            for (int j = 0; j < 32; ++j) big[j & 3] = fmaxf(big[j & 3], __uint_as_float(s[c][j]));
+          }
+        const float off = raise(fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * f);
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          if (c == 0 || n > 32) {
             uint32_t pw[16];
-            if (some & (1u << c)) {
-              uint32_t s[32];
-              load(s, c);
-              weigh(pw, s, off);
+            if (some[c]) {
+              weigh(pw, s[c], off);
             } else {
 #pragma unroll
               for (int j = 0; j < 16; ++j) pw[j] = 0;
             }
-            tmem_st16(s_at + 16 * c, pw);         // over scores that are read: 16 c + 15 < 32 (c + 1)
+            tmem_st16(s_at + 16 * c, pw);         // over the scores, which are in registers
           }
-        }
         any = true;
         tmem_wait_st();
         fence_before();
         __syncwarp();
-        if (lane == 0) bar_arrive(&bars.p_full[t]);
+        if (lane == 0) bar_arrive(&bars.p_full[t][it & 1]);
+        ++it;
       }
       if (!ok) break;
       // ---- output
       float inv = 0.f;
       if (any) {
-        ok = __all_sync(0xffffffffu, wait(&bars.o_full[t], o_phase));
+        // the last product, and with it all before it
+        ok = __all_sync(0xffffffffu, wait(&bars.pv_done[t][(it - 1) & 1], ((it - 1) >> 1) & 1));
         if (!ok) break;
-        o_phase ^= 1;
         fence_after();
         inv = sum == 0.f ? 0.f : 1.f / sum;
       }
@@ -635,135 +770,49 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         window_careful_row<D, DT>(w, x->s, x->head, x->row0 + 128 * t + (warp & 3) * 32 + __ffs(who) - 1);
       }
     }
-  } else if (warp == 8) {
+  } else if (warp < 10) {
     // ------------------------------------------------------------ products
-    // the whole warp walks and waits, so that operands stay uniform; one lane issues
-    const bool leader = elect_one();
-    uint32_t k_it = 0, v_it = 0, p_phase[2] = {0, 0}, q_phase[2] = {0, 0}, o_uses[2] = {0, 0};
-    bool ok = true;
-    const uint32_t q_desc = rows_desc(smem_addr(base + L::kQ));
-    const uint32_t k_desc = rows_desc(smem_addr(base + L::kK));
-    const uint32_t v_desc = values_desc(smem_addr(base + L::kV));
-    auto until = [&](uint64_t* bar, uint32_t parity) {
-      ok = ok && __all_sync(0xffffffffu, wait(bar, parity));
-    };
-    for (const Unit* x; ok && (x = units.next()); units.done()) {
-      // a tile's product with the values of the key tile before is still due
-      bool due[2] = {false, false}, begun[2] = {false, false};
-      int due_width = 0;
-      bool v_used = false;
-      const int tiles = x->tiles;
-      for (int k = 0; k <= tiles && ok; ++k) {
-        int key0 = 0, n = 0, width = 0;
-        bool need[2] = {false, false};
-        if (k < tiles) {
-          x->tile(k, key0, n, width);
-          need[0] = x->needs(0, key0, n);
-          need[1] = x->needs(1, key0, n);
-        }
-        const bool k_used = need[0] || need[1];
-        const uint32_t ks = k_it % kStages, vs = v_it % kStages;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (due[t]) {
-            until(&bars.v_full[vs], (v_it / kStages) & 1);
-            if (!begun[t] && o_uses[t] > 0) until(&bars.o_empty[t], (o_uses[t] - 1) & 1);
-            until(&bars.p_full[t], p_phase[t]);
-            if (!ok) break;
-            p_phase[t] ^= 1;
-            fence_after();
-            const uint32_t vd = v_desc + vs * (L::kTile >> 4);
-            const uint32_t o = tmem + 256 + t * 128, pa = tmem + t * kKeys;
-            if (leader) {
-              mma_ts(o, pa, vd, kIdescO, begun[t] ? 1u : 0u);
-              mma_ts(o, pa + 8, vd + (2048 >> 4), kIdescO, 1u);
-#pragma unroll
-              for (int j = 2; j < 8; j += 2)
-                if (j * 16 < due_width) {
-                  mma_ts(o, pa + 8 * j, vd + j * (2048 >> 4), kIdescO, 1u);
-                  mma_ts(o, pa + 8 * j + 8, vd + (j + 1) * (2048 >> 4), kIdescO, 1u);
-                }
-            }
-            begun[t] = true;
-          }
-          if (need[t]) {
-            if (!begun[t] && !due[t]) {           // the tile's first scores of the unit
-              until(&bars.q_full[t], q_phase[t]);
-              q_phase[t] ^= 1;
-            }
-            until(&bars.k_full[ks], (k_it / kStages) & 1);
-            if (!ok) break;
-            fence_after();
-            const uint32_t idesc = kIdescS | (static_cast<uint32_t>(width / 8) << 17);
-            const uint32_t sa = tmem + t * kKeys;
-            const uint32_t qd = q_desc + t * (L::kTile >> 4), kd = k_desc + ks * (L::kTile >> 4);
-            if (leader) {
-#pragma unroll
-              for (int j = 0; j < D / 16; ++j) {
-                const uint32_t off = ((j / 4) * kBlockBytes + (j % 4) * 32) >> 4;
-                mma_ss(sa, qd + off, kd + off, idesc, j > 0 ? 1u : 0u);
-              }
-              mma_commit(smem_addr(&bars.s_full[t]));
-              // every score of the tile is made: its queries may be replaced
-              if (k == x->last[t]) mma_commit(smem_addr(&bars.q_empty[t]));
-            }
-          }
-        }
-        if (!ok) break;
-        if (leader) {
-          if (v_used) mma_commit(smem_addr(&bars.v_empty[vs]));
-          if (k_used) mma_commit(smem_addr(&bars.k_empty[ks]));
-        }
-        if (v_used) ++v_it;
-        if (k_used) ++k_it;
-        v_used = k_used;                          // the same events' values come next
-        due[0] = need[0];
-        due[1] = need[1];
-        due_width = width;
-      }
-      if (!ok) break;
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-        if (begun[t]) {
-          if (leader) mma_commit(smem_addr(&bars.o_full[t]));
-          ++o_uses[t];
-        }
-    }
-    if (leader) {
+    const int t = warp - 8;
+    if (elect_one()) {
+      if (t == 0)
+        products<D, DT, 0>(p, &map_q, bars, wait, base, tmem);
+      else
+        products<D, DT, 1>(p, &map_q, bars, wait, base, tmem);
       // nothing of the tensor core's may be in flight when its memory is freed
-      mma_commit(smem_addr(&bars.drain));
-      wait.drain(&bars.drain, 0);
+      mma_commit(smem_addr(&bars.drain[t]));
+      wait.drain(&bars.drain[t], 0);
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == 10) {
     // ------------------------------------------------------------ keys and values
-    uint32_t it = 0;
-    bool ok = true;
-    for (const Unit* x; ok && (x = units.next()); units.done()) {
-      const int tiles = x->tiles, head = x->head, k0 = x->s.k0;
-      for (int k = 0; k < tiles && ok; ++k) {
-        int key0, n, width;
-        x->tile(k, key0, n, width);
-        if (!x->needs(0, key0, n) && !x->needs(1, key0, n)) continue;
-        if (lane == 0) {
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (const Unit* x; ok && (x = units.next()); units.done()) {
+        const Keys keys(*x);
+        const int head = x->head, k0 = x->s.k0;
+        for (int k = 0; k < keys.tiles && ok; ++k) {
+          int key0, n;
+          keys.tile(k, key0, n);
+          if (!keys.needs<0>(key0, n) && !keys.needs<1>(key0, n)) continue;
           const uint32_t st = it % kStages, ph = ((it / kStages) & 1) ^ 1;
-          for (int side = 0; side < 2 && ok; ++side) {
+#pragma unroll
+          for (int side = 0; side < 2; ++side) {
             uint64_t* full = side ? &bars.v_full[st] : &bars.k_full[st];
             if (it >= kStages && !(ok = wait(side ? &bars.v_empty[st] : &bars.k_empty[st], ph))) break;
-            bar_expect(full, static_cast<uint32_t>(width) * 128 * L::kBlocks);
+            bar_expect(full, (n > kBox ? 2u : 1u) * kBox * 128 * L::kBlocks);
             const uint32_t dst = smem_addr(base + (side ? L::kV : L::kK) + st * L::kTile);
-            for (int r = 0; r < width; r += kBox)
 #pragma unroll
-              for (int c = 0; c < L::kBlocks; ++c)
-                tma_load_3d(dst + c * kBlockBytes + r * 128, side ? &map_v : &map_k, c * 64, head,
-                            k0 + key0 + r, full);
+            for (int r = 0; r < kKeys; r += kBox)
+              if (r < n)
+#pragma unroll
+                for (int c = 0; c < L::kBlocks; ++c)
+                  tma_load_3d(dst + c * kBlockBytes + r * 128, side ? &map_v : &map_k, c * 64, head,
+                              k0 + key0 + r, full);
           }
+          ++it;
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        ++it;
       }
-    }
-    if (lane == 0) {
       // loads in flight must land before the shared memory is released; after
       // a wait that gave up, the keys of a stage may be loaded and its values not
       const uint32_t from = it > kStages ? it - kStages : 0;
@@ -776,61 +825,6 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         while (now_ns() - t0 < 1000000) {}        // landed long before
       }
     }
-    __syncwarp();
-  } else if (warp == 10) {
-    // ------------------------------------------------------------ queries
-    uint32_t uses[2] = {0, 0};
-    bool ok = true;
-    for (const Unit* x; ok && (x = units.next()); units.done()) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (x->last[t] < 0) continue;
-        if (uses[t] > 0) ok = ok && __all_sync(0xffffffffu, wait(&bars.q_empty[t], (uses[t] - 1) & 1));
-        if (!ok) break;
-        ++uses[t];
-        const int row0 = x->row0 + 128 * t;
-        if (p.q_tma) {
-          if (lane == 0) {
-            bar_expect(&bars.q_full[t], L::kTile);
-#pragma unroll
-            for (int c = 0; c < L::kBlocks; ++c)
-              tma_load_3d(smem_addr(base + L::kQ + t * L::kTile + c * kBlockBytes), &map_q, c * 64,
-                          x->head * w.group, x->s.q0 + p.group(row0), &bars.q_full[t]);
-          }
-          __syncwarp();
-          continue;
-        }
-        constexpr int kChunks = D / 8;            // 16-byte chunks of a row
-        constexpr int kStep = kWarp / kChunks;    // rows of one warp-wide load
-        const int ch = lane % kChunks;
-        unsigned char* dst = base + L::kQ + t * L::kTile + (ch / 8) * kBlockBytes;
-        for (int r0 = 0; r0 < 128; r0 += 8 * kStep) {
-          uint4 q[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int r = r0 + j * kStep + lane / kChunks;
-            const int i = p.group(row0 + r);
-            q[j] = make_uint4(0, 0, 0, 0);
-            if (r < x->rows[t])
-              q[j] = __ldg(reinterpret_cast<const uint4*>(
-                               static_cast<const uint16_t*>(w.a.q) +
-                               (x->s.q0 + static_cast<int64_t>(i)) * w.a.ld_q +
-                               (x->head * w.group + row0 + r - i * w.group) * w.a.ld_q_head) +
-                           ch);
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<uint4*>(dst + swz_offset(r0 + j * kStep + lane / kChunks, ch % 8)) = q[j];
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) bar_arrive(&bars.q_full[t]);
-      }
-    }
-    // queries in flight must land before the shared memory is released
-    if (p.q_tma && lane == 0)
-      for (int t = 0; t < 2; ++t)
-        if (uses[t] > 0) wait.drain(&bars.q_full[t], (uses[t] - 1) & 1);
     __syncwarp();
   } else {
     // ------------------------------------------------------------ units
