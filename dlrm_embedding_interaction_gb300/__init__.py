@@ -668,6 +668,16 @@ class DlrmModel:
             pass
 
 
-from .history import (HistoryCache, history_append, history_attention,  # noqa: E402
-                      history_compact, history_copy, history_fork, history_free, history_trim,
-                      window_attention)
+# The event-history operators (history.py), loaded on first use: like the rest
+# of the binding, importing the package does not import torch.
+_HISTORY = ("HistoryCache", "history_append", "history_attention", "history_compact",
+            "history_copy", "history_fork", "history_free", "history_trim", "window_attention")
+
+
+def __getattr__(name: str):
+    if name not in _HISTORY:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import history
+    for n in _HISTORY:
+        globals()[n] = getattr(history, n)
+    return globals()[name]

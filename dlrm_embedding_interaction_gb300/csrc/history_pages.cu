@@ -300,59 +300,93 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(Pool p, int pieces) 
 
 constexpr int kWriteThreads = 128;
 
-// Quantises the new events of one page, head and side per iteration. The
-// scale needs the largest magnitude first, so the new rows are read twice,
-// the second time from L1 or L2. Where the page already holds events and its
-// scale grows, their codes are re-rounded: exact but for codes that become
-// subnormal, as scales are powers of two.
-template <int DT>
+// Eight consecutive elements as fp32.
+template <int DT, bool VEC>
+__device__ __forceinline__ void load8(float (&f)[8], const void* x, int64_t at) {
+  if (!VEC) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = load_element<DT>(x, at + i);
+  } else if (DT == DLRM_DTYPE_FP32) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
+    const float4 a = __ldg(p), b = __ldg(p + 1);
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+    f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  } else {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (DT == DLRM_DTYPE_BF16) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      } else {
+        const float2 h = f16x2_to_float2(w[i]);
+        f[2 * i] = h.x;
+        f[2 * i + 1] = h.y;
+      }
+    }
+  }
+}
+
+// Quantises the new events of one page, head and side per iteration, eight
+// elements a thread and step. The scale needs the largest magnitude first, so
+// the new rows are read twice, the second time from L1: a page's rows of one
+// head are at most 64 KB. Where the page already holds events and its scale
+// grows, their codes are re-rounded: exact but for codes that become subnormal,
+// as scales are powers of two.
+// VEC: rows at 16-byte boundaries.
+template <int DT, int D, bool VEC>
 __global__ void __launch_bounds__(kWriteThreads)
 append_kernel(Pool p, const int32_t* starts, const void* k, int64_t ld_k, int64_t ld_k_head,
               const void* v, int64_t ld_v, int64_t ld_v_head) {
   __shared__ uint32_t top[kWriteThreads / kWarp];
+  constexpr int kChunks = D / 8;                  // of a row
   const dlrm_history_t& h = p.h;
-  const int G = h.page_tokens, D = h.head_dim, H = h.n_heads;
+  const int G = h.page_tokens, H = h.n_heads;
   pdl_wait();
   pdl_trigger();
   const int64_t n = static_cast<int64_t>(p.head[kHeadItems]) * H * 2;
   for (int64_t w = blockIdx.x; w < n; w += gridDim.x) {
-    const int side = static_cast<int>(w & 1);
-    const int head = static_cast<int>((w >> 1) % H);
-    const int2 item = p.items[(w >> 1) / H];
+    // sides fastest, then heads: neighbouring CTAs read neighbouring rows
+    const int which = static_cast<int>(w / (2 * H)), rest = static_cast<int>(w - int64_t(which) * 2 * H);
+    const int side = rest >= H ? 1 : 0, head = rest - side * H;
+    const int2 item = p.items[which];
     const Request r = p.request[item.x];
     const int page = h.table[static_cast<int64_t>(r.slot) * h.max_pages + item.y];
     if (page < 0 || page >= h.n_pages) {   // a trimmed last page: cannot be, never written
       flag(h.err, DLRM_ERRBIT_INDEX_OOB);
       continue;
     }
-    const int kept = max(r.length - item.y * G, 0);             // events there already
-    const int end = min(static_cast<int>(min(static_cast<int64_t>(r.length) + r.count -
-                                                 static_cast<int64_t>(item.y) * G,
-                                             static_cast<int64_t>(G))), G);
-    const int64_t row0 = starts[item.x] + static_cast<int64_t>(item.y) * G - r.length;
+    const int64_t first = static_cast<int64_t>(item.y) * G;     // the page's first event
+    const int kept = static_cast<int>(max(r.length - first, int64_t(0)));   // events there already
+    const int end = static_cast<int>(min(int64_t(r.length) + r.count - first, int64_t(G)));
     const void* x = side ? v : k;
     const int64_t ld = side ? ld_v : ld_k;
-    const int64_t off = head * (side ? ld_v_head : ld_k_head);
+    const int64_t x0 = (starts[item.x] + first - r.length) * ld + head * (side ? ld_v_head : ld_k_head);
     const int64_t place = static_cast<int64_t>(page) * H + head;
     uint8_t* codes = (side ? h.v_codes : h.k_codes) + place * G * D;
     float* scale = (side ? h.v_scales : h.k_scales) + place;
 
     uint32_t big = 0;
-    for (int e = kept * D + threadIdx.x; e < end * D; e += kWriteThreads) {
-      const float f = load_element<DT>(x, (row0 + e / D) * ld + off + e % D);
-      const uint32_t u = __float_as_uint(f) & 0x7fffffffu;
-      if (u < 0x7f800000u) big = max(big, u);
+#pragma unroll 4
+    for (int e = kept * kChunks + threadIdx.x; e < end * kChunks; e += kWriteThreads) {
+      float f[8];
+      load8<DT, VEC>(f, x, x0 + (e / kChunks) * ld + e % kChunks * 8);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t u = __float_as_uint(f[i]) & 0x7fffffffu;
+        big = u < 0x7f800000u ? max(big, u) : big;
+      }
     }
     big = __reduce_max_sync(0xffffffffu, big);
-    __syncthreads();
+    __syncthreads();                                            // `top` of the item before is read
     if (threadIdx.x % kWarp == 0) top[threadIdx.x / kWarp] = big;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kWriteThreads / kWarp; ++i) big = max(big, top[i]);
     int e_new = scale_exponent(big);
     if (kept > 0) {
-      const float was = *scale;
-      const int e_old = static_cast<int>(__float_as_uint(was) >> 23) - 127;
+      const int e_old = static_cast<int>(__float_as_uint(*scale) >> 23) - 127;
       e_new = max(e_new, min(max(e_old, -kScaleExpMax), kScaleExpMax));
       if (e_new > e_old) {
         const float f = pow2f(max(e_old - e_new, -126));
@@ -364,15 +398,18 @@ append_kernel(Pool p, const int32_t* starts, const void* k, int64_t ld_k, int64_
           c4[i] = floats_to_e4m3x2(a.x * f, a.y * f) | (floats_to_e4m3x2(b.x * f, b.y * f) << 16);
         }
       }
+      __syncthreads();                                          // every thread has read *scale
     }
-    __syncthreads();                                            // every thread has read *scale
     if (threadIdx.x == 0) *scale = pow2f(e_new);
     const float inv = pow2f(-e_new);
-    uint16_t* c2 = reinterpret_cast<uint16_t*>(codes);
-    for (int e = kept * D / 2 + threadIdx.x; e < end * D / 2; e += kWriteThreads) {
-      const int64_t at = (row0 + 2 * e / D) * ld + off + 2 * e % D;
-      c2[e] = static_cast<uint16_t>(
-          floats_to_e4m3x2(load_element<DT>(x, at) * inv, load_element<DT>(x, at + 1) * inv));
+#pragma unroll 4
+    for (int e = kept * kChunks + threadIdx.x; e < end * kChunks; e += kWriteThreads) {
+      float f[8];
+      load8<DT, VEC>(f, x, x0 + (e / kChunks) * ld + e % kChunks * 8);
+      uint2 c;
+      c.x = floats_to_e4m3x2(f[0] * inv, f[1] * inv) | (floats_to_e4m3x2(f[2] * inv, f[3] * inv) << 16);
+      c.y = floats_to_e4m3x2(f[4] * inv, f[5] * inv) | (floats_to_e4m3x2(f[6] * inv, f[7] * inv) << 16);
+      reinterpret_cast<uint2*>(codes)[e] = c;
     }
   }
 }
@@ -598,12 +635,25 @@ unsigned grid_for(int64_t units, int per_sm) {
       1, std::min<int64_t>(units, static_cast<int64_t>(device_sm_count()) * per_sm)));
 }
 
+struct WriteArgs {
+  const int32_t* starts;
+  const void *k, *v;
+  int64_t ld_k, ld_k_head, ld_v, ld_v_head;
+  bool vec;
+};
+
+template <int DT, int D>
+cudaError_t launch_write_vec(const Pool& p, const WriteArgs& a, unsigned grid, cudaStream_t stream) {
+  return launch_pdl(a.vec ? append_kernel<DT, D, true> : append_kernel<DT, D, false>, dim3(grid),
+                    dim3(kWriteThreads), 0, stream, p, a.starts, a.k, a.ld_k, a.ld_k_head, a.v,
+                    a.ld_v, a.ld_v_head);
+}
+
 template <int DT>
-cudaError_t launch_write(const Pool& p, const int32_t* starts, const void* k, int64_t ld_k,
-                         int64_t ld_k_head, const void* v, int64_t ld_v, int64_t ld_v_head,
-                         unsigned grid, cudaStream_t stream) {
-  return launch_pdl(append_kernel<DT>, dim3(grid), dim3(kWriteThreads), 0, stream, p, starts, k,
-                    ld_k, ld_k_head, v, ld_v, ld_v_head);
+cudaError_t launch_write(const Pool& p, const WriteArgs& a, unsigned grid, cudaStream_t stream) {
+  if (p.h.head_dim == 32) return launch_write_vec<DT, 32>(p, a, grid, stream);
+  if (p.h.head_dim == 64) return launch_write_vec<DT, 64>(p, a, grid, stream);
+  return launch_write_vec<DT, 128>(p, a, grid, stream);
 }
 
 }  // namespace
@@ -628,11 +678,15 @@ cudaError_t launch_history_append(const dlrm_history_t& h, const int32_t* slots,
   // n new events touch at most n / G + 2 pages of a history
   const int64_t pages = std::min<int64_t>(rows, rows / h.page_tokens + 2 * int64_t(batch));
   const unsigned grid = grid_for(pages * h.n_heads * 2, 16);
-  if (dtype == DLRM_DTYPE_FP32)
-    return launch_write<DLRM_DTYPE_FP32>(p, starts, k, ld_k, ld_k_head, v, ld_v, ld_v_head, grid, stream);
-  if (dtype == DLRM_DTYPE_BF16)
-    return launch_write<DLRM_DTYPE_BF16>(p, starts, k, ld_k, ld_k_head, v, ld_v, ld_v_head, grid, stream);
-  return launch_write<DLRM_DTYPE_FP16>(p, starts, k, ld_k, ld_k_head, v, ld_v, ld_v_head, grid, stream);
+  const int64_t eb = dtype_bytes(dtype);
+  auto vec = [&](const void* x, int64_t ld, int64_t ld_head) {
+    return reinterpret_cast<uintptr_t>(x) % 16 == 0 && ld * eb % 16 == 0 && ld_head * eb % 16 == 0;
+  };
+  const WriteArgs a{starts, k, v, ld_k, ld_k_head, ld_v, ld_v_head,
+                    vec(k, ld_k, ld_k_head) && vec(v, ld_v, ld_v_head)};
+  if (dtype == DLRM_DTYPE_FP32) return launch_write<DLRM_DTYPE_FP32>(p, a, grid, stream);
+  if (dtype == DLRM_DTYPE_BF16) return launch_write<DLRM_DTYPE_BF16>(p, a, grid, stream);
+  return launch_write<DLRM_DTYPE_FP16>(p, a, grid, stream);
 }
 
 cudaError_t launch_history_fork(const dlrm_history_t& h, const int32_t* src, const int32_t* dst,

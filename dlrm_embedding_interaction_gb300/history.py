@@ -13,7 +13,10 @@ faults only the device sees (they set bits in the cache's error word, read by
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional
+
+import torch
 
 from . import (DlrmError, ERR_INDEX_OOB, ERR_INVALID_ARG, ERR_OOM, ERR_TIMEOUT, ERR_UNSUPPORTED,
                OK, _check, _stream, lib)
@@ -42,8 +45,15 @@ class _Attention(ctypes.Structure):
                 + [("scale", ctypes.c_float), ("err", _VP)])
 
 
+# The same fields as _Attention, packed in one call: a ctypes structure takes
+# as long to fill, attribute by attribute, as the launch takes.
+_ATTENTION = struct.Struct("@8P10q8if0PP")
+assert _ATTENTION.size == ctypes.sizeof(_Attention)
+
+
 def _bind(lib_):
-    st, h, a = ctypes.c_int, ctypes.POINTER(_History), ctypes.POINTER(_Attention)
+    # attention arguments: a _Attention by reference, or its packed bytes
+    st, h, a = ctypes.c_int, ctypes.POINTER(_History), _VP
     sig = {
         "history_work_bytes": ([h], _I64),
         "history_reset": ([h, _VP], st),
@@ -62,16 +72,29 @@ def _bind(lib_):
         fn.argtypes, fn.restype = args, res
 
 
+_DTYPES = {torch.float32: DTYPE_FP32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16}
+
+
 def _dtype_code(t, name: str) -> int:
-    import torch
-    codes = {torch.float32: DTYPE_FP32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16}
-    if t.dtype not in codes:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
         raise TypeError(f"{name}: expected float32, bfloat16 or float16, got {t.dtype}")
-    return codes[t.dtype]
+    return code
+
+
+def _raw_stream(stream, device):
+    """The cudaStream_t of ``stream``, or of the device's current stream (read
+    without making a Stream object, which takes microseconds)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return _stream(stream)
 
 
 def _int32_vector(t, name: str, n: Optional[int], device) -> int:
-    import torch
+    if (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.dim() == 1
+            and t.get_device() == (device.index if device.type == "cuda" else -1)
+            and t.is_contiguous() and (n is None or t.shape[0] == n)):
+        return t.shape[0]
     if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
         raise TypeError(f"{name}: expected an int32 tensor")
     if t.dim() != 1 or (n is not None and t.shape[0] != n):
@@ -85,16 +108,16 @@ def _int32_vector(t, name: str, n: Optional[int], device) -> int:
 
 def _rows(t, name: str, heads: Optional[int], dim: Optional[int], device):
     """A (rows, heads, dim) tensor with unit stride along dim."""
-    import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (
-            dim is not None and t.shape[2] != dim):
+    shape = t.shape
+    if len(shape) != 3 or (heads is not None and shape[1] != heads) or (
+            dim is not None and shape[2] != dim):
         raise ValueError(f"{name}: expected (rows, {heads or 'heads'}, {dim or 'dim'}), "
-                         f"got {tuple(t.shape)}")
-    if t.device != device:
+                         f"got {tuple(shape)}")
+    if t.get_device() != (device.index if device.type == "cuda" else -1):
         raise ValueError(f"{name}: must be on {device}")
-    if t.numel() and t.shape[2] > 1 and t.stride(2) != 1:
+    if shape[2] > 1 and t.stride(2) != 1 and t.numel():
         raise ValueError(f"{name}: its last dimension must be contiguous")
 
 
@@ -110,7 +133,6 @@ class HistoryCache:
 
     def __init__(self, n_pages: int, n_slots: int, max_pages: int, n_heads: int, head_dim: int,
                  page_tokens: int = 64, device="cuda", stream=None):
-        import torch
         device = torch.device(device)
         if device.type != "cuda":
             raise ValueError("HistoryCache: device must be a CUDA device")
@@ -148,13 +170,12 @@ class HistoryCache:
 
     def reset(self, stream=None) -> None:
         """Every page free, every slot empty, the error word cleared."""
-        _check(_bound().history_reset(self._ref, _stream(stream)), "history_reset")
+        _check(_bound().history_reset(self._ref, _raw_stream(stream, self.device)), "history_reset")
 
     def error(self, stream=None) -> int:
         """Waits for ``stream``, returns the first error that the device recorded
         since the last call (INDEX_OOB before UNSUPPORTED, OOM, INVALID_ARG and
         TIMEOUT; OK if none) and clears it."""
-        import torch
         s = torch.cuda.current_stream(self.device) if stream is None else stream
         if not isinstance(s, torch.cuda.Stream):
             s = torch.cuda.ExternalStream(int(s), device=self.device)
@@ -205,7 +226,8 @@ def history_append(cache: HistoryCache, slots, starts, k, v, stream=None) -> Non
         raise ValueError(f"{where}: {b} requests for {c.n_slots} slots")
     _check(_bound().history_append(c._ref, slots.data_ptr(), starts.data_ptr(), b, k.data_ptr(),
                                    k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
-                                   v.stride(1), k.shape[0], dt, _stream(stream)), where)
+                                   v.stride(1), k.shape[0], dt, _raw_stream(stream, c.device)),
+           where)
 
 
 def _slots_call(name: str, cache, vectors, stream, *more) -> None:
@@ -216,7 +238,7 @@ def _slots_call(name: str, cache, vectors, stream, *more) -> None:
     if b > c.n_slots:
         raise ValueError(f"{name}: {b} requests for {c.n_slots} slots")
     _check(getattr(_bound(), name)(c._ref, *[t.data_ptr() for _, t in vectors], b, *more,
-                                   _stream(stream)), name)
+                                   _raw_stream(stream, c.device)), name)
 
 
 def history_fork(cache: HistoryCache, src, dst, stream=None) -> None:
@@ -245,34 +267,26 @@ def history_trim(cache: HistoryCache, slots, window: int, sinks: int = 0, stream
 
 def history_compact(cache: HistoryCache, stream=None) -> None:
     """Moves pages in use to the front of the pool and rebuilds the free stack."""
-    _check(_bound().history_compact(_cache_of(cache, "history_compact")._ref, _stream(stream)),
-           "history_compact")
+    c = _cache_of(cache, "history_compact")
+    _check(_bound().history_compact(c._ref, _raw_stream(stream, c.device)), "history_compact")
 
 
-def _attention(where, a, q, out, lse, scale, window, sinks, device):
-    import torch
-    a.dtype = _dtype_code(q, f"{where}: q")
+def _check_outputs(where, q, out, lse, window, sinks, device):
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=device)
-    elif out.dtype != q.dtype:
-        raise TypeError(f"{where}: out: expected {q.dtype}, got {out.dtype}")
-    _rows(out, f"{where}: out", q.shape[1], q.shape[2], device)
-    if out.shape[0] != q.shape[0]:
-        raise ValueError(f"{where}: out: expected {q.shape[0]} rows, got {out.shape[0]}")
+    else:
+        if not isinstance(out, torch.Tensor) or out.dtype is not q.dtype:
+            raise TypeError(f"{where}: out: expected a {q.dtype} tensor")
+        _rows(out, f"{where}: out", q.shape[1], q.shape[2], device)
+        if out.shape[0] != q.shape[0]:
+            raise ValueError(f"{where}: out: expected {q.shape[0]} rows, got {out.shape[0]}")
     if lse is not None:
-        if not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32:
+        if not isinstance(lse, torch.Tensor) or lse.dtype is not torch.float32:
             raise TypeError(f"{where}: lse: expected a float32 tensor")
-        if tuple(lse.shape) != tuple(q.shape[:2]) or lse.device != device or not lse.is_contiguous():
+        if lse.shape != q.shape[:2] or lse.device != device or not lse.is_contiguous():
             raise ValueError(f"{where}: lse: expected contiguous {tuple(q.shape[:2])} on {device}")
-        a.lse = lse.data_ptr()
     if window < 0 or sinks < 0:
         raise ValueError(f"{where}: window and sinks must not be negative")
-    a.q, a.out = q.data_ptr(), out.data_ptr()
-    a.q_rows, a.n_heads, a.head_dim = q.shape
-    a.ld_q, a.ld_q_head = q.stride(0), q.stride(1)
-    a.ld_out, a.ld_out_head = out.stride(0), out.stride(1)
-    a.window, a.sinks = int(window), int(sinks)
-    a.scale = q.shape[2] ** -0.5 if scale is None else float(scale)
     return out
 
 
@@ -295,10 +309,15 @@ def history_attention(cache: HistoryCache, slots, starts, q, out=None, *, scale=
     _rows(q, f"{where}: q", None, c.head_dim, c.device)
     if q.shape[1] < 1 or q.shape[1] % c.n_heads:
         raise ValueError(f"{where}: q: {q.shape[1]} heads are no multiple of the cache's {c.n_heads}")
-    a = _Attention()
-    out = _attention(where, a, q, out, lse, scale, window, sinks, c.device)
-    a.slots, a.q_starts, a.batch, a.causal = slots.data_ptr(), starts.data_ptr(), b, int(causal)
-    _check(_bound().history_attention(c._ref, ctypes.byref(a), _stream(stream)), where)
+    dtype = _dtype_code(q, f"{where}: q")
+    out = _check_outputs(where, q, out, lse, window, sinks, c.device)
+    rows, heads, dim = q.shape
+    qs, os = q.stride(), out.stride()
+    args = _ATTENTION.pack(
+        q.data_ptr(), 0, 0, out.data_ptr(), 0 if lse is None else lse.data_ptr(), slots.data_ptr(),
+        starts.data_ptr(), 0, rows, 0, qs[0], qs[1], 0, 0, 0, 0, os[0], os[1], b, heads, c.n_heads,
+        dim, dtype, causal, window, sinks, dim ** -0.5 if scale is None else scale, 0)
+    _check(_bound().history_attention(c._ref, args, _raw_stream(stream, c.device)), where)
     return out
 
 
@@ -311,12 +330,11 @@ def window_attention(q, k, v, starts, out=None, *, k_starts=None, scale=None, wi
     kv heads, head_dim); ``k_starts`` defaults to ``starts``. Its queries stand at
     the last positions of its keys. ``window``, ``sinks``, ``scale`` and ``lse`` as in
     history_attention. ``err_flag``: (1,) int32, receives the error bit of bad starts."""
-    import torch
     where = "window_attention"
     for t, name in ((q, "q"), (k, "k"), (v, "v")):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{where}: {name} must be a torch.Tensor")
-        if t.dtype != q.dtype:
+        if t.dtype is not q.dtype:
             raise TypeError(f"{where}: {name}: expected {q.dtype}, got {t.dtype}")
     if not q.is_cuda:
         raise ValueError(f"{where}: q must be a CUDA tensor")
@@ -334,14 +352,17 @@ def window_attention(q, k, v, starts, out=None, *, k_starts=None, scale=None, wi
     if b < 0:
         raise ValueError(f"{where}: starts: expected at least one entry")
     _int32_vector(k_starts, f"{where}: k_starts", b + 1, dev)
-    a = _Attention()
-    out = _attention(where, a, q, out, lse, scale, window, sinks, dev)
+    dtype = _dtype_code(q, f"{where}: q")
+    out = _check_outputs(where, q, out, lse, window, sinks, dev)
     if err_flag is not None:
         _int32_vector(err_flag, f"{where}: err_flag", 1, dev)
-        a.err = err_flag.data_ptr()
-    a.k, a.v = k.data_ptr(), v.data_ptr()
-    a.k_rows, a.n_kv_heads = k.shape[0], k.shape[1]
-    a.ld_k, a.ld_k_head, a.ld_v, a.ld_v_head = k.stride(0), k.stride(1), v.stride(0), v.stride(1)
-    a.q_starts, a.k_starts, a.batch, a.causal = starts.data_ptr(), k_starts.data_ptr(), b, 1
-    _check(_bound().window_attention(ctypes.byref(a), _stream(stream)), where)
+    rows, heads, dim = q.shape
+    qs, ks, vs, os = q.stride(), k.stride(), v.stride(), out.stride()
+    args = _ATTENTION.pack(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+        0 if lse is None else lse.data_ptr(), 0, starts.data_ptr(), k_starts.data_ptr(), rows,
+        k.shape[0], qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os[0], os[1], b, heads, k.shape[1],
+        dim, dtype, 1, window, sinks, dim ** -0.5 if scale is None else scale,
+        0 if err_flag is None else err_flag.data_ptr())
+    _check(_bound().window_attention(args, _raw_stream(stream, dev)), where)
     return out
