@@ -6,8 +6,9 @@
 // A call is a chain of small launches (programmatic dependent launches: each
 // starts its set-up while the one before it ends):
 //   append     plan (one CTA), write
-//   fork/copy  plan (one CTA), copy
-//   free/trim  release, count, push (one CTA a request)
+//   fork       plan (one CTA), share and copy
+//   copy       plan (one CTA), rows, copy
+//   free/trim  one CTA for few pages; else release, count, push (a CTA a request)
 //   compact    count, match, move, rename
 // The plan gives every request its place in the free stack by a prefix sum
 // over the requests, so page numbers do not depend on timing; freed pages are
@@ -99,11 +100,11 @@ __device__ __forceinline__ int block_exclusive(int x, int* sums, int& total) {
 
 enum PlanOp { kAppend, kFork, kCopy };
 
-// One CTA: gives every request its pages. Phases over all requests, with a
-// barrier between them, so that a request sees the pool as it was before the
-// call: (1) mark the slots written, the first request of a slot winning;
-// (2) check each request and count the pages it needs; (3) prefix sums give
-// stack places and work items; (4) write tables and reference counts.
+// One CTA, a thread a request: gives every request its place in the free stack
+// and in the list of work items by prefix sums. It reads tables and lengths
+// but does not change them (the next launch does), so every request sees the
+// pool as it was before the call. Of several requests that write one slot the
+// first wins: phase 1 marks the slots.
 template <int OP>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Pool p, const int32_t* src,
                                                             const int32_t* dst,
@@ -111,67 +112,17 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Pool p, const int32_
                                                             int64_t rows) {
   __shared__ int sums[kWarp + 1];
   __shared__ int done;
+  __shared__ int count_s[OP == kCopy ? kPlanThreads : 1], source_s[OP == kCopy ? kPlanThreads : 1];
   const dlrm_history_t& h = p.h;
-  const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp, warps = kPlanThreads / kWarp;
+  const int lane = threadIdx.x % kWarp;
   const int G = h.page_tokens, M = h.max_pages;
   pdl_wait();
   pdl_trigger();
   const int nfree = min(max(*h.n_free, 0), h.n_pages);
   if (threadIdx.x == 0) done = 0;
-
   for (int b = threadIdx.x; b < batch; b += kPlanThreads) {
     const int d = dst[b];
     if (d >= 0 && d < h.n_slots) atomicMin(&p.mark_slot[d], b);
-  }
-  __syncthreads();
-
-  for (int b = warp; b < batch; b += warps) {
-    Request r{-1, -1, 0, 0, 0, 0, 0, 0};
-    const int d = dst[b], s = OP == kAppend ? d : src[b];
-    uint32_t bad = 0;
-    if (d < 0 || d >= h.n_slots || s < 0 || s >= h.n_slots) {
-      bad = DLRM_ERRBIT_INDEX_OOB;
-    } else if (p.mark_slot[d] != b) {
-      bad = DLRM_ERRBIT_INVALID_ARG;
-    } else {
-      r.slot = d;
-      r.source = s;
-      const int64_t cap = static_cast<int64_t>(M) * G;
-      r.length = static_cast<int>(min(static_cast<int64_t>(max(h.lengths[s], 0)), cap));
-      if (OP == kAppend) {
-        const int t0 = starts[b], t1 = starts[b + 1];
-        if (t0 < 0 || t1 < t0 || t1 > rows) {
-          bad = DLRM_ERRBIT_OFFSETS;
-        } else if (r.length + static_cast<int64_t>(t1 - t0) > cap) {
-          bad = DLRM_ERRBIT_INVALID_ARG;
-        } else {
-          r.count = t1 - t0;
-          const int old = (r.length + G - 1) / G;
-          r.need = static_cast<int>((r.length + static_cast<int64_t>(r.count) + G - 1) / G) - old;
-          r.items = r.need + (r.count > 0 && r.length % G != 0 ? 1 : 0);
-        }
-      } else if (h.lengths[d] != 0) {
-        bad = DLRM_ERRBIT_INVALID_ARG;
-      } else if (OP == kFork) {
-        r.need = r.length % G != 0 ? 1 : 0;
-        r.items = r.need;
-      } else {
-        const int n = (r.length + G - 1) / G;
-        int c = 0;
-        for (int j = lane; j < n; j += kWarp)
-          c += h.table[static_cast<int64_t>(s) * M + j] >= 0 ? 1 : 0;
-        r.need = __reduce_add_sync(0xffffffffu, c);
-        r.items = r.need;
-      }
-    }
-    if (bad) {
-      r.slot = -1;
-      r.need = r.items = 0;
-    }
-    if (lane == 0) {
-      if (bad) flag(h.err, bad);
-      p.request[b] = r;
-    }
   }
   __syncthreads();
 
@@ -179,74 +130,104 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Pool p, const int32_
   for (int b0 = 0; b0 < batch; b0 += kPlanThreads) {
     const int b = b0 + static_cast<int>(threadIdx.x);
     Request r{-1, -1, 0, 0, 0, 0, 0, 0};
-    if (b < batch) r = p.request[b];
+    uint32_t bad = 0;
+    if (b < batch) {
+      const int d = dst[b], s = OP == kAppend ? d : src[b];
+      if (d < 0 || d >= h.n_slots || s < 0 || s >= h.n_slots) {
+        bad = DLRM_ERRBIT_INDEX_OOB;
+      } else if (__ldcg(&p.mark_slot[d]) != b) {
+        bad = DLRM_ERRBIT_INVALID_ARG;
+      } else {
+        r.slot = d;
+        r.source = s;
+        const int64_t cap = static_cast<int64_t>(M) * G;
+        r.length = static_cast<int>(min(static_cast<int64_t>(max(h.lengths[s], 0)), cap));
+        if (OP == kAppend) {
+          const int t0 = starts[b], t1 = starts[b + 1];
+          if (t0 < 0 || t1 < t0 || t1 > rows) {
+            bad = DLRM_ERRBIT_OFFSETS;
+          } else if (r.length + static_cast<int64_t>(t1 - t0) > cap) {
+            bad = DLRM_ERRBIT_INVALID_ARG;
+          } else {
+            r.count = t1 - t0;
+            const int old = (r.length + G - 1) / G;
+            r.need = static_cast<int>((r.length + static_cast<int64_t>(r.count) + G - 1) / G) - old;
+            r.items = r.need + (r.count > 0 && r.length % G != 0 ? 1 : 0);
+          }
+        } else if (h.lengths[d] != 0) {
+          bad = DLRM_ERRBIT_INVALID_ARG;
+        } else if (OP == kFork) {
+          r.need = r.length % G != 0 ? 1 : 0;
+        }
+      }
+    }
+    if (bad) {
+      flag(h.err, bad);
+      r.slot = -1;
+      r.need = r.items = 0;
+    }
+    if (OP == kCopy) {
+      // pages that a request copies (a trimmed history misses some), counted by
+      // a warp a request
+      count_s[threadIdx.x] = r.slot >= 0 ? (r.length + G - 1) / G : 0;
+      source_s[threadIdx.x] = r.source;
+      __syncthreads();
+      for (int i = threadIdx.x / kWarp; i < min(kPlanThreads, batch - b0); i += kPlanThreads / kWarp) {
+        int c = 0;
+        for (int j = lane; j < count_s[i]; j += kWarp)
+          c += h.table[static_cast<int64_t>(source_s[i]) * M + j] >= 0 ? 1 : 0;
+        c = __reduce_add_sync(0xffffffffu, c);
+        if (lane == 0) count_s[i] = c;
+      }
+      __syncthreads();
+      if (b < batch) r.need = r.items = count_s[threadIdx.x];
+    }
     int total;
     r.base = base + block_exclusive(r.need, sums, total);
     // saturates: past nfree every later request that needs a page fails
     base = min(base + total, h.n_pages + 1);
-    const bool short_of = r.need > 0 && r.base + static_cast<int64_t>(r.need) > nfree;
-    if (short_of) {
-      flag(h.err, DLRM_ERRBIT_OOM);
-      r.slot = -1;
-      r.items = 0;
-    } else if (r.need > 0) {
-      atomicMax(&done, r.base + r.need);
+    if (r.need > 0) {
+      if (r.base + static_cast<int64_t>(r.need) > nfree) {
+        flag(h.err, DLRM_ERRBIT_OOM);
+        r.slot = -1;
+        r.items = 0;
+      } else {
+        atomicMax(&done, r.base + r.need);
+      }
     }
-    r.item0 = items + block_exclusive(r.items, sums, total);
-    items += total;
-    if (b < batch) p.request[b] = r;
-  }
-  __syncthreads();
-
-  for (int b = warp; b < batch; b += warps) {
-    const Request r = p.request[b];
-    if (lane == 0) {
-      const int d = dst[b];
-      if (d >= 0 && d < h.n_slots && p.mark_slot[d] == b) p.mark_slot[d] = INT32_MAX;
+    if (OP != kFork) {
+      r.item0 = items + block_exclusive(r.items, sums, total);
+      items += total;
     }
-    if (r.slot < 0) continue;
-    int32_t* row = h.table + static_cast<int64_t>(r.slot) * M;
+    if (b < batch) {
+      p.request[b] = r;
+      if (r.source >= 0) p.mark_slot[dst[b]] = INT32_MAX;   // this request's own mark
+    }
     if (OP == kAppend) {
-      const int first = (r.length + G - 1) / G;
-      for (int i = lane; i < r.need; i += kWarp) {
-        const int page = h.free_pages[nfree - 1 - (r.base + i)];
-        row[first + i] = page;
-        h.refs[page] = 1;
+      // work items (request, page of the history); long lists by the whole warp
+      if (r.items <= 2) {
+        for (int i = 0; i < r.items; ++i) p.items[r.item0 + i] = make_int2(b, r.length / G + i);
       }
-      for (int i = lane; i < r.items; i += kWarp)
-        p.items[r.item0 + i] = make_int2(b, r.length / G + i);
-      if (lane == 0) h.lengths[r.slot] = r.length + r.count;
-    } else {
-      const int32_t* from = h.table + static_cast<int64_t>(r.source) * M;
-      const int n = (r.length + G - 1) / G;
-      const int full = OP == kFork ? r.length / G : 0;
-      int taken = 0;
-      for (int j0 = 0; j0 < n; j0 += kWarp) {
-        const int j = j0 + lane;
-        const int old = j < n ? from[j] : -1;
-        const bool fresh = old >= 0 && j >= full;
-        const unsigned mask = __ballot_sync(0xffffffffu, fresh);
-        if (fresh) {
-          const int rank = taken + __popc(mask & ((1u << lane) - 1));
-          // a page missing from a fork's last entry leaves its stack place
-          // unused only if the table broke its own rules; never read past it
-          const int page = h.free_pages[nfree - 1 - (r.base + rank)];
-          row[j] = page;
-          h.refs[page] = 1;
-          p.items[r.item0 + rank] = make_int2(old, page);
-        } else if (j < n) {
-          row[j] = old;
-          if (old >= 0) atomicAdd(&h.refs[old], 1);
-        }
-        taken += __popc(mask);
+      for (unsigned many = __ballot_sync(0xffffffffu, r.items > 2); many; many &= many - 1) {
+        const int l = __ffs(many) - 1;
+        const int n = __shfl_sync(0xffffffffu, r.items, l), at = __shfl_sync(0xffffffffu, r.item0, l);
+        const int first = __shfl_sync(0xffffffffu, r.length / G, l);
+        const int of = __shfl_sync(0xffffffffu, b, l);
+        for (int i = lane; i < n; i += kWarp) p.items[at + i] = make_int2(of, first + i);
       }
-      if (lane == 0) h.lengths[r.slot] = r.length;
     }
+    __syncthreads();                              // `sums` before the next requests
   }
   if (threadIdx.x == 0) {
     p.head[kHeadItems] = items;
+    p.head[kHeadTop] = nfree;
     *h.n_free = nfree - done;
   }
+}
+
+// Page number `rank` of request r.
+__device__ __forceinline__ int granted(const Pool& p, const Request& r, int top, int rank) {
+  return p.h.free_pages[top - 1 - (r.base + rank)];
 }
 
 // ------------------------------------------------------------------ copy
@@ -283,6 +264,68 @@ __device__ __forceinline__ void copy_piece(const dlrm_history_t& h, int side, in
 __host__ __device__ __forceinline__ int pieces_of(const dlrm_history_t& h) {
   const int64_t bytes = static_cast<int64_t>(h.n_heads) * h.page_tokens * h.head_dim;
   return static_cast<int>((bytes + kCopyPiece - 1) / kCopyPiece);
+}
+
+// A fork's table row, by the CTAs (request, piece): full pages are shared, and
+// piece by piece the last page that is not full is copied. Piece 0 writes the row.
+__global__ void __launch_bounds__(kCopyThreads) fork_kernel(Pool p, int pieces) {
+  pdl_wait();
+  pdl_trigger();
+  const dlrm_history_t& h = p.h;
+  const int G = h.page_tokens, M = h.max_pages;
+  const Request r = p.request[blockIdx.x];
+  if (r.slot < 0) return;
+  const int32_t* from = h.table + static_cast<int64_t>(r.source) * M;
+  const int full = r.length / G;
+  const int last = r.need > 0 ? from[full] : -1;
+  const int page = r.need > 0 ? granted(p, r, p.head[kHeadTop], 0) : -1;
+  if (blockIdx.y == 0) {
+    int32_t* row = h.table + static_cast<int64_t>(r.slot) * M;
+    for (int j = threadIdx.x; j < full; j += kCopyThreads) {
+      const int old = from[j];
+      row[j] = old;
+      if (old >= 0) atomicAdd(&h.refs[old], 1);
+    }
+    if (threadIdx.x == 0) {
+      if (r.need > 0) {
+        row[full] = page;
+        h.refs[page] = 1;
+      }
+      h.lengths[r.slot] = r.length;
+    }
+  }
+  // (a last page that is not full is never trimmed; a broken table's is not read)
+  if (last >= 0 && last < h.n_pages)
+    copy_piece(h, blockIdx.y / pieces, blockIdx.y % pieces, last, page);
+}
+
+// A copy's table row, by one CTA a request: the list of pages to copy.
+__global__ void __launch_bounds__(kCopyThreads) copy_rows_kernel(Pool p) {
+  __shared__ int sums[kWarp + 1];
+  pdl_wait();
+  pdl_trigger();
+  const dlrm_history_t& h = p.h;
+  const int G = h.page_tokens, M = h.max_pages;
+  const Request r = p.request[blockIdx.x];
+  if (r.slot < 0) return;
+  const int32_t* from = h.table + static_cast<int64_t>(r.source) * M;
+  int32_t* row = h.table + static_cast<int64_t>(r.slot) * M;
+  const int n = (r.length + G - 1) / G, top = p.head[kHeadTop];
+  int taken = 0;
+  for (int j0 = 0; j0 < n; j0 += kCopyThreads) {
+    const int j = j0 + static_cast<int>(threadIdx.x);
+    const int old = j < n ? from[j] : -1;
+    int total;
+    const int rank = taken + block_exclusive(old >= 0 ? 1 : 0, sums, total);
+    if (old >= 0) {
+      const int page = granted(p, r, top, rank);
+      row[j] = page;
+      h.refs[page] = 1;
+      p.items[r.item0 + rank] = make_int2(old, page);
+    }
+    taken += total;
+  }
+  if (threadIdx.x == 0) h.lengths[r.slot] = r.length;
 }
 
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(Pool p, int pieces) {
@@ -352,8 +395,20 @@ append_kernel(Pool p, const int32_t* starts, const void* k, int64_t ld_k, int64_
     const int side = rest >= H ? 1 : 0, head = rest - side * H;
     const int2 item = p.items[which];
     const Request r = p.request[item.x];
-    const int page = h.table[static_cast<int64_t>(r.slot) * h.max_pages + item.y];
-    if (page < 0 || page >= h.n_pages) {   // a trimmed last page: cannot be, never written
+    // the page there already, or one that the plan granted; one of the item's
+    // workers writes it down, one of the last item's the new length
+    int32_t* entry = h.table + static_cast<int64_t>(r.slot) * h.max_pages + item.y;
+    const int had = (r.length + G - 1) / G;
+    const bool fresh = item.y >= had;
+    const int page = fresh ? granted(p, r, p.head[kHeadTop], item.y - had) : *entry;
+    if (rest == 0 && threadIdx.x == 0) {
+      if (fresh) {
+        *entry = page;
+        h.refs[page] = 1;
+      }
+      if (which + 1 == r.item0 + r.items) h.lengths[r.slot] = r.length + r.count;
+    }
+    if (page < 0 || page >= h.n_pages) {   // a broken table: a last page that is not full is never trimmed
       flag(h.err, DLRM_ERRBIT_INDEX_OOB);
       continue;
     }
@@ -526,6 +581,106 @@ __global__ void __launch_bounds__(kFreeThreads) push_kernel(Pool p, int batch, i
   }
 }
 
+// release, count and push in one CTA, with barriers for launches: a warp a
+// request. For calls of few pages three launches take longer than the work.
+constexpr int kFreeSmallBatch = 256, kFreeSmallEntries = 16384;
+
+__global__ void __launch_bounds__(kPlanThreads) free_small_kernel(Pool p, const int32_t* slots,
+                                                                  int batch, int window, int sinks) {
+  __shared__ int slot_s[kFreeSmallBatch], first_s[kFreeSmallBatch], last_s[kFreeSmallBatch];
+  __shared__ int freed_s[kFreeSmallBatch];
+  const dlrm_history_t& h = p.h;
+  const int G = h.page_tokens, M = h.max_pages;
+  const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp, warps = kPlanThreads / kWarp;
+  pdl_wait();
+  pdl_trigger();
+  const int top = min(max(*h.n_free, 0), h.n_pages);
+  for (int b = threadIdx.x; b < batch; b += kPlanThreads) slot_s[b] = slots[b];
+  __syncthreads();
+  for (int b = warp; b < batch; b += warps) {
+    const int slot = slot_s[b];
+    const bool in = slot >= 0 && slot < h.n_slots;
+    bool again = false;                           // listed before: nothing left
+    for (int i = lane; i < b; i += kWarp) again |= slot_s[i] == slot;
+    again = __any_sync(0xffffffffu, again);
+    int first = 0, last = 0;
+    if (in && !again) {
+      const int64_t len = max(h.lengths[slot], 0);
+      last = static_cast<int>(min((len + G - 1) / G, static_cast<int64_t>(M)));
+      if (window > 0) {
+        first = static_cast<int>(min((static_cast<int64_t>(sinks) + G - 1) / G,
+                                     static_cast<int64_t>(last)));
+        last = len < window ? first
+                            : static_cast<int>(max((len - window) / G, static_cast<int64_t>(first)));
+      }
+    }
+    if (lane == 0) {
+      if (!in) flag(h.err, DLRM_ERRBIT_INDEX_OOB);
+      first_s[b] = first;
+      last_s[b] = last;
+    }
+    for (int j = first + lane; j < last; j += kWarp) {
+      const int64_t at = static_cast<int64_t>(slot) * M + j;
+      int page = h.table[at];
+      if (page < 0 || page >= h.n_pages) {
+        page = -1;
+      } else {
+        atomicSub(&h.refs[page], 1);
+        atomicMax(&p.mark_page[page], b * M + j);
+      }
+      h.table[at] = -1;
+      p.stash[b * M + j] = page;
+    }
+    if (window == 0 && in && !again && lane == 0) h.lengths[slot] = 0;
+  }
+  __threadfence_block();
+  __syncthreads();
+  auto pushed = [&](int b, int j, int& page) {
+    page = j < last_s[b] ? __ldcg(&p.stash[b * M + j]) : -1;
+    if (page < 0) return false;
+    if (__ldcg(&p.mark_page[page]) != b * M + j) {
+      page = -1;
+      return false;
+    }
+    return __ldcg(&h.refs[page]) <= 0;
+  };
+  for (int b = warp; b < batch; b += warps) {
+    int n = 0;
+    for (int j0 = first_s[b]; j0 < last_s[b]; j0 += kWarp) {
+      int page;
+      n += __popc(__ballot_sync(0xffffffffu, pushed(b, j0 + lane, page)));
+    }
+    if (lane == 0) freed_s[b] = n;
+  }
+  __syncthreads();
+  int all = 0;
+  for (int b = warp; b < batch; b += warps) {
+    int later = 0;
+    all = 0;
+    for (int i = lane; i < batch; i += kWarp) {
+      later += i > b ? freed_s[i] : 0;
+      all += freed_s[i];
+    }
+    later = __reduce_add_sync(0xffffffffu, later);
+    all = __reduce_add_sync(0xffffffffu, all);
+    int left = freed_s[b];
+    for (int j0 = first_s[b]; j0 < last_s[b]; j0 += kWarp) {
+      int page;
+      const bool push = pushed(b, j0 + lane, page);
+      const unsigned who = __ballot_sync(0xffffffffu, push);
+      if (push) {
+        const int q = later + left - 1 - __popc(who & ((1u << lane) - 1));
+        if (top + q < h.n_pages) h.free_pages[top + q] = page;
+        h.refs[page] = 0;
+      }
+      // only its own position's reader can still ask for this mark
+      if (page >= 0) p.mark_page[page] = -1;
+      left -= __popc(who);
+    }
+  }
+  if (threadIdx.x == 0) *h.n_free = min(top + all, h.n_pages);
+}
+
 // ------------------------------------------------------------------ compact
 
 constexpr int kTile = 1024;   // pages a CTA looks at
@@ -692,15 +847,16 @@ cudaError_t launch_history_append(const dlrm_history_t& h, const int32_t* slots,
 cudaError_t launch_history_fork(const dlrm_history_t& h, const int32_t* src, const int32_t* dst,
                                 int batch, bool share, cudaStream_t stream) {
   const Pool p = make_pool(h);
-  cudaError_t e = share ? launch_pdl(plan_kernel<kFork>, dim3(1), dim3(kPlanThreads), 0, stream, p,
-                                     src, dst, static_cast<const int32_t*>(nullptr), batch,
-                                     int64_t(0))
-                        : launch_pdl(plan_kernel<kCopy>, dim3(1), dim3(kPlanThreads), 0, stream, p,
-                                     src, dst, static_cast<const int32_t*>(nullptr), batch,
-                                     int64_t(0));
-  if (e != cudaSuccess) return e;
   const int pieces = pieces_of(h);
-  const int64_t pages = std::min<int64_t>(h.n_pages, int64_t(batch) * (share ? 1 : h.max_pages));
+  const int32_t* none = nullptr;
+  cudaError_t e = launch_pdl(share ? plan_kernel<kFork> : plan_kernel<kCopy>, dim3(1),
+                             dim3(kPlanThreads), 0, stream, p, src, dst, none, batch, int64_t(0));
+  if (e != cudaSuccess) return e;
+  if (share)
+    return launch_pdl(fork_kernel, dim3(batch, 2 * pieces), dim3(kCopyThreads), 0, stream, p, pieces);
+  e = launch_pdl(copy_rows_kernel, dim3(batch), dim3(kCopyThreads), 0, stream, p);
+  if (e != cudaSuccess) return e;
+  const int64_t pages = std::min<int64_t>(h.n_pages, int64_t(batch) * h.max_pages);
   return launch_pdl(copy_kernel, dim3(grid_for(pages * 2 * pieces, 8)), dim3(kCopyThreads), 0,
                     stream, p, pieces);
 }
@@ -708,6 +864,9 @@ cudaError_t launch_history_fork(const dlrm_history_t& h, const int32_t* src, con
 cudaError_t launch_history_free(const dlrm_history_t& h, const int32_t* slots, int batch,
                                 int window, int sinks, cudaStream_t stream) {
   const Pool p = make_pool(h);
+  if (batch <= kFreeSmallBatch && int64_t(batch) * h.max_pages <= kFreeSmallEntries)
+    return launch_pdl(free_small_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p, slots, batch,
+                      window, sinks);
   cudaError_t e = launch_pdl(release_kernel, dim3(batch), dim3(kFreeThreads), 0, stream, p, slots,
                              window, sinks);
   if (e != cudaSuccess) return e;
