@@ -111,4 +111,58 @@ __device__ __forceinline__ void locate(int batch, const F& units, int64_t target
   first = shared[37];
 }
 
+// As locate, for both ends of a CTA's part in one pass: cut(total, x, y) names
+// them once the total is known. request and first describe the request that
+// holds unit x, request1 and first1 the one that holds y (the last one and its
+// end where there is none).
+template <int THREADS, class F, class Cut>
+__device__ __forceinline__ void locate_range(int batch, const F& units, int64_t* shared,
+                                             int64_t& total, const Cut& cut, int64_t& x, int64_t& y,
+                                             int& request, int64_t& first, int& request1,
+                                             int64_t& first1) {
+  const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
+  constexpr int kWarps = THREADS / kWarp;
+  const int per = (batch + THREADS - 1) / THREADS;
+  const int b0 = min(batch, static_cast<int>(threadIdx.x) * per), b1 = min(batch, b0 + per);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) mine += units(b);
+  int64_t inc = mine;
+#pragma unroll
+  for (int d = 1; d < kWarp; d *= 2) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += v;
+  }
+  if (lane == kWarp - 1) shared[warp] = inc;
+  if (threadIdx.x < 2) shared[36 + 2 * threadIdx.x] = batch;
+  __syncthreads();
+  int64_t at = inc - mine;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const int64_t s = shared[w];
+    at += w < warp ? s : 0;
+    total += s;
+  }
+  cut(total, x, y);
+  for (int i = 0; i < 2; ++i) {
+    const int64_t target = i ? y : x;
+    if (target < at || target >= at + mine) continue;
+    int64_t here = at;
+    for (int b = b0; b < b1; ++b) {
+      const int64_t n = per == 1 ? mine : units(b);
+      if (target < here + n) {
+        shared[36 + 2 * i] = b;
+        shared[37 + 2 * i] = here;
+        break;
+      }
+      here += n;
+    }
+  }
+  __syncthreads();
+  request = static_cast<int>(shared[36]);
+  first = shared[37];
+  request1 = static_cast<int>(shared[38]);
+  first1 = shared[39];
+}
+
 }  // namespace dlrm

@@ -14,18 +14,21 @@
 //
 // In a CTA, warp w takes block w of each chunk and keeps its own running
 // maximum, sum and output in registers; the warps are joined once per tile.
-// Per block, S = Q K^T and O += P V are m16n8k16 MMAs whose fragments come
-// straight from global memory, without shared memory: the MMA does not care
-// which element of the head (for S) or which event (for P V) an index of its
-// inner dimension stands for, as long as both operands agree, so a thread
-// takes 16 contiguous bytes of an event's key, and 4 to 16 of a value, and
-// converts them (e4m3 to f16 is exact) in place.
+// Every warp streams its blocks through a ring of its own in shared memory
+// (cp.async, kStages deep, no block-wide barrier), with the page numbers and
+// scales of 32 blocks ahead in one register of each lane. S = Q K^T and O += P V
+// are m16n8k16 MMAs. The MMA does not care which element of the head (for S) or
+// which event (for P V) an index of its inner dimension stands for, as long as
+// both operands agree, so a thread reads 16 contiguous bytes of an event's key,
+// and 4 to 16 of a value, and converts them (e4m3 to f16 is exact) in place.
 //   keys: thread (g, c) = (lane / 4, lane % 4) holds event g of an 8-event
 //     tile, elements 64 j + 16 c + 4 ks + e (j: 64-byte part, ks: k step);
 //   values: thread (g, c) holds events 2c, 2c+1, 2c+8, 2c+9 of a 16-event
 //     step, elements g D/8 .. (g+1) D/8 - 1; the bytes of a pair of events
 //     are interleaved, then converted. Output column 2c + i of n tile nt is
 //     element (2c + i) D/8 + nt.
+// 16-byte chunks are swizzled in shared memory so that these reads meet no bank
+// twice.
 // Scales: a block lies in one page, so the page's key scale multiplies S and
 // its value scale the block's P V, both in fp32 (one FMA per output, which
 // also applies the running maximum's correction).
@@ -47,11 +50,13 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * kWarp;
 constexpr int kBlock = 32;                       // events of a warp's step
+constexpr int kWhole = 4;                        // chunks of a tile that is never split
 
 struct Params {
   dlrm_history_t h;
   dlrm_attention_t a;
   int group;                                     // query heads of a kv head
+  int vec_q;                                     // four query elements can be loaded at once
   int32_t* counters;
   float* partials;
 };
@@ -93,29 +98,26 @@ __device__ __forceinline__ Span span_of(const Params& p, int b, bool report) {
   return s;
 }
 
-template <int N>
-struct Words {
-  uint32_t w[N];
-};
-
-// Loads N consecutive words.
-template <int N>
-__device__ __forceinline__ void load_words(uint32_t* w, const uint8_t* p) {
-  if (N % 4 == 0) {
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      const uint4 x = __ldg(reinterpret_cast<const uint4*>(p) + i);
-      w[4 * i] = x.x;
-      w[4 * i + 1] = x.y;
-      w[4 * i + 2] = x.z;
-      w[4 * i + 3] = x.w;
+// Four consecutive query elements.
+template <int DT>
+__device__ __forceinline__ void load_four(float (&x)[4], const void* q, int64_t at, int vec) {
+  if (vec) {
+    if (DT == DLRM_DTYPE_FP32) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(q) + at));
+      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    } else {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(q) + at));
+      if (DT == DLRM_DTYPE_BF16) {
+        x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xffff0000u);
+        x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xffff0000u);
+      } else {
+        const float2 a = f16x2_to_float2(v.x), b = f16x2_to_float2(v.y);
+        x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+      }
     }
-  } else if (N == 2) {
-    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
-    w[0] = x.x;
-    w[1] = x.y;
   } else {
-    w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = load_element<DT>(q, at + e);
   }
 }
 
@@ -196,23 +198,55 @@ __device__ __noinline__ void careful_row(const Params& p, const Span& s, int hea
   __syncthreads();
 }
 
+// Offset of 16-byte chunk `ch` of event t in a block of keys or values. Reads:
+// keys, 8 events x 64 bytes; values, 4 events (t / 2 = 0..3 mod 4) x a few chunks.
+template <int D>
+__device__ __forceinline__ int key_offset(int t, int ch) {
+  return D == 128 ? t * 128 + ((ch ^ ((t & 1) << 2)) << 4) : t * D + (ch << 4);
+}
+template <int D>
+__device__ __forceinline__ int value_offset(int t, int ch) {
+  if (D == 128) return t * 128 + ((ch ^ (((t >> 1) & 3) << 1)) << 4);
+  if (D == 64) return (t >> 1) * 128 + ((((t & 1) * 4 + ch) ^ (((t >> 1) & 3) << 1)) << 4);
+  return (t >> 2) * 128 + ((((t & 3) * 2 + ch) ^ (((t >> 2) & 1) << 1)) << 4);
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 template <int D, int DT>
-__global__ void __launch_bounds__(kThreads) history_attention_kernel(const Params p) {
-  constexpr bool kSplit = DT == DLRM_DTYPE_FP32;
-  constexpr int kRows = kSplit ? 8 : 16;
+struct Shape {
+  static constexpr bool kSplit = DT == DLRM_DTYPE_FP32;
+  static constexpr int kRows = kSplit ? 8 : 16;
+  static constexpr int kStages = D == 128 ? 3 : 4;
+  static constexpr int kBytes = 2 * kBlock * D;   // keys and values of a block
+  static constexpr int kStride = D + 2;           // a row's sums, maximum, sum of weights
+  static constexpr int kRing = kWarps * kStages * kBytes;
+  static constexpr int kJoin = kWarps * kRows * kStride * 4;
+  static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
+};
+
+template <int D, int DT>
+__global__ void __launch_bounds__(kThreads) history_attention_kernel(const __grid_constant__ Params p) {
+  using Sh = Shape<D, DT>;
+  constexpr bool kSplit = Sh::kSplit;
+  constexpr int kRows = Sh::kRows, kStages = Sh::kStages, kStride = Sh::kStride;
   constexpr int KW = D / 16;                      // key words of a thread and event tile
   constexpr int VW = D / 32;                      // value words of a thread and event
   constexpr int NT = D / 8;                       // n tiles of the output
-  constexpr int kStride = D + 2;                  // a row's sums, maximum, sum of weights
   constexpr int kAcc = kSplit ? 2 : 4;            // output values of a thread and n tile
+  extern __shared__ __align__(128) unsigned char smem[];
+  float (*joined)[kRows][kStride] = reinterpret_cast<float (*)[kRows][kStride]>(smem);
   __shared__ int64_t scan[40];
-  __shared__ float joined[kWarps][kRows][kStride];
   __shared__ float row_factor[kRows];
   __shared__ int odd[kRows + 1];
 
   const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
   const int g = lane / 4, c = lane % 4;
   const int G = p.h.page_tokens, H = p.h.n_heads;
+  unsigned char* ring = smem + warp * kStages * Sh::kBytes;
+  const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
   pdl_wait();
   pdl_trigger();
 
@@ -220,18 +254,33 @@ __global__ void __launch_bounds__(kThreads) history_attention_kernel(const Param
     const Span s = span_of<kRows>(p, b, false);
     return static_cast<int64_t>(s.tiles) * s.chunks * H;
   };
+  int64_t total, begin, end, at;
   int b;
-  int64_t at, total;
-  locate<kThreads>(p.a.batch, units, -1, scan, b, at, total);
-  const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);
+  int64_t ctas;
+  {
+    int b1;
+    int64_t at1;
+    const int64_t cta = blockIdx.x;
+    locate_range<kThreads>(p.a.batch, units, scan, total, [&](int64_t n, int64_t& x, int64_t& y) {
+      ctas = min(static_cast<int64_t>(gridDim.x), n);
+      x = min(cta, ctas) * n / max(ctas, int64_t(1));
+      y = min(cta + 1, ctas) * n / max(ctas, int64_t(1));
+    }, begin, end, b, at, b1, at1);
+    // a cut inside a short tile moves to the tile's start: finishing it in one
+    // CTA is faster than joining parts
+    auto snap = [&](int64_t x, int of, int64_t first) {
+      if (x <= 0 || x >= total) return x;
+      const Span s = span_of<kRows>(p, of, false);
+      return s.chunks <= kWhole ? first + (x - first) / s.chunks * s.chunks : x;
+    };
+    end = snap(end, b1, at1);
+    begin = snap(begin, b, at);
+  }
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < p.a.batch; i += kThreads) span_of<kRows>(p, i, true);
-  if (blockIdx.x >= ctas) return;
-  const int64_t begin = blockIdx.x * total / ctas, end = (blockIdx.x + 1) * total / ctas;
-  locate<kThreads>(p.a.batch, units, begin, scan, b, at, total);
 
   for (int64_t u = begin; u < end;) {
-    Span s = span_of<kRows>(p, b, false);
+    const Span s = span_of<kRows>(p, b, false);
     const int64_t units_b = static_cast<int64_t>(s.tiles) * s.chunks * H;
     if (u >= at + units_b) {
       at += units_b;
@@ -245,6 +294,68 @@ __global__ void __launch_bounds__(kThreads) history_attention_kernel(const Param
     const int chunk1 = static_cast<int>(min(end, seg1) - seg0);
     const int rows = min(kRows, s.rows - tile * kRows);
     u = seg0 + chunk1;
+
+    // ---- blocks of this warp: n0, n0 + kWarps, ...; lane l knows block l of
+    // the 32 at hand (info) and of the 32 after them (ahead)
+    const int pos0 = p.a.causal ? s.len - s.rows / p.group : s.len - 1;
+    const int i_first = tile * kRows / p.group, i_last = (tile * kRows + rows - 1) / p.group;
+    const Visible v_first = visible(pos0 + (p.a.causal ? i_first : 0), s.len, p.a.window, p.a.sinks);
+    const Visible v_last = visible(pos0 + (p.a.causal ? i_last : 0), s.len, p.a.window, p.a.sinks);
+    const int n0 = chunk0 * kWarps + warp, n1 = min(chunk1 * kWarps, s.blocks);
+    const int count = n0 < n1 ? (n1 - n0 + kWarps - 1) / kWarps : 0;
+    auto first_event = [&](int i) {
+      const int n = n0 + i * kWarps;
+      return (n < s.sink_blocks ? n : n - s.sink_blocks + s.block0) * kBlock;
+    };
+    struct Info {
+      int page;                                   // -1: nothing to read
+      float ks, vs;
+    };
+    const int32_t* pages = p.h.table + static_cast<int64_t>(s.slot) * p.h.max_pages;
+    auto look = [&](int i) {
+      Info x{-1, 0.f, 0.f};
+      if (i < count) {
+        const int t0 = first_event(i);
+        // not what no row of the tile sees
+        if (t0 < v_last.end && !(t0 >= v_last.gap0 && t0 + kBlock <= v_first.gap1)) {
+          x.page = pages[t0 / G];
+          if (x.page < 0 || x.page >= p.h.n_pages) {
+            // trimmed, or a broken table: events that some row needs
+            x.page = -1;
+            flag(p.h.err, DLRM_ERRBIT_INDEX_OOB);
+          } else {
+            const int64_t place = static_cast<int64_t>(x.page) * H + head;
+            x.ks = p.h.k_scales[place];
+            x.vs = p.h.v_scales[place];
+          }
+        }
+      }
+      return x;
+    };
+    Info info = look(lane), ahead = look(kWarp + lane);
+    int base = 0;                                 // blocks [base, base + 32) are in info
+    auto fetch = [&](int i) {
+      if (i < count) {
+        const int page = __shfl_sync(0xffffffffu, i - base < kWarp ? info.page : ahead.page, i % kWarp);
+        if (page >= 0) {
+          const int64_t codes = ((static_cast<int64_t>(page) * H + head) * G + first_event(i) % G) * D;
+          const uint32_t dst = ring_at + (i % kStages) * Sh::kBytes;
+#pragma unroll
+          for (int x = 0; x < 2 * D / 32; ++x) {
+            const int id = x * kWarp + lane, t = id / (D / 16), ch = id % (D / 16);
+            copy16(dst + key_offset<D>(t, ch), p.h.k_codes + codes + id * 16);
+          }
+#pragma unroll
+          for (int x = 0; x < 2 * D / 32; ++x) {
+            const int id = x * kWarp + lane, t = id / (D / 16), ch = id % (D / 16);
+            copy16(dst + kBlock * D + value_offset<D>(t, ch), p.h.v_codes + codes + id * 16);
+          }
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch(i);
 
     // ---- queries: fragments of the tile, scaled to f16
     uint32_t qa[KW][4];
@@ -261,15 +372,19 @@ __global__ void __launch_bounds__(kThreads) history_attention_kernel(const Param
         const int i = row / p.group;
         const bool in = r == g + 8 * r2;
         const int64_t q_at = (s.q0 + static_cast<int64_t>(i)) * p.a.ld_q +
-                             (head * p.group + row % p.group) * p.a.ld_q_head;
+                             (head * p.group + row - i * p.group) * p.a.ld_q_head;
         float big = 0.f;
 #pragma unroll
-        for (int w = 0; w < KW; ++w)
+        for (int w = 0; w < KW; ++w) {
+          if (in) {
+            load_four<DT>(x[r2][w], p.a.q, q_at + key_element<D>(c, w), p.vec_q);
+          } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x[r2][w][e] = in ? load_element<DT>(p.a.q, q_at + key_element<D>(c, w) + e) : 0.f;
-            big = fmaxf(big, fabsf(x[r2][w][e]));
+            for (int e = 0; e < 4; ++e) x[r2][w][e] = 0.f;
           }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) big = fmaxf(big, fabsf(x[r2][w][e]));
+        }
         big = quad_max(big);
         const int ex = max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -100);
         const float f = pow2f(min(8 - ex, 127));
@@ -278,8 +393,7 @@ __global__ void __launch_bounds__(kThreads) history_attention_kernel(const Param
         for (int w = 0; w < KW; ++w)
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[r2][w][e] *= f;
-        vis[r2] = visible(p.a.causal ? s.len - s.rows / p.group + i : s.len - 1, s.len, p.a.window,
-                          p.a.sinks);
+        vis[r2] = visible(pos0 + (p.a.causal ? i : 0), s.len, p.a.window, p.a.sinks);
       }
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
@@ -307,52 +421,49 @@ __global__ void __launch_bounds__(kThreads) history_attention_kernel(const Param
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < kAcc; ++i) o[nt][i] = 0.f;
-    const int32_t* pages = p.h.table + static_cast<int64_t>(s.slot) * p.h.max_pages;
-    const int n0 = chunk0 * kWarps + warp, n1 = min(chunk1 * kWarps, s.blocks);
-    for (int n = n0; n < n1; n += kWarps) {
-      const int t0 = (n < s.sink_blocks ? n : n - s.sink_blocks + s.block0) * kBlock;
-      const int page = pages[t0 / G];
-      if (page < 0 || page >= p.h.n_pages) {
-        // trimmed, or a broken table: no row may need these events
-        bool need = false;
-        for (int t = t0; t < min(t0 + kBlock, s.len); ++t) need |= sees(vis[0], t) | sees(vis[1], t);
-        if (need) flag(p.h.err, DLRM_ERRBIT_INDEX_OOB);
-        continue;
+    for (int it = 0; it < count; ++it) {
+      if (it - base == kWarp) {
+        base += kWarp;
+        info = ahead;
+        ahead = look(base + kWarp + lane);
       }
-      const int64_t place = static_cast<int64_t>(page) * H + head;
-      const int64_t codes = (place * G + t0 % G) * D;
-      uint32_t kw[kBlock / 8][KW], vw[kBlock / 16][4][VW];
-#pragma unroll
-      for (int j = 0; j < kBlock / 8; ++j) {
-        const uint8_t* kp = p.h.k_codes + codes + (8 * j + g) * D;
-        if (D == 32) {
-          load_words<2>(kw[j], kp + 8 * c);
-        } else {
-#pragma unroll
-          for (int i = 0; i < KW / 4; ++i) load_words<4>(&kw[j][4 * i], kp + 64 * i + 16 * c);
-        }
-      }
-#pragma unroll
-      for (int kt = 0; kt < kBlock / 16; ++kt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = 16 * kt + 2 * c + (i & 1) + 8 * (i >> 1);
-          load_words<VW>(vw[kt][i], p.h.v_codes + codes + t * D + g * (D / 8));
-        }
-      const float ks = p.h.k_scales[place], vs = p.h.v_scales[place];
+      fetch(it + kStages - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      __syncwarp();
+      const int page = __shfl_sync(0xffffffffu, info.page, it % kWarp);
+      if (page < 0) continue;
+      const float ks = __shfl_sync(0xffffffffu, info.ks, it % kWarp);
+      const float vs = __shfl_sync(0xffffffffu, info.vs, it % kWarp);
+      const int t0 = first_event(it);
+      const unsigned char* kb = ring + (it % kStages) * Sh::kBytes;
+      const unsigned char* vb = kb + kBlock * D;
 
       // S = Q K^T
       float sc[kBlock / 8][4];
 #pragma unroll
       for (int j = 0; j < kBlock / 8; ++j) {
+        uint32_t kw[KW];
+        if (D == 32) {
+          const uint2 x = *reinterpret_cast<const uint2*>(kb + (8 * j + g) * 32 + 8 * c);
+          kw[0] = x.x;
+          kw[1] = x.y;
+        } else {
+#pragma unroll
+          for (int i = 0; i < KW / 4; ++i) {
+            const uint4 x = *reinterpret_cast<const uint4*>(kb + key_offset<D>(8 * j + g, 4 * i + c));
+            kw[4 * i] = x.x;
+            kw[4 * i + 1] = x.y;
+            kw[4 * i + 2] = x.z;
+            kw[4 * i + 3] = x.w;
+          }
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) sc[j][i] = 0.f;
 #pragma unroll
         for (int w = 0; w < KW; ++w)
-          mma_f16(sc[j], qa[w], e4m3x2_lo_to_f16x2(kw[j][w]), e4m3x2_hi_to_f16x2(kw[j][w]));
+          mma_f16(sc[j], qa[w], e4m3x2_lo_to_f16x2(kw[w]), e4m3x2_hi_to_f16x2(kw[w]));
       }
-      // masked log2 weights; values of events past the end are cleared, as
-      // their codes are whatever an earlier history left there
+      // masked log2 weights
       const float f0 = qf[0] * ks, f1 = qf[1] * ks;
       const bool whole = t0 + kBlock <= min(vis[0].end, vis[1].end) &&
                          (t0 >= vis[0].gap1 || t0 + kBlock <= vis[0].gap0) &&
@@ -381,28 +492,19 @@ __global__ void __launch_bounds__(kThreads) history_attention_kernel(const Param
         big[0] = fmaxf(big[0], fmaxf(sc[j][0], sc[j][1]));
         if (!kSplit) big[1] = fmaxf(big[1], fmaxf(sc[j][2], sc[j][3]));
       }
-      if (t0 + kBlock > s.len) {
-#pragma unroll
-        for (int kt = 0; kt < kBlock / 16; ++kt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (t0 + 16 * kt + 2 * c + (i & 1) + 8 * (i >> 1) >= s.len)
-#pragma unroll
-              for (int w = 0; w < VW; ++w) vw[kt][i][w] = 0;
-      }
       // running maximum and sum
       float alpha[2] = {1.f, 1.f};
 #pragma unroll
       for (int r = 0; r < (kSplit ? 1 : 2); ++r) {
         const float m = fmaxf(top[r], quad_max(big[r]));
-        const float base = m == -INFINITY ? 0.f : m;
-        alpha[r] = exp2_approx(top[r] - base);
+        const float off = m == -INFINITY ? 0.f : m;
+        alpha[r] = exp2_approx(top[r] - off);
         top[r] = m;
         float add = 0.f;
 #pragma unroll
         for (int j = 0; j < kBlock / 8; ++j) {
-          sc[j][2 * r] = exp2_approx(sc[j][2 * r] - base);
-          sc[j][2 * r + 1] = exp2_approx(sc[j][2 * r + 1] - base);
+          sc[j][2 * r] = exp2_approx(sc[j][2 * r] - off);
+          sc[j][2 * r + 1] = exp2_approx(sc[j][2 * r + 1] - off);
           add += sc[j][2 * r] + sc[j][2 * r + 1];
         }
         sum[r] = fmaf(sum[r], alpha[r], add);
@@ -423,6 +525,30 @@ __global__ void __launch_bounds__(kThreads) history_attention_kernel(const Param
           pa[kt][3] = pack_f16x2(sc[2 * kt + 1][2], sc[2 * kt + 1][3]);
         }
       }
+      uint32_t vw[kBlock / 16][4][VW];
+#pragma unroll
+      for (int kt = 0; kt < kBlock / 16; ++kt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = 16 * kt + 2 * c + (i & 1) + 8 * (i >> 1);
+          if (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(vb + value_offset<D>(t, g));
+            vw[kt][i][0] = x.x;
+            vw[kt][i][VW > 1 ? 1 : 0] = x.y;
+            vw[kt][i][VW > 2 ? 2 : 0] = x.z;
+            vw[kt][i][VW > 3 ? 3 : 0] = x.w;
+          } else if (D == 64) {
+            const uint2 x = *reinterpret_cast<const uint2*>(vb + value_offset<D>(t, g >> 1) + 8 * (g & 1));
+            vw[kt][i][0] = x.x;
+            vw[kt][i][VW > 1 ? 1 : 0] = x.y;
+          } else {
+            vw[kt][i][0] = *reinterpret_cast<const uint32_t*>(vb + value_offset<D>(t, g >> 2) + 4 * (g & 3));
+          }
+          // codes of events past the end are whatever an earlier history left there
+          if (t0 + t >= s.len)
+#pragma unroll
+            for (int w = 0; w < VW; ++w) vw[kt][i][w] = 0;
+        }
 #pragma unroll
       for (int w = 0; w < VW; ++w) {
         float acc[4][4];
@@ -456,10 +582,12 @@ __global__ void __launch_bounds__(kThreads) history_attention_kernel(const Param
           }
         }
       }
+      __syncwarp();                               // the stage is read: it may be filled again
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 
     // ---- join the warps
-    __syncthreads();                              // `joined` of the tile before is read
+    __syncthreads();                              // every warp's ring is done with: `joined` lies there
 #pragma unroll
     for (int r = 0; r < (kSplit ? 1 : 2); ++r) {
       const float l = quad_sum(sum[r]);
@@ -507,7 +635,8 @@ __global__ void __launch_bounds__(kThreads) history_attention_kernel(const Param
         mine[threadIdx.x * kStride + D] = row_factor[threadIdx.x];
         mine[threadIdx.x * kStride + D + 1] = joined[0][threadIdx.x][D + 1];
       }
-      // the CTAs that share this tile: first .. last, one part each
+      // the CTAs that share this tile: first .. last, one part each. (A cut moves
+      // out of short tiles only, so a split tile's cuts are where they were.)
       const int64_t first = ((seg0 + 1) * ctas - 1) / total, last = (seg1 * ctas - 1) / total;
       const int parts = static_cast<int>(last - first) + 1;
       __threadfence();
@@ -518,7 +647,7 @@ __global__ void __launch_bounds__(kThreads) history_attention_kernel(const Param
         if (before == parts - 1) p.counters[first] = 0;
       }
       __syncthreads();
-      if (!odd[kRows]) continue;
+      if (!odd[kRows]) continue;                  // (`joined` was read before the barrier)
       __threadfence();
       auto part = [&](int i) {
         return p.partials + ((first + i) * 2 + (i > 0 ? 0 : 1)) * kAttnPartial;
@@ -566,17 +695,22 @@ __global__ void __launch_bounds__(kThreads) history_attention_kernel(const Param
       for (int r = 0; r < rows; ++r)
         if (odd[r]) careful_row<DT>(p, s, head, tile * kRows + r, &joined[0][0][0]);
     }
+    __syncthreads();                              // `joined` is read: the rings may be filled
   }
 }
 
 template <int D, int DT>
 cudaError_t launch(const Params& p, cudaStream_t stream) {
-  constexpr int kRows = DT == DLRM_DTYPE_FP32 ? 8 : 16;
+  using Sh = Shape<D, DT>;
+  constexpr int kRows = Sh::kRows;
   static std::atomic<int> resident{0};            // CTAs of an SM: the same for every GB300
   int per_sm = resident.load(std::memory_order_relaxed);
   if (per_sm == 0) {
-    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-        &per_sm, history_attention_kernel<D, DT>, kThreads, 0);
+    cudaError_t e = cudaFuncSetAttribute(history_attention_kernel<D, DT>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+    if (e != cudaSuccess) return e;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, history_attention_kernel<D, DT>,
+                                                      kThreads, Sh::kSmem);
     if (e != cudaSuccess) return e;
     per_sm = std::max(1, std::min(per_sm, kAttnMaxCtas / 152));
     resident.store(per_sm, std::memory_order_relaxed);
@@ -589,7 +723,7 @@ cudaError_t launch(const Params& p, cudaStream_t stream) {
   const int64_t grid = std::min<int64_t>(
       {chunks, static_cast<int64_t>(device_sm_count()) * per_sm, int64_t(kAttnMaxCtas)});
   return launch_pdl(history_attention_kernel<D, DT>, dim3(static_cast<unsigned>(grid)),
-                    dim3(kThreads), 0, stream, p);
+                    dim3(kThreads), Sh::kSmem, stream, p);
 }
 
 template <int D>
@@ -608,6 +742,8 @@ cudaError_t launch_history_attention(const dlrm_history_t& h, const dlrm_attenti
   p.h = h;
   p.a = a;
   p.group = a.n_heads / h.n_heads;
+  const int64_t four = 4 * dtype_bytes(a.dtype);
+  p.vec_q = reinterpret_cast<uintptr_t>(a.q) % four == 0 && a.ld_q % 4 == 0 && a.ld_q_head % 4 == 0;
   p.counters = work_part<int32_t>(h, w.counters);
   p.partials = work_part<float>(h, w.partials);
   if (h.head_dim == 32) return launch_d<32>(p, stream);

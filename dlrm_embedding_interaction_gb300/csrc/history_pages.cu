@@ -582,8 +582,11 @@ __global__ void __launch_bounds__(kFreeThreads) push_kernel(Pool p, int batch, i
 }
 
 // release, count and push in one CTA, with barriers for launches: a warp a
-// request. For calls of few pages three launches take longer than the work.
-constexpr int kFreeSmallBatch = 256, kFreeSmallEntries = 16384;
+// request. For calls of few pages three launches take longer than the work: 32
+// slots of up to 17 pages 7 us against 13; 16 of up to 64 pages 11 against 13 when
+// each launch is timed alone, and no faster when they overlap; 128 of up to 64 24
+// against 15.
+constexpr int kFreeSmallBatch = 256, kFreeSmallEntries = 768;
 
 __global__ void __launch_bounds__(kPlanThreads) free_small_kernel(Pool p, const int32_t* slots,
                                                                   int batch, int window, int sinks) {
