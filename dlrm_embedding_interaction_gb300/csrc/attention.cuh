@@ -17,6 +17,18 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The same, c = A B (+ c with `add`, a constant).
+__device__ __forceinline__ void mma_f16_from(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                             uint32_t b1, bool add) {
+  if (add) {
+    mma_f16(c, a, b0, b1);
+    return;
+  }
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
@@ -111,58 +123,81 @@ __device__ __forceinline__ void locate(int batch, const F& units, int64_t target
   first = shared[37];
 }
 
-// As locate, for both ends of a CTA's part in one pass: cut(total, x, y) names
-// them once the total is known. request and first describe the request that
-// holds unit x, request1 and first1 the one that holds y (the last one and its
-// end where there is none).
-template <int THREADS, class F, class Cut>
-__device__ __forceinline__ void locate_range(int batch, const F& units, int64_t* shared,
-                                             int64_t& total, const Cut& cut, int64_t& x, int64_t& y,
-                                             int& request, int64_t& first, int& request1,
-                                             int64_t& first1) {
+// Cuts a batch's units evenly over the CTAs: request b has units(span(b)) >= 0
+// of them, fewer than 2^31 in all. CTA c of min(gridDim.x, total) takes
+// [cut(c), cut(c + 1)). Block-wide; the spans and first units of the requests
+// that hold both cuts come back in shared memory (the last request's where the
+// cut is the total).
+struct Cuts {
+  int total, ctas, each, extra;                  // the first `extra` CTAs take each + 1
+  __device__ __forceinline__ void set(int n) {
+    total = n;
+    ctas = min(static_cast<int>(gridDim.x), n);
+    each = ctas > 0 ? n / ctas : 0;
+    extra = n - each * ctas;
+  }
+  __device__ __forceinline__ int cut(int c) const {
+    c = min(c, ctas);
+    return c * each + min(c, extra);
+  }
+  __device__ __forceinline__ int owner(int unit) const {
+    const int long_ones = extra * (each + 1);
+    return unit < long_ones ? unit / (each + 1) : extra + (unit - long_ones) / each;
+  }
+};
+template <class Span>
+struct Found {
+  int request[2], first[2];
+  Span span[2];
+};
+template <int THREADS, class Span, class S, class U>
+__device__ __forceinline__ Cuts locate_cuts(int batch, const S& span, const U& units, int* sums,
+                                            Found<Span>& found) {
   const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
   constexpr int kWarps = THREADS / kWarp;
   const int per = (batch + THREADS - 1) / THREADS;
   const int b0 = min(batch, static_cast<int>(threadIdx.x) * per), b1 = min(batch, b0 + per);
-  int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += units(b);
-  int64_t inc = mine;
+  int mine = 0;
+  Span s{};
+  for (int b = b0; b < b1; ++b) {
+    s = span(b);
+    mine += units(s);
+  }
+  int inc = mine;
 #pragma unroll
   for (int d = 1; d < kWarp; d *= 2) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, inc, d);
+    const int v = __shfl_up_sync(0xffffffffu, inc, d);
     if (lane >= d) inc += v;
   }
-  if (lane == kWarp - 1) shared[warp] = inc;
-  if (threadIdx.x < 2) shared[36 + 2 * threadIdx.x] = batch;
+  if (lane == kWarp - 1) sums[warp] = inc;
   __syncthreads();
-  int64_t at = inc - mine;
-  total = 0;
+  int at = inc - mine, total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    const int64_t s = shared[w];
-    at += w < warp ? s : 0;
-    total += s;
+    const int x = sums[w];
+    at += w < warp ? x : 0;
+    total += x;
   }
-  cut(total, x, y);
+  Cuts cuts;
+  cuts.set(total);
   for (int i = 0; i < 2; ++i) {
-    const int64_t target = i ? y : x;
+    const int target = min(cuts.cut(blockIdx.x + i), total - 1);
     if (target < at || target >= at + mine) continue;
-    int64_t here = at;
+    int here = at;
     for (int b = b0; b < b1; ++b) {
-      const int64_t n = per == 1 ? mine : units(b);
+      if (per > 1) s = span(b);
+      const int n = units(s);
       if (target < here + n) {
-        shared[36 + 2 * i] = b;
-        shared[37 + 2 * i] = here;
+        found.request[i] = b;
+        found.first[i] = here;
+        found.span[i] = s;
         break;
       }
       here += n;
     }
   }
   __syncthreads();
-  request = static_cast<int>(shared[36]);
-  first = shared[37];
-  request1 = static_cast<int>(shared[38]);
-  first1 = shared[39];
+  return cuts;
 }
 
 }  // namespace dlrm

@@ -158,6 +158,10 @@ dlrm_status_t history_attention(const dlrm_history_t* h, const dlrm_attention_t*
   s = check_attention(a, h->n_heads, &run);
   if (s != DLRM_OK || !run) return s;
   if (!a->slots || !aligned_to(a->slots, 4)) return DLRM_ERR_INVALID_ARG;
+  // work units (8 rows of a kv head, 128 events) are counted in int32
+  const int64_t tiles = a->q_rows * (a->n_heads / h->n_heads) / 8 + a->batch;
+  const int64_t events = static_cast<int64_t>(h->max_pages) * h->page_tokens;
+  if (tiles * h->n_heads >= (int64_t(1) << 31) / (events / 128 + 2)) return DLRM_ERR_UNSUPPORTED;
   return status_of(dlrm::launch_history_attention(*h, *a, static_cast<cudaStream_t>(stream)));
 }
 

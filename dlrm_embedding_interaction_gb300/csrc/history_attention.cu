@@ -63,7 +63,7 @@ struct Params {
 
 // What a CTA needs to know of a request.
 struct Span {
-  int slot, rows, len, q0, tiles;                // rows: queries * group
+  int slot, queries, rows, len, q0, tiles;       // rows: queries * group
   int sink_blocks, block0, blocks, chunks;       // blocks of events: the sinks', then from block0 on
 };
 
@@ -76,7 +76,8 @@ __device__ __forceinline__ Span span_of(const Params& p, int b, bool report) {
   s.rows = 0;
   s.len = 0;
   const bool bad = q0 < 0 || q1 < q0 || q1 > p.a.q_rows;
-  if (!bad) s.rows = (q1 - q0) * p.group;
+  s.queries = bad ? 0 : q1 - q0;
+  s.rows = s.queries * p.group;
   if (s.slot >= 0 && s.slot < p.h.n_slots) {
     const int64_t cap = static_cast<int64_t>(p.h.max_pages) * p.h.page_tokens;
     s.len = static_cast<int>(min(static_cast<int64_t>(max(p.h.lengths[s.slot], 0)), cap));
@@ -136,7 +137,7 @@ __device__ __noinline__ void careful_row(const Params& p, const Span& s, int hea
                                          float* sm) {
   const int G = p.h.page_tokens, D = p.h.head_dim, M = p.h.max_pages, H = p.h.n_heads;
   const int i = row / p.group, hq = head * p.group + row % p.group;
-  const Visible v = visible(p.a.causal ? s.len - s.rows / p.group + i : s.len - 1, s.len,
+  const Visible v = visible(p.a.causal ? s.len - s.queries + i : s.len - 1, s.len,
                             p.a.window, p.a.sinks);
   const int64_t q_at = (s.q0 + static_cast<int64_t>(i)) * p.a.ld_q + hq * p.a.ld_q_head;
   const int32_t* row_pages = p.h.table + static_cast<int64_t>(s.slot) * M;
@@ -238,7 +239,8 @@ __global__ void __launch_bounds__(kThreads) history_attention_kernel(const __gri
   constexpr int kAcc = kSplit ? 2 : 4;            // output values of a thread and n tile
   extern __shared__ __align__(128) unsigned char smem[];
   float (*joined)[kRows][kStride] = reinterpret_cast<float (*)[kRows][kStride]>(smem);
-  __shared__ int64_t scan[40];
+  __shared__ int sums[kWarps];
+  __shared__ Found<Span> found;
   __shared__ float row_factor[kRows];
   __shared__ int odd[kRows + 1];
 
@@ -250,55 +252,69 @@ __global__ void __launch_bounds__(kThreads) history_attention_kernel(const __gri
   pdl_wait();
   pdl_trigger();
 
-  auto units = [&](int b) {
-    const Span s = span_of<kRows>(p, b, false);
-    return static_cast<int64_t>(s.tiles) * s.chunks * H;
+  auto units = [&](const Span& s) { return s.tiles * s.chunks * H; };
+  const Cuts cuts = locate_cuts<kThreads>(
+      p.a.batch, [&](int i) { return span_of<kRows>(p, i, false); }, units, sums, found);
+  // a cut inside a short tile moves to the tile's start: finishing it in one
+  // CTA is faster than joining parts
+  auto snap = [&](int x, int i) {
+    const int chunks = found.span[i].chunks;
+    if (x >= cuts.total || chunks > kWhole) return x;
+    const unsigned off = x - found.first[i];
+    return static_cast<int>(x - off % static_cast<unsigned>(chunks));
   };
-  int64_t total, begin, end, at;
-  int b;
-  int64_t ctas;
-  {
-    int b1;
-    int64_t at1;
-    const int64_t cta = blockIdx.x;
-    locate_range<kThreads>(p.a.batch, units, scan, total, [&](int64_t n, int64_t& x, int64_t& y) {
-      ctas = min(static_cast<int64_t>(gridDim.x), n);
-      x = min(cta, ctas) * n / max(ctas, int64_t(1));
-      y = min(cta + 1, ctas) * n / max(ctas, int64_t(1));
-    }, begin, end, b, at, b1, at1);
-    // a cut inside a short tile moves to the tile's start: finishing it in one
-    // CTA is faster than joining parts
-    auto snap = [&](int64_t x, int of, int64_t first) {
-      if (x <= 0 || x >= total) return x;
-      const Span s = span_of<kRows>(p, of, false);
-      return s.chunks <= kWhole ? first + (x - first) / s.chunks * s.chunks : x;
-    };
-    end = snap(end, b1, at1);
-    begin = snap(begin, b, at);
-  }
+  const int begin = cuts.total ? snap(cuts.cut(blockIdx.x), 0) : 0;
+  const int end = cuts.total ? snap(cuts.cut(blockIdx.x + 1), 1) : 0;
+  int b = found.request[0], at = found.first[0];
+  Span s = found.span[0];
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < p.a.batch; i += kThreads) span_of<kRows>(p, i, true);
 
-  for (int64_t u = begin; u < end;) {
-    const Span s = span_of<kRows>(p, b, false);
-    const int64_t units_b = static_cast<int64_t>(s.tiles) * s.chunks * H;
-    if (u >= at + units_b) {
-      at += units_b;
-      ++b;
+  for (int u = begin; u < end;) {
+    if (u >= at + units(s)) {
+      at += units(s);
+      s = span_of<kRows>(p, ++b, false);
       continue;
     }
-    const int64_t seg = (u - at) / s.chunks;      // (head, tile) of the request
-    const int head = static_cast<int>(seg / s.tiles), tile = static_cast<int>(seg % s.tiles);
-    const int64_t seg0 = at + seg * s.chunks, seg1 = seg0 + s.chunks;
-    const int chunk0 = static_cast<int>(u - seg0);
-    const int chunk1 = static_cast<int>(min(end, seg1) - seg0);
+    const int seg = static_cast<unsigned>(u - at) / static_cast<unsigned>(s.chunks);   // (head, tile)
+    const int head = s.tiles == 1 ? seg : static_cast<unsigned>(seg) / static_cast<unsigned>(s.tiles);
+    const int tile = seg - head * s.tiles;
+    const int seg0 = at + seg * s.chunks, seg1 = seg0 + s.chunks;
+    const int chunk0 = u - seg0, chunk1 = min(end, seg1) - seg0;
     const int rows = min(kRows, s.rows - tile * kRows);
     u = seg0 + chunk1;
 
+    // ---- queries: the loads first, the arithmetic while the events are on their way
+    float x[2][KW][4];
+    int query[2];                                 // of the thread's rows
+#pragma unroll
+    for (int r2 = 0; r2 < 2; ++r2) {
+      // rows past the last stand for it (their queries are zero), so that
+      // they do not make blocks of events partly visible
+      const int r = min(kSplit ? g : g + 8 * r2, rows - 1);
+      const int row = tile * kRows + r;
+      query[r2] = p.group == 1 ? row : static_cast<unsigned>(row) / static_cast<unsigned>(p.group);
+      const bool in = r == g + 8 * r2;
+      const int64_t q_at = (s.q0 + static_cast<int64_t>(query[r2])) * p.a.ld_q +
+                           (head * p.group + row - query[r2] * p.group) * p.a.ld_q_head;
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        if (in) {
+          load_four<DT>(x[r2][w], p.a.q, q_at + key_element<D>(c, w), p.vec_q);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[r2][w][e] = 0.f;
+        }
+      }
+    }
+
     // ---- blocks of this warp: n0, n0 + kWarps, ...; lane l knows block l of
     // the 32 at hand (info) and of the 32 after them (ahead)
-    const int pos0 = p.a.causal ? s.len - s.rows / p.group : s.len - 1;
-    const int i_first = tile * kRows / p.group, i_last = (tile * kRows + rows - 1) / p.group;
+    const int pos0 = p.a.causal ? s.len - s.queries : s.len - 1;
+    const unsigned group = p.group;
+    const int i_first = p.group == 1 ? tile * kRows : static_cast<unsigned>(tile * kRows) / group;
+    const int i_last = p.group == 1 ? tile * kRows + rows - 1
+                                    : static_cast<unsigned>(tile * kRows + rows - 1) / group;
     const Visible v_first = visible(pos0 + (p.a.causal ? i_first : 0), s.len, p.a.window, p.a.sinks);
     const Visible v_last = visible(pos0 + (p.a.causal ? i_last : 0), s.len, p.a.window, p.a.sinks);
     const int n0 = chunk0 * kWarps + warp, n1 = min(chunk1 * kWarps, s.blocks);
@@ -357,43 +373,28 @@ __global__ void __launch_bounds__(kThreads) history_attention_kernel(const __gri
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) fetch(i);
 
-    // ---- queries: fragments of the tile, scaled to f16
+    // ---- fragments of the queries, scaled to f16; a negative softmax scale is
+    // theirs, so that the factors of the scores are positive
     uint32_t qa[KW][4];
     float qf[2];
     Visible vis[2];
     {
-      float x[2][KW][4];
 #pragma unroll
       for (int r2 = 0; r2 < 2; ++r2) {
-        // rows past the last stand for it (their queries are zero), so that
-        // they do not make blocks of events partly visible
-        const int r = min(kSplit ? g : g + 8 * r2, rows - 1);
-        const int row = tile * kRows + r;
-        const int i = row / p.group;
-        const bool in = r == g + 8 * r2;
-        const int64_t q_at = (s.q0 + static_cast<int64_t>(i)) * p.a.ld_q +
-                             (head * p.group + row - i * p.group) * p.a.ld_q_head;
         float big = 0.f;
 #pragma unroll
-        for (int w = 0; w < KW; ++w) {
-          if (in) {
-            load_four<DT>(x[r2][w], p.a.q, q_at + key_element<D>(c, w), p.vec_q);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[r2][w][e] = 0.f;
-          }
+        for (int w = 0; w < KW; ++w)
 #pragma unroll
           for (int e = 0; e < 4; ++e) big = fmaxf(big, fabsf(x[r2][w][e]));
-        }
         big = quad_max(big);
         const int ex = max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -100);
-        const float f = pow2f(min(8 - ex, 127));
-        qf[r2] = pow2f(max(ex - 8, -126)) * p.a.scale * kLog2e;
+        const float f = copysignf(pow2f(min(8 - ex, 127)), p.a.scale);
+        qf[r2] = pow2f(max(ex - 8, -126)) * fabsf(p.a.scale) * kLog2e;
 #pragma unroll
         for (int w = 0; w < KW; ++w)
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[r2][w][e] *= f;
-        vis[r2] = visible(pos0 + (p.a.causal ? i : 0), s.len, p.a.window, p.a.sinks);
+        vis[r2] = visible(pos0 + (p.a.causal ? query[r2] : 0), s.len, p.a.window, p.a.sinks);
       }
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
@@ -458,29 +459,25 @@ __global__ void __launch_bounds__(kThreads) history_attention_kernel(const __gri
           }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sc[j][i] = 0.f;
-#pragma unroll
         for (int w = 0; w < KW; ++w)
-          mma_f16(sc[j], qa[w], e4m3x2_lo_to_f16x2(kw[w]), e4m3x2_hi_to_f16x2(kw[w]));
+          mma_f16_from(sc[j], qa[w], e4m3x2_lo_to_f16x2(kw[w]), e4m3x2_hi_to_f16x2(kw[w]), w > 0);
       }
-      // masked log2 weights
-      const float f0 = qf[0] * ks, f1 = qf[1] * ks;
+      // weights: exp2 of the scores times f0, f1, less the running maximum
+      // (not zero, even for a softmax scale of zero: a masked score is -infinity)
+      const float f0 = fmaxf(qf[0] * ks, 1e-37f), f1 = fmaxf(qf[1] * ks, 1e-37f);
       const bool whole = t0 + kBlock <= min(vis[0].end, vis[1].end) &&
                          (t0 >= vis[0].gap1 || t0 + kBlock <= vis[0].gap0) &&
                          (t0 >= vis[1].gap1 || t0 + kBlock <= vis[1].gap0);
-      float big[2] = {-INFINITY, -INFINITY};
+      if (kSplit) {
 #pragma unroll
-      for (int j = 0; j < kBlock / 8; ++j) {
-        if (kSplit) {
-          sc[j][0] = fmaf(sc[j][2], 1.f / 2048.f, sc[j][0]) * f0;
-          sc[j][1] = fmaf(sc[j][3], 1.f / 2048.f, sc[j][1]) * f0;
-        } else {
-          sc[j][0] *= f0;
-          sc[j][1] *= f0;
-          sc[j][2] *= f1;
-          sc[j][3] *= f1;
+        for (int j = 0; j < kBlock / 8; ++j) {
+          sc[j][0] = fmaf(sc[j][2], 1.f / 2048.f, sc[j][0]);
+          sc[j][1] = fmaf(sc[j][3], 1.f / 2048.f, sc[j][1]);
         }
-        if (!whole) {
+      }
+      if (!whole) {
+#pragma unroll
+        for (int j = 0; j < kBlock / 8; ++j) {
           const int t = t0 + 8 * j + 2 * c;
           if (!sees(vis[0], t)) sc[j][0] = -INFINITY;
           if (!sees(vis[0], t + 1)) sc[j][1] = -INFINITY;
@@ -489,6 +486,10 @@ __global__ void __launch_bounds__(kThreads) history_attention_kernel(const __gri
             if (!sees(vis[1], t + 1)) sc[j][3] = -INFINITY;
           }
         }
+      }
+      float big[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int j = 0; j < kBlock / 8; ++j) {
         big[0] = fmaxf(big[0], fmaxf(sc[j][0], sc[j][1]));
         if (!kSplit) big[1] = fmaxf(big[1], fmaxf(sc[j][2], sc[j][3]));
       }
@@ -496,20 +497,28 @@ __global__ void __launch_bounds__(kThreads) history_attention_kernel(const __gri
       float alpha[2] = {1.f, 1.f};
 #pragma unroll
       for (int r = 0; r < (kSplit ? 1 : 2); ++r) {
-        const float m = fmaxf(top[r], quad_max(big[r]));
-        const float off = m == -INFINITY ? 0.f : m;
-        alpha[r] = exp2_approx(top[r] - off);
+        const float f = r ? f1 : f0;
+        const float m = fmaxf(top[r], quad_max(big[r]) * f);
+        const float off = m == -INFINITY ? 0.f : -m;
+        alpha[r] = exp2_approx(top[r] + off);
         top[r] = m;
         float add = 0.f;
 #pragma unroll
         for (int j = 0; j < kBlock / 8; ++j) {
-          sc[j][2 * r] = exp2_approx(sc[j][2 * r] - off);
-          sc[j][2 * r + 1] = exp2_approx(sc[j][2 * r + 1] - off);
+          sc[j][2 * r] = exp2_approx(fmaf(sc[j][2 * r], f, off));
+          sc[j][2 * r + 1] = exp2_approx(fmaf(sc[j][2 * r + 1], f, off));
           add += sc[j][2 * r] + sc[j][2 * r + 1];
         }
         sum[r] = fmaf(sum[r], alpha[r], add);
       }
-      // O = alpha O + vs P V
+      // the output's correction, where the maximum of some row grew
+      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < kAcc; ++i) o[nt][i] *= alpha[i >> 1];
+      }
+      // O += vs P V
       uint32_t pa[kBlock / 16][4];
 #pragma unroll
       for (int kt = 0; kt < kBlock / 16; ++kt) {
@@ -544,18 +553,20 @@ __global__ void __launch_bounds__(kThreads) history_attention_kernel(const __gri
           } else {
             vw[kt][i][0] = *reinterpret_cast<const uint32_t*>(vb + value_offset<D>(t, g >> 2) + 4 * (g & 3));
           }
-          // codes of events past the end are whatever an earlier history left there
-          if (t0 + t >= s.len)
-#pragma unroll
-            for (int w = 0; w < VW; ++w) vw[kt][i][w] = 0;
         }
+      if (t0 + kBlock > s.len) {
+        // codes of events past the end are whatever an earlier history left there
+#pragma unroll
+        for (int kt = 0; kt < kBlock / 16; ++kt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (t0 + 16 * kt + 2 * c + (i & 1) + 8 * (i >> 1) >= s.len)
+#pragma unroll
+              for (int w = 0; w < VW; ++w) vw[kt][i][w] = 0;
+      }
 #pragma unroll
       for (int w = 0; w < VW; ++w) {
         float acc[4][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
 #pragma unroll
         for (int kt = 0; kt < kBlock / 16; ++kt) {
           // bytes of a pair of events side by side: n tiles 4w, 4w+1 and 4w+2, 4w+3
@@ -563,22 +574,20 @@ __global__ void __launch_bounds__(kThreads) history_attention_kernel(const __gri
           const uint32_t l1 = __byte_perm(vw[kt][0][w], vw[kt][1][w], 0x7362);
           const uint32_t h0 = __byte_perm(vw[kt][2][w], vw[kt][3][w], 0x5140);
           const uint32_t h1 = __byte_perm(vw[kt][2][w], vw[kt][3][w], 0x7362);
-          mma_f16(acc[0], pa[kt], e4m3x2_lo_to_f16x2(l0), e4m3x2_lo_to_f16x2(h0));
-          mma_f16(acc[1], pa[kt], e4m3x2_hi_to_f16x2(l0), e4m3x2_hi_to_f16x2(h0));
-          mma_f16(acc[2], pa[kt], e4m3x2_lo_to_f16x2(l1), e4m3x2_lo_to_f16x2(h1));
-          mma_f16(acc[3], pa[kt], e4m3x2_hi_to_f16x2(l1), e4m3x2_hi_to_f16x2(h1));
+          mma_f16_from(acc[0], pa[kt], e4m3x2_lo_to_f16x2(l0), e4m3x2_lo_to_f16x2(h0), kt > 0);
+          mma_f16_from(acc[1], pa[kt], e4m3x2_hi_to_f16x2(l0), e4m3x2_hi_to_f16x2(h0), kt > 0);
+          mma_f16_from(acc[2], pa[kt], e4m3x2_lo_to_f16x2(l1), e4m3x2_lo_to_f16x2(h1), kt > 0);
+          mma_f16_from(acc[3], pa[kt], e4m3x2_hi_to_f16x2(l1), e4m3x2_hi_to_f16x2(h1), kt > 0);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float* out = o[4 * w + i];
           if (kSplit) {
-            out[0] = fmaf(out[0], alpha[0], vs * fmaf(acc[i][2], 1.f / 2048.f, acc[i][0]));
-            out[1] = fmaf(out[1], alpha[0], vs * fmaf(acc[i][3], 1.f / 2048.f, acc[i][1]));
+            out[0] = fmaf(vs, fmaf(acc[i][2], 1.f / 2048.f, acc[i][0]), out[0]);
+            out[1] = fmaf(vs, fmaf(acc[i][3], 1.f / 2048.f, acc[i][1]), out[1]);
           } else {
-            out[0] = fmaf(out[0], alpha[0], vs * acc[i][0]);
-            out[1] = fmaf(out[1], alpha[0], vs * acc[i][1]);
-            out[2] = fmaf(out[2], alpha[1], vs * acc[i][2]);
-            out[3] = fmaf(out[3], alpha[1], vs * acc[i][3]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) out[j] = fmaf(vs, acc[i][j], out[j]);
           }
         }
       }
@@ -637,8 +646,8 @@ __global__ void __launch_bounds__(kThreads) history_attention_kernel(const __gri
       }
       // the CTAs that share this tile: first .. last, one part each. (A cut moves
       // out of short tiles only, so a split tile's cuts are where they were.)
-      const int64_t first = ((seg0 + 1) * ctas - 1) / total, last = (seg1 * ctas - 1) / total;
-      const int parts = static_cast<int>(last - first) + 1;
+      const int64_t first = cuts.owner(seg0);
+      const int parts = cuts.owner(seg1 - 1) - static_cast<int>(first) + 1;
       __threadfence();
       __syncthreads();
       if (threadIdx.x == 0) {
@@ -720,6 +729,7 @@ cudaError_t launch(const Params& p, cudaStream_t stream) {
   const int64_t events = static_cast<int64_t>(p.h.max_pages) * p.h.page_tokens;
   const int64_t tiles = p.a.q_rows * p.group / kRows + p.a.batch;
   const int64_t chunks = tiles * p.h.n_heads * ((events + chunk - 1) / chunk + 1);
+  if (chunks >= (int64_t(1) << 31)) return cudaErrorInvalidValue;   // history_attention has checked
   const int64_t grid = std::min<int64_t>(
       {chunks, static_cast<int64_t>(device_sm_count()) * per_sm, int64_t(kAttnMaxCtas)});
   return launch_pdl(history_attention_kernel<D, DT>, dim3(static_cast<unsigned>(grid)),
