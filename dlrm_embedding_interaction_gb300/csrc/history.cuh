@@ -118,6 +118,11 @@ struct HistoryWork {
 constexpr int kAttnMaxCtas = 152 * 8;
 constexpr int kAttnRows = 16;
 constexpr int kAttnPartial = kAttnRows * (128 + 2);
+// The same of the tensor-core kernel: a CTA per SM, units of 256 rows, a counter
+// for each of 8 warps.
+constexpr int kAttnTcCtas = 152;
+constexpr int kAttnTcPartial = 256 * (128 + 2);
+static_assert(kAttnTcCtas * 8 <= kAttnMaxCtas, "counters");
 
 inline HistoryWork history_work(const dlrm_history_t& h) {
   HistoryWork w{};
@@ -141,7 +146,7 @@ inline HistoryWork history_work(const dlrm_history_t& h) {
   w.movers = take(4 * pages);
   w.tiles = take(8 * (pages / 1024 + 1));
   w.counters = take(4 * kAttnMaxCtas);
-  w.partials = take(int64_t(4) * 2 * kAttnMaxCtas * kAttnPartial);
+  w.partials = take(int64_t(4) * 2 * std::max(kAttnMaxCtas * kAttnPartial, kAttnTcCtas * kAttnTcPartial));
   w.total = at;
   return w;
 }
@@ -163,6 +168,9 @@ cudaError_t launch_history_free(const dlrm_history_t& h, const int32_t* slots, i
 cudaError_t launch_history_compact(const dlrm_history_t& h, cudaStream_t stream);
 cudaError_t launch_history_attention(const dlrm_history_t& h, const dlrm_attention_t& a,
                                      cudaStream_t stream);
+bool history_tc_takes(const dlrm_history_t& h, const dlrm_attention_t& a);
+cudaError_t launch_history_attention_tc(const dlrm_history_t& h, const dlrm_attention_t& a,
+                                        int32_t* counters, float* partials, cudaStream_t stream);
 cudaError_t launch_window_attention(const dlrm_attention_t& a, cudaStream_t stream);
 
 }  // namespace dlrm

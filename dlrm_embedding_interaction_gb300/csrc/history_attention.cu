@@ -756,6 +756,7 @@ cudaError_t launch_history_attention(const dlrm_history_t& h, const dlrm_attenti
   p.vec_q = reinterpret_cast<uintptr_t>(a.q) % four == 0 && a.ld_q % 4 == 0 && a.ld_q_head % 4 == 0;
   p.counters = work_part<int32_t>(h, w.counters);
   p.partials = work_part<float>(h, w.partials);
+  if (history_tc_takes(h, a)) return launch_history_attention_tc(h, a, p.counters, p.partials, stream);
   if (h.head_dim == 32) return launch_d<32>(p, stream);
   if (h.head_dim == 64) return launch_d<64>(p, stream);
   return launch_d<128>(p, stream);

@@ -1,964 +1,41 @@
-// window_attention on the 5th-generation tensor cores: bf16 and fp16 rows that
-// TMA can read (window_attention.cu takes every other call).
+// window_attention on the tensor cores: bf16 and fp16 rows that TMA can read
+// (attention_tc.cuh; window_attention.cu takes every other call).
 //
-// A work unit is 256 rows, as two tiles of 128 (the MMA's M), of one kv head of
-// a request; rows are (query, head of the group) pairs. Persistent CTAs, one
-// per SM, take units round-robin. Per unit the keys that any of its rows sees
-// flow by in key tiles of at most 64 events: the sinks that lie apart from the
-// window first (a narrow tile), then the window from its first event on.
-//   warp 11: finds the units and writes what the others need of them into a
-//     ring in shared memory;
-//   warp 10, one lane: TMA of key and value tiles (boxes of 32 events x 64
-//     elements, 128-byte swizzle) through rings of four stages each;
-//   warps 8 and 9, one lane each: the products of tile 0 and 1: S_t = Q_t K^T
-//     (operands from shared memory), then, when the weights are there, O_t += P_t V
-//     (P from tensor memory, V as stored: the MN-major operand form). One lane's
-//     waits and issues take about as long as a tile's softmax, hence two warps.
-//     They also load their tile's queries, by TMA where the group divides 128
-//     (else the softmax warps do);
-//   warps 0-3 and 4-7: softmax of tile 0 and 1. A thread owns a row: it reads
-//     its 64 scores from tensor memory, masks, takes the maximum, writes the
-//     weights in the input's type over the scores, and keeps its sum. The
-//     output is only corrected when a row's maximum has grown by more than 2^8
-//     over the reference in use (weights up to 2^8 are as exact, and the sum is
-//     fp32), which real scores do in the first tiles only. 32 columns that none
-//     of a warp's rows sees are neither read nor exponentiated.
-// Tensor memory: two score buffers of 64 columns a tile (weights over the
-// scores) and the output, up to 128 columns a tile. With two buffers the scores
-// of the next key tile are made while the softmax works on this one's.
-//
-// What bounds it: the exponentials (16 a cycle and SM: 512 cycles a tile of
-// 128 x 64) for head_dim 32 and 64, and as much the tensor core (320 + 256 cycles)
-// for 128.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include <atomic>
-
-#include "tc.cuh"
-#include "window_attention.cuh"
+// What bounds it: the softmax warps. A step of 128 rows x 64 events takes a warp
+// about 2070 cycles, of which the exponentials are 700 and the rest latency, and
+// two warps a sub-partition do not hide it; the tensor core is 47% busy at
+// head_dim 128.
+#include "attention_tc.cuh"
 
 namespace dlrm {
 
-using namespace tc;
-
-namespace {
-
-constexpr int kThreads = 384;
-constexpr int kUnit = 256;                       // rows of a work unit
-constexpr int kKeys = 64;                        // events of a key tile
-constexpr int kBox = 32;                         // events of one TMA box
-constexpr int kQBlock = 128 * 128;               // 128 rows of 128 bytes (64 elements)
-constexpr int kBlockBytes = kKeys * 128;         // the same of a key tile
-constexpr int kStages = 4;                       // of keys, and of values
-constexpr float kSlack = 8.f;                    // log2 of the largest weight
-
-template <int D>
-struct Layout {
-  static constexpr int kBlocks = (D + 63) / 64;  // 64-element column blocks
-  static constexpr int kTile = kBlocks * kBlockBytes;
-  static constexpr int kQTile = kBlocks * kQBlock;
-  static constexpr int kQ = 0;                   // two query tiles
-  static constexpr int kK = 2 * kQTile;
-  static constexpr int kV = kK + kStages * kTile;
-  static constexpr int kBars = kV + kStages * kTile;
-  // more than half an SM's shared memory, so that one CTA is resident: it
-  // takes all of the tensor memory
-  static constexpr int kSmem = kBars + 1024 + 1024 > 120 * 1024 ? kBars + 1024 + 1024 : 120 * 1024;
-  static_assert(kSmem <= 232448, "shared memory of one CTA");
-};
-
-// n / d for 0 <= n < 2^31 by a multiplication: with s = ceil(log2 d) and
-// mul = floor(2^32 (2^s - d) / d) + 1, n / d = (hi32(n mul) + n) >> s (the
-// method of Granlund and Montgomery for invariant divisors).
-struct FastDiv {
-  uint32_t mul, shift, d;
-  __device__ __forceinline__ int operator()(int n) const {
-    return static_cast<int>((__umulhi(static_cast<uint32_t>(n), mul) + static_cast<uint32_t>(n)) >> shift);
-  }
-};
-FastDiv fast_div(int d) {
-  FastDiv f{};
-  f.d = static_cast<uint32_t>(d);
-  while ((uint64_t(1) << f.shift) < f.d) ++f.shift;
-  f.mul = static_cast<uint32_t>(((uint64_t(1) << 32) * ((uint64_t(1) << f.shift) - f.d)) / f.d + 1);
-  return f;
-}
-
-struct TcParams {
-  WindowParams w;
-  FastDiv group, heads;
-  int vec_out;
-  int q_tma;                                     // queries by TMA: boxes of group x 128 / group
-  WaitCfg wait;
-};
-
-__device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count)
-               : "memory");
-}
-__device__ __forceinline__ void bar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar))
-               : "memory");
-}
-__device__ __forceinline__ void bar_expect(uint64_t* bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(
-                   smem_addr(bar)),
-               "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y,
-                                            int z, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
-      : "memory");
-}
-
-// Bounded wait for a phase; false once this or another thread gave up.
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                       int32_t* err, uint64_t limit) {
-  const uint32_t a = smem_addr(bar);
-  const uint64_t t0 = now_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (try_wait(a, parity)) return true;
-    if ((i & 15) == 0) {
-      if (*abort_flag) return false;
-      if (now_ns() - t0 > limit) {
-        *abort_flag = 1;
-        flag(err, DLRM_ERRBIT_TIMEOUT);
-        return false;
-      }
-    }
-  }
-}
-struct Waiter {
-  volatile int* abort_flag;
-  int32_t* err;
-  uint64_t limit;
-  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
-    if (try_wait(smem_addr(bar), parity)) return true;
-    return wait_slow(bar, parity, abort_flag, err, limit);
-  }
-  // regardless of the abort flag: work in flight
-  __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) const {
-    const uint64_t t0 = now_ns();
-    while (!try_wait(smem_addr(bar), parity)) {
-      if (now_ns() - t0 > limit) {
-        flag(err, DLRM_ERRBIT_TIMEOUT);
-        return;
-      }
-    }
-  }
-};
-
-// Shared-memory descriptors: the low word holds the start address (and the
-// leading byte offset), the high word is the same for all operands here:
-// 8-row groups 1024 bytes apart, version 1, 128-byte swizzle.
-constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-// rows of the inner dimension (queries, keys): K-major
-__device__ __forceinline__ uint32_t rows_desc(uint32_t addr) { return (addr >> 4) | (1u << 16); }
-// values, as the B operand of P V: MN-major, an event's 64 elements are a row
-// of 128 bytes, 64-element column blocks kBlockBytes apart
-__device__ __forceinline__ uint32_t values_desc(uint32_t addr) {
-  return (addr >> 4) | (static_cast<uint32_t>(kBlockBytes >> 4) << 16);
-}
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
-                                       uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
-      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
-      : "memory");
-}
-// A in tensor memory: the weights.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc,
-                                       uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "mov.b64 b, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t at) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, "
-      "%27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(at));
-}
-__device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t at) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(at));
-}
-__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16};" ::"r"(at),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_wait_ld() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-
-// One work unit, in shared memory.
-struct Unit {
-  int valid, head, row0;                         // row0: first row of tile 0
-  WindowSpan s;
-  int pos0;                                      // position of the request's first query
-  int rows[2];                                   // rows of each tile
-  int end1[2], gap0[2], gap1[2];                 // of a tile's last row: end, gap0; of its first: gap1
-  int last[2];                                   // last key tile that a tile needs, -1: none
-  int sink, lo, end, sink_tiles, tiles;          // keys [0, sink) and [lo, end)
-
-  // Key tile k: events [key0, key0 + n), computed `width` wide.
-  __device__ __forceinline__ void tile(int k, int& key0, int& n, int& width) const {
-    if (k < sink_tiles) {
-      key0 = k * kKeys;
-      n = min(kKeys, sink - key0);
-    } else {
-      key0 = lo + (k - sink_tiles) * kKeys;
-      n = min(kKeys, end - key0);
-    }
-    width = (n + kBox - 1) / kBox * kBox;
-  }
-  __device__ __forceinline__ bool needs(int t, int key0, int n) const {
-    return rows[t] > 0 && key0 < end1[t] && !(key0 >= gap0[t] && key0 + n <= gap1[t]);
-  }
-};
-constexpr int kUnits = 3;                        // units known ahead
-constexpr int kReaders = 11;                     // warps that read a unit
-
-// What a loop over key tiles needs of a unit, in registers.
-struct Keys {
-  int lo, end, sink, sink_tiles, tiles;
-  bool have[2];
-  int end1[2], gap0[2], gap1[2];
-  __device__ __forceinline__ explicit Keys(const Unit& x)
-      : lo(x.lo), end(x.end), sink(x.sink), sink_tiles(x.sink_tiles), tiles(x.tiles) {
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      have[t] = x.rows[t] > 0;
-      end1[t] = x.end1[t];
-      gap0[t] = x.gap0[t];
-      gap1[t] = x.gap1[t];
-    }
-  }
-  __device__ __forceinline__ void tile(int k, int& key0, int& n) const {
-    const bool s = k < sink_tiles;
-    key0 = s ? k * kKeys : lo + (k - sink_tiles) * kKeys;
-    n = min(kKeys, (s ? sink : end) - key0);
-  }
-  template <int T>
-  __device__ __forceinline__ bool needs(int key0, int n) const {
-    return have[T] && key0 < end1[T] && !(key0 >= gap0[T] && key0 + n <= gap1[T]);
-  }
-};
-
-struct Bars {
-  uint64_t q_full[2], k_full[kStages], k_empty[kStages], v_full[kStages],
-      v_empty[kStages], s_full[2][2], p_full[2][2], pv_done[2][2], o_empty[2], u_full[kUnits],
-      u_empty[kUnits], drain[2];
-  uint32_t tmem;
-  int abort;
-  Unit units[kUnits];
-};
-static_assert(sizeof(Bars) <= 1024, "space behind the tiles");
-
-// Finds a CTA's units in order, by one warp.
-struct Walk {
-  int b = 0;
-  int before = 0;                                // units of the requests before b
-
-  __device__ __forceinline__ void find(const TcParams& tp, int u, Unit& x) {
-    const WindowParams& p = tp.w;
-    const int lane = threadIdx.x % kWarp;
-    const int heads = p.a.n_kv_heads;
-    WindowSpan s{};
-    for (;;) {
-      if (b >= p.a.batch) {
-        if (lane == 0) x.valid = 0;
-        return;
-      }
-      int n = 0;
-      if (b + lane < p.a.batch) {
-        s = window_span(p, b + lane, kUnit, false);
-        n = s.tiles * heads;
-      }
-      int inc = n;
-#pragma unroll
-      for (int d = 1; d < kWarp; d *= 2) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, d);
-        if (lane >= d) inc += y;
-      }
-      const unsigned past = __ballot_sync(0xffffffffu, before + inc > u);
-      if (past) {
-        const int at = __ffs(past) - 1;
-        before += __shfl_sync(0xffffffffu, inc - n, at);
-        if (lane == at) {
-          fill(tp, u - before, s, x);
-        }
-        b += at;
-        return;
-      }
-      before += __shfl_sync(0xffffffffu, inc, kWarp - 1);
-      b += kWarp;
-    }
-  }
-
-  // Unit i of the request with rows s, by one thread.
-  __device__ __forceinline__ void fill(const TcParams& tp, int i, const WindowSpan& s, Unit& out) {
-    const WindowParams& p = tp.w;
-    Unit x;
-    x.valid = 1;
-    x.s = s;
-    // the last rows of a request first: without a window they see the most
-    const int tile = tp.heads(i);
-    x.head = i - tile * p.a.n_kv_heads;
-    x.row0 = (s.tiles - 1 - tile) * kUnit;
-    x.pos0 = s.len - tp.group(s.rows);
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      x.rows[t] = max(0, min(128, s.rows - x.row0 - 128 * t));
-      const int r0 = min(x.row0 + 128 * t, s.rows - 1), r1 = max(r0, r0 + x.rows[t] - 1);
-      const Visible first = visible(x.pos0 + tp.group(r0), s.len, p.a.window, p.a.sinks);
-      const Visible last = visible(x.pos0 + tp.group(r1), s.len, p.a.window, p.a.sinks);
-      x.end1[t] = last.end;
-      x.gap0[t] = last.gap0;
-      x.gap1[t] = first.gap1;
-    }
-    const int u = x.rows[1] > 0 ? 1 : 0;
-    x.end = x.end1[u];
-    const bool apart = x.gap1[0] > x.gap0[u];
-    x.lo = apart ? min(x.gap1[0], x.end) : 0;
-    x.sink = apart ? min(x.gap0[u], x.end) : 0;
-    x.sink_tiles = (x.sink + kKeys - 1) / kKeys;
-    x.tiles = x.sink_tiles + (x.end - x.lo + kKeys - 1) / kKeys;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      x.last[t] = -1;
-      for (int k = x.tiles - 1; k >= 0; --k) {
-        int key0, n, width;
-        x.tile(k, key0, n, width);
-        if (x.needs(t, key0, n)) {
-          x.last[t] = k;
-          break;
-        }
-      }
-    }
-    out = x;
-  }
-};
-
-// A warp's place in the ring of units; one lane of it may walk alone.
-struct Units {
-  Bars& bars;
-  const Waiter& wait;
-  int it = 0;
-  __device__ __forceinline__ const Unit* next() {
-    const int slot = it % kUnits;
-    const bool ok = wait(&bars.u_full[slot], (it / kUnits) & 1);
-    const Unit* x = &bars.units[slot];
-    return ok && x->valid ? x : nullptr;
-  }
-  __device__ __forceinline__ void done() { bar_arrive(&bars.u_empty[it++ % kUnits]); }
-  // by all lanes
-  __device__ __forceinline__ const Unit* next_warp() {
-    const Unit* x = next();
-    return __all_sync(0xffffffffu, x != nullptr) ? x : nullptr;
-  }
-  __device__ __forceinline__ void done_warp() {
-    __syncwarp();
-    if (threadIdx.x % kWarp == 0) bar_arrive(&bars.u_empty[it % kUnits]);
-    ++it;
-  }
-};
-
-// 32 values as pairs, for the packed fp32 instructions.
-__device__ __forceinline__ void fma2(float& x, float& y, float f, float c) {
-  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\t"
-      "mov.b64 c, {%3, %3};\n\tfma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
-      : "+f"(x), "+f"(y)
-      : "f"(f), "f"(c));
-}
-__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
-  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
-      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
-      : "+f"(x), "+f"(y)
-      : "f"(a), "f"(b));
-}
-// Bits [0, n) of a word, n any integer.
-__device__ __forceinline__ uint32_t low_bits(int n) {
-  return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1;
-}
-__device__ __forceinline__ bool elect_one() {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok));
-  return ok != 0;
-}
-
-// The products of tile T of every unit, by one lane.
-template <int D, int DT, int T>
-__device__ __forceinline__ void products(const TcParams& p, const CUtensorMap* map_q, Bars& bars,
-                                         const Waiter& wait, unsigned char* base, uint32_t tmem) {
-  using L = Layout<D>;
-  constexpr int kFormat = DT == DLRM_DTYPE_BF16 ? 1 : 0;
-  // D fp32; A, B formats; M = 128; B of the second product is MN-major
-  constexpr uint32_t kIdescS = (1u << 4) | (kFormat << 7) | (kFormat << 10) | (8u << 24);
-  constexpr uint32_t kIdescO = kIdescS | (1u << 16) | (static_cast<uint32_t>(D / 8) << 17);
-  const uint32_t q_desc = rows_desc(smem_addr(base + L::kQ + T * L::kQTile));
-  const uint32_t k_desc = rows_desc(smem_addr(base + L::kK));
-  const uint32_t v_desc = values_desc(smem_addr(base + L::kV));
-  const uint32_t s_base = tmem + T * 128, o = tmem + 256 + T * 128;
-  uint32_t kv = 0, it = 0, units_done = 0;       // key tiles of the CTA, of this tile; its units
-  Units units{bars, wait};
-  for (const Unit* x; (x = units.next()); units.done()) {
-    const Keys keys(*x);
-    // the queries: every score of the unit before has been read, so the tile
-    // may be replaced
-    if (p.q_tma && x->last[T] >= 0) {
-      bar_expect(&bars.q_full[T], L::kQTile);
-#pragma unroll
-      for (int c = 0; c < L::kBlocks; ++c)
-        tma_load_3d(smem_addr(base + L::kQ + T * L::kQTile + c * kQBlock), map_q, c * 64,
-                    x->head * p.w.group, x->s.q0 + p.group(x->row0 + 128 * T), &bars.q_full[T]);
-    }
-    bool due = false, begun = false, used_before = false;
-    int due_width = 0;
-    for (int k = 0; k <= keys.tiles; ++k) {
-      int key0 = 0, n = 0;
-      bool need = false, used = false;
-      if (k < keys.tiles) {
-        keys.tile(k, key0, n);
-        need = keys.needs<T>(key0, n);
-        used = need || keys.needs<1 - T>(key0, n);
-      }
-      if (used) {
-        // scores of this tile, into the buffer that the weights before last lay in
-        const uint32_t st = kv % kStages;
-        bool ok = wait(&bars.k_full[st], (kv / kStages) & 1);
-        // (queries in flight land before anything gives up)
-        if (need && !begun && !due) {
-          if (ok) ok = wait(&bars.q_full[T], units_done & 1);
-          if (!ok && p.q_tma) wait.drain(&bars.q_full[T], units_done & 1);
-        }
-        if (!ok) return;
-        if (need) {
-          // products of different shapes are not ordered among themselves: those
-          // weights must have been used. (Product i completes phase i / 2 of
-          // barrier i % 2. Whoever waits for it knows that i - 2 is complete and
-          // that i + 2 is not issued, so the phase's parity says enough.)
-          if (it >= 2 && !wait(&bars.pv_done[T][it & 1], ((it - 2) >> 1) & 1)) return;
-          fence_after();
-          const uint32_t idesc = kIdescS | (n > 32 ? 8u << 17 : 4u << 17);
-          const uint32_t sa = s_base + (it & 1) * kKeys, kd = k_desc + st * (L::kTile >> 4);
-#pragma unroll
-          for (int j = 0; j < D / 16; ++j)
-            mma_ss(sa, q_desc + (((j / 4) * kQBlock + (j % 4) * 32) >> 4),
-                   kd + (((j / 4) * kBlockBytes + (j % 4) * 32) >> 4), idesc, j > 0 ? 1u : 0u);
-          mma_commit(smem_addr(&bars.s_full[T][it & 1]));
-          mma_commit(smem_addr(&bars.k_empty[st]));
-          ++it;
-        } else {
-          bar_arrive(&bars.k_empty[st]);
-        }
-        ++kv;
-      }
-      if (used_before) {
-        // products with the values of the tile before
-        const uint32_t vi = kv - 1 - (used ? 1 : 0), st = vi % kStages;
-        if (!wait(&bars.v_full[st], (vi / kStages) & 1)) return;
-        if (due) {
-          const uint32_t of = it - 1 - (need ? 1 : 0);
-          if (!begun && units_done > 0 && !wait(&bars.o_empty[T], (units_done - 1) & 1)) return;
-          if (!wait(&bars.p_full[T][of & 1], (of >> 1) & 1)) return;
-          fence_after();
-          const uint32_t vd = v_desc + st * (L::kTile >> 4), pa = s_base + (of & 1) * kKeys;
-          mma_ts(o, pa, vd, kIdescO, begun ? 1u : 0u);
-          mma_ts(o, pa + 8, vd + (2048 >> 4), kIdescO, 1u);
-          if (due_width > 32) {
-            mma_ts(o, pa + 16, vd + 2 * (2048 >> 4), kIdescO, 1u);
-            mma_ts(o, pa + 24, vd + 3 * (2048 >> 4), kIdescO, 1u);
-          }
-          mma_commit(smem_addr(&bars.pv_done[T][of & 1]));
-          mma_commit(smem_addr(&bars.v_empty[st]));
-          begun = true;
-        } else {
-          bar_arrive(&bars.v_empty[st]);
-        }
-      }
-      used_before = used;
-      due = need;
-      due_width = n;
-    }
-    units_done += begun ? 1 : 0;
-  }
-}
-
-template <int D, int DT>
-__global__ void __launch_bounds__(kThreads, 1)
-window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                 const __grid_constant__ CUtensorMap map_v, const __grid_constant__ TcParams p) {
-  using L = Layout<D>;
-  extern __shared__ __align__(1024) unsigned char smem_raw[];
-  unsigned char* base = reinterpret_cast<unsigned char*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  Bars& bars = *reinterpret_cast<Bars*>(base + L::kBars);
-  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
-  const WindowParams& w = p.w;
-  const Waiter wait{&bars.abort, w.a.err, wait_limit_ns(p.wait)};
-
-  if (warp == 8) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_addr(&bars.tmem)),
-                 "n"(512)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
-  if (threadIdx.x == 0) {
-    for (int t = 0; t < 2; ++t) {
-      bar_init(&bars.q_full[t], p.q_tma ? 1 : 4);
-      for (int i = 0; i < 2; ++i) {
-        bar_init(&bars.s_full[t][i], 1);
-        bar_init(&bars.p_full[t][i], 4);
-        bar_init(&bars.pv_done[t][i], 1);
-      }
-      bar_init(&bars.o_empty[t], 4);
-    }
-    for (int i = 0; i < kStages; ++i) {
-      bar_init(&bars.k_full[i], 1);
-      bar_init(&bars.k_empty[i], 2);
-      bar_init(&bars.v_full[i], 1);
-      bar_init(&bars.v_empty[i], 2);
-    }
-    for (int i = 0; i < kUnits; ++i) {
-      bar_init(&bars.u_full[i], 1);
-      bar_init(&bars.u_empty[i], kReaders);
-    }
-    for (int t = 0; t < 2; ++t) bar_init(&bars.drain[t], 1);
-    bars.abort = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  fence_before();
-  __syncthreads();
-  fence_after();
-  const uint32_t tmem = bars.tmem;
-  pdl_wait();
-  pdl_trigger();
-
-  Units units{bars, wait};
-  if (warp < 8) {
-    // ------------------------------------------------------------ softmax
-    const int t = warp / 4;
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t o_at = tmem + lanes + 256 + t * 128;
-    const float f = w.a.scale * kLog2e;
-    uint32_t it = 0;                              // key tiles so far
-    bool ok = true;
-    for (const Unit* x; ok && (x = units.next_warp()); units.done_warp()) {
-      const int rows = x->rows[t];
-      if (rows == 0) continue;
-      const Keys keys(*x);
-      const int r = (warp & 3) * 32 + lane;
-      const int row = min(x->row0 + 128 * t + r, x->s.rows - 1);
-      const bool in = r < rows;
-      const int i = p.group(row);
-      const Visible v = visible(x->pos0 + i, x->s.len, w.a.window, w.a.sinks);
-      if (!p.q_tma && x->last[t] >= 0) {
-        // this row's queries; zeros past the last row
-        unsigned char* dst = base + L::kQ + t * L::kQTile;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const uint16_t*>(w.a.q) + (x->s.q0 + static_cast<int64_t>(i)) * w.a.ld_q +
-            (x->head * w.group + row - i * w.group) * w.a.ld_q_head);
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c)
-          *reinterpret_cast<uint4*>(dst + (c / 8) * kQBlock + swz_offset(r, c % 8)) =
-              in ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) bar_arrive(&bars.q_full[t]);
-      }
-      float top = -INFINITY, sum = 0.f;
-      bool any = false;
-      const int tiles = x->last[t] + 1;
-      for (int k = 0; k < tiles; ++k) {
-        int key0, n;
-        keys.tile(k, key0, n);
-        if (!(t ? keys.needs<1>(key0, n) : keys.needs<0>(key0, n))) continue;
-        const uint32_t s_at = tmem + lanes + t * 128 + (it & 1) * kKeys;
-        ok = __all_sync(0xffffffffu, wait(&bars.s_full[t][it & 1], (it >> 1) & 1));
-        if (!ok) break;
-        fence_after();
-        // a running maximum m (times f) of scores not seen before: keeps the
-        // reference unless m passed it by more than the slack
-        auto raise = [&](float m) {
-          const bool grow = m > top + kSlack || (top == -INFINITY && m > -INFINITY);
-          if (__any_sync(0xffffffffu, grow)) {
-            const float alpha = grow ? exp2_approx(top - m) : 1.f;
-            if (grow) top = m;
-            sum *= alpha;
-            if (any) {
-              // the product before this tile's must be complete; the one before
-              // that is (its weights lay where these scores are)
-              ok = __all_sync(0xffffffffu,
-                              wait(&bars.pv_done[t][(it - 1) & 1], ((it - 1) >> 1) & 1));
-              fence_after();
-#pragma unroll 1
-              for (int c = 0; c < D; c += 16) {
-                uint32_t o[16];
-                tmem_ld16(o, o_at + c);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-                tmem_st16(o_at + c, o);
-              }
-            }
-          }
-          return top == -INFINITY ? 0.f : -top;
-        };
-        // 32 scores to 16 words of weights
-        auto weigh = [&](uint32_t (&pw)[16], const uint32_t* s, float off) {
-          float add[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            float a = __uint_as_float(s[2 * j]), b = __uint_as_float(s[2 * j + 1]);
-            fma2(a, b, f, off);
-            a = exp2_approx(a);
-            b = exp2_approx(b);
-            add2(add[2 * (j & 1)], add[2 * (j & 1) + 1], a, b);
-            pw[j] = DT == DLRM_DTYPE_BF16 ? pack_bf16(a, b) : pack_f16x2(a, b);
-          }
-          sum += (add[0] + add[1]) + (add[2] + add[3]);
-        };
-        // columns [0, 32) and [32, 64): skipped where none of the warp's rows
-        // sees any, masked where some do not see all
-        uint32_t s[2][32];
-        bool some[2] = {true, true}, part[2] = {false, false};
-        if (!__all_sync(0xffffffffu, n == kKeys && key0 + kKeys <= v.end &&
-                                         (key0 >= v.gap1 || key0 + kKeys <= v.gap0))) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int c0 = key0 + 32 * c, c1 = c0 + 32;
-            const bool all = 32 * c + 32 <= n && c1 <= v.end && (c0 >= v.gap1 || c1 <= v.gap0);
-            const bool none = 32 * c >= n || c0 >= v.end || (c0 >= v.gap0 && c1 <= v.gap1);
-            some[c] = __any_sync(0xffffffffu, !none);
-            part[c] = __any_sync(0xffffffffu, !all);
-          }
-        }
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          if (some[c]) tmem_ld32(s[c], s_at + 32 * c);
-        tmem_wait_ld();
-        float big[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          if (some[c]) {
-            if (part[c]) {
-              const int e = min(n, v.end - key0) - 32 * c;
-              const uint32_t bits = low_bits(min(v.gap0 - key0 - 32 * c, e)) |
-                                    (low_bits(e) & ~low_bits(v.gap1 - key0 - 32 * c));
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!(bits & (1u << j))) s[c][j] = 0xff800000u;
-            }
-#pragma unroll
-            for (int j = 0; j < 32; ++j) big[j & 3] = fmaxf(big[j & 3], __uint_as_float(s[c][j]));
-          }
-        const float off = raise(fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * f);
-        if (!ok) break;
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          if (c == 0 || n > 32) {
-            uint32_t pw[16];
-            if (some[c]) {
-              weigh(pw, s[c], off);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) pw[j] = 0;
-            }
-            tmem_st16(s_at + 16 * c, pw);         // over the scores, which are in registers
-          }
-        any = true;
-        tmem_wait_st();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&bars.p_full[t][it & 1]);
-        ++it;
-      }
-      if (!ok) break;
-      // ---- output
-      float inv = 0.f;
-      if (any) {
-        // the last product, and with it all before it
-        ok = __all_sync(0xffffffffu, wait(&bars.pv_done[t][(it - 1) & 1], ((it - 1) >> 1) & 1));
-        if (!ok) break;
-        fence_after();
-        inv = sum == 0.f ? 0.f : 1.f / sum;
-      }
-      const int hq = x->head * w.group + row - i * w.group;
-      const int64_t q = x->s.q0 + static_cast<int64_t>(i);
-      const int64_t o_row = q * w.a.ld_out + hq * w.a.ld_out_head;
-      bool odd = false;
-#pragma unroll
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32], h[16];
-        if (any) {
-          tmem_ld32(o, o_at + c);
-          tmem_wait_ld();
-        }
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          float a = 0.f, b = 0.f;
-          if (sum != 0.f) {
-            a = __uint_as_float(o[2 * j]) * inv;
-            b = __uint_as_float(o[2 * j + 1]) * inv;
-          }
-          odd |= !finite(a) || !finite(b);
-          h[j] = DT == DLRM_DTYPE_BF16 ? pack_bf16(a, b) : pack_f16x2(a, b);
-        }
-        if (in) {
-          uint16_t* out = static_cast<uint16_t*>(w.a.out) + o_row + c;
-          if (p.vec_out) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              reinterpret_cast<uint4*>(out)[j] =
-                  make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              out[2 * j] = static_cast<uint16_t>(h[j]);
-              out[2 * j + 1] = static_cast<uint16_t>(h[j] >> 16);
-            }
-          }
-        }
-      }
-      if (any) {
-        fence_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&bars.o_empty[t]);
-      }
-      if (in && w.a.lse)
-        w.a.lse[q * w.a.n_heads + hq] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
-      for (unsigned who = __ballot_sync(0xffffffffu, odd && in); who; who &= who - 1) {
-        __syncwarp();
-        window_careful_row<D, DT>(w, x->s, x->head, x->row0 + 128 * t + (warp & 3) * 32 + __ffs(who) - 1);
-      }
-    }
-  } else if (warp < 10) {
-    // ------------------------------------------------------------ products
-    const int t = warp - 8;
-    if (elect_one()) {
-      if (t == 0)
-        products<D, DT, 0>(p, &map_q, bars, wait, base, tmem);
-      else
-        products<D, DT, 1>(p, &map_q, bars, wait, base, tmem);
-      // nothing of the tensor core's may be in flight when its memory is freed
-      mma_commit(smem_addr(&bars.drain[t]));
-      wait.drain(&bars.drain[t], 0);
-    }
-    __syncwarp();
-  } else if (warp == 10) {
-    // ------------------------------------------------------------ keys and values
-    if (lane == 0) {
-      uint32_t it = 0;
-      bool ok = true;
-      for (const Unit* x; ok && (x = units.next()); units.done()) {
-        const Keys keys(*x);
-        const int head = x->head, k0 = x->s.k0;
-        for (int k = 0; k < keys.tiles && ok; ++k) {
-          int key0, n;
-          keys.tile(k, key0, n);
-          if (!keys.needs<0>(key0, n) && !keys.needs<1>(key0, n)) continue;
-          const uint32_t st = it % kStages, ph = ((it / kStages) & 1) ^ 1;
-#pragma unroll
-          for (int side = 0; side < 2; ++side) {
-            uint64_t* full = side ? &bars.v_full[st] : &bars.k_full[st];
-            if (it >= kStages && !(ok = wait(side ? &bars.v_empty[st] : &bars.k_empty[st], ph))) break;
-            bar_expect(full, (n > kBox ? 2u : 1u) * kBox * 128 * L::kBlocks);
-            const uint32_t dst = smem_addr(base + (side ? L::kV : L::kK) + st * L::kTile);
-#pragma unroll
-            for (int r = 0; r < kKeys; r += kBox)
-              if (r < n)
-#pragma unroll
-                for (int c = 0; c < L::kBlocks; ++c)
-                  tma_load_3d(dst + c * kBlockBytes + r * 128, side ? &map_v : &map_k, c * 64, head,
-                              k0 + key0 + r, full);
-          }
-          ++it;
-        }
-      }
-      // loads in flight must land before the shared memory is released; after
-      // a wait that gave up, the keys of a stage may be loaded and its values not
-      const uint32_t from = it > kStages ? it - kStages : 0;
-      for (uint32_t q = from; ok && q < it; ++q) {
-        wait.drain(&bars.k_full[q % kStages], (q / kStages) & 1);
-        wait.drain(&bars.v_full[q % kStages], (q / kStages) & 1);
-      }
-      if (!ok) {
-        const uint64_t t0 = now_ns();
-        while (now_ns() - t0 < 1000000) {}        // landed long before
-      }
-    }
-    __syncwarp();
-  } else {
-    // ------------------------------------------------------------ units
-    Walk walk;
-    for (int it = 0, u = blockIdx.x;; ++it, u += gridDim.x) {
-      const int slot = it % kUnits;
-      if (it >= kUnits &&
-          !__all_sync(0xffffffffu, wait(&bars.u_empty[slot], ((it / kUnits) & 1) ^ 1)))
-        break;
-      walk.find(p, u, bars.units[slot]);
-      __syncwarp();
-      const bool valid = bars.units[slot].valid != 0;
-      __syncwarp();
-      if (lane == 0) bar_arrive(&bars.u_full[slot]);
-      if (!valid) break;
-    }
-    if (blockIdx.x == 0)
-      for (int i = lane; i < w.a.batch; i += kWarp) window_span(w, i, kUnit, true);
-  }
-  fence_before();
-  __syncthreads();
-  if (warp == 8) {
-    fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512)
-                 : "memory");
-  }
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static std::atomic<void*> fn{nullptr};
-  void* f = fn.load(std::memory_order_acquire);
-  if (!f) {
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return nullptr;
-    fn.store(f, std::memory_order_release);
-  }
-  return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-}
-
-// (rows, heads, D) with strides ld, ld_head: boxes of box_rows rows x box_heads
-// heads x 64 elements; zeros past D and past the last row.
-bool encode_rows(CUtensorMap* map, const void* x, int64_t rows, int heads, int dim, int64_t ld,
-                 int64_t ld_head, int dtype, int box_rows, int box_heads) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
-  if (!enc) return false;
-  if (heads == 1) ld_head = dim;                  // not used
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads),
-                              static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld_head) * 2, static_cast<cuuint64_t>(ld) * 2};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
-  const cuuint32_t steps[3] = {1, 1, 1};
-  return enc(map,
-             dtype == DLRM_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-             3, const_cast<void*>(x), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-template <int D, int DT>
-cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const TcParams& p, unsigned grid,
-                   cudaStream_t stream) {
-  static std::atomic<uint64_t> done{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
-  if (!bit || !(done.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(window_tc_kernel<D, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Layout<D>::kSmem);
-    if (e != cudaSuccess) return e;
-    done.fetch_or(bit, std::memory_order_acq_rel);
-  }
-  return launch_pdl(window_tc_kernel<D, DT>, dim3(grid), dim3(kThreads), Layout<D>::kSmem, stream,
-                    mq, mk, mv, p);
-}
-
-}  // namespace
-
-namespace {
-
-// What TMA asks of (rows, heads, dim) in 16 bits: a 16-byte aligned base,
-// strides that are multiples of 16 bytes, below 2^40, each a whole multiple of
-// the one before.
-bool tma_rows(const void* x, int64_t ld, int64_t ld_head, int heads, int dim) {
-  if (reinterpret_cast<uintptr_t>(x) % 16 != 0 || ld % 8 != 0 || ld >= (int64_t(1) << 38)) return false;
-  if (heads == 1) return ld >= dim && ld % dim == 0;
-  return ld_head % 8 == 0 && ld_head >= dim && ld > 0 && ld % ld_head == 0;
-}
-
-}  // namespace
-
 bool window_tc_takes(const dlrm_attention_t& a) {
-  if (a.dtype == DLRM_DTYPE_FP32 || !(a.scale > 0.f) || a.k_rows < 1) return false;
-  return reinterpret_cast<uintptr_t>(a.q) % 16 == 0 && a.ld_q % 8 == 0 &&
-         (a.n_heads == 1 || a.ld_q_head % 8 == 0) &&
+  return a.dtype != DLRM_DTYPE_FP32 && a.scale > 0.f && a.k_rows > 0 &&
+         vector_rows(a.q, a.ld_q, a.ld_q_head, a.n_heads) &&
          tma_rows(a.k, a.ld_k, a.ld_k_head, a.n_kv_heads, a.head_dim) &&
          tma_rows(a.v, a.ld_v, a.ld_v_head, a.n_kv_heads, a.head_dim);
 }
 
-cudaError_t launch_window_attention_tc(const dlrm_attention_t& a, cudaStream_t stream) {
+cudaError_t launch_window_attention_tc(const dlrm_attention_t& call, cudaStream_t stream) {
+  dlrm_attention_t a = call;
+  a.causal = 1;
   TcParams p{};
-  p.w.a = a;
-  p.w.group = a.n_heads / a.n_kv_heads;
-  p.w.vec = 1;
-  p.group = fast_div(p.w.group);
-  p.heads = fast_div(a.n_kv_heads);
-  p.vec_out = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.ld_out % 8 == 0 &&
-              (a.n_heads == 1 || a.ld_out_head % 8 == 0);
-  p.q_tma = 128 % p.w.group == 0 && tma_rows(a.q, a.ld_q, a.ld_q_head, a.n_heads, a.head_dim);
-  alignas(64) CUtensorMap mq, mk, mv;
-  const int box_q = p.q_tma ? 128 / p.w.group : 1;
-  if (!encode_rows(&mk, a.k, a.k_rows, a.n_kv_heads, a.head_dim, a.ld_k, a.ld_k_head, a.dtype, kBox, 1) ||
+  alignas(64) CUtensorMap mq{}, mk, mv;
+  if (!fill_params(p, mq, a) ||
+      !encode_rows(&mk, a.k, a.k_rows, a.n_kv_heads, a.head_dim, a.ld_k, a.ld_k_head, a.dtype, kBox, 1) ||
       !encode_rows(&mv, a.v, a.k_rows, a.n_kv_heads, a.head_dim, a.ld_v, a.ld_v_head, a.dtype, kBox, 1))
-    return cudaErrorInvalidValue;
-  if (!p.q_tma)
-    mq = mk;                                      // not read
-  else if (!encode_rows(&mq, a.q, a.q_rows, a.n_heads, a.head_dim, a.ld_q, a.ld_q_head, a.dtype,
-                        box_q, p.w.group))
     return cudaErrorInvalidValue;
   const int64_t units = (a.q_rows * p.w.group / kUnit + a.batch) * a.n_kv_heads;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(units, device_sm_count()));
   const bool bf16 = a.dtype == DLRM_DTYPE_BF16;
   if (a.head_dim == 32)
-    return bf16 ? launch<32, DLRM_DTYPE_BF16>(mq, mk, mv, p, grid, stream)
-                : launch<32, DLRM_DTYPE_FP16>(mq, mk, mv, p, grid, stream);
+    return bf16 ? launch_tc<32, DLRM_DTYPE_BF16, false>(mq, mk, mv, p, grid, stream)
+                : launch_tc<32, DLRM_DTYPE_FP16, false>(mq, mk, mv, p, grid, stream);
   if (a.head_dim == 64)
-    return bf16 ? launch<64, DLRM_DTYPE_BF16>(mq, mk, mv, p, grid, stream)
-                : launch<64, DLRM_DTYPE_FP16>(mq, mk, mv, p, grid, stream);
-  return bf16 ? launch<128, DLRM_DTYPE_BF16>(mq, mk, mv, p, grid, stream)
-              : launch<128, DLRM_DTYPE_FP16>(mq, mk, mv, p, grid, stream);
+    return bf16 ? launch_tc<64, DLRM_DTYPE_BF16, false>(mq, mk, mv, p, grid, stream)
+                : launch_tc<64, DLRM_DTYPE_FP16, false>(mq, mk, mv, p, grid, stream);
+  return bf16 ? launch_tc<128, DLRM_DTYPE_BF16, false>(mq, mk, mv, p, grid, stream)
+              : launch_tc<128, DLRM_DTYPE_FP16, false>(mq, mk, mv, p, grid, stream);
 }
 
 }  // namespace dlrm
