@@ -27,9 +27,10 @@
 //     over the reference in use (weights up to 2^8 are as exact, and the sum is
 //     fp32), which real scores do in the first tiles only. 32 columns that none
 //     of a warp's rows sees are neither read nor exponentiated.
-// Tensor memory: two score buffers of 64 columns a tile (weights over the
-// scores) and the output, up to 128 columns a tile. With two buffers the scores
-// of the next key tile are made while the softmax works on this one's.
+// Tensor memory: two score buffers of 64 columns a tile, two of weights (32) and
+// the output. The scores of the next key tile are made while the softmax works on
+// this one's. At head_dim 128 there is no room for the weights: they lie over
+// their scores, whose buffer is then only free when the weights have been used.
 //
 // PAGED: candidates of few users make few units, so the key tiles of all units
 // are cut evenly over the CTAs, as in history_attention.cu; a unit that is split
@@ -77,6 +78,14 @@ struct Layout {
   // takes all of the tensor memory
   static constexpr int kSmem = kBars + 1024 + 1024 > 120 * 1024 ? kBars + 1024 + 1024 : 120 * 1024;
   static_assert(kSmem <= 232448, "shared memory of one CTA");
+  // tensor memory columns: scores of tile t in buffer i, its weights, its output.
+  // At head_dim 128 scores and outputs fill it, and weights lie over their scores.
+  static constexpr bool kOver = D == 128;
+  static __device__ __forceinline__ int s_col(int t, int i) { return t * 128 + i * kKeys; }
+  static __device__ __forceinline__ int o_col(int t) { return 256 + t * (kOver ? 128 : 64); }
+  static __device__ __forceinline__ int p_col(int t, int i) {
+    return kOver ? s_col(t, i) : 384 + t * 64 + i * 32;
+  }
 };
 
 // n / d for 0 <= n < 2^31 by a multiplication: with s = ceil(log2 d) and
@@ -130,6 +139,7 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// Not inline: a copy at every wait costs instruction cache (batch 66 -> 80 us).
 // Bounded wait for a phase; false once this or another thread gave up.
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                        int32_t* err, uint64_t limit) {
@@ -217,6 +227,18 @@ __device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t at) {
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
         "=r"(r[14]), "=r"(r[15])
       : "r"(at));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, "
+      "%27, %28, %29, %30, %31, %32};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31])
+      : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
   asm volatile(
@@ -545,9 +567,11 @@ __device__ __noinline__ void paged_careful_row(const TcParams& p, const WindowSp
         sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
 }
 
-// The products of tile T of every unit, by one lane.
-template <int D, int DT, int T, bool PAGED>
-__device__ __forceinline__ void products(const TcParams& p, const CUtensorMap* map_q, Bars& bars,
+// The products of tile T of every unit, by one lane. T is no template argument:
+// one copy of the code for both tiles keeps more of the kernel in the instruction
+// cache (16384 events 265 -> 260 us, the ragged batch 66 -> 63).
+template <int D, int DT, bool PAGED>
+__device__ __forceinline__ void products(const int T, const TcParams& p, const CUtensorMap* map_q, Bars& bars,
                                          const Waiter& wait, unsigned char* base, uint32_t tmem) {
   using L = Layout<D>;
   constexpr int kFormat = DT == DLRM_DTYPE_BF16 ? 1 : 0;
@@ -557,7 +581,7 @@ __device__ __forceinline__ void products(const TcParams& p, const CUtensorMap* m
   const uint32_t q_desc = rows_desc(smem_addr(base + L::kQ + T * L::kQTile));
   const uint32_t k_desc = rows_desc(smem_addr(base + L::kK));
   const uint32_t v_desc = values_desc(smem_addr(base + L::kV));
-  const uint32_t s_base = tmem + T * 128, o = tmem + 256 + T * 128;
+  const uint32_t o = tmem + L::o_col(T);
   uint32_t kv = 0, it = 0, units_done = 0;       // key tiles of the CTA, of this tile; its units
   Units units{bars, wait};
   for (const Unit* x; (x = units.next()); units.done()) {
@@ -578,11 +602,12 @@ __device__ __forceinline__ void products(const TcParams& p, const CUtensorMap* m
       bool need = false, used = false;
       if (k < keys.tiles) {
         keys.tile(k, key0, n);
-        need = keys.needs<T>(key0, n);
-        used = need || keys.needs<1 - T>(key0, n);
+        const bool n0 = keys.needs<0>(key0, n), n1 = keys.needs<1>(key0, n);
+        need = T ? n1 : n0;
+        used = n0 || n1;
       }
       if (used) {
-        // scores of this tile, into the buffer that the weights before last lay in
+        // scores of this tile, into the buffer of the tile before last
         const uint32_t st = kv % kStages;
         bool ok = wait(&bars.k_full[st], (kv / kStages) & 1);
         // (queries in flight land before anything gives up)
@@ -592,14 +617,16 @@ __device__ __forceinline__ void products(const TcParams& p, const CUtensorMap* m
         }
         if (!ok) return;
         if (need) {
-          // products of different shapes are not ordered among themselves: those
-          // weights must have been used. (Product i completes phase i / 2 of
-          // barrier i % 2. Whoever waits for it knows that i - 2 is complete and
-          // that i + 2 is not issued, so the phase's parity says enough.)
-          if (it >= 2 && !wait(&bars.pv_done[T][it & 1], ((it - 2) >> 1) & 1)) return;
+          // the old scores have been read: their weights have arrived. Where those
+          // lie over them they must have been used too: products of different shapes
+          // are not ordered among themselves.
+          // (Product i completes phase i / 2 of barrier i % 2. Whoever waits for it
+          // knows that i - 2 is complete, by this wait or by the commit that scores
+          // i came with, and that i + 2 is not issued: the phase's parity says enough.)
+          if (L::kOver && it >= 2 && !wait(&bars.pv_done[T][it & 1], ((it - 2) >> 1) & 1)) return;
           fence_after();
           const uint32_t idesc = kIdescS | (n > 32 ? 8u << 17 : 4u << 17);
-          const uint32_t sa = s_base + (it & 1) * kKeys, kd = k_desc + st * (L::kTile >> 4);
+          const uint32_t sa = tmem + L::s_col(T, it & 1), kd = k_desc + st * (L::kTile >> 4);
 #pragma unroll
           for (int j = 0; j < D / 16; ++j)
             mma_ss(sa, q_desc + (((j / 4) * kQBlock + (j % 4) * 32) >> 4),
@@ -621,7 +648,7 @@ __device__ __forceinline__ void products(const TcParams& p, const CUtensorMap* m
           if (!begun && units_done > 0 && !wait(&bars.o_empty[T], (units_done - 1) & 1)) return;
           if (!wait(&bars.p_full[T][of & 1], (of >> 1) & 1)) return;
           fence_after();
-          const uint32_t vd = v_desc + st * (L::kTile >> 4), pa = s_base + (of & 1) * kKeys;
+          const uint32_t vd = v_desc + st * (L::kTile >> 4), pa = tmem + L::p_col(T, of & 1);
           mma_ts(o, pa, vd, kIdescO, begun ? 1u : 0u);
           mma_ts(o, pa + 8, vd + (2048 >> 4), kIdescO, 1u);
           if (due_width > 32) {
@@ -707,9 +734,13 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
   Units units{bars, wait};
   if (warp < 8) {
     // ------------------------------------------------------------ softmax
+    // all 64 scores of a row in registers, or 32 at a time, read twice: with 16 warps
+    // (PAGED) a thread has 128 registers, and the spills cost more (ranking 67 us
+    // against 61; with 12 warps the reverse, 270 against 265 at 16384 events)
+    constexpr bool kKeep = !PAGED;
     const int t = warp / 4;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t o_at = tmem + lanes + 256 + t * 128;
+    const uint32_t o_at = tmem + lanes + L::o_col(t);
     const float f = w.a.scale * kLog2e;
     uint32_t it = 0;                              // key tiles so far
     bool ok = true;
@@ -744,7 +775,8 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         int key0, n;
         keys.tile(k, key0, n);
         if (!(t ? keys.needs<1>(key0, n) : keys.needs<0>(key0, n))) continue;
-        const uint32_t s_at = tmem + lanes + t * 128 + (it & 1) * kKeys;
+        const uint32_t s_at = tmem + lanes + L::s_col(t, it & 1);
+        const uint32_t p_at = tmem + lanes + L::p_col(t, it & 1);
         ok = __all_sync(0xffffffffu, wait(&bars.s_full[t][it & 1], (it >> 1) & 1));
         if (!ok) break;
         fence_after();
@@ -791,52 +823,89 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         };
         // columns [0, 32) and [32, 64): skipped where none of the warp's rows
         // sees any, masked where some do not see all
-        uint32_t s[2][32];
-        bool some[2] = {true, true}, part[2] = {false, false};
+        uint32_t some = 3, part = 0;
         if (!__all_sync(0xffffffffu, n == kKeys && key0 + kKeys <= v.end &&
                                          (key0 >= v.gap1 || key0 + kKeys <= v.gap0))) {
-#pragma unroll
+          some = 0;
+#pragma unroll 1
           for (int c = 0; c < 2; ++c) {
             const int c0 = key0 + 32 * c, c1 = c0 + 32;
             const bool all = 32 * c + 32 <= n && c1 <= v.end && (c0 >= v.gap1 || c1 <= v.gap0);
             const bool none = 32 * c >= n || c0 >= v.end || (c0 >= v.gap0 && c1 <= v.gap1);
-            some[c] = __any_sync(0xffffffffu, !none);
-            part[c] = __any_sync(0xffffffffu, !all);
+            some |= __any_sync(0xffffffffu, !none) ? 1u << c : 0u;
+            part |= __any_sync(0xffffffffu, !all) ? 1u << c : 0u;
           }
         }
+        auto mask = [&](uint32_t (&s)[32], int c) {
+          const int e = min(n, v.end - key0) - 32 * c;
+          const uint32_t bits = low_bits(min(v.gap0 - key0 - 32 * c, e)) |
+                                (low_bits(e) & ~low_bits(v.gap1 - key0 - 32 * c));
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-          if (some[c]) tmem_ld32(s[c], s_at + 32 * c);
-        tmem_wait_ld();
+          for (int j = 0; j < 32; ++j)
+            if (!(bits & (1u << j))) s[j] = 0xff800000u;
+        };
         float big[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (kKeep) {
+          uint32_t s[2][32];
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-          if (some[c]) {
-            if (part[c]) {
-              const int e = min(n, v.end - key0) - 32 * c;
-              const uint32_t bits = low_bits(min(v.gap0 - key0 - 32 * c, e)) |
-                                    (low_bits(e) & ~low_bits(v.gap1 - key0 - 32 * c));
+          for (int c = 0; c < 2; ++c)
+            if (some & (1u << c)) tmem_ld32(s[c], s_at + 32 * c);
+          tmem_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!(bits & (1u << j))) s[c][j] = 0xff800000u;
+          for (int c = 0; c < 2; ++c)
+            if (some & (1u << c)) {
+              if (part & (1u << c)) mask(s[c], c);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) big[j & 3] = fmaxf(big[j & 3], __uint_as_float(s[c][j]));
             }
+          const float off = raise(fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * f);
+          if (!ok) break;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) big[j & 3] = fmaxf(big[j & 3], __uint_as_float(s[c][j]));
-          }
-        const float off = raise(fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * f);
-        if (!ok) break;
+          for (int c = 0; c < 2; ++c)
+            if (c == 0 || n > 32) {
+              uint32_t pw[16];
+              if (some & (1u << c)) {
+                weigh(pw, s[c], off);
+              } else {
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-          if (c == 0 || n > 32) {
-            uint32_t pw[16];
-            if (some[c]) {
-              weigh(pw, s[c], off);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) pw[j] = 0;
+                for (int j = 0; j < 16; ++j) pw[j] = 0;
+              }
+              tmem_st16(p_at + 16 * c, pw);       // over the scores, which are in registers
             }
-            tmem_st16(s_at + 16 * c, pw);         // over the scores, which are in registers
-          }
+        } else {
+          // masked scores go back to tensor memory: one masking for both readings
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c)
+            if (some & (1u << c)) {
+              uint32_t s[32];
+              tmem_ld32(s, s_at + 32 * c);
+              tmem_wait_ld();
+              if (part & (1u << c)) {
+                mask(s, c);
+                tmem_st32(s_at + 32 * c, s);
+              }
+#pragma unroll
+              for (int j = 0; j < 32; ++j) big[j & 3] = fmaxf(big[j & 3], __uint_as_float(s[j]));
+            }
+          const float off = raise(fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * f);
+          if (!ok) break;
+          if (part) tmem_wait_st();
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c)
+            if (c == 0 || n > 32) {
+              uint32_t pw[16];
+              if (some & (1u << c)) {
+                uint32_t s[32];
+                tmem_ld32(s, s_at + 32 * c);
+                tmem_wait_ld();
+                weigh(pw, s, off);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) pw[j] = 0;
+              }
+              tmem_st16(p_at + 16 * c, pw);       // over scores that have been read
+            }
+        }
         any = true;
         tmem_wait_st();
         fence_before();
@@ -970,10 +1039,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
     // ------------------------------------------------------------ products
     const int t = warp - 8;
     if (elect_one()) {
-      if (t == 0)
-        products<D, DT, 0, PAGED>(p, &map_q, bars, wait, base, tmem);
-      else
-        products<D, DT, 1, PAGED>(p, &map_q, bars, wait, base, tmem);
+      products<D, DT, PAGED>(t, p, &map_q, bars, wait, base, tmem);
       // nothing of the tensor core's may be in flight when its memory is freed
       mma_commit(smem_addr(&bars.drain[t]));
       wait.drain(&bars.drain[t], 0);
