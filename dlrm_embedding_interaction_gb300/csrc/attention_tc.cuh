@@ -65,7 +65,13 @@ constexpr int kBlockBytes = kKeys * 128;         // the same of a key tile
 constexpr int kStages = 4;                       // of keys, and of values
 constexpr float kSlack = 8.f;                    // log2 of the largest weight
 
-template <int D>
+// Resident CTAs of an SM, score buffers of a tile, tensor memory columns.
+template <int D, bool PAGED>
+constexpr int kCtas = D == 128 || PAGED ? 1 : 2;
+template <int D, bool PAGED>
+constexpr int kBufs = 3 - kCtas<D, PAGED>;
+
+template <int D, bool PAGED>
 struct Layout {
   static constexpr int kBlocks = (D + 63) / 64;  // 64-element column blocks
   static constexpr int kTile = kBlocks * kBlockBytes;
@@ -74,15 +80,22 @@ struct Layout {
   static constexpr int kK = 2 * kQTile;
   static constexpr int kV = kK + kStages * kTile;
   static constexpr int kBars = kV + kStages * kTile;
-  // more than half an SM's shared memory, so that one CTA is resident: it
-  // takes all of the tensor memory
-  static constexpr int kSmem = kBars + 1024 + 1024 > 120 * 1024 ? kBars + 1024 + 1024 : 120 * 1024;
-  static_assert(kSmem <= 232448, "shared memory of one CTA");
+  // a lone CTA takes all of the tensor memory, so it asks for more than half an
+  // SM's shared memory
+  static constexpr int kNeed = kBars + 1024 + 1024;
+  static constexpr bool kAlone = kCtas<D, PAGED> == 1;
+  static constexpr int kSmem = kAlone && kNeed < 120 * 1024 ? 120 * 1024 : kNeed;
+  static_assert(kSmem <= (kAlone ? 232448 : 115712), "shared memory of an SM");
   // tensor memory columns: scores of tile t in buffer i, its weights, its output.
-  // At head_dim 128 scores and outputs fill it, and weights lie over their scores.
-  static constexpr bool kOver = D == 128;
-  static __device__ __forceinline__ int s_col(int t, int i) { return t * 128 + i * kKeys; }
-  static __device__ __forceinline__ int o_col(int t) { return 256 + t * (kOver ? 128 : 64); }
+  // Where there is no room for the weights they lie over their scores: with two
+  // CTAs an SM, and at head_dim 128.
+  static constexpr int kB = kBufs<D, PAGED>;
+  static constexpr bool kOver = D == 128 || kB == 1;
+  static constexpr int kColumns = kB == 1 ? 256 : 512;
+  static __device__ __forceinline__ int s_col(int t, int i) { return (t * kB + i) * kKeys; }
+  static __device__ __forceinline__ int o_col(int t) {
+    return 2 * kB * kKeys + t * (D == 128 ? 128 : 64);
+  }
   static __device__ __forceinline__ int p_col(int t, int i) {
     return kOver ? s_col(t, i) : 384 + t * 64 + i * 32;
   }
@@ -573,7 +586,7 @@ __device__ __noinline__ void paged_careful_row(const TcParams& p, const WindowSp
 template <int D, int DT, bool PAGED>
 __device__ __forceinline__ void products(const int T, const TcParams& p, const CUtensorMap* map_q, Bars& bars,
                                          const Waiter& wait, unsigned char* base, uint32_t tmem) {
-  using L = Layout<D>;
+  using L = Layout<D, PAGED>;
   constexpr int kFormat = DT == DLRM_DTYPE_BF16 ? 1 : 0;
   // D fp32; A, B formats; M = 128; B of the second product is MN-major
   constexpr uint32_t kIdescS = (1u << 4) | (kFormat << 7) | (kFormat << 10) | (8u << 24);
@@ -595,7 +608,7 @@ __device__ __forceinline__ void products(const int T, const TcParams& p, const C
         tma_load_3d(smem_addr(base + L::kQ + T * L::kQTile + c * kQBlock), map_q, c * 64,
                     x->head * p.w.group, x->s.q0 + p.group(x->row0 + 128 * T), &bars.q_full[T]);
     }
-    bool due = false, begun = false, used_before = false;
+    bool due = false, begun = false, used_before = false, queried = false;
     int due_width = 0;
     for (int k = keys.begin; k <= keys.tiles; ++k) {
       int key0 = 0, n = 0;
@@ -606,62 +619,75 @@ __device__ __forceinline__ void products(const int T, const TcParams& p, const C
         need = T ? n1 : n0;
         used = n0 || n1;
       }
-      if (used) {
-        // scores of this tile, into the buffer of the tile before last
+      // scores of this tile, into the buffer of the tile before last (of the tile
+      // before, with one buffer)
+      auto scores = [&]() -> bool {
+        if (!used) return true;
         const uint32_t st = kv % kStages;
         bool ok = wait(&bars.k_full[st], (kv / kStages) & 1);
         // (queries in flight land before anything gives up)
-        if (need && !begun && !due) {
+        if (need && !queried) {
           if (ok) ok = wait(&bars.q_full[T], units_done & 1);
           if (!ok && p.q_tma) wait.drain(&bars.q_full[T], units_done & 1);
+          queried = true;
         }
-        if (!ok) return;
+        if (!ok) return false;
         if (need) {
           // the old scores have been read: their weights have arrived. Where those
           // lie over them they must have been used too: products of different shapes
           // are not ordered among themselves.
-          // (Product i completes phase i / 2 of barrier i % 2. Whoever waits for it
-          // knows that i - 2 is complete, by this wait or by the commit that scores
-          // i came with, and that i + 2 is not issued: the phase's parity says enough.)
-          if (L::kOver && it >= 2 && !wait(&bars.pv_done[T][it & 1], ((it - 2) >> 1) & 1)) return;
+          // (Product i completes phase i / kB of barrier i % kB. Whoever waits for it
+          // knows that i - kB is complete, by this wait or by the commit that scores
+          // i came with, and that i + kB is not issued: the phase's parity says enough.)
+          if (L::kOver && it >= L::kB &&
+              !wait(&bars.pv_done[T][it % L::kB], ((it - L::kB) / L::kB) & 1))
+            return false;
           fence_after();
           const uint32_t idesc = kIdescS | (n > 32 ? 8u << 17 : 4u << 17);
-          const uint32_t sa = tmem + L::s_col(T, it & 1), kd = k_desc + st * (L::kTile >> 4);
+          const uint32_t sa = tmem + L::s_col(T, it % L::kB), kd = k_desc + st * (L::kTile >> 4);
 #pragma unroll
           for (int j = 0; j < D / 16; ++j)
             mma_ss(sa, q_desc + (((j / 4) * kQBlock + (j % 4) * 32) >> 4),
                    kd + (((j / 4) * kBlockBytes + (j % 4) * 32) >> 4), idesc, j > 0 ? 1u : 0u);
-          mma_commit(smem_addr(&bars.s_full[T][it & 1]));
+          mma_commit(smem_addr(&bars.s_full[T][it % L::kB]));
           mma_commit(smem_addr(&bars.k_empty[st]));
-          ++it;
         } else {
           bar_arrive(&bars.k_empty[st]);
         }
-        ++kv;
-      }
-      if (used_before) {
-        // products with the values of the tile before
-        const uint32_t vi = kv - 1 - (used ? 1 : 0), st = vi % kStages;
-        if (!wait(&bars.v_full[st], (vi / kStages) & 1)) return;
+        return true;
+      };
+      // products with the values of the tile before
+      auto outputs = [&]() -> bool {
+        if (!used_before) return true;
+        const uint32_t vi = kv - 1, st = vi % kStages;
+        if (!wait(&bars.v_full[st], (vi / kStages) & 1)) return false;
         if (due) {
-          const uint32_t of = it - 1 - (need ? 1 : 0);
-          if (!begun && units_done > 0 && !wait(&bars.o_empty[T], (units_done - 1) & 1)) return;
-          if (!wait(&bars.p_full[T][of & 1], (of >> 1) & 1)) return;
+          const uint32_t of = it - 1;
+          if (!begun && units_done > 0 && !wait(&bars.o_empty[T], (units_done - 1) & 1)) return false;
+          if (!wait(&bars.p_full[T][of % L::kB], (of / L::kB) & 1)) return false;
           fence_after();
-          const uint32_t vd = v_desc + st * (L::kTile >> 4), pa = tmem + L::p_col(T, of & 1);
+          const uint32_t vd = v_desc + st * (L::kTile >> 4), pa = tmem + L::p_col(T, of % L::kB);
           mma_ts(o, pa, vd, kIdescO, begun ? 1u : 0u);
           mma_ts(o, pa + 8, vd + (2048 >> 4), kIdescO, 1u);
           if (due_width > 32) {
             mma_ts(o, pa + 16, vd + 2 * (2048 >> 4), kIdescO, 1u);
             mma_ts(o, pa + 24, vd + 3 * (2048 >> 4), kIdescO, 1u);
           }
-          mma_commit(smem_addr(&bars.pv_done[T][of & 1]));
+          mma_commit(smem_addr(&bars.pv_done[T][of % L::kB]));
           mma_commit(smem_addr(&bars.v_empty[st]));
           begun = true;
         } else {
           bar_arrive(&bars.v_empty[st]);
         }
+        return true;
+      };
+      if (L::kB == 1) {
+        if (!outputs() || !scores()) return;
+      } else {
+        if (!scores() || !outputs()) return;
       }
+      kv += used ? 1 : 0;
+      it += need ? 1 : 0;
       used_before = used;
       due = need;
       due_width = n;
@@ -671,10 +697,10 @@ __device__ __forceinline__ void products(const int T, const TcParams& p, const C
 }
 
 template <int D, int DT, bool PAGED>
-__global__ void __launch_bounds__(kThreadsOf<PAGED>, 1)
+__global__ void __launch_bounds__(kThreadsOf<PAGED>, kCtas<D, PAGED>)
 attention_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                  const __grid_constant__ CUtensorMap map_v, const __grid_constant__ TcParams p) {
-  using L = Layout<D>;
+  using L = Layout<D, PAGED>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -686,7 +712,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
   if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(&bars.tmem)),
-                 "n"(512)
+                 "n"(L::kColumns)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -737,7 +763,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
     // all 64 scores of a row in registers, or 32 at a time, read twice: with 16 warps
     // (PAGED) a thread has 128 registers, and the spills cost more (ranking 67 us
     // against 61; with 12 warps the reverse, 270 against 265 at 16384 events)
-    constexpr bool kKeep = !PAGED;
+    constexpr bool kKeep = !PAGED && L::kB == 2;
     const int t = warp / 4;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t o_at = tmem + lanes + L::o_col(t);
@@ -775,9 +801,9 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         int key0, n;
         keys.tile(k, key0, n);
         if (!(t ? keys.needs<1>(key0, n) : keys.needs<0>(key0, n))) continue;
-        const uint32_t s_at = tmem + lanes + L::s_col(t, it & 1);
-        const uint32_t p_at = tmem + lanes + L::p_col(t, it & 1);
-        ok = __all_sync(0xffffffffu, wait(&bars.s_full[t][it & 1], (it >> 1) & 1));
+        const uint32_t s_at = tmem + lanes + L::s_col(t, it % L::kB);
+        const uint32_t p_at = tmem + lanes + L::p_col(t, it % L::kB);
+        ok = __all_sync(0xffffffffu, wait(&bars.s_full[t][it % L::kB], (it / L::kB) & 1));
         if (!ok) break;
         fence_after();
         // a running maximum m (times f) of scores not seen before: keeps the
@@ -792,7 +818,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
               // the product before this tile's must be complete; the one before
               // that is (its weights lay where these scores are)
               ok = __all_sync(0xffffffffu,
-                              wait(&bars.pv_done[t][(it - 1) & 1], ((it - 1) >> 1) & 1));
+                              wait(&bars.pv_done[t][(it - 1) % L::kB], ((it - 1) / L::kB) & 1));
               fence_after();
 #pragma unroll 1
               for (int c = 0; c < D; c += 16) {
@@ -910,14 +936,14 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         tmem_wait_st();
         fence_before();
         __syncwarp();
-        if (lane == 0) bar_arrive(&bars.p_full[t][it & 1]);
+        if (lane == 0) bar_arrive(&bars.p_full[t][it % L::kB]);
         ++it;
       }
       if (!ok) break;
       // ---- output
       if (any) {
         // the last product, and with it all before it
-        ok = __all_sync(0xffffffffu, wait(&bars.pv_done[t][(it - 1) & 1], ((it - 1) >> 1) & 1));
+        ok = __all_sync(0xffffffffu, wait(&bars.pv_done[t][(it - 1) % L::kB], ((it - 1) / L::kB) & 1));
         if (!ok) break;
         fence_after();
       }
@@ -1251,7 +1277,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
   __syncthreads();
   if (warp == 8) {
     fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(L::kColumns)
                  : "memory");
   }
 }
@@ -1330,11 +1356,11 @@ cudaError_t launch_tc(const CUtensorMap& mq, const CUtensorMap& mk, const CUtens
   const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
   if (!bit || !(done.load(std::memory_order_acquire) & bit)) {
     e = cudaFuncSetAttribute(attention_tc_kernel<D, DT, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Layout<D>::kSmem);
+                             Layout<D, PAGED>::kSmem);
     if (e != cudaSuccess) return e;
     done.fetch_or(bit, std::memory_order_acq_rel);
   }
-  return launch_pdl(attention_tc_kernel<D, DT, PAGED>, dim3(grid), dim3(kThreadsOf<PAGED>), Layout<D>::kSmem, stream,
+  return launch_pdl(attention_tc_kernel<D, DT, PAGED>, dim3(grid), dim3(kThreadsOf<PAGED>), Layout<D, PAGED>::kSmem, stream,
                     mq, mk, mv, p);
 }
 
