@@ -124,15 +124,16 @@ __device__ __forceinline__ void locate(int batch, const F& units, int64_t target
 }
 
 // Cuts a batch's units evenly over the CTAs: request b has units(span(b)) >= 0
-// of them, fewer than 2^31 in all. CTA c of min(gridDim.x, total) takes
-// [cut(c), cut(c + 1)). Block-wide; the spans and first units of the requests
+// of them, fewer than 2^31 in all, in pieces(span) pieces. CTA c of up to
+// gridDim.x takes [cut(c), cut(c + 1)): `least` units at least, or about a piece,
+// because a piece that is cut in many parts takes long to join. Block-wide; the spans and first units of the requests
 // that hold both cuts come back in shared memory (the last request's where the
 // cut is the total).
 struct Cuts {
   int total, ctas, each, extra;                  // the first `extra` CTAs take each + 1
-  __device__ __forceinline__ void set(int n) {
+  __device__ __forceinline__ void set(int n, int pieces, int least) {
     total = n;
-    ctas = min(static_cast<int>(gridDim.x), n);
+    ctas = min(static_cast<int>(gridDim.x), min(n, max(n / least, pieces)));
     each = ctas > 0 ? n / ctas : 0;
     extra = n - each * ctas;
   }
@@ -150,36 +151,43 @@ struct Found {
   int request[2], first[2];
   Span span[2];
 };
-template <int THREADS, class Span, class S, class U>
-__device__ __forceinline__ Cuts locate_cuts(int batch, const S& span, const U& units, int* sums,
-                                            Found<Span>& found) {
+// sums: two ints a warp.
+template <int THREADS, class Span, class S, class U, class P>
+__device__ __forceinline__ Cuts locate_cuts(int batch, int least, const S& span, const U& units,
+                                            const P& pieces, int* sums, Found<Span>& found) {
   const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
   constexpr int kWarps = THREADS / kWarp;
   const int per = (batch + THREADS - 1) / THREADS;
   const int b0 = min(batch, static_cast<int>(threadIdx.x) * per), b1 = min(batch, b0 + per);
-  int mine = 0;
+  int mine = 0, parts = 0;
   Span s{};
   for (int b = b0; b < b1; ++b) {
     s = span(b);
     mine += units(s);
+    parts += pieces(s);
   }
+  parts = __reduce_add_sync(0xffffffffu, parts);
   int inc = mine;
 #pragma unroll
   for (int d = 1; d < kWarp; d *= 2) {
     const int v = __shfl_up_sync(0xffffffffu, inc, d);
     if (lane >= d) inc += v;
   }
-  if (lane == kWarp - 1) sums[warp] = inc;
+  if (lane == kWarp - 1) {
+    sums[warp] = inc;
+    sums[kWarps + warp] = parts;
+  }
   __syncthreads();
-  int at = inc - mine, total = 0;
+  int at = inc - mine, total = 0, all = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     const int x = sums[w];
     at += w < warp ? x : 0;
     total += x;
+    all += sums[kWarps + w];
   }
   Cuts cuts;
-  cuts.set(total);
+  cuts.set(total, all, least);
   for (int i = 0; i < 2; ++i) {
     const int target = min(cuts.cut(blockIdx.x + i), total - 1);
     if (target < at || target >= at + mine) continue;

@@ -514,8 +514,10 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // PAGED: key tiles that the rows of a request see, one at least: what a unit
-// counts when the work is cut. Units of up to kWhole are not split.
-constexpr int kWhole = 8;
+// counts when the work is cut. Units of up to kWhole are not split, and of longer
+// ones a CTA takes kLeast at least: one user x 4096 events x 128 rows takes 31 us in
+// parts of 16 key tiles, 121 in parts of one.
+constexpr int kWhole = 8, kLeast = 16;
 __device__ __forceinline__ int key_tiles(const TcParams& p, const WindowSpan& s) {
   const dlrm_attention_t& a = p.w.a;
   const int queries = p.group(s.rows);
@@ -750,12 +752,13 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
   // PAGED: this CTA's part [begin, end) of all units' key tiles. A request's
   // units count as if each had all the key tiles that any of its rows sees.
   __shared__ Found<WindowSpan> found;
-  __shared__ int sums[kThreadsOf<PAGED> / kWarp];
+  __shared__ int sums[kThreadsOf<PAGED> / kWarp * 2];
   Cuts cuts{};
   if (PAGED)
     cuts = locate_cuts<kThreadsOf<PAGED>>(
-        w.a.batch, [&](int i) { return tc_span<PAGED>(p, i, false); },
-        [&](const WindowSpan& s) { return s.tiles * w.a.n_kv_heads * key_tiles(p, s); }, sums, found);
+        w.a.batch, kLeast, [&](int i) { return tc_span<PAGED>(p, i, false); },
+        [&](const WindowSpan& s) { return s.tiles * w.a.n_kv_heads * key_tiles(p, s); },
+        [&](const WindowSpan& s) { return s.tiles * w.a.n_kv_heads; }, sums, found);
 
   Units units{bars, wait};
   if (warp < 8) {
