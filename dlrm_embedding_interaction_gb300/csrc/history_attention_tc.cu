@@ -1,16 +1,27 @@
 // history_attention on the tensor cores: bf16 queries, many rows a request
 // (attention_tc.cuh; history_attention.cu takes every other call).
+//
+// What bounds it: as in window_attention_tc.cu, the softmax warps; and with few
+// units the time of one key tile after another.
 #include "attention_tc.cuh"
 
 namespace dlrm {
 
-// Rows of a request and kv head, on average, from which this kernel is taken.
-constexpr int kManyRows = 64;
+// From this many rows of a request and kv head on average, and of all together,
+// this kernel is faster than history_attention.cu's. us at head_dim 64 (128), two
+// kv heads, this kernel against that one:
+//   64 users x 1024 events, 64 rows each: 25 against 31 (40 against 53);
+//     32 rows: 25 against 25 (40 against 34)
+//   16 users x 4096 events, 128 rows: 34 against 41 (52 against 62);
+//     64 rows (2048 in all): 34 against 30 (51 against 44)
+//   1 user x 4096 events, 1024 rows (2048 in all): 36 against 30 (54 against 44)
+constexpr int kManyRows = 64, kManyInAll = 4096;
 
 bool history_tc_takes(const dlrm_history_t& h, const dlrm_attention_t& a) {
+  const int64_t rows = a.q_rows * (a.n_heads / h.n_heads);
   return a.dtype == DLRM_DTYPE_BF16 && a.scale > 0.f &&
          vector_rows(a.q, a.ld_q, a.ld_q_head, a.n_heads) &&
-         a.q_rows * (a.n_heads / h.n_heads) >= static_cast<int64_t>(a.batch) * kManyRows;
+         rows >= static_cast<int64_t>(a.batch) * kManyRows && rows * h.n_heads >= kManyInAll;
 }
 
 cudaError_t launch_history_attention_tc(const dlrm_history_t& h, const dlrm_attention_t& call,

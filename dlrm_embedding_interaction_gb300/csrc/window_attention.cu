@@ -23,6 +23,13 @@ constexpr int kBlock = 32;
 constexpr int kTileRows = kWarps * 16;
 using Params = WindowParams;
 
+// x as a tf32 head and rest, each rounded to nearest: 22 bits of x in all. (The
+// MMA cuts its operands off, which would leave a bias.)
+__device__ __forceinline__ void split_tf32(uint32_t x, uint32_t& head, uint32_t& rest) {
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(head) : "f"(__uint_as_float(x)));
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(rest) : "f"(__uint_as_float(x) - __uint_as_float(head)));
+}
+
 // N consecutive 32-bit words at a byte address, 16 bytes at a time if aligned.
 template <int N, bool HALF>
 __device__ __forceinline__ void load_row_words(uint32_t* w, const uint8_t* p, bool vec) {
@@ -141,13 +148,10 @@ __global__ void __launch_bounds__(kThreads) window_attention_kernel(const Params
         for (int w = 0; w < KW; w += 2) {
           uint32_t a[4] = {qw[0][w], qw[1][w], qw[0][w + 1], qw[1][w + 1]}, hi[4], lo[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            hi[i] = a[i] & 0xffffe000u;
-            lo[i] = __float_as_uint(__uint_as_float(a[i]) - __uint_as_float(hi[i]));
-          }
-          const uint32_t h0 = kw[w] & 0xffffe000u, h1 = kw[w + 1] & 0xffffe000u;
-          const uint32_t l0 = __float_as_uint(__uint_as_float(kw[w]) - __uint_as_float(h0));
-          const uint32_t l1 = __float_as_uint(__uint_as_float(kw[w + 1]) - __uint_as_float(h1));
+          for (int i = 0; i < 4; ++i) split_tf32(a[i], hi[i], lo[i]);
+          uint32_t h0, h1, l0, l1;
+          split_tf32(kw[w], h0, l0);
+          split_tf32(kw[w + 1], h1, l1);
           mma_tf32(sc[j], lo, h0, h1);
           mma_tf32(sc[j], hi, l0, l1);
           mma_tf32(sc[j], hi, h0, h1);
@@ -231,14 +235,13 @@ __global__ void __launch_bounds__(kThreads) window_attention_kernel(const Params
         const float pr[4] = {sc[j][0], sc[j][2], sc[j][1], sc[j][3]};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          hi[i] = __float_as_uint(pr[i]) & 0xffffe000u;
-          lo[i] = __float_as_uint(pr[i] - __uint_as_float(hi[i]));
+          split_tf32(__float_as_uint(pr[i]), hi[i], lo[i]);
         }
 #pragma unroll
         for (int w = 0; w < VW; ++w) {
-          const uint32_t h0 = vw[0][w] & 0xffffe000u, h1 = vw[1][w] & 0xffffe000u;
-          const uint32_t l0 = __float_as_uint(__uint_as_float(vw[0][w]) - __uint_as_float(h0));
-          const uint32_t l1 = __float_as_uint(__uint_as_float(vw[1][w]) - __uint_as_float(h1));
+          uint32_t h0, h1, l0, l1;
+          split_tf32(vw[0][w], h0, l0);
+          split_tf32(vw[1][w], h1, l1);
           mma_tf32(o[w], lo, h0, h1);
           mma_tf32(o[w], hi, l0, l1);
           mma_tf32(o[w], hi, h0, h1);

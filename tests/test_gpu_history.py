@@ -10,7 +10,9 @@ scores of magnitude <= S (in units of the softmax's exponent):
   fp16 / bf16 over a cache: weights carry 11 bits, relative error 2^-12 each,
     so at most 2^-11 V in all with the scores' part, and half an ulp of the
     output type, which is finfo.eps / 2 of it.
-  bf16 over plain rows: weights carry 8 bits: 2^-8 V.
+  bf16 over plain rows, and over a cache on the tensor-core kernel (64 rows a
+    request and 4096 in all): weights carry 8 bits, relative error 2^-9 each: with
+    the scores' part at most 2^-8 V.
 """
 import numpy as np
 import pytest
@@ -278,6 +280,7 @@ def test_many_requests_in_one_call():
 
 def check_attention(cache, pool, rng, slots, counts, heads, dtype, causal, window, sinks, *,
                     q=None, scale=None, lse=True, out=None):
+    """Against the bounds above."""
     at = starts_of(counts)
     dim = pool.codes[0].shape[3]
     if q is None:
@@ -286,7 +289,10 @@ def check_attention(cache, pool, rng, slots, counts, heads, dtype, causal, windo
     got = dl.history_attention(cache, i32(slots), i32(at), q, out, scale=scale, causal=causal,
                                window=window, sinks=sinks, lse=sums)
     scale = dim ** -0.5 if scale is None else scale
-    eps, half = {"fp32": 2.0 ** -16, "fp16": 2.0 ** -11, "bf16": 2.0 ** -11}[dtype], half_ulp(dtype)
+    all_rows = at[-1] * (heads // pool.codes[0].shape[1])
+    many = all_rows >= 64 * len(slots) and at[-1] * heads >= 4096
+    eps = {"fp32": 2.0 ** -16, "fp16": 2.0 ** -11, "bf16": 2.0 ** -8 if many else 2.0 ** -11}[dtype]
+    half = half_ulp(dtype)
     for b, s in enumerate(slots):
         k, v = pool.events(s)
         want, sums_want = ref.attention(f64(q[at[b]:at[b + 1]]), k, v, scale, causal, window, sinks)
@@ -339,6 +345,64 @@ def test_candidates_of_several_users():
     for dtype in TYPES:
         check_attention(cache, pool, rng, [2, 0, 3, 1], [9, 130, 77, 200], 4, dtype, False, 0, 0)
         check_attention(cache, pool, rng, [2, 0, 3, 1], [1, 300, 150, 64], 4, dtype, True, 50, 5)
+
+
+# Enough rows for the tensor-core kernel (bf16, 64 a request and 4096 in all);
+# the longest histories are split between CTAs, and 3 heads of a group do not
+# divide a tile of 128 rows.
+MANY = [(64, 64, 2, 2, [3000, 700, 0, 65], [600, 300, 5, 200]),
+        (128, 128, 1, 3, [2500, 40], [900, 500]),
+        (32, 32, 1, 4, [1111, 1999, 8], [700, 400, 20])]
+
+
+@pytest.mark.parametrize("dim,page,kv,group,lens,counts", MANY)
+@pytest.mark.parametrize("causal,window,sinks", [(False, 0, 0), (True, 0, 0), (True, 300, 5),
+                                                 (False, 100, 33), (True, 1, 0)])
+def test_many_candidates(dim, page, kv, group, lens, counts, causal, window, sinks):
+    rng = np.random.default_rng(26)
+    cache, pool = make(2 + sum(-(-n // page) for n in lens), len(lens), -(-max(lens) // page), kv, dim, page)
+    fill(cache, pool, rng, list(range(len(lens))), lens)
+    slots = list(range(len(lens)))[::-1]
+    a = check_attention(cache, pool, rng, slots, counts[::-1], kv * group, "bf16", causal, window, sinks)
+    assert torch.isfinite(a).all() and cache.error() == dl.OK
+
+
+def test_many_candidates_into_strided_outputs_and_the_same_each_time():
+    rng = np.random.default_rng(27)
+    cache, pool = make(60, 2, 50, 2, 64, 64)
+    fill(cache, pool, rng, [0, 1], [3000, 500])
+    out = torch.zeros(8, 700, 70, dtype=torch.bfloat16, device="cuda").transpose(0, 1)[:, :, 3:67]
+    q = rows(rng, 700, 8, 64, "bf16", 0.3)
+    check_attention(cache, pool, rng, [0, 1], [400, 300], 8, "bf16", False, 0, 0, q=q, out=out)
+    # launches one after another, nothing between them
+    at = i32([0, 400, 700])
+    outs = [dl.history_attention(cache, i32([0, 1]), at, q) for _ in range(100)]
+    assert cache.error() == dl.OK
+    assert all(torch.equal(x, out) for x in outs)
+
+
+def test_many_candidates_over_nan_stale_codes_and_trimmed_pages():
+    rng = np.random.default_rng(28)
+    cache, pool = make(40, 2, 30, 1, 64, 64)
+    fill(cache, pool, rng, [0, 1], [1000, 1290])
+    for slot, n in ((0, 1000), (1, 1290)):          # codes past the end
+        for c in (cache.k_codes, cache.v_codes):
+            c.view(torch.uint8)[int(cache.table[slot, n // 64]), :, n % 64:] = 0x7f
+    x = rows(rng, 10, 1, 64, "fp32")
+    x[4] = float("nan")                             # event 1004 of slot 0
+    dl.history_append(cache, i32([0]), i32([0, 10]), x, x)
+    pool.append([0], [0, 10], (f64(x), f64(x)))
+    q = rows(rng, 1200, 4, 64, "bf16", 0.3)
+    got = check_attention(cache, pool, rng, [0, 1], [600, 600], 4, "bf16", True, 0, 0, q=q)
+    assert torch.isfinite(got[:594]).all() and torch.isnan(got[594:600]).all() and torch.isfinite(got[600:]).all()
+    dl.history_trim(cache, i32([1]), 200, 3)
+    assert (cache.table[1] == -1).sum() > 9
+    want = dl.history_attention(cache, i32([1]), i32([0, 5]), q[:5], window=200, sinks=3)
+    got = dl.history_attention(cache, i32([1]), i32([0, 1200]), q, window=200, sinks=3)
+    assert cache.error() == dl.OK
+    assert (got[:5].float() - want.float()).abs().max() < 2.0 ** -7 * want.abs().max().item()
+    dl.history_attention(cache, i32([1]), i32([0, 1200]), q)   # needs what was trimmed
+    assert cache.error() == dl.ERR_INDEX_OOB
 
 
 def test_scales_that_differ_between_pages_by_millions():
@@ -559,6 +623,22 @@ def test_window_attention_keeps_masked_infinities_out(dtype):
     got = check_window(rng, [120, 80], [120, 80], 2, 2, 64, dtype, 20, 2, qkv=(q, k, v))
     assert torch.isfinite(got[:60]).all() and torch.isfinite(got[80:100]).all()
     assert torch.isinf(got[150:170, 0, 5]).all() and torch.isfinite(got[170:]).all()
+
+
+@pytest.mark.parametrize("dim", [32, 64, 128])
+def test_window_attention_launches_one_after_another(dim):
+    """Many launches with nothing between them, on units of one key tile and of many."""
+    rng = np.random.default_rng(29)
+    counts = [1, 700, 64, 3, 1500, 65, 128, 0, 260]
+    n = sum(counts)
+    q, k, v = (rows(rng, n, h, dim, "bf16", 0.3) for h in (4, 2, 2))
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    at = i32(starts_of(counts))
+    for window in (0, 100):
+        want = check_window(rng, counts, counts, 4, 2, dim, "bf16", window, 3, qkv=(q, k, v))
+        outs = [dl.window_attention(q, k, v, at, window=window, sinks=3, err_flag=err) for _ in range(100)]
+        assert err.item() == 0
+        assert all(torch.equal(x, want) for x in outs)
 
 
 def test_window_attention_flags_bad_starts():
