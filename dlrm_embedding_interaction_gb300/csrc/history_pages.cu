@@ -341,130 +341,180 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(Pool p, int pieces) 
 
 // ------------------------------------------------------------------ append
 
-constexpr int kWriteThreads = 128;
+constexpr int kWriteThreads = 256;   // at most: 128 where that holds a page's rows
+constexpr int kHold = 8;             // chunks of eight elements that a thread holds
 
-// Eight consecutive elements as fp32.
+// Eight consecutive elements, as they are. VEC: at a 16-byte boundary.
 template <int DT, bool VEC>
-__device__ __forceinline__ void load8(float (&f)[8], const void* x, int64_t at) {
-  if (!VEC) {
+__device__ __forceinline__ void load8(uint32_t* w, const void* x, int64_t at) {
+  if (!VEC && DT == DLRM_DTYPE_FP32) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = load_element<DT>(x, at + i);
-  } else if (DT == DLRM_DTYPE_FP32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
-    const float4 a = __ldg(p), b = __ldg(p + 1);
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-    f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    for (int i = 0; i < 8; ++i) w[i] = __ldg(static_cast<const uint32_t*>(x) + at + i);
+  } else if (!VEC) {
+    const uint16_t* p = static_cast<const uint16_t*>(x) + at;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = static_cast<uint32_t>(__ldg(p + 2 * i)) | static_cast<uint32_t>(__ldg(p + 2 * i + 1)) << 16;
   } else {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (DT == DLRM_DTYPE_BF16) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      } else {
-        const float2 h = f16x2_to_float2(w[i]);
-        f[2 * i] = h.x;
-        f[2 * i + 1] = h.y;
-      }
+    for (int i = 0; i < (DT == DLRM_DTYPE_FP32 ? 2 : 1); ++i) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(
+          static_cast<const char*>(x) + at * (DT == DLRM_DTYPE_FP32 ? 4 : 2)) + i);
+      w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
     }
   }
 }
 
-// Quantises the new events of one page, head and side per iteration, eight
-// elements a thread and step. The scale needs the largest magnitude first, so
-// the new rows are read twice, the second time from L1: a page's rows of one
-// head are at most 64 KB. Where the page already holds events and its scale
-// grows, their codes are re-rounded: exact but for codes that become subnormal,
-// as scales are powers of two.
-// VEC: rows at 16-byte boundaries.
+// Elements 2 i and 2 i + 1 of a chunk as fp32.
+template <int DT>
+__device__ __forceinline__ float2 pair_of(const uint32_t* w, int i) {
+  if (DT == DLRM_DTYPE_FP32)
+    return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+  if (DT == DLRM_DTYPE_BF16)
+    return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  return f16x2_to_float2(w[i]);
+}
+
+// Quantises the new events of one page, head and side per iteration. The scale
+// needs the largest magnitude before the first code, so the rows stay in
+// registers in between: at most kHold chunks a thread, all under way at once.
+// Magnitudes compare as unsigned integers, two 16-bit ones an instruction; only
+// where the largest is no number does a second look leave out what is not
+// finite. Where the page already holds events and its scale grows, their codes
+// are re-rounded: exact but for codes that become subnormal, as scales are
+// powers of two. What an item is takes a chain of four loads: the CTA's next
+// items are looked up together, a thread each.
 template <int DT, int D, bool VEC>
-__global__ void __launch_bounds__(kWriteThreads)
+__global__ void __launch_bounds__(kWriteThreads, 2)
 append_kernel(Pool p, const int32_t* starts, const void* k, int64_t ld_k, int64_t ld_k_head,
               const void* v, int64_t ld_v, int64_t ld_v_head) {
-  __shared__ uint32_t top[kWriteThreads / kWarp];
+  __shared__ uint32_t top[2][kWriteThreads / kWarp];
+  __shared__ int4 todo[kWriteThreads];            // page, first and last new event, row of event 0
   constexpr int kChunks = D / 8;                  // of a row
+  constexpr int kWords = DT == DLRM_DTYPE_FP32 ? 8 : 4;
   const dlrm_history_t& h = p.h;
-  const int G = h.page_tokens, H = h.n_heads;
+  const int G = h.page_tokens, H = h.n_heads, T = blockDim.x, t = threadIdx.x;
   pdl_wait();
   pdl_trigger();
   const int64_t n = static_cast<int64_t>(p.head[kHeadItems]) * H * 2;
-  for (int64_t w = blockIdx.x; w < n; w += gridDim.x) {
-    // sides fastest, then heads: neighbouring CTAs read neighbouring rows
-    const int which = static_cast<int>(w / (2 * H)), rest = static_cast<int>(w - int64_t(which) * 2 * H);
-    const int side = rest >= H ? 1 : 0, head = rest - side * H;
-    const int2 item = p.items[which];
-    const Request r = p.request[item.x];
-    // the page there already, or one that the plan granted; one of the item's
-    // workers writes it down, one of the last item's the new length
-    int32_t* entry = h.table + static_cast<int64_t>(r.slot) * h.max_pages + item.y;
-    const int had = (r.length + G - 1) / G;
-    const bool fresh = item.y >= had;
-    const int page = fresh ? granted(p, r, p.head[kHeadTop], item.y - had) : *entry;
-    if (rest == 0 && threadIdx.x == 0) {
-      if (fresh) {
-        *entry = page;
-        h.refs[page] = 1;
+  int left = 0;                                   // entries of `todo` from `at` on
+  int at = 0, turn = 0;                           // `top` by turns: one barrier an item
+  for (int64_t w = blockIdx.x; w < n; w += gridDim.x, ++at, --left) {
+    if (left == 0) {
+      left = T;
+      at = 0;
+      const int64_t w_of = w + static_cast<int64_t>(t) * gridDim.x;
+      __syncthreads();                            // `todo` is read
+      if (w_of < n) {
+        const int which = static_cast<int>(w_of / (2 * H));
+        const int2 item = p.items[which];         // request, page of the history
+        const Request r = p.request[item.x];
+        // the page there already, or one that the plan granted; one of the item's
+        // workers writes it down, one of the last item's the new length
+        int32_t* entry = h.table + static_cast<int64_t>(r.slot) * h.max_pages + item.y;
+        const int had = (r.length + G - 1) / G;
+        const bool fresh = item.y >= had;
+        int page = fresh ? granted(p, r, p.head[kHeadTop], item.y - had) : *entry;
+        if (page < 0 || page >= h.n_pages) {      // a broken table: a last page that is not full is never trimmed
+          flag(h.err, DLRM_ERRBIT_INDEX_OOB);
+          page = -1;
+        }
+        if (w_of == static_cast<int64_t>(which) * 2 * H) {
+          if (fresh && page >= 0) {
+            *entry = page;
+            h.refs[page] = 1;
+          }
+          if (which + 1 == r.item0 + r.items) h.lengths[r.slot] = r.length + r.count;
+        }
+        const int64_t first = static_cast<int64_t>(item.y) * G;   // the page's first event
+        todo[t] = make_int4(page, static_cast<int>(max(r.length - first, int64_t(0))),
+                            static_cast<int>(min(int64_t(r.length) + r.count - first, int64_t(G))),
+                            static_cast<int>(starts[item.x] + first - r.length));
       }
-      if (which + 1 == r.item0 + r.items) h.lengths[r.slot] = r.length + r.count;
+      __syncthreads();
     }
-    if (page < 0 || page >= h.n_pages) {   // a broken table: a last page that is not full is never trimmed
-      flag(h.err, DLRM_ERRBIT_INDEX_OOB);
-      continue;
-    }
-    const int64_t first = static_cast<int64_t>(item.y) * G;     // the page's first event
-    const int kept = static_cast<int>(max(r.length - first, int64_t(0)));   // events there already
-    const int end = static_cast<int>(min(int64_t(r.length) + r.count - first, int64_t(G)));
+    const int4 item = todo[at];
+    const int page = item.x;
+    if (page < 0) continue;
+    // heads fastest, then sides: neighbouring CTAs read neighbouring rows
+    const int rest = static_cast<int>(w % (2 * H));
+    const int side = rest >= H ? 1 : 0, head = rest - side * H;
     const void* x = side ? v : k;
     const int64_t ld = side ? ld_v : ld_k;
-    const int64_t x0 = (starts[item.x] + first - r.length) * ld + head * (side ? ld_v_head : ld_k_head);
+    const int64_t x0 = item.w * ld + head * (side ? ld_v_head : ld_k_head);
     const int64_t place = static_cast<int64_t>(page) * H + head;
     uint8_t* codes = (side ? h.v_codes : h.k_codes) + place * G * D;
     float* scale = (side ? h.v_scales : h.k_scales) + place;
 
-    uint32_t big = 0;
-#pragma unroll 4
-    for (int e = kept * kChunks + threadIdx.x; e < end * kChunks; e += kWriteThreads) {
-      float f[8];
-      load8<DT, VEC>(f, x, x0 + (e / kChunks) * ld + e % kChunks * 8);
+    const int kept = item.y;                      // events there already
+    const int e0 = kept * kChunks + t, e1 = item.z * kChunks;
+    uint32_t f[kHold][kWords];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t u = __float_as_uint(f[i]) & 0x7fffffffu;
-        big = u < 0x7f800000u ? max(big, u) : big;
+    for (int i = 0; i < kHold; ++i) {
+      const int e = e0 + i * T;
+      if (e < e1) {
+        load8<DT, VEC>(f[i], x, x0 + (e / kChunks) * ld + e % kChunks * 8);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) f[i][j] = 0;
       }
     }
-    big = __reduce_max_sync(0xffffffffu, big);
-    __syncthreads();                                            // `top` of the item before is read
-    if (threadIdx.x % kWarp == 0) top[threadIdx.x / kWarp] = big;
-    __syncthreads();
+    uint32_t big = 0;
 #pragma unroll
-    for (int i = 0; i < kWriteThreads / kWarp; ++i) big = max(big, top[i]);
+    for (int i = 0; i < kHold; ++i)
+#pragma unroll
+      for (int j = 0; j < kWords; ++j)
+        big = DT == DLRM_DTYPE_FP32 ? max(big, f[i][j] & 0x7fffffffu) : __vmaxu2(big, f[i][j] & 0x7fff7fffu);
+    if (DT != DLRM_DTYPE_FP32) {
+      big = max(big >> 16, big & 0xffffu);
+      big = DT == DLRM_DTYPE_BF16 ? big << 16 : __float_as_uint(f16x2_to_float2(big).x);
+    }
+    if (big >= 0x7f800000u) {
+      big = 0;
+#pragma unroll
+      for (int i = 0; i < kHold; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 x2 = pair_of<DT>(f[i], j);
+          const uint32_t a = __float_as_uint(x2.x) & 0x7fffffffu, b = __float_as_uint(x2.y) & 0x7fffffffu;
+          big = a < 0x7f800000u ? max(big, a) : big;
+          big = b < 0x7f800000u ? max(big, b) : big;
+        }
+    }
+    big = __reduce_max_sync(0xffffffffu, big);
+    if (t % kWarp == 0) top[turn][t / kWarp] = big;
+    __syncthreads();
+    for (int i = 0; i < T / kWarp; ++i) big = max(big, top[turn][i]);
+    turn ^= 1;
     int e_new = scale_exponent(big);
     if (kept > 0) {
       const int e_old = static_cast<int>(__float_as_uint(*scale) >> 23) - 127;
       e_new = max(e_new, min(max(e_old, -kScaleExpMax), kScaleExpMax));
       if (e_new > e_old) {
-        const float f = pow2f(max(e_old - e_new, -126));
+        const float g = pow2f(max(e_old - e_new, -126));
         uint32_t* c4 = reinterpret_cast<uint32_t*>(codes);
-        for (int i = threadIdx.x; i < kept * D / 4; i += kWriteThreads) {
+        for (int i = t; i < kept * D / 4; i += T) {
           const uint32_t c = c4[i];
           const float2 a = f16x2_to_float2(e4m3x2_lo_to_f16x2(c));
           const float2 b = f16x2_to_float2(e4m3x2_hi_to_f16x2(c));
-          c4[i] = floats_to_e4m3x2(a.x * f, a.y * f) | (floats_to_e4m3x2(b.x * f, b.y * f) << 16);
+          c4[i] = floats_to_e4m3x2(a.x * g, a.y * g) | (floats_to_e4m3x2(b.x * g, b.y * g) << 16);
         }
       }
       __syncthreads();                                          // every thread has read *scale
     }
-    if (threadIdx.x == 0) *scale = pow2f(e_new);
+    if (t == 0) *scale = pow2f(e_new);
     const float inv = pow2f(-e_new);
-#pragma unroll 4
-    for (int e = kept * kChunks + threadIdx.x; e < end * kChunks; e += kWriteThreads) {
-      float f[8];
-      load8<DT, VEC>(f, x, x0 + (e / kChunks) * ld + e % kChunks * 8);
-      uint2 c;
-      c.x = floats_to_e4m3x2(f[0] * inv, f[1] * inv) | (floats_to_e4m3x2(f[2] * inv, f[3] * inv) << 16);
-      c.y = floats_to_e4m3x2(f[4] * inv, f[5] * inv) | (floats_to_e4m3x2(f[6] * inv, f[7] * inv) << 16);
-      reinterpret_cast<uint2*>(codes)[e] = c;
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+      const int e = e0 + i * T;
+      if (e >= e1) break;
+      uint32_t c[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 x2 = pair_of<DT>(f[i], j);
+        c[j] = floats_to_e4m3x2(x2.x * inv, x2.y * inv);
+      }
+      reinterpret_cast<uint2*>(codes)[e] = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
     }
   }
 }
@@ -802,8 +852,11 @@ struct WriteArgs {
 
 template <int DT, int D>
 cudaError_t launch_write_vec(const Pool& p, const WriteArgs& a, unsigned grid, cudaStream_t stream) {
+  // a page's rows of one head fit the registers of 128 or of 256 threads
+  static_assert(kWriteThreads * kHold * 8 >= 128 * 128, "a page of 128 events of head_dim 128");
+  const int threads = p.h.page_tokens * D <= 128 * kHold * 8 ? 128 : kWriteThreads;
   return launch_pdl(a.vec ? append_kernel<DT, D, true> : append_kernel<DT, D, false>, dim3(grid),
-                    dim3(kWriteThreads), 0, stream, p, a.starts, a.k, a.ld_k, a.ld_k_head, a.v,
+                    dim3(threads), 0, stream, p, a.starts, a.k, a.ld_k, a.ld_k_head, a.v,
                     a.ld_v, a.ld_v_head);
 }
 
