@@ -4,7 +4,8 @@
 //
 // A work unit is 256 rows, as two tiles of 128 (the MMA's M), of one kv head of
 // a request; rows are (query, head of the group) pairs. Persistent CTAs, one
-// per SM. Per unit the keys that any of its rows sees flow by in key tiles of at
+// per SM, or two where tensor and shared memory have room (plain rows, head_dim up
+// to 64: the ragged batch below 58 us against 64). Per unit the keys that any of its rows sees flow by in key tiles of at
 // most 64 events: the sinks that lie apart from the window first (a narrow
 // tile), then the window from its first event on.
 //   warp 11: finds the units and writes what the others need of them into a
@@ -31,11 +32,24 @@
 // the output. The scores of the next key tile are made while the softmax works on
 // this one's. At head_dim 128 there is no room for the weights: they lie over
 // their scores, whose buffer is then only free when the weights have been used.
+// Two CTAs an SM have one score buffer a tile, weights over it, and overlap each
+// other instead.
 //
 // PAGED: candidates of few users make few units, so the key tiles of all units
 // are cut evenly over the CTAs, as in history_attention.cu; a unit that is split
 // leaves partial outputs, and of each tile's warps the one that arrives last
 // joins its 32 rows, in the order of the events.
+//
+// What bounds it: the softmax between the two products. A step of 64 keys takes
+// its warps, two a scheduler, about 2000 cycles, 700 of them the exponentials; the
+// tensor pipe is 49% active at head_dim 128. More softmax warps leave each too
+// few registers (16 warps 298 us against 254), and powers by a polynomial on the
+// FMA pipe cost more issue slots than the special function unit saves (269).
+// Measured: 2 x 16384 events, 8 heads of 128, window 2048, fp16: 254 us, 1.0
+// PFLOP/s of visible products (52% of the bf16 rate); 64 users of 100 to 1024 events,
+// 8 heads of 64 over 2, window 256, bf16: 58 us, of which the first loads and the last
+// products of short units are 10K of 26K cycles a unit; PAGED, 16 users x up to 500
+// candidates over 1000 to 4096 events, 4 heads of 64 over 2: 66 us, 0.27 PFLOP/s.
 //
 // Every wait is bounded (WaitCfg); on expiry DLRM_ERRBIT_TIMEOUT is set, every
 // role leaves its loop, work in flight is waited for and the tensor memory freed.

@@ -38,7 +38,12 @@
 // query is split into an f16 head and a rest of 11 more bits, which take two
 // MMA rows, and so is P: 8 rows a tile, errors as of fp32.
 //
-// What bounds it: reading the codes (2 D bytes an event and kv head).
+// What bounds it: reading the codes (2 D bytes an event and kv head). Measured, one
+// query a user: 4 users of 65,000 to 100,001 events, 8 heads of 128, fp16, 123 us, 84%
+// of the copy rate; 64 users of 37 to 4096 events, 8 heads of 64 over 2, bf16, 24 us,
+// half of it the start (the lengths of all requests, then table, then codes, each a
+// read that waits for the one before) and the join; one user of 150 events 9 us, all of
+// it start.
 #include <atomic>
 
 #include "attention.cuh"

@@ -1,8 +1,9 @@
 // history_attention on the tensor cores: bf16 queries, many rows a request
 // (attention_tc.cuh; history_attention.cu takes every other call).
 //
-// What bounds it: as in window_attention_tc.cu, the softmax warps; and with few
-// units the time of one key tile after another.
+// (A code times its page's scale is exact in bf16; fp16 has not the exponents.)
+// What bounds it: the softmax, and with few units the time of one key tile after
+// another.
 #include "attention_tc.cuh"
 
 namespace dlrm {

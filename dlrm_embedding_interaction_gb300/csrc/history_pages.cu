@@ -384,6 +384,9 @@ __device__ __forceinline__ float2 pair_of(const uint32_t* w, int i) {
 // are re-rounded: exact but for codes that become subnormal, as scales are
 // powers of two. What an item is takes a chain of four loads: the CTA's next
 // items are looked up together, a thread each.
+// What bounds it: HBM. 16 histories of 2000 to 4096 events, 8 heads of 128, bf16
+// (310 MB moved): 52 us under the profiler, 87% of the copy rate; with free and plan
+// 68 us (84 with the rows read twice, the second time from L1).
 template <int DT, int D, bool VEC>
 __global__ void __launch_bounds__(kWriteThreads, 2)
 append_kernel(Pool p, const int32_t* starts, const void* k, int64_t ld_k, int64_t ld_k_head,

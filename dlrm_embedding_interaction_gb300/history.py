@@ -215,11 +215,11 @@ def history_append(cache: HistoryCache, slots, starts, k, v, stream=None) -> Non
     c = _cache_of(cache, where)
     b = _int32_vector(slots, f"{where}: slots", None, c.device)
     _int32_vector(starts, f"{where}: starts", b + 1, c.device)
+    _rows(k, f"{where}: k", c.n_heads, c.head_dim, c.device)
+    _rows(v, f"{where}: v", c.n_heads, c.head_dim, c.device)
     dt = _dtype_code(k, f"{where}: k")
     if v.dtype != k.dtype:
         raise TypeError(f"{where}: v: expected {k.dtype}, got {v.dtype}")
-    _rows(k, f"{where}: k", c.n_heads, c.head_dim, c.device)
-    _rows(v, f"{where}: v", c.n_heads, c.head_dim, c.device)
     if k.shape[0] != v.shape[0]:
         raise ValueError(f"{where}: k and v must have as many rows")
     if b > c.n_slots:
