@@ -82,32 +82,37 @@ def _dtype_code(t, name: str) -> int:
     return code
 
 
-def _raw_stream(stream, device):
-    """The cudaStream_t of ``stream``, or of the device's current stream (read
+def _raw_stream(stream, index: int):
+    """The cudaStream_t of ``stream``, or of device ``index``'s current stream (read
     without making a Stream object, which takes microseconds)."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return torch._C._cuda_getCurrentRawStream(index)
     return _stream(stream)
 
 
+# The checks below run with every call: a tensor that passes costs a few attributes
+# (all of a call's about as much as the launch), and messages are made for errors
+# only. ``device`` is an index (quick) or a torch.device.
+
+def _elsewhere(t, device) -> bool:
+    return t.device != device if isinstance(device, torch.device) else t.get_device() != device
+
+
 def _int32_vector(t, name: str, n: Optional[int], device) -> int:
-    if (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.dim() == 1
-            and t.get_device() == (device.index if device.type == "cuda" else -1)
-            and t.is_contiguous() and (n is None or t.shape[0] == n)):
-        return t.shape[0]
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32:
         raise TypeError(f"{name}: expected an int32 tensor")
-    if t.dim() != 1 or (n is not None and t.shape[0] != n):
-        raise ValueError(f"{name}: expected ({'n' if n is None else n},), got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name}: must be on {device}")
+    shape = t.shape
+    if len(shape) != 1 or (n is not None and shape[0] != n):
+        raise ValueError(f"{name}: expected ({'n' if n is None else n},), got {tuple(shape)}")
+    if t.get_device() != device and _elsewhere(t, device):
+        raise ValueError(f"{name}: on {t.device}, not where the call's other tensors are")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t.shape[0]
+    return shape[0]
 
 
 def _rows(t, name: str, heads: Optional[int], dim: Optional[int], device):
-    """A (rows, heads, dim) tensor with unit stride along dim."""
+    """Shape and strides of a (rows, heads, dim) tensor with unit stride along dim."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     shape = t.shape
@@ -115,10 +120,12 @@ def _rows(t, name: str, heads: Optional[int], dim: Optional[int], device):
             dim is not None and shape[2] != dim):
         raise ValueError(f"{name}: expected (rows, {heads or 'heads'}, {dim or 'dim'}), "
                          f"got {tuple(shape)}")
-    if t.get_device() != (device.index if device.type == "cuda" else -1):
-        raise ValueError(f"{name}: must be on {device}")
-    if shape[2] > 1 and t.stride(2) != 1 and t.numel():
+    if t.get_device() != device and _elsewhere(t, device):
+        raise ValueError(f"{name}: on {t.device}, not where the call's other tensors are")
+    strides = t.stride()
+    if strides[2] != 1 and shape[2] > 1 and t.numel():
         raise ValueError(f"{name}: its last dimension must be contiguous")
+    return shape, strides
 
 
 class HistoryCache:
@@ -165,12 +172,12 @@ class HistoryCache:
         c.work, c.work_bytes = self._work.data_ptr(), work
         self.device, self.n_slots, self.max_pages = device, int(n_slots), int(max_pages)
         self.n_heads, self.head_dim, self.page_tokens = int(n_heads), int(head_dim), int(page_tokens)
-        self._c, self._ref = c, ctypes.byref(c)
+        self._c, self._ref, self._index = c, ctypes.byref(c), device.index
         self.reset(stream)
 
     def reset(self, stream=None) -> None:
         """Every page free, every slot empty, the error word cleared."""
-        _check(_bound().history_reset(self._ref, _raw_stream(stream, self.device)), "history_reset")
+        _check(_bound().history_reset(self._ref, _raw_stream(stream, self._index)), "history_reset")
 
     def error(self, stream=None) -> int:
         """Waits for ``stream``, returns the first error that the device recorded
@@ -213,48 +220,51 @@ def history_append(cache: HistoryCache, slots, starts, k, v, stream=None) -> Non
     (B,) and ``starts`` (B+1,) are int32; a slot occurs once."""
     where = "history_append"
     c = _cache_of(cache, where)
-    b = _int32_vector(slots, f"{where}: slots", None, c.device)
-    _int32_vector(starts, f"{where}: starts", b + 1, c.device)
-    _rows(k, f"{where}: k", c.n_heads, c.head_dim, c.device)
-    _rows(v, f"{where}: v", c.n_heads, c.head_dim, c.device)
-    dt = _dtype_code(k, f"{where}: k")
-    if v.dtype != k.dtype:
+    index = c._index
+    b = _int32_vector(slots, "history_append: slots", None, index)
+    _int32_vector(starts, "history_append: starts", b + 1, index)
+    (rows, _, _), ks = _rows(k, "history_append: k", c.n_heads, c.head_dim, index)
+    (v_rows, _, _), vs = _rows(v, "history_append: v", c.n_heads, c.head_dim, index)
+    dt = _dtype_code(k, "history_append: k")
+    if v.dtype is not k.dtype:
         raise TypeError(f"{where}: v: expected {k.dtype}, got {v.dtype}")
-    if k.shape[0] != v.shape[0]:
+    if v_rows != rows:
         raise ValueError(f"{where}: k and v must have as many rows")
     if b > c.n_slots:
         raise ValueError(f"{where}: {b} requests for {c.n_slots} slots")
     _check(_bound().history_append(c._ref, slots.data_ptr(), starts.data_ptr(), b, k.data_ptr(),
-                                   k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
-                                   v.stride(1), k.shape[0], dt, _raw_stream(stream, c.device)),
-           where)
+                                   ks[0], ks[1], v.data_ptr(), vs[0], vs[1], rows, dt,
+                                   _raw_stream(stream, index)), where)
 
 
 def _slots_call(name: str, cache, vectors, stream, *more) -> None:
     c = _cache_of(cache, name)
-    b = None
+    index = c._index
+    b, pointers = None, []
     for label, t in vectors:
-        b = _int32_vector(t, f"{name}: {label}", b, c.device)
+        b = _int32_vector(t, label, b, index)
+        pointers.append(t.data_ptr())
     if b > c.n_slots:
         raise ValueError(f"{name}: {b} requests for {c.n_slots} slots")
-    _check(getattr(_bound(), name)(c._ref, *[t.data_ptr() for _, t in vectors], b, *more,
-                                   _raw_stream(stream, c.device)), name)
+    _check(getattr(_bound(), name)(c._ref, *pointers, b, *more, _raw_stream(stream, index)), name)
 
 
 def history_fork(cache: HistoryCache, src, dst, stream=None) -> None:
     """The empty slot ``dst[b]`` becomes a history like ``src[b]``'s: full pages are
     shared, a last page that is not full is copied."""
-    _slots_call("history_fork", cache, (("src", src), ("dst", dst)), stream)
+    _slots_call("history_fork", cache, (("history_fork: src", src), ("history_fork: dst", dst)),
+                stream)
 
 
 def history_copy(cache: HistoryCache, src, dst, stream=None) -> None:
     """As history_fork, with every page copied."""
-    _slots_call("history_copy", cache, (("src", src), ("dst", dst)), stream)
+    _slots_call("history_copy", cache, (("history_copy: src", src), ("history_copy: dst", dst)),
+                stream)
 
 
 def history_free(cache: HistoryCache, slots, stream=None) -> None:
     """Empties slots; pages that no slot holds any more become free."""
-    _slots_call("history_free", cache, (("slots", slots),), stream)
+    _slots_call("history_free", cache, (("history_free: slots", slots),), stream)
 
 
 def history_trim(cache: HistoryCache, slots, window: int, sinks: int = 0, stream=None) -> None:
@@ -262,32 +272,34 @@ def history_trim(cache: HistoryCache, slots, window: int, sinks: int = 0, stream
     longer reads, in queries at the histories' ends or later."""
     if window < 1 or sinks < 0:
         raise ValueError("history_trim: window must be at least 1, sinks at least 0")
-    _slots_call("history_trim", cache, (("slots", slots),), stream, int(window), int(sinks))
+    _slots_call("history_trim", cache, (("history_trim: slots", slots),), stream, int(window), int(sinks))
 
 
 def history_compact(cache: HistoryCache, stream=None) -> None:
     """Moves pages in use to the front of the pool and rebuilds the free stack."""
     c = _cache_of(cache, "history_compact")
-    _check(_bound().history_compact(c._ref, _raw_stream(stream, c.device)), "history_compact")
+    _check(_bound().history_compact(c._ref, _raw_stream(stream, c._index)), "history_compact")
 
 
-def _check_outputs(where, q, out, lse, window, sinks, device):
+def _check_outputs(where, q, shape, out, lse, window, sinks, index):
+    """out, made if there is none, and its strides."""
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=device)
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        strides = out.stride()
     else:
         if not isinstance(out, torch.Tensor) or out.dtype is not q.dtype:
             raise TypeError(f"{where}: out: expected a {q.dtype} tensor")
-        _rows(out, f"{where}: out", q.shape[1], q.shape[2], device)
-        if out.shape[0] != q.shape[0]:
-            raise ValueError(f"{where}: out: expected {q.shape[0]} rows, got {out.shape[0]}")
+        got, strides = _rows(out, "out", shape[1], shape[2], index)
+        if got[0] != shape[0]:
+            raise ValueError(f"{where}: out: expected {shape[0]} rows, got {got[0]}")
     if lse is not None:
         if not isinstance(lse, torch.Tensor) or lse.dtype is not torch.float32:
             raise TypeError(f"{where}: lse: expected a float32 tensor")
-        if lse.shape != q.shape[:2] or lse.device != device or not lse.is_contiguous():
-            raise ValueError(f"{where}: lse: expected contiguous {tuple(q.shape[:2])} on {device}")
+        if lse.shape != shape[:2] or lse.get_device() != index or not lse.is_contiguous():
+            raise ValueError(f"{where}: lse: expected contiguous {tuple(shape[:2])} on {q.device}")
     if window < 0 or sinks < 0:
         raise ValueError(f"{where}: window and sinks must not be negative")
-    return out
+    return out, strides
 
 
 def history_attention(cache: HistoryCache, slots, starts, q, out=None, *, scale=None,
@@ -304,20 +316,20 @@ def history_attention(cache: HistoryCache, slots, starts, q, out=None, *, scale=
     exponentials."""
     where = "history_attention"
     c = _cache_of(cache, where)
-    b = _int32_vector(slots, f"{where}: slots", None, c.device)
-    _int32_vector(starts, f"{where}: starts", b + 1, c.device)
-    _rows(q, f"{where}: q", None, c.head_dim, c.device)
-    if q.shape[1] < 1 or q.shape[1] % c.n_heads:
-        raise ValueError(f"{where}: q: {q.shape[1]} heads are no multiple of the cache's {c.n_heads}")
-    dtype = _dtype_code(q, f"{where}: q")
-    out = _check_outputs(where, q, out, lse, window, sinks, c.device)
-    rows, heads, dim = q.shape
-    qs, os = q.stride(), out.stride()
+    index = c._index
+    b = _int32_vector(slots, "history_attention: slots", None, index)
+    _int32_vector(starts, "history_attention: starts", b + 1, index)
+    shape, qs = _rows(q, "history_attention: q", None, c.head_dim, index)
+    rows, heads, dim = shape
+    if heads < 1 or heads % c.n_heads:
+        raise ValueError(f"{where}: q: {heads} heads are no multiple of the cache's {c.n_heads}")
+    dtype = _dtype_code(q, "history_attention: q")
+    out, os = _check_outputs(where, q, shape, out, lse, window, sinks, index)
     args = _ATTENTION.pack(
         q.data_ptr(), 0, 0, out.data_ptr(), 0 if lse is None else lse.data_ptr(), slots.data_ptr(),
         starts.data_ptr(), 0, rows, 0, qs[0], qs[1], 0, 0, 0, 0, os[0], os[1], b, heads, c.n_heads,
         dim, dtype, causal, window, sinks, dim ** -0.5 if scale is None else scale, 0)
-    _check(_bound().history_attention(c._ref, args, _raw_stream(stream, c.device)), where)
+    _check(_bound().history_attention(c._ref, args, _raw_stream(stream, index)), where)
     return out
 
 
@@ -338,31 +350,31 @@ def window_attention(q, k, v, starts, out=None, *, k_starts=None, scale=None, wi
             raise TypeError(f"{where}: {name}: expected {q.dtype}, got {t.dtype}")
     if not q.is_cuda:
         raise ValueError(f"{where}: q must be a CUDA tensor")
-    dev = q.device
-    _rows(q, f"{where}: q", None, None, dev)
-    _rows(k, f"{where}: k", None, q.shape[2], dev)
-    _rows(v, f"{where}: v", k.shape[1], q.shape[2], dev)
-    if k.shape[0] != v.shape[0]:
+    index = q.get_device()
+    shape, qs = _rows(q, "window_attention: q", None, None, index)
+    rows, heads, dim = shape
+    (k_rows, kv_heads, _), ks = _rows(k, "window_attention: k", None, dim, index)
+    (v_rows, _, _), vs = _rows(v, "window_attention: v", kv_heads, dim, index)
+    if k_rows != v_rows:
         raise ValueError(f"{where}: k and v must have as many rows")
-    if k.shape[1] < 1 or q.shape[1] < 1 or q.shape[1] % k.shape[1]:
-        raise ValueError(f"{where}: {q.shape[1]} query heads are no multiple of {k.shape[1]} kv heads")
-    if k_starts is None:
-        k_starts = starts
-    b = _int32_vector(starts, f"{where}: starts", None, dev) - 1
+    if kv_heads < 1 or heads < 1 or heads % kv_heads:
+        raise ValueError(f"{where}: {heads} query heads are no multiple of {kv_heads} kv heads")
+    b = _int32_vector(starts, "window_attention: starts", None, index) - 1
     if b < 0:
         raise ValueError(f"{where}: starts: expected at least one entry")
-    _int32_vector(k_starts, f"{where}: k_starts", b + 1, dev)
-    dtype = _dtype_code(q, f"{where}: q")
-    out = _check_outputs(where, q, out, lse, window, sinks, dev)
+    if k_starts is None:
+        k_starts = starts
+    else:
+        _int32_vector(k_starts, "window_attention: k_starts", b + 1, index)
+    dtype = _dtype_code(q, "window_attention: q")
+    out, os = _check_outputs(where, q, shape, out, lse, window, sinks, index)
     if err_flag is not None:
-        _int32_vector(err_flag, f"{where}: err_flag", 1, dev)
-    rows, heads, dim = q.shape
-    qs, ks, vs, os = q.stride(), k.stride(), v.stride(), out.stride()
+        _int32_vector(err_flag, "window_attention: err_flag", 1, index)
     args = _ATTENTION.pack(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
         0 if lse is None else lse.data_ptr(), 0, starts.data_ptr(), k_starts.data_ptr(), rows,
-        k.shape[0], qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os[0], os[1], b, heads, k.shape[1],
+        k_rows, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os[0], os[1], b, heads, kv_heads,
         dim, dtype, 1, window, sinks, dim ** -0.5 if scale is None else scale,
         0 if err_flag is None else err_flag.data_ptr())
-    _check(_bound().window_attention(args, _raw_stream(stream, dev)), where)
+    _check(_bound().window_attention(args, _raw_stream(stream, index)), where)
     return out
