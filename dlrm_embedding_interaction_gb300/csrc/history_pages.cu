@@ -5,8 +5,8 @@
 // device, so no call waits for the GPU and all can be captured in a graph.
 // A call is a chain of small launches (programmatic dependent launches: each
 // starts its set-up while the one before it ends):
-//   append     plan (one CTA), write
-//   fork       plan (one CTA), share and copy
+//   append     plan (one CTA), write; of few requests every CTA plans for itself
+//   fork       plan (one CTA), share and copy; likewise
 //   copy       plan (one CTA), rows, copy
 //   free/trim  one CTA for few pages; else release, count, push (a CTA a request)
 //   compact    count, match, move, rename
@@ -22,7 +22,7 @@ namespace {
 constexpr int kPlanThreads = 1024;
 
 // Words of the scratch's head.
-enum { kHeadItems = 0, kHeadTop = 1, kHeadLive = 2, kHeadMoves = 3 };
+enum { kHeadItems = 0, kHeadTop = 1, kHeadLive = 2, kHeadMoves = 3, kHeadArrived = 4 };
 
 // What the plan knows of one request. item0: its first work item.
 struct Request {
@@ -100,6 +100,44 @@ __device__ __forceinline__ int block_exclusive(int x, int* sums, int& total) {
 
 enum PlanOp { kAppend, kFork, kCopy };
 
+// What request b asks for, but for its place among the others; bad: the error
+// bits of one that is refused. first: no earlier request writes its slot.
+template <int OP>
+__device__ __forceinline__ Request request_of(const Pool& p, int s, int d, bool first, const int32_t* starts,
+                                              int b, int64_t rows, uint32_t& bad) {
+  const dlrm_history_t& h = p.h;
+  const int G = h.page_tokens, M = h.max_pages;
+  Request r{-1, -1, 0, 0, 0, 0, 0, 0};
+  if (d < 0 || d >= h.n_slots || s < 0 || s >= h.n_slots) {
+    bad = DLRM_ERRBIT_INDEX_OOB;
+  } else if (!first) {
+    bad = DLRM_ERRBIT_INVALID_ARG;
+  } else {
+    r.slot = d;
+    r.source = s;
+    const int64_t cap = static_cast<int64_t>(M) * G;
+    r.length = static_cast<int>(min(static_cast<int64_t>(max(h.lengths[s], 0)), cap));
+    if (OP == kAppend) {
+      const int t0 = starts[b], t1 = starts[b + 1];
+      if (t0 < 0 || t1 < t0 || t1 > rows) {
+        bad = DLRM_ERRBIT_OFFSETS;
+      } else if (r.length + static_cast<int64_t>(t1 - t0) > cap) {
+        bad = DLRM_ERRBIT_INVALID_ARG;
+      } else {
+        r.count = t1 - t0;
+        const int old = (r.length + G - 1) / G;
+        r.need = static_cast<int>((r.length + static_cast<int64_t>(r.count) + G - 1) / G) - old;
+        r.items = r.need + (r.count > 0 && r.length % G != 0 ? 1 : 0);
+      }
+    } else if (h.lengths[d] != 0) {
+      bad = DLRM_ERRBIT_INVALID_ARG;
+    } else if (OP == kFork) {
+      r.need = r.length % G != 0 ? 1 : 0;
+    }
+  }
+  return r;
+}
+
 // One CTA, a thread a request: gives every request its place in the free stack
 // and in the list of work items by prefix sums. It reads tables and lengths
 // but does not change them (the next launch does), so every request sees the
@@ -133,33 +171,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Pool p, const int32_
     uint32_t bad = 0;
     if (b < batch) {
       const int d = dst[b], s = OP == kAppend ? d : src[b];
-      if (d < 0 || d >= h.n_slots || s < 0 || s >= h.n_slots) {
-        bad = DLRM_ERRBIT_INDEX_OOB;
-      } else if (__ldcg(&p.mark_slot[d]) != b) {
-        bad = DLRM_ERRBIT_INVALID_ARG;
-      } else {
-        r.slot = d;
-        r.source = s;
-        const int64_t cap = static_cast<int64_t>(M) * G;
-        r.length = static_cast<int>(min(static_cast<int64_t>(max(h.lengths[s], 0)), cap));
-        if (OP == kAppend) {
-          const int t0 = starts[b], t1 = starts[b + 1];
-          if (t0 < 0 || t1 < t0 || t1 > rows) {
-            bad = DLRM_ERRBIT_OFFSETS;
-          } else if (r.length + static_cast<int64_t>(t1 - t0) > cap) {
-            bad = DLRM_ERRBIT_INVALID_ARG;
-          } else {
-            r.count = t1 - t0;
-            const int old = (r.length + G - 1) / G;
-            r.need = static_cast<int>((r.length + static_cast<int64_t>(r.count) + G - 1) / G) - old;
-            r.items = r.need + (r.count > 0 && r.length % G != 0 ? 1 : 0);
-          }
-        } else if (h.lengths[d] != 0) {
-          bad = DLRM_ERRBIT_INVALID_ARG;
-        } else if (OP == kFork) {
-          r.need = r.length % G != 0 ? 1 : 0;
-        }
-      }
+      const bool first = d < 0 || d >= h.n_slots || __ldcg(&p.mark_slot[d]) == b;
+      r = request_of<OP>(p, s, d, first, starts, b, rows, bad);
     }
     if (bad) {
       flag(h.err, bad);
@@ -225,6 +238,83 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Pool p, const int32_
   }
 }
 
+// The plan of a call of at most kSmallBatch requests, which every CTA of the next
+// launch makes for itself instead: that launch is then the only one (one event for
+// each of 32 users, forked, appended and freed: 19.1 us against 21.0). Lengths and the
+// free stack's height change once every CTA has read them, in the CTA that is last to.
+// (More requests: an earlier request for the same slot is found by comparison with
+// each, and every CTA's plan takes longer than the launch.)
+constexpr int kSmallBatch = 128;
+struct SmallPlan {
+  Request request[kSmallBatch];
+  int4 slots[kSmallBatch / 4];
+  int sums[kWarp + 1];
+  int items, top, done;
+};
+// Returns the CTA's ticket, known to thread 0 alone and not before it asks for it:
+// commit_small, at the kernel's end, takes it.
+template <int OP>
+__device__ __forceinline__ unsigned plan_small(const Pool& p, const int32_t* src, const int32_t* dst,
+                                           const int32_t* starts, int batch, int64_t rows, SmallPlan& plan) {
+  const dlrm_history_t& h = p.h;
+  const int t = threadIdx.x;
+  const bool report = blockIdx.x == 0 && blockIdx.y == 0;
+  const int nfree = min(max(*h.n_free, 0), h.n_pages);
+  const int d = t < batch ? dst[t] : -1, s = OP == kAppend || t >= batch ? d : src[t];
+  if (t < kSmallBatch) reinterpret_cast<int*>(plan.slots)[t] = d;
+  if (t == 0) plan.done = 0;
+  __syncthreads();
+  Request r{-1, -1, 0, 0, 0, 0, 0, 0};
+  uint32_t bad = 0;
+  if (t < batch) {
+    bool first = true;
+    for (int i = 0; i < t; i += 4) {
+      const int4 x = plan.slots[i / 4];
+      first &= x.x != d && (i + 1 >= t || x.y != d) && (i + 2 >= t || x.z != d) && (i + 3 >= t || x.w != d);
+    }
+    r = request_of<OP>(p, s, d, first, starts, t, rows, bad);
+  }
+  if (bad) {
+    if (report) flag(h.err, bad);
+    r.slot = -1;
+    r.need = r.items = 0;
+  }
+  int total;
+  r.base = block_exclusive(r.need, plan.sums, total);
+  if (r.need > 0) {
+    if (r.base + static_cast<int64_t>(r.need) > nfree) {
+      if (report) flag(h.err, DLRM_ERRBIT_OOM);
+      r.slot = -1;
+      r.items = 0;
+    } else {
+      atomicMax(&plan.done, r.base + r.need);
+    }
+  }
+  r.item0 = block_exclusive(r.items, plan.sums, total);
+  if (t < kSmallBatch) plan.request[t] = r;
+  if (t == 0) {
+    plan.items = total;
+    plan.top = nfree;
+  }
+  __syncthreads();                                // every thread has read what commit_small changes
+  unsigned ticket = 0;
+  if (t == 0) {
+    __threadfence();
+    ticket = atomicInc(reinterpret_cast<unsigned*>(&p.head[kHeadArrived]), gridDim.x * gridDim.y - 1);
+  }
+  return ticket;
+}
+// By the first warp.
+__device__ __forceinline__ void commit_small(const Pool& p, int batch, unsigned ticket, const SmallPlan& plan) {
+  if (__shfl_sync(0xffffffffu, ticket, 0) != gridDim.x * gridDim.y - 1) return;
+  __threadfence();
+  for (int i = threadIdx.x; i < batch; i += kWarp) {
+    const Request& r = plan.request[i];
+    if (r.slot >= 0) p.h.lengths[r.slot] = r.length + r.count;
+  }
+  if (threadIdx.x == 0) *p.h.n_free = plan.top - plan.done;
+}
+
 // Page number `rank` of request r.
 __device__ __forceinline__ int granted(const Pool& p, const Request& r, int top, int rank) {
   return p.h.free_pages[top - 1 - (r.base + rank)];
@@ -268,17 +358,13 @@ __host__ __device__ __forceinline__ int pieces_of(const dlrm_history_t& h) {
 
 // A fork's table row, by the CTAs (request, piece): full pages are shared, and
 // piece by piece the last page that is not full is copied. Piece 0 writes the row.
-__global__ void __launch_bounds__(kCopyThreads) fork_kernel(Pool p, int pieces) {
-  pdl_wait();
-  pdl_trigger();
+__device__ __forceinline__ void fork_one(const Pool& p, const Request& r, int top, int pieces, bool lengths) {
   const dlrm_history_t& h = p.h;
   const int G = h.page_tokens, M = h.max_pages;
-  const Request r = p.request[blockIdx.x];
-  if (r.slot < 0) return;
   const int32_t* from = h.table + static_cast<int64_t>(r.source) * M;
   const int full = r.length / G;
   const int last = r.need > 0 ? from[full] : -1;
-  const int page = r.need > 0 ? granted(p, r, p.head[kHeadTop], 0) : -1;
+  const int page = r.need > 0 ? granted(p, r, top, 0) : -1;
   if (blockIdx.y == 0) {
     int32_t* row = h.table + static_cast<int64_t>(r.slot) * M;
     for (int j = threadIdx.x; j < full; j += kCopyThreads) {
@@ -291,12 +377,25 @@ __global__ void __launch_bounds__(kCopyThreads) fork_kernel(Pool p, int pieces) 
         row[full] = page;
         h.refs[page] = 1;
       }
-      h.lengths[r.slot] = r.length;
+      if (lengths) h.lengths[r.slot] = r.length;
     }
   }
   // (a last page that is not full is never trimmed; a broken table's is not read)
   if (last >= 0 && last < h.n_pages)
     copy_piece(h, blockIdx.y / pieces, blockIdx.y % pieces, last, page);
+}
+
+// dst: the call's requests where no plan came before.
+__global__ void __launch_bounds__(kCopyThreads) fork_kernel(Pool p, int pieces, const int32_t* src,
+                                                            const int32_t* dst) {
+  __shared__ SmallPlan plan;
+  pdl_wait();
+  pdl_trigger();
+  unsigned ticket = 0;
+  if (dst) ticket = plan_small<kFork>(p, src, dst, nullptr, gridDim.x, 0, plan);
+  const Request r = dst ? plan.request[blockIdx.x] : p.request[blockIdx.x];
+  if (r.slot >= 0) fork_one(p, r, dst ? plan.top : p.head[kHeadTop], pieces, !dst);
+  if (dst && threadIdx.x < kWarp) commit_small(p, gridDim.x, ticket, plan);
 }
 
 // A copy's table row, by one CTA a request: the list of pages to copy.
@@ -343,6 +442,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(Pool p, int pieces) 
 
 constexpr int kWriteThreads = 256;   // at most: 128 where that holds a page's rows
 constexpr int kHold = 8;             // chunks of eight elements that a thread holds
+// CTAs of kWriteThreads that an SM holds, by the registers of the chunks
+constexpr int write_ctas(int dtype) { return dtype == DLRM_DTYPE_FP32 ? 2 : 3; }
 
 // Eight consecutive elements, as they are. VEC: at a 16-byte boundary.
 template <int DT, bool VEC>
@@ -385,12 +486,14 @@ __device__ __forceinline__ float2 pair_of(const uint32_t* w, int i) {
 // powers of two. What an item is takes a chain of four loads: the CTA's next
 // items are looked up together, a thread each.
 // What bounds it: HBM. 16 histories of 2000 to 4096 events, 8 heads of 128, bf16
-// (310 MB moved): 52 us under the profiler, 87% of the copy rate; with free and plan
-// 68 us (84 with the rows read twice, the second time from L1).
+// (310 MB moved): 52 us under the profiler, 87% of the copy rate; with the free before
+// it 62 us (84 with the rows read twice, the second time from L1, and a plan of its own).
 template <int DT, int D, bool VEC>
-__global__ void __launch_bounds__(kWriteThreads, 2)
-append_kernel(Pool p, const int32_t* starts, const void* k, int64_t ld_k, int64_t ld_k_head,
-              const void* v, int64_t ld_v, int64_t ld_v_head) {
+__global__ void __launch_bounds__(kWriteThreads, write_ctas(DT))
+append_kernel(Pool p, const int32_t* slots, const int32_t* starts, int batch, int64_t rows,
+              const void* k, int64_t ld_k, int64_t ld_k_head, const void* v, int64_t ld_v,
+              int64_t ld_v_head) {
+  __shared__ SmallPlan plan;
   __shared__ uint32_t top[2][kWriteThreads / kWarp];
   __shared__ int4 todo[kWriteThreads];            // page, first and last new event, row of event 0
   constexpr int kChunks = D / 8;                  // of a row
@@ -399,7 +502,10 @@ append_kernel(Pool p, const int32_t* starts, const void* k, int64_t ld_k, int64_
   const int G = h.page_tokens, H = h.n_heads, T = blockDim.x, t = threadIdx.x;
   pdl_wait();
   pdl_trigger();
-  const int64_t n = static_cast<int64_t>(p.head[kHeadItems]) * H * 2;
+  const bool small = batch <= kSmallBatch;
+  unsigned ticket = 0;
+  if (small) ticket = plan_small<kAppend>(p, nullptr, slots, starts, batch, rows, plan);
+  const int64_t n = static_cast<int64_t>(small ? plan.items : p.head[kHeadItems]) * H * 2;
   int left = 0;                                   // entries of `todo` from `at` on
   int at = 0, turn = 0;                           // `top` by turns: one barrier an item
   for (int64_t w = blockIdx.x; w < n; w += gridDim.x, ++at, --left) {
@@ -410,14 +516,24 @@ append_kernel(Pool p, const int32_t* starts, const void* k, int64_t ld_k, int64_
       __syncthreads();                            // `todo` is read
       if (w_of < n) {
         const int which = static_cast<int>(w_of / (2 * H));
-        const int2 item = p.items[which];         // request, page of the history
-        const Request r = p.request[item.x];
+        int2 item;                                // request, page of the history
+        Request r;
+        if (small) {
+          int b = 0;                              // the last one whose items begin at or before it
+          for (int i = kSmallBatch / 2; i > 0; i /= 2)
+            if (b + i < batch && plan.request[b + i].item0 <= which) b += i;
+          r = plan.request[b];
+          item = make_int2(b, r.length / G + which - r.item0);
+        } else {
+          item = p.items[which];
+          r = p.request[item.x];
+        }
         // the page there already, or one that the plan granted; one of the item's
         // workers writes it down, one of the last item's the new length
         int32_t* entry = h.table + static_cast<int64_t>(r.slot) * h.max_pages + item.y;
         const int had = (r.length + G - 1) / G;
         const bool fresh = item.y >= had;
-        int page = fresh ? granted(p, r, p.head[kHeadTop], item.y - had) : *entry;
+        int page = fresh ? granted(p, r, small ? plan.top : p.head[kHeadTop], item.y - had) : *entry;
         if (page < 0 || page >= h.n_pages) {      // a broken table: a last page that is not full is never trimmed
           flag(h.err, DLRM_ERRBIT_INDEX_OOB);
           page = -1;
@@ -427,7 +543,7 @@ append_kernel(Pool p, const int32_t* starts, const void* k, int64_t ld_k, int64_
             *entry = page;
             h.refs[page] = 1;
           }
-          if (which + 1 == r.item0 + r.items) h.lengths[r.slot] = r.length + r.count;
+          if (!small && which + 1 == r.item0 + r.items) h.lengths[r.slot] = r.length + r.count;
         }
         const int64_t first = static_cast<int64_t>(item.y) * G;   // the page's first event
         todo[t] = make_int4(page, static_cast<int>(max(r.length - first, int64_t(0))),
@@ -520,6 +636,7 @@ append_kernel(Pool p, const int32_t* starts, const void* k, int64_t ld_k, int64_
       reinterpret_cast<uint2*>(codes)[e] = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
     }
   }
+  if (small && t < kWarp) commit_small(p, batch, ticket, plan);
 }
 
 // ------------------------------------------------------------------ free, trim
@@ -838,6 +955,7 @@ __global__ void __launch_bounds__(256) reset_kernel(Pool p, int32_t* counters, i
   if (first == 0) {
     *h.n_free = h.n_pages;
     *h.err = 0;
+    p.head[kHeadArrived] = 0;
   }
 }
 
@@ -847,27 +965,31 @@ unsigned grid_for(int64_t units, int per_sm) {
 }
 
 struct WriteArgs {
-  const int32_t* starts;
+  const int32_t *slots, *starts;
+  int batch;
+  int64_t rows;
   const void *k, *v;
   int64_t ld_k, ld_k_head, ld_v, ld_v_head;
   bool vec;
 };
 
 template <int DT, int D>
-cudaError_t launch_write_vec(const Pool& p, const WriteArgs& a, unsigned grid, cudaStream_t stream) {
+cudaError_t launch_write_vec(const Pool& p, const WriteArgs& a, int64_t units, cudaStream_t stream) {
   // a page's rows of one head fit the registers of 128 or of 256 threads
   static_assert(kWriteThreads * kHold * 8 >= 128 * 128, "a page of 128 events of head_dim 128");
   const int threads = p.h.page_tokens * D <= 128 * kHold * 8 ? 128 : kWriteThreads;
+  // all resident at once: a CTA begins by looking up its items, or by planning
+  const unsigned grid = grid_for(units, write_ctas(DT) * (kWriteThreads / threads));
   return launch_pdl(a.vec ? append_kernel<DT, D, true> : append_kernel<DT, D, false>, dim3(grid),
-                    dim3(threads), 0, stream, p, a.starts, a.k, a.ld_k, a.ld_k_head, a.v,
-                    a.ld_v, a.ld_v_head);
+                    dim3(threads), 0, stream, p, a.slots, a.starts, a.batch, a.rows, a.k,
+                    a.ld_k, a.ld_k_head, a.v, a.ld_v, a.ld_v_head);
 }
 
 template <int DT>
-cudaError_t launch_write(const Pool& p, const WriteArgs& a, unsigned grid, cudaStream_t stream) {
-  if (p.h.head_dim == 32) return launch_write_vec<DT, 32>(p, a, grid, stream);
-  if (p.h.head_dim == 64) return launch_write_vec<DT, 64>(p, a, grid, stream);
-  return launch_write_vec<DT, 128>(p, a, grid, stream);
+cudaError_t launch_write(const Pool& p, const WriteArgs& a, int64_t units, cudaStream_t stream) {
+  if (p.h.head_dim == 32) return launch_write_vec<DT, 32>(p, a, units, stream);
+  if (p.h.head_dim == 64) return launch_write_vec<DT, 64>(p, a, units, stream);
+  return launch_write_vec<DT, 128>(p, a, units, stream);
 }
 
 }  // namespace
@@ -886,21 +1008,23 @@ cudaError_t launch_history_append(const dlrm_history_t& h, const int32_t* slots,
                                   int64_t ld_v_head, int64_t rows, int dtype,
                                   cudaStream_t stream) {
   const Pool p = make_pool(h);
-  cudaError_t e = launch_pdl(plan_kernel<kAppend>, dim3(1), dim3(kPlanThreads), 0, stream, p,
-                             static_cast<const int32_t*>(nullptr), slots, starts, batch, rows);
-  if (e != cudaSuccess) return e;
+  if (batch > kSmallBatch) {
+    const cudaError_t e = launch_pdl(plan_kernel<kAppend>, dim3(1), dim3(kPlanThreads), 0, stream, p,
+                                     static_cast<const int32_t*>(nullptr), slots, starts, batch, rows);
+    if (e != cudaSuccess) return e;
+  }
   // n new events touch at most n / G + 2 pages of a history
   const int64_t pages = std::min<int64_t>(rows, rows / h.page_tokens + 2 * int64_t(batch));
-  const unsigned grid = grid_for(pages * h.n_heads * 2, 16);
+  const int64_t units = pages * h.n_heads * 2;
   const int64_t eb = dtype_bytes(dtype);
   auto vec = [&](const void* x, int64_t ld, int64_t ld_head) {
     return reinterpret_cast<uintptr_t>(x) % 16 == 0 && ld * eb % 16 == 0 && ld_head * eb % 16 == 0;
   };
-  const WriteArgs a{starts, k, v, ld_k, ld_k_head, ld_v, ld_v_head,
+  const WriteArgs a{slots, starts, batch, rows, k, v, ld_k, ld_k_head, ld_v, ld_v_head,
                     vec(k, ld_k, ld_k_head) && vec(v, ld_v, ld_v_head)};
-  if (dtype == DLRM_DTYPE_FP32) return launch_write<DLRM_DTYPE_FP32>(p, a, grid, stream);
-  if (dtype == DLRM_DTYPE_BF16) return launch_write<DLRM_DTYPE_BF16>(p, a, grid, stream);
-  return launch_write<DLRM_DTYPE_FP16>(p, a, grid, stream);
+  if (dtype == DLRM_DTYPE_FP32) return launch_write<DLRM_DTYPE_FP32>(p, a, units, stream);
+  if (dtype == DLRM_DTYPE_BF16) return launch_write<DLRM_DTYPE_BF16>(p, a, units, stream);
+  return launch_write<DLRM_DTYPE_FP16>(p, a, units, stream);
 }
 
 cudaError_t launch_history_fork(const dlrm_history_t& h, const int32_t* src, const int32_t* dst,
@@ -908,11 +1032,14 @@ cudaError_t launch_history_fork(const dlrm_history_t& h, const int32_t* src, con
   const Pool p = make_pool(h);
   const int pieces = pieces_of(h);
   const int32_t* none = nullptr;
+  if (share && batch <= kSmallBatch)
+    return launch_pdl(fork_kernel, dim3(batch, 2 * pieces), dim3(kCopyThreads), 0, stream, p, pieces, src, dst);
   cudaError_t e = launch_pdl(share ? plan_kernel<kFork> : plan_kernel<kCopy>, dim3(1),
                              dim3(kPlanThreads), 0, stream, p, src, dst, none, batch, int64_t(0));
   if (e != cudaSuccess) return e;
   if (share)
-    return launch_pdl(fork_kernel, dim3(batch, 2 * pieces), dim3(kCopyThreads), 0, stream, p, pieces);
+    return launch_pdl(fork_kernel, dim3(batch, 2 * pieces), dim3(kCopyThreads), 0, stream, p, pieces,
+                      none, none);
   e = launch_pdl(copy_rows_kernel, dim3(batch), dim3(kCopyThreads), 0, stream, p);
   if (e != cudaSuccess) return e;
   const int64_t pages = std::min<int64_t>(h.n_pages, int64_t(batch) * h.max_pages);

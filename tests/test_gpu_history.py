@@ -276,6 +276,35 @@ def test_many_requests_in_one_call():
     same_state(cache, pool, codes=False)
 
 
+@pytest.mark.parametrize("batch", [1, 31, 64, 127, 128, 129, 200, 1025])
+def test_requests_of_any_number_with_refusals_among_them(batch):
+    """Forks and appends of a whole batch: slots out of range, slots written twice,
+    starts that decrease, occupied destinations and a pool that runs dry part of the way."""
+    rng = np.random.default_rng(batch)
+    users = 40
+    cache, pool = make(users * 4 + batch // 2, users + batch + 5, 4, 2, 32, 32)
+    fill(cache, pool, rng, list(range(users)), rng.integers(0, 100, users).tolist())
+    src, dst = rng.integers(0, users, batch), users + rng.permutation(batch)
+    src[rng.random(batch) < 0.05] = users + batch + 5
+    dst[rng.random(batch) < 0.05] = -1
+    again = rng.random(batch) < 0.1
+    dst[again] = dst[rng.integers(0, batch, batch)][again]
+    dst[rng.random(batch) < 0.05] = 3               # not empty, or written twice
+    src, dst = src.tolist(), dst.tolist()
+    dl.history_fork(cache, i32(src), i32(dst))
+    pool.fork(src, dst, True)
+    same_state(cache, pool)
+    at = starts_of(rng.integers(0, 45, batch))
+    at[batch // 2] += 20                            # may pass the next one
+    k, v = (rows(rng, max(at[-1], 1), 2, 32, "fp32") for _ in range(2))
+    dl.history_append(cache, i32(dst), i32(at), k, v)
+    pool.append(dst, at, (f64(k), f64(v)))
+    same_state(cache, pool)
+    dl.history_free(cache, i32(dst))
+    pool.release(dst)
+    same_state(cache, pool)
+
+
 # ------------------------------------------------------------------ attention over a cache
 
 def check_attention(cache, pool, rng, slots, counts, heads, dtype, causal, window, sinks, *,
