@@ -566,6 +566,7 @@ append_kernel(Pool p, const int32_t* slots, const int32_t* starts, int batch, in
     float* scale = (side ? h.v_scales : h.k_scales) + place;
 
     const int kept = item.y;                      // events there already
+    const float was = kept > 0 ? *scale : 1.f;
     const int e0 = kept * kChunks + t, e1 = item.z * kChunks;
     uint32_t f[kHold][kWords];
 #pragma unroll
@@ -607,7 +608,7 @@ append_kernel(Pool p, const int32_t* slots, const int32_t* starts, int batch, in
     turn ^= 1;
     int e_new = scale_exponent(big);
     if (kept > 0) {
-      const int e_old = static_cast<int>(__float_as_uint(*scale) >> 23) - 127;
+      const int e_old = static_cast<int>(__float_as_uint(was) >> 23) - 127;
       e_new = max(e_new, min(max(e_old, -kScaleExpMax), kScaleExpMax));
       if (e_new > e_old) {
         const float g = pow2f(max(e_old - e_new, -126));
@@ -619,7 +620,6 @@ append_kernel(Pool p, const int32_t* slots, const int32_t* starts, int batch, in
           c4[i] = floats_to_e4m3x2(a.x * g, a.y * g) | (floats_to_e4m3x2(b.x * g, b.y * g) << 16);
         }
       }
-      __syncthreads();                                          // every thread has read *scale
     }
     if (t == 0) *scale = pow2f(e_new);
     const float inv = pow2f(-e_new);
