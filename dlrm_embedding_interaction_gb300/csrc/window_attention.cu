@@ -6,16 +6,16 @@
 // the blocks of 32 events that its own rows see, with a running maximum and
 // sum, and keeps its output in registers. Fragments come straight from global
 // memory (the four warps of a CTA read nearly the same events: L1 serves
-// them), with the inner dimensions of the MMAs permuted so that a thread's
-// loads are contiguous, as in history_attention.cu.
+// them), with the inner dimensions of the MMAs permuted so that loads are of 16
+// bytes and the four threads of a row's queries and keys read 64 in a row (each a
+// quarter of the row instead: 410 us against 358 at 4096 events, head_dim 128).
 //   bf16, fp16: m16n8k16 in the input's own type; P is rounded to that type.
 //   fp32: m16n8k8 in tf32, three products per product (head * head,
 //     head * rest, rest * head), errors as of fp32.
 // What bounds it: instructions (the splits of three products a product) and reads
 // that wait for one another, as most warps walk few blocks. 32 users of up to 512
-// events, 4 heads of 32, window 64, fp32: 23 us with 128 registers and four CTAs an
-// SM. A block's keys and values loaded together take 138 registers and 29 us;
-// five CTAs an SM by a register cap 29 us, six 38.
+// events, 4 heads of 32, window 64, fp32: 20 us, four CTAs an SM. A block's keys and
+// values loaded together take 28 us; five CTAs an SM by a register cap 29 us, six 38.
 #include "window_attention.cuh"
 
 namespace dlrm {
@@ -31,17 +31,19 @@ using Params = WindowParams;
 // x as a tf32 head and rest, each rounded to nearest: 22 bits of x in all. (The
 // MMA cuts its operands off, which would leave a bias.)
 __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t& head, uint32_t& rest) {
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(head) : "f"(__uint_as_float(x)));
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(rest) : "f"(__uint_as_float(x) - __uint_as_float(head)));
+  const float f = __uint_as_float(x);             // (x may be head)
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(head) : "f"(f));
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(rest) : "f"(f - __uint_as_float(head)));
 }
 
-// N consecutive 32-bit words at a byte address, 16 bytes at a time if aligned.
-template <int N, bool HALF>
+// N 32-bit words from a byte address on, 16 bytes at a time if aligned, a group of
+// four each STEP bytes.
+template <int N, bool HALF, int STEP = 16>
 __device__ __forceinline__ void load_row_words(uint32_t* w, const uint8_t* p, bool vec) {
   if (vec && N % 4 == 0) {
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
-      const uint4 x = __ldg(reinterpret_cast<const uint4*>(p) + i);
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(p + i * STEP));
       w[4 * i] = x.x;
       w[4 * i + 1] = x.y;
       w[4 * i + 2] = x.z;
@@ -53,12 +55,12 @@ __device__ __forceinline__ void load_row_words(uint32_t* w, const uint8_t* p, bo
     w[1] = x.y;
   } else if (!HALF) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+    for (int i = 0; i < N; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p + i / 4 * STEP) + i % 4);
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const uint16_t lo = __ldg(reinterpret_cast<const uint16_t*>(p) + 2 * i);
-      const uint16_t hi = __ldg(reinterpret_cast<const uint16_t*>(p) + 2 * i + 1);
+      const uint16_t* two = reinterpret_cast<const uint16_t*>(p + i / 4 * STEP) + i % 4 * 2;
+      const uint16_t lo = __ldg(two), hi = __ldg(two + 1);
       w[i] = lo | (static_cast<uint32_t>(hi) << 16);
     }
   }
@@ -103,9 +105,18 @@ __global__ void __launch_bounds__(kThreads) window_attention_kernel(const Params
     const int i = row / p.group;
     const uint8_t* q = static_cast<const uint8_t*>(p.a.q) +
                        ((s.q0 + static_cast<int64_t>(i)) * p.a.ld_q +
-                        (head * p.group + row % p.group) * p.a.ld_q_head + c * (D / 4)) * EB;
-    load_row_words<KW, !kF32>(qw[r], q, p.vec);
+                        (head * p.group + row % p.group) * p.a.ld_q_head) * EB + c * 16;
+    load_row_words<KW, !kF32, 64>(qw[r], q, p.vec);
     vis[r] = visible(s.len - s.rows / p.group + i, s.len, p.a.window, p.a.sinks);
+  }
+  // fp32: split once where the rests have room in registers (head_dim 32: 20.8 -> 19.8 us)
+  constexpr bool kSplitQ = kF32 && D == 32;
+  uint32_t q_rest[2][kSplitQ ? KW : 1];
+  if (kSplitQ) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int w = 0; w < KW; ++w) split_tf32(qw[r][w], qw[r][w], q_rest[r][kSplitQ ? w : 0]);
   }
   // the events that any of the warp's rows sees
   const int i0 = row0 / p.group, i1 = last_row / p.group;
@@ -120,7 +131,7 @@ __global__ void __launch_bounds__(kThreads) window_attention_kernel(const Params
     for (int i = 0; i < 4; ++i) o[nt][i] = 0.f;
 
   const uint8_t* kp = static_cast<const uint8_t*>(p.a.k) +
-                      (s.k0 * p.a.ld_k + head * p.a.ld_k_head + c * (D / 4)) * EB;
+                      (s.k0 * p.a.ld_k + head * p.a.ld_k_head) * EB + c * 16;
   const uint8_t* vp = static_cast<const uint8_t*>(p.a.v) +
                       (s.k0 * p.a.ld_v + head * p.a.ld_v_head + g * (D / 8)) * EB;
   const int64_t k_step = p.a.ld_k * EB, v_step = p.a.ld_v * EB;
@@ -138,7 +149,7 @@ __global__ void __launch_bounds__(kThreads) window_attention_kernel(const Params
       for (int i = 0; i < 4; ++i) sc[j][i] = 0.f;
       uint32_t kw[KW];
       // an event past the end stands for the last one; its weight is zero
-      load_row_words<KW, !kF32>(kw, kp + min(t0 + 8 * j + g, s.len - 1) * k_step, p.vec);
+      load_row_words<KW, !kF32, 64>(kw, kp + min(t0 + 8 * j + g, s.len - 1) * k_step, p.vec);
       if (!kF32) {
 #pragma unroll
         for (int w = 0; w < KW; w += 2) {
@@ -151,9 +162,15 @@ __global__ void __launch_bounds__(kThreads) window_attention_kernel(const Params
       } else {
 #pragma unroll
         for (int w = 0; w < KW; w += 2) {
-          uint32_t a[4] = {qw[0][w], qw[1][w], qw[0][w + 1], qw[1][w + 1]}, hi[4], lo[4];
+          uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) split_tf32(a[i], hi[i], lo[i]);
+          for (int i = 0; i < 4; ++i) {
+            hi[i] = qw[i & 1][w + (i >> 1)];
+            if (kSplitQ)
+              lo[i] = q_rest[i & 1][kSplitQ ? w + (i >> 1) : 0];
+            else
+              split_tf32(hi[i], hi[i], lo[i]);
+          }
           uint32_t h0, h1, l0, l1;
           split_tf32(kw[w], h0, l0);
           split_tf32(kw[w + 1], h1, l1);
