@@ -74,6 +74,13 @@ __global__ void __launch_bounds__(kThreads) window_attention_kernel(const Params
   constexpr int KW = D / 4 / EW;                  // words of a thread and row: D/4 elements
   constexpr int VW = D / 8 / EW;
   constexpr int NT = D / 8;
+  // Scores of a whole block from kGroup words of every row at a time, so that fp32
+  // queries are split once a block (4096 events, window 512, 4 heads of 64: 165 us ->
+  // 151, of 128: 354 -> 298); at head_dim 32 from a whole row at a time, with the
+  // queries' rests in registers (20 us against 29, as 136 registers leave three CTAs an
+  // SM). Unaligned bf16 rows: 64 wide 103 -> 82, 128 wide 268 against 284, so whole rows there.
+  constexpr bool kWholeRows = D == 32 || (D == 128 && !kF32);
+  constexpr int kTogether = kWholeRows ? 1 : kBlock / 8, kGroup = kWholeRows ? KW : 4;
   __shared__ int64_t scan[40];
   const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
   const int g = lane / 4, c = lane % 4;
@@ -109,7 +116,6 @@ __global__ void __launch_bounds__(kThreads) window_attention_kernel(const Params
     load_row_words<KW, !kF32, 64>(qw[r], q, p.vec);
     vis[r] = visible(s.len - s.rows / p.group + i, s.len, p.a.window, p.a.sinks);
   }
-  // fp32: split once where the rests have room in registers (head_dim 32: 20.8 -> 19.8 us)
   constexpr bool kSplitQ = kF32 && D == 32;
   uint32_t q_rest[2][kSplitQ ? KW : 1];
   if (kSplitQ) {
@@ -144,39 +150,52 @@ __global__ void __launch_bounds__(kThreads) window_attention_kernel(const Params
     }
     float sc[kBlock / 8][4];
 #pragma unroll
-    for (int j = 0; j < kBlock / 8; ++j) {
+    for (int j0 = 0; j0 < kBlock / 8; j0 += kTogether) {
+      const uint8_t* row[kTogether];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sc[j][i] = 0.f;
-      uint32_t kw[KW];
-      // an event past the end stands for the last one; its weight is zero
-      load_row_words<KW, !kF32, 64>(kw, kp + min(t0 + 8 * j + g, s.len - 1) * k_step, p.vec);
-      if (!kF32) {
+      for (int j = 0; j < kTogether; ++j) {
 #pragma unroll
-        for (int w = 0; w < KW; w += 2) {
-          const uint32_t a[4] = {qw[0][w], qw[1][w], qw[0][w + 1], qw[1][w + 1]};
-          if (DT == DLRM_DTYPE_BF16)
-            mma_bf16(sc[j], a, kw[w], kw[w + 1]);
-          else
-            mma_f16(sc[j], a, kw[w], kw[w + 1]);
-        }
-      } else {
+        for (int i = 0; i < 4; ++i) sc[j0 + j][i] = 0.f;
+        // an event past the end stands for the last one; its weight is zero
+        row[j] = kp + min(t0 + 8 * (j0 + j) + g, s.len - 1) * k_step;
+      }
 #pragma unroll
-        for (int w = 0; w < KW; w += 2) {
-          uint32_t hi[4], lo[4];
+      for (int w0 = 0; w0 < KW; w0 += kGroup) {
+        uint32_t kw[kTogether][kGroup];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            hi[i] = qw[i & 1][w + (i >> 1)];
-            if (kSplitQ)
-              lo[i] = q_rest[i & 1][kSplitQ ? w + (i >> 1) : 0];
-            else
-              split_tf32(hi[i], hi[i], lo[i]);
+        for (int j = 0; j < kTogether; ++j)
+          load_row_words<kGroup, !kF32, 64>(kw[j], row[j] + w0 * 16, p.vec);
+#pragma unroll
+        for (int w = w0; w < w0 + kGroup; w += 2) {
+          if (!kF32) {
+            const uint32_t a[4] = {qw[0][w], qw[1][w], qw[0][w + 1], qw[1][w + 1]};
+#pragma unroll
+            for (int j = 0; j < kTogether; ++j) {
+              if (DT == DLRM_DTYPE_BF16)
+                mma_bf16(sc[j0 + j], a, kw[j][w - w0], kw[j][w - w0 + 1]);
+              else
+                mma_f16(sc[j0 + j], a, kw[j][w - w0], kw[j][w - w0 + 1]);
+            }
+          } else {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              hi[i] = qw[i & 1][w + (i >> 1)];
+              if (kSplitQ)
+                lo[i] = q_rest[i & 1][kSplitQ ? w + (i >> 1) : 0];
+              else
+                split_tf32(hi[i], hi[i], lo[i]);
+            }
+#pragma unroll
+            for (int j = 0; j < kTogether; ++j) {
+              uint32_t h0, h1, l0, l1;
+              split_tf32(kw[j][w - w0], h0, l0);
+              split_tf32(kw[j][w - w0 + 1], h1, l1);
+              mma_tf32(sc[j0 + j], lo, h0, h1);
+              mma_tf32(sc[j0 + j], hi, l0, l1);
+              mma_tf32(sc[j0 + j], hi, h0, h1);
+            }
           }
-          uint32_t h0, h1, l0, l1;
-          split_tf32(kw[w], h0, l0);
-          split_tf32(kw[w + 1], h1, l1);
-          mma_tf32(sc[j], lo, h0, h1);
-          mma_tf32(sc[j], hi, l0, l1);
-          mma_tf32(sc[j], hi, h0, h1);
         }
       }
     }
