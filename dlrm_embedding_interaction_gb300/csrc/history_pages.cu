@@ -751,32 +751,29 @@ __global__ void __launch_bounds__(kFreeThreads) push_kernel(Pool p, int batch, i
   }
 }
 
-// release, count and push in one CTA, with barriers for launches: a warp a
-// request. For calls of few pages three launches take longer than the work: 32
-// slots of up to 17 pages 7 us against 13; 16 of up to 64 pages 11 against 13 when
-// each launch is timed alone, and no faster when they overlap; 128 of up to 64 24
-// against 15.
-constexpr int kFreeSmallBatch = 256, kFreeSmallEntries = 768;
+// release, count and push in one CTA, with barriers for launches and a warp for each
+// request. us of a fork and a free, this way against three launches: 32 slots of up
+// to 32 pages 10.1 against 11.9, of up to 64 11.9 against 11.7; 16 of up to 64 10.9
+// against 11.5. With several requests a warp: 48 slots of up to 16 pages 12.9 against
+// 11.7, 256 of up to 3 31.7 against 13.8.
+constexpr int kFreeSmallBatch = kWarp, kFreeSmallEntries = 2048;
+static_assert(kFreeSmallBatch == kPlanThreads / kWarp, "a warp a request, a lane a request");
 
 __global__ void __launch_bounds__(kPlanThreads) free_small_kernel(Pool p, const int32_t* slots,
                                                                   int batch, int window, int sinks) {
-  __shared__ int slot_s[kFreeSmallBatch], first_s[kFreeSmallBatch], last_s[kFreeSmallBatch];
   __shared__ int freed_s[kFreeSmallBatch];
   const dlrm_history_t& h = p.h;
   const int G = h.page_tokens, M = h.max_pages;
-  const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp, warps = kPlanThreads / kWarp;
+  const int lane = threadIdx.x % kWarp, b = threadIdx.x / kWarp;
   pdl_wait();
   pdl_trigger();
   const int top = min(max(*h.n_free, 0), h.n_pages);
-  for (int b = threadIdx.x; b < batch; b += kPlanThreads) slot_s[b] = slots[b];
-  __syncthreads();
-  for (int b = warp; b < batch; b += warps) {
-    const int slot = slot_s[b];
+  int first = 0, last = 0;                        // pages [first, last) of request b's table go
+  if (b < batch) {
+    const int slot = slots[b];
     const bool in = slot >= 0 && slot < h.n_slots;
-    bool again = false;                           // listed before: nothing left
-    for (int i = lane; i < b; i += kWarp) again |= slot_s[i] == slot;
-    again = __any_sync(0xffffffffu, again);
-    int first = 0, last = 0;
+    // listed before: nothing left
+    const bool again = __any_sync(0xffffffffu, lane < b && slots[lane] == slot);
     if (in && !again) {
       const int64_t len = max(h.lengths[slot], 0);
       last = static_cast<int>(min((len + G - 1) / G, static_cast<int64_t>(M)));
@@ -787,11 +784,7 @@ __global__ void __launch_bounds__(kPlanThreads) free_small_kernel(Pool p, const 
                             : static_cast<int>(max((len - window) / G, static_cast<int64_t>(first)));
       }
     }
-    if (lane == 0) {
-      if (!in) flag(h.err, DLRM_ERRBIT_INDEX_OOB);
-      first_s[b] = first;
-      last_s[b] = last;
-    }
+    if (!in && lane == 0) flag(h.err, DLRM_ERRBIT_INDEX_OOB);
     for (int j = first + lane; j < last; j += kWarp) {
       const int64_t at = static_cast<int64_t>(slot) * M + j;
       int page = h.table[at];
@@ -804,12 +797,13 @@ __global__ void __launch_bounds__(kPlanThreads) free_small_kernel(Pool p, const 
       h.table[at] = -1;
       p.stash[b * M + j] = page;
     }
+    __syncwarp();
     if (window == 0 && in && !again && lane == 0) h.lengths[slot] = 0;
   }
   __threadfence_block();
   __syncthreads();
-  auto pushed = [&](int b, int j, int& page) {
-    page = j < last_s[b] ? __ldcg(&p.stash[b * M + j]) : -1;
+  auto pushed = [&](int j, int& page) {
+    page = j < last ? __ldcg(&p.stash[b * M + j]) : -1;
     if (page < 0) return false;
     if (__ldcg(&p.mark_page[page]) != b * M + j) {
       page = -1;
@@ -817,39 +811,28 @@ __global__ void __launch_bounds__(kPlanThreads) free_small_kernel(Pool p, const 
     }
     return __ldcg(&h.refs[page]) <= 0;
   };
-  for (int b = warp; b < batch; b += warps) {
-    int n = 0;
-    for (int j0 = first_s[b]; j0 < last_s[b]; j0 += kWarp) {
-      int page;
-      n += __popc(__ballot_sync(0xffffffffu, pushed(b, j0 + lane, page)));
-    }
-    if (lane == 0) freed_s[b] = n;
+  int left = 0;
+  for (int j0 = first; j0 < last; j0 += kWarp) {
+    int page;
+    left += __popc(__ballot_sync(0xffffffffu, pushed(j0 + lane, page)));
   }
+  if (lane == 0) freed_s[b] = left;
   __syncthreads();
-  int all = 0;
-  for (int b = warp; b < batch; b += warps) {
-    int later = 0;
-    all = 0;
-    for (int i = lane; i < batch; i += kWarp) {
-      later += i > b ? freed_s[i] : 0;
-      all += freed_s[i];
+  const int freed = freed_s[lane];                // of request `lane`; none past the batch
+  const int later = __reduce_add_sync(0xffffffffu, lane > b ? freed : 0);
+  const int all = __reduce_add_sync(0xffffffffu, freed);
+  for (int j0 = first; j0 < last; j0 += kWarp) {
+    int page;
+    const bool push = pushed(j0 + lane, page);
+    const unsigned who = __ballot_sync(0xffffffffu, push);
+    if (push) {
+      const int q = later + left - 1 - __popc(who & ((1u << lane) - 1));
+      if (top + q < h.n_pages) h.free_pages[top + q] = page;
+      h.refs[page] = 0;
     }
-    later = __reduce_add_sync(0xffffffffu, later);
-    all = __reduce_add_sync(0xffffffffu, all);
-    int left = freed_s[b];
-    for (int j0 = first_s[b]; j0 < last_s[b]; j0 += kWarp) {
-      int page;
-      const bool push = pushed(b, j0 + lane, page);
-      const unsigned who = __ballot_sync(0xffffffffu, push);
-      if (push) {
-        const int q = later + left - 1 - __popc(who & ((1u << lane) - 1));
-        if (top + q < h.n_pages) h.free_pages[top + q] = page;
-        h.refs[page] = 0;
-      }
-      // only its own position's reader can still ask for this mark
-      if (page >= 0) p.mark_page[page] = -1;
-      left -= __popc(who);
-    }
+    // only its own position's reader can still ask for this mark
+    if (page >= 0) p.mark_page[page] = -1;
+    left -= __popc(who);
   }
   if (threadIdx.x == 0) *h.n_free = min(top + all, h.n_pages);
 }
