@@ -49,7 +49,7 @@
 // PFLOP/s of visible products (52% of the bf16 rate); 64 users of 100 to 1024 events,
 // 8 heads of 64 over 2, window 256, bf16: 58 us, of which the first loads and the last
 // products of short units are 10K of 26K cycles a unit; PAGED, 16 users x up to 500
-// candidates over 1000 to 4096 events, 4 heads of 64 over 2: 66 us, 0.27 PFLOP/s.
+// candidates over 1000 to 4096 events, 4 heads of 64 over 2: 63 us, 0.28 PFLOP/s.
 //
 // Every wait is bounded (WaitCfg); on expiry DLRM_ERRBIT_TIMEOUT is set, every
 // role leaves its loop, work in flight is waited for and the tensor memory freed.
@@ -1096,7 +1096,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
       float ks[kPer], vs[kPer];
     };
     const int tid = threadIdx.x - 384;
-    const int G = p.h.page_tokens;
+    const int G = p.h.page_tokens, shift = __ffs(G) - 1;   // a power of two
     uint32_t it = 0;
     bool ok = true;
     for (const Unit* x; ok && (x = units.next_warp()); units.done_warp()) {
@@ -1122,10 +1122,10 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
           y.k[i] = y.v[i] = make_uint4(0, 0, 0, 0);
           y.ks[i] = y.vs[i] = 1.f;
           if (row < width && e < len) {
-            const int page = pages[e / G];
+            const int page = pages[e >> shift];
             if (page >= 0 && page < p.h.n_pages) {
               const int64_t at = static_cast<int64_t>(page) * p.h.n_heads + head;
-              const int64_t code = (at * G + e % G) * D + ch * 16;
+              const int64_t code = (at * G + (e & (G - 1))) * D + ch * 16;
               y.k[i] = __ldg(reinterpret_cast<const uint4*>(p.h.k_codes + code));
               y.v[i] = __ldg(reinterpret_cast<const uint4*>(p.h.v_codes + code));
               y.ks[i] = __ldg(p.h.k_scales + at);

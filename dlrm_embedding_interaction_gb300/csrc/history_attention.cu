@@ -40,9 +40,9 @@
 //
 // What bounds it: reading the codes (2 D bytes an event and kv head). Measured, one
 // query a user: 4 users of 65,000 to 100,001 events, 8 heads of 128, fp16, 123 us, 84%
-// of the copy rate; 64 users of 37 to 4096 events, 8 heads of 64 over 2, bf16, 24 us,
+// of the copy rate; 64 users of 37 to 4096 events, 8 heads of 64 over 2, bf16, 22 us,
 // half of it the start (the lengths of all requests, then table, then codes, each a
-// read that waits for the one before) and the join; one user of 150 events 9 us, all of
+// read that waits for the one before) and the join; one user of 150 events 5 us, all of
 // it start.
 #include <atomic>
 
@@ -236,8 +236,12 @@ struct Shape {
   static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
 };
 
+// Three CTAs an SM up to head_dim 64 (left to itself the compiler stops at 128 registers at
+// 32: 256 users, window 256, 13.0 us against 12.2, and spills at 64: 64 users 26.7
+// against 21.6), two at 128.
 template <int D, int DT>
-__global__ void __launch_bounds__(kThreads) history_attention_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 3)
+history_attention_kernel(const __grid_constant__ Params p) {
   using Sh = Shape<D, DT>;
   constexpr bool kSplit = Sh::kSplit;
   constexpr int kRows = Sh::kRows, kStages = Sh::kStages, kStride = Sh::kStride;
@@ -254,7 +258,7 @@ __global__ void __launch_bounds__(kThreads) history_attention_kernel(const __gri
 
   const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
   const int g = lane / 4, c = lane % 4;
-  const int G = p.h.page_tokens, H = p.h.n_heads;
+  const int G = p.h.page_tokens, H = p.h.n_heads, shift = __ffs(G) - 1;   // G: a power of two
   unsigned char* ring = smem + warp * kStages * Sh::kBytes;
   const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
   pdl_wait();
@@ -343,7 +347,7 @@ __global__ void __launch_bounds__(kThreads) history_attention_kernel(const __gri
         const int t0 = first_event(i);
         // not what no row of the tile sees
         if (t0 < v_last.end && !(t0 >= v_last.gap0 && t0 + kBlock <= v_first.gap1)) {
-          x.page = pages[t0 / G];
+          x.page = pages[t0 >> shift];
           if (x.page < 0 || x.page >= p.h.n_pages) {
             // trimmed, or a broken table: events that some row needs
             x.page = -1;
@@ -363,7 +367,7 @@ __global__ void __launch_bounds__(kThreads) history_attention_kernel(const __gri
       if (i < count) {
         const int page = __shfl_sync(0xffffffffu, i - base < kWarp ? info.page : ahead.page, i % kWarp);
         if (page >= 0) {
-          const int64_t codes = ((static_cast<int64_t>(page) * H + head) * G + first_event(i) % G) * D;
+          const int64_t codes = ((static_cast<int64_t>(page) * H + head) * G + (first_event(i) & (G - 1))) * D;
           const uint32_t dst = ring_at + (i % kStages) * Sh::kBytes;
 #pragma unroll
           for (int x = 0; x < 2 * D / 32; ++x) {
