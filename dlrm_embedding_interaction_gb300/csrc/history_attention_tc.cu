@@ -11,11 +11,12 @@ namespace dlrm {
 // From this many rows of a request and kv head on average, and of all together,
 // this kernel is faster than history_attention.cu's. us at head_dim 64 (128), two
 // kv heads, this kernel against that one:
-//   64 users x 1024 events, 64 rows each: 25 against 31 (40 against 53);
-//     32 rows: 25 against 25 (40 against 34)
-//   16 users x 4096 events, 128 rows: 34 against 41 (52 against 62);
-//     64 rows (2048 in all): 34 against 30 (51 against 44)
-//   1 user x 4096 events, 1024 rows (2048 in all): 36 against 30 (54 against 44)
+//   64 users x 1024 events, 64 rows each: 23 against 29 (35 against 52);
+//     32 rows: 23 against 24 (35 against 34)
+//   16 users x 4096 events, 128 rows: 33 against 39 (47 against 61);
+//     64 rows (2048 in all): 32 against 28 (46 against 43)
+//   16 users x 256 events, 128 rows: 10.9 against 10.4 (15.2 against 14.6)
+//   1 user x 4096 events, 1024 rows (2048 in all): 35 against 28 (50 against 43)
 constexpr int kManyRows = 64, kManyInAll = 4096;
 
 bool history_tc_takes(const dlrm_history_t& h, const dlrm_attention_t& a) {
