@@ -169,9 +169,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Pool p, const int32_
     const int b = b0 + static_cast<int>(threadIdx.x);
     Request r{-1, -1, 0, 0, 0, 0, 0, 0};
     uint32_t bad = 0;
+    bool marked = false;                          // the mark of its slot is this request's
     if (b < batch) {
       const int d = dst[b], s = OP == kAppend ? d : src[b];
-      const bool first = d < 0 || d >= h.n_slots || __ldcg(&p.mark_slot[d]) == b;
+      const bool in = d >= 0 && d < h.n_slots;
+      marked = in && __ldcg(&p.mark_slot[d]) == b;
+      const bool first = !in || marked;
       r = request_of<OP>(p, s, d, first, starts, b, rows, bad);
     }
     if (bad) {
@@ -214,7 +217,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Pool p, const int32_
     }
     if (b < batch) {
       p.request[b] = r;
-      if (r.source >= 0) p.mark_slot[dst[b]] = INT32_MAX;   // this request's own mark
+      // every reading of a mark lies before the barriers of the sum: the next call finds
+      // none, whatever became of this request
+      if (marked) p.mark_slot[dst[b]] = INT32_MAX;
     }
     if (OP == kAppend) {
       // work items (request, page of the history); long lists by the whole warp
