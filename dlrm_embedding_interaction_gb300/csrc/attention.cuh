@@ -64,7 +64,9 @@ __device__ __forceinline__ Visible visible(int pos, int len, int window, int sin
   v.end = max(min(len, pos + 1), 0);
   v.gap0 = v.gap1 = 0;
   if (window > 0) {
-    v.gap1 = max(pos - window + 1, 0);
+    // (a row before the first event, of more queries than events, has no gap, and its
+    // window may begin below -2^31)
+    v.gap1 = max(max(pos, 0) - window + 1, 0);
     v.gap0 = min(sinks, v.gap1);
   }
   return v;

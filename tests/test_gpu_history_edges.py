@@ -74,3 +74,22 @@ def test_a_refused_fork_of_many_leaves_nothing_behind(batch):
         assert cache.error() == dl.OK
         dl.history_free(cache, i32(dst))
         pool.release(dst)
+
+
+# ------------------------------------------------------------------ windows
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("dim", [32, 64, 128])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 40])
+def test_the_largest_window_with_more_queries_than_events(dtype, dim, window):
+    """The first rows stand before the first event: such a window's start lies below -2^31."""
+    rng = np.random.default_rng(41)
+    for counts, lens in (([4, 70, 300], [1, 20, 150]), ([33], [1])):
+        for sinks in (0, 2, 2 ** 31 - 1):
+            base.check_window(rng, counts, lens, 4, 2, dim, dtype, window, sinks)
+    lens, counts = [1, 20, 150, 700], [4, 70, 300, 710]
+    cache, pool = make(20, 4, 11, 2, dim, 64)
+    fill(cache, pool, rng, [0, 1, 2, 3], lens)
+    for n in (1, 3, 4):                             # the last: enough rows for the tensor-core kernel
+        base.check_attention(cache, pool, rng, list(range(n)), counts[:n], 4, dtype, True, window, 1)
+    assert cache.error() == dl.OK
