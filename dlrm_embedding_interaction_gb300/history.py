@@ -82,9 +82,17 @@ def _dtype_code(t, name: str) -> int:
     return code
 
 
+def _current_device() -> int:
+    return torch._C._cuda_getDevice()
+
+
 def _raw_stream(stream, index: int):
     """The cudaStream_t of ``stream``, or of device ``index``'s current stream (read
-    without making a Stream object, which takes microseconds)."""
+    without making a Stream object, which takes microseconds). A launch goes to the
+    current device, so that has to be the tensors'."""
+    if index != _current_device():
+        raise ValueError(f"the tensors are on device {index}, the current device is {_current_device()}: "
+                         "make theirs current (torch.cuda.device)")
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(index)
     return _stream(stream)
@@ -135,7 +143,8 @@ class HistoryCache:
     histories of at most ``max_pages`` pages each. The tensors (``k_codes``,
     ``v_codes``, ``k_scales``, ``v_scales``, ``table``, ``lengths``, ``refs``,
     ``free_pages``, ``n_free``, ``err``) are the caller's to read, e.g. to save
-    a pool; calls on one cache go to one stream.
+    a pool; calls on one cache go to one stream. Its device has to be the current one,
+    here and in every call.
     """
 
     def __init__(self, n_pages: int, n_slots: int, max_pages: int, n_heads: int, head_dim: int,
@@ -143,6 +152,8 @@ class HistoryCache:
         device = torch.device(device)
         if device.type != "cuda":
             raise ValueError("HistoryCache: device must be a CUDA device")
+        if device.index is not None and device.index != torch.cuda.current_device():
+            raise ValueError(f"HistoryCache: {device} is not the current device: make it so (torch.cuda.device)")
         c = _History(int(n_pages), int(page_tokens), int(n_heads), int(head_dim), int(n_slots),
                      int(max_pages))
         bound = _bound()
