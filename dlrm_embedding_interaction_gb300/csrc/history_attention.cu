@@ -756,17 +756,27 @@ template <int D, int DT>
 cudaError_t launch(const Params& p, cudaStream_t stream) {
   using Sh = Shape<D, DT>;
   constexpr int kRows = Sh::kRows;
-  static std::atomic<int> resident{0};            // CTAs of an SM: the same for every GB300
-  int per_sm = resident.load(std::memory_order_relaxed);
-  if (per_sm == 0) {
-    cudaError_t e = cudaFuncSetAttribute(history_attention_kernel<D, DT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+  // The shared memory that the kernel may take is set once on every device, by a bit
+  // each; the CTAs of an SM are the same on every GB300.
+  static std::atomic<uint64_t> done{0};
+  static std::atomic<int> resident{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
+  int per_sm = 0;
+  if (!bit || !(done.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(history_attention_kernel<D, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Sh::kSmem);
     if (e != cudaSuccess) return e;
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, history_attention_kernel<D, DT>,
                                                       kThreads, Sh::kSmem);
     if (e != cudaSuccess) return e;
     per_sm = std::max(1, std::min(per_sm, kAttnMaxCtas / 152));
     resident.store(per_sm, std::memory_order_relaxed);
+    done.fetch_or(bit, std::memory_order_acq_rel);
+  } else {
+    per_sm = resident.load(std::memory_order_relaxed);
   }
   // no more CTAs than chunks there can be
   const int64_t chunk = kWarps * kBlock;

@@ -1,0 +1,54 @@
+"""The launch code of the event-history operators on the host, against a stand-in for the
+CUDA runtime (fake_cudart.cpp): no kernel runs, no GPU is needed."""
+import ctypes
+import os
+import shutil
+import subprocess
+
+import pytest
+
+torch = pytest.importorskip("torch")
+import dlrm_embedding_interaction_gb300 as dl  # noqa: E402
+from dlrm_embedding_interaction_gb300 import history  # noqa: E402
+from test_history_checks import attention, pool  # noqa: E402
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+
+
+@pytest.fixture(scope="module")
+def lib(tmp_path_factory):
+    """The library's own objects over the stand-in."""
+    from dlrm_embedding_interaction_gb300 import build
+    if not (shutil.which("g++") and os.path.exists(build.nvcc())):
+        pytest.skip("no compilers")
+    build.build()
+    out = str(tmp_path_factory.mktemp("fake") / "libfake.so")
+    include = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(build.nvcc()))), "include")
+    objects = [os.path.join(build.OBJ_DIR, os.path.basename(s)[:-3] + ".o") for s in build.sources()]
+    # what the stand-in lacks is not called here: left unresolved
+    r = subprocess.run(["g++", "-std=c++17", "-O1", "-fPIC", "-shared", "-I", include, "-Wl,-z,lazy",
+                        "-Wl,-Bsymbolic", os.path.join(HERE, "fake_cudart.cpp"), *objects, "-o", out],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-2000:]
+    lib = ctypes.CDLL(out, mode=os.RTLD_LAZY | os.RTLD_LOCAL)
+    history._bind(lib)
+    return lib
+
+
+@pytest.mark.parametrize("head_dim", [32, 64, 128])
+@pytest.mark.parametrize("dtype", [0, 1, 2])
+@pytest.mark.parametrize("rows", [5, 5000])
+def test_attention_launches_on_every_device_of_a_process(lib, head_dim, dtype, rows):
+    """The shared memory that a kernel may take is an attribute of each device."""
+    h = ctypes.byref(pool(head_dim=head_dim))
+    ld = 4 * head_dim
+    a = ctypes.byref(attention(head_dim=head_dim, dtype=dtype, q_rows=rows, k_rows=rows, ld_q=ld,
+                               ld_q_head=head_dim, ld_out=ld, ld_out_head=head_dim, ld_k=ld // 2,
+                               ld_k_head=head_dim, ld_v=ld // 2, ld_v_head=head_dim))
+    for device in (0, 1, 0, 2, 63, 64, 65):
+        lib.fake_set_device(device)
+        before = lib.fake_launches()
+        assert lib.history_attention(h, a, None) == dl.OK, device
+        assert lib.window_attention(a, None) == dl.OK, device
+        assert lib.fake_launches() == before + 2
+    lib.fake_set_device(0)
