@@ -74,6 +74,11 @@ __device__ __forceinline__ Visible visible(int pos, int len, int window, int sin
 __device__ __forceinline__ bool sees(const Visible& v, int t) {
   return t < v.end && (t < v.gap0 || t >= v.gap1);
 }
+// Any event at all: a row without weights is zeros if it sees none, else 0 / 0 (all its
+// scores are -infinity).
+__device__ __forceinline__ bool sees_any(const Visible& v) {
+  return v.end > 0 && (v.gap0 > 0 || v.gap1 < v.end);
+}
 
 // Finds where a CTA's work lies: request b has units(b) >= 0 units, and the
 // CTA wants the request that holds unit `target` of all of them, or wants the

@@ -559,6 +559,7 @@ __device__ __noinline__ void paged_careful_row(const TcParams& p, const WindowSp
     acc[e] = 0.f;
   }
   float top = -INFINITY, sum = 0.f;
+  bool any = false;                               // there are events to see
   for (int t = 0; t < v.end; ++t) {
     if (!sees(v, t)) {
       t = v.gap1 - 1;
@@ -566,6 +567,7 @@ __device__ __noinline__ void paged_careful_row(const TcParams& p, const WindowSp
     }
     const int page = pages[t / G];
     if (page < 0 || page >= p.h.n_pages) continue;
+    any = true;
     const int64_t at = static_cast<int64_t>(page) * p.h.n_heads + head;
     const int64_t c = (at * G + t % G) * D + lane;
     float x = 0.f;
@@ -590,10 +592,10 @@ __device__ __noinline__ void paged_careful_row(const TcParams& p, const WindowSp
   }
   const int64_t o = (s.q0 + static_cast<int64_t>(i)) * a.ld_out + hq * a.ld_out_head;
 #pragma unroll
-  for (int e = 0; e < N; ++e) store_element<DT>(a.out, o + lane + 32 * e, sum == 0.f ? 0.f : acc[e] / sum);
+  for (int e = 0; e < N; ++e) store_element<DT>(a.out, o + lane + 32 * e, any ? acc[e] / sum : 0.f);
   if (lane == 0 && a.lse)
     a.lse[(s.q0 + static_cast<int64_t>(i)) * a.n_heads + hq] =
-        sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
+        any ? (top == -INFINITY ? 0.f : top) * kLn2 + logf(sum) : -INFINITY;
 }
 
 // The products of tile T of every unit, by one lane. T is no template argument:
@@ -1069,6 +1071,8 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
       }
       if (mine && in && w.a.lse)
         w.a.lse[q * w.a.n_heads + hq] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
+      if (sum == 0.f)
+        odd |= sees_any(visible(x->pos0 + (!PAGED || w.a.causal ? i : 0), x->s.len, w.a.window, w.a.sinks));
       for (unsigned who = __ballot_sync(0xffffffffu, odd && in && mine); who; who &= who - 1) {
         __syncwarp();
         const int again = x->row0 + 128 * t + (warp & 3) * 32 + __ffs(who) - 1;

@@ -138,8 +138,8 @@ __device__ __forceinline__ int key_element(int c, int word) {
 }
 
 // One row of the tile from the definition, event by event, for a row whose
-// output is not finite: 0 * NaN of a masked event's value must not reach it.
-// One CTA, every thread.
+// output is not finite (0 * NaN of a masked event's value must not reach it), or that
+// sees events but found no weights. One CTA, every thread.
 template <int DT>
 __device__ __noinline__ void careful_row(const Params& p, const Span& s, int head, int row,
                                          float* sm) {
@@ -153,14 +153,17 @@ __device__ __noinline__ void careful_row(const Params& p, const Span& s, int hea
   float* red = sm + kThreads;
   auto code = [](uint8_t c) { return f16x2_to_float2(e4m3x2_to_f16x2(c)).x; };
   float top = -INFINITY, sum = 0.f, acc = 0.f;
+  bool any = false;                               // there are events to see
   const int d = threadIdx.x;
   for (int pass = 0; pass < 2; ++pass) {
     for (int t0 = 0; t0 < v.end; t0 += kThreads) {
       const int t = t0 + static_cast<int>(threadIdx.x);
       float x = -INFINITY;
+      bool there = false;
       if (t < v.end && sees(v, t)) {
         const int page = row_pages[t / G];
         if (page >= 0 && page < p.h.n_pages) {
+          there = true;
           const int64_t place = static_cast<int64_t>(page) * H + head;
           const uint8_t* k = p.h.k_codes + (place * G + t % G) * D;
           float dot = 0.f;
@@ -172,12 +175,13 @@ __device__ __noinline__ void careful_row(const Params& p, const Span& s, int hea
         top = (x > top || x != x) ? x : top;      // a NaN stays
       } else {
         __syncthreads();
-        prob[threadIdx.x] = x == -INFINITY ? -1.f : exp2f(x - top);
+        prob[threadIdx.x] = there ? exp2f(x - top) : -1.f;
         __syncthreads();
         const int n = min(kThreads, v.end - t0);
         for (int u = 0; u < n; ++u) {
           const float pr = prob[u];
           if (pr == -1.f) continue;
+          any = true;
           sum += pr;
           if (d < D) {
             const int page = row_pages[(t0 + u) / G];
@@ -200,10 +204,9 @@ __device__ __noinline__ void careful_row(const Params& p, const Span& s, int hea
     }
   }
   const int64_t o_at = (s.q0 + static_cast<int64_t>(i)) * p.a.ld_out + hq * p.a.ld_out_head;
-  if (d < D) store_element<DT>(p.a.out, o_at + d, sum == 0.f ? 0.f : acc / sum);
+  if (d < D) store_element<DT>(p.a.out, o_at + d, any ? acc / sum : 0.f);
   if (d == 0 && p.a.lse)
-    p.a.lse[(s.q0 + static_cast<int64_t>(i)) * p.a.n_heads + hq] =
-        sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
+    p.a.lse[(s.q0 + static_cast<int64_t>(i)) * p.a.n_heads + hq] = any ? top * kLn2 + logf(sum) : -INFINITY;
   __syncthreads();
 }
 
@@ -741,7 +744,9 @@ history_attention_kernel(const __grid_constant__ Params p) {
       store_element<DT>(p.a.out, i * p.a.ld_out + hq * p.a.ld_out_head + d, x);
       if (d == 0 && p.a.lse)
         p.a.lse[i * p.a.n_heads + hq] = l == 0.f ? -INFINITY : row_factor[r] * kLn2 + logf(l);
-      if (!finite(x)) odd[r] = odd[kRows] = 1;
+      if (!finite(x) || (l == 0.f && d == 0 &&
+                         sees_any(visible(pos0 + (p.a.causal ? row / p.group : 0), s.len, p.a.window, p.a.sinks))))
+        odd[r] = odd[kRows] = 1;
     }
     __syncthreads();
     if (odd[kRows]) {

@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kThreads) window_attention_kernel(const Params
     const int i = row / p.group, hq = head * p.group + row % p.group;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const int64_t at_o = (s.q0 + static_cast<int64_t>(i)) * p.a.ld_out + hq * p.a.ld_out_head;
-    bool bad = false;
+    bool bad = l == 0.f;                          // no events to see, or no weights: one look more
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll

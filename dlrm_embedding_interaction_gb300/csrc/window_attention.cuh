@@ -32,7 +32,8 @@ __device__ __forceinline__ WindowSpan window_span(const WindowParams& p, int b, 
 }
 
 // One row from the definition, event by event, by one warp: for a row whose
-// output is not finite (0 * a masked event's infinity or NaN).
+// output is not finite (0 * a masked event's infinity or NaN), or that sees events
+// but found no weights (scores of -infinity).
 template <int D, int DT>
 __device__ __noinline__ void window_careful_row(const WindowParams& p, const WindowSpan& s, int head, int row) {
   const int lane = threadIdx.x % kWarp;
@@ -47,12 +48,14 @@ __device__ __noinline__ void window_careful_row(const WindowParams& p, const Win
     acc[e] = 0.f;
   }
   float top = -INFINITY, sum = 0.f;
+  bool any = false;                               // there are events to see
   for (int t = 0; t < v.end; ++t) {
     if (!sees(v, t)) {
       t = v.gap1 - 1;
       continue;
     }
     const int64_t kt = s.k0 + static_cast<int64_t>(t);
+    any = true;
     float x = 0.f;
 #pragma unroll
     for (int e = 0; e < N; ++e)
@@ -75,10 +78,10 @@ __device__ __noinline__ void window_careful_row(const WindowParams& p, const Win
   }
   const int64_t o = (s.q0 + static_cast<int64_t>(i)) * p.a.ld_out + hq * p.a.ld_out_head;
 #pragma unroll
-  for (int e = 0; e < N; ++e) store_element<DT>(p.a.out, o + lane + 32 * e, sum == 0.f ? 0.f : acc[e] / sum);
+  for (int e = 0; e < N; ++e) store_element<DT>(p.a.out, o + lane + 32 * e, any ? acc[e] / sum : 0.f);
   if (lane == 0 && p.a.lse)
     p.a.lse[(s.q0 + static_cast<int64_t>(i)) * p.a.n_heads + hq] =
-        sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
+        any ? (top == -INFINITY ? 0.f : top) * kLn2 + logf(sum) : -INFINITY;
 }
 
 // The tcgen05 kernel: whether it takes this call, and its launch.

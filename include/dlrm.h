@@ -586,7 +586,8 @@ dlrm_status_t history_compact(const dlrm_history_t* h, void* stream);
  * Row i of a request's n rows over `len` events stands at position
  * len - n + i with causal != 0, else at len - 1. Event t is visible when
  * t < len, t <= position, and, with window > 0, t > position - window or
- * t < sinks. A row that sees nothing gets zeros and lse -infinity. Scores,
+ * t < sinks. A row that sees nothing gets zeros and lse -infinity; one that sees
+ * events whose scores are all -infinity is 0 / 0, NaN, with lse -infinity. Scores,
  * softmax statistics and sums are fp32; masked events have no influence,
  * whatever they hold.
  *   q, out  (q_rows, n_heads, head_dim) of dtype; (t, h, d) at

@@ -93,3 +93,47 @@ def test_the_largest_window_with_more_queries_than_events(dtype, dim, window):
     for n in (1, 3, 4):                             # the last: enough rows for the tensor-core kernel
         base.check_attention(cache, pool, rng, list(range(n)), counts[:n], 4, dtype, True, window, 1)
     assert cache.error() == dl.OK
+
+
+# ------------------------------------------------------------------ scores and weights
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("dim,n", [(32, 3), (64, 40), (64, 700), (128, 300)])
+def test_scores_of_minus_infinity_are_no_empty_rows(dtype, dim, n):
+    """A row all of whose visible scores are -infinity is 0 / 0, as its definition says, not
+    zeros like a row that sees nothing; with other events beside them they weigh nothing."""
+    rng = np.random.default_rng(42)
+    q, k, v = (rows(rng, n, h, dim, dtype, 0.3) for h in (4, 2, 2))
+    q[:, :, 3] = q[:, :, 3].abs() + 0.5
+    k[0, :, 3] = -float("inf")                      # what the first row sees
+    k[1, 0, 3] = -float("inf")
+    want, _ = ref.attention(f64(q), f64(k), f64(v), dim ** -0.5, True, 0, 0)
+    assert np.isnan(want[0]).all() and np.isnan(want[1, :2]).all() and np.isfinite(want[2:]).all()
+    lse = torch.empty(n, 4, device="cuda")
+    got = dl.window_attention(q, k, v, i32([0, n]), lse=lse)
+    np.testing.assert_array_equal(np.isnan(f64(got)), np.isnan(want))
+    assert (lse[0] == -float("inf")).all() and (lse[1, :2] == -float("inf")).all()
+    assert torch.isfinite(lse[1, 2:]).all() and torch.isfinite(lse[2:]).all()
+    eps = {"fp32": 2.0 ** -16, "fp16": 2.0 ** -11, "bf16": 2.0 ** -8}[dtype]
+    bound = eps * np.abs(f64(v)).max() + base.half_ulp(dtype) * np.abs(want[2:])
+    assert (np.abs(f64(got)[2:] - want[2:]) <= bound).all()
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("count", [1, 2100])
+def test_infinite_queries_over_a_cache(dtype, count):
+    """Codes hold no infinities, queries may: scores are then infinite of either sign, and NaN
+    where the code is zero."""
+    rng = np.random.default_rng(43)
+    cache, pool = make(8, 2, 4, 2, 64, 64)
+    one = torch.ones(5, 2, 64, device="cuda")
+    dl.history_append(cache, i32([0]), i32([0, 5]), one, one)
+    pool.append([0], [0, 5], (f64(one), f64(one)))
+    q = rows(rng, count, 4, 64, dtype, 0.3)
+    q[0, :, 7] = -float("inf")
+    q[count // 2, 1, 9] = float("inf")
+    k, v = pool.events(0)
+    want, _ = ref.attention(f64(q), k, v, 0.125, False, 0, 0)
+    assert np.isnan(want[0]).all() and np.isnan(want[count // 2, 1]).all()
+    got = dl.history_attention(cache, i32([0]), i32([0, count]), q)
+    np.testing.assert_array_equal(np.isnan(f64(got)), np.isnan(want))
