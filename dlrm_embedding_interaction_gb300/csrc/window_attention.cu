@@ -26,6 +26,12 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * kWarp;
 constexpr int kBlock = 32;
 constexpr int kTileRows = kWarps * 16;
+// fp32: blocks after which the sums leave the MMA's accumulators. An MMA cuts its sum off
+// where it should round, so a sum over 4096 events loses 2^-16 of itself, and one over
+// 65,000 2^-11.5. The sums so far wait in shared memory (registers are short; a second set
+// of sums in them took 30 us for 26 at head_dim 32) and are added with rounding: no
+// accumulator sums more than 15 blocks.
+constexpr int kFlush = 8;
 using Params = WindowParams;
 
 // x as a tf32 head and rest, each rounded to nearest: 22 bits of x in all. (The
@@ -66,8 +72,12 @@ __device__ __forceinline__ void load_row_words(uint32_t* w, const uint8_t* p, bo
   }
 }
 
+// fp32: four CTAs an SM at head_dim 32 (27.4 us with 8 bytes of spills against 26.5: 32
+// users, 4 heads, window 64); any number above, where the compiler would spill for a third
+// CTA (4096 events, window 512, head_dim 64: 121 us against 84).
 template <int D, int DT>
-__global__ void __launch_bounds__(kThreads) window_attention_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, DT != DLRM_DTYPE_FP32 ? 0 : D == 32 ? 4 : 1)
+window_attention_kernel(const Params p) {
   constexpr bool kF32 = DT == DLRM_DTYPE_FP32;
   constexpr int EB = kF32 ? 4 : 2;
   constexpr int EW = 4 / EB;                      // elements of a word
@@ -82,6 +92,8 @@ __global__ void __launch_bounds__(kThreads) window_attention_kernel(const Params
   constexpr bool kWholeRows = D == 32 || (D == 128 && !kF32);
   constexpr int kTogether = kWholeRows ? 1 : kBlock / 8, kGroup = kWholeRows ? KW : 4;
   __shared__ int64_t scan[40];
+  // the thread's sums so far, and the maxima that they are relative to
+  __shared__ float held[kF32 ? NT * 4 + 2 : 1][kThreads];
   const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
   const int g = lane / 4, c = lane % 4;
   const int heads = p.a.n_kv_heads;
@@ -142,6 +154,29 @@ __global__ void __launch_bounds__(kThreads) window_attention_kernel(const Params
                       (s.k0 * p.a.ld_v + head * p.a.ld_v_head + g * (D / 8)) * EB;
   const int64_t k_step = p.a.ld_k * EB, v_step = p.a.ld_v * EB;
 
+  bool holds = false;
+  // the sums, with those held: to be held, or (last) to stay
+  auto gather = [&](bool last) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const float f = holds ? exp2_approx(held[NT * 4 + r][threadIdx.x] - (top[r] == -INFINITY ? 0.f : top[r])) : 0.f;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 2 * r; i < 2 * r + 2; ++i) {
+          float& there = held[nt * 4 + i][threadIdx.x];
+          const float x = holds ? fmaf(there, f, o[nt][i]) : o[nt][i];
+          if (last) {
+            o[nt][i] = x;
+          } else {
+            there = x;
+            o[nt][i] = 0.f;
+          }
+        }
+      if (!last) held[NT * 4 + r][threadIdx.x] = top[r];
+    }
+    holds = true;
+  };
   for (int t0 = 0; t0 < v1.end; t0 += kBlock) {
     // past the sinks of every row and before the window of the first: skip to it
     if (t0 >= v1.gap0 && t0 + kBlock <= v0.gap1) {
@@ -288,8 +323,10 @@ __global__ void __launch_bounds__(kThreads) window_attention_kernel(const Params
           mma_tf32(o[w], hi, h0, h1);
         }
       }
+      if ((t0 & ((kFlush - 1) * kBlock)) == (kFlush - 1) * kBlock) gather(false);
     }
   }
+  if (kF32 && holds) gather(true);
 
   uint32_t odd = 0;                               // rows to be done again, by bit
 #pragma unroll

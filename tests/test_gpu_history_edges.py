@@ -137,3 +137,29 @@ def test_infinite_queries_over_a_cache(dtype, count):
     assert np.isnan(want[0]).all() and np.isnan(want[count // 2, 1]).all()
     got = dl.history_attention(cache, i32([0]), i32([0, count]), q)
     np.testing.assert_array_equal(np.isnan(f64(got)), np.isnan(want))
+
+
+@pytest.mark.parametrize("dim", [32, 64, 128])
+@pytest.mark.parametrize("n", [300, 4096, 16384, 65000])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (3000, 500)])
+def test_sums_of_fp32_over_many_events(dim, n, window, sinks):
+    """Values of one sign, where errors that point the same way add up: the output stays
+    within 2^-16 of them, however many events it sums."""
+    rng = np.random.default_rng(44)
+    q = rows(rng, 70, 2, dim, "fp32", 0.3)
+    k = rows(rng, n, 1, dim, "fp32", 0.3)
+    v = torch.from_numpy(rng.random((n, 1, dim)) + 1.0).float().cuda()
+    for rows_of in (1, 70):
+        x = q[:rows_of]
+        lse = torch.empty(rows_of, 2, device="cuda")
+        got = dl.window_attention(x, k, v, i32([0, rows_of]), k_starts=i32([0, n]), window=window, sinks=sinks,
+                                  lse=lse)
+        pos = torch.arange(n - rows_of, n, device="cuda")[:, None]
+        t = torch.arange(n, device="cuda")[None]
+        see = (t <= pos) & ((t > pos - window) | (t < sinks) if window else t >= 0)
+        s = torch.einsum("ihd,td->hit", x.double(), k[:, 0].double()) * dim ** -0.5
+        s = s.masked_fill(~see, -float("inf"))
+        want = torch.einsum("hit,td->ihd", s.softmax(-1), v[:, 0].double())
+        assert (got.double() - want).abs().max().item() <= 2.0 ** -16 * 2.0
+        sums = s.logsumexp(-1).T
+        assert ((lse.double() - sums).abs() <= 2.0 ** -17 * (1 + sums.abs())).all()
