@@ -78,6 +78,9 @@ constexpr int kQBlock = 128 * 128;               // 128 rows of 128 bytes (64 el
 constexpr int kBlockBytes = kKeys * 128;         // the same of a key tile
 constexpr int kStages = 4;                       // of keys, and of values
 constexpr float kSlack = 8.f;                    // log2 of the largest weight
+// ... and f16 weights are 2^kRaise times larger, as in kLift
+template <int DT>
+constexpr int kRaise = DT == DLRM_DTYPE_FP16 ? kLift - 8 : 0;
 
 // Resident CTAs of an SM, score buffers of a tile, tensor memory columns.
 template <int D, bool PAGED>
@@ -830,6 +833,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         auto raise = [&](float m) {
           const bool grow = m > top + kSlack || (top == -INFINITY && m > -INFINITY);
           if (__any_sync(0xffffffffu, grow)) {
+            if (kRaise<DT>) m = ceilf(m);
             const float alpha = grow ? exp2_approx(top - m) : 1.f;
             if (grow) top = m;
             sum *= alpha;
@@ -850,7 +854,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
               }
             }
           }
-          return top == -INFINITY ? 0.f : -top;
+          return top == -INFINITY ? 0.f : kRaise<DT> - top;
         };
         // 32 scores to 16 words of weights
         auto weigh = [&](uint32_t (&pw)[16], const uint32_t* s, float off) {
@@ -1070,7 +1074,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         }
       }
       if (mine && in && w.a.lse)
-        w.a.lse[q * w.a.n_heads + hq] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
+        w.a.lse[q * w.a.n_heads + hq] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum * pow2f(-kRaise<DT>));
       if (sum == 0.f)
         odd |= sees_any(visible(x->pos0 + (!PAGED || w.a.causal ? i : 0), x->s.len, w.a.window, w.a.sinks));
       for (unsigned who = __ballot_sync(0xffffffffu, odd && in && mine); who; who &= who - 1) {

@@ -76,6 +76,13 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return r;
 }
 
+// Weights that are rounded to f16 are made larger by a power of two (2^kLift of the
+// row's largest), as f16 has no normal numbers below 2^-14: the weights of a long history's
+// many events beside one that outweighs them would lose their bits there, or vanish. The
+// sums are those of the larger weights. A row's reference is a whole number, so that its
+// difference to kLift has no rounding.
+constexpr int kLift = 15;
+
 template <int DT>
 __device__ __forceinline__ float load_element(const void* p, int64_t i) {
   if (DT == DLRM_DTYPE_FP32) return static_cast<const float*>(p)[i];

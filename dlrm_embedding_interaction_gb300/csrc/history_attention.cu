@@ -36,7 +36,8 @@
 // Queries become f16 after a division by a power of two for each row. A bf16
 // or fp16 query and P (11 bits) take one MMA row: 16 rows a tile. An fp32
 // query is split into an f16 head and a rest of 11 more bits, which take two
-// MMA rows, and so is P: 8 rows a tile, errors as of fp32.
+// MMA rows, and so is P: 8 rows a tile, errors as of fp32. Weights are relative to a
+// whole number at or above the largest score, 2^15 times as large (kLift).
 //
 // What bounds it: reading the codes (2 D bytes an event and kv head). Measured, one
 // query a user: 4 users of 65,000 to 100,001 events, 8 heads of 128, fp16, 123 us, 84%
@@ -514,9 +515,9 @@ history_attention_kernel(const __grid_constant__ Params p) {
 #pragma unroll
       for (int r = 0; r < (kSplit ? 1 : 2); ++r) {
         const float f = r ? f1 : f0;
-        const float m = fmaxf(top[r], quad_max(big[r]) * f);
-        const float off = m == -INFINITY ? 0.f : -m;
-        alpha[r] = exp2_approx(top[r] + off);
+        const float m = fmaxf(top[r], ceilf(quad_max(big[r]) * f));
+        const float off = m == -INFINITY ? 0.f : kLift - m;
+        alpha[r] = m == -INFINITY ? 1.f : exp2_approx(top[r] - m);
         top[r] = m;
         float add = 0.f;
 #pragma unroll
@@ -743,7 +744,7 @@ history_attention_kernel(const __grid_constant__ Params p) {
       const int hq = head * p.group + row % p.group;
       store_element<DT>(p.a.out, i * p.a.ld_out + hq * p.a.ld_out_head + d, x);
       if (d == 0 && p.a.lse)
-        p.a.lse[i * p.a.n_heads + hq] = l == 0.f ? -INFINITY : row_factor[r] * kLn2 + logf(l);
+        p.a.lse[i * p.a.n_heads + hq] = l == 0.f ? -INFINITY : row_factor[r] * kLn2 + logf(l * pow2f(-kLift));
       if (!finite(x) || (l == 0.f && d == 0 &&
                          sees_any(visible(pos0 + (p.a.causal ? row / p.group : 0), s.len, p.a.window, p.a.sinks))))
         odd[r] = odd[kRows] = 1;

@@ -30,7 +30,8 @@ constexpr int kTileRows = kWarps * 16;
 // where it should round, so a sum over 4096 events loses 2^-16 of itself, and one over
 // 65,000 2^-11.5. The sums so far wait in shared memory (registers are short; a second set
 // of sums in them took 30 us for 26 at head_dim 32) and are added with rounding: no
-// accumulator sums more than 15 blocks.
+// accumulator sums more than 15 blocks. (The weights' sum goes with them: small ones are
+// added up before they meet a large one.)
 constexpr int kFlush = 8;
 using Params = WindowParams;
 
@@ -79,6 +80,7 @@ template <int D, int DT>
 __global__ void __launch_bounds__(kThreads, DT != DLRM_DTYPE_FP32 ? 0 : D == 32 ? 4 : 1)
 window_attention_kernel(const Params p) {
   constexpr bool kF32 = DT == DLRM_DTYPE_FP32;
+  constexpr int kRaise = DT == DLRM_DTYPE_FP16 ? kLift : 0;   // log2 of the largest weight
   constexpr int EB = kF32 ? 4 : 2;
   constexpr int EW = 4 / EB;                      // elements of a word
   constexpr int KW = D / 4 / EW;                  // words of a thread and row: D/4 elements
@@ -92,8 +94,9 @@ window_attention_kernel(const Params p) {
   constexpr bool kWholeRows = D == 32 || (D == 128 && !kF32);
   constexpr int kTogether = kWholeRows ? 1 : kBlock / 8, kGroup = kWholeRows ? KW : 4;
   __shared__ int64_t scan[40];
-  // the thread's sums so far, and the maxima that they are relative to
-  __shared__ float held[kF32 ? NT * 4 + 2 : 1][kThreads];
+  // the thread's sums so far, of values and of weights, and the maxima that they are
+  // relative to
+  __shared__ float held[kF32 ? NT * 4 + 4 : 1][kThreads];
   const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
   const int g = lane / 4, c = lane % 4;
   const int heads = p.a.n_kv_heads;
@@ -173,7 +176,13 @@ window_attention_kernel(const Params p) {
             o[nt][i] = 0.f;
           }
         }
-      if (!last) held[NT * 4 + r][threadIdx.x] = top[r];
+      float& weights = held[NT * 4 + 2 + r][threadIdx.x];
+      sum[r] = holds ? fmaf(weights, f, sum[r]) : sum[r];
+      if (!last) {
+        weights = sum[r];
+        sum[r] = 0.f;
+        held[NT * 4 + r][threadIdx.x] = top[r];
+      }
     }
     holds = true;
   };
@@ -249,9 +258,9 @@ window_attention_kernel(const Params p) {
     float alpha[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const float m = fmaxf(top[r], quad_max(big[r]));
-      const float base = m == -INFINITY ? 0.f : m;
-      alpha[r] = exp2_approx(top[r] - base);
+      const float most = quad_max(big[r]), m = fmaxf(top[r], kRaise ? ceilf(most) : most);
+      const float none = m == -INFINITY ? 0.f : m, base = none - kRaise;
+      alpha[r] = exp2_approx(top[r] - none);
       top[r] = m;
       float add = 0.f;
 #pragma unroll
@@ -349,7 +358,7 @@ window_attention_kernel(const Params p) {
     }
     if (in && c == 0 && p.a.lse)
       p.a.lse[(s.q0 + static_cast<int64_t>(i)) * p.a.n_heads + hq] =
-          l == 0.f ? -INFINITY : top[r] * kLn2 + logf(l);
+          l == 0.f ? -INFINITY : top[r] * kLn2 + logf(l * pow2f(-kRaise));
     const unsigned who = __ballot_sync(0xffffffffu, bad && in);
 #pragma unroll
     for (int x = 0; x < 8; ++x)

@@ -163,3 +163,34 @@ def test_sums_of_fp32_over_many_events(dim, n, window, sinks):
         assert (got.double() - want).abs().max().item() <= 2.0 ** -16 * 2.0
         sums = s.logsumexp(-1).T
         assert ((lse.double() - sums).abs() <= 2.0 ** -17 * (1 + sums.abs())).all()
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_many_small_weights_beside_a_large_one(dtype):
+    """One event outweighs each of 65,000 others by 2^25.2, yet together they have 0.16% of
+    the weight. Values are 0 for the one and 1 for the others, so the output is their share."""
+    n, dim = 65000, 64
+    for plain in (False, True):
+        k, v = torch.zeros(n, 1, dim, device="cuda"), torch.ones(n, 1, dim, device="cuda")
+        k[0, 0, 0], v[0] = 1.0, 0.0
+        q = torch.zeros(1 if not plain else 40, 1, dim, device="cuda")
+        q[:, 0, 0] = 17.5
+        rest = (n - 1 - (np.arange(len(q))[::-1] if plain else np.zeros(1))) * np.exp(-17.5)
+        want = rest / (1 + rest)
+        if plain:
+            q, k, v = (t.to(TYPES[dtype]) for t in (q, k, v))
+            outs = [dl.window_attention(q[-c:], k, v, i32([0, c]), k_starts=i32([0, n]), scale=1.0)
+                    for c in (1, 40)]               # up to head_dim 64 the number of rows picks the kernel
+        else:
+            cache = dl.HistoryCache(1100, 1, 1100, 1, dim)
+            dl.history_append(cache, i32([0]), i32([0, n]), k, v)
+            q = q.to(TYPES[dtype])
+            outs = [dl.history_attention(cache, i32([0]), i32([0, len(x)]), x, scale=1.0)
+                    for x in (q, q.expand(4200, 1, dim))]
+        # every weight is off by at most its rounding (2^-22, 2^-12 or 2^-9 of it, as the type
+        # of the weights may be), and so is their sum; and half an ulp of the output
+        eps = {"fp32": 2.0 ** -16, "fp16": 2.0 ** -11, "bf16": 2.0 ** -8}[dtype]
+        for out in outs:
+            share = want[-len(out):] if plain else want
+            err = np.abs(f64(out)[:, 0] - share[:, None])
+            assert (err <= (eps + base.half_ulp(dtype)) * share[:, None]).all(), (plain, len(out), err.max())
