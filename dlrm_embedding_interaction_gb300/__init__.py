@@ -35,7 +35,7 @@ EXPORTS = ("dlrm_version", "dlrm_status_string", "dlrm_create", "dlrm_forward",
            "dlrm_forward_kernels",
            "history_work_bytes", "history_reset", "history_append", "history_fork",
            "history_copy", "history_free", "history_trim", "history_compact",
-           "history_attention", "window_attention")
+           "history_attention", "window_attention", "attention_test_stall")
 NOALLOC_SCRATCH_BYTES = 16 << 20
 TRACE_SLOTS = 40
 
@@ -670,7 +670,7 @@ class DlrmModel:
 
 # The event-history operators (history.py), loaded on first use: like the rest
 # of the binding, importing the package does not import torch.
-_HISTORY = ("HistoryCache", "history_append", "history_attention", "history_compact",
+_HISTORY = ("HistoryCache", "attention_test_stall", "history_append", "history_attention", "history_compact",
             "history_copy", "history_fork", "history_free", "history_trim", "window_attention")
 
 

@@ -77,6 +77,7 @@ constexpr int kBox = 32;                         // events of one TMA box
 constexpr int kQBlock = 128 * 128;               // 128 rows of 128 bytes (64 elements)
 constexpr int kBlockBytes = kKeys * 128;         // the same of a key tile
 constexpr int kStages = 4;                       // of keys, and of values
+constexpr uint64_t kLandNs = 10000000;           // limit of a wait for work in flight
 constexpr float kSlack = 8.f;                    // log2 of the largest weight
 // ... and f16 weights are 2^kRaise times larger, as in kLift
 template <int DT>
@@ -195,11 +196,11 @@ struct Waiter {
     if (try_wait(smem_addr(bar), parity)) return true;
     return wait_slow(bar, parity, abort_flag, err, limit);
   }
-  // regardless of the abort flag: work in flight
+  // regardless of the abort flag and the limit: work in flight, which takes microseconds
   __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) const {
     const uint64_t t0 = now_ns();
     while (!try_wait(smem_addr(bar), parity)) {
-      if (now_ns() - t0 > limit) {
+      if (now_ns() - t0 > kLandNs) {
         flag(err, DLRM_ERRBIT_TIMEOUT);
         return;
       }
@@ -603,10 +604,11 @@ __device__ __noinline__ void paged_careful_row(const TcParams& p, const WindowSp
 
 // The products of tile T of every unit, by one lane. T is no template argument:
 // one copy of the code for both tiles keeps more of the kernel in the instruction
-// cache (16384 events 265 -> 260 us, the ragged batch 66 -> 63).
+// cache (16384 events 265 -> 260 us, the ragged batch 66 -> 63). Returns the phase of
+// q_full in which queries may still be landing, -1 for none.
 template <int D, int DT, bool PAGED>
-__device__ __forceinline__ void products(const int T, const TcParams& p, const CUtensorMap* map_q, Bars& bars,
-                                         const Waiter& wait, unsigned char* base, uint32_t tmem) {
+__device__ __forceinline__ int products(const int T, const TcParams& p, const CUtensorMap* map_q, Bars& bars,
+                                        const Waiter& wait, unsigned char* base, uint32_t tmem) {
   using L = Layout<D, PAGED>;
   constexpr int kFormat = DT == DLRM_DTYPE_BF16 ? 1 : 0;
   // D fp32; A, B formats; M = 128; B of the second product is MN-major
@@ -617,6 +619,7 @@ __device__ __forceinline__ void products(const int T, const TcParams& p, const C
   const uint32_t v_desc = values_desc(smem_addr(base + L::kV));
   const uint32_t o = tmem + L::o_col(T);
   uint32_t kv = 0, it = 0, units_done = 0;       // key tiles of the CTA, of this tile; its units
+  int landing = -1;
   Units units{bars, wait};
   for (const Unit* x; (x = units.next()); units.done()) {
     const Keys keys(*x);
@@ -628,6 +631,7 @@ __device__ __forceinline__ void products(const int T, const TcParams& p, const C
       for (int c = 0; c < L::kBlocks; ++c)
         tma_load_3d(smem_addr(base + L::kQ + T * L::kQTile + c * kQBlock), map_q, c * 64,
                     x->head * p.w.group, x->s.q0 + p.group(x->row0 + 128 * T), &bars.q_full[T]);
+      landing = units_done & 1;
     }
     bool due = false, begun = false, used_before = false, queried = false;
     int due_width = 0;
@@ -645,14 +649,12 @@ __device__ __forceinline__ void products(const int T, const TcParams& p, const C
       auto scores = [&]() -> bool {
         if (!used) return true;
         const uint32_t st = kv % kStages;
-        bool ok = wait(&bars.k_full[st], (kv / kStages) & 1);
-        // (queries in flight land before anything gives up)
+        if (!wait(&bars.k_full[st], (kv / kStages) & 1)) return false;
         if (need && !queried) {
-          if (ok) ok = wait(&bars.q_full[T], units_done & 1);
-          if (!ok && p.q_tma) wait.drain(&bars.q_full[T], units_done & 1);
+          if (!wait(&bars.q_full[T], units_done & 1)) return false;
+          landing = -1;
           queried = true;
         }
-        if (!ok) return false;
         if (need) {
           // the old scores have been read: their weights have arrived. Where those
           // lie over them they must have been used too: products of different shapes
@@ -703,9 +705,9 @@ __device__ __forceinline__ void products(const int T, const TcParams& p, const C
         return true;
       };
       if (L::kB == 1) {
-        if (!outputs() || !scores()) return;
+        if (!outputs() || !scores()) return landing;
       } else {
-        if (!scores() || !outputs()) return;
+        if (!scores() || !outputs()) return landing;
       }
       kv += used ? 1 : 0;
       it += need ? 1 : 0;
@@ -715,6 +717,7 @@ __device__ __forceinline__ void products(const int T, const TcParams& p, const C
     }
     units_done += begun ? 1 : 0;
   }
+  return landing;
 }
 
 template <int D, int DT, bool PAGED>
@@ -1090,8 +1093,10 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
     // ------------------------------------------------------------ products
     const int t = warp - 8;
     if (elect_one()) {
-      products<D, DT, PAGED>(t, p, &map_q, bars, wait, base, tmem);
-      // nothing of the tensor core's may be in flight when its memory is freed
+      const int landing = products<D, DT, PAGED>(t, p, &map_q, bars, wait, base, tmem);
+      // neither queries nor anything of the tensor core's may be in flight when its
+      // memory is freed
+      if (landing >= 0) wait.drain(&bars.q_full[t], landing);
       mma_commit(smem_addr(&bars.drain[t]));
       wait.drain(&bars.drain[t], 0);
     }
@@ -1218,21 +1223,20 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
           ++it;
         }
       }
-      // loads in flight must land before the shared memory is released; after
-      // a wait that gave up, the keys of a stage may be loaded and its values not
-      const uint32_t from = it > kStages ? it - kStages : 0;
-      for (uint32_t q = from; ok && q < it; ++q) {
+      // loads in flight must land before the shared memory is released: the last of
+      // every stage, and of the tile at which a wait gave up perhaps the keys (if they were
+      // not asked for, this wait runs out too)
+      const uint32_t to = ok ? it : it - 1;
+      for (uint32_t q = to > kStages ? to - kStages : 0; q < it; ++q) {
         wait.drain(&bars.k_full[q % kStages], (q / kStages) & 1);
-        wait.drain(&bars.v_full[q % kStages], (q / kStages) & 1);
-      }
-      if (!ok) {
-        const uint64_t t0 = now_ns();
-        while (now_ns() - t0 < 1000000) {}        // landed long before
+        if (q < to) wait.drain(&bars.v_full[q % kStages], (q / kStages) & 1);
       }
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------ units
+    // (failure tests: the first CTA never hears of its first one)
+    auto withhold = [&](int it) { return it == 0 && p.wait.withhold_last && blockIdx.x == 0; };
     if (!PAGED) {
       Walk walk;
       for (int it = 0, u = blockIdx.x;; ++it, u += gridDim.x) {
@@ -1244,7 +1248,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         __syncwarp();
         const bool valid = bars.units[slot].valid != 0;
         __syncwarp();
-        if (lane == 0) bar_arrive(&bars.u_full[slot]);
+        if (lane == 0 && !withhold(it)) bar_arrive(&bars.u_full[slot]);
         if (!valid) break;
       }
     } else if (lane == 0) {
@@ -1290,7 +1294,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         x.parts = from > 0 || to < each ? cuts.owner(unit0 + each - 1) - x.part0 + 1 : 1;
         x.place = from > 0 ? 0 : 1;
         out = x;
-        bar_arrive(&bars.u_full[slot]);
+        if (!withhold(it)) bar_arrive(&bars.u_full[slot]);
         u += to - from;
       }
     }
@@ -1354,6 +1358,7 @@ bool tma_rows(const void* x, int64_t ld, int64_t ld_head, int heads, int dim) {
 
 // What both calls give the kernel; false where the driver refuses a tensor map.
 bool fill_params(TcParams& p, CUtensorMap& map_q, const dlrm_attention_t& a) {
+  p.wait = attention_wait();
   p.w.a = a;
   p.w.group = a.n_heads / a.n_kv_heads;
   p.w.vec = 1;

@@ -179,5 +179,6 @@ bool history_tc_takes(const dlrm_history_t& h, const dlrm_attention_t& a);
 cudaError_t launch_history_attention_tc(const dlrm_history_t& h, const dlrm_attention_t& a,
                                         int32_t* counters, float* partials, cudaStream_t stream);
 cudaError_t launch_window_attention(const dlrm_attention_t& a, cudaStream_t stream);
+WaitCfg attention_wait();                        // attention_test_stall's
 
 }  // namespace dlrm

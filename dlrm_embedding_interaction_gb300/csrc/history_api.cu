@@ -1,8 +1,13 @@
 // The C ABI of the event-history operators (include/dlrm.h): argument checks
 // and launches.
+#include <atomic>
+
 #include "history.cuh"
 
 namespace {
+
+std::atomic<int64_t> stall_limit_ns{0};
+std::atomic<int32_t> stall_withhold{0};
 
 using dlrm::aligned_to;
 
@@ -74,7 +79,23 @@ dlrm_status_t check_attention(const dlrm_attention_t* a, int kv_heads, bool* run
 
 }  // namespace
 
+namespace dlrm {
+WaitCfg attention_wait() {
+  WaitCfg w;
+  w.limit_ns = static_cast<uint64_t>(stall_limit_ns.load(std::memory_order_relaxed));
+  w.withhold_last = stall_withhold.load(std::memory_order_relaxed);
+  return w;
+}
+}  // namespace dlrm
+
 extern "C" {
+
+dlrm_status_t attention_test_stall(int64_t wait_limit_ns, int32_t withhold) {
+  if (wait_limit_ns < 0) return DLRM_ERR_INVALID_ARG;
+  stall_limit_ns.store(wait_limit_ns, std::memory_order_relaxed);
+  stall_withhold.store(withhold, std::memory_order_relaxed);
+  return DLRM_OK;
+}
 
 int64_t history_work_bytes(const dlrm_history_t* h) {
   return check_shape(h) == DLRM_OK ? dlrm::history_work(*h).total : -1;

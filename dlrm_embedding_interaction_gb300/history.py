@@ -66,6 +66,7 @@ def _bind(lib_):
         "history_compact": ([h, _VP], st),
         "history_attention": ([h, a, _VP], st),
         "window_attention": ([a, _VP], st),
+        "attention_test_stall": ([_I64, _I32], st),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib_, name)
@@ -352,7 +353,8 @@ def window_attention(q, k, v, starts, out=None, *, k_starts=None, scale=None, wi
     head_dim) and the rows [k_starts[b], k_starts[b+1]) of ``k`` and ``v`` (rows,
     kv heads, head_dim); ``k_starts`` defaults to ``starts``. Its queries stand at
     the last positions of its keys. ``window``, ``sinks``, ``scale`` and ``lse`` as in
-    history_attention. ``err_flag``: (1,) int32, receives the error bit of bad starts."""
+    history_attention. ``err_flag``: (1,) int32, receives the error bits of bad starts and
+    of a wait that ran out."""
     where = "window_attention"
     for t, name in ((q, "q"), (k, "k"), (v, "v")):
         if not isinstance(t, torch.Tensor):
@@ -389,3 +391,11 @@ def window_attention(q, k, v, starts, out=None, *, k_starts=None, scale=None, wi
         0 if err_flag is None else err_flag.data_ptr())
     _check(_bound().window_attention(args, _raw_stream(stream, index)), where)
     return out
+
+
+def attention_test_stall(wait_limit_ns: int = 0, withhold: bool = False) -> None:
+    """Failure-detection test hook: the limit of the bounded device waits of later
+    attention calls (0: the default) and, with ``withhold``, a piece of work is kept back, so
+    that the wait on it runs out (TIMEOUT in the cache's error word, or in ``err_flag``).
+    ``attention_test_stall()`` restores normal operation."""
+    _check(_bound().attention_test_stall(int(wait_limit_ns), 1 if withhold else 0), "attention_test_stall")

@@ -620,6 +620,17 @@ typedef struct {
 dlrm_status_t history_attention(const dlrm_history_t* h, const dlrm_attention_t* a, void* stream);
 dlrm_status_t window_attention(const dlrm_attention_t* a, void* stream);
 
+/* Test hook of the failure detection, as dlrm_test_stall, for later calls of both
+ * in this process. Their tensor-core kernels' waits are bounded: on expiry the
+ * kernel sets DLRM_ERRBIT_TIMEOUT (in the pool's err; of window_attention in err,
+ * without which nothing tells), waits (bounded) for its copies and tensor-core
+ * work, frees its tensor memory and returns. Outputs of such a call are undefined.
+ * wait_limit_ns: the limit of those waits (0: the default, 2 s; waits for work in
+ * flight have one of their own, 10 ms); withhold != 0: the first CTA keeps its first
+ * piece of work back. (0, 0) restores normal operation. INVALID_ARG for a negative
+ * limit. */
+dlrm_status_t attention_test_stall(int64_t wait_limit_ns, int32_t withhold);
+
 #ifdef __cplusplus
 }
 #endif

@@ -194,3 +194,73 @@ def test_many_small_weights_beside_a_large_one(dtype):
             share = want[-len(out):] if plain else want
             err = np.abs(f64(out)[:, 0] - share[:, None])
             assert (err <= (eps + base.half_ulp(dtype)) * share[:, None]).all(), (plain, len(out), err.max())
+
+
+# ------------------------------------------------------------------ waits that run out
+
+LIMIT_NS = 2_000_000      # 2 ms: far above any wait of a healthy call here
+
+
+def stalled(call, error):
+    """call(), with a piece of its work withheld: TIMEOUT after the limit, not the default's 2 s."""
+    import time
+    dl.attention_test_stall(LIMIT_NS, False)
+    call()
+    assert error() == dl.OK
+    dl.attention_test_stall(LIMIT_NS, True)
+    try:
+        torch.cuda.synchronize()
+        t0 = time.perf_counter()
+        call()
+        status = error()                            # waits for the GPU
+        elapsed = time.perf_counter() - t0
+    finally:
+        dl.attention_test_stall()
+    assert status == dl.ERR_TIMEOUT
+    assert elapsed < 0.5, elapsed
+
+
+@pytest.mark.parametrize("dim", [32, 64, 128])
+@pytest.mark.parametrize("counts", [[700], [40, 300, 5000, 64, 1000]])
+def test_a_wait_of_window_attention_that_runs_out_reports_timeout(dim, counts):
+    rng = np.random.default_rng(45)
+    n = sum(counts)
+    q, k, v = (rows(rng, n, h, dim, "bf16", 0.3) for h in (4, 2, 2))
+    at, err = i32(starts_of(counts)), torch.zeros(1, dtype=torch.int32, device="cuda")
+    want = dl.window_attention(q, k, v, at, window=300, sinks=3)
+
+    def error():
+        bits = err.item()
+        err.zero_()
+        return dl.ERR_TIMEOUT if bits == 1 << dl.ERR_TIMEOUT else bits
+
+    stalled(lambda: dl.window_attention(q, k, v, at, window=300, sinks=3, err_flag=err), error)
+    for _ in range(3):
+        assert torch.equal(dl.window_attention(q, k, v, at, window=300, sinks=3, err_flag=err), want)
+    assert err.item() == 0
+
+
+@pytest.mark.parametrize("dim", [32, 64, 128])
+def test_window_attention_that_gives_up_in_the_middle(dim):
+    """A limit shorter than what its roles wait for one another in a long call: every CTA
+    gives up with copies in flight, and calls after it are as ever."""
+    rng = np.random.default_rng(46)
+    n = 16384                                       # more units a CTA than it knows ahead
+    q, k, v = (rows(rng, 3 * n, 8, dim, "bf16", 0.3) for _ in range(3))
+    at, err = i32([0, n, 2 * n, 3 * n]), torch.zeros(1, dtype=torch.int32, device="cuda")
+    want = dl.window_attention(q, k, v, at)
+    for limit in (20_000, 50_000, 100_000):
+        dl.attention_test_stall(limit)
+        try:
+            dl.window_attention(q, k, v, at, err_flag=err)
+            assert err.item() == 1 << dl.ERR_TIMEOUT
+        finally:
+            dl.attention_test_stall()
+        err.zero_()
+        assert torch.equal(dl.window_attention(q, k, v, at, err_flag=err), want)
+        assert err.item() == 0
+
+
+def test_the_stall_hook_checks_its_arguments():
+    with pytest.raises(dl.DlrmError):
+        dl.attention_test_stall(-1)
