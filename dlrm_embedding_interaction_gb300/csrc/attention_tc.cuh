@@ -482,6 +482,80 @@ struct Walk {
   }
 };
 
+// PAGED: key tiles that the rows of a request see, one at least: what a unit
+// counts when the work is cut. Units of up to kWhole are not split, and of longer
+// ones a CTA takes kLeast at least: one user x 4096 events x 128 rows takes 31 us in
+// parts of 16 key tiles, 121 in parts of one.
+constexpr int kWhole = 8, kLeast = 16;
+__device__ __forceinline__ int key_tiles(const TcParams& p, const WindowSpan& s) {
+  const dlrm_attention_t& a = p.w.a;
+  const int queries = p.group(s.rows);
+  const Visible first = visible(a.causal ? s.len - queries : s.len - 1, s.len, a.window, a.sinks);
+  const int sink = min(first.gap0, s.len), lo = first.gap1;
+  return max((sink + kKeys - 1) / kKeys + max(s.len - lo + kKeys - 1, 0) / kKeys, 1);
+}
+
+// PAGED: the units of a CTA's part of all key tiles in order, by one thread.
+struct PagedWalk {
+  int u = 0, end = 0, b = 0, first = 0, each = 1;
+  WindowSpan s{};
+
+  __device__ __forceinline__ PagedWalk(const TcParams& p, const Cuts& cuts, const Found<WindowSpan>& found) {
+    if (cuts.total == 0) return;
+    // a cut inside a short unit moves to the unit's start
+    auto snap = [&](int u, int i) {
+      const int each = key_tiles(p, found.span[i]);
+      return u >= cuts.total || each > kWhole ? u : u - (u - found.first[i]) % each;
+    };
+    u = snap(cuts.cut(blockIdx.x), 0);
+    end = snap(cuts.cut(blockIdx.x + 1), 1);
+    b = found.request[0];
+    first = found.first[0];
+    s = found.span[0];
+    each = key_tiles(p, s);
+  }
+  // false: no more
+  __device__ __forceinline__ bool next(const TcParams& p, const Cuts& cuts, Unit& x) {
+    if (u >= end) return false;
+    const int heads = p.w.a.n_kv_heads;
+    while (u - first >= s.tiles * heads * each) {
+      first += s.tiles * heads * each;
+      s = tc_span<true>(p, ++b, false);
+      each = key_tiles(p, s);
+    }
+    const int i = (u - first) / each, from = u - first - i * each;
+    const int to = min(each, from + end - u);
+    x = make_unit<true>(p, i, s);
+    // its part of the unit's own key tiles
+    const int64_t all = x.tiles;
+    x.begin = static_cast<int>(from * all / each);
+    x.tiles = static_cast<int>(to * all / each);
+    find_last(x);
+    const int unit0 = first + i * each;
+    x.part0 = cuts.owner(unit0);
+    x.parts = from > 0 || to < each ? cuts.owner(unit0 + each - 1) - x.part0 + 1 : 1;
+    x.place = from > 0 ? 0 : 1;
+    u += to - from;
+    return true;
+  }
+};
+
+// PAGED: a CTA that gave up still counts for the units that it shares, from the first that
+// each softmax warp has not finished on: counters are zero after every call. One thread.
+__device__ __noinline__ void count_given_up(const TcParams& p, const Cuts& cuts, const Found<WindowSpan>& found,
+                                            const int* finished) {
+  PagedWalk walk(p, cuts, found);
+  Unit x;
+  for (int n = 0; walk.next(p, cuts, x); ++n) {
+    if (x.parts == 1) continue;
+    for (int w = 0; w < 8; ++w) {
+      if (n < finished[w] || x.rows[w / 4] == 0) continue;
+      int32_t* counter = &p.counters[x.part0 * 8 + w];
+      if (atomicAdd(counter, 1) == x.parts - 1) *counter = 0;
+    }
+  }
+}
+
 // A warp's place in the ring of units; one lane of it may walk alone.
 struct Units {
   Bars& bars;
@@ -529,19 +603,6 @@ __device__ __forceinline__ bool elect_one() {
       "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok));
   return ok != 0;
-}
-
-// PAGED: key tiles that the rows of a request see, one at least: what a unit
-// counts when the work is cut. Units of up to kWhole are not split, and of longer
-// ones a CTA takes kLeast at least: one user x 4096 events x 128 rows takes 31 us in
-// parts of 16 key tiles, 121 in parts of one.
-constexpr int kWhole = 8, kLeast = 16;
-__device__ __forceinline__ int key_tiles(const TcParams& p, const WindowSpan& s) {
-  const dlrm_attention_t& a = p.w.a;
-  const int queries = p.group(s.rows);
-  const Visible first = visible(a.causal ? s.len - queries : s.len - 1, s.len, a.window, a.sinks);
-  const int sink = min(first.gap0, s.len), lo = first.gap1;
-  return max((sink + kKeys - 1) / kKeys + max(s.len - lo + kKeys - 1, 0) / kKeys, 1);
 }
 
 // PAGED: one row from the definition, by one warp, as window_careful_row.
@@ -775,6 +836,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
   // units count as if each had all the key tiles that any of its rows sees.
   __shared__ Found<WindowSpan> found;
   __shared__ int sums[kThreadsOf<PAGED> / kWarp * 2];
+  __shared__ int finished[8];                     // units that a softmax warp has finished
   Cuts cuts{};
   if (PAGED)
     cuts = locate_cuts<kThreadsOf<PAGED>>(
@@ -1089,6 +1151,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
           window_careful_row<D, DT>(w, x->s, x->head, again);
       }
     }
+    if (PAGED && lane == 0) finished[warp] = units.it;
   } else if (warp < 10) {
     // ------------------------------------------------------------ products
     const int t = warp - 8;
@@ -1252,50 +1315,18 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         if (!valid) break;
       }
     } else if (lane == 0) {
-      // a cut inside a short unit moves to the unit's start
-      auto snap = [&](int u, int i) {
-        const int each = key_tiles(p, found.span[i]);
-        return u >= cuts.total || each > kWhole ? u : u - (u - found.first[i]) % each;
-      };
-      int u = 0, end = 0, b = 0, first = 0, each = 1;
-      WindowSpan s{};
-      if (cuts.total > 0) {
-        u = snap(cuts.cut(blockIdx.x), 0);
-        end = snap(cuts.cut(blockIdx.x + 1), 1);
-        b = found.request[0];
-        first = found.first[0];
-        s = found.span[0];
-        each = key_tiles(p, s);
-      }
+      PagedWalk walk(p, cuts, found);
       for (int it = 0;; ++it) {
         const int slot = it % kUnits;
         if (it >= kUnits && !wait(&bars.u_empty[slot], ((it / kUnits) & 1) ^ 1)) break;
-        Unit& out = bars.units[slot];
-        if (u >= end) {
-          out.valid = 0;
-          bar_arrive(&bars.u_full[slot]);
-          break;
-        }
-        while (u - first >= s.tiles * w.a.n_kv_heads * each) {
-          first += s.tiles * w.a.n_kv_heads * each;
-          s = tc_span<PAGED>(p, ++b, false);
-          each = key_tiles(p, s);
-        }
-        const int i = (u - first) / each, from = u - first - i * each;
-        const int to = min(each, from + end - u);
-        Unit x = make_unit<PAGED>(p, i, s);
-        // its part of the unit's own key tiles
-        const int64_t all = x.tiles;
-        x.begin = static_cast<int>(from * all / each);
-        x.tiles = static_cast<int>(to * all / each);
-        find_last(x);
-        const int unit0 = first + i * each;
-        x.part0 = cuts.owner(unit0);
-        x.parts = from > 0 || to < each ? cuts.owner(unit0 + each - 1) - x.part0 + 1 : 1;
-        x.place = from > 0 ? 0 : 1;
-        out = x;
+        Unit x;
+        const bool more = walk.next(p, cuts, x);
+        if (more)
+          bars.units[slot] = x;
+        else
+          bars.units[slot].valid = 0;
         if (!withhold(it)) bar_arrive(&bars.u_full[slot]);
-        u += to - from;
+        if (!more) break;
       }
     }
     __syncwarp();
@@ -1304,6 +1335,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
   }
   fence_before();
   __syncthreads();
+  if (PAGED && bars.abort && threadIdx.x == 0) count_given_up(p, cuts, found, finished);
   if (warp == 8) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(L::kColumns)

@@ -261,6 +261,33 @@ def test_window_attention_that_gives_up_in_the_middle(dim):
         assert err.item() == 0
 
 
+@pytest.mark.parametrize("dim", [32, 64, 128])
+@pytest.mark.parametrize("lens,counts", [([6000], [2100]), ([3000, 64, 5000, 900], [700, 1000, 500, 300])])
+def test_a_cache_is_as_ever_after_a_wait_that_ran_out(dim, lens, counts):
+    """Units that CTAs share: those that did their part must not count for the next call."""
+    rng = np.random.default_rng(47)
+    cache, pool = make(2 + sum(-(-n // 64) for n in lens), len(lens), 100, 2, dim, 64)
+    fill(cache, pool, rng, list(range(len(lens))), lens)
+    slots, at = i32(range(len(lens))), i32(starts_of(counts))
+    q = rows(rng, sum(counts), 4, dim, "bf16", 0.3)
+    one = rows(rng, len(lens), 4, dim, "bf16", 0.3)
+
+    def many():
+        return dl.history_attention(cache, slots, at, q)
+
+    def few():                                      # the other kernel, over the same scratch
+        return dl.history_attention(cache, slots, i32(range(len(lens) + 1)), one)
+
+    want, want_few = many(), few()
+    for turn in range(2):
+        stalled(many, cache.error)
+        for _ in range(2):
+            got, got_few = (many(), few()) if turn else (few(), many())[::-1]
+            assert torch.equal(got_few, want_few)
+            assert torch.equal(got, want)
+        assert cache.error() == dl.OK
+
+
 def test_the_stall_hook_checks_its_arguments():
     with pytest.raises(dl.DlrmError):
         dl.attention_test_stall(-1)
