@@ -130,8 +130,15 @@ __device__ __forceinline__ void locate(int batch, const F& units, int64_t target
   first = shared[37];
 }
 
+// Sum of two counts, INT_MAX from there on.
+__device__ __forceinline__ int add_counts(int a, int b) {
+  return static_cast<int>(min(static_cast<unsigned>(a) + static_cast<unsigned>(b), 0x7fffffffu));
+}
+
 // Cuts a batch's units evenly over the CTAs: request b has units(span(b)) >= 0
-// of them, fewer than 2^31 in all, in pieces(span) pieces. CTA c of up to
+// of them, fewer than 2^31 in all, in pieces(span) pieces, `most` at most in all. (Starts
+// that decrease can claim rows many times over and make more of either: then nothing is
+// done.) CTA c of up to
 // gridDim.x takes [cut(c), cut(c + 1)): `least` units at least, or about a piece,
 // because a piece that is cut in many parts takes long to join. Block-wide; the spans and first units of the requests
 // that hold both cuts come back in shared memory (the last request's where the
@@ -160,24 +167,28 @@ struct Found {
 };
 // sums: two ints a warp.
 template <int THREADS, class Span, class S, class U, class P>
-__device__ __forceinline__ Cuts locate_cuts(int batch, int least, const S& span, const U& units,
-                                            const P& pieces, int* sums, Found<Span>& found) {
+__device__ __forceinline__ Cuts locate_cuts(int batch, int least, int most, const S& span,
+                                            const U& units, const P& pieces, int* sums,
+                                            Found<Span>& found) {
   const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
   constexpr int kWarps = THREADS / kWarp;
   const int per = (batch + THREADS - 1) / THREADS;
   const int b0 = min(batch, static_cast<int>(threadIdx.x) * per), b1 = min(batch, b0 + per);
-  int mine = 0, parts = 0;
+  unsigned mine = 0;
+  int parts = 0;
   Span s{};
   for (int b = b0; b < b1; ++b) {
     s = span(b);
     mine += units(s);
-    parts += pieces(s);
+    parts = add_counts(parts, pieces(s));
   }
-  parts = __reduce_add_sync(0xffffffffu, parts);
-  int inc = mine;
+  // of a warp: 2^31 and more stay that
+  const int high = __reduce_add_sync(0xffffffffu, parts >> 16);
+  parts = add_counts(min(high, 0x7fff) << 16, __reduce_add_sync(0xffffffffu, parts & 0xffff));
+  unsigned inc = mine;
 #pragma unroll
   for (int d = 1; d < kWarp; d *= 2) {
-    const int v = __shfl_up_sync(0xffffffffu, inc, d);
+    const unsigned v = __shfl_up_sync(0xffffffffu, inc, d);
     if (lane >= d) inc += v;
   }
   if (lane == kWarp - 1) {
@@ -185,19 +196,21 @@ __device__ __forceinline__ Cuts locate_cuts(int batch, int least, const S& span,
     sums[kWarps + warp] = parts;
   }
   __syncthreads();
-  int at = inc - mine, total = 0, all = 0;
+  unsigned before = inc - mine, sum = 0;
+  int all = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    const int x = sums[w];
-    at += w < warp ? x : 0;
-    total += x;
-    all += sums[kWarps + w];
+    const unsigned x = sums[w];
+    before += w < warp ? x : 0;
+    sum += x;
+    all = add_counts(all, sums[kWarps + w]);
   }
+  const int at = static_cast<int>(before), total = all > most ? 0 : static_cast<int>(sum);
   Cuts cuts;
   cuts.set(total, all, least);
   for (int i = 0; i < 2; ++i) {
     const int target = min(cuts.cut(blockIdx.x + i), total - 1);
-    if (target < at || target >= at + mine) continue;
+    if (target < at || target >= at + static_cast<int>(mine)) continue;
     int here = at;
     for (int b = b0; b < b1; ++b) {
       if (per > 1) s = span(b);

@@ -142,6 +142,7 @@ struct TcParams {
   int32_t* counters;
   float* partials;
   FastDiv group, heads;
+  int most;                                      // units that starts which never decrease make
   int vec_out;
   int q_tma;                                     // queries by TMA: boxes of group x 128 / group
   WaitCfg wait;
@@ -450,7 +451,8 @@ struct Walk {
     const int heads = p.a.n_kv_heads;
     WindowSpan s{};
     for (;;) {
-      if (b >= p.a.batch) {
+      // (starts that decrease can claim rows many times over: not without end)
+      if (b >= p.a.batch || u >= tp.most) {
         if (lane == 0) x.valid = 0;
         return;
       }
@@ -840,7 +842,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
   Cuts cuts{};
   if (PAGED)
     cuts = locate_cuts<kThreadsOf<PAGED>>(
-        w.a.batch, kLeast, [&](int i) { return tc_span<PAGED>(p, i, false); },
+        w.a.batch, kLeast, p.most, [&](int i) { return tc_span<PAGED>(p, i, false); },
         [&](const WindowSpan& s) { return s.tiles * w.a.n_kv_heads * key_tiles(p, s); },
         [&](const WindowSpan& s) { return s.tiles * w.a.n_kv_heads; }, sums, found);
 
@@ -1396,6 +1398,7 @@ bool fill_params(TcParams& p, CUtensorMap& map_q, const dlrm_attention_t& a) {
   p.w.vec = 1;
   p.group = fast_div(p.w.group);
   p.heads = fast_div(a.n_kv_heads);
+  p.most = static_cast<int>((a.q_rows * p.w.group / kUnit + a.batch) * a.n_kv_heads);
   p.vec_out = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.ld_out % 8 == 0 &&
               (a.n_heads == 1 || a.ld_out_head % 8 == 0);
   p.q_tma = 128 % p.w.group == 0 && tma_rows(a.q, a.ld_q, a.ld_q_head, a.n_heads, a.head_dim);

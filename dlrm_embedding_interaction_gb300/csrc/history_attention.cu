@@ -65,6 +65,7 @@ struct Params {
   dlrm_history_t h;
   dlrm_attention_t a;
   int group;                                     // query heads of a kv head
+  int most;                                      // (head, tile)s that starts which never decrease make
   int vec_q;                                     // four query elements can be loaded at once
   int32_t* counters;
   float* partials;
@@ -270,7 +271,7 @@ history_attention_kernel(const __grid_constant__ Params p) {
 
   auto units = [&](const Span& s) { return s.tiles * s.chunks * H; };
   const Cuts cuts = locate_cuts<kThreads>(
-      p.a.batch, kLeast, [&](int i) { return span_of<kRows>(p, i, false); }, units,
+      p.a.batch, kLeast, p.most, [&](int i) { return span_of<kRows>(p, i, false); }, units,
       [&](const Span& s) { return s.tiles * H; }, sums, found);
   // a cut inside a short tile moves to the tile's start: finishing it in one
   // CTA is faster than joining parts
@@ -759,7 +760,7 @@ history_attention_kernel(const __grid_constant__ Params p) {
 }
 
 template <int D, int DT>
-cudaError_t launch(const Params& p, cudaStream_t stream) {
+cudaError_t launch(Params& p, cudaStream_t stream) {
   using Sh = Shape<D, DT>;
   constexpr int kRows = Sh::kRows;
   // The shared memory that the kernel may take is set once on every device, by a bit
@@ -790,6 +791,7 @@ cudaError_t launch(const Params& p, cudaStream_t stream) {
   const int64_t tiles = p.a.q_rows * p.group / kRows + p.a.batch;
   const int64_t chunks = tiles * p.h.n_heads * ((events + chunk - 1) / chunk + 1);
   if (chunks >= (int64_t(1) << 31)) return cudaErrorInvalidValue;   // history_attention has checked
+  p.most = static_cast<int>(tiles * p.h.n_heads);
   const int64_t grid = std::min<int64_t>(
       {chunks, static_cast<int64_t>(device_sm_count()) * per_sm, int64_t(kAttnMaxCtas)});
   return launch_pdl(history_attention_kernel<D, DT>, dim3(static_cast<unsigned>(grid)),
@@ -797,7 +799,7 @@ cudaError_t launch(const Params& p, cudaStream_t stream) {
 }
 
 template <int D>
-cudaError_t launch_d(const Params& p, cudaStream_t stream) {
+cudaError_t launch_d(Params& p, cudaStream_t stream) {
   if (p.a.dtype == DLRM_DTYPE_FP32) return launch<D, DLRM_DTYPE_FP32>(p, stream);
   if (p.a.dtype == DLRM_DTYPE_BF16) return launch<D, DLRM_DTYPE_BF16>(p, stream);
   return launch<D, DLRM_DTYPE_FP16>(p, stream);

@@ -33,9 +33,8 @@ cudaError_t launch_window_attention_tc(const dlrm_attention_t& call, cudaStream_
       !encode_rows(&mk, a.k, a.k_rows, a.n_kv_heads, a.head_dim, a.ld_k, a.ld_k_head, a.dtype, kBox, 1) ||
       !encode_rows(&mv, a.v, a.k_rows, a.n_kv_heads, a.head_dim, a.ld_v, a.ld_v_head, a.dtype, kBox, 1))
     return cudaErrorInvalidValue;
-  const int64_t units = (a.q_rows * p.w.group / kUnit + a.batch) * a.n_kv_heads;
   const int ctas = a.head_dim == 128 ? kCtas<128, false> : kCtas<64, false>;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(units, device_sm_count() * ctas));
+  const unsigned grid = static_cast<unsigned>(std::min(p.most, device_sm_count() * ctas));
   const bool bf16 = a.dtype == DLRM_DTYPE_BF16;
   if (a.head_dim == 32)
     return bf16 ? launch_tc<32, DLRM_DTYPE_BF16, false>(mq, mk, mv, p, grid, stream)

@@ -507,7 +507,9 @@ dlrm_status_t linear_bias_act(const float* x, int32_t ld_x, const float* W, cons
  * (not the others) without effect:
  *   DLRM_ERRBIT_INDEX_OOB    a slot outside [0, n_slots), or a page that a
  *                            query needs and the table does not hold
- *   DLRM_ERRBIT_OFFSETS      starts that decrease or pass the row count
+ *   DLRM_ERRBIT_OFFSETS      starts that decrease or pass the row count (requests
+ *                            that overlap, which takes a decrease between them,
+ *                            have undefined outputs)
  *   DLRM_ERRBIT_OOM          too few free pages: this request and every later
  *                            one of the call that needs a page
  *   DLRM_ERRBIT_INVALID_ARG  a slot written twice in one call (the first

@@ -196,6 +196,32 @@ def test_many_small_weights_beside_a_large_one(dtype):
             assert (err <= (eps + base.half_ulp(dtype)) * share[:, None]).all(), (plain, len(out), err.max())
 
 
+# ------------------------------------------------------------------ starts
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("n", [1 << 20, 1 << 13])
+def test_starts_that_claim_all_rows_many_times_over(dtype, n):
+    """Every second request decreases and is refused, the others have all rows each. The
+    longer rows make more work in all than 31 bits count. Over a cache such a call does
+    nothing but say so, over plain rows no more than its rows are; the next is as ever."""
+    rng = np.random.default_rng(48)
+    cache, pool = make(70, 2, 65, 8, 32, 64)
+    fill(cache, pool, rng, [0, 1], [4096, 100])
+    batch = min(4096, n // 100)
+    at = i32([0, n] * (batch // 2) + [0])
+    q = rows(rng, 1, 8, 32, dtype).expand(n, 8, 32)
+    out = torch.full((n, 8, 32), 9.0, dtype=TYPES[dtype], device="cuda")
+    dl.history_attention(cache, i32([0] * (len(at) - 1)), at, q, out)
+    assert cache.error() == dl.ERR_UNSUPPORTED
+    assert (out == 9).all()
+    base.check_attention(cache, pool, rng, [1, 0], [3, 2], 8, dtype, False, 0, 0)
+    assert cache.error() == dl.OK
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q = q.contiguous()
+    dl.window_attention(q, q, q, at, out, window=64, err_flag=err)
+    assert err.item() == dl.ERRBIT_OFFSETS
+
+
 # ------------------------------------------------------------------ waits that run out
 
 LIMIT_NS = 2_000_000      # 2 ms: far above any wait of a healthy call here
