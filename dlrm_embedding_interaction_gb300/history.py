@@ -4,7 +4,10 @@ it, and windowed attention over plain rows.
 Argument checks and marshalling only, like the rest of the binding:
 include/dlrm.h defines the pool, the codes and every operator, and says which
 faults only the device sees (they set bits in the cache's error word, read by
-``HistoryCache.error()``). Nothing here waits for the GPU but ``error()``.
+``HistoryCache.error()``). Nothing here waits for the GPU but ``error()``. With ``stream``
+the launches go there, and tensors that a call makes belong to that stream, as under
+``torch.cuda.stream``; its order against the inputs' and outputs' other streams is the
+caller's.
 
     cache = HistoryCache(n_pages, n_slots, max_pages, n_heads, head_dim)
     history_append(cache, slots, starts, k, v)            # (rows, n_heads, head_dim)
@@ -12,6 +15,7 @@ faults only the device sees (they set bits in the cache's error word, read by
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import struct
 from typing import Optional
@@ -99,6 +103,16 @@ def _raw_stream(stream, index: int):
     return _stream(stream)
 
 
+def _on(stream, device):
+    """A context in which tensors are made on ``stream``: from memory that no work queued on
+    another stream still uses, filled in its order."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
 # The checks below run with every call: a tensor that passes costs a few attributes
 # (all of a call's about as much as the launch), and messages are made for errors
 # only. ``device`` is an index (quick) or a torch.device.
@@ -144,8 +158,8 @@ class HistoryCache:
     histories of at most ``max_pages`` pages each. The tensors (``k_codes``,
     ``v_codes``, ``k_scales``, ``v_scales``, ``table``, ``lengths``, ``refs``,
     ``free_pages``, ``n_free``, ``err``) are the caller's to read, e.g. to save
-    a pool; calls on one cache go to one stream. Its device has to be the current one,
-    here and in every call.
+    a pool; calls on one cache go to one stream, the one that made it or one that has
+    waited for it. Its device has to be the current one, here and in every call.
     """
 
     def __init__(self, n_pages: int, n_slots: int, max_pages: int, n_heads: int, head_dim: int,
@@ -167,17 +181,18 @@ class HistoryCache:
         shape = (n_pages, n_heads, page_tokens, head_dim)
         new = dict(device=device)
         i32 = dict(dtype=torch.int32, device=device)
-        self.k_codes = torch.zeros(shape, dtype=torch.uint8, **new).view(torch.float8_e4m3fn)
-        self.v_codes = torch.zeros(shape, dtype=torch.uint8, **new).view(torch.float8_e4m3fn)
-        self.k_scales = torch.zeros(shape[:2], **new)
-        self.v_scales = torch.zeros(shape[:2], **new)
-        self.table = torch.empty((n_slots, max_pages), **i32)
-        self.lengths = torch.empty(n_slots, **i32)
-        self.refs = torch.empty(n_pages, **i32)
-        self.free_pages = torch.empty(n_pages, **i32)
-        self.n_free = torch.empty(1, **i32)
-        self.err = torch.empty(1, **i32)
-        self._work = torch.empty(work, dtype=torch.uint8, **new)
+        with _on(stream, device):
+            self.k_codes = torch.zeros(shape, dtype=torch.uint8, **new).view(torch.float8_e4m3fn)
+            self.v_codes = torch.zeros(shape, dtype=torch.uint8, **new).view(torch.float8_e4m3fn)
+            self.k_scales = torch.zeros(shape[:2], **new)
+            self.v_scales = torch.zeros(shape[:2], **new)
+            self.table = torch.empty((n_slots, max_pages), **i32)
+            self.lengths = torch.empty(n_slots, **i32)
+            self.refs = torch.empty(n_pages, **i32)
+            self.free_pages = torch.empty(n_pages, **i32)
+            self.n_free = torch.empty(1, **i32)
+            self.err = torch.empty(1, **i32)
+            self._work = torch.empty(work, dtype=torch.uint8, **new)
         for name in ("k_codes", "v_codes", "k_scales", "v_scales", "table", "lengths", "refs",
                      "free_pages", "n_free", "err"):
             setattr(c, name, getattr(self, name).data_ptr())
@@ -195,10 +210,7 @@ class HistoryCache:
         """Waits for ``stream``, returns the first error that the device recorded
         since the last call (INDEX_OOB before UNSUPPORTED, OOM, INVALID_ARG and
         TIMEOUT; OK if none) and clears it."""
-        s = torch.cuda.current_stream(self.device) if stream is None else stream
-        if not isinstance(s, torch.cuda.Stream):
-            s = torch.cuda.ExternalStream(int(s), device=self.device)
-        with torch.cuda.stream(s):
+        with _on(torch.cuda.current_stream(self.device) if stream is None else stream, self.device):
             bits = int(self.err.item())
             if bits:
                 self.err.zero_()
@@ -293,10 +305,14 @@ def history_compact(cache: HistoryCache, stream=None) -> None:
     _check(_bound().history_compact(c._ref, _raw_stream(stream, c._index)), "history_compact")
 
 
-def _check_outputs(where, q, shape, out, lse, window, sinks, index):
-    """out, made if there is none, and its strides."""
+def _check_outputs(where, q, shape, out, lse, window, sinks, index, stream):
+    """out, made (on ``stream``) if there is none, and its strides."""
     if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        if stream is None:
+            out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        else:
+            with _on(stream, q.device):
+                out = torch.empty(shape, dtype=q.dtype, device=q.device)
         strides = out.stride()
     else:
         if not isinstance(out, torch.Tensor) or out.dtype is not q.dtype:
@@ -336,7 +352,7 @@ def history_attention(cache: HistoryCache, slots, starts, q, out=None, *, scale=
     if heads < 1 or heads % c.n_heads:
         raise ValueError(f"{where}: q: {heads} heads are no multiple of the cache's {c.n_heads}")
     dtype = _dtype_code(q, "history_attention: q")
-    out, os = _check_outputs(where, q, shape, out, lse, window, sinks, index)
+    out, os = _check_outputs(where, q, shape, out, lse, window, sinks, index, stream)
     args = _ATTENTION.pack(
         q.data_ptr(), 0, 0, out.data_ptr(), 0 if lse is None else lse.data_ptr(), slots.data_ptr(),
         starts.data_ptr(), 0, rows, 0, qs[0], qs[1], 0, 0, 0, 0, os[0], os[1], b, heads, c.n_heads,
@@ -380,7 +396,7 @@ def window_attention(q, k, v, starts, out=None, *, k_starts=None, scale=None, wi
     else:
         _int32_vector(k_starts, "window_attention: k_starts", b + 1, index)
     dtype = _dtype_code(q, "window_attention: q")
-    out, os = _check_outputs(where, q, shape, out, lse, window, sinks, index)
+    out, os = _check_outputs(where, q, shape, out, lse, window, sinks, index, stream)
     if err_flag is not None:
         _int32_vector(err_flag, "window_attention: err_flag", 1, index)
     args = _ATTENTION.pack(

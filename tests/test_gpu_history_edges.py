@@ -196,6 +196,39 @@ def test_many_small_weights_beside_a_large_one(dtype):
             assert (err <= (eps + base.half_ulp(dtype)) * share[:, None]).all(), (plain, len(out), err.max())
 
 
+# ------------------------------------------------------------------ streams
+
+def test_a_call_on_another_stream_while_the_current_one_is_busy():
+    """The cache, and an output that the call makes, belong to the call's stream: nothing that
+    is still queued on the current one (a fill of freed memory too) reaches them."""
+    rng = np.random.default_rng(49)
+    side = torch.cuda.Stream()
+    k = rows(rng, 200, 2, 64, "fp32")
+    q = rows(rng, 5000, 4, 64, "fp32")
+    plain = rows(rng, 5000, 4, 64, "bf16", 0.3)
+    slots, at, q_at = i32([0]), i32([0, 200]), i32([0, 5000])
+    want = dl.window_attention(plain, plain, plain, q_at)
+    pool = ref.Pool(8, 2, 4, 2, 64, 64)
+    pool.append([0], [0, 200], (f64(k), f64(k)))
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    freed = [torch.empty_like(x) for x in (q, plain)]
+    torch.cuda._sleep(200_000_000)                  # a tenth of a second
+    for x in freed:
+        x.fill_(7.0)
+    del freed, x
+    cache = dl.HistoryCache(8, 2, 4, 2, 64, stream=side)
+    dl.history_append(cache, slots, at, k, k, stream=side)
+    out = dl.history_attention(cache, slots, q_at, q, stream=side)
+    enc = dl.window_attention(plain, plain, plain, q_at, stream=side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    same_state(cache, pool)
+    assert cache.error(side) == dl.OK
+    assert torch.equal(enc, want)
+    assert torch.equal(out, dl.history_attention(cache, slots, q_at, q))
+
+
 # ------------------------------------------------------------------ starts
 
 @pytest.mark.parametrize("dtype", list(TYPES))

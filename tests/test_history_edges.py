@@ -78,3 +78,54 @@ def test_a_cache_is_made_on_the_current_device_only(monkeypatch):
     monkeypatch.setattr(torch, "zeros", lambda *a, **k: pytest.fail("allocated"))
     with pytest.raises(ValueError, match="current device"):
         dl.HistoryCache(4, 4, 4, 1, 64, device="cuda:1")
+
+
+# ------------------------------------------------------------------ streams
+
+@pytest.fixture
+def streams(monkeypatch):
+    """Which stream is current where tensors are made: "current", or what was asked for."""
+    import contextlib
+    seen, current = [], ["current"]
+
+    @contextlib.contextmanager
+    def stream(s):
+        current.append(s.number)
+        yield
+        current.pop()
+
+    class External:
+        def __init__(self, number, device=None):
+            self.number = number
+
+    def made(real):
+        def make(*shape, dtype=None, device=None):
+            seen.append(current[-1])
+            return real(*shape, dtype=dtype)
+        return make
+
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", External)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch, "zeros", made(torch.zeros))
+    monkeypatch.setattr(torch, "empty", made(torch.empty))
+    return seen
+
+
+def test_tensors_are_made_on_the_stream_of_the_call(fake, streams, monkeypatch):
+    """Otherwise they are filled, or their memory is still used, out of that stream's order."""
+    cache, lib = fake
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32)   # noqa: E731
+    q = torch.ones(3, 4, 64)
+    plain = [q.as_subclass(OnDevice)] * 3
+    for stream in (None, 77):
+        want = "current" if stream is None else stream
+        dl.history_attention(cache, i32(0), i32(0, 3), q, stream=stream)
+        dl.window_attention(*plain, i32(0, 3), stream=stream)
+        assert streams == [want] * 2
+        streams.clear()
+    monkeypatch.setattr(history, "_current_device", lambda: 0)
+    for stream in (None, 77):
+        history.HistoryCache(4, 4, 4, 1, 64, stream=stream)
+        assert len(streams) == 11 and set(streams) == {"current" if stream is None else stream}
+        streams.clear()
