@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import operator
 import struct
 from typing import Optional
 
@@ -28,6 +29,8 @@ from . import (DlrmError, ERR_INDEX_OOB, ERR_INVALID_ARG, ERR_OOM, ERR_TIMEOUT, 
 DTYPE_FP32, DTYPE_BF16, DTYPE_FP16 = 0, 1, 2
 PAGE_TOKENS = (32, 64, 128)
 HEAD_DIMS = (32, 64, 128)
+INT32_MAX = 2 ** 31 - 1
+FP32_MAX = 2.0 ** 128 - 2.0 ** 104
 
 _VP, _I32, _I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
 
@@ -169,6 +172,9 @@ class HistoryCache:
             raise ValueError("HistoryCache: device must be a CUDA device")
         if device.index is not None and device.index != torch.cuda.current_device():
             raise ValueError(f"HistoryCache: {device} is not the current device: make it so (torch.cuda.device)")
+        # (ctypes cuts integers off)
+        if max(n_pages, page_tokens, n_heads, head_dim, n_slots, max_pages) > INT32_MAX:
+            raise DlrmError(ERR_UNSUPPORTED, "HistoryCache")
         c = _History(int(n_pages), int(page_tokens), int(n_heads), int(head_dim), int(n_slots),
                      int(max_pages))
         bound = _bound()
@@ -294,9 +300,10 @@ def history_free(cache: HistoryCache, slots, stream=None) -> None:
 def history_trim(cache: HistoryCache, slots, window: int, sinks: int = 0, stream=None) -> None:
     """Gives up the pages that attention with this window and these sinks no
     longer reads, in queries at the histories' ends or later."""
-    if window < 1 or sinks < 0:
-        raise ValueError("history_trim: window must be at least 1, sinks at least 0")
-    _slots_call("history_trim", cache, (("history_trim: slots", slots),), stream, int(window), int(sinks))
+    if not 1 <= window <= INT32_MAX or not 0 <= sinks <= INT32_MAX:
+        raise ValueError("history_trim: window must be at least 1, sinks at least 0, both below 2^31")
+    _slots_call("history_trim", cache, (("history_trim: slots", slots),), stream,
+                operator.index(window), operator.index(sinks))
 
 
 def history_compact(cache: HistoryCache, stream=None) -> None:
@@ -325,9 +332,22 @@ def _check_outputs(where, q, shape, out, lse, window, sinks, index, stream):
             raise TypeError(f"{where}: lse: expected a float32 tensor")
         if lse.shape != shape[:2] or lse.get_device() != index or not lse.is_contiguous():
             raise ValueError(f"{where}: lse: expected contiguous {tuple(shape[:2])} on {q.device}")
-    if window < 0 or sinks < 0:
-        raise ValueError(f"{where}: window and sinks must not be negative")
+    if not 0 <= window <= INT32_MAX or not 0 <= sinks <= INT32_MAX:
+        raise ValueError(f"{where}: window and sinks must not be negative, nor 2^31 or more")
     return out, strides
+
+
+def _pack(where, *fields) -> bytes:
+    try:
+        return _ATTENTION.pack(*fields)
+    except struct.error as e:                       # no integer where one belongs
+        raise TypeError(f"{where}: {e}") from None
+
+
+def _scale(where, scale):
+    if not -FP32_MAX <= scale <= FP32_MAX:
+        raise ValueError(f"{where}: scale must be a finite float32")
+    return scale
 
 
 def history_attention(cache: HistoryCache, slots, starts, q, out=None, *, scale=None,
@@ -353,10 +373,10 @@ def history_attention(cache: HistoryCache, slots, starts, q, out=None, *, scale=
         raise ValueError(f"{where}: q: {heads} heads are no multiple of the cache's {c.n_heads}")
     dtype = _dtype_code(q, "history_attention: q")
     out, os = _check_outputs(where, q, shape, out, lse, window, sinks, index, stream)
-    args = _ATTENTION.pack(
-        q.data_ptr(), 0, 0, out.data_ptr(), 0 if lse is None else lse.data_ptr(), slots.data_ptr(),
+    args = _pack(
+        where, q.data_ptr(), 0, 0, out.data_ptr(), 0 if lse is None else lse.data_ptr(), slots.data_ptr(),
         starts.data_ptr(), 0, rows, 0, qs[0], qs[1], 0, 0, 0, 0, os[0], os[1], b, heads, c.n_heads,
-        dim, dtype, causal, window, sinks, dim ** -0.5 if scale is None else scale, 0)
+        dim, dtype, causal, window, sinks, dim ** -0.5 if scale is None else _scale(where, scale), 0)
     _check(_bound().history_attention(c._ref, args, _raw_stream(stream, index)), where)
     return out
 
@@ -399,11 +419,11 @@ def window_attention(q, k, v, starts, out=None, *, k_starts=None, scale=None, wi
     out, os = _check_outputs(where, q, shape, out, lse, window, sinks, index, stream)
     if err_flag is not None:
         _int32_vector(err_flag, "window_attention: err_flag", 1, index)
-    args = _ATTENTION.pack(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+    args = _pack(
+        where, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
         0 if lse is None else lse.data_ptr(), 0, starts.data_ptr(), k_starts.data_ptr(), rows,
         k_rows, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os[0], os[1], b, heads, kv_heads,
-        dim, dtype, 1, window, sinks, dim ** -0.5 if scale is None else scale,
+        dim, dtype, 1, window, sinks, dim ** -0.5 if scale is None else _scale(where, scale),
         0 if err_flag is None else err_flag.data_ptr())
     _check(_bound().window_attention(args, _raw_stream(stream, index)), where)
     return out

@@ -80,6 +80,36 @@ def test_a_cache_is_made_on_the_current_device_only(monkeypatch):
         dl.HistoryCache(4, 4, 4, 1, 64, device="cuda:1")
 
 
+# ------------------------------------------------------------------ numbers
+
+@pytest.mark.parametrize("number", [2 ** 31, 2 ** 32 + 1, 2 ** 64 + 1, -1, -2 ** 32 + 1, 2.5])
+def test_numbers_past_32_bits_are_refused(fake, number):
+    """Not cut off: a window of 2^32 + 1 is not one of 1, which gives nearly all up."""
+    cache, lib = fake
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32)   # noqa: E731
+    q = torch.zeros(3, 4, 64)
+    plain = [q.as_subclass(OnDevice)] * 3
+    for name in ("window", "sinks"):
+        for call in (lambda **n: dl.history_trim(cache, i32(0), **dict(dict(window=5), **n)),
+                     lambda **n: dl.history_attention(cache, i32(0), i32(0, 3), q, **n),
+                     lambda **n: dl.window_attention(*plain, i32(0, 3), **n)):
+            with pytest.raises((ValueError, TypeError)):
+                call(**{name: number})
+    with pytest.raises(ValueError):
+        dl.history_attention(cache, i32(0), i32(0, 3), q, scale=1e39)
+    assert not lib.calls
+
+
+def test_a_cache_of_sizes_past_32_bits_is_refused(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch, "zeros", lambda *a, **k: pytest.fail("allocated"))
+    good = dict(n_pages=4, n_slots=4, max_pages=4, n_heads=1, head_dim=64, page_tokens=64)
+    for name, value in good.items():
+        with pytest.raises(dl.DlrmError) as e:
+            dl.HistoryCache(**dict(good, **{name: value + 2 ** 32}))
+        assert e.value.status == dl.ERR_UNSUPPORTED
+
+
 # ------------------------------------------------------------------ streams
 
 @pytest.fixture
