@@ -77,6 +77,21 @@ dlrm_status_t check_attention(const dlrm_attention_t* a, int kv_heads, bool* run
   return DLRM_OK;
 }
 
+// Whether rows and heads of an output lie over one another.
+bool rows_overlap(int64_t rows, int64_t ld, int64_t heads, int64_t ld_head, int64_t dim) {
+  if ((rows > 1 && ld < dim) || (heads > 1 && ld_head < dim)) return true;
+  if (rows <= 1 || heads <= 1) return false;
+  const bool inner = ld_head <= ld;                // the smaller stride is the heads'
+  const int64_t a = inner ? ld_head : ld, na = inner ? heads : rows;
+  const int64_t b = inner ? ld : ld_head, nb = inner ? rows : heads;
+  // step j of the larger stride falls between steps i and i + 1 of the smaller
+  for (int64_t j = 1; j < nb && j * b < a * (na - 1) + dim; ++j) {
+    const int64_t i = j * b / a, r = j * b % a;
+    if ((r < dim && i < na) || (a - r < dim && i + 1 < na)) return true;
+  }
+  return false;
+}
+
 }  // namespace
 
 namespace dlrm {
@@ -183,6 +198,8 @@ dlrm_status_t history_attention(const dlrm_history_t* h, const dlrm_attention_t*
   const int64_t tiles = a->q_rows * (a->n_heads / h->n_heads) / 8 + a->batch;
   const int64_t events = static_cast<int64_t>(h->max_pages) * h->page_tokens;
   if (tiles * h->n_heads >= (int64_t(1) << 31) / (events / 128 + 2)) return DLRM_ERR_UNSUPPORTED;
+  if (rows_overlap(a->q_rows, a->ld_out, a->n_heads, a->ld_out_head, h->head_dim))
+    return DLRM_ERR_INVALID_ARG;
   return status_of(dlrm::launch_history_attention(*h, *a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -204,6 +221,8 @@ dlrm_status_t window_attention(const dlrm_attention_t* a, void* stream) {
   const int64_t group = a->n_heads / a->n_kv_heads;
   if ((a->q_rows * group / 64 + a->batch) * a->n_kv_heads >= (int64_t(1) << 31))
     return DLRM_ERR_UNSUPPORTED;
+  if (rows_overlap(a->q_rows, a->ld_out, a->n_heads, a->ld_out_head, a->head_dim))
+    return DLRM_ERR_INVALID_ARG;
   return status_of(dlrm::launch_window_attention(*a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -593,7 +593,8 @@ dlrm_status_t history_compact(const dlrm_history_t* h, void* stream);
  * softmax statistics and sums are fp32; masked events have no influence,
  * whatever they hold.
  *   q, out  (q_rows, n_heads, head_dim) of dtype; (t, h, d) at
- *           t * ld + h * ld_head + d; out must not overlap an input
+ *           t * ld + h * ld_head + d; out must not overlap an input, and its rows
+ *           and heads not one another (INVALID_ARG)
  *   lse     (q_rows, n_heads) fp32 or NULL: log of the sum of exponentials
  * history_attention reads the events of slots[b] from a pool (k, v, k_starts,
  * k_rows and their strides are not read; n_kv_heads and head_dim are the

@@ -52,3 +52,23 @@ def test_attention_launches_on_every_device_of_a_process(lib, head_dim, dtype, r
         assert lib.window_attention(a, None) == dl.OK, device
         assert lib.fake_launches() == before + 2
     lib.fake_set_device(0)
+
+
+@pytest.mark.parametrize("rows,heads,ld,ld_head,good", [
+    (5, 4, 256, 64, True), (5, 4, 0, 64, False), (5, 4, 256, 0, False), (5, 4, 63, 64, False),
+    (1, 4, 0, 64, True), (5, 1, 64, 0, True), (1, 1, 0, 0, True), (5, 4, 64, 320, True), (5, 4, 64, 64, False),
+    (5, 4, 64, 319, False), (5, 4, 255, 64, False), (5, 4, 300, 70, True), (4, 2, 128, 192, True),
+    (4, 2, 128, 191, False), (4, 2, 128, 193, False), (4, 8, 128, 192, False), (1 << 20, 4, 256, 64, True),
+    (1 << 20, 2, 128, 64, True), (1 << 20, 4, 128, 64, False)])
+def test_outputs_that_lie_over_one_another_are_refused(lib, rows, heads, ld, ld_head, good):
+    """Against every pair of places, for few rows."""
+    if rows < 100:
+        at = sorted(t * ld + h * ld_head for t in range(rows) for h in range(heads))
+        assert good == all(b - a >= 64 for a, b in zip(at, at[1:]))
+    h = ctypes.byref(pool(n_heads=1))
+    a = ctypes.byref(attention(q_rows=rows, k_rows=rows, n_heads=heads, n_kv_heads=1, ld_q=64 * heads,
+                               ld_q_head=64, ld_k=64, ld_k_head=64, ld_v=64, ld_v_head=64, ld_out=ld,
+                               ld_out_head=ld_head))
+    want = dl.OK if good else dl.ERR_INVALID_ARG
+    assert lib.history_attention(h, a, None) == want
+    assert lib.window_attention(a, None) == want
