@@ -361,7 +361,7 @@ __host__ __device__ __forceinline__ int pieces_of(const dlrm_history_t& h) {
   return static_cast<int>((bytes + kCopyPiece - 1) / kCopyPiece);
 }
 
-// A fork's table row, by the CTAs (request, piece): full pages are shared, and
+// A fork's table row, by the CTAs (request, pieces): full pages are shared, and
 // piece by piece the last page that is not full is copied. Piece 0 writes the row.
 __device__ __forceinline__ void fork_one(const Pool& p, const Request& r, int top, int pieces, bool lengths) {
   const dlrm_history_t& h = p.h;
@@ -387,7 +387,7 @@ __device__ __forceinline__ void fork_one(const Pool& p, const Request& r, int to
   }
   // (a last page that is not full is never trimmed; a broken table's is not read)
   if (last >= 0 && last < h.n_pages)
-    copy_piece(h, blockIdx.y / pieces, blockIdx.y % pieces, last, page);
+    for (int y = blockIdx.y; y < 2 * pieces; y += gridDim.y) copy_piece(h, y / pieces, y % pieces, last, page);
 }
 
 // dst: the call's requests where no plan came before.
@@ -1020,13 +1020,15 @@ cudaError_t launch_history_fork(const dlrm_history_t& h, const int32_t* src, con
   const Pool p = make_pool(h);
   const int pieces = pieces_of(h);
   const int32_t* none = nullptr;
+  // (a grid has 65535 rows at most)
+  const unsigned rows = std::min(2 * pieces, 65535);
   if (share && batch <= kSmallBatch)
-    return launch_pdl(fork_kernel, dim3(batch, 2 * pieces), dim3(kCopyThreads), 0, stream, p, pieces, src, dst);
+    return launch_pdl(fork_kernel, dim3(batch, rows), dim3(kCopyThreads), 0, stream, p, pieces, src, dst);
   cudaError_t e = launch_pdl(share ? plan_kernel<kFork> : plan_kernel<kCopy>, dim3(1),
                              dim3(kPlanThreads), 0, stream, p, src, dst, none, batch, int64_t(0));
   if (e != cudaSuccess) return e;
   if (share)
-    return launch_pdl(fork_kernel, dim3(batch, 2 * pieces), dim3(kCopyThreads), 0, stream, p, pieces,
+    return launch_pdl(fork_kernel, dim3(batch, rows), dim3(kCopyThreads), 0, stream, p, pieces,
                       none, none);
   e = launch_pdl(copy_rows_kernel, dim3(batch), dim3(kCopyThreads), 0, stream, p);
   if (e != cudaSuccess) return e;

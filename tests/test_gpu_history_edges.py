@@ -76,6 +76,23 @@ def test_a_refused_fork_of_many_leaves_nothing_behind(batch):
         pool.release(dst)
 
 
+def test_a_fork_of_a_page_of_half_a_gigabyte():
+    """More pieces to copy than a grid has rows."""
+    heads = 32768
+    cache = dl.HistoryCache(3, 3, 1, heads, 128, page_tokens=128)
+    k, v = (torch.randn(5, heads, 128, device="cuda", dtype=torch.float16) for _ in range(2))
+    dl.history_append(cache, i32([0]), i32([0, 5]), k, v)
+    dl.history_fork(cache, i32([0]), i32([2]))
+    assert cache.error() == dl.OK and cache.lengths.tolist() == [5, 0, 5]
+    a, b = (int(cache.table[s, 0]) for s in (0, 2))
+    assert a != b
+    for x in (cache.k_codes, cache.v_codes):
+        assert torch.equal(x[a].view(torch.uint8), x[b].view(torch.uint8))
+        assert x[b, :, :5].float().abs().amax(dim=(1, 2)).min() > 0
+    for x in (cache.k_scales, cache.v_scales):
+        assert torch.equal(x[a], x[b])
+
+
 # ------------------------------------------------------------------ windows
 
 @pytest.mark.parametrize("dtype", list(TYPES))

@@ -72,3 +72,15 @@ def test_outputs_that_lie_over_one_another_are_refused(lib, rows, heads, ld, ld_
     want = dl.OK if good else dl.ERR_INVALID_ARG
     assert lib.history_attention(h, a, None) == want
     assert lib.window_attention(a, None) == want
+
+
+@pytest.mark.parametrize("n_heads", [1, 16384, 32768, 131071])
+@pytest.mark.parametrize("batch", [1, 200])
+def test_pages_of_any_size_can_be_forked(lib, n_heads, batch):
+    """A page of 2^29 bytes a side has more pieces to copy than a grid has rows."""
+    h = ctypes.byref(pool(n_heads=n_heads, page_tokens=128, head_dim=128, n_slots=300))
+    assert lib.history_append(h, 0x10000, 0x10000, batch, 0x10000, 128, 128, 0x10000, 128, 128, 5, 0,
+                              None) == dl.OK
+    for call in (lib.history_fork, lib.history_copy):
+        assert call(h, 0x10000, 0x10000, batch, None) == dl.OK
+    assert lib.history_compact(h, None) == dl.OK
