@@ -517,8 +517,8 @@ history_attention_kernel(const __grid_constant__ Params p) {
       for (int r = 0; r < (kSplit ? 1 : 2); ++r) {
         const float f = r ? f1 : f0;
         const float m = fmaxf(top[r], ceilf(quad_max(big[r]) * f));
-        const float off = m == -INFINITY ? 0.f : kLift - m;
-        alpha[r] = m == -INFINITY ? 1.f : exp2_approx(top[r] - m);
+        const float base = m == -INFINITY ? 0.f : m, off = kLift - base;
+        alpha[r] = exp2_approx(top[r] - base);
         top[r] = m;
         float add = 0.f;
 #pragma unroll
@@ -746,14 +746,16 @@ history_attention_kernel(const __grid_constant__ Params p) {
       store_element<DT>(p.a.out, i * p.a.ld_out + hq * p.a.ld_out_head + d, x);
       if (d == 0 && p.a.lse)
         p.a.lse[i * p.a.n_heads + hq] = l == 0.f ? -INFINITY : row_factor[r] * kLn2 + logf(l * pow2f(-kLift));
-      if (!finite(x) || (l == 0.f && d == 0 &&
-                         sees_any(visible(pos0 + (p.a.causal ? row / p.group : 0), s.len, p.a.window, p.a.sinks))))
-        odd[r] = odd[kRows] = 1;
+      if (!finite(x) || l == 0.f) odd[r] = odd[kRows] = l == 0.f ? 2 : 1;   // 2: sees nothing, or has no weights
     }
     __syncthreads();
     if (odd[kRows]) {
-      for (int r = 0; r < rows; ++r)
-        if (odd[r]) careful_row<DT>(p, s, head, tile * kRows + r, &joined[0][0][0]);
+      for (int r = 0; r < rows; ++r) {
+        const int row = tile * kRows + r;
+        if (odd[r] == 1 || (odd[r] == 2 && sees_any(visible(pos0 + (p.a.causal ? row / p.group : 0), s.len,
+                                                            p.a.window, p.a.sinks))))
+          careful_row<DT>(p, s, head, row, &joined[0][0][0]);
+      }
     }
     __syncthreads();                              // `joined` is read: the rings may be filled
   }

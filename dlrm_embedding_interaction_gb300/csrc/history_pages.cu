@@ -263,7 +263,7 @@ __device__ __forceinline__ unsigned plan_small(const Pool& p, const int32_t* src
                                            const int32_t* starts, int batch, int64_t rows, SmallPlan& plan) {
   const dlrm_history_t& h = p.h;
   const int t = threadIdx.x;
-  const bool report = blockIdx.x == 0 && blockIdx.y == 0;
+  const bool report = blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0;
   const int nfree = min(max(*h.n_free, 0), h.n_pages);
   const int d = t < batch ? dst[t] : -1, s = OP == kAppend || t >= batch ? d : src[t];
   if (t < kSmallBatch) reinterpret_cast<int*>(plan.slots)[t] = d;
@@ -305,13 +305,13 @@ __device__ __forceinline__ unsigned plan_small(const Pool& p, const int32_t* src
   unsigned ticket = 0;
   if (t == 0) {
     __threadfence();
-    ticket = atomicInc(reinterpret_cast<unsigned*>(&p.head[kHeadArrived]), gridDim.x * gridDim.y - 1);
+    ticket = atomicInc(reinterpret_cast<unsigned*>(&p.head[kHeadArrived]), gridDim.x * gridDim.y * gridDim.z - 1);
   }
   return ticket;
 }
 // By the first warp.
 __device__ __forceinline__ void commit_small(const Pool& p, int batch, unsigned ticket, const SmallPlan& plan) {
-  if (__shfl_sync(0xffffffffu, ticket, 0) != gridDim.x * gridDim.y - 1) return;
+  if (__shfl_sync(0xffffffffu, ticket, 0) != gridDim.x * gridDim.y * gridDim.z - 1) return;
   __threadfence();
   for (int i = threadIdx.x; i < batch; i += kWarp) {
     const Request& r = plan.request[i];
@@ -361,8 +361,9 @@ __host__ __device__ __forceinline__ int pieces_of(const dlrm_history_t& h) {
   return static_cast<int>((bytes + kCopyPiece - 1) / kCopyPiece);
 }
 
-// A fork's table row, by the CTAs (request, pieces): full pages are shared, and
-// piece by piece the last page that is not full is copied. Piece 0 writes the row.
+// A fork's table row, by the CTAs (request, piece), pieces along y, and along z where a
+// grid's y ends: full pages are shared, and piece by piece the last page that is not full
+// is copied. Piece 0 writes the row.
 __device__ __forceinline__ void fork_one(const Pool& p, const Request& r, int top, int pieces, bool lengths) {
   const dlrm_history_t& h = p.h;
   const int G = h.page_tokens, M = h.max_pages;
@@ -370,7 +371,8 @@ __device__ __forceinline__ void fork_one(const Pool& p, const Request& r, int to
   const int full = r.length / G;
   const int last = r.need > 0 ? from[full] : -1;
   const int page = r.need > 0 ? granted(p, r, top, 0) : -1;
-  if (blockIdx.y == 0) {
+  const int piece = blockIdx.z * gridDim.y + blockIdx.y;
+  if (piece == 0) {
     int32_t* row = h.table + static_cast<int64_t>(r.slot) * M;
     for (int j = threadIdx.x; j < full; j += kCopyThreads) {
       const int old = from[j];
@@ -386,8 +388,8 @@ __device__ __forceinline__ void fork_one(const Pool& p, const Request& r, int to
     }
   }
   // (a last page that is not full is never trimmed; a broken table's is not read)
-  if (last >= 0 && last < h.n_pages)
-    for (int y = blockIdx.y; y < 2 * pieces; y += gridDim.y) copy_piece(h, y / pieces, y % pieces, last, page);
+  if (last >= 0 && last < h.n_pages && piece < 2 * pieces)
+    copy_piece(h, piece / pieces, piece % pieces, last, page);
 }
 
 // dst: the call's requests where no plan came before.
@@ -1020,15 +1022,16 @@ cudaError_t launch_history_fork(const dlrm_history_t& h, const int32_t* src, con
   const Pool p = make_pool(h);
   const int pieces = pieces_of(h);
   const int32_t* none = nullptr;
-  // (a grid has 65535 rows at most)
-  const unsigned rows = std::min(2 * pieces, 65535);
+  // (a grid's y and z end at 65535)
+  const unsigned z = (2 * pieces + 65534) / 65535;
+  const dim3 grid(batch, (2 * pieces + z - 1) / z, z);
   if (share && batch <= kSmallBatch)
-    return launch_pdl(fork_kernel, dim3(batch, rows), dim3(kCopyThreads), 0, stream, p, pieces, src, dst);
+    return launch_pdl(fork_kernel, grid, dim3(kCopyThreads), 0, stream, p, pieces, src, dst);
   cudaError_t e = launch_pdl(share ? plan_kernel<kFork> : plan_kernel<kCopy>, dim3(1),
                              dim3(kPlanThreads), 0, stream, p, src, dst, none, batch, int64_t(0));
   if (e != cudaSuccess) return e;
   if (share)
-    return launch_pdl(fork_kernel, dim3(batch, rows), dim3(kCopyThreads), 0, stream, p, pieces,
+    return launch_pdl(fork_kernel, grid, dim3(kCopyThreads), 0, stream, p, pieces,
                       none, none);
   e = launch_pdl(copy_rows_kernel, dim3(batch), dim3(kCopyThreads), 0, stream, p);
   if (e != cudaSuccess) return e;

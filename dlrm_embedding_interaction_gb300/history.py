@@ -90,8 +90,8 @@ def _dtype_code(t, name: str) -> int:
     return code
 
 
-def _current_device() -> int:
-    return torch._C._cuda_getDevice()
+# (absent from a build of torch without CUDA, where nothing gets as far as to ask)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _raw_stream(stream, index: int):
@@ -99,8 +99,8 @@ def _raw_stream(stream, index: int):
     without making a Stream object, which takes microseconds). A launch goes to the
     current device, so that has to be the tensors'."""
     if index != _current_device():
-        raise ValueError(f"the tensors are on device {index}, the current device is {_current_device()}: "
-                         "make theirs current (torch.cuda.device)")
+        raise ValueError(f"the tensors are not on the current device ({_current_device()}): make "
+                         f"device {index} current (torch.cuda.device)")
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(index)
     return _stream(stream)
@@ -332,16 +332,13 @@ def _check_outputs(where, q, shape, out, lse, window, sinks, index, stream):
             raise TypeError(f"{where}: lse: expected a float32 tensor")
         if lse.shape != shape[:2] or lse.get_device() != index or not lse.is_contiguous():
             raise ValueError(f"{where}: lse: expected contiguous {tuple(shape[:2])} on {q.device}")
-    if not 0 <= window <= INT32_MAX or not 0 <= sinks <= INT32_MAX:
-        raise ValueError(f"{where}: window and sinks must not be negative, nor 2^31 or more")
+    if window < 0 or sinks < 0:
+        raise ValueError(f"{where}: window and sinks must not be negative")
     return out, strides
 
 
-def _pack(where, *fields) -> bytes:
-    try:
-        return _ATTENTION.pack(*fields)
-    except struct.error as e:                       # no integer where one belongs
-        raise TypeError(f"{where}: {e}") from None
+def _unpackable(where, e):
+    return ValueError(f"{where}: window and sinks must be integers below 2^31 ({e})")
 
 
 def _scale(where, scale):
@@ -373,10 +370,13 @@ def history_attention(cache: HistoryCache, slots, starts, q, out=None, *, scale=
         raise ValueError(f"{where}: q: {heads} heads are no multiple of the cache's {c.n_heads}")
     dtype = _dtype_code(q, "history_attention: q")
     out, os = _check_outputs(where, q, shape, out, lse, window, sinks, index, stream)
-    args = _pack(
-        where, q.data_ptr(), 0, 0, out.data_ptr(), 0 if lse is None else lse.data_ptr(), slots.data_ptr(),
-        starts.data_ptr(), 0, rows, 0, qs[0], qs[1], 0, 0, 0, 0, os[0], os[1], b, heads, c.n_heads,
-        dim, dtype, causal, window, sinks, dim ** -0.5 if scale is None else _scale(where, scale), 0)
+    try:
+        args = _ATTENTION.pack(
+            q.data_ptr(), 0, 0, out.data_ptr(), 0 if lse is None else lse.data_ptr(), slots.data_ptr(),
+            starts.data_ptr(), 0, rows, 0, qs[0], qs[1], 0, 0, 0, 0, os[0], os[1], b, heads, c.n_heads,
+            dim, dtype, causal, window, sinks, dim ** -0.5 if scale is None else _scale(where, scale), 0)
+    except struct.error as e:
+        raise _unpackable(where, e) from None
     _check(_bound().history_attention(c._ref, args, _raw_stream(stream, index)), where)
     return out
 
@@ -419,12 +419,15 @@ def window_attention(q, k, v, starts, out=None, *, k_starts=None, scale=None, wi
     out, os = _check_outputs(where, q, shape, out, lse, window, sinks, index, stream)
     if err_flag is not None:
         _int32_vector(err_flag, "window_attention: err_flag", 1, index)
-    args = _pack(
-        where, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-        0 if lse is None else lse.data_ptr(), 0, starts.data_ptr(), k_starts.data_ptr(), rows,
-        k_rows, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os[0], os[1], b, heads, kv_heads,
-        dim, dtype, 1, window, sinks, dim ** -0.5 if scale is None else _scale(where, scale),
-        0 if err_flag is None else err_flag.data_ptr())
+    try:
+        args = _ATTENTION.pack(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+            0 if lse is None else lse.data_ptr(), 0, starts.data_ptr(), k_starts.data_ptr(), rows,
+            k_rows, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os[0], os[1], b, heads, kv_heads,
+            dim, dtype, 1, window, sinks, dim ** -0.5 if scale is None else _scale(where, scale),
+            0 if err_flag is None else err_flag.data_ptr())
+    except struct.error as e:
+        raise _unpackable(where, e) from None
     _check(_bound().window_attention(args, _raw_stream(stream, index)), where)
     return out
 
