@@ -98,6 +98,11 @@ __device__ __forceinline__ int block_exclusive(int x, int* sums, int& total) {
   return sums[warp] + inc - x;
 }
 
+// A page of the pool: not one trimmed away, nor what a broken table holds.
+__device__ __forceinline__ bool is_page(const dlrm_history_t& h, int page) {
+  return page >= 0 && page < h.n_pages;
+}
+
 enum PlanOp { kAppend, kFork, kCopy };
 
 // What request b asks for, but for its place among the others; bad: the error
@@ -191,7 +196,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Pool p, const int32_
       for (int i = threadIdx.x / kWarp; i < min(kPlanThreads, batch - b0); i += kPlanThreads / kWarp) {
         int c = 0;
         for (int j = lane; j < count_s[i]; j += kWarp)
-          c += h.table[static_cast<int64_t>(source_s[i]) * M + j] >= 0 ? 1 : 0;
+          c += is_page(h, h.table[static_cast<int64_t>(source_s[i]) * M + j]) ? 1 : 0;
         c = __reduce_add_sync(0xffffffffu, c);
         if (lane == 0) count_s[i] = c;
       }
@@ -377,7 +382,7 @@ __device__ __forceinline__ void fork_one(const Pool& p, const Request& r, int to
     for (int j = threadIdx.x; j < full; j += kCopyThreads) {
       const int old = from[j];
       row[j] = old;
-      if (old >= 0) atomicAdd(&h.refs[old], 1);
+      if (is_page(h, old)) atomicAdd(&h.refs[old], 1);
     }
     if (threadIdx.x == 0) {
       if (r.need > 0) {
@@ -421,9 +426,10 @@ __global__ void __launch_bounds__(kCopyThreads) copy_rows_kernel(Pool p) {
   for (int j0 = 0; j0 < n; j0 += kCopyThreads) {
     const int j = j0 + static_cast<int>(threadIdx.x);
     const int old = j < n ? from[j] : -1;
+    const bool copied = is_page(h, old);
     int total;
-    const int rank = taken + block_exclusive(old >= 0 ? 1 : 0, sums, total);
-    if (old >= 0) {
+    const int rank = taken + block_exclusive(copied ? 1 : 0, sums, total);
+    if (copied) {
       const int page = granted(p, r, top, rank);
       row[j] = page;
       h.refs[page] = 1;

@@ -76,6 +76,30 @@ def test_a_refused_fork_of_many_leaves_nothing_behind(batch):
         pool.release(dst)
 
 
+@pytest.mark.parametrize("page", [64, 2 ** 31 - 1, -2])
+def test_pages_that_a_table_cannot_hold_are_left_alone(page):
+    """A table that names a page outside the pool: such an entry is no page to any call."""
+    rng = np.random.default_rng(50)
+    cache, pool = make(64, 300, 4, 1, 32, 32)
+    fill(cache, pool, rng, [0, 1], [100, 40])
+    cache.table[0, 1] = page
+    dl.history_copy(cache, i32([0, 1]), i32([2, 3]))
+    dl.history_fork(cache, i32([0, 1]), i32([4, 5]))
+    dl.history_fork(cache, i32([0] * 200), i32(range(6, 206)))
+    assert cache.error() == dl.ERR_OOM              # of the last call's pages
+    assert cache.lengths[:7].tolist() == [100, 40, 100, 40, 100, 40, 100]
+    assert cache.table[2, 1] == -1 and (cache.table[2, [0, 2, 3]] >= 0).all()
+    assert cache.table[4, 1] == page
+    q = rows(rng, 2, 1, 32, "fp32")
+    got = dl.history_attention(cache, i32([1, 3, 5]), i32([0, 2, 2, 2]), q)
+    assert cache.error() == dl.OK and torch.isfinite(got).all()
+    dl.history_attention(cache, i32([4]), i32([0, 2]), q)
+    assert cache.error() == dl.ERR_INDEX_OOB
+    dl.history_free(cache, i32(range(0, 206)))
+    assert int(cache.n_free) == 63                  # all but the one that the table lost
+    assert cache.error() == dl.OK
+
+
 def test_a_fork_of_a_page_of_half_a_gigabyte():
     """More pieces to copy than a grid has rows."""
     heads = 32768
