@@ -11,6 +11,9 @@ std::atomic<int32_t> stall_withhold{0};
 
 using dlrm::aligned_to;
 
+// Rows are counted in int32, and rounded up to tiles of at most 256.
+constexpr int64_t kRowLimit = (int64_t(1) << 31) - 256;
+
 bool head_dim_ok(int d) { return d == 32 || d == 64 || d == 128; }
 
 dlrm_status_t check_shape(const dlrm_history_t* h) {
@@ -64,8 +67,7 @@ dlrm_status_t check_attention(const dlrm_attention_t* a, int kv_heads, bool* run
       a->n_heads % kv_heads != 0 || !dtype_ok(a->dtype) || a->window < 0 || a->sinks < 0 ||
       !(a->scale == a->scale))
     return DLRM_ERR_INVALID_ARG;
-  const int64_t limit = int64_t(1) << 31;
-  if (a->q_rows * (a->n_heads / kv_heads) >= limit) return DLRM_ERR_UNSUPPORTED;
+  if (a->q_rows >= kRowLimit || a->q_rows * (a->n_heads / kv_heads) >= kRowLimit) return DLRM_ERR_UNSUPPORTED;
   if (a->batch == 0 || a->q_rows == 0) return DLRM_OK;
   const size_t eb = static_cast<size_t>(dlrm::dtype_bytes(a->dtype));
   if (!a->q || !a->out || !a->q_starts || !aligned_to(a->q, eb) || !aligned_to(a->out, eb) ||
@@ -211,7 +213,7 @@ dlrm_status_t window_attention(const dlrm_attention_t* a, void* stream) {
   if (!head_dim_ok(a->head_dim)) return a->head_dim < 1 ? DLRM_ERR_INVALID_ARG : DLRM_ERR_UNSUPPORTED;
   if (a->k_rows < 0 || a->ld_k < 0 || a->ld_k_head < 0 || a->ld_v < 0 || a->ld_v_head < 0)
     return DLRM_ERR_INVALID_ARG;
-  if (a->k_rows >= (int64_t(1) << 31)) return DLRM_ERR_UNSUPPORTED;
+  if (a->k_rows >= kRowLimit) return DLRM_ERR_UNSUPPORTED;
   if (!run) return DLRM_OK;
   const size_t eb = static_cast<size_t>(dlrm::dtype_bytes(a->dtype));
   if (!a->k_starts || !aligned_to(a->k_starts, 4)) return DLRM_ERR_INVALID_ARG;

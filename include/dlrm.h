@@ -601,8 +601,9 @@ dlrm_status_t history_compact(const dlrm_history_t* h, void* stream);
  * pool's); window_attention reads rows [k_starts[b], k_starts[b+1]) of k and v,
  * (k_rows, n_kv_heads, head_dim) of dtype, is always causal, and flags bad
  * starts in err (NULL allowed): such a request has no rows.
- * head_dim is 32, 64 or 128 (else UNSUPPORTED, as is a call whose query rows and
- * events make 2^31 work units or more). */
+ * head_dim is 32, 64 or 128 (else UNSUPPORTED, as are 2^31 - 256 rows of k or of
+ * query heads that share a kv head, and a call whose query rows and events make
+ * 2^31 work units or more). */
 typedef struct {
   const void* q;
   const void* k;

@@ -84,3 +84,20 @@ def test_pages_of_any_size_can_be_forked(lib, n_heads, batch):
     for call in (lib.history_fork, lib.history_copy):
         assert call(h, 0x10000, 0x10000, batch, None) == dl.OK
     assert lib.history_compact(h, None) == dl.OK
+
+
+@pytest.mark.parametrize("change", [dict(k_rows=2 ** 31 - 1), dict(k_rows=2 ** 31 - 256), dict(k_rows=2 ** 62),
+                                    dict(q_rows=2 ** 31 - 1), dict(q_rows=2 ** 31 - 256),
+                                    dict(q_rows=2 ** 30, n_heads=2), dict(q_rows=2 ** 62, n_heads=2),
+                                    dict(q_rows=2 ** 62, n_heads=4), dict(q_rows=2 ** 63 - 1)])
+def test_row_counts_near_2_to_the_31_are_refused(lib, change):
+    """A step past the last tile would leave 32 bits, and a kernel's loop over keys would
+    start again from below zero."""
+    h = ctypes.byref(pool(n_heads=1))
+    good = dict(n_heads=1, n_kv_heads=1, ld_q=256, ld_q_head=64, ld_out=256, ld_out_head=64, q_rows=3, k_rows=5)
+    small = ctypes.byref(attention(**good))
+    assert lib.window_attention(small, None) == dl.OK and lib.history_attention(h, small, None) == dl.OK
+    a = ctypes.byref(attention(**dict(good, **change)))
+    assert lib.window_attention(a, None) == dl.ERR_UNSUPPORTED
+    if "q_rows" in change:
+        assert lib.history_attention(h, a, None) == dl.ERR_UNSUPPORTED
