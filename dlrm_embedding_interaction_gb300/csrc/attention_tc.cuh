@@ -23,11 +23,15 @@
 //     (else the softmax warps do);
 //   warps 0-3 and 4-7: softmax of tile 0 and 1. A thread owns a row: it reads
 //     its 64 scores from tensor memory, masks, takes the maximum, writes the
-//     weights in the input's type over the scores, and keeps its sum. The
+//     weights in the input's type (8 bits of them in bf16, 11 in fp16) over the scores,
+//     and keeps their sum as it was before the rounding. The
 //     output is only corrected when a row's maximum has grown by more than 2^8
 //     over the reference in use (weights up to 2^8 are as exact, and the sum is
 //     fp32), which real scores do in the first tiles only. 32 columns that none
-//     of a warp's rows sees are neither read nor exponentiated.
+//     of a warp's rows sees are neither read nor exponentiated. The outputs' sums are
+//     the tensor core's fp32, which cuts off what it adds: a sum loses up to 2^-24 of
+//     itself for every 16 events (fp16, one CTA: 1.3e-4 measured over 65,000, 5.2e-4 over
+//     131,072), as much as one weight's rounding at 65,000 events in fp16, 500,000 in bf16.
 // Tensor memory: two score buffers of 64 columns a tile, two of weights (32) and
 // the output. The scores of the next key tile are made while the softmax works on
 // this one's. At head_dim 128 there is no room for the weights: they lie over
@@ -40,19 +44,24 @@
 // leaves partial outputs, and of each tile's warps the one that arrives last
 // joins its 32 rows, in the order of the events.
 //
-// What bounds it: the softmax between the two products. A step of 64 keys takes
-// its warps, two a scheduler, about 2000 cycles, 700 of them the exponentials; the
-// tensor pipe is 49% active at head_dim 128. More softmax warps leave each too
-// few registers (16 warps 298 us against 254), and powers by a polynomial on the
-// FMA pipe cost more issue slots than the special function unit saves (269).
-// Measured: 2 x 16384 events, 8 heads of 128, window 2048, fp16: 254 us, 1.0
+// What bounds it: the steps of the softmax between the two products. A step of 64 keys
+// takes its warps, two a scheduler, about 2000 cycles, 700 of them the exponentials; most
+// of the others are waits of one role for another (scores, tensor memory, weights). The
+// tensor pipe is 48% active at head_dim 128. More softmax warps leave each too
+// few registers (16 warps 298 us against 254; moving registers between the roles is not
+// tried), and powers by a polynomial on the FMA pipe cost more issue slots than the
+// special function unit saves (269).
+// Measured: 2 x 16384 events, 8 heads of 128, window 2048, fp16: 258 us, 1.0
 // PFLOP/s of visible products (52% of the bf16 rate); 64 users of 100 to 1024 events,
 // 8 heads of 64 over 2, window 256, bf16: 58 us, of which the first loads and the last
 // products of short units are 10K of 26K cycles a unit; PAGED, 16 users x up to 500
 // candidates over 1000 to 4096 events, 4 heads of 64 over 2: 63 us, 0.28 PFLOP/s.
 //
 // Every wait is bounded (WaitCfg); on expiry DLRM_ERRBIT_TIMEOUT is set, every
-// role leaves its loop, work in flight is waited for and the tensor memory freed.
+// role leaves its loop, work in flight is waited for and the tensor memory freed. PAGED:
+// the CTA still counts for the units that it shares, so that the counters end at zero.
+// (How the code of the roles falls into the instruction cache is worth up to 6% of the
+// ragged batch: a branch more in the loop of warp 10, or a call after it, took 58 us to 61.)
 #pragma once
 
 #include <cuda.h>

@@ -8,14 +8,20 @@
 // memory (the four warps of a CTA read nearly the same events: L1 serves
 // them), with the inner dimensions of the MMAs permuted so that loads are of 16
 // bytes and the four threads of a row's queries and keys read 64 in a row (each a
-// quarter of the row instead: 410 us against 358 at 4096 events, head_dim 128).
-//   bf16, fp16: m16n8k16 in the input's own type; P is rounded to that type.
-//   fp32: m16n8k8 in tf32, three products per product (head * head,
-//     head * rest, rest * head), errors as of fp32.
+// quarter of the row instead: 410 us against 358 at 2 x 4096 events, head_dim 128, whole
+// rows at a time).
+//   bf16, fp16: m16n8k16 in the input's own type; P is rounded to that type (fp16: 2^15
+//     times as large, kLift).
+//   fp32: m16n8k8 in tf32, three products per product (head * head, head * rest,
+//     rest * head): 22 bits of each factor, the product of the rests left out. Outputs err
+//     by 5.2e-7 of the values (norms; 32 users of up to 512 events, window 64), where fp32
+//     products and sums err by 2.0e-7: a fourth product or a third part would cost more
+//     than it gives a ranking.
 // What bounds it: instructions (the splits of three products a product) and reads
 // that wait for one another, as most warps walk few blocks. 32 users of up to 512
-// events, 4 heads of 32, window 64, fp32: 20 us, four CTAs an SM. A block's keys and
-// values loaded together take 28 us; five CTAs an SM by a register cap 29 us, six 38.
+// events, 4 heads of 32, window 64, fp32: 20 us, four CTAs an SM (five by a register cap
+// a fifth more). A block's keys and values loaded together take 28 us. 2 x 4096 events,
+// window 512, fp32: 73 us at head_dim 32, 132 at 64, 305 at 128.
 #include "window_attention.cuh"
 
 namespace dlrm {
@@ -87,10 +93,10 @@ window_attention_kernel(const Params p) {
   constexpr int VW = D / 8 / EW;
   constexpr int NT = D / 8;
   // Scores of a whole block from kGroup words of every row at a time, so that fp32
-  // queries are split once a block (4096 events, window 512, 4 heads of 64: 165 us ->
-  // 151, of 128: 354 -> 298); at head_dim 32 from a whole row at a time, with the
-  // queries' rests in registers (20 us against 29, as 136 registers leave three CTAs an
-  // SM). Unaligned bf16 rows: 64 wide 103 -> 82, 128 wide 268 against 284, so whole rows there.
+  // queries are split once a block (2 x 4096 events, window 512, 4 heads of 128: 305 us
+  // against 364, of 64: 132 either way); at head_dim 32 from a whole row at a time, with
+  // the queries' rests in registers (47.5 us against 48.5, one user). Unaligned bf16 rows:
+  // 64 wide 82 us against 103, 128 wide 284 against 268, so whole rows there.
   constexpr bool kWholeRows = D == 32 || (D == 128 && !kF32);
   constexpr int kTogether = kWholeRows ? 1 : kBlock / 8, kGroup = kWholeRows ? KW : 4;
   __shared__ int64_t scan[40];

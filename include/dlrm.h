@@ -513,8 +513,11 @@ dlrm_status_t linear_bias_act(const float* x, int32_t ld_x, const float* W, cons
  *   DLRM_ERRBIT_OOM          too few free pages: this request and every later
  *                            one of the call that needs a page
  *   DLRM_ERRBIT_INVALID_ARG  a slot written twice in one call (the first
- *                            counts), a fork or copy into a slot that is not
- *                            empty, a history past max_pages */
+ *                            counts; history_free and history_trim, which find
+ *                            nothing left, pass over it), a fork or copy into a
+ *                            slot that is not empty, a history past max_pages
+ *   DLRM_ERRBIT_TIMEOUT      a bounded wait of history_attention ran out: its
+ *                            outputs are undefined, the pool is as it was */
 #define DLRM_ERRBIT_INVALID_ARG (1u << DLRM_ERR_INVALID_ARG)
 #define DLRM_ERRBIT_OOM         (1u << DLRM_ERR_OOM)
 
@@ -591,7 +594,14 @@ dlrm_status_t history_compact(const dlrm_history_t* h, void* stream);
  * t < sinks. A row that sees nothing gets zeros and lse -infinity; one that sees
  * events whose scores are all -infinity is 0 / 0, NaN, with lse -infinity. Scores,
  * softmax statistics and sums are fp32; masked events have no influence,
- * whatever they hold.
+ * whatever they hold. Factors of the products carry fewer bits than fp32:
+ *   over a cache    fp32: queries and weights 22. fp16: weights 11. bf16: weights 11,
+ *                   or 8 where the requests have 64 query rows a kv head and more on
+ *                   average, and all kv heads 4096 in all
+ *   over plain rows fp32: every factor 22 (and the last 22 of a product's 44 left
+ *                   out). fp16: weights 11. bf16: weights 8
+ * and sums over plain 16-bit rows, or over a cache with 8-bit weights, lose up to
+ * 2^-24 of themselves for every 16 events (2^-12 over 65,000).
  *   q, out  (q_rows, n_heads, head_dim) of dtype; (t, h, d) at
  *           t * ld + h * ld_head + d; out must not overlap an input, and its rows
  *           and heads not one another (INVALID_ARG)
