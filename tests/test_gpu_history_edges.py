@@ -388,6 +388,33 @@ def test_a_cache_is_as_ever_after_a_wait_that_ran_out(dim, lens, counts):
         assert cache.error() == dl.OK
 
 
+@pytest.mark.parametrize("dim", [32, 64, 128])
+def test_attention_over_a_cache_that_gives_up_in_the_middle(dim):
+    """Limits about as long as one step of the pipeline: CTAs give up with parts of their
+    units done, and calls after it are as ever."""
+    rng = np.random.default_rng(51)
+    lens, counts = [6000, 3000, 500, 6000], [2100, 1000, 300, 40]
+    cache, pool = make(250, 4, 100, 2, dim, 64)
+    fill(cache, pool, rng, [0, 1, 2, 3], lens)
+    slots, at = i32(range(4)), i32(starts_of(counts))
+    q = rows(rng, sum(counts), 4, dim, "bf16", 0.3)
+    want = dl.history_attention(cache, slots, at, q)
+    ran_out = 0
+    for limit in (200, 1000, 3000, 10_000):
+        dl.attention_test_stall(limit)
+        try:
+            dl.history_attention(cache, slots, at, q)
+            status = cache.error()
+        finally:
+            dl.attention_test_stall()
+        assert status in (dl.OK, dl.ERR_TIMEOUT)
+        ran_out += status == dl.ERR_TIMEOUT
+        for _ in range(2):
+            assert torch.equal(dl.history_attention(cache, slots, at, q), want)
+        assert cache.error() == dl.OK
+    assert ran_out > 0
+
+
 def test_the_stall_hook_checks_its_arguments():
     with pytest.raises(dl.DlrmError):
         dl.attention_test_stall(-1)
