@@ -112,7 +112,9 @@ def _on(stream, device):
     if stream is None:
         return contextlib.nullcontext()
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        # (1, the legacy default stream's handle, is no address, and torch takes none such)
+        stream = (torch.cuda.default_stream(device) if int(stream) == 1
+                  else torch.cuda.ExternalStream(int(stream), device=device))
     return torch.cuda.stream(stream)
 
 

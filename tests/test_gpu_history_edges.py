@@ -270,6 +270,27 @@ def test_a_call_on_another_stream_while_the_current_one_is_busy():
     assert torch.equal(out, dl.history_attention(cache, slots, q_at, q))
 
 
+def test_streams_by_their_handles():
+    """A raw cudaStream_t: a stream's own, and the legacy and per-thread default streams'."""
+    rng = np.random.default_rng(52)
+    k = rows(rng, 40, 2, 64, "fp32")
+    want = dl.window_attention(k, k, k, i32([0, 40]))
+    at, one = i32([0, 40]), i32([0])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = []
+    for stream in (0, 1, 2, side.cuda_stream, side):
+        cache = dl.HistoryCache(4, 2, 2, 2, 64, stream=stream)
+        dl.history_append(cache, one, at, k, k, stream=stream)
+        torch.cuda.synchronize()
+        outs.append(dl.history_attention(cache, one, at, k, causal=True, stream=stream))
+        got = dl.window_attention(k, k, k, at, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        assert cache.error(stream) == dl.OK
+    assert all(torch.equal(x, outs[0]) for x in outs)
+
+
 # ------------------------------------------------------------------ starts
 
 @pytest.mark.parametrize("dtype", list(TYPES))
