@@ -34,8 +34,9 @@ EXPORTS = ("dlrm_version", "dlrm_status_string", "dlrm_create", "dlrm_forward",
            "dlrm_set_cluster_batch_limit", "dlrm_get_cluster_batch_limit",
            "dlrm_forward_kernels",
            "history_work_bytes", "history_reset", "history_append", "history_fork",
-           "history_copy", "history_free", "history_trim", "history_compact",
-           "history_attention", "window_attention", "attention_test_stall")
+           "history_copy", "history_reorder", "history_free", "history_trim", "history_compact",
+           "history_attention", "history_prefix_attention", "window_attention",
+           "attention_test_stall", "beam_select_work_bytes", "beam_select")
 NOALLOC_SCRATCH_BYTES = 16 << 20
 TRACE_SLOTS = 40
 
@@ -668,16 +669,20 @@ class DlrmModel:
             pass
 
 
-# The event-history operators (history.py), loaded on first use: like the rest
-# of the binding, importing the package does not import torch.
-_HISTORY = ("HistoryCache", "attention_test_stall", "history_append", "history_attention", "history_compact",
-            "history_copy", "history_fork", "history_free", "history_trim", "window_attention")
+# The event-history operators (history.py) and the beam search's (beams.py), loaded on first
+# use: like the rest of the binding, importing the package does not import torch.
+_LAZY = {"beams": ("beam_select",),
+         "history": ("HistoryCache", "attention_test_stall", "history_append", "history_attention",
+                     "history_compact", "history_copy", "history_fork", "history_free",
+                     "history_prefix_attention", "history_reorder", "history_trim", "window_attention")}
 
 
 def __getattr__(name: str):
-    if name not in _HISTORY:
-        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import history
-    for n in _HISTORY:
-        globals()[n] = getattr(history, n)
-    return globals()[name]
+    for module, names in _LAZY.items():
+        if name in names:
+            from importlib import import_module
+            found = import_module("." + module, __name__)
+            for n in names:
+                globals()[n] = getattr(found, n)
+            return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

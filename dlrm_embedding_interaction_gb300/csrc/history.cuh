@@ -117,7 +117,7 @@ __device__ __forceinline__ bool finite(float x) {
 // The parts of a pool's scratch (byte offsets; every part 16-byte aligned).
 struct HistoryWork {
   int64_t head, mark_slot, mark_page, request, items, stash, remap, holes, movers, tiles, counters,
-      partials, total;
+      partials, mark_keep, dropped, prefix_head, members, found_tiles, tiles_of, cuts, total;
 };
 
 // CTAs of one attention launch that can hold an unfinished row tile, and the
@@ -130,6 +130,13 @@ constexpr int kAttnPartial = kAttnRows * (128 + 2);
 constexpr int kAttnTcCtas = 152;
 constexpr int kAttnTcPartial = 256 * (128 + 2);
 static_assert(kAttnTcCtas * 8 <= kAttnMaxCtas, "counters");
+constexpr int64_t kAttnPartialFloats =
+    int64_t(2) * (kAttnMaxCtas * kAttnPartial > kAttnTcCtas * kAttnTcPartial ? kAttnMaxCtas * kAttnPartial
+                                                                             : kAttnTcCtas * kAttnTcPartial);
+// Attention with a shared prefix: bytes of what its plan keeps of a request and of a
+// tile of 8 rows or more; tiles of a call beside those of its groups, which are
+// no more than the slots.
+constexpr int kPrefixMember = 32, kPrefixTile = 48, kPrefixTiles = 32768;
 
 inline HistoryWork history_work(const dlrm_history_t& h) {
   HistoryWork w{};
@@ -153,7 +160,14 @@ inline HistoryWork history_work(const dlrm_history_t& h) {
   w.movers = take(4 * pages);
   w.tiles = take(8 * (pages / 1024 + 1));
   w.counters = take(4 * kAttnMaxCtas);
-  w.partials = take(int64_t(4) * 2 * std::max(kAttnMaxCtas * kAttnPartial, kAttnTcCtas * kAttnTcPartial));
+  w.partials = take(4 * kAttnPartialFloats);
+  w.mark_keep = take(4 * slots);
+  w.dropped = take(4 * entries);
+  w.prefix_head = take(16);
+  w.members = take(kPrefixMember * slots);
+  w.found_tiles = take(kPrefixTile * (kPrefixTiles + slots));
+  w.tiles_of = take(kPrefixTile * (kPrefixTiles + slots));
+  w.cuts = take(8 * (kAttnMaxCtas + 1));
   w.total = at;
   return w;
 }
@@ -178,7 +192,16 @@ cudaError_t launch_history_attention(const dlrm_history_t& h, const dlrm_attenti
 bool history_tc_takes(const dlrm_history_t& h, const dlrm_attention_t& a);
 cudaError_t launch_history_attention_tc(const dlrm_history_t& h, const dlrm_attention_t& a,
                                         int32_t* counters, float* partials, cudaStream_t stream);
+cudaError_t launch_history_prefix_attention(const dlrm_history_t& h, const dlrm_attention_t& a,
+                                            const int32_t* groups, int n_groups, cudaStream_t stream);
+cudaError_t launch_history_reorder(const dlrm_history_t& h, const int32_t* slots, const int32_t* parents,
+                                   int batch, cudaStream_t stream);
 cudaError_t launch_window_attention(const dlrm_attention_t& a, cudaStream_t stream);
+// beam_select.cu
+constexpr int kBeamMaxWidth = 256;
+int64_t beam_select_work(const dlrm_beam_select_t& a);
+bool beam_select_fits(const dlrm_beam_select_t& a);
+cudaError_t launch_beam_select(const dlrm_beam_select_t& a, cudaStream_t stream);
 WaitCfg attention_wait();                        // attention_test_stall's
 
 }  // namespace dlrm

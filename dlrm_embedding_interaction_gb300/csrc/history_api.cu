@@ -94,6 +94,16 @@ bool rows_overlap(int64_t rows, int64_t ld, int64_t heads, int64_t ld_head, int6
   return false;
 }
 
+dlrm_status_t check_select(const dlrm_beam_select_t* a) {
+  if (!a || a->rows < 0 || a->vocab < 1 || a->ld < 0 || a->ld_allowed < 0 || a->groups < 0 || a->width < 1 ||
+      !dtype_ok(a->dtype))
+    return DLRM_ERR_INVALID_ARG;
+  if (a->width > dlrm::kBeamMaxWidth || a->rows >= (int64_t(1) << 31) ||
+      a->vocab > (int64_t(1) << 31) - (int64_t(1) << 20) || !dlrm::beam_select_fits(*a))
+    return DLRM_ERR_UNSUPPORTED;
+  return DLRM_OK;
+}
+
 }  // namespace
 
 namespace dlrm {
@@ -163,6 +173,16 @@ dlrm_status_t history_copy(const dlrm_history_t* h, const int32_t* src, const in
       dlrm::launch_history_fork(*h, src, dst, batch, false, static_cast<cudaStream_t>(stream)));
 }
 
+dlrm_status_t history_reorder(const dlrm_history_t* h, const int32_t* slots, const int32_t* parents,
+                              int32_t batch, void* stream) {
+  dlrm_status_t s = check_pool(h);
+  if (s == DLRM_OK) s = check_slots(h, slots, batch);
+  if (s == DLRM_OK) s = check_slots(h, parents, batch);
+  if (s != DLRM_OK || batch == 0) return s;
+  return status_of(
+      dlrm::launch_history_reorder(*h, slots, parents, batch, static_cast<cudaStream_t>(stream)));
+}
+
 dlrm_status_t history_free(const dlrm_history_t* h, const int32_t* slots, int32_t batch,
                            void* stream) {
   dlrm_status_t s = check_pool(h);
@@ -203,6 +223,47 @@ dlrm_status_t history_attention(const dlrm_history_t* h, const dlrm_attention_t*
   if (rows_overlap(a->q_rows, a->ld_out, a->n_heads, a->ld_out_head, h->head_dim))
     return DLRM_ERR_INVALID_ARG;
   return status_of(dlrm::launch_history_attention(*h, *a, static_cast<cudaStream_t>(stream)));
+}
+
+dlrm_status_t history_prefix_attention(const dlrm_history_t* h, const dlrm_attention_t* a,
+                                       const int32_t* groups, int32_t n_groups, void* stream) {
+  dlrm_status_t s = check_pool(h);
+  if (s != DLRM_OK) return s;
+  bool run;
+  s = check_attention(a, h->n_heads, &run);
+  if (s != DLRM_OK) return s;
+  if (a->batch > h->n_slots || n_groups < 0 || n_groups > h->n_slots) return DLRM_ERR_INVALID_ARG;
+  if (!run || n_groups == 0) return DLRM_OK;
+  if (!a->slots || !aligned_to(a->slots, 4) || !groups || !aligned_to(groups, 4)) return DLRM_ERR_INVALID_ARG;
+  // tiles of 8 rows of a kv head have space in the scratch, and work units (a block of
+  // 32 events of a tile) are counted in int32: a tile reads the shared events and
+  // those of its requests, and a request lies in a tile more than it fills
+  const int64_t tiles = a->q_rows * (a->n_heads / h->n_heads) / 8 + n_groups;
+  const int64_t events = static_cast<int64_t>(h->max_pages) * h->page_tokens;
+  if (tiles > dlrm::kPrefixTiles + n_groups ||
+      (2 * tiles + a->batch) * h->n_heads >= (int64_t(1) << 31) / (events / 32 + 3))
+    return DLRM_ERR_UNSUPPORTED;
+  if (rows_overlap(a->q_rows, a->ld_out, a->n_heads, a->ld_out_head, h->head_dim))
+    return DLRM_ERR_INVALID_ARG;
+  return status_of(dlrm::launch_history_prefix_attention(*h, *a, groups, n_groups,
+                                                         static_cast<cudaStream_t>(stream)));
+}
+
+int64_t beam_select_work_bytes(const dlrm_beam_select_t* a) {
+  return check_select(a) == DLRM_OK ? dlrm::beam_select_work(*a) : -1;
+}
+
+dlrm_status_t beam_select(const dlrm_beam_select_t* a, void* stream) {
+  const dlrm_status_t s = check_select(a);
+  if (s != DLRM_OK || a->groups == 0) return s;
+  if (!a->starts || !aligned_to(a->starts, 4) || !a->out_scores || !aligned_to(a->out_scores, 4) || !a->out_rows ||
+      !aligned_to(a->out_rows, 4) || !a->out_tokens || !aligned_to(a->out_tokens, 4) || !aligned_to(a->err, 4) ||
+      !aligned_to(a->scores, 4))
+    return DLRM_ERR_INVALID_ARG;
+  if (a->rows > 0 && (!a->logits || !aligned_to(a->logits, dlrm::dtype_bytes(a->dtype)) || !a->work ||
+                      !aligned_to(a->work, 16) || a->work_bytes < dlrm::beam_select_work(*a)))
+    return DLRM_ERR_INVALID_ARG;
+  return status_of(dlrm::launch_beam_select(*a, static_cast<cudaStream_t>(stream)));
 }
 
 dlrm_status_t window_attention(const dlrm_attention_t* a, void* stream) {

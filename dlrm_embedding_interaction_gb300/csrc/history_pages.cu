@@ -9,6 +9,7 @@
 //   fork       plan (one CTA), share and copy; likewise
 //   copy       plan (one CTA), rows, copy
 //   free/trim  one CTA for few pages; else release, count, push (a CTA a request)
+//   reorder    plan (one CTA), take (references and copies), commit
 //   compact    count, match, move, rename
 // The plan gives every request its place in the free stack by a prefix sum
 // over the requests, so page numbers do not depend on timing; freed pages are
@@ -49,6 +50,8 @@ struct Pool {
   int32_t* holes;
   int32_t* movers;
   int32_t* tiles;
+  int32_t* mark_keep;
+  int32_t* dropped;
 };
 
 Pool make_pool(const dlrm_history_t& h) {
@@ -65,6 +68,8 @@ Pool make_pool(const dlrm_history_t& h) {
   p.holes = work_part<int32_t>(h, w.holes);
   p.movers = work_part<int32_t>(h, w.movers);
   p.tiles = work_part<int32_t>(h, w.tiles);
+  p.mark_keep = work_part<int32_t>(h, w.mark_keep);
+  p.dropped = work_part<int32_t>(h, w.dropped);
   return p;
 }
 
@@ -850,6 +855,245 @@ __global__ void __launch_bounds__(kPlanThreads) free_small_kernel(Pool p, const 
   if (threadIdx.x == 0) *h.n_free = min(top + all, h.n_pages);
 }
 
+// ------------------------------------------------------------------ reorder
+
+// What the plan of a reordering knows of request b, in a Request: slot (-1: no effect),
+// source (-1: the slot becomes empty), length of the source, count: events of the slot
+// before the call, need: a page to copy the source's last one to, which is number
+// `base` of the call's.
+//
+// A slot's table is read by every request that continues it and written by its own, and
+// a page is free when all have counted, so three launches: the plan; references, copies
+// and the new tables into scratch; then tables and lengths from there, and one CTA that
+// pushes the pages that lost their last reference. Last pages that are not full have one
+// holder: those of slots that nobody continues are known to the plan, and are the first
+// that copies go to.
+__global__ void __launch_bounds__(kPlanThreads) reorder_plan_kernel(Pool p, const int32_t* slots,
+                                                                    const int32_t* parents, int batch) {
+  __shared__ int sums[kWarp + 1];
+  const dlrm_history_t& h = p.h;
+  const int G = h.page_tokens, M = h.max_pages;
+  pdl_wait();
+  pdl_trigger();
+  const int nfree = min(max(*h.n_free, 0), h.n_pages);
+  auto in = [&](int slot) { return slot >= 0 && slot < h.n_slots; };
+  auto length_of = [&](int slot) {
+    return static_cast<int>(min(static_cast<int64_t>(max(h.lengths[slot], 0)), static_cast<int64_t>(M) * G));
+  };
+  // the page of a slot's last events, if it is not full
+  auto part_of = [&](int slot, int length) {
+    const int page = length % G != 0 ? h.table[static_cast<int64_t>(slot) * M + length / G] : -1;
+    return is_page(h, page) ? page : -1;
+  };
+  for (int b = threadIdx.x; b < batch; b += kPlanThreads) {
+    const int d = slots[b];
+    if (in(d)) atomicMin(&p.mark_slot[d], b);
+  }
+  __syncthreads();
+  // of the requests that continue a slot, its own or else the first one keeps its last page
+  for (int b = threadIdx.x; b < batch; b += kPlanThreads) {
+    const int d = slots[b], from = parents[b];
+    Request r{-1, -1, 0, 0, 0, 0, 0, 0};
+    if (!in(d)) {
+      flag(h.err, DLRM_ERRBIT_INDEX_OOB);
+    } else if (__ldcg(&p.mark_slot[d]) != b) {
+      flag(h.err, DLRM_ERRBIT_INVALID_ARG);
+    } else {
+      r.slot = d;
+      int s = from == -1 ? -1 : from >= 0 && from < batch ? slots[from] : h.n_slots;
+      if (s != -1 && !in(s)) s = h.n_slots;
+      if (from != -1 && s == -1) s = h.n_slots;   // the slot of the request named is none
+      if (s == h.n_slots) {
+        flag(h.err, DLRM_ERRBIT_INDEX_OOB);
+        s = d;
+      }
+      r.source = s;
+      if (s >= 0) atomicMin(&p.mark_keep[s], s == d ? -1 : b);
+    }
+    p.request[b] = r;
+  }
+  __syncthreads();
+  int copies = 0, given = 0;
+  for (int b0 = 0; b0 < batch; b0 += kPlanThreads) {
+    const int b = b0 + static_cast<int>(threadIdx.x);
+    Request r{-1, -1, 0, 0, 0, 0, 0, 0};
+    int page = -1;                                // given up
+    if (b < batch) {
+      r = p.request[b];
+      if (r.slot >= 0) {
+        r.count = length_of(r.slot);
+        if (__ldcg(&p.mark_keep[r.slot]) == INT32_MAX) page = part_of(r.slot, r.count);
+        if (r.source >= 0) {
+          r.length = length_of(r.source);
+          const int me = r.source == r.slot ? -1 : b;
+          r.need = __ldcg(&p.mark_keep[r.source]) != me && part_of(r.source, r.length) >= 0;
+        }
+      }
+    }
+    int total;
+    r.base = copies + block_exclusive(r.need, sums, total);
+    copies += total;
+    const int rank = given + block_exclusive(page >= 0 ? 1 : 0, sums, total);
+    given += total;
+    // (as many as pages at most, whatever a broken table says)
+    if (page >= 0 && rank < h.n_pages) p.holes[rank] = page;
+    if (b < batch) p.request[b] = r;
+    __syncthreads();                              // `sums` before the next requests
+  }
+  __syncthreads();
+  given = min(given, h.n_pages);
+  const bool short_of = copies - given > nfree;   // then nothing at all is done
+  for (int b = threadIdx.x; b < batch; b += kPlanThreads) {
+    const int d = slots[b];
+    if (in(d)) {
+      p.mark_slot[d] = INT32_MAX;
+      p.mark_keep[d] = INT32_MAX;
+    }
+    p.request[b].items = 0;
+    if (short_of) p.request[b].slot = -1;
+  }
+  if (threadIdx.x == 0) {
+    if (short_of) flag(h.err, DLRM_ERRBIT_OOM);
+    p.head[kHeadItems] = given;
+    p.head[kHeadTop] = nfree;
+    p.head[kHeadMoves] = short_of ? 0 : max(copies - given, 0);   // taken from the stack
+  }
+}
+
+// By the CTAs (request, piece): piece by piece the copy of a last page; piece 0 counts
+// references, and writes down the new table row and, in order, the pages that the old one
+// holds no more.
+__global__ void __launch_bounds__(kCopyThreads) reorder_take_kernel(Pool p, int pieces) {
+  __shared__ int sums[kWarp + 1];
+  pdl_wait();
+  pdl_trigger();
+  const dlrm_history_t& h = p.h;
+  const int G = h.page_tokens, M = h.max_pages, b = blockIdx.x;
+  const Request r = p.request[b];
+  if (r.slot < 0 || r.source == r.slot) return;
+  const int piece = blockIdx.z * gridDim.y + blockIdx.y;
+  const int given = p.head[kHeadItems], top = p.head[kHeadTop];
+  const int32_t* from = h.table + static_cast<int64_t>(max(r.source, 0)) * M;
+  const int32_t* old_row = h.table + static_cast<int64_t>(r.slot) * M;
+  const int n_new = r.source < 0 ? 0 : (r.length + G - 1) / G, n_old = (r.count + G - 1) / G;
+  int page = -1;
+  if (r.need) page = r.base < given ? p.holes[r.base] : h.free_pages[top - 1 - (r.base - given)];
+  if (piece == 0) {
+    int drops = 0;
+    for (int j0 = 0; j0 < max(n_old, n_new); j0 += kCopyThreads) {
+      const int j = j0 + static_cast<int>(threadIdx.x);
+      const int was = j < n_old ? old_row[j] : -1;
+      int now = j < n_new ? from[j] : -1;
+      if (r.need && j == n_new - 1) now = page;
+      if (j < n_new) p.stash[static_cast<int64_t>(b) * M + j] = now;
+      const bool drop = was != now && is_page(h, was);
+      int total;
+      const int rank = drops + block_exclusive(drop ? 1 : 0, sums, total);
+      drops += total;
+      if (drop) {
+        atomicSub(&h.refs[was], 1);
+        atomicMax(&p.mark_page[was], b * M + rank);
+        p.dropped[static_cast<int64_t>(b) * M + rank] = was;
+      }
+      if (was != now && is_page(h, now)) atomicAdd(&h.refs[now], 1);
+    }
+    if (threadIdx.x == 0) p.request[b].items = drops;
+  }
+  // (r.need: the source's last page is one of the pool's)
+  if (r.need && is_page(h, page) && piece < 2 * pieces)
+    copy_piece(h, piece / pieces, piece % pieces, from[n_new - 1], page);
+}
+
+constexpr int kCommitThreads = 1024;
+
+// CTA 0 pushes freed pages, the last position of the last request first; the others
+// write tables, a warp a request.
+__global__ void __launch_bounds__(kCommitThreads) reorder_commit_kernel(Pool p, int batch) {
+  __shared__ int sums[kWarp + 1];
+  pdl_wait();
+  pdl_trigger();
+  const dlrm_history_t& h = p.h;
+  const int G = h.page_tokens, M = h.max_pages, lane = threadIdx.x % kWarp;
+  if (blockIdx.x > 0) {
+    const int b = (blockIdx.x - 1) * (kCommitThreads / kWarp) + threadIdx.x / kWarp;
+    if (b >= batch) return;
+    const Request r = p.request[b];
+    if (r.slot < 0 || r.source == r.slot) return;
+    const int n_new = r.source < 0 ? 0 : (r.length + G - 1) / G, n_old = (r.count + G - 1) / G;
+    int32_t* row = h.table + static_cast<int64_t>(r.slot) * M;
+    for (int j = lane; j < max(n_old, n_new); j += kWarp)
+      row[j] = j < n_new ? p.stash[static_cast<int64_t>(b) * M + j] : -1;
+    if (lane == 0) h.lengths[r.slot] = r.length;
+    return;
+  }
+  const int top = p.head[kHeadTop] - p.head[kHeadMoves];
+  auto freed = [&](int b, int i, int& page) {     // whether this position pushes its page
+    const int at = b * M + i;
+    page = p.dropped[static_cast<int64_t>(b) * M + i];
+    if (__ldcg(&p.mark_page[page]) != at) {
+      page = -1;
+      return false;
+    }
+    return __ldcg(&h.refs[page]) <= 0;
+  };
+  // requests from the last one down, a thread each; many pages of one by its warp
+  int pushed = 0;
+  for (int e0 = 0; e0 < batch; e0 += kCommitThreads) {
+    const int b = batch - 1 - e0 - static_cast<int>(threadIdx.x);
+    const int items = b >= 0 ? p.request[b].items : 0;
+    int n = 0;
+    if (items <= 2)
+      for (int i = 0; i < items; ++i) {
+        int page;
+        n += freed(b, i, page);
+      }
+    for (unsigned many = __ballot_sync(0xffffffffu, items > 2); many; many &= many - 1) {
+      const int l = __ffs(many) - 1;
+      const int of = __shfl_sync(0xffffffffu, b, l), all = __shfl_sync(0xffffffffu, items, l);
+      int c = 0;
+      for (int i0 = 0; i0 < all; i0 += kWarp) {
+        int page;
+        c += __popc(__ballot_sync(0xffffffffu, i0 + lane < all && freed(of, i0 + lane, page)));
+      }
+      if (lane == l) n = c;
+    }
+    int total;
+    const int before = pushed + block_exclusive(n, sums, total);
+    pushed += total;
+    // every thread has counted: marks may go, each by its own position's reader
+    if (items <= 2) {
+      int q = top + before;
+      for (int i = items - 1; i >= 0; --i) {
+        int page;
+        if (freed(b, i, page)) {
+          if (q < h.n_pages) h.free_pages[q] = page;
+          ++q;
+          h.refs[page] = 0;
+        }
+        if (page >= 0) p.mark_page[page] = -1;
+      }
+    }
+    for (unsigned many = __ballot_sync(0xffffffffu, items > 2); many; many &= many - 1) {
+      const int l = __ffs(many) - 1;
+      const int of = __shfl_sync(0xffffffffu, b, l), all = __shfl_sync(0xffffffffu, items, l);
+      int q = top + __shfl_sync(0xffffffffu, before, l);
+      for (int i0 = (all - 1) / kWarp * kWarp; i0 >= 0; i0 -= kWarp) {
+        int page = -1;
+        const bool push = i0 + lane < all && freed(of, i0 + lane, page);
+        const unsigned who = __ballot_sync(0xffffffffu, push);
+        if (push) {
+          const int at = q + __popc(who >> lane) - 1;   // this lane's bit among those from it on
+          if (at < h.n_pages) h.free_pages[at] = page;
+          h.refs[page] = 0;
+        }
+        if (page >= 0) p.mark_page[page] = -1;
+        q += __popc(who);
+      }
+    }
+  }
+  if (threadIdx.x == 0 && batch > 0) *h.n_free = min(top + pushed, h.n_pages);
+}
+
 // ------------------------------------------------------------------ compact
 
 constexpr int kTile = 1024;   // pages a CTA looks at
@@ -932,7 +1176,8 @@ __global__ void __launch_bounds__(256) rename_kernel(Pool p) {
   if (first == 0) *h.n_free = h.n_pages - live;
 }
 
-__global__ void __launch_bounds__(256) reset_kernel(Pool p, int32_t* counters, int n_counters) {
+__global__ void __launch_bounds__(256) reset_kernel(Pool p, int32_t* counters, int n_counters,
+                                                    int32_t* prefix_head) {
   const dlrm_history_t& h = p.h;
   const int64_t first = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
   const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
@@ -946,12 +1191,14 @@ __global__ void __launch_bounds__(256) reset_kernel(Pool p, int32_t* counters, i
   for (int64_t i = first; i < h.n_slots; i += step) {
     h.lengths[i] = 0;
     p.mark_slot[i] = INT32_MAX;
+    p.mark_keep[i] = INT32_MAX;
   }
   for (int64_t i = first; i < n_counters; i += step) counters[i] = 0;
   if (first == 0) {
     *h.n_free = h.n_pages;
     *h.err = 0;
     p.head[kHeadArrived] = 0;
+    *prefix_head = 0;
   }
 }
 
@@ -994,7 +1241,7 @@ cudaError_t launch_history_reset(const dlrm_history_t& h, cudaStream_t stream) {
   const int64_t most = std::max<int64_t>(static_cast<int64_t>(h.n_slots) * h.max_pages, h.n_pages);
   const HistoryWork w = history_work(h);
   reset_kernel<<<grid_for((most + 255) / 256, 8), 256, 0, stream>>>(
-      make_pool(h), work_part<int32_t>(h, w.counters), kAttnMaxCtas);
+      make_pool(h), work_part<int32_t>(h, w.counters), kAttnMaxCtas, work_part<int32_t>(h, w.prefix_head));
   return cudaGetLastError();
 }
 
@@ -1059,6 +1306,22 @@ cudaError_t launch_history_free(const dlrm_history_t& h, const int32_t* slots, i
   if (e != cudaSuccess) return e;
   return launch_pdl(push_kernel, dim3(batch), dim3(kFreeThreads), 0, stream, p, batch,
                     window > 0 ? 0 : 1);
+}
+
+cudaError_t launch_history_reorder(const dlrm_history_t& h, const int32_t* slots, const int32_t* parents,
+                                   int batch, cudaStream_t stream) {
+  const Pool p = make_pool(h);
+  cudaError_t e = launch_pdl(reorder_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p, slots, parents, batch);
+  if (e != cudaSuccess) return e;
+  const int pieces = pieces_of(h);
+  // (a grid's y and z end at 65535)
+  const unsigned z = (2 * pieces + 65534) / 65535;
+  e = launch_pdl(reorder_take_kernel, dim3(batch, (2 * pieces + z - 1) / z, z), dim3(kCopyThreads), 0, stream, p,
+                 pieces);
+  if (e != cudaSuccess) return e;
+  constexpr int kPer = kCommitThreads / kWarp;
+  return launch_pdl(reorder_commit_kernel, dim3(1 + (batch + kPer - 1) / kPer), dim3(kCommitThreads), 0, stream, p,
+                    batch);
 }
 
 cudaError_t launch_history_compact(const dlrm_history_t& h, cudaStream_t stream) {

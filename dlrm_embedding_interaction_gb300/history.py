@@ -68,10 +68,12 @@ def _bind(lib_):
                            st),
         "history_fork": ([h, _VP, _VP, _I32, _VP], st),
         "history_copy": ([h, _VP, _VP, _I32, _VP], st),
+        "history_reorder": ([h, _VP, _VP, _I32, _VP], st),
         "history_free": ([h, _VP, _I32, _VP], st),
         "history_trim": ([h, _VP, _I32, _I32, _I32, _VP], st),
         "history_compact": ([h, _VP], st),
         "history_attention": ([h, a, _VP], st),
+        "history_prefix_attention": ([h, a, _VP, _I32, _VP], st),
         "window_attention": ([a, _VP], st),
         "attention_test_stall": ([_I64, _I32], st),
     }
@@ -294,6 +296,16 @@ def history_copy(cache: HistoryCache, src, dst, stream=None) -> None:
                 stream)
 
 
+def history_reorder(cache: HistoryCache, slots, parents, stream=None) -> None:
+    """``slots[b]`` becomes a history like the one that ``slots[parents[b]]`` held before
+    the call (-1: empty), all at once: a step of a beam search, with ``beam_select``'s
+    ``rows`` as parents. Full pages are shared, last ones that are not full copied for all
+    that continue them but one. ``slots`` and ``parents`` (B,) are int32; a slot occurs
+    once."""
+    _slots_call("history_reorder", cache, (("history_reorder: slots", slots),
+                                           ("history_reorder: parents", parents)), stream)
+
+
 def history_free(cache: HistoryCache, slots, stream=None) -> None:
     """Empties slots; pages that no slot holds any more become free."""
     _slots_call("history_free", cache, (("history_free: slots", slots),), stream)
@@ -361,16 +373,45 @@ def history_attention(cache: HistoryCache, slots, starts, q, out=None, *, scale=
     ``window`` events and the first ``sinks``. ``scale`` defaults to head_dim
     ** -0.5. ``lse``, (rows, query heads) float32, receives the log of the sum of
     exponentials."""
-    where = "history_attention"
+    return _cache_attention("history_attention", cache, slots, starts, None, q, out, scale, causal, window,
+                            sinks, lse, stream)
+
+
+def history_prefix_attention(cache: HistoryCache, slots, starts, groups, q, out=None, *, scale=None,
+                             causal: bool = False, window: int = 0, sinks: int = 0, lse=None,
+                             stream=None):
+    """history_attention for histories that begin alike, forks of one history above all:
+    requests [groups[g], groups[g+1]) are a group, and the first pages that its slots
+    have in common are read once for all its rows; returns ``out``.
+
+    ``groups``: (n_groups + 1,) int32. The result is history_attention's whatever the
+    groups; rows of requests that no group holds stay as they were. At most as many
+    requests and groups as the cache has slots."""
+    return _cache_attention("history_prefix_attention", cache, slots, starts, groups, q, out, scale, causal,
+                            window, sinks, lse, stream)
+
+
+_LABELS = {where: tuple(f"{where}: {name}" for name in ("slots", "starts", "groups", "q"))
+           for where in ("history_attention", "history_prefix_attention")}
+
+
+def _cache_attention(where, cache, slots, starts, groups, q, out, scale, causal, window, sinks, lse, stream):
     c = _cache_of(cache, where)
     index = c._index
-    b = _int32_vector(slots, "history_attention: slots", None, index)
-    _int32_vector(starts, "history_attention: starts", b + 1, index)
-    shape, qs = _rows(q, "history_attention: q", None, c.head_dim, index)
+    l_slots, l_starts, l_groups, l_q = _LABELS[where]
+    b = _int32_vector(slots, l_slots, None, index)
+    _int32_vector(starts, l_starts, b + 1, index)
+    shape, qs = _rows(q, l_q, None, c.head_dim, index)
     rows, heads, dim = shape
     if heads < 1 or heads % c.n_heads:
         raise ValueError(f"{where}: q: {heads} heads are no multiple of the cache's {c.n_heads}")
-    dtype = _dtype_code(q, "history_attention: q")
+    dtype = _dtype_code(q, l_q)
+    if groups is not None:
+        n_groups = _int32_vector(groups, l_groups, None, index) - 1
+        if n_groups < 0:
+            raise ValueError(f"{where}: groups: expected at least one entry")
+        if max(b, n_groups) > c.n_slots:
+            raise ValueError(f"{where}: {b} requests in {n_groups} groups for {c.n_slots} slots")
     out, os = _check_outputs(where, q, shape, out, lse, window, sinks, index, stream)
     try:
         args = _ATTENTION.pack(
@@ -379,7 +420,11 @@ def history_attention(cache: HistoryCache, slots, starts, q, out=None, *, scale=
             dim, dtype, causal, window, sinks, dim ** -0.5 if scale is None else _scale(where, scale), 0)
     except struct.error as e:
         raise _unpackable(where, e) from None
-    _check(_bound().history_attention(c._ref, args, _raw_stream(stream, index)), where)
+    if groups is None:
+        _check(_bound().history_attention(c._ref, args, _raw_stream(stream, index)), where)
+    else:
+        _check(_bound().history_prefix_attention(c._ref, args, groups.data_ptr(), n_groups,
+                                                 _raw_stream(stream, index)), where)
     return out
 
 

@@ -567,6 +567,19 @@ dlrm_status_t history_fork(const dlrm_history_t* h, const int32_t* src, const in
 dlrm_status_t history_copy(const dlrm_history_t* h, const int32_t* src, const int32_t* dst,
                            int32_t batch, void* stream);
 
+/* Slot slots[b] becomes a history like the one that slots[parents[b]] held before the
+ * call (parents index the call's own requests; parents[b] = b: as it was; -1: empty), all
+ * at once: the step of a beam search. Full pages are shared. Of the requests that continue
+ * a history whose last page is not full, that slot's own keeps the page, or else the
+ * first; the others get copies, in pages that the call's slots give up because nobody
+ * continues them (in the order of the requests), then from the free stack. Pages that
+ * lose their last reference return to the stack as in history_free. A request whose parent
+ * is out of range leaves its slot as it was (INDEX_OOB); with too few pages the whole call
+ * has no effect (OOM).
+ *   slots, parents (batch) int32, batch <= n_slots; a slot occurs once */
+dlrm_status_t history_reorder(const dlrm_history_t* h, const int32_t* slots, const int32_t* parents,
+                              int32_t batch, void* stream);
+
 /* Empties slots: their pages lose a reference, and pages without one return
  * to the free stack (the last page of the last slot first, so that what was
  * taken last is the first to be taken again). */
@@ -634,6 +647,19 @@ typedef struct {
 dlrm_status_t history_attention(const dlrm_history_t* h, const dlrm_attention_t* a, void* stream);
 dlrm_status_t window_attention(const dlrm_attention_t* a, void* stream);
 
+/* history_attention for requests whose histories begin alike, forks of one history
+ * above all: requests [groups[g], groups[g+1]) are a group, and the first pages that the
+ * tables of all its slots (those with rows and events) have in common are read once for
+ * all its rows. Outputs are history_attention's whatever the groups, but for rounding
+ * (weights carry 22 bits with fp32 rows, 11 with fp16 and bf16). Rows of requests that no
+ * group holds stay as they were.
+ *   groups  (n_groups + 1) int32; batch and n_groups <= n_slots
+ * Starts or groups that decrease or leave their range refuse the whole call
+ * (DLRM_ERRBIT_OFFSETS). UNSUPPORTED: more than 2^18 query rows of heads that share a kv
+ * head, and 2^31 work units or more. */
+dlrm_status_t history_prefix_attention(const dlrm_history_t* h, const dlrm_attention_t* a,
+                                       const int32_t* groups, int32_t n_groups, void* stream);
+
 /* Test hook of the failure detection, as dlrm_test_stall, for later calls of both
  * in this process. Their tensor-core kernels' waits are bounded: on expiry the
  * kernel sets DLRM_ERRBIT_TIMEOUT (in the pool's err; of window_attention in err,
@@ -644,6 +670,48 @@ dlrm_status_t window_attention(const dlrm_attention_t* a, void* stream);
  * piece of work back. (0, 0) restores normal operation. INVALID_ARG for a negative
  * limit. */
 dlrm_status_t attention_test_stall(int64_t wait_limit_ns, int32_t withhold);
+
+/* One step of a beam search over a vocabulary. Rows are beams, and rows
+ * [starts[g], starts[g+1]) are group g's (a user's); of its candidates, the pairs of a row
+ * i and a token t that the row allows, the `width` with the largest
+ *   scores[i] + logits[i][t] - log sum over allowed u of exp(logits[i][u])
+ * are written in falling order, equal ones by row, then token: their scores, rows (of the
+ * call, as history_reorder's parents are) and tokens. A token that is not allowed has no
+ * influence, whatever its logit; a row that allows one token alone continues with it
+ * at no cost. A row without an allowed token, or with a score of -infinity, has no
+ * candidates, and a logit of -infinity makes none. Places past the candidates hold
+ * -infinity, -1, -1. Scores are compared in 64 bits; the rows' logarithms of sums of
+ * exponentials are off by 2^-20 at most (far less with many terms), and rows whose scores
+ * lie closer may change places.
+ *   logits  (rows, vocab) of dtype, row i at i * ld; scores (rows) fp32, NULL: zeros
+ *   allowed (rows, vocab) bytes, 0: not allowed, row i at i * ld_allowed (0: one row for
+ *           all); NULL: every token is
+ *   starts  (groups + 1) int32; out_* (groups, width)
+ *   err     NULL or an int32 word for DLRM_ERRBIT_*: OFFSETS for starts that decrease or
+ *           pass the rows (that group has no rows), INVALID_ARG for a row with a NaN or
+ *           +infinity among its allowed logits or as its score (it has no candidates)
+ *   work    scratch of beam_select_work_bytes() bytes, 16-byte aligned, for this call
+ * width is 1 to 256, vocab 1 to 2^31 - 2^20; fewer than 2^31 rows and chunks of rows
+ * (else UNSUPPORTED). */
+typedef struct {
+  const void* logits;
+  const float* scores;
+  const uint8_t* allowed;
+  const int32_t* starts;
+  float* out_scores;
+  int32_t* out_rows;
+  int32_t* out_tokens;
+  int32_t* err;
+  void* work;
+  int64_t work_bytes;
+  int64_t rows, vocab, ld, ld_allowed;
+  int32_t groups, width, dtype;
+} dlrm_beam_select_t;
+
+/* Bytes of scratch for a call of these sizes (no pointer is read), or -1 for sizes that
+ * beam_select refuses. */
+int64_t beam_select_work_bytes(const dlrm_beam_select_t* a);
+dlrm_status_t beam_select(const dlrm_beam_select_t* a, void* stream);
 
 #ifdef __cplusplus
 }
