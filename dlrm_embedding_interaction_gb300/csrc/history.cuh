@@ -136,7 +136,7 @@ constexpr int64_t kAttnPartialFloats =
 // Attention with a shared prefix: bytes of what its plan keeps of a request and of a
 // tile of 8 rows or more; tiles of a call beside those of its groups, which are
 // no more than the slots.
-constexpr int kPrefixMember = 32, kPrefixTile = 48, kPrefixTiles = 32768;
+constexpr int kPrefixMember = 32, kPrefixTile = 48, kPrefixCut = 64, kPrefixTiles = 32768;
 
 inline HistoryWork history_work(const dlrm_history_t& h) {
   HistoryWork w{};
@@ -167,7 +167,7 @@ inline HistoryWork history_work(const dlrm_history_t& h) {
   w.members = take(kPrefixMember * slots);
   w.found_tiles = take(kPrefixTile * (kPrefixTiles + slots));
   w.tiles_of = take(kPrefixTile * (kPrefixTiles + slots));
-  w.cuts = take(8 * (kAttnMaxCtas + 1));
+  w.cuts = take(kPrefixCut * (kAttnMaxCtas + 1));
   w.total = at;
   return w;
 }

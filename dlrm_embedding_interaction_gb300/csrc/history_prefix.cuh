@@ -1,0 +1,831 @@
+// The second launch of history_prefix_attention: its kernel and what its plan hands it
+// (history_prefix.cu says how both work). One source file for each head_dim makes its
+// instances.
+#pragma once
+
+#include <atomic>
+
+#include "history_attention.cuh"
+
+namespace dlrm {
+namespace prefix {
+
+
+constexpr int kWholeBlocks = 16;                 // blocks of a tile that is never split
+constexpr int kLeastBlocks = 16;                 // blocks of a CTA at least, where tiles are longer
+constexpr int kWeights = 32;                     // parts whose weights lie in shared memory at once
+
+// What the plan knows of a request with rows, and of the tiles.
+struct Member {
+  int32_t slot, len, queries;
+  int32_t row0, rows;                            // among the group's rows
+  int32_t first;                                 // blocks of the group's earlier requests
+  int32_t sinks, block0;                         // blocks of its own events: the sinks', then from block0 on
+};
+static_assert(sizeof(Member) == kPrefixMember, "scratch size of a member");
+struct Tile {
+  int32_t first, blocks;                         // units of work (chunk of a kv head) before it; its blocks
+  int32_t q0, row0, rows;                        // the group's first query row; rows among the group's
+  int32_t member0, member1;                      // first and last request with rows in the tile
+  int32_t slot;                                  // whose table gives the shared pages
+  int32_t shared_sinks, shared0, shared_blocks;  // blocks of shared events: the sinks', then from shared0 on
+  int32_t own0;                                  // first block that is not shared
+};
+static_assert(sizeof(Tile) == kPrefixTile, "scratch size of a tile");
+
+struct Cut {                                     // where a CTA begins
+  int32_t unit, place;                           // first unit, and the tile that holds it
+  int32_t units, ctas;                           // of the call
+  Tile tile;
+};
+static_assert(sizeof(Cut) == kPrefixCut, "scratch size of a cut");
+
+// Chunks of a tile: one even where there is nothing to read, which writes zeros.
+__device__ __forceinline__ int chunks_of(const Tile& t, int split) {
+  return t.rows > 0 ? max(static_cast<int>(static_cast<unsigned>(t.blocks + split - 1) / static_cast<unsigned>(split)), 1) : 0;
+}
+// Blocks of a request's own events.
+__device__ __forceinline__ int blocks_of(const Member& m) {
+  return m.rows > 0 && m.len > 0 ? m.sinks + max((m.len + kBlock - 1) / kBlock - m.block0, 0) : 0;
+}
+
+struct Params {
+  dlrm_history_t h;
+  dlrm_attention_t a;
+  const int32_t* groups;
+  int n_groups;
+  int group;                                     // query heads of a kv head
+  int rows, split;                               // of a tile; warps that split a chunk's blocks
+  int grid;                                      // CTAs of the second launch
+  int vec_q;
+  int32_t* arrived;                              // CTAs of the plan that are done
+  Member* members;
+  Tile* found;                                   // tiles, with gaps between the groups
+  Tile* tiles;                                   // without
+  Cut* cuts;                                     // of each CTA, and the end
+  int32_t* counters;
+  float* partials;
+};
+
+cudaError_t launch_plan(const Params& p, cudaStream_t stream);
+// By head_dim.
+cudaError_t launch_32(Params& p, cudaStream_t stream);
+cudaError_t launch_64(Params& p, cudaStream_t stream);
+cudaError_t launch_128(Params& p, cudaStream_t stream);
+
+// Two fp32 at a time.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+// SPLIT: queries and weights as an f16 head and rest, in two MMA rows: fp32 rows, and
+// 16-bit ones that are no more than 8, whose other MMA rows would be empty. Without it
+// fp16 weights have their rest in a product of its own (an output has 11 bits too).
+template <int D, int DT, bool SPLIT, int MT, int WR>
+struct Shape {
+  static constexpr int kTile = SPLIT ? 8 : 16;    // rows of an MMA tile
+  static constexpr int kRows = kTile * MT * WR;
+  static constexpr int kSets = kWarps / WR;       // sets of warps, a ring and a block of each chunk each
+  static constexpr int kStages = WR == 1 ? (D == 128 ? 3 : 4) : D == 128 ? 4 : 6;
+  static constexpr int kBytes = 2 * kBlock * D;   // keys and values of a block
+  static constexpr int kStride = D + 4;           // of a row's sums in shared memory
+  static constexpr int kPartial = kRows * (D + 2);   // of a part in scratch: sums, maxima, sums of weights
+  static constexpr int kRing = kSets * kStages * kBytes;
+  static constexpr int kJoin = (kSets * kRows * (kStride + 2) + kWeights * kRows) * 4;
+  static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
+};
+
+template <int D, int DT, bool SPLIT, int MT, int WR>
+__global__ void __launch_bounds__(kThreads, D == 128 ? 2 : MT == 1 ? 3 : 2)
+prefix_attention_kernel(const __grid_constant__ Params p) {
+  using Sh = Shape<D, DT, SPLIT, MT, WR>;
+  constexpr bool kRest = !SPLIT && DT == DLRM_DTYPE_FP16;
+  constexpr int kTile = Sh::kTile, kRows = Sh::kRows, kSets = Sh::kSets, kStages = Sh::kStages;
+  constexpr int kStride = Sh::kStride, kPartial = Sh::kPartial;
+  constexpr int KW = D / 16;                      // key words of a thread and event tile
+  constexpr int VW = D / 32;                      // value words of a thread and event
+  constexpr int NT = D / 8;                       // n tiles of the output
+  constexpr int kPairsO = SPLIT ? 1 : 2;          // pairs of output values of a thread and n tile
+  constexpr int kR2 = SPLIT ? 1 : 2;              // rows of a thread and row tile
+  extern __shared__ __align__(128) unsigned char smem[];
+  // after the events: sums of each set and row, then maxima, sums of weights, weights of parts
+  float (*joined)[kRows][kStride] = reinterpret_cast<float (*)[kRows][kStride]>(smem);
+  float (*tops)[kRows] = reinterpret_cast<float (*)[kRows]>(&joined[kSets][0][0]);
+  float (*totals)[kRows] = reinterpret_cast<float (*)[kRows]>(&tops[kSets][0]);
+  float (*weight)[kRows] = reinterpret_cast<float (*)[kRows]>(&totals[kSets][0]);
+  __shared__ float row_top[kRows], row_total[kRows];
+  __shared__ int odd[kRows + 1];
+  __shared__ int see_end[kRows], see_gap0[kRows], see_gap1[kRows], row_member[kRows];
+  __shared__ int64_t row_at[kRows];               // query row, of the call
+  __shared__ int row_head[kRows];                 // head of the group
+  // requests with rows in the tile: their rows [lo, hi) of it, first block
+  __shared__ int n_members, n_arrived;
+  __shared__ int m_lo[kRows], m_hi[kRows], m_first[kRows];
+  __shared__ Member m_of[kRows];
+
+  const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
+  const int set = warp / WR, wr = warp % WR;
+  const int g = lane / 4, c = lane % 4;
+  const int G = p.h.page_tokens, H = p.h.n_heads, shift = __ffs(G) - 1;   // G: a power of two
+  const unsigned group = p.group;
+  unsigned char* ring = smem + set * kStages * Sh::kBytes;
+  const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+  pdl_wait();
+  pdl_trigger();
+  const Cut from = p.cuts[blockIdx.x];
+  const int end = p.cuts[blockIdx.x + 1].unit;
+  Cuts cuts;
+  cuts.total = from.units;
+  cuts.ctas = from.ctas;
+  cuts.each = cuts.ctas > 0 ? static_cast<unsigned>(cuts.total) / static_cast<unsigned>(cuts.ctas) : 0;
+  cuts.extra = cuts.total - cuts.each * cuts.ctas;
+  int place = from.place;
+  Tile s = from.tile;
+  int chunks = chunks_of(s, kSets);
+  bool fresh = true;                              // a tile whose requests are not known yet
+
+  for (int u = from.unit; u < end;) {
+    if (u >= s.first + chunks * H) {
+      s = p.tiles[++place];
+      chunks = chunks_of(s, kSets);
+      fresh = true;
+    }
+    const int head = static_cast<unsigned>(u - s.first) / static_cast<unsigned>(chunks);
+    const int seg0 = s.first + head * chunks, seg1 = seg0 + chunks;
+    const int chunk0 = u - seg0, chunk1 = min(end, seg1) - seg0;
+    const int rows = s.rows;
+    u = seg0 + chunk1;
+
+    // ---- the tile's requests; at the same time the queries and the first shared pages.
+    // Everything below is a chain of loads, so what does not hang together starts together
+    Member mine{};
+    if (fresh && warp == 0 && s.member0 + lane <= s.member1) mine = p.members[s.member0 + lane];
+    float x[MT][2][KW][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int r2 = 0; r2 < 2; ++r2) {
+        const int r = (wr * MT + mt) * kTile + (SPLIT ? g : g + 8 * r2);
+        const bool in = r < rows;
+        const int row = s.row0 + min(r, rows - 1);
+        const int query = group == 1 ? row : static_cast<unsigned>(row) / group;
+        const int64_t q_at = (s.q0 + static_cast<int64_t>(query)) * p.a.ld_q +
+                             (head * p.group + row - query * p.group) * p.a.ld_q_head;
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+          if (in && !(SPLIT && r2)) {
+            load_four<DT>(x[mt][r2][w], p.a.q, q_at + key_element<D>(c, w), p.vec_q);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[mt][r2][w][e] = 0.f;
+          }
+        }
+      }
+
+    // ---- blocks of this set of warps: n0, n0 + kSets, ...; lane l knows block l of
+    // the 32 at hand (info) and of the 32 after them (ahead)
+    const int n0 = chunk0 * kSets + set, n1 = min(chunk1 * kSets, s.blocks);
+    const int count = n0 < n1 ? (n1 - n0 + kSets - 1) / kSets : 0;
+    struct Info {
+      int page;                                   // -1: nothing to read
+      int t0, member;                             // first event; whose own, or -1: shared
+      float ks, vs;
+    };
+    auto open = [&](Info& x, int slot) {
+      x.page = p.h.table[static_cast<int64_t>(slot) * p.h.max_pages + (x.t0 >> shift)];
+      if (x.page < 0 || x.page >= p.h.n_pages) {
+        // trimmed, or a broken table: events that some row needs
+        x.page = -1;
+        flag(p.h.err, DLRM_ERRBIT_INDEX_OOB);
+      } else {
+        const int64_t where = static_cast<int64_t>(x.page) * H + head;
+        x.ks = p.h.k_scales[where];
+        x.vs = p.h.v_scales[where];
+      }
+    };
+    auto look_shared = [&](int i) {
+      Info x{-1, 0, -1, 0.f, 0.f};
+      const int n = n0 + i * kSets;
+      if (i < count && n < s.shared_blocks) {
+        x.t0 = (n < s.shared_sinks ? n : n - s.shared_sinks + s.shared0) * kBlock;
+        open(x, s.slot);
+      }
+      return x;
+    };
+    auto look_own = [&](int i, Info& x) {
+      const int n = n0 + i * kSets;
+      if (i < count && n >= s.shared_blocks) {
+        int k = 0;                                // the last request whose blocks begin at or before it
+        for (int d = n_members; d > 1;) {
+          const int half = d / 2;
+          if (m_first[k + half] <= n) k += half;
+          d -= half;
+        }
+        const Member& m = m_of[k];
+        const int j = n - m_first[k];
+        x.member = k;
+        x.t0 = (j < m.sinks ? s.own0 + j : j - m.sinks + m.block0) * kBlock;
+        open(x, m.slot);
+      }
+    };
+    Info info = look_shared(lane), ahead = look_shared(kWarp + lane);
+    if (fresh) {
+      __syncthreads();                            // the tile before is done with
+      if (warp == 0) {
+        int n = 0, first = s.shared_blocks;
+        for (int b0 = s.member0; b0 <= s.member1; b0 += kWarp) {
+          if (b0 > s.member0) {
+            mine = Member{};
+            if (b0 + lane <= s.member1) mine = p.members[b0 + lane];
+          }
+          const bool in = mine.rows > 0;
+          const unsigned who = __ballot_sync(0xffffffffu, in);
+          const int blocks = blocks_of(mine);
+          int inc = blocks;
+#pragma unroll
+          for (int d = 1; d < kWarp; d *= 2) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += y;
+          }
+          const int i = n + __popc(who & ((1u << lane) - 1));
+          if (in && i < kRows) {                  // (each has a row of the tile)
+            m_lo[i] = max(mine.row0 - s.row0, 0);
+            m_hi[i] = min(mine.row0 + mine.rows - s.row0, s.rows);
+            m_first[i] = first + inc - blocks;
+            m_of[i] = mine;
+          }
+          n += __popc(who);
+          first += __shfl_sync(0xffffffffu, inc, kWarp - 1);
+        }
+        if (lane == 0) n_members = min(n, kRows);
+      }
+      __syncthreads();
+    }
+    look_own(lane, info);
+    look_own(kWarp + lane, ahead);
+    int base = 0;                                 // blocks [base, base + 32) are in info
+    auto fetch = [&](int i) {
+      if (i < count) {
+        const bool here = i - base < kWarp;
+        const int page = __shfl_sync(0xffffffffu, here ? info.page : ahead.page, i % kWarp);
+        const int t0 = __shfl_sync(0xffffffffu, here ? info.t0 : ahead.t0, i % kWarp);
+        if (page >= 0) {
+          const int64_t codes = ((static_cast<int64_t>(page) * H + head) * G + (t0 & (G - 1))) * D;
+          const uint32_t dst = ring_at + (i % kStages) * Sh::kBytes;
+          constexpr int kSide = 2 * D;            // 16-byte chunks of a side
+#pragma unroll
+          for (int x = 0; x < 2 * kSide / (kWarp * WR); ++x) {
+            const int both = (x * WR + wr) * kWarp + lane;   // (a warp's chunks lie on one side)
+            const int id = both % kSide, t = id / (D / 16), ch = id % (D / 16);
+            if (both < kSide)
+              copy16(dst + key_offset<D>(t, ch), p.h.k_codes + codes + id * 16);
+            else
+              copy16(dst + kBlock * D + value_offset<D>(t, ch), p.h.v_codes + codes + id * 16);
+          }
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto set_barrier = [&] {
+      if (WR == 1)
+        __syncwarp();
+      else if (WR == kWarps)
+        __syncthreads();
+      else if (set == 0)
+        asm volatile("bar.sync 1, %0;" ::"n"(WR * kWarp) : "memory");
+      else
+        asm volatile("bar.sync 2, %0;" ::"n"(WR * kWarp) : "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch(i);
+
+    // ---- what each row sees (rows past the last stand for it)
+    if (fresh) {
+      for (int r = threadIdx.x; r < kRows; r += kThreads) {
+        const int row = min(r, rows - 1), of = s.row0 + row;
+        int i = 0;                                // the last request that begins at or before it
+        for (int d = n_members; d > 1;) {
+          const int half = d / 2;
+          if (m_lo[i + half] <= row) i += half;
+          d -= half;
+        }
+        const Member& m = m_of[i];
+        const int query = static_cast<unsigned>(of - m.row0) / group;
+        const Visible v = visible(p.a.causal ? m.len - m.queries + query : m.len - 1, m.len, p.a.window, p.a.sinks);
+        see_end[r] = v.end;
+        see_gap0[r] = v.gap0;
+        see_gap1[r] = v.gap1;
+        row_member[r] = i;
+        const int at = static_cast<unsigned>(of) / group;
+        row_at[r] = s.q0 + static_cast<int64_t>(at);
+        row_head[r] = of - at * p.group;
+      }
+      __syncthreads();
+      fresh = false;
+    }
+
+    // ---- fragments of the queries, scaled to f16; a negative softmax scale is
+    // theirs, so that the factors of the scores are positive
+    uint32_t qa[MT][KW][4];
+    float qf[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int r2 = 0; r2 < kR2; ++r2) {
+        float big = 0.f;
+#pragma unroll
+        for (int w = 0; w < KW; ++w)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) big = fmaxf(big, fabsf(x[mt][r2][w][e]));
+        big = quad_max(big);
+        const int ex = max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -100);
+        const float f = copysignf(pow2f(min(8 - ex, 127)), p.a.scale);
+        qf[mt][r2] = pow2f(max(ex - 8, -126)) * fabsf(p.a.scale) * kLog2e;
+#pragma unroll
+        for (int w = 0; w < KW; ++w)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[mt][r2][w][e] *= f;
+      }
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        const float (&x0)[4] = x[mt][0][w], (&x1)[4] = x[mt][1][w];
+        qa[mt][w][0] = pack_f16x2(x0[0], x0[1]);
+        qa[mt][w][2] = pack_f16x2(x0[2], x0[3]);
+        if (SPLIT) {
+          const float2 h0 = f16x2_to_float2(qa[mt][w][0]), h1 = f16x2_to_float2(qa[mt][w][2]);
+          qa[mt][w][1] = pack_f16x2((x0[0] - h0.x) * 2048.f, (x0[1] - h0.y) * 2048.f);
+          qa[mt][w][3] = pack_f16x2((x0[2] - h1.x) * 2048.f, (x0[3] - h1.y) * 2048.f);
+        } else {
+          qa[mt][w][1] = pack_f16x2(x1[0], x1[1]);
+          qa[mt][w][3] = pack_f16x2(x1[2], x1[3]);
+        }
+      }
+    }
+
+    // ---- events
+    float2 o[MT][NT][kPairsO];
+    float top[MT][2], sum[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      top[mt][0] = top[mt][1] = -INFINITY;
+      sum[mt][0] = sum[mt][1] = 0.f;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < kPairsO; ++i) o[mt][nt][i] = make_float2(0.f, 0.f);
+    }
+    for (int it = 0; it < count; ++it) {
+      if (it - base == kWarp) {
+        base += kWarp;
+        info = ahead;
+        ahead = look_shared(base + kWarp + lane);
+        look_own(base + kWarp + lane, ahead);
+      }
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+      set_barrier();                              // block `it` is there, and block it - 1 done with
+      fetch(it + kStages - 1);
+      const int page = __shfl_sync(0xffffffffu, info.page, it % kWarp);
+      const int member = __shfl_sync(0xffffffffu, info.member, it % kWarp);
+      if (page < 0) continue;
+      // rows of the tile that the block is for
+      const int lo = member < 0 ? 0 : m_lo[member], hi = member < 0 ? kRows : m_hi[member];
+      if (hi <= wr * MT * kTile || lo >= (wr + 1) * MT * kTile || rows <= wr * MT * kTile) continue;
+      const float ks = __shfl_sync(0xffffffffu, info.ks, it % kWarp);
+      const float vs = __shfl_sync(0xffffffffu, info.vs, it % kWarp);
+      const int t0 = __shfl_sync(0xffffffffu, info.t0, it % kWarp);
+      const unsigned char* kb = ring + (it % kStages) * Sh::kBytes;
+      const unsigned char* vb = kb + kBlock * D;
+      bool takes[MT];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+        takes[mt] = MT == 1 || (hi > (wr * MT + mt) * kTile && lo < (wr * MT + mt + 1) * kTile);
+
+      // S = Q K^T
+      float sc[MT][kBlock / 8][4];
+#pragma unroll
+      for (int j = 0; j < kBlock / 8; ++j) {
+        uint32_t kw[KW];
+        if (D == 32) {
+          const uint2 y = *reinterpret_cast<const uint2*>(kb + (8 * j + g) * 32 + 8 * c);
+          kw[0] = y.x;
+          kw[1] = y.y;
+        } else {
+#pragma unroll
+          for (int i = 0; i < KW / 4; ++i) {
+            const uint4 y = *reinterpret_cast<const uint4*>(kb + key_offset<D>(8 * j + g, 4 * i + c));
+            kw[4 * i] = y.x;
+            kw[4 * i + 1] = y.y;
+            kw[4 * i + 2] = y.z;
+            kw[4 * i + 3] = y.w;
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+          const uint32_t b0 = e4m3x2_lo_to_f16x2(kw[w]), b1 = e4m3x2_hi_to_f16x2(kw[w]);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) mma_f16_from(sc[mt][j], qa[mt][w], b0, b1, w > 0);
+        }
+      }
+      // weights: exp2 of the scores times the factors, less the running maximum
+      uint32_t pa[MT][kBlock / 16][4], pr[kRest ? MT : 1][kBlock / 16][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        if (!takes[mt]) continue;
+        const int r0 = (wr * MT + mt) * kTile + g;
+        if (SPLIT) {
+#pragma unroll
+          for (int j = 0; j < kBlock / 8; ++j) {
+            sc[mt][j][0] = fmaf(sc[mt][j][2], 1.f / 2048.f, sc[mt][j][0]);
+            sc[mt][j][1] = fmaf(sc[mt][j][3], 1.f / 2048.f, sc[mt][j][1]);
+          }
+        }
+        float alpha[2] = {1.f, 1.f};
+#pragma unroll
+        for (int r2 = 0; r2 < kR2; ++r2) {
+          const int r = r0 + 8 * r2;
+          const Visible v{see_end[r], see_gap0[r], see_gap1[r]};
+          const int row = min(r, rows - 1);
+          const bool ours = row >= lo && row < hi;
+          if (!(ours && t0 + kBlock <= v.end && (t0 >= v.gap1 || t0 + kBlock <= v.gap0))) {
+#pragma unroll
+            for (int j = 0; j < kBlock / 8; ++j) {
+              const int t = t0 + 8 * j + 2 * c;
+              if (!ours || !sees(v, t)) sc[mt][j][2 * r2] = -INFINITY;
+              if (!ours || !sees(v, t + 1)) sc[mt][j][2 * r2 + 1] = -INFINITY;
+            }
+          }
+          float big = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < kBlock / 8; ++j)
+            big = fmaxf(big, fmaxf(sc[mt][j][2 * r2], sc[mt][j][2 * r2 + 1]));
+          // (the factor is not zero, even for a softmax scale of zero: a masked score is -infinity)
+          const float f = fmaxf(qf[mt][r2] * ks, 1e-37f);
+          const float m = fmaxf(top[mt][r2], ceilf(quad_max(big) * f));
+          const float ref = m == -INFINITY ? 0.f : m, off = kLift - ref;
+          alpha[r2] = exp2_approx(top[mt][r2] - ref);
+          top[mt][r2] = m;
+          float2 add = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int j = 0; j < kBlock / 8; ++j) {
+            const float2 e = fma2(make_float2(sc[mt][j][2 * r2], sc[mt][j][2 * r2 + 1]), make_float2(f, f),
+                                  make_float2(off, off));
+            sc[mt][j][2 * r2] = exp2_approx(e.x);
+            sc[mt][j][2 * r2 + 1] = exp2_approx(e.y);
+            add = fma2(make_float2(sc[mt][j][2 * r2], sc[mt][j][2 * r2 + 1]), make_float2(1.f, 1.f), add);
+          }
+          sum[mt][r2] = fmaf(sum[mt][r2], alpha[r2], add.x + add.y);
+        }
+        // the output's correction, where the maximum of some row grew
+        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < kPairsO; ++i) {
+              o[mt][nt][i].x *= alpha[i];
+              o[mt][nt][i].y *= alpha[i];
+            }
+        }
+#pragma unroll
+        for (int kt = 0; kt < kBlock / 16; ++kt) {
+          const float (&s0)[4] = sc[mt][2 * kt], (&s1)[4] = sc[mt][2 * kt + 1];
+          uint32_t (&a)[4] = pa[mt][kt];
+          a[0] = pack_f16x2(s0[0], s0[1]);
+          a[2] = pack_f16x2(s1[0], s1[1]);
+          if (SPLIT) {
+            const float2 h0 = f16x2_to_float2(a[0]), h1 = f16x2_to_float2(a[2]);
+            a[1] = pack_f16x2((s0[0] - h0.x) * 2048.f, (s0[1] - h0.y) * 2048.f);
+            a[3] = pack_f16x2((s1[0] - h1.x) * 2048.f, (s1[1] - h1.y) * 2048.f);
+          } else {
+            a[1] = pack_f16x2(s0[2], s0[3]);
+            a[3] = pack_f16x2(s1[2], s1[3]);
+          }
+          if (kRest) {
+            uint32_t (&b)[4] = pr[kRest ? mt : 0][kt];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 h = f16x2_to_float2(a[i]);
+              const float (&y)[4] = i < 2 ? s0 : s1;
+              b[i] = pack_f16x2((y[2 * (i & 1)] - h.x) * 2048.f, (y[2 * (i & 1) + 1] - h.y) * 2048.f);
+            }
+          }
+        }
+      }
+      // O += vs P V
+      uint32_t vw[kBlock / 16][4][VW];
+#pragma unroll
+      for (int kt = 0; kt < kBlock / 16; ++kt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = 16 * kt + 2 * c + (i & 1) + 8 * (i >> 1);
+          if (D == 128) {
+            const uint4 y = *reinterpret_cast<const uint4*>(vb + value_offset<D>(t, g));
+            vw[kt][i][0] = y.x;
+            vw[kt][i][VW > 1 ? 1 : 0] = y.y;
+            vw[kt][i][VW > 2 ? 2 : 0] = y.z;
+            vw[kt][i][VW > 3 ? 3 : 0] = y.w;
+          } else if (D == 64) {
+            const uint2 y = *reinterpret_cast<const uint2*>(vb + value_offset<D>(t, g >> 1) + 8 * (g & 1));
+            vw[kt][i][0] = y.x;
+            vw[kt][i][VW > 1 ? 1 : 0] = y.y;
+          } else {
+            vw[kt][i][0] = *reinterpret_cast<const uint32_t*>(vb + value_offset<D>(t, g >> 2) + 4 * (g & 3));
+          }
+        }
+      if (member >= 0 && t0 + kBlock > m_of[member].len) {
+        // codes of events past the end are whatever an earlier history left there
+        const int len = m_of[member].len;
+#pragma unroll
+        for (int kt = 0; kt < kBlock / 16; ++kt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (t0 + 16 * kt + 2 * c + (i & 1) + 8 * (i >> 1) >= len)
+#pragma unroll
+              for (int w = 0; w < VW; ++w) vw[kt][i][w] = 0;
+      }
+      const float2 vs2 = make_float2(vs, vs), less = make_float2(1.f / 2048.f, 1.f / 2048.f);
+#pragma unroll
+      for (int w = 0; w < VW; ++w) {
+        // bytes of a pair of events side by side: n tiles 4w, 4w+1 and 4w+2, 4w+3
+        uint32_t b[kBlock / 16][4][2];
+#pragma unroll
+        for (int kt = 0; kt < kBlock / 16; ++kt) {
+          const uint32_t l0 = __byte_perm(vw[kt][0][w], vw[kt][1][w], 0x5140);
+          const uint32_t l1 = __byte_perm(vw[kt][0][w], vw[kt][1][w], 0x7362);
+          const uint32_t h0 = __byte_perm(vw[kt][2][w], vw[kt][3][w], 0x5140);
+          const uint32_t h1 = __byte_perm(vw[kt][2][w], vw[kt][3][w], 0x7362);
+          b[kt][0][0] = e4m3x2_lo_to_f16x2(l0), b[kt][0][1] = e4m3x2_lo_to_f16x2(h0);
+          b[kt][1][0] = e4m3x2_hi_to_f16x2(l0), b[kt][1][1] = e4m3x2_hi_to_f16x2(h0);
+          b[kt][2][0] = e4m3x2_lo_to_f16x2(l1), b[kt][2][1] = e4m3x2_lo_to_f16x2(h1);
+          b[kt][3][0] = e4m3x2_hi_to_f16x2(l1), b[kt][3][1] = e4m3x2_hi_to_f16x2(h1);
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          if (!takes[mt]) continue;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float acc[4];
+#pragma unroll
+            for (int kt = 0; kt < kBlock / 16; ++kt) mma_f16_from(acc, pa[mt][kt], b[kt][i][0], b[kt][i][1], kt > 0);
+            float2* out = o[mt][4 * w + i];
+            float2 lo2 = make_float2(acc[0], acc[1]);
+            const float2 hi2 = make_float2(acc[2], acc[3]);
+            if (SPLIT) {
+              lo2 = fma2(hi2, less, lo2);
+              out[0] = fma2(vs2, lo2, out[0]);
+            } else {
+              float2 hi3 = hi2;
+              if (kRest) {
+                float rest[4];
+#pragma unroll
+                for (int kt = 0; kt < kBlock / 16; ++kt)
+                  mma_f16_from(rest, pr[kRest ? mt : 0][kt], b[kt][i][0], b[kt][i][1], kt > 0);
+                lo2 = fma2(make_float2(rest[0], rest[1]), less, lo2);
+                hi3 = fma2(make_float2(rest[2], rest[3]), less, hi3);
+              }
+              out[0] = fma2(vs2, lo2, out[0]);
+              out[kPairsO - 1] = fma2(vs2, hi3, out[kPairsO - 1]);
+            }
+          }
+        }
+      }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+
+    // ---- join the sets of warps
+    __syncthreads();                              // every ring is done with: `joined` lies there
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int r2 = 0; r2 < kR2; ++r2) {
+        const int r = (wr * MT + mt) * kTile + g + 8 * r2;
+        const float l = quad_sum(sum[mt][r2]);
+        float* out = joined[set][r];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          out[2 * c * (D / 8) + nt] = o[mt][nt][r2].x;
+          out[(2 * c + 1) * (D / 8) + nt] = o[mt][nt][r2].y;
+        }
+        if (c == 0) {
+          tops[set][r] = top[mt][r2];
+          totals[set][r] = l;
+        }
+      }
+    __syncthreads();
+    for (int r = threadIdx.x; r < kRows; r += kThreads) {
+      float m = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kSets; ++w) m = fmaxf(m, tops[w][r]);
+      const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int w = 0; w < kSets; ++w) {
+        const float f = exp2_approx(tops[w][r] - ref);
+        l = fmaf(f, totals[w][r], l);
+        tops[w][r] = f;
+      }
+      row_top[r] = m;
+      row_total[r] = l;
+    }
+    if (threadIdx.x == 0) odd[kRows] = 0;
+    __syncthreads();
+    const bool split = chunk0 > 0 || chunk1 < chunks;
+    float* mine_at = p.partials + (static_cast<int64_t>(blockIdx.x) * 2 + (chunk0 > 0 ? 0 : 1)) * kPartial;
+    auto sums_of = [&](int r, int d) {            // four sums of a row, over the sets
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kSets; ++w) {
+        const float f = tops[w][r];
+        const float4 z = *reinterpret_cast<const float4*>(&joined[w][r][d]);
+        y.x = fmaf(f, z.x, y.x), y.y = fmaf(f, z.y, y.y), y.z = fmaf(f, z.z, y.z), y.w = fmaf(f, z.w, y.w);
+      }
+      return y;
+    };
+    // outputs, and which rows need a closer look
+    auto finish = [&](int r, int d, const float4& y) {
+      const float l = row_total[r];
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float z[4] = {y.x * inv, y.y * inv, y.z * inv, y.w * inv};
+      const int hq = head * p.group + row_head[r];
+      const int64_t at = row_at[r] * p.a.ld_out + hq * p.a.ld_out_head + d;
+      bool fine = l != 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        store_element<DT>(p.a.out, at + e, l == 0.f ? 0.f : z[e]);
+        fine &= finite(z[e]);
+      }
+      if (d == 0) {
+        if (p.a.lse)
+          p.a.lse[row_at[r] * p.a.n_heads + hq] = l == 0.f ? -INFINITY : row_top[r] * kLn2 + logf(l * pow2f(-kLift));
+      }
+      if (!fine) odd[r] = odd[kRows] = l == 0.f ? 2 : 1;   // 2: sees nothing, or has no weights
+    };
+    for (int r = threadIdx.x; r < kRows; r += kThreads) odd[r] = 0;
+    constexpr int kQuads = (kRows * D / 4 + kThreads - 1) / kThreads;
+    if (!split) {
+      __syncthreads();
+#pragma unroll 4
+      for (int e = 0; e < kQuads; ++e) {
+        const int of = 4 * (e * kThreads + threadIdx.x), r = of / D, d = of % D;
+        if (r < rows) finish(r, d, sums_of(r, d));
+      }
+    } else {
+#pragma unroll 4
+      for (int e = 0; e < kQuads; ++e) {
+        const int of = 4 * (e * kThreads + threadIdx.x), r = of / D, d = of % D;
+        if (r < rows) *reinterpret_cast<float4*>(mine_at + of) = sums_of(r, d);
+      }
+      for (int r = threadIdx.x; r < rows; r += kThreads) {
+        mine_at[kRows * D + r] = row_top[r];
+        mine_at[kRows * D + kRows + r] = row_total[r];
+      }
+      // the CTAs that share this piece: first .. last, one part each. (A cut moves
+      // out of short pieces only, so a split one's cuts are where they were.)
+      const int64_t first = cuts.owner(seg0);
+      const int parts = cuts.owner(seg1 - 1) - static_cast<int>(first) + 1;
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        const int before = atomicAdd(&p.counters[first], 1);
+        n_arrived = before;
+        if (before == parts - 1) p.counters[first] = 0;
+      }
+      __syncthreads();
+      if (n_arrived != parts - 1) continue;       // (`joined` was read before the barrier)
+      __threadfence();
+      auto part = [&](int i) { return p.partials + ((first + i) * 2 + (i > 0 ? 0 : 1)) * kPartial; };
+      // maximum of each row over the parts, the parts' weights, then the weighted sums
+      float big = -INFINITY, l = 0.f;             // of row threadIdx.x
+      static_assert(kRows <= kThreads, "a thread a row");
+      for (int p0 = 0; p0 < parts; p0 += kWeights) {
+        const int n = min(kWeights, parts - p0);
+        for (int e = threadIdx.x; e < n * kRows; e += kThreads)
+          weight[e / kRows][e % kRows] = e % kRows < rows ? __ldcg(part(p0 + e / kRows) + kRows * D + e % kRows) : -INFINITY;
+        __syncthreads();
+        if (threadIdx.x < kRows)
+          for (int i = 0; i < n; ++i) big = fmaxf(big, weight[i][threadIdx.x]);
+        if (p0 + n < parts) __syncthreads();
+      }
+      if (threadIdx.x < kRows) row_top[threadIdx.x] = big;
+      float4 acc[kQuads];
+#pragma unroll
+      for (int e = 0; e < kQuads; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int p0 = 0; p0 < parts; p0 += kWeights) {
+        const int n = min(kWeights, parts - p0);
+        __syncthreads();
+        for (int e = threadIdx.x; e < n * kRows; e += kThreads) {
+          const int i = e / kRows, r = e % kRows;
+          const float m = row_top[r];
+          const float t = parts > kWeights ? r < rows ? __ldcg(part(p0 + i) + kRows * D + r) : -INFINITY : weight[i][r];
+          weight[i][r] = m == -INFINITY ? 0.f : exp2_approx(t - m);
+        }
+        __syncthreads();
+        if (threadIdx.x < rows)
+          for (int i = 0; i < n; ++i)
+            l = fmaf(weight[i][threadIdx.x], __ldcg(part(p0 + i) + kRows * D + kRows + threadIdx.x), l);
+#pragma unroll 2
+        for (int i = 0; i < n; ++i) {
+          const float* q = part(p0 + i);
+#pragma unroll
+          for (int e = 0; e < kQuads; ++e) {
+            const int of = 4 * (e * kThreads + threadIdx.x), r = of / D;
+            if (r >= rows) continue;
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(q + of));
+            const float f = weight[i][r];
+            acc[e].x = fmaf(f, y.x, acc[e].x), acc[e].y = fmaf(f, y.y, acc[e].y);
+            acc[e].z = fmaf(f, y.z, acc[e].z), acc[e].w = fmaf(f, y.w, acc[e].w);
+          }
+        }
+      }
+      if (threadIdx.x < rows) row_total[threadIdx.x] = l;
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < kQuads; ++e) {
+        const int of = 4 * (e * kThreads + threadIdx.x), r = of / D, d = of % D;
+        if (r < rows) finish(r, d, acc[e]);
+      }
+    }
+    __syncthreads();
+    if (odd[kRows]) {
+      for (int r = 0; r < rows; ++r) {
+        const int hq = head * p.group + row_head[r];
+        const Visible v{see_end[r], see_gap0[r], see_gap1[r]};
+        if (odd[r] == 1 || (odd[r] == 2 && sees_any(v)))
+          careful_row<DT>(p.h, p.a, m_of[row_member[r]].slot, v, head, row_at[r] * p.a.ld_q + hq * p.a.ld_q_head,
+                          row_at[r] * p.a.ld_out + hq * p.a.ld_out_head, row_at[r] * p.a.n_heads + hq,
+                          &joined[0][0][0]);
+      }
+    }
+    __syncthreads();                              // `joined` is read: the rings may be filled
+  }
+}
+
+template <int D, int DT, bool SPLIT, int MT, int WR>
+cudaError_t launch(Params& p, cudaStream_t stream) {
+  using Sh = Shape<D, DT, SPLIT, MT, WR>;
+  // set once on every device, by a bit each; the CTAs of an SM are the same on every GB300
+  static std::atomic<uint64_t> done{0};
+  static std::atomic<int> resident{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
+  int per_sm = 0;
+  if (!bit || !(done.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(prefix_attention_kernel<D, DT, SPLIT, MT, WR>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+    if (e != cudaSuccess) return e;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, prefix_attention_kernel<D, DT, SPLIT, MT, WR>,
+                                                      kThreads, Sh::kSmem);
+    if (e != cudaSuccess) return e;
+    per_sm = std::max(1, per_sm);
+    resident.store(per_sm, std::memory_order_relaxed);
+    done.fetch_or(bit, std::memory_order_acq_rel);
+  } else {
+    per_sm = resident.load(std::memory_order_relaxed);
+  }
+  // no more CTAs than counters, than partial results have space, and than pieces of
+  // kLeastBlocks there can be
+  const int64_t events = static_cast<int64_t>(p.h.max_pages) * p.h.page_tokens;
+  const int64_t tiles = p.a.q_rows * p.group / Sh::kRows + p.n_groups;
+  const int64_t blocks = (tiles * 2 + p.a.batch) * p.h.n_heads * (events / kBlock + 2);
+  p.rows = Sh::kRows;
+  p.split = Sh::kSets;
+  p.grid = static_cast<int>(std::min<int64_t>(
+      {std::max<int64_t>(blocks / kLeastBlocks, tiles * p.h.n_heads), static_cast<int64_t>(device_sm_count()) * per_sm,
+       int64_t(kAttnMaxCtas), kAttnPartialFloats / (2 * Sh::kPartial)}));
+  e = launch_plan(p, stream);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(prefix_attention_kernel<D, DT, SPLIT, MT, WR>, dim3(p.grid), dim3(kThreads), Sh::kSmem, stream, p);
+}
+
+template <int D, int DT>
+cudaError_t launch_rows(Params& p, cudaStream_t stream) {
+  // by the rows of a group and kv head, on average; at head_dim 128 a warp has registers
+  // for one row tile
+  constexpr bool kSplit = DT == DLRM_DTYPE_FP32;
+  constexpr int kTile = kSplit ? 8 : 16, MT = D == 128 ? 1 : 2;
+  const int64_t rows = (p.a.q_rows * p.group + p.n_groups - 1) / p.n_groups;
+  if (rows <= 8) return launch<D, DT, true, 1, 1>(p, stream);
+  if constexpr (!kSplit) {
+    if (rows <= kTile) return launch<D, DT, kSplit, 1, 1>(p, stream);
+  }
+  if (MT > 1 && rows <= kTile * MT) return launch<D, DT, kSplit, MT, 1>(p, stream);
+  if constexpr (MT == 1) {
+    if (rows > 2 * kTile) return launch<D, DT, kSplit, MT, 4>(p, stream);
+  }
+  return launch<D, DT, kSplit, MT, 2>(p, stream);
+}
+
+template <int D>
+cudaError_t launch_d(Params& p, cudaStream_t stream) {
+  if (p.a.dtype == DLRM_DTYPE_FP32) return launch_rows<D, DLRM_DTYPE_FP32>(p, stream);
+  if (p.a.dtype == DLRM_DTYPE_BF16) return launch_rows<D, DLRM_DTYPE_BF16>(p, stream);
+  return launch_rows<D, DLRM_DTYPE_FP16>(p, stream);
+}
+
+}  // namespace prefix
+}  // namespace dlrm
