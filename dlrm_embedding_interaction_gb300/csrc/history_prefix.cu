@@ -20,7 +20,8 @@ namespace prefix {
 
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 256;
+constexpr int kHere = 256;                       // requests of a group that shared memory holds
 
 // Exclusive prefix sum over the CTA; total in every thread.
 __device__ __forceinline__ int scan(int x, int* sums, int& total) {
@@ -35,7 +36,7 @@ __device__ __forceinline__ int scan(int x, int* sums, int& total) {
   if (lane == kWarp - 1) sums[warp] = inc;
   __syncthreads();
   if (warp == 0) {
-    const int s = sums[lane];
+    const int s = lane < kPlanThreads / kWarp ? sums[lane] : 0;
     int si = s;
 #pragma unroll
     for (int d = 1; d < kWarp; d *= 2) {
@@ -50,11 +51,15 @@ __device__ __forceinline__ int scan(int x, int* sums, int& total) {
   return sums[warp] + inc - x;
 }
 
+// What bounds it: a chain of loads, each of which waits for the one before: groups, starts
+// and slots, lengths, tables; then, in the last CTA, the tiles. What belongs to a group
+// stays in shared memory in between, for up to kHere requests.
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_constant__ Params p) {
   __shared__ int sums[kWarp + 1];
   __shared__ int ref_s, len_s, gap_s, shared_s, last_s;
+  __shared__ Member here[kHere];
   const dlrm_history_t& h = p.h;
-  const int G = h.page_tokens, M = h.max_pages, t = threadIdx.x, lane = t % kWarp;
+  const int G = h.page_tokens, M = h.max_pages, t = threadIdx.x, lane = t % kWarp, g = blockIdx.x;
   const int32_t* starts = p.a.q_starts;
   if (t == 0) {
     ref_s = INT32_MAX;
@@ -63,61 +68,65 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
   }
   pdl_wait();
   pdl_trigger();
+  const int b0 = p.groups[g], b1 = p.groups[g + 1], first_b = p.groups[0], last_b = p.groups[p.n_groups];
   // starts or groups that decrease or leave their range: nothing is done
   bool bad = false;
-  for (int i = t; i <= p.a.batch; i += kPlanThreads) {
-    const int x = starts[i];
-    bad |= x < 0 || x > p.a.q_rows || (i < p.a.batch && starts[i + 1] < x);
-  }
   for (int i = t; i <= p.n_groups; i += kPlanThreads) {
     const int x = p.groups[i];
     bad |= x < 0 || x > p.a.batch || (i < p.n_groups && p.groups[i + 1] < x);
   }
+  for (int i = t; i <= p.a.batch; i += kPlanThreads) {
+    const int x = starts[i];
+    bad |= x < 0 || x > p.a.q_rows || (i < p.a.batch && starts[i + 1] < x);
+  }
   bad = __syncthreads_or(bad);
-  const int g = blockIdx.x;
-  auto tile_base = [&](int group) {              // at least a group's tiles apart
-    return static_cast<int>(static_cast<int64_t>(starts[p.groups[group]]) * p.group / p.rows) + group;
+  // tiles of a group have places of their own, at least as many as it needs
+  const auto place_of = [&](int start, int group) {
+    return static_cast<int>(static_cast<int64_t>(start) * p.group / p.rows) + group;
   };
+  int first_place = 0, last_place = 0;
   if (!bad) {
-    const int b0 = p.groups[g], b1 = p.groups[g + 1], q0 = starts[b0];
+    first_place = place_of(starts[first_b], 0);
+    last_place = place_of(starts[last_b], p.n_groups);
+    const int q0 = starts[b0], q1 = starts[b1];
     const int64_t cap = static_cast<int64_t>(M) * G;
+    Member* members = b1 - b0 <= kHere ? here : p.members + b0;   // of the group
     // ---- lengths; the events that every request with rows and events has
-    auto first_seen = [&](int len, int queries) {   // of its first row
-      return visible(p.a.causal ? len - queries : len - 1, len, p.a.window, p.a.sinks);
+    const auto first_seen = [&](const Member& m) {   // of its first row
+      return visible(p.a.causal ? m.len - m.queries : m.len - 1, m.len, p.a.window, p.a.sinks);
     };
     for (int b = b0 + t; b < b1; b += kPlanThreads) {
       Member m{};
       m.slot = p.a.slots[b];
-      m.queries = starts[b + 1] - starts[b];
-      m.row0 = (starts[b] - q0) * p.group;
+      const int s0 = starts[b];
+      m.queries = starts[b + 1] - s0;
+      m.row0 = (s0 - q0) * p.group;
       m.rows = m.queries * p.group;
       if (m.slot >= 0 && m.slot < h.n_slots) {
         m.len = static_cast<int>(min(static_cast<int64_t>(max(h.lengths[m.slot], 0)), cap));
       } else {
         flag(h.err, DLRM_ERRBIT_INDEX_OOB);
       }
-      p.members[b] = m;
+      members[b - b0] = m;
       if (m.rows > 0 && m.len > 0) {
-        atomicMin(&ref_s, b);
+        atomicMin(&ref_s, b - b0);
         atomicMin(&len_s, m.len);
-        atomicMin(&gap_s, first_seen(m.len, m.queries).gap1);
+        atomicMin(&gap_s, first_seen(m).gap1);
       }
     }
     __syncthreads();
-    const int ref = ref_s;
-    if (t == 0) shared_s = ref == INT32_MAX ? 0 : len_s / G;
+    const int ref = ref_s, pages = ref == INT32_MAX ? 0 : len_s / G;
+    if (t == 0) shared_s = pages;
     __syncthreads();
     // ---- shared pages: the first entry that differs, 8 x 32 entries of a request at a time
-    const int pages = shared_s;
-    int ref_slot = -1;
+    const int ref_slot = ref == INT32_MAX ? -1 : members[ref].slot;
     if (pages > 0) {
-      ref_slot = p.members[ref].slot;
       const int32_t* mine = h.table + static_cast<int64_t>(ref_slot) * M;
       const int pieces = (pages + 255) / 256;
       const int64_t work = static_cast<int64_t>(b1 - b0) * pieces;
       for (int64_t w = t / kWarp; w < work; w += kPlanThreads / kWarp) {
-        const int b = b0 + static_cast<int>(w / pieces), j0 = static_cast<int>(w % pieces) * 256 + lane;
-        const Member m = p.members[b];
+        const int b = static_cast<int>(w / pieces), j0 = static_cast<int>(w % pieces) * 256 + lane;
+        const Member& m = members[b];
         if (b == ref || m.rows == 0 || m.len == 0) continue;
         const int32_t* row = h.table + static_cast<int64_t>(m.slot) * M;
         int differ = INT32_MAX;
@@ -134,34 +143,36 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     const int shared = shared_s * G;             // events
     // ---- every request's blocks of its own, and how many lie before them
     int before = 0;
-    for (int c0 = b0; c0 < b1; c0 += kPlanThreads) {
+    for (int c0 = 0; c0 < b1 - b0; c0 += kPlanThreads) {
       const int b = c0 + t;
       int n = 0;
       Member m{};
-      if (b < b1) {
-        m = p.members[b];
+      if (b < b1 - b0) {
+        m = members[b];
         if (m.rows > 0 && m.len > 0) {
-          const Visible v = first_seen(m.len, m.queries);
-          const int end = (m.len + kBlock - 1) / kBlock, low = shared / kBlock;
+          const Visible v = first_seen(m);
+          const int low = shared / kBlock;
           m.block0 = max(v.gap1 / kBlock, low);
           m.sinks = v.gap1 > shared ? max((min(v.gap0, m.len) + kBlock - 1) / kBlock - low, 0) : 0;
           if (low + m.sinks >= m.block0) {       // no gap: blocks from `shared` on
             m.sinks = 0;
             m.block0 = low;
           }
-          n = m.sinks + max(end - m.block0, 0);
+          n = blocks_of(m);
         }
       }
       int total;
       m.first = before + scan(n, sums, total);
       before += total;
-      if (b < b1) p.members[b] = m;
+      if (b < b1 - b0) {
+        p.members[b0 + b] = m;
+        members[b] = m;
+      }
       __syncthreads();
     }
-    __syncthreads();
     // ---- tiles
-    const int rows = (starts[b1] - q0) * p.group, tiles = (rows + p.rows - 1) / p.rows;
-    const int base = tile_base(g), next = tile_base(g + 1);
+    const int rows = (q1 - q0) * p.group, tiles = (rows + p.rows - 1) / p.rows;
+    const int base = place_of(q0, g), next = place_of(q1, g + 1);
     const int gap1 = gap_s == INT32_MAX ? 0 : gap_s, gap0 = min(p.a.sinks, gap1);
     Tile x{};
     x.q0 = q0;
@@ -171,11 +182,11 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     x.shared_sinks = min((min(gap0, shared) + kBlock - 1) / kBlock, x.shared0);
     if (x.shared_sinks == x.shared0) x.shared_sinks = x.shared0 = 0;
     x.shared_blocks = x.shared_sinks + x.own0 - x.shared0;
-    auto holds = [&](int row) {                  // the request of a row
-      int lo = b0, hi = b1;                      // the last one that begins at or before it
+    const auto holds = [&](int row) {            // the request of a row
+      int lo = 0, hi = b1 - b0;                  // the last one that begins at or before it
       while (hi - lo > 1) {
         const int mid = lo + (hi - lo) / 2;
-        if ((starts[mid] - q0) * p.group <= row) lo = mid; else hi = mid;
+        if (members[mid].row0 <= row) lo = mid; else hi = mid;
       }
       return lo;
     };
@@ -186,8 +197,10 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
         y.rows = min(p.rows, rows - y.row0);
         y.member0 = holds(y.row0);
         y.member1 = holds(y.row0 + y.rows - 1);
-        const Member last = p.members[y.member1];
-        y.blocks = y.shared_blocks - p.members[y.member0].first + last.first + blocks_of(last);
+        const Member last = members[y.member1];
+        y.blocks = y.shared_blocks - members[y.member0].first + last.first + blocks_of(last);
+        y.member0 += b0;
+        y.member1 += b0;
       }
       p.found[base + i] = y;
     }
@@ -196,41 +209,42 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
   __threadfence();
   __syncthreads();
   if (t == 0) {
-    const unsigned before = atomicInc(reinterpret_cast<unsigned*>(p.arrived), gridDim.x - 1);
-    last_s = before == gridDim.x - 1;
+    const unsigned n = atomicInc(reinterpret_cast<unsigned*>(p.arrived), gridDim.x - 1);
+    last_s = n == gridDim.x - 1;
   }
   __syncthreads();
   if (!last_s) return;
   __threadfence();
   if (bad && t == 0) flag(h.err, DLRM_ERRBIT_OFFSETS);
-  const int t0 = bad ? 0 : tile_base(0), t1 = bad ? 0 : tile_base(p.n_groups);
-  int units = 0, dense = 0, pieces = 0;
-  const int per = (t1 - t0 + kPlanThreads - 1) / kPlanThreads;
-  const int mine0 = min(t1, t0 + t * per), mine1 = min(t1, mine0 + per);
-  for (int i = mine0; i < mine1; ++i) {
+  int units = 0, dense = 0;
+  const int per = (last_place - first_place + kPlanThreads - 1) / kPlanThreads;
+  const int mine0 = min(last_place, first_place + t * per), mine1 = min(last_place, mine0 + per);
+  const auto tile_at = [&](int i) {
     Tile y;
-    y.blocks = __ldcg(&p.found[i].blocks);
-    y.rows = __ldcg(&p.found[i].rows);
-    const int chunks = chunks_of(y, p.split);
+    const int4* from = reinterpret_cast<const int4*>(&p.found[i]);
+    int4* to = reinterpret_cast<int4*>(&y);
+#pragma unroll
+    for (int w = 0; w < static_cast<int>(sizeof(Tile) / 16); ++w) to[w] = __ldcg(from + w);
+    return y;
+  };
+  Tile only{};                                    // the thread's tile, if it is one
+  for (int i = mine0; i < mine1; ++i) {
+    only = tile_at(i);
+    const int chunks = chunks_of(only, p.split);
     units += chunks * h.n_heads;
     dense += chunks > 0;
   }
   int total, n_tiles;
   int at = scan(units, sums, total);
   int place = scan(dense, sums, n_tiles);
-  pieces = n_tiles * h.n_heads;
   Cuts cuts;
   cuts.total = total;
-  cuts.ctas = min(p.grid, min(total, max(total / max(kLeastBlocks / p.split, 1), pieces)));
+  cuts.ctas = min(p.grid, min(total, max(total / max(kLeastBlocks / p.split, 1), n_tiles * h.n_heads)));
   cuts.each = cuts.ctas > 0 ? total / cuts.ctas : 0;
   cuts.extra = total - cuts.each * cuts.ctas;
   const int whole = kWholeBlocks / p.split;
   for (int i = mine0; i < mine1; ++i) {
-    Tile y;
-    const int4* from = reinterpret_cast<const int4*>(&p.found[i]);
-    int4* to = reinterpret_cast<int4*>(&y);
-#pragma unroll
-    for (int w = 0; w < static_cast<int>(sizeof(Tile) / 16); ++w) to[w] = __ldcg(from + w);
+    Tile y = per == 1 ? only : tile_at(i);
     const int chunks = chunks_of(y, p.split);
     if (chunks == 0) continue;
     y.first = at;

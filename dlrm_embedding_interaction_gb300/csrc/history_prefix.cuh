@@ -91,11 +91,12 @@ struct Shape {
   static constexpr int kTile = SPLIT ? 8 : 16;    // rows of an MMA tile
   static constexpr int kRows = kTile * MT * WR;
   static constexpr int kSets = kWarps / WR;       // sets of warps, a ring and a block of each chunk each
-  static constexpr int kStages = WR == 1 ? (D == 128 ? 3 : 4) : D == 128 ? 4 : 6;
+  static constexpr int kPer = WR == 1 ? 1 : 2;    // blocks of a stage: warps that share a ring meet once a stage
+  static constexpr int kStages = WR > 1 || D == 128 ? 3 : 4;
   static constexpr int kBytes = 2 * kBlock * D;   // keys and values of a block
   static constexpr int kStride = D + 4;           // of a row's sums in shared memory
   static constexpr int kPartial = kRows * (D + 2);   // of a part in scratch: sums, maxima, sums of weights
-  static constexpr int kRing = kSets * kStages * kBytes;
+  static constexpr int kRing = kSets * kStages * kPer * kBytes;
   static constexpr int kJoin = (kSets * kRows * (kStride + 2) + kWeights * kRows) * 4;
   static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
 };
@@ -106,7 +107,7 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
   using Sh = Shape<D, DT, SPLIT, MT, WR>;
   constexpr bool kRest = !SPLIT && DT == DLRM_DTYPE_FP16;
   constexpr int kTile = Sh::kTile, kRows = Sh::kRows, kSets = Sh::kSets, kStages = Sh::kStages;
-  constexpr int kStride = Sh::kStride, kPartial = Sh::kPartial;
+  constexpr int kStride = Sh::kStride, kPartial = Sh::kPartial, kPer = Sh::kPer;
   constexpr int KW = D / 16;                      // key words of a thread and event tile
   constexpr int VW = D / 32;                      // value words of a thread and event
   constexpr int NT = D / 8;                       // n tiles of the output
@@ -125,6 +126,7 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
   __shared__ int row_head[kRows];                 // head of the group
   // requests with rows in the tile: their rows [lo, hi) of it, first block
   __shared__ int n_members, n_arrived;
+  __shared__ int clear_end, clear_gap;            // events that every row of the tile sees lie between
   __shared__ int m_lo[kRows], m_hi[kRows], m_first[kRows];
   __shared__ Member m_of[kRows];
 
@@ -133,7 +135,7 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
   const int g = lane / 4, c = lane % 4;
   const int G = p.h.page_tokens, H = p.h.n_heads, shift = __ffs(G) - 1;   // G: a power of two
   const unsigned group = p.group;
-  unsigned char* ring = smem + set * kStages * Sh::kBytes;
+  unsigned char* ring = smem + set * kStages * kPer * Sh::kBytes;
   const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
   pdl_wait();
   pdl_trigger();
@@ -192,18 +194,17 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
     const int n0 = chunk0 * kSets + set, n1 = min(chunk1 * kSets, s.blocks);
     const int count = n0 < n1 ? (n1 - n0 + kSets - 1) / kSets : 0;
     struct Info {
-      int page;                                   // -1: nothing to read
+      int64_t codes;                              // first byte of the block's codes; -1: nothing to read
       int t0, member;                             // first event; whose own, or -1: shared
       float ks, vs;
     };
     auto open = [&](Info& x, int slot) {
-      x.page = p.h.table[static_cast<int64_t>(slot) * p.h.max_pages + (x.t0 >> shift)];
-      if (x.page < 0 || x.page >= p.h.n_pages) {
-        // trimmed, or a broken table: events that some row needs
-        x.page = -1;
-        flag(p.h.err, DLRM_ERRBIT_INDEX_OOB);
+      const int page = p.h.table[static_cast<int64_t>(slot) * p.h.max_pages + (x.t0 >> shift)];
+      if (page < 0 || page >= p.h.n_pages) {
+        flag(p.h.err, DLRM_ERRBIT_INDEX_OOB);     // trimmed, or a broken table: events that some row needs
       } else {
-        const int64_t where = static_cast<int64_t>(x.page) * H + head;
+        const int64_t where = static_cast<int64_t>(page) * H + head;
+        x.codes = (where * G + (x.t0 & (G - 1))) * D;
         x.ks = p.h.k_scales[where];
         x.vs = p.h.v_scales[where];
       }
@@ -262,21 +263,23 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
           n += __popc(who);
           first += __shfl_sync(0xffffffffu, inc, kWarp - 1);
         }
-        if (lane == 0) n_members = min(n, kRows);
+        if (lane == 0) {
+          n_members = min(n, kRows);
+          clear_end = INT32_MAX;
+          clear_gap = 0;
+        }
       }
       __syncthreads();
     }
     look_own(lane, info);
     look_own(kWarp + lane, ahead);
     int base = 0;                                 // blocks [base, base + 32) are in info
-    auto fetch = [&](int i) {
+    auto fetch_block = [&](int i) {
       if (i < count) {
-        const bool here = i - base < kWarp;
-        const int page = __shfl_sync(0xffffffffu, here ? info.page : ahead.page, i % kWarp);
-        const int t0 = __shfl_sync(0xffffffffu, here ? info.t0 : ahead.t0, i % kWarp);
-        if (page >= 0) {
-          const int64_t codes = ((static_cast<int64_t>(page) * H + head) * G + (t0 & (G - 1))) * D;
-          const uint32_t dst = ring_at + (i % kStages) * Sh::kBytes;
+        const int64_t mine_codes = i - base < kWarp ? info.codes : ahead.codes;
+        const int64_t codes = __shfl_sync(0xffffffffu, mine_codes, i % kWarp);
+        if (codes >= 0) {
+          const uint32_t dst = ring_at + (i % (kStages * kPer)) * Sh::kBytes;
           constexpr int kSide = 2 * D;            // 16-byte chunks of a side
 #pragma unroll
           for (int x = 0; x < 2 * kSide / (kWarp * WR); ++x) {
@@ -289,6 +292,10 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
           }
         }
       }
+    };
+    auto fetch = [&](int i) {                     // a stage
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) fetch_block(i + j);
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     auto set_barrier = [&] {
@@ -302,7 +309,7 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
         asm volatile("bar.sync 2, %0;" ::"n"(WR * kWarp) : "memory");
     };
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) fetch(i);
+    for (int i = 0; i < kStages - 1; ++i) fetch(i * kPer);
 
     // ---- what each row sees (rows past the last stand for it)
     if (fresh) {
@@ -320,6 +327,8 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
         see_end[r] = v.end;
         see_gap0[r] = v.gap0;
         see_gap1[r] = v.gap1;
+        atomicMin(&clear_end, v.end);
+        atomicMax(&clear_gap, v.gap1);
         row_member[r] = i;
         const int at = static_cast<unsigned>(of) / group;
         row_at[r] = s.q0 + static_cast<int64_t>(at);
@@ -386,24 +395,28 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
         ahead = look_shared(base + kWarp + lane);
         look_own(base + kWarp + lane, ahead);
       }
-      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-      set_barrier();                              // block `it` is there, and block it - 1 done with
-      fetch(it + kStages - 1);
-      const int page = __shfl_sync(0xffffffffu, info.page, it % kWarp);
-      const int member = __shfl_sync(0xffffffffu, info.member, it % kWarp);
-      if (page < 0) continue;
-      // rows of the tile that the block is for
-      const int lo = member < 0 ? 0 : m_lo[member], hi = member < 0 ? kRows : m_hi[member];
-      if (hi <= wr * MT * kTile || lo >= (wr + 1) * MT * kTile || rows <= wr * MT * kTile) continue;
-      const float ks = __shfl_sync(0xffffffffu, info.ks, it % kWarp);
-      const float vs = __shfl_sync(0xffffffffu, info.vs, it % kWarp);
-      const int t0 = __shfl_sync(0xffffffffu, info.t0, it % kWarp);
-      const unsigned char* kb = ring + (it % kStages) * Sh::kBytes;
+      if (it % kPer == 0) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        set_barrier();                            // this stage is there, and the one before it done with
+        fetch(it + (kStages - 1) * kPer);
+      }
+      const int at = it % kWarp;
+      const bool there = __shfl_sync(0xffffffffu, info.codes >= 0, at);
+      const int member = __shfl_sync(0xffffffffu, info.member, at);
+      const float ks = __shfl_sync(0xffffffffu, info.ks, at);
+      const float vs = __shfl_sync(0xffffffffu, info.vs, at);
+      const int t0 = __shfl_sync(0xffffffffu, info.t0, at);
+      if (!there || rows <= wr * MT * kTile) continue;
+      // rows of the tile that the block is for; whether they all see all of it
+      int lo = 0, hi = kRows;
+      if (member >= 0) {
+        lo = m_lo[member];
+        hi = m_hi[member];
+        if (hi <= wr * MT * kTile || lo >= (wr + 1) * MT * kTile) continue;
+      }
+      const bool clear = member < 0 && t0 + kBlock <= clear_end && t0 >= clear_gap;
+      const unsigned char* kb = ring + (it % (kStages * kPer)) * Sh::kBytes;
       const unsigned char* vb = kb + kBlock * D;
-      bool takes[MT];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-        takes[mt] = MT == 1 || (hi > (wr * MT + mt) * kTile && lo < (wr * MT + mt + 1) * kTile);
 
       // S = Q K^T
       float sc[MT][kBlock / 8][4];
@@ -431,65 +444,103 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
           for (int mt = 0; mt < MT; ++mt) mma_f16_from(sc[mt][j], qa[mt][w], b0, b1, w > 0);
         }
       }
-      // weights: exp2 of the scores times the factors, less the running maximum
-      uint32_t pa[MT][kBlock / 16][4], pr[kRest ? MT : 1][kBlock / 16][4];
+      if (SPLIT) {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        if (!takes[mt]) continue;
-        const int r0 = (wr * MT + mt) * kTile + g;
-        if (SPLIT) {
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int j = 0; j < kBlock / 8; ++j) {
             sc[mt][j][0] = fmaf(sc[mt][j][2], 1.f / 2048.f, sc[mt][j][0]);
             sc[mt][j][1] = fmaf(sc[mt][j][3], 1.f / 2048.f, sc[mt][j][1]);
           }
-        }
-        float alpha[2] = {1.f, 1.f};
+      }
+      if (!clear) {
 #pragma unroll
-        for (int r2 = 0; r2 < kR2; ++r2) {
-          const int r = r0 + 8 * r2;
-          const Visible v{see_end[r], see_gap0[r], see_gap1[r]};
-          const int row = min(r, rows - 1);
-          const bool ours = row >= lo && row < hi;
-          if (!(ours && t0 + kBlock <= v.end && (t0 >= v.gap1 || t0 + kBlock <= v.gap0))) {
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int r2 = 0; r2 < kR2; ++r2) {
+            const int r = (wr * MT + mt) * kTile + g + 8 * r2;
+            const int row = min(r, rows - 1);
+            // of the thread's events t0 + 2 c + 8 j (+ 1), those before `some`, but for a gap
+            const int some = row >= lo && row < hi ? see_end[r] - t0 - 2 * c : 0;
 #pragma unroll
             for (int j = 0; j < kBlock / 8; ++j) {
-              const int t = t0 + 8 * j + 2 * c;
-              if (!ours || !sees(v, t)) sc[mt][j][2 * r2] = -INFINITY;
-              if (!ours || !sees(v, t + 1)) sc[mt][j][2 * r2 + 1] = -INFINITY;
+              if (8 * j >= some) sc[mt][j][2 * r2] = -INFINITY;
+              if (8 * j + 1 >= some) sc[mt][j][2 * r2 + 1] = -INFINITY;
+            }
+            if (p.a.window > 0) {
+              const int gap0 = see_gap0[r] - t0 - 2 * c, gap1 = see_gap1[r] - t0 - 2 * c;
+#pragma unroll
+              for (int j = 0; j < kBlock / 8; ++j) {
+                if (8 * j >= gap0 && 8 * j < gap1) sc[mt][j][2 * r2] = -INFINITY;
+                if (8 * j + 1 >= gap0 && 8 * j + 1 < gap1) sc[mt][j][2 * r2 + 1] = -INFINITY;
+              }
             }
           }
-          float big = -INFINITY;
+      }
+      // weights: exp2 of the scores times the factors, less the running maximum. All rows
+      // side by side: a row alone is a chain of waits
+      float big[MT][kR2], alpha[MT][2];
 #pragma unroll
-          for (int j = 0; j < kBlock / 8; ++j)
-            big = fmaxf(big, fmaxf(sc[mt][j][2 * r2], sc[mt][j][2 * r2 + 1]));
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int r2 = 0; r2 < kR2; ++r2) {
+          float x0 = fmaxf(sc[mt][0][2 * r2], sc[mt][0][2 * r2 + 1]), x1 = fmaxf(sc[mt][1][2 * r2], sc[mt][1][2 * r2 + 1]);
+          x0 = fmaxf(x0, fmaxf(sc[mt][2][2 * r2], sc[mt][2][2 * r2 + 1]));
+          x1 = fmaxf(x1, fmaxf(sc[mt][3][2 * r2], sc[mt][3][2 * r2 + 1]));
+          big[mt][r2] = fmaxf(x0, x1);
+        }
+#pragma unroll
+      for (int x = 1; x <= 2; x *= 2)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int r2 = 0; r2 < kR2; ++r2)
+            big[mt][r2] = fmaxf(big[mt][r2], __shfl_xor_sync(0xffffffffu, big[mt][r2], x));
+      bool grew = false;
+      float f[MT][kR2], off[MT][kR2];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int r2 = 0; r2 < kR2; ++r2) {
           // (the factor is not zero, even for a softmax scale of zero: a masked score is -infinity)
-          const float f = fmaxf(qf[mt][r2] * ks, 1e-37f);
-          const float m = fmaxf(top[mt][r2], ceilf(quad_max(big) * f));
-          const float ref = m == -INFINITY ? 0.f : m, off = kLift - ref;
-          alpha[r2] = exp2_approx(top[mt][r2] - ref);
+          f[mt][r2] = fmaxf(qf[mt][r2] * ks, 1e-37f);
+          const float m = fmaxf(top[mt][r2], ceilf(big[mt][r2] * f[mt][r2]));
+          const float ref = m == -INFINITY ? 0.f : m;
+          off[mt][r2] = kLift - ref;
+          alpha[mt][r2] = exp2_approx(top[mt][r2] - ref);
+          grew |= m > top[mt][r2];
           top[mt][r2] = m;
+        }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int r2 = 0; r2 < kR2; ++r2) {
           float2 add = make_float2(0.f, 0.f);
+          const float2 f2 = make_float2(f[mt][r2], f[mt][r2]), off2 = make_float2(off[mt][r2], off[mt][r2]);
 #pragma unroll
           for (int j = 0; j < kBlock / 8; ++j) {
-            const float2 e = fma2(make_float2(sc[mt][j][2 * r2], sc[mt][j][2 * r2 + 1]), make_float2(f, f),
-                                  make_float2(off, off));
+            const float2 e = fma2(make_float2(sc[mt][j][2 * r2], sc[mt][j][2 * r2 + 1]), f2, off2);
             sc[mt][j][2 * r2] = exp2_approx(e.x);
             sc[mt][j][2 * r2 + 1] = exp2_approx(e.y);
             add = fma2(make_float2(sc[mt][j][2 * r2], sc[mt][j][2 * r2 + 1]), make_float2(1.f, 1.f), add);
           }
-          sum[mt][r2] = fmaf(sum[mt][r2], alpha[r2], add.x + add.y);
+          sum[mt][r2] = fmaf(sum[mt][r2], alpha[mt][r2], add.x + add.y);
         }
-        // the output's correction, where the maximum of some row grew
-        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+      // the output's correction, where the maximum of some row grew
+      if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < kPairsO; ++i) {
-              o[mt][nt][i].x *= alpha[i];
-              o[mt][nt][i].y *= alpha[i];
+              o[mt][nt][i].x *= alpha[mt][i];
+              o[mt][nt][i].y *= alpha[mt][i];
             }
-        }
+      }
+      uint32_t pa[MT][kBlock / 16][4], pr[kRest ? MT : 1][kBlock / 16][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int kt = 0; kt < kBlock / 16; ++kt) {
           const float (&s0)[4] = sc[mt][2 * kt], (&s1)[4] = sc[mt][2 * kt + 1];
@@ -514,7 +565,6 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
             }
           }
         }
-      }
       // O += vs P V
       uint32_t vw[kBlock / 16][4][VW];
 #pragma unroll
@@ -563,35 +613,32 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
           b[kt][2][0] = e4m3x2_lo_to_f16x2(l1), b[kt][2][1] = e4m3x2_lo_to_f16x2(h1);
           b[kt][3][0] = e4m3x2_hi_to_f16x2(l1), b[kt][3][1] = e4m3x2_hi_to_f16x2(h1);
         }
+        float acc[MT][4][4], rest[kRest ? MT : 1][4][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          if (!takes[mt]) continue;
+        for (int kt = 0; kt < kBlock / 16; ++kt)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              mma_f16_from(acc[mt][i], pa[mt][kt], b[kt][i][0], b[kt][i][1], kt > 0);
+              if (kRest) mma_f16_from(rest[kRest ? mt : 0][i], pr[kRest ? mt : 0][kt], b[kt][i][0], b[kt][i][1], kt > 0);
+            }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float acc[4];
-#pragma unroll
-            for (int kt = 0; kt < kBlock / 16; ++kt) mma_f16_from(acc, pa[mt][kt], b[kt][i][0], b[kt][i][1], kt > 0);
             float2* out = o[mt][4 * w + i];
-            float2 lo2 = make_float2(acc[0], acc[1]);
-            const float2 hi2 = make_float2(acc[2], acc[3]);
+            float2 y0 = make_float2(acc[mt][i][0], acc[mt][i][1]), y1 = make_float2(acc[mt][i][2], acc[mt][i][3]);
             if (SPLIT) {
-              lo2 = fma2(hi2, less, lo2);
-              out[0] = fma2(vs2, lo2, out[0]);
-            } else {
-              float2 hi3 = hi2;
-              if (kRest) {
-                float rest[4];
-#pragma unroll
-                for (int kt = 0; kt < kBlock / 16; ++kt)
-                  mma_f16_from(rest, pr[kRest ? mt : 0][kt], b[kt][i][0], b[kt][i][1], kt > 0);
-                lo2 = fma2(make_float2(rest[0], rest[1]), less, lo2);
-                hi3 = fma2(make_float2(rest[2], rest[3]), less, hi3);
-              }
-              out[0] = fma2(vs2, lo2, out[0]);
-              out[kPairsO - 1] = fma2(vs2, hi3, out[kPairsO - 1]);
+              y0 = fma2(y1, less, y0);
+            } else if (kRest) {
+              const float (&z)[4] = rest[kRest ? mt : 0][i];
+              y0 = fma2(make_float2(z[0], z[1]), less, y0);
+              y1 = fma2(make_float2(z[2], z[3]), less, y1);
             }
+            out[0] = fma2(vs2, y0, out[0]);
+            if (!SPLIT) out[kPairsO - 1] = fma2(vs2, y1, out[kPairsO - 1]);
           }
-        }
       }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
