@@ -12,8 +12,8 @@ makes belong to that stream.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import operator
 import struct
 
@@ -55,6 +55,12 @@ def _bound():
         _bind(loaded)
         _bound_lib = loaded
     return _bound_lib
+
+
+@functools.lru_cache(maxsize=256)
+def _work_bytes(sizes) -> int:
+    """Of a call of these sizes; they alone decide, so they are remembered."""
+    return _bound().beam_select_work_bytes(_SELECT.pack(*(0,) * 10, *sizes))
 
 
 def beam_select(logits, scores, starts, width: int, *, allowed=None, err_flag=None, stream=None):
@@ -111,19 +117,22 @@ def beam_select(logits, scores, starts, width: int, *, allowed=None, err_flag=No
     if max(rows, groups) > INT32_MAX:
         raise DlrmError(ERR_UNSUPPORTED, where)
     queue = _raw_stream(stream, index)
-    bound = _bound()
     sizes = (rows, vocab, ld, ld_allowed, groups, width, dtype)
-    need = bound.beam_select_work_bytes(_SELECT.pack(*(0,) * 10, *sizes))
+    need = _work_bytes(sizes)
     if need < 0:
         raise DlrmError(ERR_UNSUPPORTED, where)
-    with _on(stream, logits.device) if stream is not None else contextlib.nullcontext():
-        out = torch.empty(3, groups, width, dtype=torch.int32, device=logits.device)
-        work = torch.empty(need, dtype=torch.uint8, device=logits.device)
+    if stream is None:
+        out = torch.empty((3, groups, width), dtype=torch.int32, device=logits.device)
+        work = torch.empty(need, dtype=torch.uint8, device=logits.device) if need else None
+    else:
+        with _on(stream, logits.device):
+            out = torch.empty((3, groups, width), dtype=torch.int32, device=logits.device)
+            work = torch.empty(need, dtype=torch.uint8, device=logits.device) if need else None
     first, step = out.data_ptr(), 4 * groups * width
     args = _SELECT.pack(logits.data_ptr(), 0 if scores is None else scores.data_ptr(),
                         0 if allowed is None else allowed.data_ptr(), starts.data_ptr(), first, first + step,
-                        first + 2 * step, 0 if err_flag is None else err_flag.data_ptr(), work.data_ptr(), need,
-                        *sizes)
-    _check(bound.beam_select(args, queue), where)
-    best, parents, tokens = out.unbind(0)
+                        first + 2 * step, 0 if err_flag is None else err_flag.data_ptr(),
+                        0 if work is None else work.data_ptr(), need, *sizes)
+    _check(_bound().beam_select(args, queue), where)
+    best, parents, tokens = out.unbind()
     return best.view(torch.float32), parents, tokens

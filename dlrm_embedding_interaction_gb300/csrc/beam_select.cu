@@ -15,8 +15,10 @@
 // to the exact value, and ties to the exact index.
 //
 // The order hangs by differences of the rows' logarithms, so these are held more
-// precisely than fp32: the sums' terms have rounding errors of their own (2^-23 each, not
-// of one sign), their sums are exact to 2^-40 or so, and scores are compared in 64 bits.
+// precisely than fp32: the sums' terms have rounding errors of their own (2^-22 each, not
+// of one sign), sums and logarithms are kept in two floats (64-bit arithmetic has few
+// units: a logarithm in it took the join of 64 users 2.4 us, the sums 13), and the scores of
+// the few that are ranked are compared in 64 bits.
 #include <float.h>
 
 #include "history.cuh"
@@ -25,28 +27,42 @@ namespace dlrm {
 
 namespace {
 
-constexpr int kScanThreads = 256;
+constexpr int kScanThreads = 128;
 constexpr int kJoinThreads = 512;
 constexpr int kVectors = 4;                      // 16-byte vectors of a thread and tile
 constexpr int kSubsets = 64;                     // widths up to here: one subset a thread will do
 constexpr int kFinal = 2048;                     // candidates that are ranked at most
-static_assert(kBeamMaxWidth <= kScanThreads && kBeamMaxWidth <= kFinal, "a subset for each place");
+constexpr int kLists = 1024;                     // lists of a group that shared memory knows
+constexpr int kRowsHere = 256;                   // rows of a group whose states lie in shared memory
+static_assert(kSubsets <= kScanThreads && kBeamMaxWidth <= kScanThreads * kVectors && kBeamMaxWidth <= kJoinThreads &&
+                  kBeamMaxWidth <= kFinal, "a subset for each place");
 
+// A sum in two floats: the rounding errors of `sum` in `rest`.
+struct Sum {
+  float sum, rest;
+  __device__ __forceinline__ void add(float x) {
+    const float s = sum + x, z = s - sum;
+    rest += (sum - (s - z)) + (x - z);
+    sum = s;
+  }
+};
 struct Part {                                    // of a chunk of a row
-  float top;                                     // reference of the sum; -infinity: nothing allowed
+  Sum sum;                                       // of exponentials, times 2^-power(ref), or e^-ref if it is far
+  float ref;                                     // near the largest logit; -infinity: nothing allowed
+  float top;                                     // largest logit
   int32_t count;                                 // entries of its list
-  double sum;                                    // of exp(logit - top)
+  int32_t pad;
 };
 struct Entry {
   float logit;
   int32_t token;
 };
 struct RowState {
-  double lse;
+  Sum lse;                                       // (first the sum of exponentials, and its reference in offset)
   float offset;                                  // score - lse; -infinity: the row has no candidates
   int32_t pad;
 };
-static_assert(sizeof(Part) == 16 && sizeof(Entry) == 8 && sizeof(RowState) == 16, "scratch sizes");
+static_assert(sizeof(Part) == 24 && sizeof(Entry) == 8 && sizeof(RowState) == 16, "scratch sizes");
 
 struct Params {
   dlrm_beam_select_t a;
@@ -71,24 +87,95 @@ __device__ __forceinline__ float bound_of(uint32_t k) {
   return k <= key_of(-FLT_MAX) ? -FLT_MAX : of_key(k);
 }
 
-// exp(x - ref): log2(e) in two parts, the larger one rounded down so that an infinite
-// difference stays one; rounding errors of the arguments then have no common sign.
+// Exponentials of a row are powers of two of x log2(e) - power(ref), in one FMA: the power is a
+// whole number, so sums with other references differ by powers of two. log2(e) in fp32 is
+// short of kLow: x kLow is left out of the powers, ref kLow (nearly all of it) comes back with the
+// logarithm. References that are far from zero are subtracted instead.
+constexpr float kLog2E = 1.4426950408889634f, kLow = 1.92596299e-8f;
+constexpr float kLn2 = 0.693147180559945309f, kLn2Low = -1.90465430e-9f;
+constexpr float kFar = 65536.f;
+__device__ __forceinline__ float power(float ref) { return ceilf(ref * kLog2E); }
 __device__ __forceinline__ float exp_from(float x, float ref) {
-  constexpr float kHigh = 1.44269490242004394531f, kLow = 1.38468919e-7f;
-  const float d = x - ref;
-  return exp2_approx(fmaf(d, kHigh, d * kLow));
+  return fabsf(ref) < kFar ? exp2_approx(fmaf(x, kLog2E, -power(ref))) : exp2_approx((x - ref) * kLog2E);
+}
+// Two at a time: x a + b.
+__device__ __forceinline__ float2 exp2_of(float2 x, float a, float b) {
+  float2 y;
+  asm("{\n\t.reg .b64 x, a, b;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 a, {%4, %4};\n\tmov.b64 b, {%5, %5};\n\t"
+      "fma.rn.f32x2 x, x, a, b;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(x.x), "f"(x.y), "f"(a), "f"(b));
+  y.x = exp2_approx(y.x);
+  y.y = exp2_approx(y.y);
+  return y;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+  float2 z;
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 a, a, b;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(z.x), "=f"(z.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return z;
+}
+// Over the warp, the same in every lane.
+__device__ __forceinline__ Sum warp_sum(Sum s) {
+#pragma unroll
+  for (int d = kWarp / 2; d > 0; d /= 2) {
+    const float x = __shfl_xor_sync(0xffffffffu, s.sum, d);
+    s.rest += __shfl_xor_sync(0xffffffffu, s.rest, d);
+    s.add(x);
+  }
+  return s;
+}
+// What a sum with reference `from` is with reference `to` (>= from).
+__device__ __forceinline__ Sum moved(Sum s, float from, float to) {
+  if (from == to) return s;
+  if (from == -INFINITY) return Sum{s.sum, 0.f};  // zero, or NaN
+  const float f = fabsf(from) < kFar && fabsf(to) < kFar ? pow2f(static_cast<int>(fmaxf(power(from) - power(to), -126.f)))
+                                                         : exp2_approx((from - to) * kLog2E);
+  return Sum{s.sum * f, s.rest * f};              // (a power of two is exact)
+}
+// log(s) with its reference, in two floats: s = m 2^k with m around 1, log m = 2 artanh z,
+// z = (m - 1) / (m + 1), by the series 2 z (1 + z^2 / 3 + z^4 / 5 + ...), |z| <= 0.172.
+__device__ __forceinline__ Sum log_sum(const Sum& s, float ref) {
+  const int k = (static_cast<int>(__float_as_uint(s.sum) - 0x3f3504f3u)) >> 23;   // m from sqrt(1/2) on
+  const float scale = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+  const float m = s.sum * scale, low = s.rest * scale;
+  const float p = m - 1.f, q = m + 1.f, q_low = (m - (q - 1.f)) + low;   // p is exact
+  const float z = p / q;
+  const float z_low = (fmaf(-z, q, p) + low - z * q_low) / q;
+  const float z2 = z * z;
+  float t = fmaf(z2, 1.f / 11, 1.f / 9);
+  t = fmaf(t, z2, 1.f / 7);
+  t = fmaf(t, z2, 1.f / 5);
+  t = fmaf(t, z2, 1.f / 3) * z2 * z;
+  Sum y{2.f * z, 2.f * z_low};
+  y.rest = fmaf(2.f, t, y.rest);
+  const bool far = !(fabsf(ref) < kFar);
+  const float n = static_cast<float>(k) + (far ? 0.f : power(ref));
+  const float high = n * kLn2;
+  y.rest += fmaf(n, kLn2, -high) + n * kLn2Low;
+  y.add(high);
+  if (far)
+    y.add(ref);
+  else
+    y.rest += ref * (kLow * kLn2);
+  const float sum = y.sum + y.rest;
+  return Sum{sum, (y.sum - sum) + y.rest};
 }
 
-// Largest key with kBits bits past the first that not all threads' keys have in common
-// which k or more of the keys reach; a thread has N. Block-wide. red: 2 ints a warp.
+// A lower bound of the k-th largest of the threads' keys, N each, bit by bit from the first
+// that they do not have in common until few more than k reach it (keys of -infinity do not
+// count, and are the bound where there are fewer than k others). Block-wide. red: 2 ints a warp.
 template <int THREADS, int N>
 __device__ __forceinline__ uint32_t block_bound(const uint32_t (&key)[N], int k, uint32_t* red) {
-  constexpr int kBits = 12, kWarps = THREADS / kWarp;
-  uint32_t hi = key[0], lo = key[0];
+  constexpr int kWarps = THREADS / kWarp;
+  const uint32_t none = key_of(-INFINITY);
+  uint32_t hi = none, lo = 0xffffffffu;
 #pragma unroll
-  for (int i = 1; i < N; ++i) {
+  for (int i = 0; i < N; ++i) {
     hi = max(hi, key[i]);
-    lo = min(lo, key[i]);
+    lo = key[i] > none ? min(lo, key[i]) : lo;
   }
   hi = __reduce_max_sync(0xffffffffu, hi);
   lo = __reduce_min_sync(0xffffffffu, lo);
@@ -102,16 +189,22 @@ __device__ __forceinline__ uint32_t block_bound(const uint32_t (&key)[N], int k,
     hi = max(hi, red[w]);
     lo = min(lo, red[kWarps + w]);
   }
-  __syncthreads();
+  int there = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) there += __syncthreads_count(key[i] > none);
+  if (there < k) return none;
   if (hi == lo) return hi;
   const int first = 31 - __clz(hi ^ lo);
   uint32_t bound = first == 31 ? 0u : hi & (0xffffffffu << (first + 1));
-  for (int bit = first; bit >= max(first - kBits + 1, 0); --bit) {
+  for (int bit = first; bit >= 0 && there > k + k / 4 + 8; --bit) {
     const uint32_t trial = bound | (1u << bit);
     int n = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) n += __syncthreads_count(key[i] >= trial);
-    if (n >= k) bound = trial;
+    if (n >= k) {
+      bound = trial;
+      there = n;
+    }
   }
   return bound;
 }
@@ -175,18 +268,58 @@ __device__ __forceinline__ uint2 load_allowed(const uint8_t* row, int64_t e0, in
   const int bits = (off & 3) * 8;
   return make_uint2(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits));
 }
-// Element e of a vector, -infinity where it is not allowed.
+// The vector with -infinity where a byte of `may` is zero.
 template <int DT>
-__device__ __forceinline__ float element_of(const uint4& v, int e) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  if (DT == DLRM_DTYPE_FP32) return __uint_as_float(w[e]);
-  const uint32_t x = w[e / 2];
-  if (DT == DLRM_DTYPE_BF16) return __uint_as_float(e % 2 ? x & 0xffff0000u : x << 16);
-  const float2 f = f16x2_to_float2(x);
-  return e % 2 ? f.y : f.x;
+__device__ __forceinline__ void hide(uint4& v, const uint2& may) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if (DT == DLRM_DTYPE_FP32) {
+    const uint32_t m = __vcmpne4(may.x, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t k = __byte_perm(m, 0, 0x1111 * i);
+      w[i] = (w[i] & k) | (0xff800000u & ~k);
+    }
+  } else {
+    constexpr uint32_t kNone = DT == DLRM_DTYPE_BF16 ? 0xff80ff80u : 0xfc00fc00u;
+    const uint32_t m[2] = {__vcmpne4(may.x, 0), __vcmpne4(may.y, 0)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t k = __byte_perm(m[i / 2], 0, i % 2 ? 0x3322 : 0x1100);
+      w[i] = (w[i] & k) | (kNone & ~k);
+    }
+  }
+  v = make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ bool byte_of(const uint2& m, int e) {
-  return ((e < 4 ? m.x : m.y) >> (8 * (e % 4)) & 0xff) != 0;
+// Bytes that allow the first n of a vector's elements.
+__device__ __forceinline__ uint2 first_bytes(int n) {
+  const uint64_t m = n >= 8 ? ~uint64_t(0) : n <= 0 ? 0 : (uint64_t(1) << (8 * n)) - 1;
+  return make_uint2(static_cast<uint32_t>(m), static_cast<uint32_t>(m >> 32));
+}
+// Pair i of a vector's elements.
+template <int DT>
+__device__ __forceinline__ float2 pair_of(const uint4& v, int i) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if (DT == DLRM_DTYPE_FP32) return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+  if (DT == DLRM_DTYPE_BF16) return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  return f16x2_to_float2(w[i]);
+}
+// Largest element (NaN passed over).
+template <int DT>
+__device__ __forceinline__ float largest(const uint4& v) {
+  if (DT == DLRM_DTYPE_FP32)
+    return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+  uint32_t m, n;
+  if (DT == DLRM_DTYPE_BF16) {
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(v.x), "r"(v.y));
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(n) : "r"(v.z), "r"(v.w));
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(n));
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
+  asm("max.f16x2 %0, %1, %2;" : "=r"(m) : "r"(v.x), "r"(v.y));
+  asm("max.f16x2 %0, %1, %2;" : "=r"(n) : "r"(v.z), "r"(v.w));
+  asm("max.f16x2 %0, %0, %1;" : "+r"(m) : "r"(n));
+  const float2 f = f16x2_to_float2(m);
+  return fmaxf(f.x, f.y);
 }
 
 // ------------------------------------------------------------------ scan
@@ -276,14 +409,17 @@ __device__ __forceinline__ int tighten(Entry* list, int n, int k) {
   return kept;
 }
 
+// What bounds it: HBM, and the instructions around one exponential a logit (about four).
+// The list holds vectors by their largest element; their elements are looked at
+// once more at the end.
 template <int DT, bool MASK, bool ALIGNED>
-__global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kScanThreads, 8) beam_scan_kernel(const __grid_constant__ Params p) {
   constexpr int kVec = Row<DT>::kVec, kWarps = kScanThreads / kWarp;
   constexpr int kTile = kScanThreads * kVec * kVectors;
   extern __shared__ __align__(16) unsigned char smem[];
-  Entry* list = reinterpret_cast<Entry*>(smem);
+  Entry* list = reinterpret_cast<Entry*>(smem);  // of vectors: largest logit, first token
   __shared__ uint32_t red[2 * kWarps];
-  __shared__ double sums[kWarps];
+  __shared__ Sum sums[kWarps];
   __shared__ int count_s, other_s;
   const int t = threadIdx.x, lane = t % kWarp, warp = t / kWarp;
   const int64_t row = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks, vocab = p.a.vocab;
@@ -291,7 +427,7 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
   const char* logits = static_cast<const char*>(p.a.logits) + row * p.a.ld * Row<DT>::kBytes;
   const uint8_t* allowed = MASK ? p.a.allowed + row * p.a.ld_allowed : nullptr;
   const int width = p.a.width;
-  if (t == 0) count_s = 0;
+  if (t == 0) count_s = other_s = 0;
   pdl_wait();
   pdl_trigger();
 
@@ -308,26 +444,31 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
     }
   };
   load(e0);
-  float ref = -INFINITY, sum = 0.f, rest = 0.f;   // the sum in two parts
-  float bound = -FLT_MAX;
+  float ref = -INFINITY;
+  Sum sum{0.f, 0.f};
+  float bound = -FLT_MAX, peak = -INFINITY;
   bool many = false;                              // the list overflowed
   for (int64_t at = e0; at < e1; at += kTile) {
-    float x[kVectors][kVec], top[kVectors];
+    uint4 now[kVectors];
+    float top[kVectors];
 #pragma unroll
     for (int v = 0; v < kVectors; ++v) {
-      const int64_t e = at + (v * kScanThreads + t) * kVec;
-      top[v] = -INFINITY;
+      now[v] = raw[v];
+      if (MASK) hide<DT>(now[v], may[v]);
+    }
+    if (at + kTile > e1) {
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        x[v][i] = element_of<DT>(raw[v], i);
-        if (e + i >= e1 || (MASK && !byte_of(may[v], i))) x[v][i] = -INFINITY;
-        top[v] = fmaxf(top[v], x[v][i]);
+      for (int v = 0; v < kVectors; ++v) {
+        const int64_t left = e1 - (at + (v * kScanThreads + t) * kVec);
+        if (left < kVec) hide<DT>(now[v], first_bytes(static_cast<int>(max(left, int64_t(0)))));
       }
     }
-    if (at + kTile < e1) load(at + kTile);
-    float most = top[0];
 #pragma unroll
-    for (int v = 1; v < kVectors; ++v) most = fmaxf(most, top[v]);
+    for (int v = 0; v < kVectors; ++v) top[v] = largest<DT>(now[v]);
+    if (at + kTile < e1) load(at + kTile);
+    const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+    peak = fmaxf(peak, most);
+    static_assert(kVectors == 4, "largest of a thread");
     if (at == e0) {
       // the bound; and one reference for all threads, so that sums need no factors
       uint32_t key;
@@ -349,133 +490,182 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
       for (int w = 1; w < kWarps; ++w) all = max(all, red[w]);
       ref = of_key(all);
     } else if (most > ref + 20.f) {
-      const float f = exp_from(ref, most);
-      sum *= f;
-      rest *= f;
+      sum = moved(sum, ref, most);
       ref = most;
     }
-    const float base = ref == -INFINITY ? 0.f : ref;
-    float part[kVectors];
-#pragma unroll
-    for (int v = 0; v < kVectors; ++v) {
-      part[v] = 0.f;
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) part[v] += exp_from(x[v][i], base);
-    }
-    // sum + rest, the rounding errors of sum in rest
-#pragma unroll
-    for (int v = 0; v < kVectors; ++v) {
-      const float s = sum + part[v], z = s - sum;
-      rest += (sum - (s - z)) + (part[v] - z);
-      sum = s;
-    }
-    if (!many && most >= bound) {
+    float2 part[kVectors];
+    if (fabsf(ref) < kFar || ref == -INFINITY) {
+      const float less = ref == -INFINITY ? 0.f : -power(ref);
 #pragma unroll
       for (int v = 0; v < kVectors; ++v) {
-        if (top[v] < bound) continue;
-        const int64_t e = at + (v * kScanThreads + t) * kVec;
+        part[v] = exp2_of(pair_of<DT>(now[v], 0), kLog2E, less);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i)
-          if (x[v][i] >= bound) {
-            const int place = atomicAdd(&count_s, 1);
-            if (place < p.cap) list[place] = Entry{x[v][i], static_cast<int>(e + i)};
-          }
+        for (int i = 1; i < kVec / 2; ++i) part[v] = add2(part[v], exp2_of(pair_of<DT>(now[v], i), kLog2E, less));
       }
+    } else {
+#pragma unroll
+      for (int v = 0; v < kVectors; ++v) {
+        part[v] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kVec / 2; ++i) {
+          const float2 x = pair_of<DT>(now[v], i);
+          part[v].x += exp_from(x.x, ref);
+          part[v].y += exp_from(x.y, ref);
+        }
+      }
+    }
+    const float2 y = add2(add2(part[0], part[1]), add2(part[2], part[3]));
+    sum.add(y.x + y.y);
+    if (!many) {
+#pragma unroll
+      for (int v = 0; v < kVectors; ++v)
+        if (top[v] >= bound) {
+          const int place = atomicAdd(&count_s, 1);
+          if (place < p.cap) list[place] = Entry{top[v], static_cast<int>(at + (v * kScanThreads + t) * kVec)};
+        }
     }
     __syncthreads();
     const int count = count_s;
     many |= count > p.cap;
-    if (!many && count > 2 * width + 32) {
+    if (!many && count > (at + kTile < e1 ? p.cap / 2 : width + width / 4 + 8)) {
       __syncthreads();                            // `count_s` is read
       if (warp == 0) {
         const int n = tighten(list, count, width);
         if (lane == 0) count_s = n;
       }
       __syncthreads();
-      if (count_s > p.cap / 2) {
-        many = true;                              // ties: the exact way, at the end
-      } else {
-        // the least that is left
-        float least = INFINITY;
-        for (int i = lane; i < count_s; i += kWarp) least = fminf(least, list[i].logit);
-        bound = of_key(__reduce_min_sync(0xffffffffu, key_of(least)));
-      }
+      const int n = count_s;
+      many |= n > p.cap / 4;                      // ties: the exact way, at the end
+      // the least that is left
+      float least = INFINITY;
+      for (int i = lane; i < n; i += kWarp) least = fminf(least, list[i].logit);
+      bound = of_key(__reduce_min_sync(0xffffffffu, key_of(least)));
     }
     __syncthreads();
   }
-  // ---- the chunk's sum, in 64 bits
-  const uint32_t hi = __reduce_max_sync(0xffffffffu, key_of(ref));
+  // ---- the chunk's sum
+  const uint32_t hi = __reduce_max_sync(0xffffffffu, key_of(ref)), most = __reduce_max_sync(0xffffffffu, key_of(peak));
+  if (lane == 0) {
+    red[warp] = hi;
+    red[kWarps + warp] = most;
+  }
   __syncthreads();
-  if (lane == 0) red[warp] = hi;
-  __syncthreads();
-  uint32_t all = red[0];
+  uint32_t all = red[0], highest = red[kWarps];
 #pragma unroll
-  for (int w = 1; w < kWarps; ++w) all = max(all, red[w]);
+  for (int w = 1; w < kWarps; ++w) {
+    all = max(all, red[w]);
+    highest = max(highest, red[kWarps + w]);
+  }
   const float common = of_key(all);
-  double mine = static_cast<double>(sum) + static_cast<double>(rest);
-  if (ref != common) mine *= ref == -INFINITY ? 0.0 : static_cast<double>(exp_from(ref, common));
-#pragma unroll
-  for (int d = kWarp / 2; d > 0; d /= 2) mine += __shfl_xor_sync(0xffffffffu, mine, d);
-  if (lane == 0) sums[warp] = mine;
+  sum = moved(sum, ref, common);
+  sum = warp_sum(sum);
+  if (lane == 0) sums[warp] = sum;
+  // ---- the list's elements
   Entry* out = p.entries + static_cast<int64_t>(blockIdx.x) * p.cap;
-  int count = many ? exact_chunk<DT>(p, row, e0, e1, out, &other_s) : count_s;
-  __syncthreads();
-  if (!many)
-    for (int i = t; i < count; i += kScanThreads) out[i] = list[i];
+  int count = 0;
+  if (!many) {
+    const int n = count_s * kVec;
+    for (int i = t; i < n; i += kScanThreads) {
+      const int e = list[i / kVec].token + i % kVec;
+      if (e >= e1 || (MASK && !allowed[e])) continue;
+      const float x = load_element<DT>(logits, e);
+      if (!(x >= bound)) continue;
+      const int place = atomicAdd(&other_s, 1);
+      if (place < p.cap) out[place] = Entry{x, e};
+    }
+    __syncthreads();
+    count = other_s;
+    many = count > p.cap;
+    __syncthreads();
+  }
+  if (many) count = exact_chunk<DT>(p, row, e0, e1, out, &other_s);
   if (t == 0) {
-    double total = 0.0;
+    Sum total = sums[0];
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) total += sums[w];
-    p.parts[blockIdx.x] = Part{common, count, total};
+    for (int w = 1; w < kWarps; ++w) {
+      total.rest += sums[w].rest;
+      total.add(sums[w].sum);
+    }
+    p.parts[blockIdx.x] = Part{total, common, of_key(highest), count, 0};
   }
 }
 
 // ------------------------------------------------------------------ join
 
 struct Candidate {
-  double score;
+  uint64_t key;                                  // of the score (first the logit's bits)
   int32_t row, token;
 };
+// 64-bit floats as integers of the same order: compared as such, as 64-bit arithmetic has
+// few units.
 __device__ __forceinline__ uint64_t key_of(double x) {
   const uint64_t u = static_cast<uint64_t>(__double_as_longlong(x + 0.0));
   return u ^ (static_cast<uint64_t>(static_cast<int64_t>(u) >> 63) | (uint64_t(1) << 63));
+}
+__device__ __forceinline__ double of_key(uint64_t k) {
+  return __longlong_as_double(static_cast<long long>(k >> 63 ? k ^ (uint64_t(1) << 63) : ~k));
 }
 __device__ __forceinline__ uint64_t index_of(int row, int token) {
   return static_cast<uint64_t>(static_cast<uint32_t>(row)) << 32 | static_cast<uint32_t>(token);
 }
 
-// What the rows' scores and sums make of them; returns whether the row is bad.
-__device__ __forceinline__ bool row_state(const Params& p, int64_t row, float top, double sum, RowState& s) {
-  const float score = p.a.scores ? p.a.scores[row] : 0.f;
-  s.pad = 0;
-  s.lse = top == -INFINITY ? -INFINITY : static_cast<double>(top) + log(sum);
-  const bool bad = !(score < INFINITY) || !(sum < INFINITY) || top == INFINITY;
-  s.offset = bad || top == -INFINITY || score == -INFINITY ? -INFINITY
-                                                           : static_cast<float>(static_cast<double>(score) - s.lse);
-  return bad;
+// A row's state from its sum (in lse) and reference (in offset); a thread a row. Returns
+// the offset's magnitude.
+__device__ __forceinline__ float row_state(const Params& p, int64_t row, RowState& s) {
+  const float score = p.a.scores ? p.a.scores[row] : 0.f, ref = s.offset, sum = s.lse.sum;
+  const bool bad = !(score < INFINITY) || !(sum < INFINITY) || ref == INFINITY;
+  if (bad) flag(p.a.err, DLRM_ERRBIT_INVALID_ARG);
+  if (bad || ref == -INFINITY || score == -INFINITY) {
+    s.offset = -INFINITY;
+    return 0.f;
+  }
+  s.lse = log_sum(s.lse, ref);
+  s.offset = (score - s.lse.sum) - s.lse.rest;
+  return fabsf(s.offset);
 }
 
-// Selects among the candidates that each(f) calls f(row, token, logit, offset) for, every
-// thread for its own, and writes the group's outputs. Block-wide.
+// Largest magnitude of the rows' offsets, in every thread.
+__device__ __forceinline__ float widest_of(float mine, uint32_t* red) {
+  uint32_t x = __reduce_max_sync(0xffffffffu, __float_as_uint(mine));
+  __syncthreads();
+  if (threadIdx.x % kWarp == 0) red[threadIdx.x / kWarp] = x;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / kWarp; ++w) x = max(x, red[w]);
+  __syncthreads();
+  return __uint_as_float(x);
+}
+
+// Below the k-th largest of the threads' scores by what fp32 may be off: half an ulp of
+// a score's own and an ulp of its offset's, twice.
+__device__ __forceinline__ float score_bound(float most, int k, float widest, uint32_t* red) {
+  const uint32_t key[1] = {key_of(most)};
+  const float bound = bound_of(block_bound<kJoinThreads>(key, k, red));
+  return bound > -FLT_MAX ? bound - (3e-7f * (fabsf(bound) + widest) + 1e-30f) : bound;
+}
+
+// Selects among the candidates that each(bound, f) calls f(row, token, logit, offset) for,
+// every thread for its own, and writes the group's outputs; it may pass over what lies below
+// the bound. No place of the result lies below `bound`. Rows count from the group's first, s0,
+// whose states are `state`. Block-wide.
 template <class Each>
-__device__ __forceinline__ void select_of(const Params& p, int group, float widest, const Each& each,
-                                          Candidate* found, uint32_t* red, int* count_s) {
+__device__ __forceinline__ void select_of(const Params& p, int64_t s0, const RowState* state, float widest, float bound,
+                                          const Each& each, Candidate* found, uint32_t* red, int* count_s) {
   const int t = threadIdx.x, width = p.a.width;
   const auto score_of = [&](int row, float logit) {
-    return static_cast<double>(p.a.scores ? p.a.scores[row] : 0.f) + (static_cast<double>(logit) - p.rows[row].lse);
+    const Sum lse = state[row].lse;
+    return static_cast<double>(p.a.scores ? p.a.scores[s0 + row] : 0.f) +
+           ((static_cast<double>(logit) - static_cast<double>(lse.sum)) - static_cast<double>(lse.rest));
   };
   float most = -INFINITY;
-  each([&](int, int, float logit, float offset) { most = fmaxf(most, offset + logit); });
-  const uint32_t key[1] = {key_of(most)};
-  float bound = bound_of(block_bound<kJoinThreads>(key, width, red));
-  // an fp32 score is off by at most half an ulp of its own and of the offset's
-  if (bound > -FLT_MAX) bound -= 2.4e-7f * (fabsf(bound) + widest) + 1e-30f;
+  each(bound, [&](int, int, float logit, float offset) { most = fmaxf(most, offset + logit); });
+  bound = fmaxf(bound, score_bound(most, width, widest, red));
   if (t == 0) *count_s = 0;
   __syncthreads();
-  each([&](int row, int token, float logit, float offset) {
+  each(bound, [&](int row, int token, float logit, float offset) {
     if (!(offset + logit >= bound)) return;
     const int at = atomicAdd(count_s, 1);
-    if (at < kFinal) found[at] = Candidate{score_of(row, logit), row, token};
+    if (at < kFinal) found[at] = Candidate{__float_as_uint(logit), row, token};
   });
   __syncthreads();
   int n = *count_s;
@@ -483,7 +673,7 @@ __device__ __forceinline__ void select_of(const Params& p, int group, float wide
     // too many at the bound: the exact score, then the exact index among its ties
     const auto reach = [&](uint64_t k, uint64_t last) {
       int c = 0;
-      each([&](int row, int token, float logit, float offset) {
+      each(bound, [&](int row, int token, float logit, float offset) {
         if (!(offset + logit >= bound)) return;
         const uint64_t x = key_of(score_of(row, logit));
         c += x > k || (x == k && index_of(row, token) <= last);
@@ -509,30 +699,39 @@ __device__ __forceinline__ void select_of(const Params& p, int group, float wide
     __syncthreads();
     if (t == 0) *count_s = 0;
     __syncthreads();
-    each([&](int row, int token, float logit, float offset) {
+    each(bound, [&](int row, int token, float logit, float offset) {
       if (!(offset + logit >= bound)) return;
-      const double s = score_of(row, logit);
-      const uint64_t x = key_of(s);
+      const uint64_t x = key_of(score_of(row, logit));
       if (!(x > k || (x == k && index_of(row, token) <= last))) return;
       const int at = atomicAdd(count_s, 1);
-      if (at < kFinal) found[at] = Candidate{s, row, token};
+      if (at < kFinal) found[at] = Candidate{__float_as_uint(logit), row, token};
     });
     __syncthreads();
     n = min(*count_s, kFinal);
   }
-  // ---- ranks
-  const int64_t out = static_cast<int64_t>(group) * width;
   for (int i = t; i < n; i += kJoinThreads) {
     const Candidate c = found[i];
+    found[i].key = key_of(score_of(c.row, __uint_as_float(static_cast<uint32_t>(c.key))));
+  }
+  __syncthreads();
+  // ---- ranks: a candidate by several threads, where there are few
+  const int64_t out = static_cast<int64_t>(blockIdx.x) * width;
+  int share = 1;
+  while (2 * share <= kWarp && 2 * share * n <= kJoinThreads) share *= 2;
+  for (int i0 = 0; i0 < n; i0 += kJoinThreads / share) {
+    const int i = i0 + t / share;
+    const Candidate c = found[min(i, n - 1)];
     const uint64_t mine = index_of(c.row, c.token);
     int rank = 0;
-    for (int j = 0; j < n; ++j) {
+#pragma unroll 4
+    for (int j = t % share; j < n; j += share) {
       const Candidate d = found[j];
-      rank += d.score > c.score || (d.score == c.score && index_of(d.row, d.token) < mine);
+      rank += d.key > c.key || (d.key == c.key && index_of(d.row, d.token) < mine);
     }
-    if (rank < width) {
-      p.a.out_scores[out + rank] = static_cast<float>(c.score);
-      p.a.out_rows[out + rank] = c.row;
+    for (int d = 1; d < share; d *= 2) rank += __shfl_xor_sync(0xffffffffu, rank, d);
+    if (i < n && t % share == 0 && rank < width) {
+      p.a.out_scores[out + rank] = static_cast<float>(of_key(c.key));
+      p.a.out_rows[out + rank] = static_cast<int>(s0) + c.row;
       p.a.out_tokens[out + rank] = c.token;
     }
   }
@@ -553,113 +752,150 @@ __device__ __forceinline__ void group_rows(const Params& p, int group, int64_t& 
   }
 }
 
-// Largest magnitude of the rows' offsets, in every thread.
-__device__ __forceinline__ float widest_of(float mine, uint32_t* red) {
-  uint32_t x = __reduce_max_sync(0xffffffffu, __float_as_uint(mine));
-  __syncthreads();
-  if (threadIdx.x % kWarp == 0) red[threadIdx.x / kWarp] = x;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kJoinThreads / kWarp; ++w) x = max(x, red[w]);
-  __syncthreads();
-  return __uint_as_float(x);
-}
-
 __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_constant__ Params p) {
   __shared__ Candidate found[kFinal];
   __shared__ uint32_t red[2 * kJoinThreads / kWarp];
-  __shared__ int count_s;
+  __shared__ int count_s, n_open, open[kLists], list_count[kLists];   // open: lists to look at
+  __shared__ float list_top[kLists];             // largest score of each
   const int t = threadIdx.x, lane = t % kWarp, warp = t / kWarp;
   pdl_wait();
   pdl_trigger();
   int64_t s0, s1;
   group_rows(p, blockIdx.x, s0, s1);
-  // ---- the rows' sums
-  float widest = 0.f;
-  for (int64_t row = s0 + warp; row < s1; row += kJoinThreads / kWarp) {
-    const Part* parts = p.parts + row * p.chunks;
+  const int chunks = p.chunks;
+  RowState* state = p.rows + s0;
+  // ---- the rows' sums, a warp each, then their logarithms, a thread each
+  for (int64_t row = warp; row < s1 - s0; row += kJoinThreads / kWarp) {
+    const Part* parts = p.parts + (s0 + row) * chunks;
     uint32_t hi = 0;
-    for (int c = lane; c < p.chunks; c += kWarp) hi = max(hi, key_of(parts[c].top));
-    const float top = of_key(__reduce_max_sync(0xffffffffu, hi));
-    double sum = 0.0;
-    for (int c = lane; c < p.chunks; c += kWarp) {
-      const Part x = parts[c];
-      // (nothing allowed: zero, or NaN)
-      sum += x.top == top || x.top == -INFINITY ? x.sum : x.sum * exp(static_cast<double>(x.top) - top);
+    for (int c = lane; c < chunks; c += kWarp) hi = max(hi, key_of(parts[c].ref));
+    const float ref = of_key(__reduce_max_sync(0xffffffffu, hi));
+    Sum sum{0.f, 0.f};
+    for (int c = lane; c < chunks; c += kWarp) {
+      const Sum x = moved(parts[c].sum, parts[c].ref, ref);
+      sum.rest += x.rest;
+      sum.add(x.sum);
     }
-#pragma unroll
-    for (int d = kWarp / 2; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    RowState s;
-    if (row_state(p, row, top, sum, s) && lane == 0) flag(p.a.err, DLRM_ERRBIT_INVALID_ARG);
-    if (lane == 0) p.rows[row] = s;
-    if (s.offset != -INFINITY) widest = fmaxf(widest, fabsf(s.offset));
+    sum = warp_sum(sum);
+    if (lane == 0) state[row] = RowState{sum, ref, 0};
+  }
+  __syncthreads();
+  float widest = 0.f;
+  for (int64_t row = t; row < s1 - s0; row += kJoinThreads) {
+    RowState s = state[row];
+    widest = fmaxf(widest, row_state(p, s0 + row, s));
+    state[row] = s;
   }
   widest = widest_of(widest, red);
-  // ---- the lists, a warp each
-  const int64_t lists = (s1 - s0) * p.chunks;
-  select_of(p, blockIdx.x, widest, [&](const auto& f) {
-    for (int64_t l = warp; l < lists; l += kJoinThreads / kWarp) {
-      const int row = static_cast<int>(s0 + l / p.chunks);
-      const int64_t at = s0 * p.chunks + l;
-      const float offset = p.rows[row].offset;
-      const int n = offset == -INFINITY ? 0 : p.parts[at].count;
-      const Entry* entries = p.entries + at * p.cap;
-      for (int i = lane; i < n; i += kWarp) f(row, entries[i].token, entries[i].logit, offset);
+  // ---- the lists, a warp each; those whose largest logit lies below the bound are passed over
+  const int64_t lists = (s1 - s0) * chunks;
+  const bool few = lists <= kLists;
+  const auto score_of_list = [&](int64_t l) { return state[l / chunks].offset + p.parts[s0 * chunks + l].top; };
+  float most = -INFINITY;
+  for (int64_t l = t; l < lists; l += kJoinThreads) {
+    const float x = score_of_list(l);
+    if (few) {
+      list_top[l] = x;
+      list_count[l] = p.parts[s0 * chunks + l].count;
     }
-  }, found, red, &count_s);
+    most = fmaxf(most, x);
+  }
+  // where there are lists enough, one of their largest logits bounds the places
+  const float bound = lists >= p.a.width ? score_bound(most, p.a.width, widest, red) : -FLT_MAX;
+  const auto each = [&](float least, const auto& f) {
+    __syncthreads();                              // `open` and its count are read
+    if (t == 0) n_open = 0;
+    __syncthreads();
+    for (int64_t l = t; l < lists; l += kJoinThreads) {
+      if (!((few ? list_top[l] : score_of_list(l)) >= least)) continue;
+      const int at = atomicAdd(&n_open, 1);
+      if (at < kLists) open[at] = static_cast<int>(l);
+    }
+    __syncthreads();
+    const bool known = n_open <= kLists;          // else all of them are gone through
+    const int64_t n_lists = known ? n_open : lists;
+    for (int64_t i = warp; i < n_lists; i += kJoinThreads / kWarp) {
+      const int64_t l = known ? open[i] : i;
+      const int row = static_cast<int>(l / chunks);
+      const float offset = state[row].offset;
+      const int n = offset == -INFINITY ? 0 : few ? list_count[l] : p.parts[s0 * chunks + l].count;
+      const Entry* entries = p.entries + (s0 * chunks + l) * p.cap;
+#pragma unroll 4
+      for (int j = lane; j < n; j += kWarp) f(row, entries[j].token, entries[j].logit, offset);
+    }
+  };
+  select_of(p, s0, state, widest, bound, each, found, red, &count_s);
 }
 
 // Everything of a group in one CTA: its rows stay in L1 between the passes.
 template <int DT>
 __global__ void __launch_bounds__(kJoinThreads) beam_small_kernel(const __grid_constant__ Params p) {
   __shared__ Candidate found[kFinal];
+  __shared__ RowState here[kRowsHere];
   __shared__ uint32_t red[2 * kJoinThreads / kWarp];
   __shared__ int count_s;
-  const int t = threadIdx.x, lane = t % kWarp, warp = t / kWarp, vocab = p.a.vocab;
+  const int t = threadIdx.x, lane = t % kWarp, warp = t / kWarp, vocab = static_cast<int>(p.a.vocab);
   pdl_wait();
   pdl_trigger();
   int64_t s0, s1;
   group_rows(p, blockIdx.x, s0, s1);
-  const auto logit_of = [&](int64_t row, int e) {
-    const float x = load_element<DT>(p.a.logits, row * p.a.ld + e);
-    return p.a.allowed && !p.a.allowed[row * p.a.ld_allowed + e] ? -INFINITY : x;
-  };
-  float widest = 0.f;
-  for (int64_t row = s0 + warp; row < s1; row += kJoinThreads / kWarp) {
-    float top = -INFINITY;
-    for (int e = lane; e < vocab; e += kWarp) top = fmaxf(top, logit_of(row, e));
-    top = of_key(__reduce_max_sync(0xffffffffu, key_of(top)));
-    const float base = top == -INFINITY ? 0.f : top;
-    double sum = 0.0;
-    for (int e0 = lane; e0 < vocab; e0 += 32 * kWarp) {
-      float part = 0.f;
-      for (int e = e0; e < min(vocab, e0 + 32 * kWarp); e += kWarp) part += exp_from(logit_of(row, e), base);
-      sum += part;
+  RowState* state = s1 - s0 <= kRowsHere ? here : p.rows + s0;
+  // eight logits of a row, kWarp apart
+  const auto load8 = [&](float (&x)[8], int64_t row, int first) {
+    uint8_t may[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = first + i * kWarp;
+      x[i] = e < vocab ? load_element<DT>(p.a.logits, row * p.a.ld + e) : -INFINITY;
+      may[i] = p.a.allowed && e < vocab ? p.a.allowed[row * p.a.ld_allowed + e] : 1;
     }
 #pragma unroll
-    for (int d = kWarp / 2; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    RowState s;
-    if (row_state(p, row, top, sum, s) && lane == 0) flag(p.a.err, DLRM_ERRBIT_INVALID_ARG);
-    if (lane == 0) p.rows[row] = s;
-    if (s.offset != -INFINITY) widest = fmaxf(widest, fabsf(s.offset));
+    for (int i = 0; i < 8; ++i) x[i] = may[i] ? x[i] : -INFINITY;
+  };
+  for (int64_t row = s0 + warp; row < s1; row += kJoinThreads / kWarp) {
+    float x[8], top = -INFINITY;
+    for (int e = lane; e < vocab; e += 8 * kWarp) {
+      load8(x, row, e);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, x[i]);
+    }
+    top = of_key(__reduce_max_sync(0xffffffffu, key_of(top)));
+    const float ref = top == -INFINITY ? 0.f : top;
+    Sum sum{0.f, 0.f};
+    for (int e = lane; e < vocab; e += 8 * kWarp) {
+      if (vocab > 8 * kWarp) load8(x, row, e);    // (else they are there)
+      float part = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) part += exp_from(x[i], ref);
+      sum.add(part);
+    }
+    sum = warp_sum(sum);
+    if (lane == 0) state[row - s0] = RowState{sum, top, 0};
+  }
+  __syncthreads();
+  float widest = 0.f;
+  for (int64_t row = t; row < s1 - s0; row += kJoinThreads) {
+    RowState s = state[row];
+    widest = fmaxf(widest, row_state(p, s0 + row, s));
+    state[row] = s;
   }
   widest = widest_of(widest, red);
   // a warp takes 256 tokens of a row at a time
   const int pieces = (vocab + 255) / 256;
   const int64_t all = (s1 - s0) * pieces;
-  select_of(p, blockIdx.x, widest, [&](const auto& f) {
+  const auto each = [&](float, const auto& f) {
     for (int64_t u = warp; u < all; u += kJoinThreads / kWarp) {
-      const int row = static_cast<int>(s0 + u / pieces), first = static_cast<int>(u % pieces) * 256 + lane;
-      const float offset = p.rows[row].offset;
+      const int row = static_cast<int>(u / pieces), first = static_cast<int>(u % pieces) * 256 + lane;
+      const float offset = state[row].offset;
       if (offset == -INFINITY) continue;
+      float x[8];
+      load8(x, s0 + row, first);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int token = first + i * kWarp;
-        const float x = token < vocab ? logit_of(row, token) : -INFINITY;
-        if (x > -INFINITY) f(row, token, x, offset);
-      }
+      for (int i = 0; i < 8; ++i)
+        if (x[i] > -INFINITY) f(row, first + i * kWarp, x[i], offset);
     }
-  }, found, red, &count_s);
+  };
+  select_of(p, s0, state, widest, -FLT_MAX, each, found, red, &count_s);
 }
 
 // ------------------------------------------------------------------ launches
@@ -667,9 +903,10 @@ __global__ void __launch_bounds__(kJoinThreads) beam_small_kernel(const __grid_c
 // One launch for groups of at most this many logits, on average.
 constexpr int64_t kSmallGroup = 32768;
 constexpr int kSmallVocab = 4096;
-// CTAs of the scan that chunks are made for: rows are cut until there are so many.
+// CTAs of the scan that chunks are made for, two for each place that the SMs have; and a
+// list more for each two places of the result, which gives the join its bound.
 constexpr int64_t kScanCtas = 152 * 8 * 2;
-constexpr int kMostTiles = 8;                    // of a chunk
+constexpr int kLeastTiles = 2, kMostTiles = 16;  // of a chunk
 
 struct Plan {
   bool small;
@@ -678,13 +915,15 @@ struct Plan {
 };
 Plan plan_of(const dlrm_beam_select_t& a) {
   Plan s{};
-  s.bytes = round_up(a.rows * static_cast<int64_t>(sizeof(RowState)), 16);
   s.small = a.rows == 0 || (a.vocab <= kSmallVocab && a.rows * a.vocab <= kSmallGroup * a.groups);
+  if (s.small && a.rows <= kRowsHere) return s;
+  s.bytes = a.rows * static_cast<int64_t>(sizeof(RowState));
   if (s.small) return s;
   const int64_t tile = kScanThreads * kVectors * (a.dtype == DLRM_DTYPE_FP32 ? 4 : 8);
   const int64_t tiles = (a.vocab + tile - 1) / tile;
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(tiles, kScanCtas / std::max<int64_t>(a.rows, 1)));
-  s.tiles = static_cast<int>(std::min<int64_t>((tiles + want - 1) / want, kMostTiles));
+  const int64_t each = (a.rows + a.groups - 1) / std::max(a.groups, 1);   // rows of a group
+  const int64_t want = std::max((kScanCtas + a.rows - 1) / a.rows, (3 * a.width / 2 + each - 1) / each);
+  s.tiles = static_cast<int>(std::max<int64_t>(kLeastTiles, std::min<int64_t>(tiles / want, kMostTiles)));
   s.chunks = static_cast<int>((tiles + s.tiles - 1) / s.tiles);
   s.cap = 8 * a.width + 256;
   s.parts = s.bytes;

@@ -260,8 +260,9 @@ dlrm_status_t beam_select(const dlrm_beam_select_t* a, void* stream) {
       !aligned_to(a->out_rows, 4) || !a->out_tokens || !aligned_to(a->out_tokens, 4) || !aligned_to(a->err, 4) ||
       !aligned_to(a->scores, 4))
     return DLRM_ERR_INVALID_ARG;
-  if (a->rows > 0 && (!a->logits || !aligned_to(a->logits, dlrm::dtype_bytes(a->dtype)) || !a->work ||
-                      !aligned_to(a->work, 16) || a->work_bytes < dlrm::beam_select_work(*a)))
+  const int64_t work = dlrm::beam_select_work(*a);
+  if ((a->rows > 0 && (!a->logits || !aligned_to(a->logits, dlrm::dtype_bytes(a->dtype)))) ||
+      (work > 0 && (!a->work || !aligned_to(a->work, 16) || a->work_bytes < work)))
     return DLRM_ERR_INVALID_ARG;
   return status_of(dlrm::launch_beam_select(*a, static_cast<cudaStream_t>(stream)));
 }

@@ -20,7 +20,7 @@ namespace prefix {
 
 namespace {
 
-constexpr int kPlanThreads = 256;
+constexpr int kPlanThreads = 512;
 constexpr int kHere = 256;                       // requests of a group that shared memory holds
 
 // Exclusive prefix sum over the CTA; total in every thread.
