@@ -409,37 +409,78 @@ __device__ __forceinline__ int tighten(Entry* list, int n, int k) {
   return kept;
 }
 
-// What bounds it: HBM, and the instructions around one exponential a logit (about four).
-// The list holds vectors by their largest element; their elements are looked at
-// once more at the end.
+// A lower bound of the k-th largest of a warp's keys, N a lane, as block_bound.
+template <int N>
+__device__ __forceinline__ uint32_t warp_bound(const uint32_t (&key)[N], int k) {
+  const uint32_t none = key_of(-INFINITY);
+  uint32_t hi = none, lo = 0xffffffffu;
+  int there = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    hi = max(hi, key[i]);
+    lo = key[i] > none ? min(lo, key[i]) : lo;
+    there += __popc(__ballot_sync(0xffffffffu, key[i] > none));
+  }
+  if (there < k) return none;
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  if (hi == lo) return hi;
+  const int first = 31 - __clz(hi ^ lo);
+  uint32_t bound = first == 31 ? 0u : hi & (0xffffffffu << (first + 1));
+  for (int bit = first; bit >= 0 && there > k + k / 8; --bit) {
+    const uint32_t trial = bound | (1u << bit);
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) n += __popc(__ballot_sync(0xffffffffu, key[i] >= trial));
+    if (n >= k) {
+      bound = trial;
+      there = n;
+    }
+  }
+  return bound;
+}
+
+// What bounds it: the instructions around one exponential a logit (about six), then HBM.
+// Warps meet twice, after the first tile and at the end: each has a list of its own, of vectors
+// by their largest element; their elements are looked at once more at the end.
 template <int DT, bool MASK, bool ALIGNED>
 __global__ void __launch_bounds__(kScanThreads, 8) beam_scan_kernel(const __grid_constant__ Params p) {
   constexpr int kVec = Row<DT>::kVec, kWarps = kScanThreads / kWarp;
   constexpr int kTile = kScanThreads * kVec * kVectors;
   extern __shared__ __align__(16) unsigned char smem[];
-  Entry* list = reinterpret_cast<Entry*>(smem);  // of vectors: largest logit, first token
   __shared__ uint32_t red[2 * kWarps];
   __shared__ Sum sums[kWarps];
-  __shared__ int count_s, other_s;
+  __shared__ int counts[kWarps], other_s;
   const int t = threadIdx.x, lane = t % kWarp, warp = t / kWarp;
   const int64_t row = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks, vocab = p.a.vocab;
   const int64_t e0 = chunk * p.tiles * kTile, e1 = min(vocab, e0 + static_cast<int64_t>(p.tiles) * kTile);
   const char* logits = static_cast<const char*>(p.a.logits) + row * p.a.ld * Row<DT>::kBytes;
   const uint8_t* allowed = MASK ? p.a.allowed + row * p.a.ld_allowed : nullptr;
-  const int width = p.a.width;
-  if (t == 0) count_s = other_s = 0;
+  const int width = p.a.width, room = p.cap / kWarps;   // of a warp's list
+  Entry* every = reinterpret_cast<Entry*>(smem);  // largest logit and first token of vectors
+  Entry* list = every + warp * room;
+  if (t == 0) other_s = 0;
   pdl_wait();
   pdl_trigger();
 
   uint4 raw[kVectors];
   uint2 may[kVectors];
   auto load = [&](int64_t at) {
+    if (at + kTile <= e1) {
 #pragma unroll
-    for (int v = 0; v < kVectors; ++v) {
-      const int64_t e = at + (v * kScanThreads + t) * kVec;
-      if (e < e1) {
+      for (int v = 0; v < kVectors; ++v) {
+        const int64_t e = at + (v * kScanThreads + t) * kVec;
         raw[v] = load_vector<DT, ALIGNED>(logits, e, vocab);
         if (MASK) may[v] = load_allowed<kVec, ALIGNED>(allowed, e, vocab);
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < kVectors; ++v) {
+        const int64_t e = at + (v * kScanThreads + t) * kVec;
+        if (e < e1) {
+          raw[v] = load_vector<DT, ALIGNED>(logits, e, vocab);
+          if (MASK) may[v] = load_allowed<kVec, ALIGNED>(allowed, e, vocab);
+        }
       }
     }
   };
@@ -447,7 +488,8 @@ __global__ void __launch_bounds__(kScanThreads, 8) beam_scan_kernel(const __grid
   float ref = -INFINITY;
   Sum sum{0.f, 0.f};
   float bound = -FLT_MAX, peak = -INFINITY;
-  bool many = false;                              // the list overflowed
+  int count = 0;                                  // of the warp's list
+  bool many = false;                              // it overflowed
   for (int64_t at = e0; at < e1; at += kTile) {
     uint4 now[kVectors];
     float top[kVectors];
@@ -470,25 +512,35 @@ __global__ void __launch_bounds__(kScanThreads, 8) beam_scan_kernel(const __grid
     peak = fmaxf(peak, most);
     static_assert(kVectors == 4, "largest of a thread");
     if (at == e0) {
-      // the bound; and one reference for all threads, so that sums need no factors
+      // every warp has its share of `width` maxima at the least of the warps' bounds or
+      // above; and one reference for all threads, so that sums need no factors
+      constexpr int kShare = kWarps;
+      const int share = (width + kShare - 1) / kShare;
       uint32_t key;
       if (width <= kSubsets) {
         const uint32_t mine[1] = {key_of(most)};
-        key = block_bound<kScanThreads>(mine, width, red);
+        key = warp_bound(mine, share);
       } else {
         uint32_t mine[kVectors];
 #pragma unroll
         for (int v = 0; v < kVectors; ++v) mine[v] = key_of(top[v]);
-        key = block_bound<kScanThreads>(mine, width, red);
+        key = warp_bound(mine, share);
       }
-      bound = bound_of(key);
       const uint32_t hi = __reduce_max_sync(0xffffffffu, key_of(most));
-      if (lane == 0) red[warp] = hi;
+      if (lane == 0) {
+        red[warp] = hi;
+        red[kWarps + warp] = key;
+      }
       __syncthreads();
       uint32_t all = red[0];
+      key = red[kWarps];
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) all = max(all, red[w]);
+      for (int w = 1; w < kWarps; ++w) {
+        all = max(all, red[w]);
+        key = min(key, red[kWarps + w]);
+      }
       ref = of_key(all);
+      bound = bound_of(key);
     } else if (most > ref + 20.f) {
       sum = moved(sum, ref, most);
       ref = most;
@@ -516,57 +568,78 @@ __global__ void __launch_bounds__(kScanThreads, 8) beam_scan_kernel(const __grid
     }
     const float2 y = add2(add2(part[0], part[1]), add2(part[2], part[3]));
     sum.add(y.x + y.y);
-    if (!many) {
+    // ---- the warp's list
+    unsigned who[kVectors];
+    int n = 0;
 #pragma unroll
-      for (int v = 0; v < kVectors; ++v)
-        if (top[v] >= bound) {
-          const int place = atomicAdd(&count_s, 1);
-          if (place < p.cap) list[place] = Entry{top[v], static_cast<int>(at + (v * kScanThreads + t) * kVec)};
-        }
+    for (int v = 0; v < kVectors; ++v) {
+      who[v] = __ballot_sync(0xffffffffu, top[v] >= bound);
+      n += __popc(who[v]);
     }
-    __syncthreads();
-    const int count = count_s;
-    many |= count > p.cap;
-    if (!many && count > (at + kTile < e1 ? p.cap / 2 : width + width / 4 + 8)) {
-      __syncthreads();                            // `count_s` is read
-      if (warp == 0) {
-        const int n = tighten(list, count, width);
-        if (lane == 0) count_s = n;
+    if (n > 0) {
+      if (count + n > room && !many) {
+        // what is not among the warp's largest is not among the chunk's
+        __syncwarp();
+        if (count > width) count = tighten(list, count, width);
+        many = count + n > room;
       }
-      __syncthreads();
-      const int n = count_s;
-      many |= n > p.cap / 4;                      // ties: the exact way, at the end
-      // the least that is left
-      float least = INFINITY;
-      for (int i = lane; i < n; i += kWarp) least = fminf(least, list[i].logit);
-      bound = of_key(__reduce_min_sync(0xffffffffu, key_of(least)));
+      if (!many) {
+#pragma unroll
+        for (int v = 0; v < kVectors; ++v) {
+          if (top[v] >= bound)
+            list[count + __popc(who[v] & ((1u << lane) - 1))] =
+                Entry{top[v], static_cast<int>(at + (v * kScanThreads + t) * kVec)};
+          count += __popc(who[v]);
+        }
+      }
     }
-    __syncthreads();
   }
-  // ---- the chunk's sum
+  // ---- the chunk's sum, and the warps' lists as one
   const uint32_t hi = __reduce_max_sync(0xffffffffu, key_of(ref)), most = __reduce_max_sync(0xffffffffu, key_of(peak));
+  __syncthreads();                                // (of one tile: `red` is read)
   if (lane == 0) {
     red[warp] = hi;
     red[kWarps + warp] = most;
+    counts[warp] = many ? -1 : count;
   }
   __syncthreads();
   uint32_t all = red[0], highest = red[kWarps];
+  int before = 0, total = 0;
+  many = false;
 #pragma unroll
-  for (int w = 1; w < kWarps; ++w) {
+  for (int w = 0; w < kWarps; ++w) {
     all = max(all, red[w]);
     highest = max(highest, red[kWarps + w]);
+    many |= counts[w] < 0;
+    before += w < warp ? counts[w] : 0;
+    total += counts[w];
   }
   const float common = of_key(all);
-  sum = moved(sum, ref, common);
-  sum = warp_sum(sum);
+  sum = warp_sum(moved(sum, ref, common));
   if (lane == 0) sums[warp] = sum;
+  Entry* joined = every + p.cap;
+  if (!many)
+    for (int i = lane; i < count; i += kWarp) joined[before + i] = list[i];
+  __syncthreads();
+  if (!many && total > width + width / 4 + 8) {
+    if (warp == 0) {
+      const int n = tighten(joined, total, width);
+      if (lane == 0) counts[0] = n;
+    }
+    __syncthreads();
+    total = counts[0];
+    // the least that is left
+    float least = INFINITY;
+    for (int i = lane; i < total; i += kWarp) least = fminf(least, joined[i].logit);
+    bound = of_key(__reduce_min_sync(0xffffffffu, key_of(least)));
+  }
   // ---- the list's elements
   Entry* out = p.entries + static_cast<int64_t>(blockIdx.x) * p.cap;
-  int count = 0;
+  int written = 0;
   if (!many) {
-    const int n = count_s * kVec;
+    const int n = total * kVec;
     for (int i = t; i < n; i += kScanThreads) {
-      const int e = list[i / kVec].token + i % kVec;
+      const int e = joined[i / kVec].token + i % kVec;
       if (e >= e1 || (MASK && !allowed[e])) continue;
       const float x = load_element<DT>(logits, e);
       if (!(x >= bound)) continue;
@@ -574,19 +647,19 @@ __global__ void __launch_bounds__(kScanThreads, 8) beam_scan_kernel(const __grid
       if (place < p.cap) out[place] = Entry{x, e};
     }
     __syncthreads();
-    count = other_s;
-    many = count > p.cap;
+    written = other_s;
+    many = written > p.cap;                       // ties
     __syncthreads();
   }
-  if (many) count = exact_chunk<DT>(p, row, e0, e1, out, &other_s);
+  if (many) written = exact_chunk<DT>(p, row, e0, e1, out, &other_s);
   if (t == 0) {
-    Sum total = sums[0];
+    Sum total_sum = sums[0];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) {
-      total.rest += sums[w].rest;
-      total.add(sums[w].sum);
+      total_sum.rest += sums[w].rest;
+      total_sum.add(sums[w].sum);
     }
-    p.parts[blockIdx.x] = Part{total, common, of_key(highest), count, 0};
+    p.parts[blockIdx.x] = Part{total_sum, common, of_key(highest), written, 0};
   }
 }
 
@@ -935,7 +1008,7 @@ Plan plan_of(const dlrm_beam_select_t& a) {
 template <int DT, bool MASK>
 cudaError_t launch_scan(const Params& p, bool aligned, cudaStream_t stream) {
   const unsigned grid = static_cast<unsigned>(p.a.rows * p.chunks);
-  const size_t smem = p.cap * sizeof(Entry);
+  const size_t smem = 2 * p.cap * sizeof(Entry);
   return aligned ? launch_pdl(beam_scan_kernel<DT, MASK, true>, dim3(grid), dim3(kScanThreads), smem, stream, p)
                  : launch_pdl(beam_scan_kernel<DT, MASK, false>, dim3(grid), dim3(kScanThreads), smem, stream, p);
 }
