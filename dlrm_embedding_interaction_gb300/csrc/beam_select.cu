@@ -28,14 +28,15 @@ namespace dlrm {
 namespace {
 
 constexpr int kScanThreads = 128;
-constexpr int kJoinThreads = 512;
+constexpr int kJoinThreads = 1024;
+constexpr int kSmallThreads = 512;
 constexpr int kVectors = 4;                      // 16-byte vectors of a thread and tile
 constexpr int kSubsets = 64;                     // widths up to here: one subset a thread will do
 constexpr int kFinal = 2048;                     // candidates that are ranked at most
 constexpr int kLists = 1024;                     // lists of a group that shared memory knows
 constexpr int kRowsHere = 256;                   // rows of a group whose states lie in shared memory
-static_assert(kSubsets <= kScanThreads && kBeamMaxWidth <= kScanThreads * kVectors && kBeamMaxWidth <= kJoinThreads &&
-                  kBeamMaxWidth <= kFinal, "a subset for each place");
+static_assert(kSubsets <= kScanThreads && kBeamMaxWidth <= kScanThreads * kVectors && kBeamMaxWidth <= kSmallThreads &&
+                  kSmallThreads <= kJoinThreads && kBeamMaxWidth <= kFinal, "a subset for each place");
 
 // A sum in two floats: the rounding errors of `sum` in `rest`.
 struct Sum {
@@ -211,7 +212,7 @@ __device__ __forceinline__ uint32_t block_bound(const uint32_t (&key)[N], int k,
 
 // ------------------------------------------------------------------ rows as loaded
 
-// kVec consecutive logits (16 bytes) from element e0 of a row on, as words. A row may begin
+// Consecutive logits, 16 bytes from `at` on, as words; the row ends at `end`. A row may begin
 // at any element: then two aligned vectors are shifted together. Aligned vectors that
 // hold an element of the row are read whole.
 template <int DT>
@@ -220,15 +221,19 @@ struct Row {
   static constexpr int kBytes = DT == DLRM_DTYPE_FP32 ? 4 : 2;
 };
 
-template <int DT, bool ALIGNED>
-__device__ __forceinline__ uint4 load_vector(const char* row, int64_t e0, int64_t n) {
-  const char* at = row + e0 * Row<DT>::kBytes;
+// NEXT: the next lane loads what follows, as in a tile of which the row holds everything.
+template <bool ALIGNED, bool NEXT>
+__device__ __forceinline__ uint4 load_vector(const char* at, const char* end) {
   if (ALIGNED) return __ldg(reinterpret_cast<const uint4*>(at));
   const int off = static_cast<int>(reinterpret_cast<uintptr_t>(at) & 15);
   const uint4* base = reinterpret_cast<const uint4*>(at - off);
   const uint4 a = __ldg(base);
   uint4 b = make_uint4(0, 0, 0, 0);
-  if (reinterpret_cast<const char*>(base + 1) < row + n * Row<DT>::kBytes) b = __ldg(base + 1);
+  if (NEXT) {
+    b = make_uint4(__shfl_down_sync(0xffffffffu, a.x, 1), __shfl_down_sync(0xffffffffu, a.y, 1),
+                   __shfl_down_sync(0xffffffffu, a.z, 1), __shfl_down_sync(0xffffffffu, a.w, 1));
+  }
+  if ((!NEXT || threadIdx.x % kWarp == kWarp - 1) && reinterpret_cast<const char*>(base + 1) < end) b = __ldg(base + 1);
   uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   if (off & 8) {
 #pragma unroll
@@ -243,15 +248,16 @@ __device__ __forceinline__ uint4 load_vector(const char* row, int64_t e0, int64_
                     __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
 }
 // The same of the bytes that allow tokens: kVec of them.
-template <int VEC, bool ALIGNED>
-__device__ __forceinline__ uint2 load_allowed(const uint8_t* row, int64_t e0, int64_t n) {
-  const uint8_t* at = row + e0;
+template <int VEC, bool ALIGNED, bool NEXT>
+__device__ __forceinline__ uint2 load_allowed(const uint8_t* at, const uint8_t* end) {
   if (VEC == 4) {
     if (ALIGNED) return make_uint2(__ldg(reinterpret_cast<const uint32_t*>(at)), 0);
     const int off = static_cast<int>(reinterpret_cast<uintptr_t>(at) & 3);
     const uint32_t* base = reinterpret_cast<const uint32_t*>(at - off);
     const uint32_t a = __ldg(base);
-    const uint32_t b = reinterpret_cast<const uint8_t*>(base + 1) < row + n ? __ldg(base + 1) : 0;
+    uint32_t b = NEXT ? __shfl_down_sync(0xffffffffu, a, 1) : 0;
+    if ((!NEXT || threadIdx.x % kWarp == kWarp - 1) && reinterpret_cast<const uint8_t*>(base + 1) < end)
+      b = __ldg(base + 1);
     return make_uint2(__funnelshift_r(a, b, off * 8), 0);
   }
   if (ALIGNED) return __ldg(reinterpret_cast<const uint2*>(at));
@@ -259,7 +265,9 @@ __device__ __forceinline__ uint2 load_allowed(const uint8_t* row, int64_t e0, in
   const uint2* base = reinterpret_cast<const uint2*>(at - off);
   const uint2 a = __ldg(base);
   uint2 b = make_uint2(0, 0);
-  if (reinterpret_cast<const uint8_t*>(base + 1) < row + n) b = __ldg(base + 1);
+  if (NEXT) b = make_uint2(__shfl_down_sync(0xffffffffu, a.x, 1), __shfl_down_sync(0xffffffffu, a.y, 1));
+  if ((!NEXT || threadIdx.x % kWarp == kWarp - 1) && reinterpret_cast<const uint8_t*>(base + 1) < end)
+    b = __ldg(base + 1);
   uint32_t w[4] = {a.x, a.y, b.x, b.y};
   if (off & 4) {
 #pragma unroll
@@ -427,7 +435,7 @@ __device__ __forceinline__ uint32_t warp_bound(const uint32_t (&key)[N], int k) 
   if (hi == lo) return hi;
   const int first = 31 - __clz(hi ^ lo);
   uint32_t bound = first == 31 ? 0u : hi & (0xffffffffu << (first + 1));
-  for (int bit = first; bit >= 0 && there > k + k / 8; --bit) {
+  for (int bit = first; bit >= 0 && there > k + k / 4 + 1; --bit) {
     const uint32_t trial = bound | (1u << bit);
     int n = 0;
 #pragma unroll
@@ -444,7 +452,7 @@ __device__ __forceinline__ uint32_t warp_bound(const uint32_t (&key)[N], int k) 
 // Warps meet twice, after the first tile and at the end: each has a list of its own, of vectors
 // by their largest element; their elements are looked at once more at the end.
 template <int DT, bool MASK, bool ALIGNED>
-__global__ void __launch_bounds__(kScanThreads, 8) beam_scan_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kScanThreads, MASK || !ALIGNED ? 6 : 8) beam_scan_kernel(const __grid_constant__ Params p) {
   constexpr int kVec = Row<DT>::kVec, kWarps = kScanThreads / kWarp;
   constexpr int kTile = kScanThreads * kVec * kVectors;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -457,40 +465,45 @@ __global__ void __launch_bounds__(kScanThreads, 8) beam_scan_kernel(const __grid
   const char* logits = static_cast<const char*>(p.a.logits) + row * p.a.ld * Row<DT>::kBytes;
   const uint8_t* allowed = MASK ? p.a.allowed + row * p.a.ld_allowed : nullptr;
   const int width = p.a.width, room = p.cap / kWarps;   // of a warp's list
-  Entry* every = reinterpret_cast<Entry*>(smem);  // largest logit and first token of vectors
+  Entry* every = reinterpret_cast<Entry*>(smem);  // largest logit, first token (of the chunk's) of vectors
   Entry* list = every + warp * room;
   if (t == 0) other_s = 0;
   pdl_wait();
   pdl_trigger();
 
+  const int n = static_cast<int>(e1 - e0);        // of the chunk
+  const char* at_logits = logits + (e0 + t * kVec) * Row<DT>::kBytes;
+  const uint8_t* at_allowed = MASK ? allowed + e0 + t * kVec : nullptr;
+  const char* end_logits = logits + vocab * Row<DT>::kBytes;
+  const uint8_t* end_allowed = MASK ? allowed + vocab : nullptr;
   uint4 raw[kVectors];
   uint2 may[kVectors];
-  auto load = [&](int64_t at) {
-    if (at + kTile <= e1) {
+  auto load = [&](int at) {
+    if (at + kTile <= n) {
 #pragma unroll
       for (int v = 0; v < kVectors; ++v) {
-        const int64_t e = at + (v * kScanThreads + t) * kVec;
-        raw[v] = load_vector<DT, ALIGNED>(logits, e, vocab);
-        if (MASK) may[v] = load_allowed<kVec, ALIGNED>(allowed, e, vocab);
+        raw[v] = load_vector<ALIGNED, true>(at_logits + v * (kScanThreads * 16), end_logits);
+        if (MASK) may[v] = load_allowed<kVec, ALIGNED, true>(at_allowed + v * (kScanThreads * kVec), end_allowed);
       }
     } else {
 #pragma unroll
       for (int v = 0; v < kVectors; ++v) {
-        const int64_t e = at + (v * kScanThreads + t) * kVec;
-        if (e < e1) {
-          raw[v] = load_vector<DT, ALIGNED>(logits, e, vocab);
-          if (MASK) may[v] = load_allowed<kVec, ALIGNED>(allowed, e, vocab);
-        }
+        if (at + (v * kScanThreads + t) * kVec >= n) continue;
+        raw[v] = load_vector<ALIGNED, false>(at_logits + v * (kScanThreads * 16), end_logits);
+        if (MASK) may[v] = load_allowed<kVec, ALIGNED, false>(at_allowed + v * (kScanThreads * kVec), end_allowed);
       }
     }
+    at_logits += kTile * Row<DT>::kBytes;
+    if (MASK) at_allowed += kTile;
   };
-  load(e0);
+  load(0);
   float ref = -INFINITY;
   Sum sum{0.f, 0.f};
   float bound = -FLT_MAX, peak = -INFINITY;
   int count = 0;                                  // of the warp's list
   bool many = false;                              // it overflowed
-  for (int64_t at = e0; at < e1; at += kTile) {
+#pragma unroll 1
+  for (int at = 0; at < n; at += kTile) {
     uint4 now[kVectors];
     float top[kVectors];
 #pragma unroll
@@ -498,20 +511,20 @@ __global__ void __launch_bounds__(kScanThreads, 8) beam_scan_kernel(const __grid
       now[v] = raw[v];
       if (MASK) hide<DT>(now[v], may[v]);
     }
-    if (at + kTile > e1) {
+    if (at + kTile > n) {
 #pragma unroll
       for (int v = 0; v < kVectors; ++v) {
-        const int64_t left = e1 - (at + (v * kScanThreads + t) * kVec);
-        if (left < kVec) hide<DT>(now[v], first_bytes(static_cast<int>(max(left, int64_t(0)))));
+        const int left = n - (at + (v * kScanThreads + t) * kVec);
+        if (left < kVec) hide<DT>(now[v], first_bytes(left));
       }
     }
 #pragma unroll
     for (int v = 0; v < kVectors; ++v) top[v] = largest<DT>(now[v]);
-    if (at + kTile < e1) load(at + kTile);
+    if (at + kTile < n) load(at + kTile);
     const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
     peak = fmaxf(peak, most);
     static_assert(kVectors == 4, "largest of a thread");
-    if (at == e0) {
+    if (at == 0) {
       // every warp has its share of `width` maxima at the least of the warps' bounds or
       // above; and one reference for all threads, so that sums need no factors
       constexpr int kShare = kWarps;
@@ -570,31 +583,38 @@ __global__ void __launch_bounds__(kScanThreads, 8) beam_scan_kernel(const __grid
     sum.add(y.x + y.y);
     // ---- the warp's list
     unsigned who[kVectors];
-    int n = 0;
+    int more = 0;
 #pragma unroll
     for (int v = 0; v < kVectors; ++v) {
       who[v] = __ballot_sync(0xffffffffu, top[v] >= bound);
-      n += __popc(who[v]);
+      more += __popc(who[v]);
     }
-    if (n > 0) {
-      if (count + n > room && !many) {
+    if (more > 0) {
+      if (count + more > room && !many) {
         // what is not among the warp's largest is not among the chunk's
         __syncwarp();
         if (count > width) count = tighten(list, count, width);
-        many = count + n > room;
+        many = count + more > room;
       }
       if (!many) {
 #pragma unroll
         for (int v = 0; v < kVectors; ++v) {
           if (top[v] >= bound)
             list[count + __popc(who[v] & ((1u << lane) - 1))] =
-                Entry{top[v], static_cast<int>(at + (v * kScanThreads + t) * kVec)};
+                Entry{top[v], at + (v * kScanThreads + t) * kVec};
           count += __popc(who[v]);
         }
       }
     }
   }
   // ---- the chunk's sum, and the warps' lists as one
+  constexpr int kOwn = 8;                         // entries of a thread
+  static_assert(kBeamMaxWidth <= kOwn * kWarp, "a warp's largest");
+  if (count > kOwn * kWarp) {
+    __syncwarp();
+    count = tighten(list, count, width);
+    many |= count > kOwn * kWarp;
+  }
   const uint32_t hi = __reduce_max_sync(0xffffffffu, key_of(ref)), most = __reduce_max_sync(0xffffffffu, key_of(peak));
   __syncthreads();                                // (of one tile: `red` is read)
   if (lane == 0) {
@@ -622,24 +642,33 @@ __global__ void __launch_bounds__(kScanThreads, 8) beam_scan_kernel(const __grid
     for (int i = lane; i < count; i += kWarp) joined[before + i] = list[i];
   __syncthreads();
   if (!many && total > width + width / 4 + 8) {
-    if (warp == 0) {
-      const int n = tighten(joined, total, width);
-      if (lane == 0) counts[0] = n;
+    uint32_t key[kOwn];
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i)
+      key[i] = t + i * kScanThreads < total ? key_of(joined[t + i * kScanThreads].logit) : key_of(-INFINITY);
+    bound = bound_of(block_bound<kScanThreads>(key, width, red));
+    if (t == 0) counts[0] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {              // what is left, to the front of the warps' lists
+      const bool stays = t + i * kScanThreads < total && of_key(key[i]) >= bound;
+      const unsigned who = __ballot_sync(0xffffffffu, stays);
+      int at = 0;
+      if (lane == 0 && who) at = atomicAdd(&counts[0], __popc(who));
+      at = __shfl_sync(0xffffffffu, at, 0);
+      if (stays) every[at + __popc(who & ((1u << lane) - 1))] = joined[t + i * kScanThreads];
     }
+    joined = every;
     __syncthreads();
     total = counts[0];
-    // the least that is left
-    float least = INFINITY;
-    for (int i = lane; i < total; i += kWarp) least = fminf(least, joined[i].logit);
-    bound = of_key(__reduce_min_sync(0xffffffffu, key_of(least)));
   }
   // ---- the list's elements
   Entry* out = p.entries + static_cast<int64_t>(blockIdx.x) * p.cap;
   int written = 0;
   if (!many) {
-    const int n = total * kVec;
-    for (int i = t; i < n; i += kScanThreads) {
-      const int e = joined[i / kVec].token + i % kVec;
+    const int first = static_cast<int>(e0);
+    for (int i = t; i < total * kVec; i += kScanThreads) {
+      const int e = first + joined[i / kVec].token + i % kVec;
       if (e >= e1 || (MASK && !allowed[e])) continue;
       const float x = load_element<DT>(logits, e);
       if (!(x >= bound)) continue;
@@ -698,22 +727,24 @@ __device__ __forceinline__ float row_state(const Params& p, int64_t row, RowStat
 }
 
 // Largest magnitude of the rows' offsets, in every thread.
+template <int THREADS>
 __device__ __forceinline__ float widest_of(float mine, uint32_t* red) {
   uint32_t x = __reduce_max_sync(0xffffffffu, __float_as_uint(mine));
   __syncthreads();
   if (threadIdx.x % kWarp == 0) red[threadIdx.x / kWarp] = x;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kJoinThreads / kWarp; ++w) x = max(x, red[w]);
+  for (int w = 0; w < THREADS / kWarp; ++w) x = max(x, red[w]);
   __syncthreads();
   return __uint_as_float(x);
 }
 
 // Below the k-th largest of the threads' scores by what fp32 may be off: half an ulp of
 // a score's own and an ulp of its offset's, twice.
+template <int THREADS>
 __device__ __forceinline__ float score_bound(float most, int k, float widest, uint32_t* red) {
   const uint32_t key[1] = {key_of(most)};
-  const float bound = bound_of(block_bound<kJoinThreads>(key, k, red));
+  const float bound = bound_of(block_bound<THREADS>(key, k, red));
   return bound > -FLT_MAX ? bound - (3e-7f * (fabsf(bound) + widest) + 1e-30f) : bound;
 }
 
@@ -721,7 +752,7 @@ __device__ __forceinline__ float score_bound(float most, int k, float widest, ui
 // every thread for its own, and writes the group's outputs; it may pass over what lies below
 // the bound. No place of the result lies below `bound`. Rows count from the group's first, s0,
 // whose states are `state`. Block-wide.
-template <class Each>
+template <int THREADS, class Each>
 __device__ __forceinline__ void select_of(const Params& p, int64_t s0, const RowState* state, float widest, float bound,
                                           const Each& each, Candidate* found, uint32_t* red, int* count_s) {
   const int t = threadIdx.x, width = p.a.width;
@@ -732,7 +763,7 @@ __device__ __forceinline__ void select_of(const Params& p, int64_t s0, const Row
   };
   float most = -INFINITY;
   each(bound, [&](int, int, float logit, float offset) { most = fmaxf(most, offset + logit); });
-  bound = fmaxf(bound, score_bound(most, width, widest, red));
+  bound = fmaxf(bound, score_bound<THREADS>(most, width, widest, red));
   if (t == 0) *count_s = 0;
   __syncthreads();
   each(bound, [&](int row, int token, float logit, float offset) {
@@ -782,7 +813,7 @@ __device__ __forceinline__ void select_of(const Params& p, int64_t s0, const Row
     __syncthreads();
     n = min(*count_s, kFinal);
   }
-  for (int i = t; i < n; i += kJoinThreads) {
+  for (int i = t; i < n; i += THREADS) {
     const Candidate c = found[i];
     found[i].key = key_of(score_of(c.row, __uint_as_float(static_cast<uint32_t>(c.key))));
   }
@@ -790,8 +821,8 @@ __device__ __forceinline__ void select_of(const Params& p, int64_t s0, const Row
   // ---- ranks: a candidate by several threads, where there are few
   const int64_t out = static_cast<int64_t>(blockIdx.x) * width;
   int share = 1;
-  while (2 * share <= kWarp && 2 * share * n <= kJoinThreads) share *= 2;
-  for (int i0 = 0; i0 < n; i0 += kJoinThreads / share) {
+  while (2 * share <= kWarp && 2 * share * n <= THREADS) share *= 2;
+  for (int i0 = 0; i0 < n; i0 += THREADS / share) {
     const int i = i0 + t / share;
     const Candidate c = found[min(i, n - 1)];
     const uint64_t mine = index_of(c.row, c.token);
@@ -808,7 +839,7 @@ __device__ __forceinline__ void select_of(const Params& p, int64_t s0, const Row
       p.a.out_tokens[out + rank] = c.token;
     }
   }
-  for (int i = n + t; i < width; i += kJoinThreads) {
+  for (int i = n + t; i < width; i += THREADS) {
     p.a.out_scores[out + i] = -INFINITY;
     p.a.out_rows[out + i] = -1;
     p.a.out_tokens[out + i] = -1;
@@ -859,7 +890,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_co
     widest = fmaxf(widest, row_state(p, s0 + row, s));
     state[row] = s;
   }
-  widest = widest_of(widest, red);
+  widest = widest_of<kJoinThreads>(widest, red);
   // ---- the lists, a warp each; those whose largest logit lies below the bound are passed over
   const int64_t lists = (s1 - s0) * chunks;
   const bool few = lists <= kLists;
@@ -874,7 +905,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_co
     most = fmaxf(most, x);
   }
   // where there are lists enough, one of their largest logits bounds the places
-  const float bound = lists >= p.a.width ? score_bound(most, p.a.width, widest, red) : -FLT_MAX;
+  const float bound = lists >= p.a.width ? score_bound<kJoinThreads>(most, p.a.width, widest, red) : -FLT_MAX;
   const auto each = [&](float least, const auto& f) {
     __syncthreads();                              // `open` and its count are read
     if (t == 0) n_open = 0;
@@ -897,15 +928,15 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_co
       for (int j = lane; j < n; j += kWarp) f(row, entries[j].token, entries[j].logit, offset);
     }
   };
-  select_of(p, s0, state, widest, bound, each, found, red, &count_s);
+  select_of<kJoinThreads>(p, s0, state, widest, bound, each, found, red, &count_s);
 }
 
 // Everything of a group in one CTA: its rows stay in L1 between the passes.
 template <int DT>
-__global__ void __launch_bounds__(kJoinThreads) beam_small_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kSmallThreads) beam_small_kernel(const __grid_constant__ Params p) {
   __shared__ Candidate found[kFinal];
   __shared__ RowState here[kRowsHere];
-  __shared__ uint32_t red[2 * kJoinThreads / kWarp];
+  __shared__ uint32_t red[2 * kSmallThreads / kWarp];
   __shared__ int count_s;
   const int t = threadIdx.x, lane = t % kWarp, warp = t / kWarp, vocab = static_cast<int>(p.a.vocab);
   pdl_wait();
@@ -925,7 +956,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_small_kernel(const __grid_c
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = may[i] ? x[i] : -INFINITY;
   };
-  for (int64_t row = s0 + warp; row < s1; row += kJoinThreads / kWarp) {
+  for (int64_t row = s0 + warp; row < s1; row += kSmallThreads / kWarp) {
     float x[8], top = -INFINITY;
     for (int e = lane; e < vocab; e += 8 * kWarp) {
       load8(x, row, e);
@@ -947,17 +978,17 @@ __global__ void __launch_bounds__(kJoinThreads) beam_small_kernel(const __grid_c
   }
   __syncthreads();
   float widest = 0.f;
-  for (int64_t row = t; row < s1 - s0; row += kJoinThreads) {
+  for (int64_t row = t; row < s1 - s0; row += kSmallThreads) {
     RowState s = state[row];
     widest = fmaxf(widest, row_state(p, s0 + row, s));
     state[row] = s;
   }
-  widest = widest_of(widest, red);
+  widest = widest_of<kSmallThreads>(widest, red);
   // a warp takes 256 tokens of a row at a time
   const int pieces = (vocab + 255) / 256;
   const int64_t all = (s1 - s0) * pieces;
   const auto each = [&](float, const auto& f) {
-    for (int64_t u = warp; u < all; u += kJoinThreads / kWarp) {
+    for (int64_t u = warp; u < all; u += kSmallThreads / kWarp) {
       const int row = static_cast<int>(u / pieces), first = static_cast<int>(u % pieces) * 256 + lane;
       const float offset = state[row].offset;
       if (offset == -INFINITY) continue;
@@ -968,7 +999,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_small_kernel(const __grid_c
         if (x[i] > -INFINITY) f(row, first + i * kWarp, x[i], offset);
     }
   };
-  select_of(p, s0, state, widest, -FLT_MAX, each, found, red, &count_s);
+  select_of<kSmallThreads>(p, s0, state, widest, -FLT_MAX, each, found, red, &count_s);
 }
 
 // ------------------------------------------------------------------ launches
@@ -976,9 +1007,9 @@ __global__ void __launch_bounds__(kJoinThreads) beam_small_kernel(const __grid_c
 // One launch for groups of at most this many logits, on average.
 constexpr int64_t kSmallGroup = 32768;
 constexpr int kSmallVocab = 4096;
-// CTAs of the scan that chunks are made for, two for each place that the SMs have; and a
-// list more for each two places of the result, which gives the join its bound.
-constexpr int64_t kScanCtas = 152 * 8 * 2;
+// CTAs of the scan that chunks are made for, one for each place that the SMs have (with two,
+// 32 x 32768 of 64 users 52 us against 50).
+constexpr int64_t kScanCtas = 152 * 8;
 constexpr int kLeastTiles = 2, kMostTiles = 16;  // of a chunk
 
 struct Plan {
@@ -994,8 +1025,7 @@ Plan plan_of(const dlrm_beam_select_t& a) {
   if (s.small) return s;
   const int64_t tile = kScanThreads * kVectors * (a.dtype == DLRM_DTYPE_FP32 ? 4 : 8);
   const int64_t tiles = (a.vocab + tile - 1) / tile;
-  const int64_t each = (a.rows + a.groups - 1) / std::max(a.groups, 1);   // rows of a group
-  const int64_t want = std::max((kScanCtas + a.rows - 1) / a.rows, (3 * a.width / 2 + each - 1) / each);
+  const int64_t want = (kScanCtas + a.rows - 1) / a.rows;
   s.tiles = static_cast<int>(std::max<int64_t>(kLeastTiles, std::min<int64_t>(tiles / want, kMostTiles)));
   s.chunks = static_cast<int>((tiles + s.tiles - 1) / s.tiles);
   s.cap = 8 * a.width + 256;
@@ -1016,7 +1046,7 @@ cudaError_t launch_scan(const Params& p, bool aligned, cudaStream_t stream) {
 template <int DT>
 cudaError_t launch(const Params& p, bool small, cudaStream_t stream) {
   if (small)
-    return launch_pdl(beam_small_kernel<DT>, dim3(p.a.groups), dim3(kJoinThreads), 0, stream, p);
+    return launch_pdl(beam_small_kernel<DT>, dim3(p.a.groups), dim3(kSmallThreads), 0, stream, p);
   constexpr int kVec = Row<DT>::kVec;
   const bool aligned = aligned_to(p.a.logits, 16) && (p.a.rows == 1 || p.a.ld % kVec == 0) &&
                        (!p.a.allowed || (aligned_to(p.a.allowed, kVec) && (p.a.rows == 1 || p.a.ld_allowed % kVec == 0)));
