@@ -12,6 +12,7 @@ makes belong to that stream.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import operator
@@ -23,6 +24,8 @@ from . import DlrmError, ERR_INVALID_ARG, ERR_UNSUPPORTED, _check, lib
 from .history import INT32_MAX, _dtype_code, _int32_vector, _on, _raw_stream
 
 MAX_WIDTH = 256
+_RESULTS = (torch.float32, torch.int32, torch.int32)
+_NOWHERE = contextlib.nullcontext()
 
 _VP, _I32, _I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
 
@@ -121,18 +124,12 @@ def beam_select(logits, scores, starts, width: int, *, allowed=None, err_flag=No
     need = _work_bytes(sizes)
     if need < 0:
         raise DlrmError(ERR_UNSUPPORTED, where)
-    if stream is None:
-        out = torch.empty((3, groups, width), dtype=torch.int32, device=logits.device)
+    with _NOWHERE if stream is None else _on(stream, logits.device):
+        best, parents, tokens = (torch.empty((groups, width), dtype=t, device=logits.device) for t in _RESULTS)
         work = torch.empty(need, dtype=torch.uint8, device=logits.device) if need else None
-    else:
-        with _on(stream, logits.device):
-            out = torch.empty((3, groups, width), dtype=torch.int32, device=logits.device)
-            work = torch.empty(need, dtype=torch.uint8, device=logits.device) if need else None
-    first, step = out.data_ptr(), 4 * groups * width
     args = _SELECT.pack(logits.data_ptr(), 0 if scores is None else scores.data_ptr(),
-                        0 if allowed is None else allowed.data_ptr(), starts.data_ptr(), first, first + step,
-                        first + 2 * step, 0 if err_flag is None else err_flag.data_ptr(),
+                        0 if allowed is None else allowed.data_ptr(), starts.data_ptr(), best.data_ptr(),
+                        parents.data_ptr(), tokens.data_ptr(), 0 if err_flag is None else err_flag.data_ptr(),
                         0 if work is None else work.data_ptr(), need, *sizes)
     _check(_bound().beam_select(args, queue), where)
-    best, parents, tokens = out.unbind()
-    return best.view(torch.float32), parents, tokens
+    return best, parents, tokens

@@ -868,91 +868,108 @@ __global__ void __launch_bounds__(kPlanThreads) free_small_kernel(Pool p, const 
 // pushes the pages that lost their last reference. Last pages that are not full have one
 // holder: those of slots that nobody continues are known to the plan, and are the first
 // that copies go to.
+// ONE: no more requests than threads, so that each stays in its thread's registers, and
+// everything that does not wait for the other requests is loaded before they are asked.
+template <bool ONE>
 __global__ void __launch_bounds__(kPlanThreads) reorder_plan_kernel(Pool p, const int32_t* slots,
                                                                     const int32_t* parents, int batch) {
   __shared__ int sums[kWarp + 1];
   const dlrm_history_t& h = p.h;
-  const int G = h.page_tokens, M = h.max_pages;
+  const int G = h.page_tokens, M = h.max_pages, t = threadIdx.x, T = blockDim.x;
   pdl_wait();
   pdl_trigger();
   const int nfree = min(max(*h.n_free, 0), h.n_pages);
   auto in = [&](int slot) { return slot >= 0 && slot < h.n_slots; };
-  auto length_of = [&](int slot) {
-    return static_cast<int>(min(static_cast<int64_t>(max(h.lengths[slot], 0)), static_cast<int64_t>(M) * G));
+  struct One {
+    Request r;
+    int own, part_own, part;                      // its slot; last pages, not full, of its slot and its source
+    uint32_t bad;
   };
-  // the page of a slot's last events, if it is not full
-  auto part_of = [&](int slot, int length) {
-    const int page = length % G != 0 ? h.table[static_cast<int64_t>(slot) * M + length / G] : -1;
-    return is_page(h, page) ? page : -1;
+  auto look = [&](int b) {
+    One x{{-1, -1, 0, 0, 0, 0, 0, 0}, -1, -1, -1, 0};
+    if (b >= batch) return x;
+    x.own = slots[b];
+    const int from = parents[b];
+    const int named = from >= 0 && from < batch ? slots[from] : -1;
+    if (!in(x.own)) {
+      x.bad = DLRM_ERRBIT_INDEX_OOB;
+      return x;
+    }
+    const auto length_of = [&](int slot) {
+      return static_cast<int>(min(static_cast<int64_t>(max(h.lengths[slot], 0)), static_cast<int64_t>(M) * G));
+    };
+    const auto part_of = [&](int slot, int length) {
+      const int page = length % G != 0 ? h.table[static_cast<int64_t>(slot) * M + length / G] : -1;
+      return is_page(h, page) ? page : -1;
+    };
+    x.r.slot = x.own;
+    x.r.source = from == -1 ? -1 : named;
+    if (from != -1 && !in(named)) {
+      x.bad = DLRM_ERRBIT_INDEX_OOB;              // it keeps its history
+      x.r.source = x.own;
+    }
+    x.r.count = length_of(x.own);
+    if (x.r.source >= 0) x.r.length = length_of(x.r.source);
+    x.part_own = part_of(x.own, x.r.count);
+    if (x.r.source >= 0) x.part = part_of(x.r.source, x.r.length);
+    return x;
   };
-  for (int b = threadIdx.x; b < batch; b += kPlanThreads) {
-    const int d = slots[b];
+  One mine = look(t);
+  for (int b = t; b < batch; b += T) {
+    const int d = ONE ? mine.own : slots[b];
     if (in(d)) atomicMin(&p.mark_slot[d], b);
   }
   __syncthreads();
   // of the requests that continue a slot, its own or else the first one keeps its last page
-  for (int b = threadIdx.x; b < batch; b += kPlanThreads) {
-    const int d = slots[b], from = parents[b];
-    Request r{-1, -1, 0, 0, 0, 0, 0, 0};
-    if (!in(d)) {
-      flag(h.err, DLRM_ERRBIT_INDEX_OOB);
-    } else if (__ldcg(&p.mark_slot[d]) != b) {
-      flag(h.err, DLRM_ERRBIT_INVALID_ARG);
-    } else {
-      r.slot = d;
-      int s = from == -1 ? -1 : from >= 0 && from < batch ? slots[from] : h.n_slots;
-      if (s != -1 && !in(s)) s = h.n_slots;
-      if (from != -1 && s == -1) s = h.n_slots;   // the slot of the request named is none
-      if (s == h.n_slots) {
-        flag(h.err, DLRM_ERRBIT_INDEX_OOB);
-        s = d;
-      }
-      r.source = s;
-      if (s >= 0) atomicMin(&p.mark_keep[s], s == d ? -1 : b);
+  for (int b = t; b < batch; b += T) {
+    if (!ONE) mine = look(b);
+    if (mine.own == mine.r.slot && in(mine.own) && __ldcg(&p.mark_slot[mine.own]) != b) {
+      mine.bad = DLRM_ERRBIT_INVALID_ARG;         // a slot that an earlier request has
+      mine.r.slot = -1;
     }
-    p.request[b] = r;
+    if (mine.bad) flag(h.err, mine.bad);
+    if (mine.r.slot >= 0 && mine.r.source >= 0)
+      atomicMin(&p.mark_keep[mine.r.source], mine.r.source == mine.r.slot ? -1 : b);
+    if (!ONE) p.request[b] = mine.r;
   }
   __syncthreads();
   int copies = 0, given = 0;
-  for (int b0 = 0; b0 < batch; b0 += kPlanThreads) {
-    const int b = b0 + static_cast<int>(threadIdx.x);
-    Request r{-1, -1, 0, 0, 0, 0, 0, 0};
-    int page = -1;                                // given up
-    if (b < batch) {
-      r = p.request[b];
-      if (r.slot >= 0) {
-        r.count = length_of(r.slot);
-        if (__ldcg(&p.mark_keep[r.slot]) == INT32_MAX) page = part_of(r.slot, r.count);
-        if (r.source >= 0) {
-          r.length = length_of(r.source);
-          const int me = r.source == r.slot ? -1 : b;
-          r.need = __ldcg(&p.mark_keep[r.source]) != me && part_of(r.source, r.length) >= 0;
-        }
-      }
+  for (int b0 = 0; b0 < batch; b0 += T) {
+    const int b = b0 + t;
+    if (!ONE) {
+      mine = look(b);
+      if (b < batch) mine.r = p.request[b];
     }
-    int total;
-    r.base = copies + block_exclusive(r.need, sums, total);
-    copies += total;
-    const int rank = given + block_exclusive(page >= 0 ? 1 : 0, sums, total);
-    given += total;
+    Request& r = mine.r;
+    bool gives = false;
+    if (r.slot >= 0) {
+      gives = mine.part_own >= 0 && __ldcg(&p.mark_keep[r.slot]) == INT32_MAX;
+      r.need = r.source >= 0 && mine.part >= 0 && __ldcg(&p.mark_keep[r.source]) != (r.source == r.slot ? -1 : b);
+    }
+    int total;                                    // of both counts, 16 bits each
+    const int rank = block_exclusive(r.need | (gives ? 1 << 16 : 0), sums, total);
+    static_assert(kPlanThreads < 1 << 15, "16 bits a count");
+    r.base = copies + (rank & 0xffff);
     // (as many as pages at most, whatever a broken table says)
-    if (page >= 0 && rank < h.n_pages) p.holes[rank] = page;
-    if (b < batch) p.request[b] = r;
+    if (gives && given + (rank >> 16) < h.n_pages) p.holes[given + (rank >> 16)] = mine.part_own;
+    copies += total & 0xffff;
+    given += total >> 16;
+    if (!ONE && b < batch) p.request[b] = r;
     __syncthreads();                              // `sums` before the next requests
   }
-  __syncthreads();
   given = min(given, h.n_pages);
   const bool short_of = copies - given > nfree;   // then nothing at all is done
-  for (int b = threadIdx.x; b < batch; b += kPlanThreads) {
-    const int d = slots[b];
+  for (int b = t; b < batch; b += T) {
+    const int d = ONE ? mine.own : slots[b];
     if (in(d)) {
       p.mark_slot[d] = INT32_MAX;
       p.mark_keep[d] = INT32_MAX;
     }
-    p.request[b].items = 0;
-    if (short_of) p.request[b].slot = -1;
+    Request r = ONE ? mine.r : p.request[b];
+    if (short_of) r.slot = -1;
+    p.request[b] = r;
   }
-  if (threadIdx.x == 0) {
+  if (t == 0) {
     if (short_of) flag(h.err, DLRM_ERRBIT_OOM);
     p.head[kHeadItems] = given;
     p.head[kHeadTop] = nfree;
@@ -1010,6 +1027,7 @@ constexpr int kCommitThreads = 1024;
 // write tables, a warp a request.
 __global__ void __launch_bounds__(kCommitThreads) reorder_commit_kernel(Pool p, int batch) {
   __shared__ int sums[kWarp + 1];
+  __shared__ int before[kCommitThreads];
   pdl_wait();
   pdl_trigger();
   const dlrm_history_t& h = p.h;
@@ -1027,68 +1045,41 @@ __global__ void __launch_bounds__(kCommitThreads) reorder_commit_kernel(Pool p, 
     return;
   }
   const int top = p.head[kHeadTop] - p.head[kHeadMoves];
-  auto freed = [&](int b, int i, int& page) {     // whether this position pushes its page
-    const int at = b * M + i;
-    page = p.dropped[static_cast<int64_t>(b) * M + i];
-    if (__ldcg(&p.mark_page[page]) != at) {
-      page = -1;
-      return false;
-    }
-    return __ldcg(&h.refs[page]) <= 0;
-  };
-  // requests from the last one down, a thread each; many pages of one by its warp
+  // Positions from the last one of the last request down, kCommitThreads at a time: whose they
+  // are is found among the counts of as many requests. A page is its last position's to push, and that
+  // one's mark to clear: no other position's reader takes it for its own, before or after.
   int pushed = 0;
   for (int e0 = 0; e0 < batch; e0 += kCommitThreads) {
-    const int b = batch - 1 - e0 - static_cast<int>(threadIdx.x);
-    const int items = b >= 0 ? p.request[b].items : 0;
-    int n = 0;
-    if (items <= 2)
-      for (int i = 0; i < items; ++i) {
-        int page;
-        n += freed(b, i, page);
+    const int e = e0 + static_cast<int>(threadIdx.x);
+    int all;
+    const int first = block_exclusive(e < batch ? p.request[batch - 1 - e].items : 0, sums, all);
+    __syncthreads();                              // (the one before is read)
+    before[threadIdx.x] = first;
+    __syncthreads();
+    for (int f0 = 0; f0 < all; f0 += kCommitThreads) {
+      const int f = f0 + static_cast<int>(threadIdx.x);
+      int page = -1;
+      bool push = false;
+      if (f < all) {
+        int k = 0;                                // the last request whose positions begin at or before it
+#pragma unroll
+        for (int d = kCommitThreads / 2; d > 0; d /= 2)
+          if (before[k + d] <= f) k += d;
+        const int b = batch - 1 - e0 - k;
+        const int end = k + 1 < kCommitThreads ? before[k + 1] : all;
+        const int64_t at = static_cast<int64_t>(b) * M + (end - 1 - f);
+        page = p.dropped[at];
+        if (__ldcg(&p.mark_page[page]) != at) page = -1;
+        push = page >= 0 && __ldcg(&h.refs[page]) <= 0;
       }
-    for (unsigned many = __ballot_sync(0xffffffffu, items > 2); many; many &= many - 1) {
-      const int l = __ffs(many) - 1;
-      const int of = __shfl_sync(0xffffffffu, b, l), all = __shfl_sync(0xffffffffu, items, l);
-      int c = 0;
-      for (int i0 = 0; i0 < all; i0 += kWarp) {
-        int page;
-        c += __popc(__ballot_sync(0xffffffffu, i0 + lane < all && freed(of, i0 + lane, page)));
+      int n;
+      const int q = top + pushed + block_exclusive(push ? 1 : 0, sums, n);
+      if (push) {
+        if (q < h.n_pages) h.free_pages[q] = page;
+        h.refs[page] = 0;
       }
-      if (lane == l) n = c;
-    }
-    int total;
-    const int before = pushed + block_exclusive(n, sums, total);
-    pushed += total;
-    // every thread has counted: marks may go, each by its own position's reader
-    if (items <= 2) {
-      int q = top + before;
-      for (int i = items - 1; i >= 0; --i) {
-        int page;
-        if (freed(b, i, page)) {
-          if (q < h.n_pages) h.free_pages[q] = page;
-          ++q;
-          h.refs[page] = 0;
-        }
-        if (page >= 0) p.mark_page[page] = -1;
-      }
-    }
-    for (unsigned many = __ballot_sync(0xffffffffu, items > 2); many; many &= many - 1) {
-      const int l = __ffs(many) - 1;
-      const int of = __shfl_sync(0xffffffffu, b, l), all = __shfl_sync(0xffffffffu, items, l);
-      int q = top + __shfl_sync(0xffffffffu, before, l);
-      for (int i0 = (all - 1) / kWarp * kWarp; i0 >= 0; i0 -= kWarp) {
-        int page = -1;
-        const bool push = i0 + lane < all && freed(of, i0 + lane, page);
-        const unsigned who = __ballot_sync(0xffffffffu, push);
-        if (push) {
-          const int at = q + __popc(who >> lane) - 1;   // this lane's bit among those from it on
-          if (at < h.n_pages) h.free_pages[at] = page;
-          h.refs[page] = 0;
-        }
-        if (page >= 0) p.mark_page[page] = -1;
-        q += __popc(who);
-      }
+      if (page >= 0) p.mark_page[page] = -1;
+      pushed += n;
     }
   }
   if (threadIdx.x == 0 && batch > 0) *h.n_free = min(top + pushed, h.n_pages);
@@ -1311,7 +1302,9 @@ cudaError_t launch_history_free(const dlrm_history_t& h, const int32_t* slots, i
 cudaError_t launch_history_reorder(const dlrm_history_t& h, const int32_t* slots, const int32_t* parents,
                                    int batch, cudaStream_t stream) {
   const Pool p = make_pool(h);
-  cudaError_t e = launch_pdl(reorder_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p, slots, parents, batch);
+  const int threads = batch >= kPlanThreads ? kPlanThreads : (batch + kWarp - 1) / kWarp * kWarp;
+  cudaError_t e = launch_pdl(batch <= kPlanThreads ? reorder_plan_kernel<true> : reorder_plan_kernel<false>, dim3(1),
+                             dim3(threads), 0, stream, p, slots, parents, batch);
   if (e != cudaSuccess) return e;
   const int pieces = pieces_of(h);
   // (a grid's y and z end at 65535)
