@@ -235,13 +235,13 @@ dlrm_status_t history_prefix_attention(const dlrm_history_t* h, const dlrm_atten
   if (a->batch > h->n_slots || n_groups < 0 || n_groups > h->n_slots) return DLRM_ERR_INVALID_ARG;
   if (!run || n_groups == 0) return DLRM_OK;
   if (!a->slots || !aligned_to(a->slots, 4) || !groups || !aligned_to(groups, 4)) return DLRM_ERR_INVALID_ARG;
-  // tiles of 8 rows of a kv head have space in the scratch, and work units (a block of
-  // 32 events of a tile) are counted in int32: a tile reads the shared events and
-  // those of its requests, and a request lies in a tile more than it fills
+  // tiles of 8 rows of a kv head have space in the scratch, and work (blocks of 32 events
+  // of a tile, and what a tile costs beside them) is counted in int32: a tile reads the
+  // shared events and those of its requests, and a request lies in a tile more than it fills
   const int64_t tiles = a->q_rows * (a->n_heads / h->n_heads) / 8 + n_groups;
   const int64_t events = static_cast<int64_t>(h->max_pages) * h->page_tokens;
   if (tiles > dlrm::kPrefixTiles + n_groups ||
-      (2 * tiles + a->batch) * h->n_heads >= (int64_t(1) << 31) / (events / 32 + 3))
+      (2 * tiles + a->batch) * h->n_heads >= (int64_t(1) << 30) / (events / 32 + 16))
     return DLRM_ERR_UNSUPPORTED;
   if (rows_overlap(a->q_rows, a->ld_out, a->n_heads, a->ld_out_head, h->head_dim))
     return DLRM_ERR_INVALID_ARG;

@@ -216,7 +216,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
   if (!last_s) return;
   __threadfence();
   if (bad && t == 0) flag(h.err, DLRM_ERRBIT_OFFSETS);
-  int units = 0, dense = 0;
+  int work = 0, dense = 0;
+  const int cost = kCostBlocks / p.split;
   const int per = (last_place - first_place + kPlanThreads - 1) / kPlanThreads;
   const int mine0 = min(last_place, first_place + t * per), mine1 = min(last_place, mine0 + per);
   const auto tile_at = [&](int i) {
@@ -231,38 +232,45 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
   for (int i = mine0; i < mine1; ++i) {
     only = tile_at(i);
     const int chunks = chunks_of(only, p.split);
-    units += chunks * h.n_heads;
+    work += chunks > 0 ? (chunks + cost) * h.n_heads : 0;
     dense += chunks > 0;
   }
+  // the work of a CTA: of all, but kLeastBlocks at least where pieces are longer on average
   int total, n_tiles;
-  int at = scan(units, sums, total);
+  scan(work, sums, total);
   int place = scan(dense, sums, n_tiles);
-  Cuts cuts;
-  cuts.total = total;
-  cuts.ctas = min(p.grid, min(total, max(total / max(kLeastBlocks / p.split, 1), n_tiles * h.n_heads)));
-  cuts.each = cuts.ctas > 0 ? total / cuts.ctas : 0;
-  cuts.extra = total - cuts.each * cuts.ctas;
-  const int whole = kWholeBlocks / p.split;
+  const int pieces = n_tiles * h.n_heads;
+  const Cuts cuts(max((total + p.grid - 1) / p.grid, max(min(kLeastBlocks / p.split + cost, pieces ? total / pieces : 1), 1)),
+                  p.split);
+  work = 0;
+  for (int i = mine0; i < mine1; ++i) {
+    const int chunks = chunks_of(per == 1 ? only : tile_at(i), p.split);
+    work += chunks > 0 ? cuts.work(chunks) * h.n_heads : 0;
+  }
+  int at = scan(work, sums, total);
+  const int ctas = cuts.from(total);
   for (int i = mine0; i < mine1; ++i) {
     Tile y = per == 1 ? only : tile_at(i);
     const int chunks = chunks_of(y, p.split);
     if (chunks == 0) continue;
     y.first = at;
     p.tiles[place] = y;
-    // the CTAs that begin in this tile; a cut inside a short piece moves to its
-    // start: finishing it in one CTA is faster than joining parts
-    const int end = at + chunks * h.n_heads;
-    int c = cuts.owner(at);
-    if (cuts.cut(c) < at) ++c;
-    for (; c < cuts.ctas && cuts.cut(c) < end; ++c) {
-      int cut = cuts.cut(c);
-      if (chunks <= whole) cut -= static_cast<unsigned>(cut - at) % static_cast<unsigned>(chunks);
-      p.cuts[c] = Cut{cut, place, total, cuts.ctas, y};
+    // the CTAs that begin in this tile: with a piece, inside it, or with the next one
+    for (int head = 0; head < h.n_heads; ++head) {
+      const int start = at + head * cuts.work(chunks), end = start + cuts.work(chunks);
+      int inner;
+      const int n = cuts.inside(start, chunks, inner);
+      // (without an inside, those before its middle begin with it)
+      const int c1 = n > 0 ? inner : cuts.from(start + (end - start) / 2), c2 = cuts.from(end);
+      for (int c = cuts.from(start); c < min(c1, ctas); ++c) p.cuts[c] = Cut{place, head, 0, cuts.each, y};
+      for (int c = inner; c < min(inner + n, ctas); ++c)
+        p.cuts[c] = Cut{place, head, cuts.chunk(c, start, chunks), cuts.each, y};
+      for (int c = n > 0 ? inner + n : c1; c < min(c2, ctas); ++c) p.cuts[c] = Cut{place, head + 1, 0, cuts.each, y};
     }
-    at = end;
+    at += cuts.work(chunks) * h.n_heads;
     ++place;
   }
-  for (int c = cuts.ctas + t; c <= p.grid; c += kPlanThreads) p.cuts[c] = Cut{total, n_tiles, total, cuts.ctas, Tile{}};
+  for (int c = ctas + t; c <= p.grid; c += kPlanThreads) p.cuts[c] = Cut{n_tiles, 0, 0, cuts.each, Tile{}};
 }
 
 }  // namespace
@@ -285,6 +293,7 @@ cudaError_t launch_history_prefix_attention(const dlrm_history_t& h, const dlrm_
   p.group = a.n_heads / h.n_heads;
   const int64_t four = 4 * dtype_bytes(a.dtype);
   p.vec_q = reinterpret_cast<uintptr_t>(a.q) % four == 0 && a.ld_q % 4 == 0 && a.ld_q_head % 4 == 0;
+  p.vec_out = reinterpret_cast<uintptr_t>(a.out) % four == 0 && a.ld_out % 4 == 0 && a.ld_out_head % 4 == 0;
   p.arrived = work_part<int32_t>(h, w.prefix_head);
   p.members = work_part<Member>(h, w.members);
   p.found = work_part<Tile>(h, w.found_tiles);

@@ -11,8 +11,9 @@ namespace dlrm {
 namespace prefix {
 
 
-constexpr int kWholeBlocks = 16;                 // blocks of a tile that is never split
-constexpr int kLeastBlocks = 16;                 // blocks of a CTA at least, where tiles are longer
+constexpr int kWholeBlocks = 16;                 // blocks of a piece that is never split
+constexpr int kLeastBlocks = 16;                 // blocks of a CTA at least, where pieces are longer
+constexpr int kCostBlocks = 12;                  // blocks in whose time a piece is begun and ended
 constexpr int kWeights = 32;                     // parts whose weights lie in shared memory at once
 
 // What the plan knows of a request with rows, and of the tiles.
@@ -24,7 +25,7 @@ struct Member {
 };
 static_assert(sizeof(Member) == kPrefixMember, "scratch size of a member");
 struct Tile {
-  int32_t first, blocks;                         // units of work (chunk of a kv head) before it; its blocks
+  int32_t first, blocks;                         // work before it, as Cuts counts it; its blocks
   int32_t q0, row0, rows;                        // the group's first query row; rows among the group's
   int32_t member0, member1;                      // first and last request with rows in the tile
   int32_t slot;                                  // whose table gives the shared pages
@@ -34,8 +35,9 @@ struct Tile {
 static_assert(sizeof(Tile) == kPrefixTile, "scratch size of a tile");
 
 struct Cut {                                     // where a CTA begins
-  int32_t unit, place;                           // first unit, and the tile that holds it
-  int32_t units, ctas;                           // of the call
+  int32_t place, piece;                          // tile, and which of its pieces (kv heads)
+  int32_t chunk;                                 // of the piece
+  int32_t each;                                  // work of a CTA
   Tile tile;
 };
 static_assert(sizeof(Cut) == kPrefixCut, "scratch size of a cut");
@@ -44,6 +46,32 @@ static_assert(sizeof(Cut) == kPrefixCut, "scratch size of a cut");
 __device__ __forceinline__ int chunks_of(const Tile& t, int split) {
   return t.rows > 0 ? max(static_cast<int>(static_cast<unsigned>(t.blocks + split - 1) / static_cast<unsigned>(split)), 1) : 0;
 }
+// Cuts the pieces (a tile and kv head) of a call evenly over the CTAs. A piece counts as its
+// chunks and `cost` more, as it takes time to begin and to end, and, from four CTAs' work on, as a
+// whole number of them, so that no CTA has parts of two such pieces. CTA c begins at c `each` of
+// the whole, but where that lies within `near` of a piece's ends, or in a piece too short
+// to be split, it begins with that piece or with the next.
+struct Cuts {
+  int each, cost, near, whole;
+  __device__ __forceinline__ Cuts(int each, int split)
+      : each(each), cost(kCostBlocks / split), near(kCostBlocks / split), whole(kWholeBlocks / split) {}
+  __device__ __forceinline__ int work(int chunks) const {
+    const int n = chunks + cost;
+    return n >= 4 * each ? n / each * each : n;
+  }
+  // The first CTA that begins at or after `w`.
+  __device__ __forceinline__ int from(int w) const { return static_cast<unsigned>(w + each - 1) / static_cast<unsigned>(each); }
+  // CTAs [first, first + n) begin inside the piece of `chunks` chunks at `start`.
+  __device__ __forceinline__ int inside(int start, int chunks, int& first) const {
+    first = from(start + near);
+    return chunks <= whole ? 0 : max(from(start + work(chunks) - near) - first, 0);
+  }
+  // The chunk at which CTA c, one of them, begins.
+  __device__ __forceinline__ int chunk(int c, int start, int chunks) const {
+    return static_cast<int>(static_cast<int64_t>(c * each - start) * chunks / work(chunks));
+  }
+};
+
 // Blocks of a request's own events.
 __device__ __forceinline__ int blocks_of(const Member& m) {
   return m.rows > 0 && m.len > 0 ? m.sinks + max((m.len + kBlock - 1) / kBlock - m.block0, 0) : 0;
@@ -57,7 +85,7 @@ struct Params {
   int group;                                     // query heads of a kv head
   int rows, split;                               // of a tile; warps that split a chunk's blocks
   int grid;                                      // CTAs of the second launch
-  int vec_q;
+  int vec_q, vec_out;                            // four elements can be loaded, stored at once
   int32_t* arrived;                              // CTAs of the plan that are done
   Member* members;
   Tile* found;                                   // tiles, with gaps between the groups
@@ -72,6 +100,17 @@ cudaError_t launch_plan(const Params& p, cudaStream_t stream);
 cudaError_t launch_32(Params& p, cudaStream_t stream);
 cudaError_t launch_64(Params& p, cudaStream_t stream);
 cudaError_t launch_128(Params& p, cudaStream_t stream);
+
+template <int DT>
+__device__ __forceinline__ void store_four(void* out, int64_t at, const float (&z)[4]) {
+  if (DT == DLRM_DTYPE_FP32)
+    *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = make_float4(z[0], z[1], z[2], z[3]);
+  else if (DT == DLRM_DTYPE_BF16)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = make_uint2(pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3]));
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) =
+        make_uint2(pack_f16x2(z[0], z[1]), pack_f16x2(z[2], z[3]));
+}
 
 // Two fp32 at a time.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -137,31 +176,40 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
   const unsigned group = p.group;
   unsigned char* ring = smem + set * kStages * kPer * Sh::kBytes;
   const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+  // what this thread copies of a block: from its first 16-byte chunk of a side on
+  constexpr int kSide = 2 * D;                    // chunks of a side
+  static_assert(kSide % (kWarp * WR) == 0 || 2 * kSide == kWarp * WR, "chunks of a thread");
+  const int id = (wr * kWarp + lane) % kSide;
+  const uint32_t dst_k = ring_at + key_offset<D>(id / (D / 16), id % (D / 16));
+  const uint32_t dst_v = ring_at + kBlock * D + value_offset<D>(id / (D / 16), id % (D / 16));
+  const uint8_t* const src_k = p.h.k_codes + id * 16;
+  const uint8_t* const src_v = p.h.v_codes + id * 16;
   pdl_wait();
   pdl_trigger();
-  const Cut from = p.cuts[blockIdx.x];
-  const int end = p.cuts[blockIdx.x + 1].unit;
-  Cuts cuts;
-  cuts.total = from.units;
-  cuts.ctas = from.ctas;
-  cuts.each = cuts.ctas > 0 ? static_cast<unsigned>(cuts.total) / static_cast<unsigned>(cuts.ctas) : 0;
-  cuts.extra = cuts.total - cuts.each * cuts.ctas;
-  int place = from.place;
+  const Cut from = p.cuts[blockIdx.x], to = p.cuts[blockIdx.x + 1];
+  const Cuts cuts(from.each, kSets);
+  int place = from.place, head = from.piece, begin = from.chunk;
   Tile s = from.tile;
-  int chunks = chunks_of(s, kSets);
   bool fresh = true;                              // a tile whose requests are not known yet
 
-  for (int u = from.unit; u < end;) {
-    if (u >= s.first + chunks * H) {
-      s = p.tiles[++place];
-      chunks = chunks_of(s, kSets);
+  const auto ends = [&] {                         // nothing is left before `to`
+    return place > to.place || (place == to.place && (head > to.piece || (head == to.piece && begin >= to.chunk)));
+  };
+  while (!ends()) {
+    if (head == H) {
+      ++place;
+      head = begin = 0;
       fresh = true;
+      if (ends()) break;
+      s = p.tiles[place];
     }
-    const int head = static_cast<unsigned>(u - s.first) / static_cast<unsigned>(chunks);
-    const int seg0 = s.first + head * chunks, seg1 = seg0 + chunks;
-    const int chunk0 = u - seg0, chunk1 = min(end, seg1) - seg0;
+    const int chunks = chunks_of(s, kSets);
+    const int chunk0 = begin, chunk1 = place == to.place && head == to.piece ? to.chunk : chunks;
+    const int piece = s.first + head * cuts.work(chunks);   // where it begins, as Cuts counts
+    const int kv = head;
     const int rows = s.rows;
-    u = seg0 + chunk1;
+    begin = 0;
+    ++head;
 
     // ---- the tile's requests; at the same time the queries and the first shared pages.
     // Everything below is a chain of loads, so what does not hang together starts together
@@ -177,7 +225,7 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
         const int row = s.row0 + min(r, rows - 1);
         const int query = group == 1 ? row : static_cast<unsigned>(row) / group;
         const int64_t q_at = (s.q0 + static_cast<int64_t>(query)) * p.a.ld_q +
-                             (head * p.group + row - query * p.group) * p.a.ld_q_head;
+                             (kv * p.group + row - query * p.group) * p.a.ld_q_head;
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
           if (in && !(SPLIT && r2)) {
@@ -203,7 +251,7 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
       if (page < 0 || page >= p.h.n_pages) {
         flag(p.h.err, DLRM_ERRBIT_INDEX_OOB);     // trimmed, or a broken table: events that some row needs
       } else {
-        const int64_t where = static_cast<int64_t>(page) * H + head;
+        const int64_t where = static_cast<int64_t>(page) * H + kv;
         x.codes = (where * G + (x.t0 & (G - 1))) * D;
         x.ks = p.h.k_scales[where];
         x.vs = p.h.v_scales[where];
@@ -279,16 +327,20 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
         const int64_t mine_codes = i - base < kWarp ? info.codes : ahead.codes;
         const int64_t codes = __shfl_sync(0xffffffffu, mine_codes, i % kWarp);
         if (codes >= 0) {
-          const uint32_t dst = ring_at + (i % (kStages * kPer)) * Sh::kBytes;
-          constexpr int kSide = 2 * D;            // 16-byte chunks of a side
+          const uint32_t dst = (i % (kStages * kPer)) * Sh::kBytes;
+          constexpr int kStep = kWarp * WR;       // 16-byte chunks of the set's threads
+          if (kSide % kStep == 0) {
+            // a thread's chunks lie 8 events apart, or a multiple, for which the swizzles of keys
+            // and values are alike, or 4, for which that of values changes in one bit
+            constexpr int kApart = kStep / (D / 16) % 8;
+            static_assert(kSide % kStep != 0 || kApart == 0 || (kApart == 4 && D == 128), "swizzle");
+            constexpr uint32_t kFlip = kApart == 4 ? 64 : 0;
 #pragma unroll
-          for (int x = 0; x < 2 * kSide / (kWarp * WR); ++x) {
-            const int both = (x * WR + wr) * kWarp + lane;   // (a warp's chunks lie on one side)
-            const int id = both % kSide, t = id / (D / 16), ch = id % (D / 16);
-            if (both < kSide)
-              copy16(dst + key_offset<D>(t, ch), p.h.k_codes + codes + id * 16);
-            else
-              copy16(dst + kBlock * D + value_offset<D>(t, ch), p.h.v_codes + codes + id * 16);
+            for (int x = 0; x < kSide / kStep; ++x) copy16(dst + dst_k + x * kStep * 16, src_k + codes + x * kStep * 16);
+#pragma unroll
+            for (int x = 0; x < kSide / kStep; ++x) copy16(dst + (x % 2 ? dst_v ^ kFlip : dst_v) + x * kStep * 16, src_v + codes + x * kStep * 16);
+          } else {                                // two warps a side
+            copy16(dst + (wr < WR / 2 ? dst_k : dst_v), (wr < WR / 2 ? src_k : src_v) + codes);
           }
         }
       }
@@ -695,14 +747,19 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
     auto finish = [&](int r, int d, const float4& y) {
       const float l = row_total[r];
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const float z[4] = {y.x * inv, y.y * inv, y.z * inv, y.w * inv};
-      const int hq = head * p.group + row_head[r];
+      // (no weights: zeros)
+      const float z[4] = {l == 0.f ? 0.f : y.x * inv, l == 0.f ? 0.f : y.y * inv, l == 0.f ? 0.f : y.z * inv,
+                          l == 0.f ? 0.f : y.w * inv};
+      const int hq = kv * p.group + row_head[r];
       const int64_t at = row_at[r] * p.a.ld_out + hq * p.a.ld_out_head + d;
       bool fine = l != 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        store_element<DT>(p.a.out, at + e, l == 0.f ? 0.f : z[e]);
-        fine &= finite(z[e]);
+      for (int e = 0; e < 4; ++e) fine &= finite(z[e]);
+      if (p.vec_out) {
+        store_four<DT>(p.a.out, at, z);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) store_element<DT>(p.a.out, at + e, z[e]);
       }
       if (d == 0) {
         if (p.a.lse)
@@ -729,10 +786,11 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
         mine_at[kRows * D + r] = row_top[r];
         mine_at[kRows * D + kRows + r] = row_total[r];
       }
-      // the CTAs that share this piece: first .. last, one part each. (A cut moves
-      // out of short pieces only, so a split one's cuts are where they were.)
-      const int64_t first = cuts.owner(seg0);
-      const int parts = cuts.owner(seg1 - 1) - static_cast<int>(first) + 1;
+      // the CTAs that share this piece, one part each: the one that begins it, and those
+      // that begin inside
+      int inner;
+      const int parts = cuts.inside(piece, chunks, inner) + 1;
+      const int64_t first = inner - 1;
       __threadfence();
       __syncthreads();
       if (threadIdx.x == 0) {
@@ -798,10 +856,10 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
     __syncthreads();
     if (odd[kRows]) {
       for (int r = 0; r < rows; ++r) {
-        const int hq = head * p.group + row_head[r];
+        const int hq = kv * p.group + row_head[r];
         const Visible v{see_end[r], see_gap0[r], see_gap1[r]};
         if (odd[r] == 1 || (odd[r] == 2 && sees_any(v)))
-          careful_row<DT>(p.h, p.a, m_of[row_member[r]].slot, v, head, row_at[r] * p.a.ld_q + hq * p.a.ld_q_head,
+          careful_row<DT>(p.h, p.a, m_of[row_member[r]].slot, v, kv, row_at[r] * p.a.ld_q + hq * p.a.ld_q_head,
                           row_at[r] * p.a.ld_out + hq * p.a.ld_out_head, row_at[r] * p.a.n_heads + hq,
                           &joined[0][0][0]);
       }
