@@ -188,7 +188,7 @@ cudaError_t launch_history_free(const dlrm_history_t& h, const int32_t* slots, i
                                 int window, int sinks, cudaStream_t stream);
 cudaError_t launch_history_compact(const dlrm_history_t& h, cudaStream_t stream);
 cudaError_t launch_history_attention(const dlrm_history_t& h, const dlrm_attention_t& a,
-                                     cudaStream_t stream);
+                                     cudaStream_t stream, const int32_t* groups = nullptr, int n_groups = 0);
 bool history_tc_takes(const dlrm_history_t& h, const dlrm_attention_t& a);
 cudaError_t launch_history_attention_tc(const dlrm_history_t& h, const dlrm_attention_t& a,
                                         int32_t* counters, float* partials, cudaStream_t stream);

@@ -67,6 +67,8 @@ struct Params {
   int vec_q;                                     // four query elements can be loaded at once
   int32_t* counters;
   float* partials;
+  const int32_t* groups;                         // checked only, where there are any
+  int n_groups;
 };
 
 // What a CTA needs to know of a request.
@@ -165,6 +167,11 @@ history_attention_kernel(const __grid_constant__ Params p) {
   Span s = found.span[0];
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < p.a.batch; i += kThreads) span_of<kRows>(p, i, true);
+  if (p.groups && blockIdx.x == 0)
+    for (int i = threadIdx.x; i <= p.n_groups; i += kThreads)
+      if (i < p.n_groups ? p.groups[i] < 0 || p.groups[i + 1] < p.groups[i] || (i == 0 && p.groups[0] != 0)
+                         : p.groups[i] != p.a.batch)
+        flag(p.h.err, DLRM_ERRBIT_OFFSETS);
 
   for (int u = begin; u < end;) {
     if (u >= at + units(s)) {
@@ -690,7 +697,7 @@ cudaError_t launch_d(Params& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_history_attention(const dlrm_history_t& h, const dlrm_attention_t& a,
-                                     cudaStream_t stream) {
+                                     cudaStream_t stream, const int32_t* groups, int n_groups) {
   const HistoryWork w = history_work(h);
   Params p;
   p.h = h;
@@ -700,6 +707,8 @@ cudaError_t launch_history_attention(const dlrm_history_t& h, const dlrm_attenti
   p.vec_q = reinterpret_cast<uintptr_t>(a.q) % four == 0 && a.ld_q % 4 == 0 && a.ld_q_head % 4 == 0;
   p.counters = work_part<int32_t>(h, w.counters);
   p.partials = work_part<float>(h, w.partials);
+  p.groups = groups;
+  p.n_groups = n_groups;
   if (history_tc_takes(h, a)) return launch_history_attention_tc(h, a, p.counters, p.partials, stream);
   if (h.head_dim == 32) return launch_d<32>(p, stream);
   if (h.head_dim == 64) return launch_d<64>(p, stream);

@@ -22,6 +22,7 @@ namespace {
 
 constexpr int kPlanThreads = 512;
 constexpr int kHere = 256;                       // requests of a group that shared memory holds
+constexpr int kTilesHere = 1024;
 
 // Exclusive prefix sum over the CTA; total in every thread.
 __device__ __forceinline__ int scan(int x, int* sums, int& total) {
@@ -58,6 +59,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
   __shared__ int sums[kWarp + 1];
   __shared__ int ref_s, len_s, gap_s, shared_s, last_s;
   __shared__ Member here[kHere];
+  __shared__ int first_s[kTilesHere];            // where tiles begin
   const dlrm_history_t& h = p.h;
   const int G = h.page_tokens, M = h.max_pages, t = threadIdx.x, lane = t % kWarp, g = blockIdx.x;
   const int32_t* starts = p.a.q_starts;
@@ -68,12 +70,30 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
   }
   pdl_wait();
   pdl_trigger();
-  const int b0 = p.groups[g], b1 = p.groups[g + 1], first_b = p.groups[0], last_b = p.groups[p.n_groups];
-  // starts or groups that decrease or leave their range: nothing is done
+  // everything that hangs by a group's place alone is loaded at once, from within the arrays
+  // whatever the groups say
+  const auto request = [&](int i) { return min(max(p.groups[i], 0), p.a.batch); };
+  const int b0 = request(g), b1 = max(request(g + 1), b0), n_requests = b1 - b0;
+  const int q0 = starts[b0], q1 = starts[b1], first_q = starts[request(0)], last_q = starts[request(p.n_groups)];
+  const int64_t cap = static_cast<int64_t>(M) * G;
+  const auto member_of = [&](int b) {            // of the call's
+    Member m{};
+    m.slot = p.a.slots[b];
+    const int s0 = starts[b];
+    m.queries = starts[b + 1] - s0;
+    m.row0 = (s0 - q0) * p.group;
+    m.rows = m.queries * p.group;
+    if (m.slot >= 0 && m.slot < h.n_slots)
+      m.len = static_cast<int>(min(static_cast<int64_t>(max(h.lengths[m.slot], 0)), cap));
+    return m;
+  };
+  Member mine{};
+  if (t < n_requests) mine = member_of(b0 + t);
+  // starts or groups that decrease, leave their range or leave requests out: nothing is done
   bool bad = false;
   for (int i = t; i <= p.n_groups; i += kPlanThreads) {
     const int x = p.groups[i];
-    bad |= x < 0 || x > p.a.batch || (i < p.n_groups && p.groups[i + 1] < x);
+    bad |= i < p.n_groups ? x < 0 || p.groups[i + 1] < x || (i == 0 && x != 0) : x != p.a.batch;
   }
   for (int i = t; i <= p.a.batch; i += kPlanThreads) {
     const int x = starts[i];
@@ -86,30 +106,19 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
   };
   int first_place = 0, last_place = 0;
   if (!bad) {
-    first_place = place_of(starts[first_b], 0);
-    last_place = place_of(starts[last_b], p.n_groups);
-    const int q0 = starts[b0], q1 = starts[b1];
-    const int64_t cap = static_cast<int64_t>(M) * G;
-    Member* members = b1 - b0 <= kHere ? here : p.members + b0;   // of the group
-    // ---- lengths; the events that every request with rows and events has
+    first_place = place_of(first_q, 0);
+    last_place = place_of(last_q, p.n_groups);
+    Member* members = n_requests <= kHere ? here : p.members + b0;   // of the group
+    // ---- the events that every request with rows and events has
     const auto first_seen = [&](const Member& m) {   // of its first row
       return visible(p.a.causal ? m.len - m.queries : m.len - 1, m.len, p.a.window, p.a.sinks);
     };
-    for (int b = b0 + t; b < b1; b += kPlanThreads) {
-      Member m{};
-      m.slot = p.a.slots[b];
-      const int s0 = starts[b];
-      m.queries = starts[b + 1] - s0;
-      m.row0 = (s0 - q0) * p.group;
-      m.rows = m.queries * p.group;
-      if (m.slot >= 0 && m.slot < h.n_slots) {
-        m.len = static_cast<int>(min(static_cast<int64_t>(max(h.lengths[m.slot], 0)), cap));
-      } else {
-        flag(h.err, DLRM_ERRBIT_INDEX_OOB);
-      }
-      members[b - b0] = m;
+    for (int b = t; b < n_requests; b += kPlanThreads) {
+      const Member m = b == t ? mine : member_of(b0 + b);
+      if (m.slot < 0 || m.slot >= h.n_slots) flag(h.err, DLRM_ERRBIT_INDEX_OOB);
+      members[b] = m;
       if (m.rows > 0 && m.len > 0) {
-        atomicMin(&ref_s, b - b0);
+        atomicMin(&ref_s, b);
         atomicMin(&len_s, m.len);
         atomicMin(&gap_s, first_seen(m).gap1);
       }
@@ -123,7 +132,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     if (pages > 0) {
       const int32_t* mine = h.table + static_cast<int64_t>(ref_slot) * M;
       const int pieces = (pages + 255) / 256;
-      const int64_t work = static_cast<int64_t>(b1 - b0) * pieces;
+      const int64_t work = static_cast<int64_t>(n_requests) * pieces;
       for (int64_t w = t / kWarp; w < work; w += kPlanThreads / kWarp) {
         const int b = static_cast<int>(w / pieces), j0 = static_cast<int>(w % pieces) * 256 + lane;
         const Member& m = members[b];
@@ -143,11 +152,11 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     const int shared = shared_s * G;             // events
     // ---- every request's blocks of its own, and how many lie before them
     int before = 0;
-    for (int c0 = 0; c0 < b1 - b0; c0 += kPlanThreads) {
+    for (int c0 = 0; c0 < n_requests; c0 += kPlanThreads) {
       const int b = c0 + t;
       int n = 0;
       Member m{};
-      if (b < b1 - b0) {
+      if (b < n_requests) {
         m = members[b];
         if (m.rows > 0 && m.len > 0) {
           const Visible v = first_seen(m);
@@ -164,7 +173,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
       int total;
       m.first = before + scan(n, sums, total);
       before += total;
-      if (b < b1 - b0) {
+      if (b < n_requests) {
         p.members[b0 + b] = m;
         members[b] = m;
       }
@@ -182,8 +191,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     x.shared_sinks = min((min(gap0, shared) + kBlock - 1) / kBlock, x.shared0);
     if (x.shared_sinks == x.shared0) x.shared_sinks = x.shared0 = 0;
     x.shared_blocks = x.shared_sinks + x.own0 - x.shared0;
-    const auto holds = [&](int row) {            // the request of a row
-      int lo = 0, hi = b1 - b0;                  // the last one that begins at or before it
+    const auto holds = [&](int row, int from) {  // the request of a row, `from` or a later one
+      int lo = from, hi = n_requests;            // the last one that begins at or before it
       while (hi - lo > 1) {
         const int mid = lo + (hi - lo) / 2;
         if (members[mid].row0 <= row) lo = mid; else hi = mid;
@@ -195,12 +204,17 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
       if (i < tiles) {
         y.row0 = i * p.rows;
         y.rows = min(p.rows, rows - y.row0);
-        y.member0 = holds(y.row0);
-        y.member1 = holds(y.row0 + y.rows - 1);
-        const Member last = members[y.member1];
-        y.blocks = y.shared_blocks - members[y.member0].first + last.first + blocks_of(last);
-        y.member0 += b0;
-        y.member1 += b0;
+        // own blocks of the rows of each of a set's warps, one a warp and chunk
+        const int each = p.rows * p.split / kWarps;
+        int m0 = holds(y.row0, 0), m1 = m0;
+        y.member0 = b0 + m0;
+        for (int r = 0; r < y.rows; r += each) {
+          if (r > 0) m0 = holds(y.row0 + r, m1);
+          m1 = holds(y.row0 + min(y.rows, r + each) - 1, m0);
+          const int blocks = members[m1].first + blocks_of(members[m1]) - members[m0].first;
+          y.own = max(y.own, (blocks + p.split - 1) / p.split);
+        }
+        y.member1 = b0 + m1;
       }
       p.found[base + i] = y;
     }
@@ -255,22 +269,36 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     if (chunks == 0) continue;
     y.first = at;
     p.tiles[place] = y;
-    // the CTAs that begin in this tile: with a piece, inside it, or with the next one
-    for (int head = 0; head < h.n_heads; ++head) {
-      const int start = at + head * cuts.work(chunks), end = start + cuts.work(chunks);
-      int inner;
-      const int n = cuts.inside(start, chunks, inner);
-      // (without an inside, those before its middle begin with it)
-      const int c1 = n > 0 ? inner : cuts.from(start + (end - start) / 2), c2 = cuts.from(end);
-      for (int c = cuts.from(start); c < min(c1, ctas); ++c) p.cuts[c] = Cut{place, head, 0, cuts.each, y};
-      for (int c = inner; c < min(inner + n, ctas); ++c)
-        p.cuts[c] = Cut{place, head, cuts.chunk(c, start, chunks), cuts.each, y};
-      for (int c = n > 0 ? inner + n : c1; c < min(c2, ctas); ++c) p.cuts[c] = Cut{place, head + 1, 0, cuts.each, y};
-    }
+    if (place < kTilesHere) first_s[place] = at;
     at += cuts.work(chunks) * h.n_heads;
     ++place;
   }
-  for (int c = ctas + t; c <= p.grid; c += kPlanThreads) p.cuts[c] = Cut{n_tiles, 0, 0, cuts.each, Tile{}};
+  __syncthreads();
+  // a CTA begins with a piece, inside it, or with the next one
+  for (int c = t; c <= p.grid; c += kPlanThreads) {
+    Cut x{n_tiles, 0, 0, cuts.each, Tile{}};
+    if (c < ctas) {
+      const int w = c * cuts.each;
+      int lo = 0, hi = n_tiles;                   // the last tile that begins at or before it
+      while (hi - lo > 1) {
+        const int mid = lo + (hi - lo) / 2;
+        if ((mid < kTilesHere ? first_s[mid] : __ldcg(&p.tiles[mid].first)) <= w) lo = mid; else hi = mid;
+      }
+      x.place = lo;
+      const int4* from = reinterpret_cast<const int4*>(&p.tiles[lo]);
+      int4* to = reinterpret_cast<int4*>(&x.tile);
+#pragma unroll
+      for (int i = 0; i < static_cast<int>(sizeof(Tile) / 16); ++i) to[i] = __ldcg(from + i);
+      const int chunks = chunks_of(x.tile, p.split), length = cuts.work(chunks);
+      x.piece = static_cast<unsigned>(w - x.tile.first) / static_cast<unsigned>(length);
+      const int start = x.tile.first + x.piece * length, off = w - start;
+      if (chunks > cuts.whole && off >= cuts.near && off < length - cuts.near)
+        x.chunk = cuts.chunk(c, start, chunks);
+      else if (chunks > cuts.whole ? off >= cuts.near : off >= length / 2)
+        ++x.piece;
+    }
+    p.cuts[c] = x;
+  }
 }
 
 }  // namespace
@@ -283,8 +311,19 @@ cudaError_t launch_plan(const Params& p, cudaStream_t stream) {
 
 cudaError_t launch_history_prefix_attention(const dlrm_history_t& h, const dlrm_attention_t& a,
                                             const int32_t* groups, int n_groups, cudaStream_t stream) {
-  const HistoryWork w = history_work(h);
   using namespace prefix;
+  // Too little to share: history_attention's time, by its pieces (a request's 16 rows of a kv
+  // head, 0.013 us each) and by the bytes that all requests together can read (7.5 TB/s,
+  // most of them from L2) at most kApart us above its least, where the plan alone takes
+  // longer. In us, one query a request: 1 user x 4 beams x 400 events of 8 heads over 2
+  // 8.1 against 17, 64 x 4 x 400 16 against 21; 64 x 16 x 1500 74 against 48.
+  constexpr double kApart = 12.0;
+  const int64_t cap = static_cast<int64_t>(h.max_pages) * h.page_tokens;
+  const int64_t seen = a.window > 0 ? std::min<int64_t>(cap, int64_t(a.window) + a.sinks + 2 * kBlock) : cap;
+  const int64_t tiles = a.batch + a.q_rows * (a.n_heads / h.n_heads) / 16;
+  if (0.013 * tiles * h.n_heads + 2e-6 / 7.5 * tiles * h.n_heads * seen * h.head_dim <= kApart && !history_tc_takes(h, a))
+    return launch_history_attention(h, a, stream, groups, n_groups);
+  const HistoryWork w = history_work(h);
   Params p;
   p.h = h;
   p.a = a;

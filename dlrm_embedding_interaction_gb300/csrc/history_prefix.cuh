@@ -25,7 +25,7 @@ struct Member {
 };
 static_assert(sizeof(Member) == kPrefixMember, "scratch size of a member");
 struct Tile {
-  int32_t first, blocks;                         // work before it, as Cuts counts it; its blocks
+  int32_t first, own;                            // work before it, as Cuts counts it; chunks of its requests' own events
   int32_t q0, row0, rows;                        // the group's first query row; rows among the group's
   int32_t member0, member1;                      // first and last request with rows in the tile
   int32_t slot;                                  // whose table gives the shared pages
@@ -42,9 +42,13 @@ struct Cut {                                     // where a CTA begins
 };
 static_assert(sizeof(Cut) == kPrefixCut, "scratch size of a cut");
 
-// Chunks of a tile: one even where there is nothing to read, which writes zeros.
+// Chunks of a tile: a block of shared events for each set of warps, then one of their own events
+// for each warp; one even where there is nothing to read, which writes zeros.
+__device__ __forceinline__ int shared_chunks(const Tile& t, int split) {
+  return static_cast<unsigned>(t.shared_blocks + split - 1) / static_cast<unsigned>(split);
+}
 __device__ __forceinline__ int chunks_of(const Tile& t, int split) {
-  return t.rows > 0 ? max(static_cast<int>(static_cast<unsigned>(t.blocks + split - 1) / static_cast<unsigned>(split)), 1) : 0;
+  return t.rows > 0 ? max(shared_chunks(t, split) + t.own, 1) : 0;
 }
 // Cuts the pieces (a tile and kv head) of a call evenly over the CTAs. A piece counts as its
 // chunks and `cost` more, as it takes time to begin and to end, and, from four CTAs' work on, as a
@@ -130,12 +134,16 @@ struct Shape {
   static constexpr int kTile = SPLIT ? 8 : 16;    // rows of an MMA tile
   static constexpr int kRows = kTile * MT * WR;
   static constexpr int kSets = kWarps / WR;       // sets of warps, a ring and a block of each chunk each
-  static constexpr int kPer = WR == 1 ? 1 : 2;    // blocks of a stage: warps that share a ring meet once a stage
+  // blocks of a stage: warps that share a ring meet once a stage (at head_dim 128 there is
+  // space for one)
+  static constexpr int kPer = WR == 1 || (D == 128 && WR == 2) ? 1 : 2;
   static constexpr int kStages = WR > 1 || D == 128 ? 3 : 4;
+  static constexpr int kOwn = WR == 1 ? 0 : D == 128 ? 1 : 2;   // blocks of own events, a warp (WR = 1: in its ring)
   static constexpr int kBytes = 2 * kBlock * D;   // keys and values of a block
   static constexpr int kStride = D + 4;           // of a row's sums in shared memory
   static constexpr int kPartial = kRows * (D + 2);   // of a part in scratch: sums, maxima, sums of weights
-  static constexpr int kRing = kSets * kStages * kPer * kBytes;
+  static constexpr int kShared = kSets * kStages * kPer * kBytes;
+  static constexpr int kRing = kShared + kWarps * kOwn * kBytes;
   static constexpr int kJoin = (kSets * kRows * (kStride + 2) + kWeights * kRows) * 4;
   static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
 };
@@ -167,6 +175,7 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
   __shared__ int n_members, n_arrived;
   __shared__ int clear_end, clear_gap;            // events that every row of the tile sees lie between
   __shared__ int m_lo[kRows], m_hi[kRows], m_first[kRows];
+  __shared__ int own_first[WR], own_end[WR];      // blocks of own events of the rows of a set's warps
   __shared__ Member m_of[kRows];
 
   const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
@@ -179,6 +188,8 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
   // what this thread copies of a block: from its first 16-byte chunk of a side on
   constexpr int kSide = 2 * D;                    // chunks of a side
   static_assert(kSide % (kWarp * WR) == 0 || 2 * kSide == kWarp * WR, "chunks of a thread");
+  constexpr int kOwn = Sh::kOwn;
+  unsigned char* const own_ring = smem + Sh::kShared + warp * kOwn * Sh::kBytes;
   const int id = (wr * kWarp + lane) % kSide;
   const uint32_t dst_k = ring_at + key_offset<D>(id / (D / 16), id % (D / 16));
   const uint32_t dst_v = ring_at + kBlock * D + value_offset<D>(id / (D / 16), id % (D / 16));
@@ -237,10 +248,10 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
         }
       }
 
-    // ---- blocks of this set of warps: n0, n0 + kSets, ...; lane l knows block l of
-    // the 32 at hand (info) and of the 32 after them (ahead)
-    const int n0 = chunk0 * kSets + set, n1 = min(chunk1 * kSets, s.blocks);
-    const int count = n0 < n1 ? (n1 - n0 + kSets - 1) / kSets : 0;
+    // ---- the warp's blocks, one a chunk: first shared ones, its set's, then those of its own rows'
+    // requests; lane l knows block l of the 32 at hand (info) and of the 32 after them (ahead)
+    const int n_shared = shared_chunks(s, kSets), count = chunk1 - chunk0;
+    const int first_own = max(n_shared - chunk0, 0);   // chunks from here on are own events'
     struct Info {
       int64_t codes;                              // first byte of the block's codes; -1: nothing to read
       int t0, member;                             // first event; whose own, or -1: shared
@@ -259,16 +270,16 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
     };
     auto look_shared = [&](int i) {
       Info x{-1, 0, -1, 0.f, 0.f};
-      const int n = n0 + i * kSets;
-      if (i < count && n < s.shared_blocks) {
+      const int n = (chunk0 + i) * kSets + set;
+      if (i < count && i < first_own && n < s.shared_blocks) {
         x.t0 = (n < s.shared_sinks ? n : n - s.shared_sinks + s.shared0) * kBlock;
         open(x, s.slot);
       }
       return x;
     };
     auto look_own = [&](int i, Info& x) {
-      const int n = n0 + i * kSets;
-      if (i < count && n >= s.shared_blocks) {
+      const int n = own_first[wr] + (chunk0 + i - n_shared) * kSets + set;
+      if (i < count && i >= first_own && n < own_end[wr]) {
         int k = 0;                                // the last request whose blocks begin at or before it
         for (int d = n_members; d > 1;) {
           const int half = d / 2;
@@ -286,7 +297,7 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
     if (fresh) {
       __syncthreads();                            // the tile before is done with
       if (warp == 0) {
-        int n = 0, first = s.shared_blocks;
+        int n = 0, first = 0;
         for (int b0 = s.member0; b0 <= s.member1; b0 += kWarp) {
           if (b0 > s.member0) {
             mine = Member{};
@@ -316,16 +327,37 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
           clear_end = INT32_MAX;
           clear_gap = 0;
         }
+        __syncwarp();
+        // own blocks of the rows of each of a set's warps
+        if (lane < WR) {
+          constexpr int kMine = kRows / WR;
+          const auto holds = [&](int row) {       // the last request that begins at or before it
+            int i = 0;
+            for (int d = n_members; d > 1;) {
+              const int half = d / 2;
+              if (m_lo[i + half] <= row) i += half;
+              d -= half;
+            }
+            return i;
+          };
+          const bool any = rows > lane * kMine;
+          const int last = any ? holds(min(rows, (lane + 1) * kMine) - 1) : 0;
+          own_first[lane] = any ? m_first[holds(lane * kMine)] : 0;
+          own_end[lane] = any ? m_first[last] + blocks_of(m_of[last]) : 0;
+        }
       }
       __syncthreads();
     }
     look_own(lane, info);
     look_own(kWarp + lane, ahead);
     int base = 0;                                 // blocks [base, base + 32) are in info
-    auto fetch_block = [&](int i) {
-      if (i < count) {
-        const int64_t mine_codes = i - base < kWarp ? info.codes : ahead.codes;
-        const int64_t codes = __shfl_sync(0xffffffffu, mine_codes, i % kWarp);
+    auto codes_of = [&](int i) {
+      const int64_t mine_codes = i - base < kWarp ? info.codes : ahead.codes;
+      return __shfl_sync(0xffffffffu, mine_codes, i % kWarp);
+    };
+    auto fetch_block = [&](int i) {               // by the set's warps
+      if (i < (kOwn ? min(first_own, count) : count)) {
+        const int64_t codes = codes_of(i);
         if (codes >= 0) {
           const uint32_t dst = (i % (kStages * kPer)) * Sh::kBytes;
           constexpr int kStep = kWarp * WR;       // 16-byte chunks of the set's threads
@@ -338,7 +370,8 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
 #pragma unroll
             for (int x = 0; x < kSide / kStep; ++x) copy16(dst + dst_k + x * kStep * 16, src_k + codes + x * kStep * 16);
 #pragma unroll
-            for (int x = 0; x < kSide / kStep; ++x) copy16(dst + (x % 2 ? dst_v ^ kFlip : dst_v) + x * kStep * 16, src_v + codes + x * kStep * 16);
+            for (int x = 0; x < kSide / kStep; ++x)
+              copy16(dst + (x % 2 ? dst_v ^ kFlip : dst_v) + x * kStep * 16, src_v + codes + x * kStep * 16);
           } else {                                // two warps a side
             copy16(dst + (wr < WR / 2 ? dst_k : dst_v), (wr < WR / 2 ? src_k : src_v) + codes);
           }
@@ -348,6 +381,22 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
     auto fetch = [&](int i) {                     // a stage
 #pragma unroll
       for (int j = 0; j < kPer; ++j) fetch_block(i + j);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto fetch_own = [&](int i) {                 // by the warp, for itself
+      if (kOwn > 0 && i < count) {
+        const int64_t codes = codes_of(i);
+        if (codes >= 0) {
+          const uint32_t dst =
+              static_cast<uint32_t>(__cvta_generic_to_shared(own_ring)) + (kOwn == 2 ? i % 2 : 0) * Sh::kBytes;
+#pragma unroll
+          for (int x = 0; x < kSide / kWarp; ++x) {
+            const int c16 = x * kWarp + lane, t = c16 / (D / 16), ch = c16 % (D / 16);
+            copy16(dst + key_offset<D>(t, ch), p.h.k_codes + codes + c16 * 16);
+            copy16(dst + kBlock * D + value_offset<D>(t, ch), p.h.v_codes + codes + c16 * 16);
+          }
+        }
+      }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     auto set_barrier = [&] {
@@ -362,6 +411,7 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
     };
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) fetch(i * kPer);
+    if (kOwn > 0 && first_own == 0) fetch_own(0);
 
     // ---- what each row sees (rows past the last stand for it)
     if (fresh) {
@@ -447,10 +497,24 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
         ahead = look_shared(base + kWarp + lane);
         look_own(base + kWarp + lane, ahead);
       }
-      if (it % kPer == 0) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-        set_barrier();                            // this stage is there, and the one before it done with
-        fetch(it + (kStages - 1) * kPer);
+      const unsigned char* kb;
+      if (kOwn == 0 || it < first_own) {
+        if (it % kPer == 0) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+          set_barrier();                          // this stage is there, and the one before it done with
+          fetch(it + (kStages - 1) * kPer);
+        }
+        if (kOwn > 0 && it == first_own - 1) fetch_own(first_own);
+        kb = ring + (it % (kStages * kPer)) * Sh::kBytes;
+      } else {
+        if (kOwn == 1 && it > first_own) {
+          __syncwarp();                           // the block before is done with
+          fetch_own(it);
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncwarp();
+        if (kOwn == 2) fetch_own(it + 1);
+        kb = own_ring + (kOwn == 2 ? it % 2 : 0) * Sh::kBytes;
       }
       const int at = it % kWarp;
       const bool there = __shfl_sync(0xffffffffu, info.codes >= 0, at);
@@ -467,7 +531,6 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
         if (hi <= wr * MT * kTile || lo >= (wr + 1) * MT * kTile) continue;
       }
       const bool clear = member < 0 && t0 + kBlock <= clear_end && t0 >= clear_gap;
-      const unsigned char* kb = ring + (it % (kStages * kPer)) * Sh::kBytes;
       const unsigned char* vb = kb + kBlock * D;
 
       // S = Q K^T

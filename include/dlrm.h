@@ -651,12 +651,13 @@ dlrm_status_t window_attention(const dlrm_attention_t* a, void* stream);
  * above all: requests [groups[g], groups[g+1]) are a group, and the first pages that the
  * tables of all its slots (those with rows and events) have in common are read once for
  * all its rows. Outputs are history_attention's whatever the groups, but for rounding
- * (weights carry 22 bits with fp32 rows, 11 with fp16 and bf16). Rows of requests that no
- * group holds stay as they were.
- *   groups  (n_groups + 1) int32; batch and n_groups <= n_slots
- * Starts or groups that decrease or leave their range refuse the whole call
- * (DLRM_ERRBIT_OFFSETS). UNSUPPORTED: more than 2^18 query rows of heads that share a kv
- * head, and 2^31 work units or more. */
+ * (weights carry 22 bits with fp32 and fp16 rows, 11 with bf16). A call that is too small
+ * for sharing to pay reads each history for itself (weights of 11 bits with fp16, too).
+ *   groups  (n_groups + 1) int32 from 0 to batch; batch and n_groups <= n_slots
+ * Starts or groups that decrease, leave their range or leave requests out set
+ * DLRM_ERRBIT_OFFSETS; the call's outputs are then undefined, and its work stays
+ * bounded. UNSUPPORTED: more than 2^18 query rows of heads that share a kv head, and
+ * 2^30 work units or more. */
 dlrm_status_t history_prefix_attention(const dlrm_history_t* h, const dlrm_attention_t* a,
                                        const int32_t* groups, int32_t n_groups, void* stream);
 

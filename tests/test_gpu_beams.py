@@ -47,15 +47,21 @@ def append(cache, pool, rng, slots, counts, spread=0.5):
     pool.append(slots, at, (f64(k), f64(v)))
 
 
-def beams(rng, lens, counts, new, kv, dim, page, spread=0.5, spare=0):
+SHARED = 1 << 25                                  # bytes a side that make every call large enough to share
+
+
+def beams(rng, lens, counts, new, kv, dim, page, spread=0.5, spare=0, shared=True, idle=0):
     """Users' histories in the first slots, and their beams, forks with events of their
-    own, in the following ones, user by user: cache, restatement, the beams' slots, groups."""
+    own, in the following ones, user by user: cache, restatement, the beams' slots, groups.
+    shared: tables with room for so many events that no call passes as a small one."""
     users, n = len(lens), sum(counts)
     src = [u for u, c in enumerate(counts) for _ in range(c)]
     slots = list(range(users, users + n))
     most = max(-(-(x + max(new, default=0)) // page) for x in lens) + 1
+    if shared:
+        most = max(most, SHARED // (n * kv * dim * page) + 1)
     total = sum(-(-x // page) for x in lens) + sum(2 + x // page for x in new) + spare
-    cache, pool = make(total + 1, users + n + 1, most, kv, dim, page)
+    cache, pool = make(total + 1, users + n + 1 + idle, most, kv, dim, page)
     append(cache, pool, rng, list(range(users)), lens, spread)
     dl.history_fork(cache, i32(src), i32(slots))
     pool.fork(src, slots, True)
@@ -89,15 +95,19 @@ def check_rows(pool, slots, at, q, out, lse, dtype, *, scale=None, causal=False,
 @pytest.mark.parametrize("dim,page,kv,group", [(32, 32, 3, 1), (64, 64, 2, 4), (128, 128, 1, 2), (64, 32, 1, 5),
                                                (128, 32, 2, 1), (32, 128, 1, 8)])
 @pytest.mark.parametrize("causal,window,sinks", [(False, 0, 0), (True, 0, 0), (True, 70, 3), (False, 33, 40)])
-def test_beams_of_ragged_histories(dtype, dim, page, kv, group, causal, window, sinks):
+@pytest.mark.parametrize("shared", [True, False])
+def test_beams_of_ragged_histories(dtype, dim, page, kv, group, causal, window, sinks, shared):
     rng = np.random.default_rng(dim + page + kv + group + window)
     lens = [1, 0, page, 3 * page + 5, 700, 2 * page - 1]
     counts = [3, 2, 1, 9, 20, 4]
     n = sum(counts)
     new = [int(x) for x in rng.integers(0, 2 * page, n)]
     new[0] = new[4] = 0
-    cache, pool, slots, groups = beams(rng, lens, counts, new, kv, dim, page)
-    queries = [int(x) for x in rng.integers(0, 4, n)]
+    # (a window bounds what a call reads: there, requests without rows make it a large one)
+    more = 1000 // kv if shared and window else 0
+    cache, pool, slots, groups = beams(rng, lens, counts, new, kv, dim, page, shared=shared, idle=more)
+    queries = [int(x) for x in rng.integers(0, 4, n)] + [0] * more
+    slots, groups = slots + [0] * more, groups + [n + more]
     at = starts_of(queries)
     q = rows(rng, at[-1], kv * group, dim, dtype, 0.3)
     lse = torch.full(q.shape[:2], 7.0, device="cuda")
