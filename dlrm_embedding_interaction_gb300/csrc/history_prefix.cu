@@ -9,10 +9,8 @@
 // tiles of all kv heads, chunk by chunk, into equal parts for the second launch.
 //
 // The second launch is history_attention's method (history_attention.cu: layouts of
-// keys and values, scales, splits of fp32, the join of parts) with more rows a block of
-// events: WR warps share a ring of blocks and take MT MMA row tiles each, and a warp
-// converts a block's codes once for its MT tiles. A block of one request's own events
-// is multiplied with the row tiles that hold its rows alone, and masked for the others'.
+// keys and values, scales, splits of fp32, the join of parts) over a tile's list of
+// blocks; a block of one request's own events is masked for the other rows.
 #include "history_prefix.cuh"
 
 namespace dlrm {
@@ -204,17 +202,10 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
       if (i < tiles) {
         y.row0 = i * p.rows;
         y.rows = min(p.rows, rows - y.row0);
-        // own blocks of the rows of each of a set's warps, one a warp and chunk
-        const int each = p.rows * p.split / kWarps;
-        int m0 = holds(y.row0, 0), m1 = m0;
+        const int m0 = holds(y.row0, 0), m1 = holds(y.row0 + y.rows - 1, m0);
         y.member0 = b0 + m0;
-        for (int r = 0; r < y.rows; r += each) {
-          if (r > 0) m0 = holds(y.row0 + r, m1);
-          m1 = holds(y.row0 + min(y.rows, r + each) - 1, m0);
-          const int blocks = members[m1].first + blocks_of(members[m1]) - members[m0].first;
-          y.own = max(y.own, (blocks + p.split - 1) / p.split);
-        }
         y.member1 = b0 + m1;
+        y.blocks = y.shared_blocks + members[m1].first + blocks_of(members[m1]) - members[m0].first;
       }
       p.found[base + i] = y;
     }
@@ -231,7 +222,6 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
   __threadfence();
   if (bad && t == 0) flag(h.err, DLRM_ERRBIT_OFFSETS);
   int work = 0, dense = 0;
-  const int cost = kCostBlocks / p.split;
   const int per = (last_place - first_place + kPlanThreads - 1) / kPlanThreads;
   const int mine0 = min(last_place, first_place + t * per), mine1 = min(last_place, mine0 + per);
   const auto tile_at = [&](int i) {
@@ -245,27 +235,26 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
   Tile only{};                                    // the thread's tile, if it is one
   for (int i = mine0; i < mine1; ++i) {
     only = tile_at(i);
-    const int chunks = chunks_of(only, p.split);
-    work += chunks > 0 ? (chunks + cost) * h.n_heads : 0;
+    const int chunks = chunks_of(only);
+    work += chunks > 0 ? (chunks + kCost) * h.n_heads : 0;
     dense += chunks > 0;
   }
-  // the work of a CTA: of all, but kLeastBlocks at least where pieces are longer on average
+  // the work of a CTA: of all, but kLeast chunks at least where pieces are longer on average
   int total, n_tiles;
   scan(work, sums, total);
   int place = scan(dense, sums, n_tiles);
   const int pieces = n_tiles * h.n_heads;
-  const Cuts cuts(max((total + p.grid - 1) / p.grid, max(min(kLeastBlocks / p.split + cost, pieces ? total / pieces : 1), 1)),
-                  p.split);
+  const Cuts cuts(max((total + p.grid - 1) / p.grid, max(min(kLeast + kCost, pieces ? total / pieces : 1), 1)));
   work = 0;
   for (int i = mine0; i < mine1; ++i) {
-    const int chunks = chunks_of(per == 1 ? only : tile_at(i), p.split);
+    const int chunks = chunks_of(per == 1 ? only : tile_at(i));
     work += chunks > 0 ? cuts.work(chunks) * h.n_heads : 0;
   }
   int at = scan(work, sums, total);
   const int ctas = cuts.from(total);
   for (int i = mine0; i < mine1; ++i) {
     Tile y = per == 1 ? only : tile_at(i);
-    const int chunks = chunks_of(y, p.split);
+    const int chunks = chunks_of(y);
     if (chunks == 0) continue;
     y.first = at;
     p.tiles[place] = y;
@@ -289,12 +278,12 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
       int4* to = reinterpret_cast<int4*>(&x.tile);
 #pragma unroll
       for (int i = 0; i < static_cast<int>(sizeof(Tile) / 16); ++i) to[i] = __ldcg(from + i);
-      const int chunks = chunks_of(x.tile, p.split), length = cuts.work(chunks);
+      const int chunks = chunks_of(x.tile), length = cuts.work(chunks);
       x.piece = static_cast<unsigned>(w - x.tile.first) / static_cast<unsigned>(length);
       const int start = x.tile.first + x.piece * length, off = w - start;
-      if (chunks > cuts.whole && off >= cuts.near && off < length - cuts.near)
+      if (chunks > kWhole && off >= kNear && off < length - kNear)
         x.chunk = cuts.chunk(c, start, chunks);
-      else if (chunks > cuts.whole ? off >= cuts.near : off >= length / 2)
+      else if (chunks > kWhole ? off >= kNear : off >= length / 2)
         ++x.piece;
     }
     p.cuts[c] = x;

@@ -11,9 +11,11 @@ namespace dlrm {
 namespace prefix {
 
 
-constexpr int kWholeBlocks = 16;                 // blocks of a piece that is never split
-constexpr int kLeastBlocks = 16;                 // blocks of a CTA at least, where pieces are longer
-constexpr int kCostBlocks = 12;                  // blocks in whose time a piece is begun and ended
+constexpr int kWhole = 4;                        // chunks of a piece that is never split
+constexpr int kLeast = 4;                        // chunks of a CTA at least, where pieces are longer
+constexpr int kCost = 3;                         // chunks in whose time a piece is begun and ended
+constexpr int kNear = 3;                         // a cut as near as this to a piece's end moves there
+static_assert(kWhole >= 2 * kNear - kCost, "a piece that is split has an inside");
 constexpr int kWeights = 32;                     // parts whose weights lie in shared memory at once
 
 // What the plan knows of a request with rows, and of the tiles.
@@ -25,7 +27,7 @@ struct Member {
 };
 static_assert(sizeof(Member) == kPrefixMember, "scratch size of a member");
 struct Tile {
-  int32_t first, own;                            // work before it, as Cuts counts it; chunks of its requests' own events
+  int32_t first, blocks;                         // work before it, as Cuts counts it; its blocks
   int32_t q0, row0, rows;                        // the group's first query row; rows among the group's
   int32_t member0, member1;                      // first and last request with rows in the tile
   int32_t slot;                                  // whose table gives the shared pages
@@ -42,33 +44,28 @@ struct Cut {                                     // where a CTA begins
 };
 static_assert(sizeof(Cut) == kPrefixCut, "scratch size of a cut");
 
-// Chunks of a tile: a block of shared events for each set of warps, then one of their own events
-// for each warp; one even where there is nothing to read, which writes zeros.
-__device__ __forceinline__ int shared_chunks(const Tile& t, int split) {
-  return static_cast<unsigned>(t.shared_blocks + split - 1) / static_cast<unsigned>(split);
-}
-__device__ __forceinline__ int chunks_of(const Tile& t, int split) {
-  return t.rows > 0 ? max(shared_chunks(t, split) + t.own, 1) : 0;
+// Chunks of a tile, a block a warp; one even where there is nothing to read, which writes zeros.
+__device__ __forceinline__ int chunks_of(const Tile& t) {
+  return t.rows > 0 ? max((t.blocks + kWarps - 1) / kWarps, 1) : 0;
 }
 // Cuts the pieces (a tile and kv head) of a call evenly over the CTAs. A piece counts as its
-// chunks and `cost` more, as it takes time to begin and to end, and, from four CTAs' work on, as a
+// chunks and kCost more, as it takes time to begin and to end, and, from four CTAs' work on, as a
 // whole number of them, so that no CTA has parts of two such pieces. CTA c begins at c `each` of
-// the whole, but where that lies within `near` of a piece's ends, or in a piece too short
+// the whole, but where that lies within kNear of a piece's ends, or in a piece too short
 // to be split, it begins with that piece or with the next.
 struct Cuts {
-  int each, cost, near, whole;
-  __device__ __forceinline__ Cuts(int each, int split)
-      : each(each), cost(kCostBlocks / split), near(kCostBlocks / split), whole(kWholeBlocks / split) {}
+  int each;
+  __device__ __forceinline__ explicit Cuts(int each) : each(each) {}
   __device__ __forceinline__ int work(int chunks) const {
-    const int n = chunks + cost;
+    const int n = chunks + kCost;
     return n >= 4 * each ? n / each * each : n;
   }
   // The first CTA that begins at or after `w`.
   __device__ __forceinline__ int from(int w) const { return static_cast<unsigned>(w + each - 1) / static_cast<unsigned>(each); }
   // CTAs [first, first + n) begin inside the piece of `chunks` chunks at `start`.
   __device__ __forceinline__ int inside(int start, int chunks, int& first) const {
-    first = from(start + near);
-    return chunks <= whole ? 0 : max(from(start + work(chunks) - near) - first, 0);
+    first = from(start + kNear);
+    return chunks <= kWhole ? 0 : max(from(start + work(chunks) - kNear) - first, 0);
   }
   // The chunk at which CTA c, one of them, begins.
   __device__ __forceinline__ int chunk(int c, int start, int chunks) const {
@@ -87,7 +84,7 @@ struct Params {
   const int32_t* groups;
   int n_groups;
   int group;                                     // query heads of a kv head
-  int rows, split;                               // of a tile; warps that split a chunk's blocks
+  int rows;                                      // of a tile
   int grid;                                      // CTAs of the second launch
   int vec_q, vec_out;                            // four elements can be loaded, stored at once
   int32_t* arrived;                              // CTAs of the plan that are done
@@ -129,43 +126,43 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 // SPLIT: queries and weights as an f16 head and rest, in two MMA rows: fp32 rows, and
 // 16-bit ones that are no more than 8, whose other MMA rows would be empty. Without it
 // fp16 weights have their rest in a product of its own (an output has 11 bits too).
-template <int D, int DT, bool SPLIT, int MT, int WR>
+template <int D, bool SPLIT>
 struct Shape {
-  static constexpr int kTile = SPLIT ? 8 : 16;    // rows of an MMA tile
-  static constexpr int kRows = kTile * MT * WR;
-  static constexpr int kSets = kWarps / WR;       // sets of warps, a ring and a block of each chunk each
-  // blocks of a stage: warps that share a ring meet once a stage (at head_dim 128 there is
-  // space for one)
-  static constexpr int kPer = WR == 1 || (D == 128 && WR == 2) ? 1 : 2;
-  static constexpr int kStages = WR > 1 || D == 128 ? 3 : 4;
-  static constexpr int kOwn = WR == 1 ? 0 : D == 128 ? 1 : 2;   // blocks of own events, a warp (WR = 1: in its ring)
+  static constexpr int kRows = SPLIT ? 8 : 16;    // of a tile
+  static constexpr int kStages = D == 128 ? 3 : 4;
   static constexpr int kBytes = 2 * kBlock * D;   // keys and values of a block
   static constexpr int kStride = D + 4;           // of a row's sums in shared memory
   static constexpr int kPartial = kRows * (D + 2);   // of a part in scratch: sums, maxima, sums of weights
-  static constexpr int kShared = kSets * kStages * kPer * kBytes;
-  static constexpr int kRing = kShared + kWarps * kOwn * kBytes;
-  static constexpr int kJoin = (kSets * kRows * (kStride + 2) + kWeights * kRows) * 4;
+  static constexpr int kRing = kWarps * kStages * kBytes;
+  static constexpr int kJoin = (kWarps * kRows * (kStride + 2) + 2 * kWeights * kRows) * 4;
   static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
 };
 
-template <int D, int DT, bool SPLIT, int MT, int WR>
-__global__ void __launch_bounds__(kThreads, D == 128 ? 2 : MT == 1 ? 3 : 2)
+// Tiles of 16 rows (8 of fp32), a block a warp, whatever the rows of a group: two row tiles a
+// warp, which halves the conversions, and warps that share a block, which reads it once for up
+// to 64 rows, both took longer (64 users, 1500 events, 13 beams of 4 rows: 44 and 47 us
+// against 43; 2 x 50,000 events at head_dim 128, 52 rows: 175 with shared blocks against 145,
+// 1.4 times the time of the bytes). Each step of a warp is a chain of waits, so warps that go
+// on by themselves are worth more than shorter work; tiles that follow one another find the
+// events in L2.
+template <int D, int DT, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
 prefix_attention_kernel(const __grid_constant__ Params p) {
-  using Sh = Shape<D, DT, SPLIT, MT, WR>;
+  using Sh = Shape<D, SPLIT>;
   constexpr bool kRest = !SPLIT && DT == DLRM_DTYPE_FP16;
-  constexpr int kTile = Sh::kTile, kRows = Sh::kRows, kSets = Sh::kSets, kStages = Sh::kStages;
-  constexpr int kStride = Sh::kStride, kPartial = Sh::kPartial, kPer = Sh::kPer;
+  constexpr int kRows = Sh::kRows, kStages = Sh::kStages, kStride = Sh::kStride, kPartial = Sh::kPartial;
   constexpr int KW = D / 16;                      // key words of a thread and event tile
   constexpr int VW = D / 32;                      // value words of a thread and event
   constexpr int NT = D / 8;                       // n tiles of the output
-  constexpr int kPairsO = SPLIT ? 1 : 2;          // pairs of output values of a thread and n tile
-  constexpr int kR2 = SPLIT ? 1 : 2;              // rows of a thread and row tile
+  constexpr int kR2 = SPLIT ? 1 : 2;              // rows of a thread
   extern __shared__ __align__(128) unsigned char smem[];
-  // after the events: sums of each set and row, then maxima, sums of weights, weights of parts
+  // after the events: sums of each warp and row, then maxima, sums of weights; of parts, weights
+  // and sums of weights
   float (*joined)[kRows][kStride] = reinterpret_cast<float (*)[kRows][kStride]>(smem);
-  float (*tops)[kRows] = reinterpret_cast<float (*)[kRows]>(&joined[kSets][0][0]);
-  float (*totals)[kRows] = reinterpret_cast<float (*)[kRows]>(&tops[kSets][0]);
-  float (*weight)[kRows] = reinterpret_cast<float (*)[kRows]>(&totals[kSets][0]);
+  float (*tops)[kRows] = reinterpret_cast<float (*)[kRows]>(&joined[kWarps][0][0]);
+  float (*totals)[kRows] = reinterpret_cast<float (*)[kRows]>(&tops[kWarps][0]);
+  float (*weight)[kRows] = reinterpret_cast<float (*)[kRows]>(&totals[kWarps][0]);
+  float (*weight_sum)[kRows] = reinterpret_cast<float (*)[kRows]>(&weight[kWeights][0]);
   __shared__ float row_top[kRows], row_total[kRows];
   __shared__ int odd[kRows + 1];
   __shared__ int see_end[kRows], see_gap0[kRows], see_gap1[kRows], row_member[kRows];
@@ -175,30 +172,27 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
   __shared__ int n_members, n_arrived;
   __shared__ int clear_end, clear_gap;            // events that every row of the tile sees lie between
   __shared__ int m_lo[kRows], m_hi[kRows], m_first[kRows];
-  __shared__ int own_first[WR], own_end[WR];      // blocks of own events of the rows of a set's warps
   __shared__ Member m_of[kRows];
 
   const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
-  const int set = warp / WR, wr = warp % WR;
   const int g = lane / 4, c = lane % 4;
   const int G = p.h.page_tokens, H = p.h.n_heads, shift = __ffs(G) - 1;   // G: a power of two
   const unsigned group = p.group;
-  unsigned char* ring = smem + set * kStages * kPer * Sh::kBytes;
-  const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
-  // what this thread copies of a block: from its first 16-byte chunk of a side on
+  unsigned char* const ring = smem + warp * kStages * Sh::kBytes;
+  // what this thread copies of a block: 16-byte chunks of keys and values, 32 apart
   constexpr int kSide = 2 * D;                    // chunks of a side
-  static_assert(kSide % (kWarp * WR) == 0 || 2 * kSide == kWarp * WR, "chunks of a thread");
-  constexpr int kOwn = Sh::kOwn;
-  unsigned char* const own_ring = smem + Sh::kShared + warp * kOwn * Sh::kBytes;
-  const int id = (wr * kWarp + lane) % kSide;
-  const uint32_t dst_k = ring_at + key_offset<D>(id / (D / 16), id % (D / 16));
-  const uint32_t dst_v = ring_at + kBlock * D + value_offset<D>(id / (D / 16), id % (D / 16));
-  const uint8_t* const src_k = p.h.k_codes + id * 16;
-  const uint8_t* const src_v = p.h.v_codes + id * 16;
+  const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+  const uint32_t dst_k = ring_at + key_offset<D>(lane / (D / 16), lane % (D / 16));
+  const uint32_t dst_v = ring_at + kBlock * D + value_offset<D>(lane / (D / 16), lane % (D / 16));
+  const uint8_t* const src_k = p.h.k_codes + lane * 16;
+  const uint8_t* const src_v = p.h.v_codes + lane * 16;
+  // those of a thread lie 8 events apart, or a multiple, for which the swizzles of keys and
+  // values are alike, or 4, for which that of values changes in one bit
+  constexpr uint32_t kFlip = D == 128 ? 64 : 0;
   pdl_wait();
   pdl_trigger();
   const Cut from = p.cuts[blockIdx.x], to = p.cuts[blockIdx.x + 1];
-  const Cuts cuts(from.each, kSets);
+  const Cuts cuts(from.each);
   int place = from.place, head = from.piece, begin = from.chunk;
   Tile s = from.tile;
   bool fresh = true;                              // a tile whose requests are not known yet
@@ -214,7 +208,7 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
       if (ends()) break;
       s = p.tiles[place];
     }
-    const int chunks = chunks_of(s, kSets);
+    const int chunks = chunks_of(s);
     const int chunk0 = begin, chunk1 = place == to.place && head == to.piece ? to.chunk : chunks;
     const int piece = s.first + head * cuts.work(chunks);   // where it begins, as Cuts counts
     const int kv = head;
@@ -226,32 +220,29 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
     // Everything below is a chain of loads, so what does not hang together starts together
     Member mine{};
     if (fresh && warp == 0 && s.member0 + lane <= s.member1) mine = p.members[s.member0 + lane];
-    float x[MT][2][KW][4];
+    float x[2][KW][4];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int r2 = 0; r2 < 2; ++r2) {
+      const int r = SPLIT ? g : g + 8 * r2;
+      const int row = s.row0 + min(r, rows - 1);
+      const int query = group == 1 ? row : static_cast<unsigned>(row) / group;
+      const int64_t q_at = (s.q0 + static_cast<int64_t>(query)) * p.a.ld_q +
+                           (kv * p.group + row - query * p.group) * p.a.ld_q_head;
 #pragma unroll
-      for (int r2 = 0; r2 < 2; ++r2) {
-        const int r = (wr * MT + mt) * kTile + (SPLIT ? g : g + 8 * r2);
-        const bool in = r < rows;
-        const int row = s.row0 + min(r, rows - 1);
-        const int query = group == 1 ? row : static_cast<unsigned>(row) / group;
-        const int64_t q_at = (s.q0 + static_cast<int64_t>(query)) * p.a.ld_q +
-                             (kv * p.group + row - query * p.group) * p.a.ld_q_head;
+      for (int w = 0; w < KW; ++w) {
+        if (r < rows && !(SPLIT && r2)) {
+          load_four<DT>(x[r2][w], p.a.q, q_at + key_element<D>(c, w), p.vec_q);
+        } else {
 #pragma unroll
-        for (int w = 0; w < KW; ++w) {
-          if (in && !(SPLIT && r2)) {
-            load_four<DT>(x[mt][r2][w], p.a.q, q_at + key_element<D>(c, w), p.vec_q);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[mt][r2][w][e] = 0.f;
-          }
+          for (int e = 0; e < 4; ++e) x[r2][w][e] = 0.f;
         }
       }
+    }
 
-    // ---- the warp's blocks, one a chunk: first shared ones, its set's, then those of its own rows'
-    // requests; lane l knows block l of the 32 at hand (info) and of the 32 after them (ahead)
-    const int n_shared = shared_chunks(s, kSets), count = chunk1 - chunk0;
-    const int first_own = max(n_shared - chunk0, 0);   // chunks from here on are own events'
+    // ---- blocks of this warp: n0, n0 + kWarps, ..., shared ones first, then the requests' own;
+    // lane l knows block l of the 32 at hand (info) and of the 32 after them (ahead)
+    const int n0 = chunk0 * kWarps + warp, n1 = min(chunk1 * kWarps, s.blocks);
+    const int count = n0 < n1 ? (n1 - n0 + kWarps - 1) / kWarps : 0;
     struct Info {
       int64_t codes;                              // first byte of the block's codes; -1: nothing to read
       int t0, member;                             // first event; whose own, or -1: shared
@@ -270,16 +261,16 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
     };
     auto look_shared = [&](int i) {
       Info x{-1, 0, -1, 0.f, 0.f};
-      const int n = (chunk0 + i) * kSets + set;
-      if (i < count && i < first_own && n < s.shared_blocks) {
+      const int n = n0 + i * kWarps;
+      if (i < count && n < s.shared_blocks) {
         x.t0 = (n < s.shared_sinks ? n : n - s.shared_sinks + s.shared0) * kBlock;
         open(x, s.slot);
       }
       return x;
     };
     auto look_own = [&](int i, Info& x) {
-      const int n = own_first[wr] + (chunk0 + i - n_shared) * kSets + set;
-      if (i < count && i >= first_own && n < own_end[wr]) {
+      const int n = n0 + i * kWarps - s.shared_blocks;
+      if (i < count && n >= 0) {
         int k = 0;                                // the last request whose blocks begin at or before it
         for (int d = n_members; d > 1;) {
           const int half = d / 2;
@@ -327,96 +318,34 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
           clear_end = INT32_MAX;
           clear_gap = 0;
         }
-        __syncwarp();
-        // own blocks of the rows of each of a set's warps
-        if (lane < WR) {
-          constexpr int kMine = kRows / WR;
-          const auto holds = [&](int row) {       // the last request that begins at or before it
-            int i = 0;
-            for (int d = n_members; d > 1;) {
-              const int half = d / 2;
-              if (m_lo[i + half] <= row) i += half;
-              d -= half;
-            }
-            return i;
-          };
-          const bool any = rows > lane * kMine;
-          const int last = any ? holds(min(rows, (lane + 1) * kMine) - 1) : 0;
-          own_first[lane] = any ? m_first[holds(lane * kMine)] : 0;
-          own_end[lane] = any ? m_first[last] + blocks_of(m_of[last]) : 0;
-        }
       }
       __syncthreads();
     }
     look_own(lane, info);
     look_own(kWarp + lane, ahead);
     int base = 0;                                 // blocks [base, base + 32) are in info
-    auto codes_of = [&](int i) {
-      const int64_t mine_codes = i - base < kWarp ? info.codes : ahead.codes;
-      return __shfl_sync(0xffffffffu, mine_codes, i % kWarp);
-    };
-    auto fetch_block = [&](int i) {               // by the set's warps
-      if (i < (kOwn ? min(first_own, count) : count)) {
-        const int64_t codes = codes_of(i);
+    auto fetch = [&](int i) {
+      if (i < count) {
+        const int64_t mine_codes = i - base < kWarp ? info.codes : ahead.codes;
+        const int64_t codes = __shfl_sync(0xffffffffu, mine_codes, i % kWarp);
         if (codes >= 0) {
-          const uint32_t dst = (i % (kStages * kPer)) * Sh::kBytes;
-          constexpr int kStep = kWarp * WR;       // 16-byte chunks of the set's threads
-          if (kSide % kStep == 0) {
-            // a thread's chunks lie 8 events apart, or a multiple, for which the swizzles of keys
-            // and values are alike, or 4, for which that of values changes in one bit
-            constexpr int kApart = kStep / (D / 16) % 8;
-            static_assert(kSide % kStep != 0 || kApart == 0 || (kApart == 4 && D == 128), "swizzle");
-            constexpr uint32_t kFlip = kApart == 4 ? 64 : 0;
+          const uint32_t at = (i % kStages) * Sh::kBytes;
 #pragma unroll
-            for (int x = 0; x < kSide / kStep; ++x) copy16(dst + dst_k + x * kStep * 16, src_k + codes + x * kStep * 16);
+          for (int y = 0; y < kSide / kWarp; ++y) copy16(dst_k + at + y * kWarp * 16, src_k + codes + y * kWarp * 16);
 #pragma unroll
-            for (int x = 0; x < kSide / kStep; ++x)
-              copy16(dst + (x % 2 ? dst_v ^ kFlip : dst_v) + x * kStep * 16, src_v + codes + x * kStep * 16);
-          } else {                                // two warps a side
-            copy16(dst + (wr < WR / 2 ? dst_k : dst_v), (wr < WR / 2 ? src_k : src_v) + codes);
-          }
-        }
-      }
-    };
-    auto fetch = [&](int i) {                     // a stage
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) fetch_block(i + j);
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    auto fetch_own = [&](int i) {                 // by the warp, for itself
-      if (kOwn > 0 && i < count) {
-        const int64_t codes = codes_of(i);
-        if (codes >= 0) {
-          const uint32_t dst =
-              static_cast<uint32_t>(__cvta_generic_to_shared(own_ring)) + (kOwn == 2 ? i % 2 : 0) * Sh::kBytes;
-#pragma unroll
-          for (int x = 0; x < kSide / kWarp; ++x) {
-            const int c16 = x * kWarp + lane, t = c16 / (D / 16), ch = c16 % (D / 16);
-            copy16(dst + key_offset<D>(t, ch), p.h.k_codes + codes + c16 * 16);
-            copy16(dst + kBlock * D + value_offset<D>(t, ch), p.h.v_codes + codes + c16 * 16);
-          }
+          for (int y = 0; y < kSide / kWarp; ++y)
+            copy16((y % 2 ? dst_v ^ kFlip : dst_v) + at + y * kWarp * 16, src_v + codes + y * kWarp * 16);
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    auto set_barrier = [&] {
-      if (WR == 1)
-        __syncwarp();
-      else if (WR == kWarps)
-        __syncthreads();
-      else if (set == 0)
-        asm volatile("bar.sync 1, %0;" ::"n"(WR * kWarp) : "memory");
-      else
-        asm volatile("bar.sync 2, %0;" ::"n"(WR * kWarp) : "memory");
-    };
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) fetch(i * kPer);
-    if (kOwn > 0 && first_own == 0) fetch_own(0);
+    for (int i = 0; i < kStages - 1; ++i) fetch(i);
 
     // ---- what each row sees (rows past the last stand for it)
     if (fresh) {
-      for (int r = threadIdx.x; r < kRows; r += kThreads) {
-        const int row = min(r, rows - 1), of = s.row0 + row;
+      if (threadIdx.x < kRows) {
+        const int r = threadIdx.x, row = min(r, rows - 1), of = s.row0 + row;
         int i = 0;                                // the last request that begins at or before it
         for (int d = n_members; d > 1;) {
           const int half = d / 2;
@@ -442,53 +371,48 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
 
     // ---- fragments of the queries, scaled to f16; a negative softmax scale is
     // theirs, so that the factors of the scores are positive
-    uint32_t qa[MT][KW][4];
-    float qf[MT][2];
+    uint32_t qa[KW][4];
+    float qf[kR2];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int r2 = 0; r2 < kR2; ++r2) {
+      float big = 0.f;
 #pragma unroll
-      for (int r2 = 0; r2 < kR2; ++r2) {
-        float big = 0.f;
+      for (int w = 0; w < KW; ++w)
 #pragma unroll
-        for (int w = 0; w < KW; ++w)
+        for (int e = 0; e < 4; ++e) big = fmaxf(big, fabsf(x[r2][w][e]));
+      big = quad_max(big);
+      const int ex = max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -100);
+      const float f = copysignf(pow2f(min(8 - ex, 127)), p.a.scale);
+      qf[r2] = pow2f(max(ex - 8, -126)) * fabsf(p.a.scale) * kLog2e;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) big = fmaxf(big, fabsf(x[mt][r2][w][e]));
-        big = quad_max(big);
-        const int ex = max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -100);
-        const float f = copysignf(pow2f(min(8 - ex, 127)), p.a.scale);
-        qf[mt][r2] = pow2f(max(ex - 8, -126)) * fabsf(p.a.scale) * kLog2e;
+      for (int w = 0; w < KW; ++w)
 #pragma unroll
-        for (int w = 0; w < KW; ++w)
+        for (int e = 0; e < 4; ++e) x[r2][w][e] *= f;
+    }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[mt][r2][w][e] *= f;
-      }
-#pragma unroll
-      for (int w = 0; w < KW; ++w) {
-        const float (&x0)[4] = x[mt][0][w], (&x1)[4] = x[mt][1][w];
-        qa[mt][w][0] = pack_f16x2(x0[0], x0[1]);
-        qa[mt][w][2] = pack_f16x2(x0[2], x0[3]);
-        if (SPLIT) {
-          const float2 h0 = f16x2_to_float2(qa[mt][w][0]), h1 = f16x2_to_float2(qa[mt][w][2]);
-          qa[mt][w][1] = pack_f16x2((x0[0] - h0.x) * 2048.f, (x0[1] - h0.y) * 2048.f);
-          qa[mt][w][3] = pack_f16x2((x0[2] - h1.x) * 2048.f, (x0[3] - h1.y) * 2048.f);
-        } else {
-          qa[mt][w][1] = pack_f16x2(x1[0], x1[1]);
-          qa[mt][w][3] = pack_f16x2(x1[2], x1[3]);
-        }
+    for (int w = 0; w < KW; ++w) {
+      const float (&x0)[4] = x[0][w], (&x1)[4] = x[1][w];
+      qa[w][0] = pack_f16x2(x0[0], x0[1]);
+      qa[w][2] = pack_f16x2(x0[2], x0[3]);
+      if (SPLIT) {
+        const float2 h0 = f16x2_to_float2(qa[w][0]), h1 = f16x2_to_float2(qa[w][2]);
+        qa[w][1] = pack_f16x2((x0[0] - h0.x) * 2048.f, (x0[1] - h0.y) * 2048.f);
+        qa[w][3] = pack_f16x2((x0[2] - h1.x) * 2048.f, (x0[3] - h1.y) * 2048.f);
+      } else {
+        qa[w][1] = pack_f16x2(x1[0], x1[1]);
+        qa[w][3] = pack_f16x2(x1[2], x1[3]);
       }
     }
 
     // ---- events
-    float2 o[MT][NT][kPairsO];
-    float top[MT][2], sum[MT][2];
+    float2 o[NT][kR2];
+    float top[kR2], sum[kR2];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      top[mt][0] = top[mt][1] = -INFINITY;
-      sum[mt][0] = sum[mt][1] = 0.f;
+    for (int r2 = 0; r2 < kR2; ++r2) {
+      top[r2] = -INFINITY;
+      sum[r2] = 0.f;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < kPairsO; ++i) o[mt][nt][i] = make_float2(0.f, 0.f);
+      for (int nt = 0; nt < NT; ++nt) o[nt][r2] = make_float2(0.f, 0.f);
     }
     for (int it = 0; it < count; ++it) {
       if (it - base == kWarp) {
@@ -497,44 +421,23 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
         ahead = look_shared(base + kWarp + lane);
         look_own(base + kWarp + lane, ahead);
       }
-      const unsigned char* kb;
-      if (kOwn == 0 || it < first_own) {
-        if (it % kPer == 0) {
-          asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-          set_barrier();                          // this stage is there, and the one before it done with
-          fetch(it + (kStages - 1) * kPer);
-        }
-        if (kOwn > 0 && it == first_own - 1) fetch_own(first_own);
-        kb = ring + (it % (kStages * kPer)) * Sh::kBytes;
-      } else {
-        if (kOwn == 1 && it > first_own) {
-          __syncwarp();                           // the block before is done with
-          fetch_own(it);
-        }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        __syncwarp();
-        if (kOwn == 2) fetch_own(it + 1);
-        kb = own_ring + (kOwn == 2 ? it % 2 : 0) * Sh::kBytes;
-      }
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+      __syncwarp();                               // block `it` is there, and block it - 1 done with
+      fetch(it + kStages - 1);
       const int at = it % kWarp;
       const bool there = __shfl_sync(0xffffffffu, info.codes >= 0, at);
       const int member = __shfl_sync(0xffffffffu, info.member, at);
       const float ks = __shfl_sync(0xffffffffu, info.ks, at);
       const float vs = __shfl_sync(0xffffffffu, info.vs, at);
       const int t0 = __shfl_sync(0xffffffffu, info.t0, at);
-      if (!there || rows <= wr * MT * kTile) continue;
-      // rows of the tile that the block is for; whether they all see all of it
-      int lo = 0, hi = kRows;
-      if (member >= 0) {
-        lo = m_lo[member];
-        hi = m_hi[member];
-        if (hi <= wr * MT * kTile || lo >= (wr + 1) * MT * kTile) continue;
-      }
+      if (!there) continue;
+      // whether every row of the tile sees all of the block
       const bool clear = member < 0 && t0 + kBlock <= clear_end && t0 >= clear_gap;
+      const unsigned char* kb = ring + (it % kStages) * Sh::kBytes;
       const unsigned char* vb = kb + kBlock * D;
 
       // S = Q K^T
-      float sc[MT][kBlock / 8][4];
+      float sc[kBlock / 8][4];
 #pragma unroll
       for (int j = 0; j < kBlock / 8; ++j) {
         uint32_t kw[KW];
@@ -553,133 +456,111 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
           }
         }
 #pragma unroll
-        for (int w = 0; w < KW; ++w) {
-          const uint32_t b0 = e4m3x2_lo_to_f16x2(kw[w]), b1 = e4m3x2_hi_to_f16x2(kw[w]);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) mma_f16_from(sc[mt][j], qa[mt][w], b0, b1, w > 0);
-        }
+        for (int w = 0; w < KW; ++w)
+          mma_f16_from(sc[j], qa[w], e4m3x2_lo_to_f16x2(kw[w]), e4m3x2_hi_to_f16x2(kw[w]), w > 0);
       }
       if (SPLIT) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int j = 0; j < kBlock / 8; ++j) {
-            sc[mt][j][0] = fmaf(sc[mt][j][2], 1.f / 2048.f, sc[mt][j][0]);
-            sc[mt][j][1] = fmaf(sc[mt][j][3], 1.f / 2048.f, sc[mt][j][1]);
-          }
+        for (int j = 0; j < kBlock / 8; ++j) {
+          sc[j][0] = fmaf(sc[j][2], 1.f / 2048.f, sc[j][0]);
+          sc[j][1] = fmaf(sc[j][3], 1.f / 2048.f, sc[j][1]);
+        }
       }
       if (!clear) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int r2 = 0; r2 < kR2; ++r2) {
-            const int r = (wr * MT + mt) * kTile + g + 8 * r2;
-            const int row = min(r, rows - 1);
-            // of the thread's events t0 + 2 c + 8 j (+ 1), those before `some`, but for a gap
-            const int some = row >= lo && row < hi ? see_end[r] - t0 - 2 * c : 0;
-#pragma unroll
-            for (int j = 0; j < kBlock / 8; ++j) {
-              if (8 * j >= some) sc[mt][j][2 * r2] = -INFINITY;
-              if (8 * j + 1 >= some) sc[mt][j][2 * r2 + 1] = -INFINITY;
-            }
-            if (p.a.window > 0) {
-              const int gap0 = see_gap0[r] - t0 - 2 * c, gap1 = see_gap1[r] - t0 - 2 * c;
-#pragma unroll
-              for (int j = 0; j < kBlock / 8; ++j) {
-                if (8 * j >= gap0 && 8 * j < gap1) sc[mt][j][2 * r2] = -INFINITY;
-                if (8 * j + 1 >= gap0 && 8 * j + 1 < gap1) sc[mt][j][2 * r2 + 1] = -INFINITY;
-              }
-            }
-          }
-      }
-      // weights: exp2 of the scores times the factors, less the running maximum. All rows
-      // side by side: a row alone is a chain of waits
-      float big[MT][kR2], alpha[MT][2];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+        // rows of the tile that the block is for
+        const int lo = member < 0 ? 0 : m_lo[member], hi = member < 0 ? kRows : m_hi[member];
 #pragma unroll
         for (int r2 = 0; r2 < kR2; ++r2) {
-          float x0 = fmaxf(sc[mt][0][2 * r2], sc[mt][0][2 * r2 + 1]), x1 = fmaxf(sc[mt][1][2 * r2], sc[mt][1][2 * r2 + 1]);
-          x0 = fmaxf(x0, fmaxf(sc[mt][2][2 * r2], sc[mt][2][2 * r2 + 1]));
-          x1 = fmaxf(x1, fmaxf(sc[mt][3][2 * r2], sc[mt][3][2 * r2 + 1]));
-          big[mt][r2] = fmaxf(x0, x1);
-        }
-#pragma unroll
-      for (int x = 1; x <= 2; x *= 2)
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int r2 = 0; r2 < kR2; ++r2)
-            big[mt][r2] = fmaxf(big[mt][r2], __shfl_xor_sync(0xffffffffu, big[mt][r2], x));
-      bool grew = false;
-      float f[MT][kR2], off[MT][kR2];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int r2 = 0; r2 < kR2; ++r2) {
-          // (the factor is not zero, even for a softmax scale of zero: a masked score is -infinity)
-          f[mt][r2] = fmaxf(qf[mt][r2] * ks, 1e-37f);
-          const float m = fmaxf(top[mt][r2], ceilf(big[mt][r2] * f[mt][r2]));
-          const float ref = m == -INFINITY ? 0.f : m;
-          off[mt][r2] = kLift - ref;
-          alpha[mt][r2] = exp2_approx(top[mt][r2] - ref);
-          grew |= m > top[mt][r2];
-          top[mt][r2] = m;
-        }
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int r2 = 0; r2 < kR2; ++r2) {
-          float2 add = make_float2(0.f, 0.f);
-          const float2 f2 = make_float2(f[mt][r2], f[mt][r2]), off2 = make_float2(off[mt][r2], off[mt][r2]);
+          const int r = g + 8 * r2, row = min(r, rows - 1);
+          // of the thread's events t0 + 2 c + 8 j (+ 1), those before `some`, but for a gap
+          const int some = row >= lo && row < hi ? see_end[r] - t0 - 2 * c : 0;
 #pragma unroll
           for (int j = 0; j < kBlock / 8; ++j) {
-            const float2 e = fma2(make_float2(sc[mt][j][2 * r2], sc[mt][j][2 * r2 + 1]), f2, off2);
-            sc[mt][j][2 * r2] = exp2_approx(e.x);
-            sc[mt][j][2 * r2 + 1] = exp2_approx(e.y);
-            add = fma2(make_float2(sc[mt][j][2 * r2], sc[mt][j][2 * r2 + 1]), make_float2(1.f, 1.f), add);
+            if (8 * j >= some) sc[j][2 * r2] = -INFINITY;
+            if (8 * j + 1 >= some) sc[j][2 * r2 + 1] = -INFINITY;
           }
-          sum[mt][r2] = fmaf(sum[mt][r2], alpha[mt][r2], add.x + add.y);
+          if (p.a.window > 0) {
+            const int gap0 = see_gap0[r] - t0 - 2 * c, gap1 = see_gap1[r] - t0 - 2 * c;
+#pragma unroll
+            for (int j = 0; j < kBlock / 8; ++j) {
+              if (8 * j >= gap0 && 8 * j < gap1) sc[j][2 * r2] = -INFINITY;
+              if (8 * j + 1 >= gap0 && 8 * j + 1 < gap1) sc[j][2 * r2 + 1] = -INFINITY;
+            }
+          }
         }
+      }
+      // weights: exp2 of the scores times the factors, less the running maximum; a thread's
+      // rows side by side
+      float big[kR2], alpha[kR2], f[kR2], off[kR2];
+#pragma unroll
+      for (int r2 = 0; r2 < kR2; ++r2) {
+        const float x0 = fmaxf(fmaxf(sc[0][2 * r2], sc[0][2 * r2 + 1]), fmaxf(sc[2][2 * r2], sc[2][2 * r2 + 1]));
+        const float x1 = fmaxf(fmaxf(sc[1][2 * r2], sc[1][2 * r2 + 1]), fmaxf(sc[3][2 * r2], sc[3][2 * r2 + 1]));
+        big[r2] = fmaxf(x0, x1);
+      }
+#pragma unroll
+      for (int y = 1; y <= 2; y *= 2)
+#pragma unroll
+        for (int r2 = 0; r2 < kR2; ++r2) big[r2] = fmaxf(big[r2], __shfl_xor_sync(0xffffffffu, big[r2], y));
+      bool grew = false;
+#pragma unroll
+      for (int r2 = 0; r2 < kR2; ++r2) {
+        // (the factor is not zero, even for a softmax scale of zero: a masked score is -infinity)
+        f[r2] = fmaxf(qf[r2] * ks, 1e-37f);
+        const float m = fmaxf(top[r2], ceilf(big[r2] * f[r2]));
+        const float ref = m == -INFINITY ? 0.f : m;
+        off[r2] = kLift - ref;
+        alpha[r2] = exp2_approx(top[r2] - ref);
+        grew |= m > top[r2];
+        top[r2] = m;
+      }
+#pragma unroll
+      for (int r2 = 0; r2 < kR2; ++r2) {
+        float2 add = make_float2(0.f, 0.f);
+        const float2 f2 = make_float2(f[r2], f[r2]), off2 = make_float2(off[r2], off[r2]);
+#pragma unroll
+        for (int j = 0; j < kBlock / 8; ++j) {
+          const float2 e = fma2(make_float2(sc[j][2 * r2], sc[j][2 * r2 + 1]), f2, off2);
+          sc[j][2 * r2] = exp2_approx(e.x);
+          sc[j][2 * r2 + 1] = exp2_approx(e.y);
+          add = fma2(make_float2(sc[j][2 * r2], sc[j][2 * r2 + 1]), make_float2(1.f, 1.f), add);
+        }
+        sum[r2] = fmaf(sum[r2], alpha[r2], add.x + add.y);
+      }
       // the output's correction, where the maximum of some row grew
       if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < kPairsO; ++i) {
-              o[mt][nt][i].x *= alpha[mt][i];
-              o[mt][nt][i].y *= alpha[mt][i];
-            }
-      }
-      uint32_t pa[MT][kBlock / 16][4], pr[kRest ? MT : 1][kBlock / 16][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int kt = 0; kt < kBlock / 16; ++kt) {
-          const float (&s0)[4] = sc[mt][2 * kt], (&s1)[4] = sc[mt][2 * kt + 1];
-          uint32_t (&a)[4] = pa[mt][kt];
-          a[0] = pack_f16x2(s0[0], s0[1]);
-          a[2] = pack_f16x2(s1[0], s1[1]);
-          if (SPLIT) {
-            const float2 h0 = f16x2_to_float2(a[0]), h1 = f16x2_to_float2(a[2]);
-            a[1] = pack_f16x2((s0[0] - h0.x) * 2048.f, (s0[1] - h0.y) * 2048.f);
-            a[3] = pack_f16x2((s1[0] - h1.x) * 2048.f, (s1[1] - h1.y) * 2048.f);
-          } else {
-            a[1] = pack_f16x2(s0[2], s0[3]);
-            a[3] = pack_f16x2(s1[2], s1[3]);
+          for (int r2 = 0; r2 < kR2; ++r2) {
+            o[nt][r2].x *= alpha[r2];
+            o[nt][r2].y *= alpha[r2];
           }
-          if (kRest) {
-            uint32_t (&b)[4] = pr[kRest ? mt : 0][kt];
+      }
+      uint32_t pa[kBlock / 16][4], pr[kBlock / 16][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 h = f16x2_to_float2(a[i]);
-              const float (&y)[4] = i < 2 ? s0 : s1;
-              b[i] = pack_f16x2((y[2 * (i & 1)] - h.x) * 2048.f, (y[2 * (i & 1) + 1] - h.y) * 2048.f);
-            }
+      for (int kt = 0; kt < kBlock / 16; ++kt) {
+        const float (&s0)[4] = sc[2 * kt], (&s1)[4] = sc[2 * kt + 1];
+        uint32_t (&a)[4] = pa[kt];
+        a[0] = pack_f16x2(s0[0], s0[1]);
+        a[2] = pack_f16x2(s1[0], s1[1]);
+        if (SPLIT) {
+          const float2 h0 = f16x2_to_float2(a[0]), h1 = f16x2_to_float2(a[2]);
+          a[1] = pack_f16x2((s0[0] - h0.x) * 2048.f, (s0[1] - h0.y) * 2048.f);
+          a[3] = pack_f16x2((s1[0] - h1.x) * 2048.f, (s1[1] - h1.y) * 2048.f);
+        } else {
+          a[1] = pack_f16x2(s0[2], s0[3]);
+          a[3] = pack_f16x2(s1[2], s1[3]);
+        }
+        if (kRest) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 h = f16x2_to_float2(a[i]);
+            const float (&y)[4] = i < 2 ? s0 : s1;
+            pr[kt][i] = pack_f16x2((y[2 * (i & 1)] - h.x) * 2048.f, (y[2 * (i & 1) + 1] - h.y) * 2048.f);
           }
         }
+      }
       // O += vs P V
       uint32_t vw[kBlock / 16][4][VW];
 #pragma unroll
@@ -715,91 +596,83 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
       const float2 vs2 = make_float2(vs, vs), less = make_float2(1.f / 2048.f, 1.f / 2048.f);
 #pragma unroll
       for (int w = 0; w < VW; ++w) {
-        // bytes of a pair of events side by side: n tiles 4w, 4w+1 and 4w+2, 4w+3
-        uint32_t b[kBlock / 16][4][2];
+        float acc[4][4], rest[4][4];
 #pragma unroll
         for (int kt = 0; kt < kBlock / 16; ++kt) {
+          // bytes of a pair of events side by side: n tiles 4w, 4w+1 and 4w+2, 4w+3
           const uint32_t l0 = __byte_perm(vw[kt][0][w], vw[kt][1][w], 0x5140);
           const uint32_t l1 = __byte_perm(vw[kt][0][w], vw[kt][1][w], 0x7362);
           const uint32_t h0 = __byte_perm(vw[kt][2][w], vw[kt][3][w], 0x5140);
           const uint32_t h1 = __byte_perm(vw[kt][2][w], vw[kt][3][w], 0x7362);
-          b[kt][0][0] = e4m3x2_lo_to_f16x2(l0), b[kt][0][1] = e4m3x2_lo_to_f16x2(h0);
-          b[kt][1][0] = e4m3x2_hi_to_f16x2(l0), b[kt][1][1] = e4m3x2_hi_to_f16x2(h0);
-          b[kt][2][0] = e4m3x2_lo_to_f16x2(l1), b[kt][2][1] = e4m3x2_lo_to_f16x2(h1);
-          b[kt][3][0] = e4m3x2_hi_to_f16x2(l1), b[kt][3][1] = e4m3x2_hi_to_f16x2(h1);
-        }
-        float acc[MT][4][4], rest[kRest ? MT : 1][4][4];
-#pragma unroll
-        for (int kt = 0; kt < kBlock / 16; ++kt)
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              mma_f16_from(acc[mt][i], pa[mt][kt], b[kt][i][0], b[kt][i][1], kt > 0);
-              if (kRest) mma_f16_from(rest[kRest ? mt : 0][i], pr[kRest ? mt : 0][kt], b[kt][i][0], b[kt][i][1], kt > 0);
-            }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+          const uint32_t b[4][2] = {{e4m3x2_lo_to_f16x2(l0), e4m3x2_lo_to_f16x2(h0)},
+                                    {e4m3x2_hi_to_f16x2(l0), e4m3x2_hi_to_f16x2(h0)},
+                                    {e4m3x2_lo_to_f16x2(l1), e4m3x2_lo_to_f16x2(h1)},
+                                    {e4m3x2_hi_to_f16x2(l1), e4m3x2_hi_to_f16x2(h1)}};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float2* out = o[mt][4 * w + i];
-            float2 y0 = make_float2(acc[mt][i][0], acc[mt][i][1]), y1 = make_float2(acc[mt][i][2], acc[mt][i][3]);
-            if (SPLIT) {
-              y0 = fma2(y1, less, y0);
-            } else if (kRest) {
-              const float (&z)[4] = rest[kRest ? mt : 0][i];
-              y0 = fma2(make_float2(z[0], z[1]), less, y0);
-              y1 = fma2(make_float2(z[2], z[3]), less, y1);
-            }
-            out[0] = fma2(vs2, y0, out[0]);
-            if (!SPLIT) out[kPairsO - 1] = fma2(vs2, y1, out[kPairsO - 1]);
+            mma_f16_from(acc[i], pa[kt], b[i][0], b[i][1], kt > 0);
+            if (kRest) mma_f16_from(rest[i], pr[kt], b[i][0], b[i][1], kt > 0);
           }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float2* out = o[4 * w + i];
+          float2 y0 = make_float2(acc[i][0], acc[i][1]), y1 = make_float2(acc[i][2], acc[i][3]);
+          if (SPLIT) {
+            y0 = fma2(y1, less, y0);
+          } else if (kRest) {
+            y0 = fma2(make_float2(rest[i][0], rest[i][1]), less, y0);
+            y1 = fma2(make_float2(rest[i][2], rest[i][3]), less, y1);
+          }
+          out[0] = fma2(vs2, y0, out[0]);
+          if (!SPLIT) out[kR2 - 1] = fma2(vs2, y1, out[kR2 - 1]);
+        }
       }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 
-    // ---- join the sets of warps
+    // ---- join the warps
     __syncthreads();                              // every ring is done with: `joined` lies there
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int r2 = 0; r2 < kR2; ++r2) {
+      const int r = g + 8 * r2;
+      const float l = quad_sum(sum[r2]);
+      float* out = joined[warp][r];
 #pragma unroll
-      for (int r2 = 0; r2 < kR2; ++r2) {
-        const int r = (wr * MT + mt) * kTile + g + 8 * r2;
-        const float l = quad_sum(sum[mt][r2]);
-        float* out = joined[set][r];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          out[2 * c * (D / 8) + nt] = o[mt][nt][r2].x;
-          out[(2 * c + 1) * (D / 8) + nt] = o[mt][nt][r2].y;
-        }
-        if (c == 0) {
-          tops[set][r] = top[mt][r2];
-          totals[set][r] = l;
-        }
+      for (int nt = 0; nt < NT; ++nt) {
+        out[2 * c * (D / 8) + nt] = o[nt][r2].x;
+        out[(2 * c + 1) * (D / 8) + nt] = o[nt][r2].y;
       }
+      if (c == 0) {
+        tops[warp][r] = top[r2];
+        totals[warp][r] = l;
+      }
+    }
     __syncthreads();
-    for (int r = threadIdx.x; r < kRows; r += kThreads) {
+    if (threadIdx.x < kRows) {
+      const int r = threadIdx.x;
       float m = -INFINITY, l = 0.f;
 #pragma unroll
-      for (int w = 0; w < kSets; ++w) m = fmaxf(m, tops[w][r]);
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, tops[w][r]);
       const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
-      for (int w = 0; w < kSets; ++w) {
+      for (int w = 0; w < kWarps; ++w) {
         const float f = exp2_approx(tops[w][r] - ref);
         l = fmaf(f, totals[w][r], l);
         tops[w][r] = f;
       }
       row_top[r] = m;
       row_total[r] = l;
+      odd[r] = 0;
+      if (r == 0) odd[kRows] = 0;
     }
-    if (threadIdx.x == 0) odd[kRows] = 0;
     __syncthreads();
     const bool split = chunk0 > 0 || chunk1 < chunks;
     float* mine_at = p.partials + (static_cast<int64_t>(blockIdx.x) * 2 + (chunk0 > 0 ? 0 : 1)) * kPartial;
-    auto sums_of = [&](int r, int d) {            // four sums of a row, over the sets
+    auto sums_of = [&](int r, int d) {            // four sums of a row, over the warps
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kSets; ++w) {
+      for (int w = 0; w < kWarps; ++w) {
         const float f = tops[w][r];
         const float4 z = *reinterpret_cast<const float4*>(&joined[w][r][d]);
         y.x = fmaf(f, z.x, y.x), y.y = fmaf(f, z.y, y.y), y.z = fmaf(f, z.z, y.z), y.w = fmaf(f, z.w, y.w);
@@ -824,30 +697,26 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) store_element<DT>(p.a.out, at + e, z[e]);
       }
-      if (d == 0) {
-        if (p.a.lse)
-          p.a.lse[row_at[r] * p.a.n_heads + hq] = l == 0.f ? -INFINITY : row_top[r] * kLn2 + logf(l * pow2f(-kLift));
-      }
+      if (d == 0 && p.a.lse)
+        p.a.lse[row_at[r] * p.a.n_heads + hq] = l == 0.f ? -INFINITY : row_top[r] * kLn2 + logf(l * pow2f(-kLift));
       if (!fine) odd[r] = odd[kRows] = l == 0.f ? 2 : 1;   // 2: sees nothing, or has no weights
     };
-    for (int r = threadIdx.x; r < kRows; r += kThreads) odd[r] = 0;
     constexpr int kQuads = (kRows * D / 4 + kThreads - 1) / kThreads;
     if (!split) {
-      __syncthreads();
-#pragma unroll 4
+#pragma unroll
       for (int e = 0; e < kQuads; ++e) {
         const int of = 4 * (e * kThreads + threadIdx.x), r = of / D, d = of % D;
         if (r < rows) finish(r, d, sums_of(r, d));
       }
     } else {
-#pragma unroll 4
+#pragma unroll
       for (int e = 0; e < kQuads; ++e) {
         const int of = 4 * (e * kThreads + threadIdx.x), r = of / D, d = of % D;
         if (r < rows) *reinterpret_cast<float4*>(mine_at + of) = sums_of(r, d);
       }
-      for (int r = threadIdx.x; r < rows; r += kThreads) {
-        mine_at[kRows * D + r] = row_top[r];
-        mine_at[kRows * D + kRows + r] = row_total[r];
+      if (threadIdx.x < rows) {
+        mine_at[kRows * D + threadIdx.x] = row_top[threadIdx.x];
+        mine_at[kRows * D + kRows + threadIdx.x] = row_total[threadIdx.x];
       }
       // the CTAs that share this piece, one part each: the one that begins it, and those
       // that begin inside
@@ -865,14 +734,21 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
       if (n_arrived != parts - 1) continue;       // (`joined` was read before the barrier)
       __threadfence();
       auto part = [&](int i) { return p.partials + ((first + i) * 2 + (i > 0 ? 0 : 1)) * kPartial; };
-      // maximum of each row over the parts, the parts' weights, then the weighted sums
+      // maximum of each row over the parts, the parts' weights, then the weighted sums,
+      // kWeights parts at a time
       float big = -INFINITY, l = 0.f;             // of row threadIdx.x
-      static_assert(kRows <= kThreads, "a thread a row");
+      auto load_tops = [&](int p0, int n) {
+        for (int e = threadIdx.x; e < n * kRows; e += kThreads) {
+          const int i = e / kRows, r = e % kRows;
+          const float* q = part(p0 + i) + kRows * D;
+          weight[i][r] = r < rows ? __ldcg(q + r) : -INFINITY;
+          weight_sum[i][r] = r < rows ? __ldcg(q + kRows + r) : 0.f;
+        }
+        __syncthreads();
+      };
       for (int p0 = 0; p0 < parts; p0 += kWeights) {
         const int n = min(kWeights, parts - p0);
-        for (int e = threadIdx.x; e < n * kRows; e += kThreads)
-          weight[e / kRows][e % kRows] = e % kRows < rows ? __ldcg(part(p0 + e / kRows) + kRows * D + e % kRows) : -INFINITY;
-        __syncthreads();
+        load_tops(p0, n);
         if (threadIdx.x < kRows)
           for (int i = 0; i < n; ++i) big = fmaxf(big, weight[i][threadIdx.x]);
         if (p0 + n < parts) __syncthreads();
@@ -884,17 +760,15 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
       for (int p0 = 0; p0 < parts; p0 += kWeights) {
         const int n = min(kWeights, parts - p0);
         __syncthreads();
-        for (int e = threadIdx.x; e < n * kRows; e += kThreads) {
-          const int i = e / kRows, r = e % kRows;
-          const float m = row_top[r];
-          const float t = parts > kWeights ? r < rows ? __ldcg(part(p0 + i) + kRows * D + r) : -INFINITY : weight[i][r];
-          weight[i][r] = m == -INFINITY ? 0.f : exp2_approx(t - m);
-        }
+        if (parts > kWeights) load_tops(p0, n);   // (else they are there)
+        if (threadIdx.x < kRows)
+          for (int i = 0; i < n; ++i) {
+            const float f = big == -INFINITY ? 0.f : exp2_approx(weight[i][threadIdx.x] - big);
+            weight[i][threadIdx.x] = f;
+            l = fmaf(f, weight_sum[i][threadIdx.x], l);
+          }
         __syncthreads();
-        if (threadIdx.x < rows)
-          for (int i = 0; i < n; ++i)
-            l = fmaf(weight[i][threadIdx.x], __ldcg(part(p0 + i) + kRows * D + kRows + threadIdx.x), l);
-#pragma unroll 2
+#pragma unroll 4
         for (int i = 0; i < n; ++i) {
           const float* q = part(p0 + i);
 #pragma unroll
@@ -931,9 +805,9 @@ prefix_attention_kernel(const __grid_constant__ Params p) {
   }
 }
 
-template <int D, int DT, bool SPLIT, int MT, int WR>
+template <int D, int DT, bool SPLIT>
 cudaError_t launch(Params& p, cudaStream_t stream) {
-  using Sh = Shape<D, DT, SPLIT, MT, WR>;
+  using Sh = Shape<D, SPLIT>;
   // set once on every device, by a bit each; the CTAs of an SM are the same on every GB300
   static std::atomic<uint64_t> done{0};
   static std::atomic<int> resident{0};
@@ -943,10 +817,10 @@ cudaError_t launch(Params& p, cudaStream_t stream) {
   const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
   int per_sm = 0;
   if (!bit || !(done.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(prefix_attention_kernel<D, DT, SPLIT, MT, WR>,
+    e = cudaFuncSetAttribute(prefix_attention_kernel<D, DT, SPLIT>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
     if (e != cudaSuccess) return e;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, prefix_attention_kernel<D, DT, SPLIT, MT, WR>,
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, prefix_attention_kernel<D, DT, SPLIT>,
                                                       kThreads, Sh::kSmem);
     if (e != cudaSuccess) return e;
     per_sm = std::max(1, per_sm);
@@ -956,36 +830,27 @@ cudaError_t launch(Params& p, cudaStream_t stream) {
     per_sm = resident.load(std::memory_order_relaxed);
   }
   // no more CTAs than counters, than partial results have space, and than pieces of
-  // kLeastBlocks there can be
+  // kLeast chunks there can be
   const int64_t events = static_cast<int64_t>(p.h.max_pages) * p.h.page_tokens;
   const int64_t tiles = p.a.q_rows * p.group / Sh::kRows + p.n_groups;
   const int64_t blocks = (tiles * 2 + p.a.batch) * p.h.n_heads * (events / kBlock + 2);
   p.rows = Sh::kRows;
-  p.split = Sh::kSets;
   p.grid = static_cast<int>(std::min<int64_t>(
-      {std::max<int64_t>(blocks / kLeastBlocks, tiles * p.h.n_heads), static_cast<int64_t>(device_sm_count()) * per_sm,
+      {std::max<int64_t>(blocks / (kLeast * kWarps), tiles * p.h.n_heads), static_cast<int64_t>(device_sm_count()) * per_sm,
        int64_t(kAttnMaxCtas), kAttnPartialFloats / (2 * Sh::kPartial)}));
   e = launch_plan(p, stream);
   if (e != cudaSuccess) return e;
-  return launch_pdl(prefix_attention_kernel<D, DT, SPLIT, MT, WR>, dim3(p.grid), dim3(kThreads), Sh::kSmem, stream, p);
+  return launch_pdl(prefix_attention_kernel<D, DT, SPLIT>, dim3(p.grid), dim3(kThreads), Sh::kSmem, stream, p);
 }
 
 template <int D, int DT>
 cudaError_t launch_rows(Params& p, cudaStream_t stream) {
-  // by the rows of a group and kv head, on average; at head_dim 128 a warp has registers
-  // for one row tile
-  constexpr bool kSplit = DT == DLRM_DTYPE_FP32;
-  constexpr int kTile = kSplit ? 8 : 16, MT = D == 128 ? 1 : 2;
-  const int64_t rows = (p.a.q_rows * p.group + p.n_groups - 1) / p.n_groups;
-  if (rows <= 8) return launch<D, DT, true, 1, 1>(p, stream);
-  if constexpr (!kSplit) {
-    if (rows <= kTile) return launch<D, DT, kSplit, 1, 1>(p, stream);
+  // 16-bit rows that are no more than 8 of a group and kv head, on average, leave half of an
+  // MMA's rows empty: they take the rests' place
+  if constexpr (DT != DLRM_DTYPE_FP32) {
+    if (p.a.q_rows * p.group > int64_t(8) * p.n_groups) return launch<D, DT, false>(p, stream);
   }
-  if (MT > 1 && rows <= kTile * MT) return launch<D, DT, kSplit, MT, 1>(p, stream);
-  if constexpr (MT == 1) {
-    if (rows > 2 * kTile) return launch<D, DT, kSplit, MT, 4>(p, stream);
-  }
-  return launch<D, DT, kSplit, MT, 2>(p, stream);
+  return launch<D, DT, true>(p, stream);
 }
 
 template <int D>
