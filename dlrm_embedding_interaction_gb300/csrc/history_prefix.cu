@@ -20,7 +20,7 @@ namespace {
 
 constexpr int kPlanThreads = 512;
 constexpr int kHere = 256;                       // requests of a group that shared memory holds
-constexpr int kTilesHere = 1024;
+constexpr int kTilesHere = 256;                  // tiles that shared memory holds
 
 // Exclusive prefix sum over the CTA; total in every thread.
 __device__ __forceinline__ int scan(int x, int* sums, int& total) {
@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
   __shared__ int sums[kWarp + 1];
   __shared__ int ref_s, len_s, gap_s, shared_s, last_s;
   __shared__ Member here[kHere];
-  __shared__ int first_s[kTilesHere];            // where tiles begin
+  __shared__ Tile tiles_s[kTilesHere];
   const dlrm_history_t& h = p.h;
   const int G = h.page_tokens, M = h.max_pages, t = threadIdx.x, lane = t % kWarp, g = blockIdx.x;
   const int32_t* starts = p.a.q_starts;
@@ -224,14 +224,15 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
   int work = 0, dense = 0;
   const int per = (last_place - first_place + kPlanThreads - 1) / kPlanThreads;
   const int mine0 = min(last_place, first_place + t * per), mine1 = min(last_place, mine0 + per);
-  const auto tile_at = [&](int i) {
+  const auto copy_of = [](const Tile* tile) {
     Tile y;
-    const int4* from = reinterpret_cast<const int4*>(&p.found[i]);
+    const int4* from = reinterpret_cast<const int4*>(tile);
     int4* to = reinterpret_cast<int4*>(&y);
 #pragma unroll
     for (int w = 0; w < static_cast<int>(sizeof(Tile) / 16); ++w) to[w] = __ldcg(from + w);
     return y;
   };
+  const auto tile_at = [&](int i) { return copy_of(&p.found[i]); };
   Tile only{};                                    // the thread's tile, if it is one
   for (int i = mine0; i < mine1; ++i) {
     only = tile_at(i);
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
     if (chunks == 0) continue;
     y.first = at;
     p.tiles[place] = y;
-    if (place < kTilesHere) first_s[place] = at;
+    if (place < kTilesHere) tiles_s[place] = y;
     at += cuts.work(chunks) * h.n_heads;
     ++place;
   }
@@ -271,18 +272,15 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
       int lo = 0, hi = n_tiles;                   // the last tile that begins at or before it
       while (hi - lo > 1) {
         const int mid = lo + (hi - lo) / 2;
-        if ((mid < kTilesHere ? first_s[mid] : __ldcg(&p.tiles[mid].first)) <= w) lo = mid; else hi = mid;
+        if ((mid < kTilesHere ? tiles_s[mid].first : __ldcg(&p.tiles[mid].first)) <= w) lo = mid; else hi = mid;
       }
       x.place = lo;
-      const int4* from = reinterpret_cast<const int4*>(&p.tiles[lo]);
-      int4* to = reinterpret_cast<int4*>(&x.tile);
-#pragma unroll
-      for (int i = 0; i < static_cast<int>(sizeof(Tile) / 16); ++i) to[i] = __ldcg(from + i);
+      x.tile = lo < kTilesHere ? tiles_s[lo] : copy_of(&p.tiles[lo]);
       const int chunks = chunks_of(x.tile), length = cuts.work(chunks);
       x.piece = static_cast<unsigned>(w - x.tile.first) / static_cast<unsigned>(length);
       const int start = x.tile.first + x.piece * length, off = w - start;
       if (chunks > kWhole && off >= kNear && off < length - kNear)
-        x.chunk = cuts.chunk(c, start, chunks);
+        x.chunk = Cuts::chunk(off, length, chunks);
       else if (chunks > kWhole ? off >= kNear : off >= length / 2)
         ++x.piece;
     }

@@ -19,14 +19,14 @@ static_assert(kWhole >= 2 * kNear - kCost, "a piece that is split has an inside"
 constexpr int kWeights = 32;                     // parts whose weights lie in shared memory at once
 
 // What the plan knows of a request with rows, and of the tiles.
-struct Member {
+struct alignas(16) Member {
   int32_t slot, len, queries;
   int32_t row0, rows;                            // among the group's rows
   int32_t first;                                 // blocks of the group's earlier requests
   int32_t sinks, block0;                         // blocks of its own events: the sinks', then from block0 on
 };
 static_assert(sizeof(Member) == kPrefixMember, "scratch size of a member");
-struct Tile {
+struct alignas(16) Tile {
   int32_t first, blocks;                         // work before it, as Cuts counts it; its blocks
   int32_t q0, row0, rows;                        // the group's first query row; rows among the group's
   int32_t member0, member1;                      // first and last request with rows in the tile
@@ -36,7 +36,7 @@ struct Tile {
 };
 static_assert(sizeof(Tile) == kPrefixTile, "scratch size of a tile");
 
-struct Cut {                                     // where a CTA begins
+struct alignas(16) Cut {                                     // where a CTA begins
   int32_t place, piece;                          // tile, and which of its pieces (kv heads)
   int32_t chunk;                                 // of the piece
   int32_t each;                                  // work of a CTA
@@ -67,9 +67,12 @@ struct Cuts {
     first = from(start + kNear);
     return chunks <= kWhole ? 0 : max(from(start + work(chunks) - kNear) - first, 0);
   }
-  // The chunk at which CTA c, one of them, begins.
-  __device__ __forceinline__ int chunk(int c, int start, int chunks) const {
-    return static_cast<int>(static_cast<int64_t>(c * each - start) * chunks / work(chunks));
+  // The chunk at which one of them begins that lies `off` behind the start of a piece of
+  // `length` in all: its share, and a chunk at least to either side. (In fp32, which keeps the
+  // order; the CTAs lie kLeast chunks apart or more.)
+  __device__ __forceinline__ static int chunk(int off, int length, int chunks) {
+    const int n = static_cast<int>(static_cast<float>(off) / static_cast<float>(length) * static_cast<float>(chunks));
+    return min(max(n, 1), chunks - 1);
   }
 };
 
