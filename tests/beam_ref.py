@@ -75,7 +75,7 @@ def log_probabilities(logits, allowed=None):
     top = x.max(1, keepdims=True)
     base = np.where(np.isfinite(top), top, 0.0)
     with np.errstate(divide="ignore", invalid="ignore"):
-        out = x - (base + np.log(np.exp(x - base).sum(1, keepdims=True)))
+        out = (x - base) - np.log(np.exp(x - base).sum(1, keepdims=True))   # (log n stays beside any base)
     return np.where(np.isneginf(x), -np.inf, out)
 
 
