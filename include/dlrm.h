@@ -689,7 +689,8 @@ dlrm_status_t attention_test_stall(int64_t wait_limit_ns, int32_t withhold);
  *           all); NULL: every token is
  *   starts  (groups + 1) int32; out_* (groups, width)
  *   err     NULL or an int32 word for DLRM_ERRBIT_*: OFFSETS for starts that decrease or
- *           pass the rows (that group has no rows), INVALID_ARG for a row with a NaN or
+ *           pass the rows (that group has no rows; where others then have rows in
+ *           common, theirs are undefined), INVALID_ARG for a row with a NaN or
  *           +infinity among its allowed logits or as its score (it has no candidates)
  *   work    scratch of beam_select_work_bytes() bytes, 16-byte aligned, for this call
  * width is 1 to 256, vocab 1 to 2^31 - 2^20; fewer than 2^31 rows and chunks of rows

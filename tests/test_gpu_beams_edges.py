@@ -130,6 +130,26 @@ def test_trimmed_pages_are_read_by_no_window_that_left_them():
     assert cache.error() == dl.ERR_INDEX_OOB
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("shared", [True, False])
+def test_rows_of_no_request_stay_and_slots_may_occur_twice(dtype, shared):
+    rng = np.random.default_rng(17)
+    cache, pool, slots, groups = beams(rng, [200, 90], [4, 3], [2] * 7, 2, 64, 64, shared=shared)
+    slots = [slots[0], slots[0], slots[2], 0, slots[4], slots[5], slots[5]]   # (0: the user's own)
+    at = [3, 4, 6, 6, 9, 10, 11, 12]
+    q = rows(rng, 14, 4, 64, dtype, 0.3)
+    out, lse = torch.full_like(q, 9.0), torch.full((14, 4), 9.0, device="cuda")
+    shared_attention(cache, slots, at, groups, q, out=out, lse=lse)
+    check_rows(pool, slots, at, q, out, lse, dtype)
+    for x in (out, lse):
+        assert (x[:3] == 9).all() and (x[12:] == 9).all()
+    before = out.clone()
+    shared_attention(cache, [], [0], [0], q[:0], out=out[:0])
+    shared_attention(cache, slots, [5] * 8, groups, q, out=out)   # no rows at all
+    shared_attention(cache, [], [0], [0, 0, 0], q, out=out)       # groups of nothing
+    assert torch.equal(out, before) and cache.error() == dl.OK
+
+
 @pytest.mark.parametrize("shared", [True, False])
 def test_bad_requests_are_reported_and_the_next_call_is_as_ever(shared):
     rng = np.random.default_rng(5)
@@ -249,6 +269,37 @@ def test_too_few_pages_leave_everything_as_it_was():
     assert cache.error() == dl.OK
 
 
+@pytest.mark.parametrize("seed", range(4))
+def test_reordering_among_the_other_operators(seed):
+    """Forks, trims, frees, appends and compactions in between."""
+    rng = np.random.default_rng(200 + seed)
+    cache, pool = make(120, 12, 8, 1, 32, 32)
+    for step in range(40):
+        slots = rng.permutation(12)[:int(rng.integers(1, 13))].tolist()
+        kind = int(rng.integers(0, 6))
+        if kind == 0:
+            parents = rng.integers(-1, len(slots), len(slots)).tolist()
+            dl.history_reorder(cache, i32(slots), i32(parents))
+            assert pool.reorder(slots, parents)
+        elif kind == 1:
+            window, sinks = int(rng.integers(1, 90)), int(rng.integers(0, 40))
+            dl.history_trim(cache, i32(slots), window, sinks)
+            pool.release(slots, window, sinks)
+        elif kind == 2:
+            dl.history_free(cache, i32(slots[:2]))
+            pool.release(slots[:2])
+        elif kind == 3:
+            dl.history_fork(cache, i32(slots), i32(slots[::-1]))
+            pool.fork(slots, slots[::-1], True)
+        elif kind == 4:
+            dl.history_compact(cache)
+            pool.compact()
+        else:
+            append(cache, pool, rng, slots, rng.integers(0, 40, len(slots)).tolist())
+        same_state(cache, pool)
+    cache.error()
+
+
 @pytest.mark.parametrize("page", [64, 2 ** 31 - 1, -2])
 def test_reordering_past_pages_that_a_table_cannot_hold(page):
     rng = np.random.default_rng(10)
@@ -285,6 +336,16 @@ def test_strides_and_broadcast_masks():
         one[2, 7] = True                            # a beam with one way on: at no cost
         got = dl.beam_select(logits, scores, i32(starts), 2, allowed=one)
         assert got[0][0, 0] == scores[2] and got[1].tolist() == [[2, -1]] and got[2].tolist() == [[7, -1]]
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("vocab", [200, 70000])
+def test_zeros_of_both_signs_are_equal(dtype, vocab):
+    rng = np.random.default_rng(18)
+    x = torch.zeros(3, vocab, dtype=TYPES[dtype], device="cuda")
+    x[torch.from_numpy(rng.random((3, vocab)) < 0.5).cuda()] = -0.0
+    got = dl.beam_select(x, None, i32([0, 3]), 100)
+    assert (got[1] == 0).all() and got[2].tolist() == [list(range(100))]
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
