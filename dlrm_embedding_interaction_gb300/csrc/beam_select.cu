@@ -212,70 +212,52 @@ __device__ __forceinline__ uint32_t block_bound(const uint32_t (&key)[N], int k,
 
 // ------------------------------------------------------------------ rows as loaded
 
-// Consecutive logits, 16 bytes from `at` on, as words; the row ends at `end`. A row may begin
-// at any element: then two aligned vectors are shifted together. Aligned vectors that
-// hold an element of the row are read whole.
+// Rows are read as aligned 16-byte vectors, of which each lane has its own and, from the next
+// lane, what a row that begins between two vectors needs of the following one. So a row is
+// grouped by its tokens wherever it lies, and rows that are alike get sums that are alike. Vectors
+// are moved into place when they are used, not when they are asked for.
 template <int DT>
 struct Row {
   static constexpr int kVec = DT == DLRM_DTYPE_FP32 ? 4 : 8;
   static constexpr int kBytes = DT == DLRM_DTYPE_FP32 ? 4 : 2;
 };
 
-// NEXT: the next lane loads what follows, as in a tile of which the row holds everything.
-template <bool ALIGNED, bool NEXT>
-__device__ __forceinline__ uint4 load_vector(const char* at, const char* end) {
-  if (ALIGNED) return __ldg(reinterpret_cast<const uint4*>(at));
-  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(at) & 15);
-  const uint4* base = reinterpret_cast<const uint4*>(at - off);
-  const uint4 a = __ldg(base);
-  uint4 b = make_uint4(0, 0, 0, 0);
-  if (NEXT) {
-    b = make_uint4(__shfl_down_sync(0xffffffffu, a.x, 1), __shfl_down_sync(0xffffffffu, a.y, 1),
-                   __shfl_down_sync(0xffffffffu, a.z, 1), __shfl_down_sync(0xffffffffu, a.w, 1));
-  }
-  if ((!NEXT || threadIdx.x % kWarp == kWarp - 1) && reinterpret_cast<const char*>(base + 1) < end) b = __ldg(base + 1);
-  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  if (off & 8) {
+// The lane's vectors, Q words and `bits` on; `tail` is what follows the last lane's last one.
+template <int DT, int Q>
+__device__ __forceinline__ void move_vectors(uint4 (&now)[kVectors], const uint4 (&raw)[kVectors], const uint4& tail, int bits) {
+  const int lane = threadIdx.x % kWarp;
+  const uint32_t last[4] = {tail.x, tail.y, tail.z, tail.w};
 #pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-  }
-  if (off & 4) {
+  for (int v = 0; v < kVectors; ++v) {
+    const uint4 a = raw[v], b = raw[v + 1 < kVectors ? v + 1 : v];
+    const uint32_t mine[4] = {a.x, a.y, a.z, a.w}, first[4] = {b.x, b.y, b.z, b.w};
+    uint32_t w[8] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    for (int i = 0; i < Q + (DT != DLRM_DTYPE_FP32); ++i) {
+      const uint32_t x = v + 1 < kVectors && lane == 0 ? first[i] : mine[i];
+      w[4 + i] = __shfl_sync(0xffffffffu, x, (lane + 1) % kWarp);
+      if (v + 1 == kVectors && lane == kWarp - 1) w[4 + i] = last[i];
+    }
+    if (DT != DLRM_DTYPE_FP32) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i + Q], w[i + Q + 1], bits);
+      now[v] = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      now[v] = make_uint4(w[Q], w[Q + 1], w[Q + 2], w[Q + 3]);
+    }
   }
-  const int bits = (off & 3) * 8;
-  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
-                    __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
 }
-// The same of the bytes that allow tokens: kVec of them.
-template <int VEC, bool ALIGNED, bool NEXT>
-__device__ __forceinline__ uint2 load_allowed(const uint8_t* at, const uint8_t* end) {
-  if (VEC == 4) {
-    if (ALIGNED) return make_uint2(__ldg(reinterpret_cast<const uint32_t*>(at)), 0);
-    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(at) & 3);
-    const uint32_t* base = reinterpret_cast<const uint32_t*>(at - off);
-    const uint32_t a = __ldg(base);
-    uint32_t b = NEXT ? __shfl_down_sync(0xffffffffu, a, 1) : 0;
-    if ((!NEXT || threadIdx.x % kWarp == kWarp - 1) && reinterpret_cast<const uint8_t*>(base + 1) < end)
-      b = __ldg(base + 1);
-    return make_uint2(__funnelshift_r(a, b, off * 8), 0);
+
+// The bytes that allow a vector's elements begin at any byte: as aligned words, of which the last
+// is needed only where they do not begin with a word.
+template <int DT>
+struct May {
+  uint32_t w[Row<DT>::kVec / 4 + 1];
+  __device__ __forceinline__ uint2 bytes(int shift) const {
+    return make_uint2(__funnelshift_r(w[0], w[1], shift),
+                      Row<DT>::kVec == 8 ? __funnelshift_r(w[1], w[Row<DT>::kVec / 4], shift) : 0);
   }
-  if (ALIGNED) return __ldg(reinterpret_cast<const uint2*>(at));
-  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(at) & 7);
-  const uint2* base = reinterpret_cast<const uint2*>(at - off);
-  const uint2 a = __ldg(base);
-  uint2 b = make_uint2(0, 0);
-  if (NEXT) b = make_uint2(__shfl_down_sync(0xffffffffu, a.x, 1), __shfl_down_sync(0xffffffffu, a.y, 1));
-  if ((!NEXT || threadIdx.x % kWarp == kWarp - 1) && reinterpret_cast<const uint8_t*>(base + 1) < end)
-    b = __ldg(base + 1);
-  uint32_t w[4] = {a.x, a.y, b.x, b.y};
-  if (off & 4) {
-#pragma unroll
-    for (int i = 0; i < 3; ++i) w[i] = w[i + 1];
-  }
-  const int bits = (off & 3) * 8;
-  return make_uint2(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits));
-}
+};
 // The vector with -infinity where a byte of `may` is zero.
 template <int DT>
 __device__ __forceinline__ void hide(uint4& v, const uint2& may) {
@@ -381,9 +363,9 @@ __device__ __noinline__ int exact_chunk(const Params& p, int64_t row, int64_t e0
   return *counter;
 }
 
-// Drops what is below the k-th largest of a list of n >= k entries (to 12 bits past what all
-// have in common); returns how many stay. One warp.
-__device__ __forceinline__ int tighten(Entry* list, int n, int k) {
+// Drops entries below a lower bound of the k-th largest of a list of n >= k, until few more than k
+// are left (or ties); returns how many stay, and the bound. One warp.
+__device__ __forceinline__ int tighten(Entry* list, int n, int k, float& least) {
   const int lane = threadIdx.x % kWarp;
   uint32_t hi = 0, lo = 0xffffffffu;
   for (int i = lane; i < n; i += kWarp) {
@@ -393,16 +375,23 @@ __device__ __forceinline__ int tighten(Entry* list, int n, int k) {
   }
   hi = __reduce_max_sync(0xffffffffu, hi);
   lo = __reduce_min_sync(0xffffffffu, lo);
+  least = of_key(lo);
   if (hi == lo) return n;
   const int first = 31 - __clz(hi ^ lo);
   uint32_t bound = first == 31 ? 0u : hi & (0xffffffffu << (first + 1));
-  for (int bit = first; bit >= max(first - 11, 0); --bit) {
+  int there = n;
+  for (int bit = first; bit >= 0 && there > k + k / 4 + 1; --bit) {
     const uint32_t trial = bound | (1u << bit);
     int c = 0;
+#pragma unroll 4
     for (int i = lane; i < n; i += kWarp) c += key_of(list[i].logit) >= trial;
-    if (__reduce_add_sync(0xffffffffu, c) >= k) bound = trial;
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (c >= k) {
+      bound = trial;
+      there = c;
+    }
   }
-  const float least = of_key(bound);
+  least = bound_of(bound);
   int kept = 0;
   for (int i0 = 0; i0 < n; i0 += kWarp) {
     Entry x{};
@@ -451,9 +440,9 @@ __device__ __forceinline__ uint32_t warp_bound(const uint32_t (&key)[N], int k) 
 // What bounds it: the instructions around one exponential a logit (about six), then HBM.
 // Warps meet twice, after the first tile and at the end: each has a list of its own, of vectors
 // by their largest element; their elements are looked at once more at the end.
-template <int DT, bool MASK, bool ALIGNED>
-__global__ void __launch_bounds__(kScanThreads, MASK || !ALIGNED ? 6 : 8) beam_scan_kernel(const __grid_constant__ Params p) {
-  constexpr int kVec = Row<DT>::kVec, kWarps = kScanThreads / kWarp;
+template <int DT, bool MASK>
+__global__ void __launch_bounds__(kScanThreads, MASK ? 6 : 8) beam_scan_kernel(const __grid_constant__ Params p) {
+  constexpr int kVec = Row<DT>::kVec, kWarps = kScanThreads / kWarp, kWords = kVec / 4;
   constexpr int kTile = kScanThreads * kVec * kVectors;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ uint32_t red[2 * kWarps];
@@ -472,26 +461,42 @@ __global__ void __launch_bounds__(kScanThreads, MASK || !ALIGNED ? 6 : 8) beam_s
   pdl_trigger();
 
   const int n = static_cast<int>(e1 - e0);        // of the chunk
-  const char* at_logits = logits + (e0 + t * kVec) * Row<DT>::kBytes;
-  const uint8_t* at_allowed = MASK ? allowed + e0 + t * kVec : nullptr;
-  const char* end_logits = logits + vocab * Row<DT>::kBytes;
-  const uint8_t* end_allowed = MASK ? allowed + vocab : nullptr;
-  uint4 raw[kVectors];
-  uint2 may[kVectors];
+  const int first = (warp * kVectors * kWarp + lane) * kVec;   // the thread's of a tile; the others kWarp vectors apart
+  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(logits) & 15);
+  const char* at_logits = logits - off + (e0 + first) * Row<DT>::kBytes;
+  const int shift = MASK ? static_cast<int>(reinterpret_cast<uintptr_t>(allowed) & 3) * 8 : 0;
+  const uint8_t* at_allowed = MASK ? allowed - shift / 8 + e0 + first : nullptr;
+  uint4 raw[kVectors], tail = make_uint4(0, 0, 0, 0);
+  May<DT> may[kVectors];
   auto load = [&](int at) {
     if (at + kTile <= n) {
 #pragma unroll
       for (int v = 0; v < kVectors; ++v) {
-        raw[v] = load_vector<ALIGNED, true>(at_logits + v * (kScanThreads * 16), end_logits);
-        if (MASK) may[v] = load_allowed<kVec, ALIGNED, true>(at_allowed + v * (kScanThreads * kVec), end_allowed);
+        raw[v] = __ldg(reinterpret_cast<const uint4*>(at_logits) + v * kWarp);
+        if (MASK) {
+          const uint32_t* words = reinterpret_cast<const uint32_t*>(at_allowed + v * kWarp * kVec);
+#pragma unroll
+          for (int i = 0; i < kWords; ++i) may[v].w[i] = __ldg(words + i);
+          may[v].w[kWords] = shift ? __ldg(words + kWords) : 0;
+        }
       }
+      if (off && lane == kWarp - 1) tail = __ldg(reinterpret_cast<const uint4*>(at_logits) + (kVectors - 1) * kWarp + 1);
     } else {
+      // vectors and words that hold something of the row
+      const char* end_logits = logits + vocab * Row<DT>::kBytes;
 #pragma unroll
       for (int v = 0; v < kVectors; ++v) {
-        if (at + (v * kScanThreads + t) * kVec >= n) continue;
-        raw[v] = load_vector<ALIGNED, false>(at_logits + v * (kScanThreads * 16), end_logits);
-        if (MASK) may[v] = load_allowed<kVec, ALIGNED, false>(at_allowed + v * (kScanThreads * kVec), end_allowed);
+        const uint4* vector = reinterpret_cast<const uint4*>(at_logits) + v * kWarp;
+        if (reinterpret_cast<const char*>(vector) < end_logits) raw[v] = __ldg(vector);
+        if (MASK) {
+          const uint32_t* words = reinterpret_cast<const uint32_t*>(at_allowed + v * kWarp * kVec);
+#pragma unroll
+          for (int i = 0; i <= kWords; ++i)
+            may[v].w[i] = reinterpret_cast<const uint8_t*>(words + i) < allowed + vocab ? __ldg(words + i) : 0;
+        }
       }
+      const uint4* vector = reinterpret_cast<const uint4*>(at_logits) + (kVectors - 1) * kWarp + 1;
+      if (lane == kWarp - 1 && reinterpret_cast<const char*>(vector) < end_logits) tail = __ldg(vector);
     }
     at_logits += kTile * Row<DT>::kBytes;
     if (MASK) at_allowed += kTile;
@@ -506,17 +511,21 @@ __global__ void __launch_bounds__(kScanThreads, MASK || !ALIGNED ? 6 : 8) beam_s
   for (int at = 0; at < n; at += kTile) {
     uint4 now[kVectors];
     float top[kVectors];
+    if (off == 0) {
 #pragma unroll
-    for (int v = 0; v < kVectors; ++v) {
-      now[v] = raw[v];
-      if (MASK) hide<DT>(now[v], may[v]);
+      for (int v = 0; v < kVectors; ++v) now[v] = raw[v];
+    } else if (off < 8) {
+      if (off < 4) move_vectors<DT, 0>(now, raw, tail, off * 8); else move_vectors<DT, 1>(now, raw, tail, off % 4 * 8);
+    } else {
+      if (off < 12) move_vectors<DT, 2>(now, raw, tail, off % 4 * 8); else move_vectors<DT, 3>(now, raw, tail, off % 4 * 8);
+    }
+    if (MASK) {
+#pragma unroll
+      for (int v = 0; v < kVectors; ++v) hide<DT>(now[v], may[v].bytes(shift));
     }
     if (at + kTile > n) {
 #pragma unroll
-      for (int v = 0; v < kVectors; ++v) {
-        const int left = n - (at + (v * kScanThreads + t) * kVec);
-        if (left < kVec) hide<DT>(now[v], first_bytes(left));
-      }
+      for (int v = 0; v < kVectors; ++v) hide<DT>(now[v], first_bytes(n - (at + first + v * kWarp * kVec)));
     }
 #pragma unroll
     for (int v = 0; v < kVectors; ++v) top[v] = largest<DT>(now[v]);
@@ -593,7 +602,8 @@ __global__ void __launch_bounds__(kScanThreads, MASK || !ALIGNED ? 6 : 8) beam_s
       if (count + more > room && !many) {
         // what is not among the warp's largest is not among the chunk's
         __syncwarp();
-        if (count > width) count = tighten(list, count, width);
+        float least;
+        if (count > width) count = tighten(list, count, width, least);
         many = count + more > room;
       }
       if (!many) {
@@ -601,20 +611,13 @@ __global__ void __launch_bounds__(kScanThreads, MASK || !ALIGNED ? 6 : 8) beam_s
         for (int v = 0; v < kVectors; ++v) {
           if (top[v] >= bound)
             list[count + __popc(who[v] & ((1u << lane) - 1))] =
-                Entry{top[v], at + (v * kScanThreads + t) * kVec};
+                Entry{top[v], at + first + v * kWarp * kVec};
           count += __popc(who[v]);
         }
       }
     }
   }
   // ---- the chunk's sum, and the warps' lists as one
-  constexpr int kOwn = 8;                         // entries of a thread
-  static_assert(kBeamMaxWidth <= kOwn * kWarp, "a warp's largest");
-  if (count > kOwn * kWarp) {
-    __syncwarp();
-    count = tighten(list, count, width);
-    many |= count > kOwn * kWarp;
-  }
   const uint32_t hi = __reduce_max_sync(0xffffffffu, key_of(ref)), most = __reduce_max_sync(0xffffffffu, key_of(peak));
   __syncthreads();                                // (of one tile: `red` is read)
   if (lane == 0) {
@@ -642,33 +645,24 @@ __global__ void __launch_bounds__(kScanThreads, MASK || !ALIGNED ? 6 : 8) beam_s
     for (int i = lane; i < count; i += kWarp) joined[before + i] = list[i];
   __syncthreads();
   if (!many && total > width + width / 4 + 8) {
-    uint32_t key[kOwn];
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i)
-      key[i] = t + i * kScanThreads < total ? key_of(joined[t + i * kScanThreads].logit) : key_of(-INFINITY);
-    bound = bound_of(block_bound<kScanThreads>(key, width, red));
-    if (t == 0) counts[0] = 0;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i) {              // what is left, to the front of the warps' lists
-      const bool stays = t + i * kScanThreads < total && of_key(key[i]) >= bound;
-      const unsigned who = __ballot_sync(0xffffffffu, stays);
-      int at = 0;
-      if (lane == 0 && who) at = atomicAdd(&counts[0], __popc(who));
-      at = __shfl_sync(0xffffffffu, at, 0);
-      if (stays) every[at + __popc(who & ((1u << lane) - 1))] = joined[t + i * kScanThreads];
+    if (warp == 0) {                              // (all warps with a barrier a bit: 3000 cycles, not 1500)
+      float least;
+      total = tighten(joined, total, width, least);
+      if (lane == 0) {
+        counts[0] = total;
+        red[0] = key_of(fmaxf(bound, least));
+      }
     }
-    joined = every;
     __syncthreads();
     total = counts[0];
+    bound = of_key(red[0]);
   }
   // ---- the list's elements
   Entry* out = p.entries + static_cast<int64_t>(blockIdx.x) * p.cap;
   int written = 0;
   if (!many) {
-    const int first = static_cast<int>(e0);
     for (int i = t; i < total * kVec; i += kScanThreads) {
-      const int e = first + joined[i / kVec].token + i % kVec;
+      const int e = static_cast<int>(e0) + joined[i / kVec].token + i % kVec;
       if (e >= e1 || (MASK && !allowed[e])) continue;
       const float x = load_element<DT>(logits, e);
       if (!(x >= bound)) continue;
@@ -1007,9 +1001,9 @@ __global__ void __launch_bounds__(kSmallThreads) beam_small_kernel(const __grid_
 // One launch for groups of at most this many logits, on average.
 constexpr int64_t kSmallGroup = 32768;
 constexpr int kSmallVocab = 4096;
-// CTAs of the scan that chunks are made for, one for each place that the SMs have (with two,
-// 32 x 32768 of 64 users 52 us against 50).
-constexpr int64_t kScanCtas = 152 * 8;
+// CTAs of the scan that chunks are made for: one for each place that the SMs have for masked
+// rows (33 of 1,000,003 with 825 CTAs 60 us, 1155 68, 1650 65; 8 places without a mask).
+constexpr int64_t kScanCtas = 152 * 6;
 constexpr int kLeastTiles = 2, kMostTiles = 16;  // of a chunk
 
 struct Plan {
@@ -1023,10 +1017,11 @@ Plan plan_of(const dlrm_beam_select_t& a) {
   if (s.small && a.rows <= kRowsHere) return s;
   s.bytes = a.rows * static_cast<int64_t>(sizeof(RowState));
   if (s.small) return s;
-  const int64_t tile = kScanThreads * kVectors * (a.dtype == DLRM_DTYPE_FP32 ? 4 : 8);
-  const int64_t tiles = (a.vocab + tile - 1) / tile;
-  const int64_t want = (kScanCtas + a.rows - 1) / a.rows;
-  s.tiles = static_cast<int>(std::max<int64_t>(kLeastTiles, std::min<int64_t>(tiles / want, kMostTiles)));
+  const int vec = a.dtype == DLRM_DTYPE_FP32 ? 4 : 8;
+  const int64_t tile = kScanThreads * kVectors * vec, tiles = (a.vocab + tile - 1) / tile;
+  const int64_t chunks = std::max((tiles + kMostTiles - 1) / kMostTiles,
+                                  std::min(kScanCtas / a.rows, (tiles + kLeastTiles - 1) / kLeastTiles));
+  s.tiles = static_cast<int>((tiles + chunks - 1) / chunks);
   s.chunks = static_cast<int>((tiles + s.tiles - 1) / s.tiles);
   s.cap = 8 * a.width + 256;
   s.parts = s.bytes;
@@ -1035,22 +1030,14 @@ Plan plan_of(const dlrm_beam_select_t& a) {
   return s;
 }
 
-template <int DT, bool MASK>
-cudaError_t launch_scan(const Params& p, bool aligned, cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>(p.a.rows * p.chunks);
-  const size_t smem = 2 * p.cap * sizeof(Entry);
-  return aligned ? launch_pdl(beam_scan_kernel<DT, MASK, true>, dim3(grid), dim3(kScanThreads), smem, stream, p)
-                 : launch_pdl(beam_scan_kernel<DT, MASK, false>, dim3(grid), dim3(kScanThreads), smem, stream, p);
-}
-
 template <int DT>
 cudaError_t launch(const Params& p, bool small, cudaStream_t stream) {
   if (small)
     return launch_pdl(beam_small_kernel<DT>, dim3(p.a.groups), dim3(kSmallThreads), 0, stream, p);
-  constexpr int kVec = Row<DT>::kVec;
-  const bool aligned = aligned_to(p.a.logits, 16) && (p.a.rows == 1 || p.a.ld % kVec == 0) &&
-                       (!p.a.allowed || (aligned_to(p.a.allowed, kVec) && (p.a.rows == 1 || p.a.ld_allowed % kVec == 0)));
-  const cudaError_t e = p.a.allowed ? launch_scan<DT, true>(p, aligned, stream) : launch_scan<DT, false>(p, aligned, stream);
+  const dim3 grid(static_cast<unsigned>(p.a.rows * p.chunks));
+  const size_t smem = 2 * p.cap * sizeof(Entry);
+  const cudaError_t e = launch_pdl(p.a.allowed ? beam_scan_kernel<DT, true> : beam_scan_kernel<DT, false>, grid,
+                                   dim3(kScanThreads), smem, stream, p);
   if (e != cudaSuccess) return e;
   return launch_pdl(beam_join_kernel, dim3(p.a.groups), dim3(kJoinThreads), 0, stream, p);
 }
