@@ -34,7 +34,8 @@ constexpr int kVectors = 4;                      // 16-byte vectors of a thread 
 constexpr int kSubsets = 64;                     // widths up to here: one subset a thread will do
 constexpr int kFinal = 2048;                     // candidates that are ranked at most
 constexpr int kLists = 1024;                     // lists of a group that shared memory knows
-constexpr int kRowsHere = 256;                   // rows of a group whose states lie in shared memory
+constexpr int kRowsHere = 256;                   // rows of a group whose states lie in shared memory,
+constexpr int kRowsJoin = 128;                   // and of the join's
 static_assert(kSubsets <= kScanThreads && kBeamMaxWidth <= kScanThreads * kVectors && kBeamMaxWidth <= kSmallThreads &&
                   kSmallThreads <= kJoinThreads && kBeamMaxWidth <= kFinal, "a subset for each place");
 
@@ -61,7 +62,7 @@ struct Entry {
 struct RowState {
   Sum lse;                                       // (first the sum of exponentials, and its reference in offset)
   float offset;                                  // score - lse; -infinity: the row has no candidates
-  int32_t pad;
+  float score;
 };
 static_assert(sizeof(Part) == 24 && sizeof(Entry) == 8 && sizeof(RowState) == 16, "scratch sizes");
 
@@ -165,43 +166,66 @@ __device__ __forceinline__ Sum log_sum(const Sum& s, float ref) {
   return Sum{sum, (y.sum - sum) + y.rest};
 }
 
-// A lower bound of the k-th largest of the threads' keys, N each, bit by bit from the first
-// that they do not have in common until few more than k reach it (keys of -infinity do not
-// count, and are the bound where there are fewer than k others). Block-wide. red: 2 ints a warp.
-template <int THREADS, int N>
-__device__ __forceinline__ uint32_t block_bound(const uint32_t (&key)[N], int k, uint32_t* red) {
+// A lower bound of the k-th largest of the threads' keys: the first eight bits that they do not
+// have in common by a count of each value, then bit by bit, until few more than k
+// reach it (keys of -infinity do not count, and are the bound where there are fewer than k
+// others). Block-wide; between two calls the caller has a barrier. red: kRed words a warp.
+constexpr int kRed = 19;
+template <int THREADS>
+__device__ __forceinline__ uint32_t block_bound(uint32_t key, int k, uint32_t* red) {
   constexpr int kWarps = THREADS / kWarp;
+  static_assert(kWarps <= kWarp, "a warp's lanes hold what all warps found");
+  const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
   const uint32_t none = key_of(-INFINITY);
-  uint32_t hi = none, lo = 0xffffffffu;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    hi = max(hi, key[i]);
-    lo = key[i] > none ? min(lo, key[i]) : lo;
+  uint32_t hi = __reduce_max_sync(0xffffffffu, key), lo = __reduce_min_sync(0xffffffffu, key > none ? key : 0xffffffffu);
+  int there = __popc(__ballot_sync(0xffffffffu, key > none));
+  if (lane == 0) {
+    red[warp] = hi;
+    red[kWarps + warp] = lo;
+    red[2 * kWarps + warp] = there;
   }
-  hi = __reduce_max_sync(0xffffffffu, hi);
-  lo = __reduce_min_sync(0xffffffffu, lo);
-  if (threadIdx.x % kWarp == 0) {
-    red[threadIdx.x / kWarp] = hi;
-    red[kWarps + threadIdx.x / kWarp] = lo;
-  }
+  constexpr int kValues = 256, kEach = kValues / kWarp;
+  static_assert(16 * kWarps >= kValues && THREADS >= kValues, "room");
+  int* values = reinterpret_cast<int*>(red + 3 * kWarps);
+  if (threadIdx.x < kValues) values[threadIdx.x] = 0;
   __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    hi = max(hi, red[w]);
-    lo = min(lo, red[kWarps + w]);
-  }
-  int there = 0;
-#pragma unroll
-  for (int i = 0; i < N; ++i) there += __syncthreads_count(key[i] > none);
+  const bool one = lane < kWarps;
+  hi = __reduce_max_sync(0xffffffffu, one ? red[lane] : 0);
+  lo = __reduce_min_sync(0xffffffffu, one ? red[kWarps + lane] : 0xffffffffu);
+  there = __reduce_add_sync(0xffffffffu, one ? red[2 * kWarps + lane] : 0);
   if (there < k) return none;
   if (hi == lo) return hi;
   const int first = 31 - __clz(hi ^ lo);
   uint32_t bound = first == 31 ? 0u : hi & (0xffffffffu << (first + 1));
-  for (int bit = first; bit >= 0 && there > k + k / 4 + 8; --bit) {
-    const uint32_t trial = bound | (1u << bit);
-    int n = 0;
+  const int low = max(first - 7, 0);
+  if (there > k + k / 4 + 8) {
+    if (key > none) atomicAdd(&values[key >> low & (kValues - 1)], 1);
+    __syncthreads();
+    int mine[kEach], from = 0;                    // keys of the lane's values, and with those of later lanes
 #pragma unroll
-    for (int i = 0; i < N; ++i) n += __syncthreads_count(key[i] >= trial);
+    for (int i = 0; i < kEach; ++i) from += mine[i] = values[lane * kEach + i];
+    const int own = from;
+#pragma unroll
+    for (int d = 1; d < kWarp; d *= 2) {
+      const int x = __shfl_down_sync(0xffffffffu, from, d);
+      if (lane + d < kWarp) from += x;
+    }
+    const int last = 31 - __clz(__ballot_sync(0xffffffffu, from >= k));   // (lane 0 has all)
+    int reach = from - own, value = 0, at = 0;    // of the largest value that k reach
+#pragma unroll
+    for (int i = kEach - 1; i >= 0; --i) {
+      reach += mine[i];
+      if (at < k) {
+        at = reach;
+        value = lane * kEach + i;
+      }
+    }
+    bound |= static_cast<uint32_t>(__shfl_sync(0xffffffffu, value, last)) << low;
+    there = __shfl_sync(0xffffffffu, at, last);
+  }
+  for (int bit = low - 1; bit >= 0 && there > k + k / 4 + 8; --bit) {
+    const uint32_t trial = bound | (1u << bit);
+    const int n = __syncthreads_count(key >= trial);
     if (n >= k) {
       bound = trial;
       there = n;
@@ -705,10 +729,10 @@ __device__ __forceinline__ uint64_t index_of(int row, int token) {
   return static_cast<uint64_t>(static_cast<uint32_t>(row)) << 32 | static_cast<uint32_t>(token);
 }
 
-// A row's state from its sum (in lse) and reference (in offset); a thread a row. Returns
+// A row's state from its sum (in lse), reference (in offset) and score; a thread a row. Returns
 // the offset's magnitude.
-__device__ __forceinline__ float row_state(const Params& p, int64_t row, RowState& s) {
-  const float score = p.a.scores ? p.a.scores[row] : 0.f, ref = s.offset, sum = s.lse.sum;
+__device__ __forceinline__ float row_state(const Params& p, RowState& s) {
+  const float score = s.score, ref = s.offset, sum = s.lse.sum;
   const bool bad = !(score < INFINITY) || !(sum < INFINITY) || ref == INFINITY;
   if (bad) flag(p.a.err, DLRM_ERRBIT_INVALID_ARG);
   if (bad || ref == -INFINITY || score == -INFINITY) {
@@ -724,11 +748,11 @@ __device__ __forceinline__ float row_state(const Params& p, int64_t row, RowStat
 template <int THREADS>
 __device__ __forceinline__ float widest_of(float mine, uint32_t* red) {
   uint32_t x = __reduce_max_sync(0xffffffffu, __float_as_uint(mine));
+  const int lane = threadIdx.x % kWarp;
   __syncthreads();
-  if (threadIdx.x % kWarp == 0) red[threadIdx.x / kWarp] = x;
+  if (lane == 0) red[threadIdx.x / kWarp] = x;
   __syncthreads();
-#pragma unroll
-  for (int w = 0; w < THREADS / kWarp; ++w) x = max(x, red[w]);
+  x = __reduce_max_sync(0xffffffffu, lane < THREADS / kWarp ? red[lane] : 0);
   __syncthreads();
   return __uint_as_float(x);
 }
@@ -737,41 +761,74 @@ __device__ __forceinline__ float widest_of(float mine, uint32_t* red) {
 // a score's own and an ulp of its offset's, twice.
 template <int THREADS>
 __device__ __forceinline__ float score_bound(float most, int k, float widest, uint32_t* red) {
-  const uint32_t key[1] = {key_of(most)};
-  const float bound = bound_of(block_bound<THREADS>(key, k, red));
+  const float bound = bound_of(block_bound<THREADS>(key_of(most), k, red));
   return bound > -FLT_MAX ? bound - (3e-7f * (fabsf(bound) + widest) + 1e-30f) : bound;
 }
 
-// Selects among the candidates that each(bound, f) calls f(row, token, logit, offset) for,
-// every thread for its own, and writes the group's outputs; it may pass over what lies below
+// Selects among the candidates that each(bound, most, f) calls f(row, token, logit, offset)
+// for, every thread for its own, and writes the group's outputs; it may pass over what lies below
 // the bound. No place of the result lies below `bound`. Rows count from the group's first, s0,
-// whose states are `state`. Block-wide.
-template <int THREADS, class Each>
+// whose states are `state`. LISTS: candidates come in lists, of which each looks at `most` entries;
+// the first bound is that of a part of them. Block-wide.
+template <int THREADS, bool LISTS, class Each>
 __device__ __forceinline__ void select_of(const Params& p, int64_t s0, const RowState* state, float widest, float bound,
                                           const Each& each, Candidate* found, uint32_t* red, int* count_s) {
   const int t = threadIdx.x, width = p.a.width;
   const auto score_of = [&](int row, float logit) {
-    const Sum lse = state[row].lse;
-    return static_cast<double>(p.a.scores ? p.a.scores[s0 + row] : 0.f) +
-           ((static_cast<double>(logit) - static_cast<double>(lse.sum)) - static_cast<double>(lse.rest));
+    const RowState s = state[row];
+    return static_cast<double>(s.score) +
+           ((static_cast<double>(logit) - static_cast<double>(s.lse.sum)) - static_cast<double>(s.lse.rest));
   };
-  float most = -INFINITY;
-  each(bound, [&](int, int, float logit, float offset) { most = fmaxf(most, offset + logit); });
-  bound = fmaxf(bound, score_bound<THREADS>(most, width, widest, red));
-  if (t == 0) *count_s = 0;
-  __syncthreads();
-  each(bound, [&](int row, int token, float logit, float offset) {
-    if (!(offset + logit >= bound)) return;
+  const auto better = [&](int entries) {         // the bound, by the threads' largest
+    float most = -INFINITY;
+    each(bound, entries, [&](int, int, float logit, float offset) { most = fmaxf(most, offset + logit); });
+    bound = fmaxf(bound, score_bound<THREADS>(most, width, widest, red));
+  };
+  const auto put = [&](const Candidate& c) {
     const int at = atomicAdd(count_s, 1);
-    if (at < kFinal) found[at] = Candidate{__float_as_uint(logit), row, token};
-  });
-  __syncthreads();
-  int n = *count_s;
+    if (at < kFinal) found[at] = c;
+  };
+  const auto collect = [&] {
+    if (t == 0) *count_s = 0;
+    __syncthreads();
+    each(bound, INT_MAX, [&](int row, int token, float logit, float offset) {
+      if (offset + logit >= bound) put(Candidate{__float_as_uint(logit), row, token});
+    });
+    __syncthreads();
+    return *count_s;
+  };
+  better(LISTS ? kWarp : INT_MAX);
+  int n = collect();
+  if (LISTS && n > kFinal) {
+    better(INT_MAX);
+    n = collect();
+  } else if (LISTS && n > width + width / 4 + 64) {
+    // the best of those that are here
+    constexpr int kMine = kFinal / THREADS;
+    Candidate mine[kMine];
+    float score[kMine], most = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      score[i] = -INFINITY;
+      if (t + i * THREADS >= n) continue;
+      mine[i] = found[t + i * THREADS];
+      score[i] = state[mine[i].row].offset + __uint_as_float(static_cast<uint32_t>(mine[i].key));
+      most = fmaxf(most, score[i]);
+    }
+    bound = fmaxf(bound, score_bound<THREADS>(most, width, widest, red));
+    if (t == 0) *count_s = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+      if (t + i * THREADS < n && score[i] >= bound) put(mine[i]);
+    __syncthreads();
+    n = *count_s;
+  }
   if (n > kFinal) {
     // too many at the bound: the exact score, then the exact index among its ties
     const auto reach = [&](uint64_t k, uint64_t last) {
       int c = 0;
-      each(bound, [&](int row, int token, float logit, float offset) {
+      each(bound, INT_MAX, [&](int row, int token, float logit, float offset) {
         if (!(offset + logit >= bound)) return;
         const uint64_t x = key_of(score_of(row, logit));
         c += x > k || (x == k && index_of(row, token) <= last);
@@ -797,12 +854,10 @@ __device__ __forceinline__ void select_of(const Params& p, int64_t s0, const Row
     __syncthreads();
     if (t == 0) *count_s = 0;
     __syncthreads();
-    each(bound, [&](int row, int token, float logit, float offset) {
+    each(bound, INT_MAX, [&](int row, int token, float logit, float offset) {
       if (!(offset + logit >= bound)) return;
       const uint64_t x = key_of(score_of(row, logit));
-      if (!(x > k || (x == k && index_of(row, token) <= last))) return;
-      const int at = atomicAdd(count_s, 1);
-      if (at < kFinal) found[at] = Candidate{__float_as_uint(logit), row, token};
+      if (x > k || (x == k && index_of(row, token) <= last)) put(Candidate{__float_as_uint(logit), row, token});
     });
     __syncthreads();
     n = min(*count_s, kFinal);
@@ -852,45 +907,51 @@ __device__ __forceinline__ void group_rows(const Params& p, int group, int64_t& 
 
 __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_constant__ Params p) {
   __shared__ Candidate found[kFinal];
-  __shared__ uint32_t red[2 * kJoinThreads / kWarp];
+  __shared__ uint32_t red[kRed * kJoinThreads / kWarp];
   __shared__ int count_s, n_open, open[kLists], list_count[kLists];   // open: lists to look at
   __shared__ float list_top[kLists];             // largest score of each
+  __shared__ RowState here[kRowsJoin];
   const int t = threadIdx.x, lane = t % kWarp, warp = t / kWarp;
   pdl_wait();
   pdl_trigger();
   int64_t s0, s1;
   group_rows(p, blockIdx.x, s0, s1);
   const int chunks = p.chunks;
-  RowState* state = p.rows + s0;
+  RowState* state = s1 - s0 <= kRowsJoin ? here : p.rows + s0;
+  const auto score_of_row = [&](int64_t row) { return p.a.scores && row < s1 - s0 ? p.a.scores[s0 + row] : 0.f; };
+  const float mine = score_of_row(t);
   // ---- the rows' sums, a warp each, then their logarithms, a thread each
   for (int64_t row = warp; row < s1 - s0; row += kJoinThreads / kWarp) {
     const Part* parts = p.parts + (s0 + row) * chunks;
-    uint32_t hi = 0;
-    for (int c = lane; c < chunks; c += kWarp) hi = max(hi, key_of(parts[c].ref));
+    const Part first = lane < chunks ? parts[lane] : Part{Sum{0.f, 0.f}, -INFINITY, -INFINITY, 0, 0};
+    uint32_t hi = key_of(first.ref);
+    for (int c = lane + kWarp; c < chunks; c += kWarp) hi = max(hi, key_of(parts[c].ref));
     const float ref = of_key(__reduce_max_sync(0xffffffffu, hi));
-    Sum sum{0.f, 0.f};
-    for (int c = lane; c < chunks; c += kWarp) {
+    Sum sum = moved(first.sum, first.ref, ref);
+    for (int c = lane + kWarp; c < chunks; c += kWarp) {
       const Sum x = moved(parts[c].sum, parts[c].ref, ref);
       sum.rest += x.rest;
       sum.add(x.sum);
     }
     sum = warp_sum(sum);
-    if (lane == 0) state[row] = RowState{sum, ref, 0};
+    if (lane == 0) state[row] = RowState{sum, ref, 0.f};
   }
   __syncthreads();
   float widest = 0.f;
   for (int64_t row = t; row < s1 - s0; row += kJoinThreads) {
     RowState s = state[row];
-    widest = fmaxf(widest, row_state(p, s0 + row, s));
+    s.score = row == t ? mine : score_of_row(row);
+    widest = fmaxf(widest, row_state(p, s));
     state[row] = s;
   }
   widest = widest_of<kJoinThreads>(widest, red);
   // ---- the lists, a warp each; those whose largest logit lies below the bound are passed over
-  const int64_t lists = (s1 - s0) * chunks;
+  // (below 2^31, as all rows' chunks are; 64-bit divisions took the join of 4 x 206 lists 5 us)
+  const unsigned lists = static_cast<unsigned>((s1 - s0) * chunks), per_row = chunks;
   const bool few = lists <= kLists;
-  const auto score_of_list = [&](int64_t l) { return state[l / chunks].offset + p.parts[s0 * chunks + l].top; };
+  const auto score_of_list = [&](unsigned l) { return state[l / per_row].offset + p.parts[s0 * chunks + l].top; };
   float most = -INFINITY;
-  for (int64_t l = t; l < lists; l += kJoinThreads) {
+  for (unsigned l = t; l < lists; l += kJoinThreads) {
     const float x = score_of_list(l);
     if (few) {
       list_top[l] = x;
@@ -899,30 +960,53 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_co
     most = fmaxf(most, x);
   }
   // where there are lists enough, one of their largest logits bounds the places
-  const float bound = lists >= p.a.width ? score_bound<kJoinThreads>(most, p.a.width, widest, red) : -FLT_MAX;
-  const auto each = [&](float least, const auto& f) {
+  const float bound = lists >= static_cast<unsigned>(p.a.width) ? score_bound<kJoinThreads>(most, p.a.width, widest, red) : -FLT_MAX;
+  const auto each = [&](float least, int entries_each, const auto& f) {
     __syncthreads();                              // `open` and its count are read
     if (t == 0) n_open = 0;
     __syncthreads();
-    for (int64_t l = t; l < lists; l += kJoinThreads) {
+    for (unsigned l = t; l < lists; l += kJoinThreads) {
       if (!((few ? list_top[l] : score_of_list(l)) >= least)) continue;
       const int at = atomicAdd(&n_open, 1);
       if (at < kLists) open[at] = static_cast<int>(l);
     }
     __syncthreads();
     const bool known = n_open <= kLists;          // else all of them are gone through
-    const int64_t n_lists = known ? n_open : lists;
-    for (int64_t i = warp; i < n_lists; i += kJoinThreads / kWarp) {
-      const int64_t l = known ? open[i] : i;
-      const int row = static_cast<int>(l / chunks);
-      const float offset = state[row].offset;
-      const int n = offset == -INFINITY ? 0 : few ? list_count[l] : p.parts[s0 * chunks + l].count;
-      const Entry* entries = p.entries + (s0 * chunks + l) * p.cap;
-#pragma unroll 4
-      for (int j = lane; j < n; j += kWarp) f(row, entries[j].token, entries[j].logit, offset);
+    const unsigned n_lists = known ? n_open : lists;
+    // kAtOnce lists at a time, kOfEach times 32 entries of each
+    constexpr int kAtOnce = 2, kOfEach = 2, kWarps = kJoinThreads / kWarp;
+    for (unsigned i0 = warp; i0 < n_lists; i0 += kAtOnce * kWarps) {
+      const Entry* entries[kAtOnce];
+      int row[kAtOnce], n[kAtOnce], longest = 0;
+      float offset[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const unsigned i = i0 + k * kWarps;
+        n[k] = 0;
+        if (i >= n_lists) continue;
+        const unsigned l = known ? open[i] : i;
+        row[k] = static_cast<int>(l / per_row);
+        offset[k] = state[row[k]].offset;
+        n[k] = offset[k] == -INFINITY ? 0 : min(few ? list_count[l] : p.parts[s0 * chunks + l].count, entries_each);
+        entries[k] = p.entries + (s0 * chunks + l) * p.cap;
+        longest = max(longest, n[k]);
+      }
+      for (int j = lane; j < longest; j += kOfEach * kWarp) {
+        Entry x[kAtOnce][kOfEach];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k)
+#pragma unroll
+          for (int u = 0; u < kOfEach; ++u)
+            if (j + u * kWarp < n[k]) x[k][u] = entries[k][j + u * kWarp];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k)
+#pragma unroll
+          for (int u = 0; u < kOfEach; ++u)
+            if (j + u * kWarp < n[k]) f(row[k], x[k][u].token, x[k][u].logit, offset[k]);
+      }
     }
   };
-  select_of<kJoinThreads>(p, s0, state, widest, bound, each, found, red, &count_s);
+  select_of<kJoinThreads, true>(p, s0, state, widest, bound, each, found, red, &count_s);
 }
 
 // Everything of a group in one CTA: its rows stay in L1 between the passes.
@@ -930,7 +1014,7 @@ template <int DT>
 __global__ void __launch_bounds__(kSmallThreads) beam_small_kernel(const __grid_constant__ Params p) {
   __shared__ Candidate found[kFinal];
   __shared__ RowState here[kRowsHere];
-  __shared__ uint32_t red[2 * kSmallThreads / kWarp];
+  __shared__ uint32_t red[kRed * kSmallThreads / kWarp];
   __shared__ int count_s;
   const int t = threadIdx.x, lane = t % kWarp, warp = t / kWarp, vocab = static_cast<int>(p.a.vocab);
   pdl_wait();
@@ -968,22 +1052,26 @@ __global__ void __launch_bounds__(kSmallThreads) beam_small_kernel(const __grid_
       sum.add(part);
     }
     sum = warp_sum(sum);
-    if (lane == 0) state[row - s0] = RowState{sum, top, 0};
+    if (lane == 0) state[row - s0] = RowState{sum, top, 0.f};
   }
   __syncthreads();
   float widest = 0.f;
   for (int64_t row = t; row < s1 - s0; row += kSmallThreads) {
     RowState s = state[row];
-    widest = fmaxf(widest, row_state(p, s0 + row, s));
+    s.score = p.a.scores ? p.a.scores[s0 + row] : 0.f;
+    widest = fmaxf(widest, row_state(p, s));
     state[row] = s;
   }
   widest = widest_of<kSmallThreads>(widest, red);
   // a warp takes 256 tokens of a row at a time
   const int pieces = (vocab + 255) / 256;
   const int64_t all = (s1 - s0) * pieces;
-  const auto each = [&](float, const auto& f) {
+  const auto divided = [&](int64_t u) {           // by the pieces of a row
+    return all >> 32 ? u / pieces : static_cast<int64_t>(static_cast<uint32_t>(u) / static_cast<uint32_t>(pieces));
+  };
+  const auto each = [&](float, int, const auto& f) {
     for (int64_t u = warp; u < all; u += kSmallThreads / kWarp) {
-      const int row = static_cast<int>(u / pieces), first = static_cast<int>(u % pieces) * 256 + lane;
+      const int row = static_cast<int>(divided(u)), first = static_cast<int>(u - static_cast<int64_t>(row) * pieces) * 256 + lane;
       const float offset = state[row].offset;
       if (offset == -INFINITY) continue;
       float x[8];
@@ -993,7 +1081,7 @@ __global__ void __launch_bounds__(kSmallThreads) beam_small_kernel(const __grid_
         if (x[i] > -INFINITY) f(row, first + i * kWarp, x[i], offset);
     }
   };
-  select_of<kSmallThreads>(p, s0, state, widest, -FLT_MAX, each, found, red, &count_s);
+  select_of<kSmallThreads, false>(p, s0, state, widest, -FLT_MAX, each, found, red, &count_s);
 }
 
 // ------------------------------------------------------------------ launches
