@@ -100,17 +100,7 @@ __device__ __forceinline__ float power(float ref) { return ceilf(ref * kLog2E); 
 __device__ __forceinline__ float exp_from(float x, float ref) {
   return fabsf(ref) < kFar ? exp2_approx(fmaf(x, kLog2E, -power(ref))) : exp2_approx((x - ref) * kLog2E);
 }
-// Two at a time: x a + b.
-__device__ __forceinline__ float2 exp2_of(float2 x, float a, float b) {
-  float2 y;
-  asm("{\n\t.reg .b64 x, a, b;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 a, {%4, %4};\n\tmov.b64 b, {%5, %5};\n\t"
-      "fma.rn.f32x2 x, x, a, b;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "=f"(y.x), "=f"(y.y)
-      : "f"(x.x), "f"(x.y), "f"(a), "f"(b));
-  y.x = exp2_approx(y.x);
-  y.y = exp2_approx(y.y);
-  return y;
-}
+// Two at a time.
 __device__ __forceinline__ float2 add2(float2 x, float2 y) {
   float2 z;
   asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 a, a, b;\n\t"
@@ -593,14 +583,19 @@ __global__ void __launch_bounds__(kScanThreads, MASK ? 6 : 8) beam_scan_kernel(c
       sum = moved(sum, ref, most);
       ref = most;
     }
+    // (sums two at a time; powers, too, would have their factors moved into pairs: 41.2 us, not 40.2)
     float2 part[kVectors];
     if (fabsf(ref) < kFar || ref == -INFINITY) {
       const float less = ref == -INFINITY ? 0.f : -power(ref);
 #pragma unroll
       for (int v = 0; v < kVectors; ++v) {
-        part[v] = exp2_of(pair_of<DT>(now[v], 0), kLog2E, less);
+        part[v] = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 1; i < kVec / 2; ++i) part[v] = add2(part[v], exp2_of(pair_of<DT>(now[v], i), kLog2E, less));
+        for (int i = 0; i < kVec / 2; ++i) {
+          const float2 x = pair_of<DT>(now[v], i);
+          const float2 y = make_float2(exp2_approx(fmaf(x.x, kLog2E, less)), exp2_approx(fmaf(x.y, kLog2E, less)));
+          part[v] = i == 0 ? y : add2(part[v], y);
+        }
       }
     } else {
 #pragma unroll
