@@ -1011,7 +1011,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_co
 // Everything of a group in one CTA: its rows stay in L1 between the passes. What bounds it: the
 // chain of its passes (4 rows of 256 logits 9 us, 256 groups of 32 such rows 15).
 template <int DT>
-__global__ void __launch_bounds__(kSmallThreads) beam_small_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kSmallThreads, 2) beam_small_kernel(const __grid_constant__ Params p) {
   __shared__ Candidate found[kFinal];
   __shared__ RowState here[kRowsHere];
   __shared__ uint32_t red[kRed * kSmallThreads / kWarp];
@@ -1034,10 +1034,14 @@ __global__ void __launch_bounds__(kSmallThreads) beam_small_kernel(const __grid_
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = may[i] ? x[i] : -INFINITY;
   };
-  for (int64_t row = s0 + warp; row < s1; row += kSmallThreads / kWarp) {
-    float x[8], top = -INFINITY;
+  // up to kHeld rows a warp of up to 256 logits stay in registers, and are read once
+  constexpr int kWarps = kSmallThreads / kWarp, kHeld = 2;
+  const bool holds = s1 - s0 <= kHeld * kWarps && vocab <= 256;
+  float held[kHeld][8];
+  const auto sums = [&](int64_t row, float (&x)[8], bool loaded) {
+    float top = -INFINITY;
     for (int e = lane; e < vocab; e += 8 * kWarp) {
-      load8(x, row, e);
+      if (!loaded) load8(x, row, e);
 #pragma unroll
       for (int i = 0; i < 8; ++i) top = fmaxf(top, x[i]);
     }
@@ -1053,6 +1057,19 @@ __global__ void __launch_bounds__(kSmallThreads) beam_small_kernel(const __grid_
     }
     sum = warp_sum(sum);
     if (lane == 0) state[row - s0] = RowState{sum, top, 0.f};
+  };
+  if (holds) {
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+      if (warp + k * kWarps < s1 - s0) load8(held[k], s0 + warp + k * kWarps, lane);
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+      if (warp + k * kWarps < s1 - s0) sums(s0 + warp + k * kWarps, held[k], true);
+  } else {
+    for (int64_t row = s0 + warp; row < s1; row += kWarps) {
+      float x[8];
+      sums(row, x, false);
+    }
   }
   __syncthreads();
   float widest = 0.f;
@@ -1070,7 +1087,19 @@ __global__ void __launch_bounds__(kSmallThreads) beam_small_kernel(const __grid_
     return all >> 32 ? u / pieces : static_cast<int64_t>(static_cast<uint32_t>(u) / static_cast<uint32_t>(pieces));
   };
   const auto each = [&](float, int, const auto& f) {
-    for (int64_t u = warp; u < all; u += kSmallThreads / kWarp) {
+    if (holds) {
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) {
+        const int row = warp + k * kWarps;
+        const float offset = row < s1 - s0 ? state[row].offset : -INFINITY;
+        if (offset == -INFINITY) continue;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (held[k][i] > -INFINITY) f(row, lane + i * kWarp, held[k][i], offset);
+      }
+      return;
+    }
+    for (int64_t u = warp; u < all; u += kWarps) {
       const int row = static_cast<int>(divided(u)), first = static_cast<int>(u - static_cast<int64_t>(row) * pieces) * 256 + lane;
       const float offset = state[row].offset;
       if (offset == -INFINITY) continue;

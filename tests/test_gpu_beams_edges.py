@@ -339,6 +339,29 @@ def test_strides_and_broadcast_masks():
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("vocab", [4096, 8197, 16383, 40960])
+def test_rows_may_begin_at_any_element(dtype, vocab):
+    """Wherever logits and masks lie the result is the same bit for bit, and what lies before
+    and behind a row is not the row's."""
+    rng = np.random.default_rng(20)
+    x = torch.from_numpy(rng.standard_normal((3, vocab))).to(TYPES[dtype]).cuda()
+    mask = torch.from_numpy(rng.random((3, vocab)) < 0.5).cuda()
+    starts = i32([0, 1, 3])
+    want = [dl.beam_select(x, None, starts, 40, allowed=m) for m in (None, mask)]
+    check_select(x, None, [0, 1, 3], 40, None, want[0])
+    check_select(x, None, [0, 1, 3], 40, mask, want[1])
+    for offset in range(9):
+        wide = torch.full((3, vocab + 21), float("nan"), dtype=x.dtype, device="cuda")
+        wide[:, offset:offset + vocab] = x
+        wide_mask = torch.ones(3, vocab + 23, dtype=torch.bool, device="cuda")
+        wide_mask[:, 2 * offset % 7:2 * offset % 7 + vocab] = mask
+        for m, expected in ((None, want[0]), (wide_mask[:, 2 * offset % 7:2 * offset % 7 + vocab], want[1])):
+            err = torch.zeros(1, dtype=torch.int32, device="cuda")
+            got = dl.beam_select(wide[:, offset:offset + vocab], None, starts, 40, allowed=m, err_flag=err)
+            assert int(err) == 0 and all(torch.equal(a, b) for a, b in zip(got, expected)), offset
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("vocab", [200, 70000])
 def test_zeros_of_both_signs_are_equal(dtype, vocab):
     rng = np.random.default_rng(18)
