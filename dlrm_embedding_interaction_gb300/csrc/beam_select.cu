@@ -550,34 +550,50 @@ __global__ void __launch_bounds__(kScanThreads, MASK ? 6 : 8) beam_scan_kernel(c
     peak = fmaxf(peak, most);
     static_assert(kVectors == 4, "largest of a thread");
     if (at == 0) {
-      // every warp has its share of `width` maxima at the least of the warps' bounds or
-      // above; and one reference for all threads, so that sums need no factors
-      constexpr int kShare = kWarps;
-      const int share = (width + kShare - 1) / kShare;
-      uint32_t key;
-      if (width <= kSubsets) {
-        const uint32_t mine[1] = {key_of(most)};
-        key = warp_bound(mine, share);
+      // each warp has its share of `width` maxima, as many as it has of all, at the least of the
+      // warps' bounds or above (equal shares would leave no bound where few warps have tokens: the
+      // end of a row, or a mask that allows a range); and one reference for all threads, so that
+      // sums need no factors
+      const bool few = width <= kSubsets;         // one subset a thread
+      int have = 0;
+      if (few) {
+        have = __popc(__ballot_sync(0xffffffffu, most > -INFINITY));
       } else {
-        uint32_t mine[kVectors];
 #pragma unroll
-        for (int v = 0; v < kVectors; ++v) mine[v] = key_of(top[v]);
-        key = warp_bound(mine, share);
+        for (int v = 0; v < kVectors; ++v) have += __popc(__ballot_sync(0xffffffffu, top[v] > -INFINITY));
       }
       const uint32_t hi = __reduce_max_sync(0xffffffffu, key_of(most));
       if (lane == 0) {
         red[warp] = hi;
-        red[kWarps + warp] = key;
+        counts[warp] = have;
       }
       __syncthreads();
       uint32_t all = red[0];
-      key = red[kWarps];
+      int maxima = counts[0];
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) {
         all = max(all, red[w]);
-        key = min(key, red[kWarps + w]);
+        maxima += counts[w];
       }
       ref = of_key(all);
+      uint32_t key = maxima < width ? 0u : 0xffffffffu;
+      if (have > 0 && maxima >= width) {
+        const int share = static_cast<unsigned>(width * have + maxima - 1) / static_cast<unsigned>(maxima);
+        if (few) {
+          const uint32_t mine[1] = {key_of(most)};
+          key = warp_bound(mine, share);
+        } else {
+          uint32_t mine[kVectors];
+#pragma unroll
+          for (int v = 0; v < kVectors; ++v) mine[v] = key_of(top[v]);
+          key = warp_bound(mine, share);
+        }
+      }
+      if (lane == 0) red[kWarps + warp] = key;
+      __syncthreads();
+      key = red[kWarps];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) key = min(key, red[kWarps + w]);
       bound = bound_of(key);
     } else if (most > ref + 20.f) {
       sum = moved(sum, ref, most);
@@ -613,18 +629,26 @@ __global__ void __launch_bounds__(kScanThreads, MASK ? 6 : 8) beam_scan_kernel(c
     sum.add(y.x + y.y);
     // ---- the warp's list
     unsigned who[kVectors];
-    int more = 0;
+    int more;
+    const auto look = [&] {
+      more = 0;
 #pragma unroll
-    for (int v = 0; v < kVectors; ++v) {
-      who[v] = __ballot_sync(0xffffffffu, top[v] >= bound);
-      more += __popc(who[v]);
-    }
+      for (int v = 0; v < kVectors; ++v) {
+        who[v] = __ballot_sync(0xffffffffu, top[v] >= bound);
+        more += __popc(who[v]);
+      }
+    };
+    look();
     if (more > 0) {
       if (count + more > room && !many) {
         // what is not among the warp's largest is not among the chunk's
         __syncwarp();
-        float least;
-        if (count > width) count = tighten(list, count, width, least);
+        if (count > width) {
+          float least;
+          count = tighten(list, count, width, least);
+          bound = fmaxf(bound, least);
+          look();
+        }
         many = count + more > room;
       }
       if (!many) {

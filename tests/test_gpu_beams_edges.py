@@ -362,6 +362,24 @@ def test_rows_may_begin_at_any_element(dtype, vocab):
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("width", [3, 27, 100])
+def test_masks_of_ranges_and_logits_that_rise(dtype, width):
+    """Tokens in a few places of a chunk only, and chunks whose last logits are the largest."""
+    rng = np.random.default_rng(21)
+    vocab = 20011
+    x = torch.from_numpy(rng.standard_normal((9, vocab))).to(TYPES[dtype]).cuda()
+    x[4] += torch.linspace(0, 30, vocab, device="cuda").to(x.dtype)
+    x[5] -= torch.linspace(0, 30, vocab, device="cuda").to(x.dtype)
+    mask = torch.zeros(9, vocab, dtype=torch.bool, device="cuda")
+    for row, (a, b) in enumerate([(0, 700), (1000, 1030), (5000, 9000), (19990, vocab), (0, vocab), (0, vocab), (4090, 4100),
+                                  (0, 2), (12000, 12900)]):
+        mask[row, a:b] = True
+    for starts in ([0, 9], list(range(10)), [0, 2, 4, 7, 9]):
+        check_select(x, None, starts, width, mask, dl.beam_select(x, None, i32(starts), width, allowed=mask))
+        check_select(x, None, starts, width, None, dl.beam_select(x, None, i32(starts), width))
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("vocab", [200, 70000])
 def test_zeros_of_both_signs_are_equal(dtype, vocab):
     rng = np.random.default_rng(18)
