@@ -321,16 +321,20 @@ cudaError_t launch_plan(const Params& p, cudaStream_t stream) {
 cudaError_t launch_history_prefix_attention(const dlrm_history_t& h, const dlrm_attention_t& a,
                                             const int32_t* groups, int n_groups, cudaStream_t stream) {
   using namespace prefix;
-  // Too little to share: history_attention's time, by its pieces (a request's 16 rows of a kv
-  // head, 0.013 us each) and by the bytes that all requests together can read (7.5 TB/s,
-  // most of them from L2) at most kApart us above its least, where the plan alone takes
-  // longer. In us, one query a request: 1 user x 4 beams x 400 events of 8 heads over 2
-  // 8.1 against 17, 64 x 4 x 400 16 against 21; 64 x 16 x 1500 74 against 48.
-  constexpr double kApart = 12.0;
+  // Too little to share: history_attention's time over its least, by its pieces (a request's
+  // rows of a kv head, 16 at a time, 0.007 us each) and the bytes that all requests together
+  // can read (7.5 TB/s, most of them from L2), is not above the plan's time and that of the shared
+  // pieces (a group's rows, a tile at a time, 0.0127 us each; how many events they share is not
+  // known here). In us, apart against shared, one query a request: 1 user x 4 beams x 400 events
+  // of 8 heads over 2 8.1 and 17, 17 x 12 x 430 fp16 18 and 29, 720 beams of five queries and 20
+  // events 17 and 31; 36 x 3 x 1500 at head_dim 128 41 and 33, 64 x 16 x 1500 74 and 48.
+  constexpr double kPlan = 12.0, kPiece = 0.007, kShared = 0.0127, kBytes = 7.5e6;
   const int64_t cap = static_cast<int64_t>(h.max_pages) * h.page_tokens;
   const int64_t seen = a.window > 0 ? std::min<int64_t>(cap, int64_t(a.window) + a.sinks + 2 * kBlock) : cap;
-  const int64_t tiles = a.batch + a.q_rows * (a.n_heads / h.n_heads) / 16;
-  if (0.013 * tiles * h.n_heads + 2e-6 / 7.5 * tiles * h.n_heads * seen * h.head_dim <= kApart && !history_tc_takes(h, a))
+  const int64_t rows = a.q_rows * (a.n_heads / h.n_heads);   // of a kv head
+  const double apart = static_cast<double>(a.batch + rows / 16) * h.n_heads;
+  const double tiles = static_cast<double>(n_groups + rows / (splits(a.dtype, rows, n_groups) ? 8 : 16)) * h.n_heads;
+  if (apart * (kPiece + 2 * h.head_dim / kBytes * seen) <= kPlan + kShared * tiles && !history_tc_takes(h, a))
     return launch_history_attention(h, a, stream, groups, n_groups);
   const HistoryWork w = history_work(h);
   Params p;

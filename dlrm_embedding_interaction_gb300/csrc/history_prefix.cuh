@@ -98,6 +98,13 @@ struct Params {
   float* partials;
 };
 
+// Whether queries and weights are split (Shape) for so many rows of a kv head: fp32, and 16-bit
+// rows that are no more than 8 of a group on average and leave half of an MMA's rows empty, whose
+// place the rests take.
+inline bool splits(int dtype, int64_t rows, int n_groups) {
+  return dtype == DLRM_DTYPE_FP32 || rows <= int64_t(8) * n_groups;
+}
+
 cudaError_t launch_plan(const Params& p, cudaStream_t stream);
 // By head_dim.
 cudaError_t launch_32(Params& p, cudaStream_t stream);
@@ -849,10 +856,8 @@ cudaError_t launch(Params& p, cudaStream_t stream) {
 
 template <int D, int DT>
 cudaError_t launch_rows(Params& p, cudaStream_t stream) {
-  // 16-bit rows that are no more than 8 of a group and kv head, on average, leave half of an
-  // MMA's rows empty: they take the rests' place
   if constexpr (DT != DLRM_DTYPE_FP32) {
-    if (p.a.q_rows * p.group > int64_t(8) * p.n_groups) return launch<D, DT, false>(p, stream);
+    if (!splits(DT, p.a.q_rows * p.group, p.n_groups)) return launch<D, DT, false>(p, stream);
   }
   return launch<D, DT, true>(p, stream);
 }

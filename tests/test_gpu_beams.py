@@ -47,7 +47,7 @@ def append(cache, pool, rng, slots, counts, spread=0.5):
     pool.append(slots, at, (f64(k), f64(v)))
 
 
-SHARED = 1 << 25                                  # bytes a side that make every call large enough to share
+SHARED = 1 << 27                                  # bytes a side that make every call large enough to share
 
 
 def beams(rng, lens, counts, new, kv, dim, page, spread=0.5, spare=0, shared=True, idle=0):
@@ -104,7 +104,7 @@ def test_beams_of_ragged_histories(dtype, dim, page, kv, group, causal, window, 
     new = [int(x) for x in rng.integers(0, 2 * page, n)]
     new[0] = new[4] = 0
     # (a window bounds what a call reads: there, requests without rows make it a large one)
-    more = 1000 // kv if shared and window else 0
+    more = 3000 // kv if shared and window else 0
     cache, pool, slots, groups = beams(rng, lens, counts, new, kv, dim, page, shared=shared, idle=more)
     queries = [int(x) for x in rng.integers(0, 4, n)] + [0] * more
     slots, groups = slots + [0] * more, groups + [n + more]

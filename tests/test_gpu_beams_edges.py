@@ -56,7 +56,7 @@ def test_strided_queries_and_outputs(dtype, layout):
 def test_what_masked_events_hold_has_no_influence(dtype):
     """NaN and infinities outside the window, in shared and in own pages, and behind the end."""
     rng = np.random.default_rng(2)
-    idle = 1000
+    idle = 3000
     cache, pool, slots, groups = beams(rng, [300], [4], [0] * 4, 1, 64, 32, spare=20, idle=idle)
     bad = torch.full((40, 1, 64), float("nan"), device="cuda")
     bad[::2] = float("inf")
@@ -115,7 +115,7 @@ def test_infinite_queries_and_rows_without_weights(dtype):
 
 def test_trimmed_pages_are_read_by_no_window_that_left_them():
     rng = np.random.default_rng(4)
-    idle = 1000
+    idle = 3000
     cache, pool, slots, groups = beams(rng, [500], [4], [3, 40, 3, 70], 1, 64, 32, spare=10, idle=idle)
     for where in (slots[:2], slots[2:]):
         dl.history_trim(cache, i32(where), 100, 10)
