@@ -452,8 +452,8 @@ __device__ __forceinline__ uint32_t warp_bound(const uint32_t (&key)[N], int k) 
 }
 
 // What bounds it: instructions (a conversion, half an FMA, one exponential and half a sum a
-// logit; issue slots are 59% busy) and what each CTA begins and ends with, then HBM: 1643 rows of
-// 32,768 bf16 logits 35 us (3.1 TB/s), 33 of 1,000,003 masked fp16 ones 44 us (2.3 TB/s).
+// logit; issue slots are 63% busy) and what each CTA begins and ends with, then HBM: 1643 rows of
+// 32,768 bf16 logits 36 us (3.0 TB/s), 33 of 1,000,003 masked fp16 ones 42 us (2.4 TB/s).
 // Warps meet twice, after the first tile and at the end: each has a list of its own, of vectors
 // by their largest element; their elements are looked at once more at the end.
 template <int DT, bool MASK>
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kScanThreads, MASK ? 6 : 8) beam_scan_kernel(c
       sum = moved(sum, ref, most);
       ref = most;
     }
-    // (sums two at a time; powers, too, would have their factors moved into pairs: 41.2 us, not 40.2)
+    // (sums two at a time; powers, too, would have their factors moved into pairs: 2.5% longer)
     float2 part[kVectors];
     if (fabsf(ref) < kFar || ref == -INFINITY) {
       const float less = ref == -INFINITY ? 0.f : -power(ref);
@@ -927,7 +927,7 @@ __device__ __forceinline__ void group_rows(const Params& p, int group, int64_t& 
 }
 
 // What bounds it: a chain of loads and barriers: sums, tops of the lists, a part of the lists,
-// the lists, ranks (64 groups of 26 lists 12 us, 4 groups of 206 lists of 100 19 us).
+// the lists, ranks (64 groups of 26 lists 12 us, 4 groups of 206 lists of 100 20 us).
 __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_constant__ Params p) {
   __shared__ Candidate found[kFinal];
   __shared__ uint32_t red[kRed * kJoinThreads / kWarp];
@@ -1033,7 +1033,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_co
 }
 
 // Everything of a group in one CTA: its rows stay in L1 between the passes. What bounds it: the
-// chain of its passes (4 rows of 256 logits 9 us, 256 groups of 32 such rows 15).
+// chain of its passes (4 rows of 256 logits 9 to 10 us, 256 groups of 32 such rows 14).
 template <int DT>
 __global__ void __launch_bounds__(kSmallThreads, 2) beam_small_kernel(const __grid_constant__ Params p) {
   __shared__ Candidate found[kFinal];
@@ -1143,7 +1143,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) beam_small_kernel(const __gr
 constexpr int64_t kSmallGroup = 32768;
 constexpr int kSmallVocab = 4096;
 // CTAs of the scan that chunks are made for: one for each place that the SMs have for masked
-// rows (33 of 1,000,003 with 825 CTAs 60 us, 1155 68, 1650 65; 8 places without a mask).
+// rows (33 of 1,000,003 with 825 CTAs took 60 us, with 1155 68, 1650 65; 8 places without a mask).
 constexpr int64_t kScanCtas = 152 * 6;
 constexpr int kLeastTiles = 2, kMostTiles = 16;  // of a chunk
 
