@@ -448,7 +448,7 @@ def test_bad_rows_and_starts_are_reported_and_the_others_served(vocab):
 
 @pytest.mark.parametrize("counts,vocab,width", [([700], 40, 200), ([1] * 3000, 30, 2), ([0, 300, 1], 5000, 256),
                                                 ([40], 200000, 10), ([2], 3000017, 64),
-                                                ([1, 2], 2 ** 24 + 9, 5)])
+                                                ([1, 2], 2 ** 24 + 9, 5), ([1500], 5000, 7), ([3, 2500], 4500, 100)])
 def test_many_rows_groups_and_chunks(counts, vocab, width):
     g = torch.Generator(device="cuda")
     g.manual_seed(14)
