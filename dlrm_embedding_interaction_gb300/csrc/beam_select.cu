@@ -119,12 +119,23 @@ __device__ __forceinline__ Sum warp_sum(Sum s) {
   }
   return s;
 }
-// What a sum with reference `from` is with reference `to` (>= from).
+// What a sum with reference `from` is with reference `to` (>= from). A near reference scales by
+// 2^-power(ref), a far one by 2^-(ref kLog2E); where one is near and one far, the power between
+// the two scales is one FMA, too (e^(from - to) there left out what power() rounds up: a sum up
+// to twice too small or large).
 __device__ __forceinline__ Sum moved(Sum s, float from, float to) {
   if (from == to) return s;
   if (from == -INFINITY) return Sum{s.sum, 0.f};  // zero, or NaN
-  const float f = fabsf(from) < kFar && fabsf(to) < kFar ? pow2f(static_cast<int>(fmaxf(power(from) - power(to), -126.f)))
-                                                         : exp2_approx((from - to) * kLog2E);
+  const bool near_from = fabsf(from) < kFar, near_to = fabsf(to) < kFar;
+  float f;
+  if (near_from && near_to)
+    f = pow2f(static_cast<int>(fmaxf(power(from) - power(to), -126.f)));
+  else if (near_from)
+    f = exp2_approx(fmaf(-to, kLog2E, power(from)));
+  else if (near_to)
+    f = exp2_approx(fmaf(from, kLog2E, -power(to)));
+  else
+    f = exp2_approx((from - to) * kLog2E);
   return Sum{s.sum * f, s.rest * f};              // (a power of two is exact)
 }
 // log(s) with its reference, in two floats: s = m 2^k with m around 1, log m = 2 artanh z,

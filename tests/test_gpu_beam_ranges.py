@@ -1,0 +1,73 @@
+"""The beam search's operators on the GPU over ranges of values and sizes where one way of
+computing passes into another. Bounds as in test_gpu_beams.py."""
+import numpy as np
+import pytest
+
+import beam_ref
+import test_gpu_beams as base
+
+torch = pytest.importorskip("torch")
+import dlrm_embedding_interaction_gb300 as dl  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+f64, i32 = base.f64, base.i32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    if not torch.cuda.is_available():
+        pytest.fail("the gpu tests need a CUDA device")
+    from dlrm_embedding_interaction_gb300 import build
+    build.build()
+    torch.cuda.set_device(0)
+
+
+# ------------------------------------------------------------------ selection
+
+@pytest.mark.parametrize("first,second", [(-1, 1), (1, -1), (-21, 1), (1, 1), (-1, -1)])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("where", ["two chunks", "two warps", "two tiles"])
+def test_logits_on_both_sides_of_65536(where, sign, first, second):
+    """Sums of exponentials have one scale for references below 65,536 in magnitude and another
+    from there on; parts of a row (chunks, a CTA's warps, a thread's tiles of 2048 tokens) may
+    have either. A row's two logits that count stand on sides `first` and `second` of the edge
+    or further below it. One candidate a group: its score is -log(1 + e^(difference)), within
+    2^-20 and half an ulp of fp32."""
+    rows = 96
+    at = {"two chunks": (5, 20000), "two warps": (5, 1500), "two tiles": (5, 2048 + 5)}[where]
+    near = np.linspace(1 / 128, 1.6, rows)
+    x = np.full((rows, 30000), -1e9, np.float32)
+    # (steps of 2^-7 and 2^-8: numbers of fp32 on either side)
+    for column, side, gap in ((at[0], first, near), (at[1], second, near[::-1] + 1 / 128)):
+        gap = gap if abs(side) == 1 else gap + abs(side)
+        x[:, column] = (sign * 65536 + np.sign(side) * gap).astype(np.float32)
+    logits = torch.from_numpy(x).cuda()
+    starts = list(range(rows + 1))
+    got = dl.beam_select(logits, None, i32(starts), 1)
+    want, _, tokens, _ = beam_ref.select(f64(logits), np.zeros(rows), starts, 1)
+    best = got[0].cpu().numpy().astype(np.float64)
+    assert (np.abs(best - want) <= 2.0 ** -20 + 2.0 ** -24 * np.abs(want)).all(), np.abs(best - want).max()
+    np.testing.assert_array_equal(got[2].cpu().numpy(), tokens)
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+def test_rows_around_65536_keep_their_order(sign):
+    """Rows of one group whose scores are the logarithms of their own sums: every candidate's
+    score is its logit, so the order over all rows is that of the logits, which lie 2^-7 apart."""
+    rng = np.random.default_rng(1)
+    rows, vocab, width = 24, 20000, 48
+    x = np.full((rows, vocab), -1e9, np.float32)
+    steps = rng.permutation(rows * 8).reshape(rows, 8)
+    columns = rng.permutation(vocab)[:rows * 8].reshape(rows, 8)
+    np.put_along_axis(x, columns, (sign * 65536 + (steps - rows * 4) / 128.0).astype(np.float32), 1)
+    d = x.astype(np.float64)
+    top = d.max(1, keepdims=True)
+    # a sum that is a number of fp32 (2^-7 apart) less: scores take the whole part of it
+    lse = (np.log(np.exp(d - top).sum(1, keepdims=True)) + top)[:, 0]
+    scores = torch.from_numpy(lse.astype(np.float32)).cuda()
+    got = dl.beam_select(torch.from_numpy(x).cuda(), scores, i32([0, rows]), width)
+    want, want_rows, want_tokens, every = beam_ref.select(d, f64(scores), [0, rows], width)
+    picked = every[got[1].cpu().numpy(), got[2].cpu().numpy()]
+    # (a score is the logit and up to 2^-8 that the row's logarithm lost as a number of fp32)
+    assert (np.abs(picked - want) <= 2.0 ** -19).all(), np.abs(picked - want).max()
+    assert (np.abs(got[0].cpu().numpy() - want) <= 2.0 ** -20 + 2.0 ** -24 * np.abs(want)).all()
