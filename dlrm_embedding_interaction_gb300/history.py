@@ -384,9 +384,10 @@ def history_prefix_attention(cache: HistoryCache, slots, starts, groups, q, out=
     requests [groups[g], groups[g+1]) are a group, and the first pages that its slots
     have in common are read once for all its rows; returns ``out``.
 
-    ``groups``: (n_groups + 1,) int32. The result is history_attention's whatever the
-    groups; rows of requests that no group holds stay as they were. At most as many
-    requests and groups as the cache has slots."""
+    ``groups``: (n_groups + 1,) int32, from 0 to the number of requests: each request is in a
+    group. Groups that leave requests out or decrease set an error bit, and the call's
+    outputs are then undefined. The result is history_attention's whatever the groups. At
+    most as many requests and groups as the cache has slots."""
     return _cache_attention("history_prefix_attention", cache, slots, starts, groups, q, out, scale, causal,
                             window, sinks, lse, stream)
 
@@ -410,6 +411,8 @@ def _cache_attention(where, cache, slots, starts, groups, q, out, scale, causal,
         n_groups = _int32_vector(groups, l_groups, None, index) - 1
         if n_groups < 0:
             raise ValueError(f"{where}: groups: expected at least one entry")
+        if n_groups == 0 and b > 0:
+            raise ValueError(f"{where}: {b} requests in no group")
         if max(b, n_groups) > c.n_slots:
             raise ValueError(f"{where}: {b} requests in {n_groups} groups for {c.n_slots} slots")
     out, os = _check_outputs(where, q, shape, out, lse, window, sinks, index, stream)

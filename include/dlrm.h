@@ -656,7 +656,8 @@ dlrm_status_t window_attention(const dlrm_attention_t* a, void* stream);
  *   groups  (n_groups + 1) int32 from 0 to batch; batch and n_groups <= n_slots
  * Starts or groups that decrease, leave their range or leave requests out set
  * DLRM_ERRBIT_OFFSETS; the call's outputs are then undefined, and its work stays
- * bounded. UNSUPPORTED: more than 2^18 query rows of heads that share a kv head, and
+ * bounded. A call with n_groups 0 does nothing: it reads no group, sets no bit, and leaves out
+ * as it was, even with requests. UNSUPPORTED: more than 2^18 query rows of heads that share a kv head, and
  * 2^30 work units or more. */
 dlrm_status_t history_prefix_attention(const dlrm_history_t* h, const dlrm_attention_t* a,
                                        const int32_t* groups, int32_t n_groups, void* stream);
