@@ -761,49 +761,43 @@ __device__ __forceinline__ uint64_t index_of(int row, int token) {
   return static_cast<uint64_t>(static_cast<uint32_t>(row)) << 32 | static_cast<uint32_t>(token);
 }
 
-// A row's state from its sum (in lse), reference (in offset) and score; a thread a row. Returns
-// the offset's magnitude.
-__device__ __forceinline__ float row_state(const Params& p, RowState& s) {
+// A row's state from its sum (in lse), reference (in offset) and score; a thread a row.
+__device__ __forceinline__ void row_state(const Params& p, RowState& s) {
   const float score = s.score, ref = s.offset, sum = s.lse.sum;
   const bool bad = !(score < INFINITY) || !(sum < INFINITY) || ref == INFINITY;
   if (bad) flag(p.a.err, DLRM_ERRBIT_INVALID_ARG);
   if (bad || ref == -INFINITY || score == -INFINITY) {
     s.offset = -INFINITY;
-    return 0.f;
+    return;
   }
   s.lse = log_sum(s.lse, ref);
   s.offset = (score - s.lse.sum) - s.lse.rest;
-  return fabsf(s.offset);
 }
 
-// Largest magnitude of the rows' offsets, in every thread.
-template <int THREADS>
-__device__ __forceinline__ float widest_of(float mine, uint32_t* red) {
-  uint32_t x = __reduce_max_sync(0xffffffffu, __float_as_uint(mine));
-  const int lane = threadIdx.x % kWarp;
-  __syncthreads();
-  if (lane == 0) red[threadIdx.x / kWarp] = x;
-  __syncthreads();
-  x = __reduce_max_sync(0xffffffffu, lane < THREADS / kWarp ? red[lane] : 0);
-  __syncthreads();
-  return __uint_as_float(x);
-}
+// Scores in fp32 only decide which candidates are looked at. offset + logit is off by two
+// roundings of the offset and one of the sum. Lowered or raised by four half ulps, of which one is
+// for its own rounding, the offset leaves the sum's alone: bounds are those of lowered
+// scores, and raised ones have to reach them. So a row that is far from the others (a beam that is
+// not in use, at -1e9) makes no margin but its own wide: with one for all rows 128 beams of 4096
+// tokens, 16 of them in use, took 5600 us, and take 27.
+__device__ __forceinline__ float lowered(float offset) { return fmaf(fabsf(offset), -0x1p-22f, offset); }
+__device__ __forceinline__ float raised(float offset) { return fmaf(fabsf(offset), 0x1p-22f, offset); }
 
-// Below the k-th largest of the threads' scores by what fp32 may be off: half an ulp of
-// a score's own and an ulp of its offset's, twice.
+// Below the k-th largest of the threads' lowered scores by the rounding of that sum, of the
+// raised one that is to reach it and of the bound itself: three half ulps, and 5 are taken.
 template <int THREADS>
-__device__ __forceinline__ float score_bound(float most, int k, float widest, uint32_t* red) {
+__device__ __forceinline__ float score_bound(float most, int k, uint32_t* red) {
   const float bound = bound_of(block_bound<THREADS>(key_of(most), k, red));
-  return bound > -FLT_MAX ? bound - (3e-7f * (fabsf(bound) + widest) + 1e-30f) : bound;
+  return bound > -FLT_MAX ? fmaxf(bound - (3e-7f * fabsf(bound) + 1e-30f), -FLT_MAX) : bound;
 }
 
 // Selects among the candidates that each(bound, most, f) calls f(row, token, logit, offset)
 // for, every thread for its own, and writes the group's outputs; it may pass over what lies below
-// the bound. No place of the result lies below `bound`. Rows count from the group's first, s0,
+// the bound. No place's raised score lies below `bound`. Rows count from the group's first, s0,
 // whose states are `state`. LISTS: candidates come in lists, of which each looks at `most` entries;
 // the first bound is that of a part of them. Block-wide.
 template <int THREADS, bool LISTS, class Each>
-__device__ __forceinline__ void select_of(const Params& p, int64_t s0, const RowState* state, float widest, float bound,
+__device__ __forceinline__ void select_of(const Params& p, int64_t s0, const RowState* state, float bound,
                                           const Each& each, Candidate* found, uint32_t* red, int* count_s) {
   const int t = threadIdx.x, width = p.a.width;
   const auto score_of = [&](int row, float logit) {
@@ -813,8 +807,8 @@ __device__ __forceinline__ void select_of(const Params& p, int64_t s0, const Row
   };
   const auto better = [&](int entries) {         // the bound, by the threads' largest
     float most = -INFINITY;
-    each(bound, entries, [&](int, int, float logit, float offset) { most = fmaxf(most, offset + logit); });
-    bound = fmaxf(bound, score_bound<THREADS>(most, width, widest, red));
+    each(bound, entries, [&](int, int, float logit, float offset) { most = fmaxf(most, lowered(offset) + logit); });
+    bound = fmaxf(bound, score_bound<THREADS>(most, width, red));
   };
   const auto put = [&](const Candidate& c) {
     const int at = atomicAdd(count_s, 1);
@@ -824,7 +818,7 @@ __device__ __forceinline__ void select_of(const Params& p, int64_t s0, const Row
     if (t == 0) *count_s = 0;
     __syncthreads();
     each(bound, INT_MAX, [&](int row, int token, float logit, float offset) {
-      if (offset + logit >= bound) put(Candidate{__float_as_uint(logit), row, token});
+      if (raised(offset) + logit >= bound) put(Candidate{__float_as_uint(logit), row, token});
     });
     __syncthreads();
     return *count_s;
@@ -838,16 +832,17 @@ __device__ __forceinline__ void select_of(const Params& p, int64_t s0, const Row
     // the best of those that are here
     constexpr int kMine = kFinal / THREADS;
     Candidate mine[kMine];
-    float score[kMine], most = -INFINITY;
+    float score[kMine], most = -INFINITY;         // (raised)
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
       score[i] = -INFINITY;
       if (t + i * THREADS >= n) continue;
       mine[i] = found[t + i * THREADS];
-      score[i] = state[mine[i].row].offset + __uint_as_float(static_cast<uint32_t>(mine[i].key));
-      most = fmaxf(most, score[i]);
+      const float offset = state[mine[i].row].offset, logit = __uint_as_float(static_cast<uint32_t>(mine[i].key));
+      score[i] = raised(offset) + logit;
+      most = fmaxf(most, lowered(offset) + logit);
     }
-    bound = fmaxf(bound, score_bound<THREADS>(most, width, widest, red));
+    bound = fmaxf(bound, score_bound<THREADS>(most, width, red));
     if (t == 0) *count_s = 0;
     __syncthreads();
 #pragma unroll
@@ -861,7 +856,7 @@ __device__ __forceinline__ void select_of(const Params& p, int64_t s0, const Row
     const auto reach = [&](uint64_t k, uint64_t last) {
       int c = 0;
       each(bound, INT_MAX, [&](int row, int token, float logit, float offset) {
-        if (!(offset + logit >= bound)) return;
+        if (!(raised(offset) + logit >= bound)) return;
         const uint64_t x = key_of(score_of(row, logit));
         c += x > k || (x == k && index_of(row, token) <= last);
       });
@@ -887,7 +882,7 @@ __device__ __forceinline__ void select_of(const Params& p, int64_t s0, const Row
     if (t == 0) *count_s = 0;
     __syncthreads();
     each(bound, INT_MAX, [&](int row, int token, float logit, float offset) {
-      if (!(offset + logit >= bound)) return;
+      if (!(raised(offset) + logit >= bound)) return;
       const uint64_t x = key_of(score_of(row, logit));
       if (x > k || (x == k && index_of(row, token) <= last)) put(Candidate{__float_as_uint(logit), row, token});
     });
@@ -943,7 +938,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_co
   __shared__ Candidate found[kFinal];
   __shared__ uint32_t red[kRed * kJoinThreads / kWarp];
   __shared__ int count_s, n_open, open[kLists], list_count[kLists];   // open: lists to look at
-  __shared__ float list_top[kLists];             // largest score of each
+  __shared__ float list_top[kLists];             // largest (raised) score of each
   __shared__ RowState here[kRowsJoin];
   const int t = threadIdx.x, lane = t % kWarp, warp = t / kWarp;
   pdl_wait();
@@ -971,30 +966,31 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_co
     if (lane == 0) state[row] = RowState{sum, ref, 0.f};
   }
   __syncthreads();
-  float widest = 0.f;
   for (int64_t row = t; row < s1 - s0; row += kJoinThreads) {
     RowState s = state[row];
     s.score = row == t ? mine : score_of_row(row);
-    widest = fmaxf(widest, row_state(p, s));
+    row_state(p, s);
     state[row] = s;
   }
-  widest = widest_of<kJoinThreads>(widest, red);
+  __syncthreads();
   // ---- the lists, a warp each; those whose largest logit lies below the bound are passed over
   // (below 2^31, as all rows' chunks are)
   const unsigned lists = static_cast<unsigned>((s1 - s0) * chunks), per_row = chunks;
   const bool few = lists <= kLists;
-  const auto score_of_list = [&](unsigned l) { return state[l / per_row].offset + p.parts[s0 * chunks + l].top; };
+  const auto score_of_list = [&](unsigned l) { return raised(state[l / per_row].offset) + p.parts[s0 * chunks + l].top; };
   float most = -INFINITY;
   for (unsigned l = t; l < lists; l += kJoinThreads) {
-    const float x = score_of_list(l);
+    const float offset = state[l / per_row].offset;
+    const Part& part = p.parts[s0 * chunks + l];
+    const float top = part.top;
     if (few) {
-      list_top[l] = x;
-      list_count[l] = p.parts[s0 * chunks + l].count;
+      list_top[l] = raised(offset) + top;
+      list_count[l] = part.count;
     }
-    most = fmaxf(most, x);
+    most = fmaxf(most, lowered(offset) + top);
   }
   // where there are lists enough, one of their largest logits bounds the places
-  const float bound = lists >= static_cast<unsigned>(p.a.width) ? score_bound<kJoinThreads>(most, p.a.width, widest, red) : -FLT_MAX;
+  const float bound = lists >= static_cast<unsigned>(p.a.width) ? score_bound<kJoinThreads>(most, p.a.width, red) : -FLT_MAX;
   const auto each = [&](float least, int entries_each, const auto& f) {
     __syncthreads();                              // `open` and its count are read
     if (t == 0) n_open = 0;
@@ -1040,7 +1036,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_co
       }
     }
   };
-  select_of<kJoinThreads, true>(p, s0, state, widest, bound, each, found, red, &count_s);
+  select_of<kJoinThreads, true>(p, s0, state, bound, each, found, red, &count_s);
 }
 
 // Everything of a group in one CTA: its rows stay in L1 between the passes. What bounds it: the
@@ -1107,14 +1103,13 @@ __global__ void __launch_bounds__(kSmallThreads, 2) beam_small_kernel(const __gr
     }
   }
   __syncthreads();
-  float widest = 0.f;
   for (int64_t row = t; row < s1 - s0; row += kSmallThreads) {
     RowState s = state[row];
     s.score = p.a.scores ? p.a.scores[s0 + row] : 0.f;
-    widest = fmaxf(widest, row_state(p, s));
+    row_state(p, s);
     state[row] = s;
   }
-  widest = widest_of<kSmallThreads>(widest, red);
+  __syncthreads();
   // a warp takes 256 tokens of a row at a time
   const int pieces = (vocab + 255) / 256;
   const int64_t all = (s1 - s0) * pieces;
@@ -1145,7 +1140,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) beam_small_kernel(const __gr
         if (x[i] > -INFINITY) f(row, first + i * kWarp, x[i], offset);
     }
   };
-  select_of<kSmallThreads, false>(p, s0, state, widest, -FLT_MAX, each, found, red, &count_s);
+  select_of<kSmallThreads, false>(p, s0, state, -FLT_MAX, each, found, red, &count_s);
 }
 
 // ------------------------------------------------------------------ launches

@@ -71,3 +71,72 @@ def test_rows_around_65536_keep_their_order(sign):
     # (a score is the logit and up to 2^-8 that the row's logarithm lost as a number of fp32)
     assert (np.abs(picked - want) <= 2.0 ** -19).all(), np.abs(picked - want).max()
     assert (np.abs(got[0].cpu().numpy() - want) <= 2.0 ** -20 + 2.0 ** -24 * np.abs(want)).all()
+
+
+def microseconds(call, turns=5):
+    """The least of a few timings of the call."""
+    times = []
+    for _ in range(turns):
+        begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        begin.record()
+        call()
+        end.record()
+        torch.cuda.synchronize()
+        times.append(1000 * begin.elapsed_time(end))
+    return min(times)
+
+
+# Beams that are not in use, as searches mark them.
+UNUSED = [-1e4, -1e9, float(np.finfo(np.float32).min)]
+
+
+@pytest.mark.parametrize("unused", UNUSED)
+@pytest.mark.parametrize("dtype,vocab,width", [("fp32", 256, 8), ("fp32", 4096, 8), ("bf16", 32768, 16), ("fp16", 300007, 100)])
+@pytest.mark.parametrize("used", [1, 7])
+def test_beams_that_are_not_in_use(dtype, vocab, width, used, unused):
+    """They lose to every continuation of the others, and cost no more than if they were in use
+    (ten times, as calls of microseconds are noisy; where the farthest row's rounding is
+    everybody's margin it is a hundred times)."""
+    rng = np.random.default_rng(vocab + used)
+    beams, groups = 8, 4
+    starts = list(range(0, groups * beams + 1, beams))
+    logits = torch.from_numpy(2 * rng.standard_normal((groups * beams, vocab))).to(base.TYPES[dtype]).cuda()
+    scores = torch.from_numpy(-5 * rng.random(groups * beams)).float().cuda()
+    at = i32(starts)
+    before = microseconds(lambda: dl.beam_select(logits, scores, at, width))
+    scores.view(groups, beams)[:, used:] = unused
+    got = dl.beam_select(logits, scores, at, width)
+    best, rows, tokens = (x.cpu().numpy() for x in got)
+    want, want_rows, want_tokens, every = beam_ref.select(f64(logits), f64(scores), starts, width)
+    assert ((rows - np.arange(groups)[:, None] * beams) < used).all()
+    assert (np.abs(best - want) <= 2.0 ** -20 + 2.0 ** -24 * np.abs(want)).all()
+    assert (np.abs(every[rows, tokens] - want) <= 2.0 ** -19).all()
+    assert microseconds(lambda: dl.beam_select(logits, scores, at, width)) <= 10 * before
+
+
+@pytest.mark.parametrize("dtype", list(base.TYPES))
+@pytest.mark.parametrize("vocab", [500, 9001])
+@pytest.mark.parametrize("spread", [1e3, 1e5, 1e9, 1e30])
+def test_rows_far_apart_are_compared_exactly(dtype, vocab, spread):
+    """Scores and logits of all magnitudes, among them rows whose score makes up for where their
+    logits lie, so that candidates of every row are close to the bound: the order is that of 64
+    bits, up to what the logarithms may be off (2^-19) and 64 bits round (2^-50 of the largest)."""
+    rng = np.random.default_rng(vocab)
+    rows, width = 40, 50
+    x = rng.standard_normal((rows, vocab))
+    if dtype == "fp32":
+        x[::3] += np.float32(spread) * np.sign(rng.standard_normal((len(x[::3]), 1))) * 0.75
+    logits = torch.from_numpy(x).to(base.TYPES[dtype]).cuda()
+    s = -3 * rng.random(rows)
+    s[1::4] -= spread
+    s[2::4] = -rng.random(len(s[2::4])) * spread
+    scores = torch.from_numpy(s).float().cuda()
+    starts = [0, 4, 5, rows]
+    best, parents, tokens = (y.cpu().numpy() for y in dl.beam_select(logits, scores, i32(starts), width))
+    want, _, _, every = beam_ref.select(f64(logits), f64(scores), starts, width)
+    tol = 2.0 ** -19 + 2.0 ** -50 * spread
+    assert (np.abs(best - want) <= tol + 2.0 ** -24 * np.abs(want)).all()
+    picked = every[parents, tokens]
+    assert (np.abs(picked - want) <= tol + 2.0 ** -50 * np.abs(want)).all()
+    for g in range(3):
+        assert len(set(zip(parents[g].tolist(), tokens[g].tolist()))) == width
