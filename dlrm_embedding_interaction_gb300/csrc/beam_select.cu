@@ -11,8 +11,8 @@
 // Selection never sorts the data. The k-th largest of the maxima of k or more disjoint
 // subsets (a thread's elements each) is a lower bound of the k-th largest element, found
 // bit by bit with counting barriers; few elements reach it, and those are ranked by
-// comparison with one another. Where many do (ties, adverse orders) the bound is bisected
-// to the exact value, and ties to the exact index.
+// comparison with one another. Where many do (ties, adverse orders) the bound is made
+// the exact value, and ties at it go by their index.
 //
 // The order hangs by differences of the rows' logarithms, so these are held more
 // precisely than fp32: the sums' terms have rounding errors of their own (2^-22 each, not
@@ -32,12 +32,15 @@ constexpr int kJoinThreads = 1024;
 constexpr int kSmallThreads = 512;
 constexpr int kVectors = 4;                      // 16-byte vectors of a thread and tile
 constexpr int kSubsets = 64;                     // widths up to here: one subset a thread will do
-constexpr int kFinal = 2048;                     // candidates that are ranked at most
+constexpr int kFinal = 2048;                     // candidates that shared memory holds
+// Candidates that are ranked at most, by comparison with one another: a call that ranked 1792
+// took 407 us, and takes 44 with an exact bound that leaves 512 or fewer.
+constexpr int kRanked = 512;
 constexpr int kLists = 1024;                     // lists of a group that shared memory knows
 constexpr int kRowsHere = 256;                   // rows of a group whose states lie in shared memory,
 constexpr int kRowsJoin = 128;                   // and of the join's
 static_assert(kSubsets <= kScanThreads && kBeamMaxWidth <= kScanThreads * kVectors && kBeamMaxWidth <= kSmallThreads &&
-                  kSmallThreads <= kJoinThreads && kBeamMaxWidth <= kFinal, "a subset for each place");
+                  kSmallThreads <= kJoinThreads && kBeamMaxWidth <= kRanked && kRanked <= kFinal, "a subset for each place");
 
 // A sum in two floats: the rounding errors of `sum` in `rest`.
 struct Sum {
@@ -167,6 +170,36 @@ __device__ __forceinline__ Sum log_sum(const Sum& s, float ref) {
   return Sum{sum, (y.sum - sum) + y.rest};
 }
 
+// Of counts of kValues values: the largest value that k (or more) of those counted reach, and how
+// many do. Every warp for itself; there are k.
+constexpr int kValues = 256;
+__device__ __forceinline__ void reached(const int* values, int k, int& value, int& there) {
+  constexpr int kEach = kValues / kWarp;
+  const int lane = threadIdx.x % kWarp;
+  int mine[kEach], from = 0;                      // keys of the lane's values, and with those of later lanes
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) from += mine[i] = values[lane * kEach + i];
+  const int own = from;
+#pragma unroll
+  for (int d = 1; d < kWarp; d *= 2) {
+    const int x = __shfl_down_sync(0xffffffffu, from, d);
+    if (lane + d < kWarp) from += x;
+  }
+  const int last = 31 - __clz(__ballot_sync(0xffffffffu, from >= k));   // (lane 0 has all)
+  int reach = from - own, at = 0;                 // of the largest value that k reach
+  value = 0;
+#pragma unroll
+  for (int i = kEach - 1; i >= 0; --i) {
+    reach += mine[i];
+    if (at < k) {
+      at = reach;
+      value = lane * kEach + i;
+    }
+  }
+  value = __shfl_sync(0xffffffffu, value, last);
+  there = __shfl_sync(0xffffffffu, at, last);
+}
+
 // A lower bound of the k-th largest of the threads' keys: the first eight bits that they do not
 // have in common by a count of each value, then bit by bit, until few more than k
 // reach it (keys of -infinity do not count, and are the bound where there are fewer than k
@@ -185,7 +218,6 @@ __device__ __forceinline__ uint32_t block_bound(uint32_t key, int k, uint32_t* r
     red[kWarps + warp] = lo;
     red[2 * kWarps + warp] = there;
   }
-  constexpr int kValues = 256, kEach = kValues / kWarp;
   static_assert(16 * kWarps >= kValues && THREADS >= kValues, "room");
   int* values = reinterpret_cast<int*>(red + 3 * kWarps);
   if (threadIdx.x < kValues) values[threadIdx.x] = 0;
@@ -202,27 +234,9 @@ __device__ __forceinline__ uint32_t block_bound(uint32_t key, int k, uint32_t* r
   if (there > k + k / 4 + 8) {
     if (key > none) atomicAdd(&values[key >> low & (kValues - 1)], 1);
     __syncthreads();
-    int mine[kEach], from = 0;                    // keys of the lane's values, and with those of later lanes
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) from += mine[i] = values[lane * kEach + i];
-    const int own = from;
-#pragma unroll
-    for (int d = 1; d < kWarp; d *= 2) {
-      const int x = __shfl_down_sync(0xffffffffu, from, d);
-      if (lane + d < kWarp) from += x;
-    }
-    const int last = 31 - __clz(__ballot_sync(0xffffffffu, from >= k));   // (lane 0 has all)
-    int reach = from - own, value = 0, at = 0;    // of the largest value that k reach
-#pragma unroll
-    for (int i = kEach - 1; i >= 0; --i) {
-      reach += mine[i];
-      if (at < k) {
-        at = reach;
-        value = lane * kEach + i;
-      }
-    }
-    bound |= static_cast<uint32_t>(__shfl_sync(0xffffffffu, value, last)) << low;
-    there = __shfl_sync(0xffffffffu, at, last);
+    int value;
+    reached(values, k, value, there);
+    bound |= static_cast<uint32_t>(value) << low;
   }
   for (int bit = low - 1; bit >= 0 && there > k + k / 4 + 8; --bit) {
     const uint32_t trial = bound | (1u << bit);
@@ -851,43 +865,91 @@ __device__ __forceinline__ void select_of(const Params& p, int64_t s0, const Row
     __syncthreads();
     n = *count_s;
   }
-  if (n > kFinal) {
-    // too many at the bound: the exact score, then the exact index among its ties
-    const auto reach = [&](uint64_t k, uint64_t last) {
-      int c = 0;
-      each(bound, INT_MAX, [&](int row, int token, float logit, float offset) {
-        if (!(raised(offset) + logit >= bound)) return;
-        const uint64_t x = key_of(score_of(row, logit));
-        c += x > k || (x == k && index_of(row, token) <= last);
+  if (n > kRanked) {
+    // too many at the bound: a bound of the exact scores that few enough reach, or, where
+    // ties at it are too many, one of their places, too
+    auto* range = reinterpret_cast<unsigned long long*>(found);
+    int* values = reinterpret_cast<int*>(found + 1);
+    // the largest bound that `need` keys reach, as far as it takes until no more than `room` do, by
+    // counts of eight bits at a time from the first that differs; `reach` do, and `above` lie
+    // above it
+    const auto bound_of_keys = [&](const auto& keys, int need, int room, int& reach, int& above) {
+      uint64_t hi = 0, lo = ~uint64_t(0);
+      keys([&](uint64_t x) {
+        hi = max(hi, x);
+        lo = min(lo, x);
       });
+#pragma unroll
+      for (int d = kWarp / 2; d > 0; d /= 2) {
+        hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, d));
+        lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, d));
+      }
+      __syncthreads();                            // (what `found` held before is read)
+      if (t == 0) {
+        range[0] = 0;
+        range[1] = ~0ull;
+      }
       __syncthreads();
-      if (t == 0) *count_s = 0;
+      if (t % kWarp == 0) {
+        atomicMax(&range[0], hi);
+        atomicMin(&range[1], lo);
+      }
       __syncthreads();
-      c = __reduce_add_sync(0xffffffffu, c);
-      if (t % kWarp == 0) atomicAdd(count_s, c);
-      __syncthreads();
-      return *count_s;
+      hi = range[0];
+      lo = range[1];
+      int low = hi == lo ? 0 : 64 - __clzll(hi ^ lo);   // bits from here on are found
+      uint64_t bound = low == 64 ? 0 : hi >> low << low;
+      reach = INT_MAX;
+      above = 0;
+      while (low > 0) {
+        const int next = max(low - 8, 0);
+        for (int i = t; i < kValues; i += THREADS) values[i] = 0;
+        __syncthreads();
+        keys([&](uint64_t x) {
+          if (((x ^ bound) >> next) >> (low - next) == 0) atomicAdd(&values[(x >> next) & ((1 << (low - next)) - 1)], 1);
+        });
+        __syncthreads();
+        int value, there;
+        reached(values, need - above, value, there);
+        bound |= static_cast<uint64_t>(value) << next;
+        reach = above + there;
+        if (reach <= room) break;
+        above += there - values[value];
+        low = next;
+        __syncthreads();                          // `values` are read
+      }
+      return bound;
     };
-    uint64_t k = 0, last = 0;
-    for (int bit = 63; bit >= 0; --bit) {
-      const uint64_t trial = k | (uint64_t(1) << bit);
-      if (reach(trial, ~uint64_t(0)) >= width) k = trial;
-    }
-    // the least index up to which the ties fill the places
-    for (int bit = 63; bit >= 0; --bit) {
-      const uint64_t trial = last | (uint64_t(1) << bit);
-      if (reach(k, trial - 1) < width) last = trial;
+    const auto exact = [&](const auto& f) {
+      each(bound, INT_MAX, [&](int row, int token, float logit, float offset) {
+        if (raised(offset) + logit >= bound) f(key_of(score_of(row, logit)), row, token, logit);
+      });
+    };
+    const auto place_of = [&](int row, int token) {   // later ones less
+      return ~(static_cast<uint64_t>(row) * static_cast<uint64_t>(p.a.vocab) + static_cast<uint64_t>(token));
+    };
+    int reach, above;
+    const uint64_t k = bound_of_keys(
+        [&](const auto& f) { exact([&](uint64_t x, int, int, float) { f(x); }); }, width, kRanked, reach, above);
+    uint64_t first = 0;
+    if (reach > kRanked) {
+      int more, before;
+      first = bound_of_keys(
+          [&](const auto& f) {
+            exact([&](uint64_t x, int row, int token, float) {
+              if (x == k) f(place_of(row, token));
+            });
+          },
+          width - above, kRanked - above, more, before);
     }
     __syncthreads();
     if (t == 0) *count_s = 0;
     __syncthreads();
-    each(bound, INT_MAX, [&](int row, int token, float logit, float offset) {
-      if (!(raised(offset) + logit >= bound)) return;
-      const uint64_t x = key_of(score_of(row, logit));
-      if (x > k || (x == k && index_of(row, token) <= last)) put(Candidate{__float_as_uint(logit), row, token});
+    exact([&](uint64_t x, int row, int token, float logit) {
+      if (x > k || (x == k && place_of(row, token) >= first)) put(Candidate{__float_as_uint(logit), row, token});
     });
     __syncthreads();
-    n = min(*count_s, kFinal);
+    n = min(*count_s, kRanked);
   }
   for (int i = t; i < n; i += THREADS) {
     const Candidate c = found[i];

@@ -682,7 +682,9 @@ dlrm_status_t attention_test_stall(int64_t wait_limit_ns, int32_t withhold);
  * influence, whatever its logit; a row that allows one token alone continues with it
  * at no cost. A row without an allowed token, or with a score of -infinity, has no
  * candidates, and a logit of -infinity makes none. Places past the candidates hold
- * -infinity, -1, -1. Scores are compared in 64 bits; the rows' logarithms of sums of
+ * -infinity, -1, -1. Scores are compared in 64 bits (of a row's tokens that are equal in them
+ * but not in their logits, beside a score of -1e30, those with the larger logits or the
+ * first ones may be taken); the rows' logarithms of sums of
  * exponentials are off by 2^-20 at most (far less with many terms), and rows whose scores
  * lie closer may change places.
  *   logits  (rows, vocab) of dtype, row i at i * ld; scores (rows) fp32, NULL: zeros

@@ -140,3 +140,38 @@ def test_rows_far_apart_are_compared_exactly(dtype, vocab, spread):
     assert (np.abs(picked - want) <= tol + 2.0 ** -50 * np.abs(want)).all()
     for g in range(3):
         assert len(set(zip(parents[g].tolist(), tokens[g].tolist()))) == width
+
+
+@pytest.mark.parametrize("unused", UNUSED)
+@pytest.mark.parametrize("dtype,vocab,width", [("fp32", 300, 16), ("fp32", 4096, 16), ("bf16", 32768, 100), ("fp16", 300007, 16)])
+def test_places_that_only_unused_beams_can_take(dtype, vocab, width, unused):
+    """One beam in use may continue with three tokens; the other places go to beams whose
+    scores agree in most of their bits, or in all 64 (numbers of 64 bits lie 2^75 apart at
+    -3.4e38, so that a row's continuations are equal there, and the first row takes all
+    places). (Thirty times: a part of the candidates is gone through a few times more, in 64
+    bits. One bit of the score at a time takes hundreds of times.)"""
+    rng = np.random.default_rng(vocab)
+    beams, groups = 8, 3
+    starts = list(range(0, groups * beams + 1, beams))
+    logits = torch.from_numpy(2 * rng.standard_normal((groups * beams, vocab))).to(base.TYPES[dtype]).cuda()
+    allowed = torch.ones(groups * beams, vocab, dtype=torch.bool, device="cuda")
+    scores = torch.zeros(groups * beams, device="cuda")
+    at = i32(starts)
+    call = lambda: dl.beam_select(logits, scores, at, width, allowed=allowed)   # noqa: E731
+    before = microseconds(call)
+    used = 3
+    allowed[used::beams] = False
+    allowed[used::beams, ::vocab // 3 + 1] = True
+    scores.view(groups, beams)[:] = unused
+    scores[used::beams] = -1.0
+    best, rows, tokens = (x.cpu().numpy() for x in call())
+    want, want_rows, want_tokens, every = beam_ref.select(f64(logits), f64(scores), starts, width, allowed.cpu().numpy())
+    assert (rows[:, :3] % beams == used).all() and (rows[:, 3:] % beams != used).all()
+    if unused < -1e30:
+        np.testing.assert_array_equal(rows[:, 3:], want_rows[:, 3:])
+    for g in range(groups):
+        assert len(set(zip(rows[g].tolist(), tokens[g].tolist()))) == width
+    tol = 2.0 ** -19 + 2.0 ** -50 * np.abs(want)
+    assert (np.abs(every[rows, tokens] - want) <= tol).all()
+    assert (np.abs(best - want) <= tol + 2.0 ** -24 * np.abs(want)).all()
+    assert microseconds(call) <= 30 * before, (microseconds(call), before)
