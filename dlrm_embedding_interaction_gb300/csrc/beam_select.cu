@@ -34,7 +34,7 @@ constexpr int kVectors = 4;                      // 16-byte vectors of a thread 
 constexpr int kSubsets = 64;                     // widths up to here: one subset a thread will do
 constexpr int kFinal = 2048;                     // candidates that shared memory holds
 // Candidates that are ranked at most, by comparison with one another: a call that ranked 1792
-// took 407 us, and takes 44 with an exact bound that leaves 512 or fewer.
+// took 407 us, and takes 35 with an exact bound that leaves 512 or fewer.
 constexpr int kRanked = 512;
 constexpr int kLists = 1024;                     // lists of a group that shared memory knows
 constexpr int kRowsHere = 256;                   // rows of a group whose states lie in shared memory,
@@ -871,42 +871,45 @@ __device__ __forceinline__ void select_of(const Params& p, int64_t s0, const Row
     auto* range = reinterpret_cast<unsigned long long*>(found);
     int* values = reinterpret_cast<int*>(found + 1);
     // the largest bound that `need` keys reach, as far as it takes until no more than `room` do, by
-    // counts of eight bits at a time from the first that differs; `reach` do, and `above` lie
-    // above it
+    // counts of eight bits at a time, each from the first that differs among those left; `reach`
+    // do, and `above` lie above it
     const auto bound_of_keys = [&](const auto& keys, int need, int room, int& reach, int& above) {
-      uint64_t hi = 0, lo = ~uint64_t(0);
-      keys([&](uint64_t x) {
-        hi = max(hi, x);
-        lo = min(lo, x);
-      });
-#pragma unroll
-      for (int d = kWarp / 2; d > 0; d /= 2) {
-        hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, d));
-        lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, d));
-      }
-      __syncthreads();                            // (what `found` held before is read)
-      if (t == 0) {
-        range[0] = 0;
-        range[1] = ~0ull;
-      }
-      __syncthreads();
-      if (t % kWarp == 0) {
-        atomicMax(&range[0], hi);
-        atomicMin(&range[1], lo);
-      }
-      __syncthreads();
-      hi = range[0];
-      lo = range[1];
-      int low = hi == lo ? 0 : 64 - __clzll(hi ^ lo);   // bits from here on are found
-      uint64_t bound = low == 64 ? 0 : hi >> low << low;
+      uint64_t bound = 0;
       reach = INT_MAX;
       above = 0;
-      while (low > 0) {
-        const int next = max(low - 8, 0);
+      for (int low = 64; low > 0;) {              // bits from `low` on are found
+        uint64_t hi = 0, lo = ~uint64_t(0);
+        keys([&](uint64_t x) {
+          if ((x ^ bound) >> (low - 1) >> 1 != 0) return;
+          hi = max(hi, x);
+          lo = min(lo, x);
+        });
+#pragma unroll
+        for (int d = kWarp / 2; d > 0; d /= 2) {
+          hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, d));
+          lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, d));
+        }
+        __syncthreads();                          // (what `found` held before is read)
+        if (t == 0) {
+          range[0] = 0;
+          range[1] = ~0ull;
+        }
         for (int i = t; i < kValues; i += THREADS) values[i] = 0;
         __syncthreads();
+        if (t % kWarp == 0) {
+          atomicMax(&range[0], hi);
+          atomicMin(&range[1], lo);
+        }
+        __syncthreads();
+        hi = range[0];
+        lo = range[1];
+        bound = hi;
+        if (hi == lo) break;
+        low = 64 - __clzll(hi ^ lo);
+        bound = hi >> (low - 1) >> 1 << 1 << (low - 1);
+        const int next = max(low - 8, 0);
         keys([&](uint64_t x) {
-          if (((x ^ bound) >> next) >> (low - next) == 0) atomicAdd(&values[(x >> next) & ((1 << (low - next)) - 1)], 1);
+          if ((x ^ bound) >> (low - 1) >> 1 == 0) atomicAdd(&values[(x >> next) & ((1 << (low - next)) - 1)], 1);
         });
         __syncthreads();
         int value, there;
@@ -916,7 +919,7 @@ __device__ __forceinline__ void select_of(const Params& p, int64_t s0, const Row
         if (reach <= room) break;
         above += there - values[value];
         low = next;
-        __syncthreads();                          // `values` are read
+        __syncthreads();                          // `values` and `range` are read
       }
       return bound;
     };
