@@ -175,3 +175,67 @@ def test_places_that_only_unused_beams_can_take(dtype, vocab, width, unused):
     assert (np.abs(every[rows, tokens] - want) <= tol).all()
     assert (np.abs(best - want) <= tol + 2.0 ** -24 * np.abs(want)).all()
     assert microseconds(call) <= 30 * before, (microseconds(call), before)
+
+
+@pytest.mark.parametrize("fill", ["lowest", -1e4, 0.0])
+@pytest.mark.parametrize("dtype,vocab,width", [("fp32", 20011, 5), ("bf16", 32768, 16), ("fp16", 300007, 100), ("bf16", 300007, 256)])
+@pytest.mark.parametrize("left", [0, 3, 200])
+def test_tokens_masked_by_a_value(dtype, vocab, width, left, fill):
+    """Most logits of a row are one number (tokens masked by a value of their own, or a head
+    that saturates), so that it is the bound wherever a chunk has few others; ties go by token.
+    Ten times as long as other logits take is the noise of short calls and some passes more; a
+    pass for each bit of the value and of the index takes thirty to fifty times. Where a group
+    has fewer tokens left than places (the group of one row has `left`), what the others' lists
+    hold is equal, at most 11 rows of 37 lists of 256: 104,000 scores in 64 bits, of 7 operations
+    each, 2 a clock and SM, are 190 us a pass, and four passes (range, places, counts, the taken
+    ones) 770, 15 times the 50 us; thirty are allowed."""
+    rng = np.random.default_rng(vocab + left)
+    rows, t = 24, base.TYPES[dtype]
+    logits = torch.from_numpy(2 * rng.standard_normal((rows, vocab))).to(t).cuda()
+    starts = [0, 6, 12, 13, rows]
+    at = i32(starts)
+    before = microseconds(lambda: dl.beam_select(logits, None, at, width))
+    value = torch.finfo(t).min if fill == "lowest" else fill
+    x = torch.full_like(logits, value)
+    for row in range(rows):                       # rows of their own tokens, some of them side by side
+        keep = rng.permutation(vocab)[:left] if row % 2 else np.arange(left) + 37 * row
+        x[row, torch.from_numpy(keep).cuda()] = logits[row, torch.from_numpy(keep).cuda()]
+    got = dl.beam_select(x, None, at, width)
+    best, parents, tokens = (y.cpu().numpy() for y in got)
+    want, want_rows, want_tokens, every = beam_ref.select(f64(x), np.zeros(rows), starts, width)
+    assert (np.abs(best - want) <= 2.0 ** -20 + 2.0 ** -24 * np.abs(want)).all()
+    assert (np.abs(every[parents, tokens] - want) <= 2.0 ** -19).all()
+    for g in range(len(starts) - 1):              # of each row: its largest logits, the first of equal ones
+        for row in set(parents[g].tolist()):
+            mine = tokens[g][parents[g] == row]
+            order = np.argsort(-f64(x[row]), kind="stable")[:len(mine)]
+            np.testing.assert_array_equal(mine, order)
+    assert microseconds(lambda: dl.beam_select(x, None, at, width)) <= (10 if left >= width else 30) * before
+
+
+@pytest.mark.parametrize("dtype", list(base.TYPES))
+@pytest.mark.parametrize("kind", ["steps", "all rise", "two levels", "masked steps", "one above"])
+@pytest.mark.parametrize("width", [1, 33, 256])
+def test_chunks_that_overflow_their_lists(dtype, kind, width):
+    """Rows in which every tile has larger logits than the one before, with and without ties."""
+    vocab, t = 70001, base.TYPES[dtype]
+    rng = np.random.default_rng(width)
+    i = np.arange(vocab)
+    x = {"steps": i // 700 * 0.125, "all rise": i * (40.0 / vocab), "two levels": (i % 3 == 1) * 5.0 + i // 30000,
+         "masked steps": i // 300 * 0.0625, "one above": (i == 50000) * 1.0 - (i % 2) * 1e-3}[kind]
+    logits = torch.from_numpy(np.stack([x, x[::-1].copy(), rng.permutation(x)] * 3)).to(t).cuda()
+    allowed = torch.from_numpy(rng.random(logits.shape) < 0.7).cuda() if kind == "masked steps" else None
+    starts = list(range(0, 10, 3))
+    got = dl.beam_select(logits, None, i32(starts), width, allowed=allowed)
+    best, parents, tokens = (y.cpu().numpy() for y in got)
+    mask = None if allowed is None else allowed.cpu().numpy()
+    want, _, _, every = beam_ref.select(f64(logits), np.zeros(9), starts, width, mask)
+    assert (np.abs(best - want) <= 2.0 ** -20 + 2.0 ** -24 * np.abs(want)).all()
+    assert (np.abs(every[parents, tokens] - want) <= 2.0 ** -19).all()
+    for g in range(3):
+        for row in set(parents[g].tolist()):
+            mine = tokens[g][parents[g] == row]
+            y = f64(logits[row])
+            if mask is not None:
+                y = np.where(mask[row], y, -np.inf)
+            np.testing.assert_array_equal(mine, np.argsort(-y, kind="stable")[:len(mine)])
