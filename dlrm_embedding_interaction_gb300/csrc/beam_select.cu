@@ -1254,7 +1254,10 @@ __global__ void __launch_bounds__(kSmallThreads, 2) beam_small_kernel(const __gr
 
 // ------------------------------------------------------------------ launches
 
-// One launch for groups of at most this many logits, on average.
+// One launch for groups of at most this many logits, on average: the host does not know more of the
+// groups. Where one of them holds all rows, its CTA does all the work: 64 groups of 16 x 256
+// fp32 logits 22 us, one of 1024 x 256 among 63 without rows 134; 256 groups of 4 x 4096 25, one of
+// 1024 x 4096 2190.
 constexpr int64_t kSmallGroup = 32768;
 constexpr int kSmallVocab = 4096;
 // CTAs of the scan that chunks are made for: one for each place that the SMs have for masked

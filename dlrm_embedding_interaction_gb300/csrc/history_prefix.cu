@@ -328,6 +328,14 @@ cudaError_t launch_history_prefix_attention(const dlrm_history_t& h, const dlrm_
   // known here). In us, apart against shared, one query a request: 1 user x 4 beams x 400 events
   // of 8 heads over 2 8.1 and 17, 17 x 12 x 430 fp16 18 and 29, 720 beams of five queries and 20
   // events 17 and 31; 36 x 3 x 1500 at head_dim 128 41 and 33, 64 x 16 x 1500 74 and 48.
+  // The host knows what the tables have room for, not how long the histories are: in tables with
+  // room for 8192 events 16 users x 8 x 1000 take 26 and would take 15 apart, 17 x 12 x 430 fp16 29
+  // and 15, one user x 4 x 150 in room for 100,000 21 and 14.
+  // bf16 calls of 64 rows a request and more and 4096 in all, which history_attention takes on
+  // tcgen05 tiles with weights of 8 bits, are not read apart: here bf16 weights have 11. With 64
+  // rows a request that costs little or nothing (apart against shared, head_dim 128: 64 users x 1
+  // x 1024 49 and 54, 4 x 8 x 100,000 744 and 658; 64 x 4 x 64 at head_dim 64 19 and 42), with more
+  // it does: 256 rows 61 and 148, 1265 and 2522, 23 and 128.
   constexpr double kPlan = 12.0, kPiece = 0.007, kShared = 0.0127, kBytes = 7.5e6;
   const int64_t cap = static_cast<int64_t>(h.max_pages) * h.page_tokens;
   const int64_t seen = a.window > 0 ? std::min<int64_t>(cap, int64_t(a.window) + a.sinks + 2 * kBlock) : cap;

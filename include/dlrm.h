@@ -653,6 +653,8 @@ dlrm_status_t window_attention(const dlrm_attention_t* a, void* stream);
  * all its rows. Outputs are history_attention's whatever the groups, but for rounding
  * (weights carry 22 bits with fp32 and fp16 rows, 11 with bf16). A call that is too small
  * for sharing to pay reads each history for itself (weights of 11 bits with fp16, too).
+ * What is too small goes by what the tables have room for. bf16 requests of 128 rows a kv
+ * head and more take less time in history_attention, where their weights may have 8 bits.
  *   groups  (n_groups + 1) int32 from 0 to batch; batch and n_groups <= n_slots
  * Starts or groups that decrease, leave their range or leave requests out set
  * DLRM_ERRBIT_OFFSETS; the call's outputs are then undefined, and its work stays
