@@ -514,8 +514,8 @@ __device__ __forceinline__ uint32_t warp_bound(const uint32_t (&key)[N], int k) 
 }
 
 // What bounds it: instructions (a conversion, half an FMA, one exponential and half a sum a
-// logit; issue slots are 63% busy) and what each CTA begins and ends with, then HBM: 1643 rows of
-// 32,768 bf16 logits 36 us (3.0 TB/s), 33 of 1,000,003 masked fp16 ones 42 us (2.4 TB/s).
+// logit; issue slots are 66% busy) and what each CTA begins and ends with, then HBM: 1643 rows of
+// 32,768 bf16 logits 34 us (3.2 TB/s), 33 of 1,000,003 masked fp16 ones 41 us (2.5 TB/s).
 // Warps meet twice, after the first tile and at the end: each has a list of its own, of vectors
 // by their largest element; their elements are looked at once more at the end.
 template <int DT, bool MASK>
