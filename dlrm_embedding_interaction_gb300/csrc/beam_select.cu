@@ -947,6 +947,9 @@ __device__ __forceinline__ void select_of(const Params& p, int64_t s0, const Row
         __syncthreads();
         hi = range[0];
         lo = range[1];
+        // (none: bad starts let another group write the rows' states meanwhile; both agree with
+        // `bound` from `low` on, so `low` falls whatever they hold)
+        if (hi < lo) break;
         bound = hi;
         if (hi == lo) break;
         low = 64 - __clzll(hi ^ lo);

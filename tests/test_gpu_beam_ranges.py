@@ -239,3 +239,29 @@ def test_chunks_that_overflow_their_lists(dtype, kind, width):
             if mask is not None:
                 y = np.where(mask[row], y, -np.inf)
             np.testing.assert_array_equal(mine, np.argsort(-y, kind="stable")[:len(mine)])
+
+
+@pytest.mark.parametrize("vocab", [300, 5000])
+@pytest.mark.parametrize("kind", ["equal", "spread", "unused"])
+def test_groups_that_bad_starts_lay_over_one_another(vocab, kind):
+    """Starts that decrease leave two groups with rows in common, more than shared memory holds
+    the states of: what they write is undefined, but the call ends, reports them, and serves
+    the group before them; the next call is as ever."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    logits = torch.zeros(900, vocab, device="cuda")
+    if kind != "equal":
+        logits.normal_(generator=g)
+    scores = torch.zeros(900, device="cuda")
+    if kind == "unused":
+        scores[1::2] = -1e9
+    more = [900] * 20 if vocab == 300 else []     # groups enough for one launch
+    good = dl.beam_select(logits, scores, i32([0, 10, 600, 900] + more), 20)
+    for _ in range(20):
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = dl.beam_select(logits, scores, i32([0, 10, 600, 40, 900] + more), 20, err_flag=err)
+        assert int(err) & dl.ERRBIT_OFFSETS
+        assert all(torch.equal(a[0], b[0]) for a, b in zip(got, good))
+        assert (got[1][2] == -1).all()            # from 600 to 40: none
+    again = dl.beam_select(logits, scores, i32([0, 10, 600, 900] + more), 20)
+    assert all(torch.equal(a, b) for a, b in zip(again, good))
